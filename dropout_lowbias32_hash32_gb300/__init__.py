@@ -54,6 +54,13 @@ _FILL_SIGS = {
     "rng_fill_normal_f64_noalloc": [_u32, _u32, _sz, _p, _p],
     "rng_dropout_fwd": [_p, _p, _f32, _u32, _u32, _sz, _p],
     "rng_dropout_bwd": [_p, _p, _f32, _u32, _u32, _sz, _p],
+    "rng_dropout_layer_norm_fwd": [_p, _sz, _p, _p, _sz, _p, _p, _p, _sz, _p, _sz, _p, _p, _sz, _sz, _int, _int, _f32,
+                                   _u32, _u32, _f32, _p],
+    "rng_dropout_layer_norm_bwd": [_p, _sz, _p, _sz, _p, _sz, _p, _p, _p, _p, _sz, _p, _sz, _p, _p, _p, _sz, _sz, _int,
+                                   _int, _f32, _u32, _u32, _p, _sz, _p],
+    "rng_attention_fwd": [_p, _p],
+    "rng_attention_bwd": [_p, _p],
+    "rng_relative_bucket": [_i64, _i32, _i32, _i32, C.POINTER(_i32)],
     "rng_debug_set_miss_capacity": [_sz],
     "rng_debug_last_miss_count": [C.POINTER(_u64)],
     "rng_debug_eval_f64": [_int, _p, _p, _sz, _p],
@@ -63,6 +70,10 @@ for _name, _args in _FILL_SIGS.items():
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _int
+for _name, _args in {"rng_dropout_layer_norm_bwd_workspace": [_sz, _sz], "rng_attention_fwd_workspace": [_p],
+                     "rng_attention_bwd_workspace": [_p]}.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _sz
 _lib.rng_status_string.argtypes = [_int]
 _lib.rng_status_string.restype = C.c_char_p
 _lib.rng_last_error.argtypes = []
@@ -231,6 +242,276 @@ def rng_dropout_fwd(x, y, p, seed, first_counter, stream=None):
 
 def rng_dropout_bwd(dy, dx, p, seed, first_counter, stream=None):
     return _dropout("rng_dropout_bwd", dy, dx, p, seed, first_counter, stream)
+
+
+# ---- a transformer layer's dropout ----------------------------------------------
+RNG_F32, RNG_F16, RNG_BF16 = 0, 1, 2
+
+
+class AttentionArgs(C.Structure):
+    """rng_attention_args of include/rng.h."""
+    _fields_ = [("dtype", _int), ("batch", _i32), ("len_q", _i32), ("len_k", _i32), ("heads_q", _i32),
+                ("heads_kv", _i32), ("head_dim", _i32), ("q", _p), ("k", _p), ("v", _p), ("q_stride", _i64 * 3),
+                ("k_stride", _i64 * 3), ("v_stride", _i64 * 3), ("o", _p), ("o_stride", _i64 * 3), ("lse", _p),
+                ("key_lengths", _p), ("causal", _i32), ("queries_last", _i32), ("scale", _f32), ("bias_table", _p),
+                ("num_buckets", _i32), ("max_distance", _i32), ("bidirectional", _i32), ("p", _f32), ("seed", _u32),
+                ("first_counter", _u32), ("d_o", _p), ("dq", _p), ("dk", _p), ("dv", _p), ("do_stride", _i64 * 3),
+                ("dq_stride", _i64 * 3), ("dk_stride", _i64 * 3), ("dv_stride", _i64 * 3), ("dbias_table", _p),
+                ("workspace", _p), ("workspace_bytes", _sz)]
+
+
+_codes: dict = {}  # torch dtype -> rng_dtype, made at the first use of torch
+
+
+def _dtype_code(t, name: str) -> int:
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: RNG_F32, torch.float16: RNG_F16, torch.bfloat16: RNG_BF16})
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must have dtype float32, float16 or bfloat16, not {t.dtype}")
+    return code
+
+
+def _same(t, name: str, like, like_name: str, dtype=None) -> None:
+    """t lies on like's device and has its dtype (or the given one)."""
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, {like_name} on {like.device}")
+    if t.dtype != (dtype or like.dtype):
+        raise TypeError(f"{name} must have dtype {dtype or like.dtype}, not {t.dtype}")
+
+
+def _row_array(t, name: str, like, like_name: str) -> tuple:
+    """(pointer, elements between rows) of a [..., cols] tensor whose leading
+    dimensions lie one row stride apart; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t is not like:
+        _same(t, name, like, like_name)
+        if t.shape != like.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, {like_name} {tuple(like.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1]
+    if t.numel() == 0:
+        return t.data_ptr(), t.shape[-1]
+    stride, rows = None, 1  # from the last leading dimension out
+    for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = s
+        elif s != stride * rows:
+            raise ValueError(f"{name}'s rows must lie one stride apart")
+        rows *= n
+    if t.shape[-1] != 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), t.shape[-1] if stride is None else stride
+
+
+def _flat(t, name: str, n: int, like, like_name: str, dtype) -> int | None:
+    """Pointer of a contiguous tensor of n elements; None for None."""
+    if t is None:
+        return None
+    _same(t, name, like, like_name, dtype)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    return t.data_ptr()
+
+
+def _cuda_rows(t, name: str) -> tuple:
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    cols = t.shape[-1]
+    return (t.numel() // cols if cols else 0), cols
+
+
+def _param_dtype(weights, like):
+    """The weights' common dtype (the activations' when there are none)."""
+    for w in weights:
+        if w is not None:
+            return w.dtype, _dtype_code(w, "a weight")
+    return like.dtype, _dtype_code(like, "x")
+
+
+def _scratch(workspace, need: int, like, stream):
+    """The caller's workspace, or one of the caching allocator's."""
+    if need == 0:
+        return None, 0, None
+    import torch
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        if stream is not None:  # its memory may be reused only after that stream's work
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+            workspace.record_stream(stream)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _call(name: str, t, stream, *args):
+    """The entry point on t's device and stream, the stream its last argument."""
+    import torch
+    fn = getattr(_lib, name)
+    if torch.cuda.current_device() == t.device.index:
+        _check(fn(*args, _stream(stream, t)), name)
+    else:
+        with _on_device(t):
+            _check(fn(*args, _stream(stream, t)), name)
+
+
+def rng_dropout_layer_norm_fwd(x, gamma, beta, y, mean=None, rstd=None, *, bias=None, residual=None, h=None, p=0.0,
+                               seed=0, first_counter=0, eps=1e-5, stream=None):
+    """h = residual + dropout(x + bias); y = (h - mean) * rstd * gamma + beta
+    over the last dimension; see rng.h.  Writes y and, where given, h, mean
+    and rstd; returns y."""
+    name = "rng_dropout_layer_norm_fwd"
+    rows, cols = _cuda_rows(x, "x")
+    code = _dtype_code(x, "x")
+    wd, wcode = _param_dtype((gamma, beta, bias), x)
+    import torch
+    f32 = torch.float32
+    _call(name, x, stream, *_row_array(x, "x", x, "x"), _flat(bias, "bias", cols, x, "x", wd),
+          *_row_array(residual, "residual", x, "x"), _flat(gamma, "gamma", cols, x, "x", wd),
+          _flat(beta, "beta", cols, x, "x", wd), *_row_array(y, "y", x, "x"), *_row_array(h, "h", x, "x"),
+          _flat(mean, "mean", rows, x, "x", f32), _flat(rstd, "rstd", rows, x, "x", f32), rows, cols, code, wcode,
+          p, seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF, eps)
+    return y
+
+
+def rng_dropout_layer_norm_bwd_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace of rng_dropout_layer_norm_bwd on the current device."""
+    return _lib.rng_dropout_layer_norm_bwd_workspace(rows, cols)
+
+
+def rng_dropout_layer_norm_bwd(dy, h, gamma, mean, rstd, dx, dgamma=None, dbeta=None, *, dh=None, dresidual=None,
+                               dbias=None, p=0.0, seed=0, first_counter=0, workspace=None, stream=None):
+    """The gradient of rng_dropout_layer_norm_fwd from its h, mean and rstd;
+    dh is the gradient that reaches h past the norm.  Writes dx and, where
+    given, dresidual, dgamma, dbeta and dbias; returns dx."""
+    name = "rng_dropout_layer_norm_bwd"
+    rows, cols = _cuda_rows(dy, "dy")
+    code = _dtype_code(dy, "dy")
+    wd, wcode = _param_dtype((gamma, dgamma, dbeta, dbias), dy)
+    import torch
+    f32 = torch.float32
+    with _on_device(dy):
+        need = _lib.rng_dropout_layer_norm_bwd_workspace(rows, cols)
+    ws, ws_bytes, hold = _scratch(workspace, need, dy, stream)
+    _call(name, dy, stream, *_row_array(dy, "dy", dy, "dy"), *_row_array(h, "h", dy, "dy"),
+          *_row_array(dh, "dh", dy, "dy"), _flat(gamma, "gamma", cols, dy, "dy", wd),
+          _flat(mean, "mean", rows, dy, "dy", f32), _flat(rstd, "rstd", rows, dy, "dy", f32),
+          *_row_array(dx, "dx", dy, "dy"), *_row_array(dresidual, "dresidual", dy, "dy"),
+          _flat(dgamma, "dgamma", cols, dy, "dy", wd), _flat(dbeta, "dbeta", cols, dy, "dy", wd),
+          _flat(dbias, "dbias", cols, dy, "dy", wd), rows, cols, code, wcode, p, seed & 0xFFFFFFFF,
+          first_counter & 0xFFFFFFFF, ws, ws_bytes)
+    del hold
+    return dx
+
+
+def _heads_array(args, field: str, t, name: str, shape, like) -> None:
+    if t is not like:
+        _same(t, name, like, "q")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    b, l, h, d = t.stride()
+    if d != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    setattr(args, field, t.data_ptr())
+    setattr(args, "do_stride" if field == "d_o" else field + "_stride", (b, l, h))
+
+
+def _attention_args(q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table, max_distance, bidirectional,
+                    p, seed, first_counter) -> AttentionArgs:
+    if not getattr(q, "is_cuda", False):
+        raise TypeError("q must be a CUDA tensor")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [batch, length, heads, head_dim]")
+    import torch
+    a = AttentionArgs()
+    a.dtype = _dtype_code(q, "q")
+    a.batch, a.len_q, a.heads_q, a.head_dim = q.shape
+    a.len_k, a.heads_kv = k.shape[1], k.shape[2]
+    keys = (q.shape[0], k.shape[1], k.shape[2], q.shape[3])
+    _heads_array(a, "q", q, "q", q.shape, q)
+    _heads_array(a, "k", k, "k", keys, q)
+    _heads_array(a, "v", v, "v", keys, q)
+    _heads_array(a, "o", o, "o", q.shape, q)
+    if lse is not None and lse.shape != (a.batch, a.heads_q, a.len_q):
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, not [batch, heads, len_q]")
+    a.lse = _flat(lse, "lse", a.batch * a.heads_q * a.len_q, q, "q", torch.float32)
+    a.key_lengths = _flat(key_lengths, "key_lengths", a.batch, q, "q", torch.int32)
+    a.causal, a.queries_last = bool(causal), bool(queries_last)
+    a.scale = q.shape[3] ** -0.5 if scale is None else scale
+    if bias_table is not None:
+        if bias_table.dim() != 2 or bias_table.shape[1] != a.heads_q:
+            raise ValueError(f"bias_table has shape {tuple(bias_table.shape)}, not [num_buckets, heads]")
+        a.bias_table = _flat(bias_table, "bias_table", bias_table.numel(), q, "q", q.dtype)
+        a.num_buckets, a.max_distance, a.bidirectional = bias_table.shape[0], max_distance, bool(bidirectional)
+    a.p, a.seed, a.first_counter = p, seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF
+    return a
+
+
+def rng_attention_fwd_workspace(args: AttentionArgs) -> int:
+    """Bytes of workspace of rng_attention_fwd on the current device."""
+    return _lib.rng_attention_fwd_workspace(C.byref(args))
+
+
+def rng_attention_bwd_workspace(args: AttentionArgs) -> int:
+    """Bytes of workspace of rng_attention_bwd on the current device."""
+    return _lib.rng_attention_bwd_workspace(C.byref(args))
+
+
+def _attention(name, a, like, workspace, stream):
+    with _on_device(like):
+        need = getattr(_lib, name + "_workspace")(C.byref(a))
+    a.workspace, a.workspace_bytes, hold = _scratch(workspace, need, like, stream)
+    _call(name, like, stream, C.byref(a))
+    del hold
+
+
+def rng_attention_fwd(q, k, v, o, *, lse=None, key_lengths=None, causal=False, queries_last=False, scale=None,
+                      bias_table=None, max_distance=128, bidirectional=True, p=0.0, seed=0, first_counter=0,
+                      workspace=None, stream=None):
+    """Attention with a bucketed relative position bias and dropout on its
+    probabilities; q and o are [batch, len_q, heads, head_dim], k and v
+    [batch, len_k, key heads, head_dim] (any strides, the last dimension
+    contiguous); scale None: head_dim ** -0.5; see rng.h.  Writes o and, where
+    given, lse [batch, heads, len_q]; returns o."""
+    a = _attention_args(q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table, max_distance,
+                        bidirectional, p, seed, first_counter)
+    _attention("rng_attention_fwd", a, q, workspace, stream)
+    return o
+
+
+def rng_attention_bwd(do, q, k, v, o, lse, dq, dk, dv, *, dbias_table=None, key_lengths=None, causal=False,
+                      queries_last=False, scale=None, bias_table=None, max_distance=128, bidirectional=True, p=0.0,
+                      seed=0, first_counter=0, workspace=None, stream=None):
+    """The gradient of rng_attention_fwd from its o and lse and the same
+    options.  Writes dq, dk, dv and, where given, dbias_table; returns dq, dk, dv."""
+    a = _attention_args(q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table, max_distance,
+                        bidirectional, p, seed, first_counter)
+    _heads_array(a, "d_o", do, "do", q.shape, q)
+    _heads_array(a, "dq", dq, "dq", q.shape, q)
+    _heads_array(a, "dk", dk, "dk", k.shape, q)
+    _heads_array(a, "dv", dv, "dv", k.shape, q)
+    if dbias_table is not None:
+        if bias_table is None:
+            raise ValueError("dbias_table without a bias_table")
+        a.dbias_table = _flat(dbias_table, "dbias_table", bias_table.numel(), q, "q", q.dtype)
+    _attention("rng_attention_bwd", a, q, workspace, stream)
+    return dq, dk, dv
+
+
+def rng_relative_bucket(relative_position: int, num_buckets: int, max_distance: int = 128,
+                        bidirectional: bool = True) -> int:
+    """The bucket of a relative position (the key's minus the query's)."""
+    bucket = _i32()
+    _check(_lib.rng_relative_bucket(relative_position, num_buckets, max_distance, bool(bidirectional),
+                                    C.byref(bucket)), "rng_relative_bucket")
+    return bucket.value
 
 
 def rng_status_string(status: int) -> str:

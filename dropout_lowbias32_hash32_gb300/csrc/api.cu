@@ -28,6 +28,8 @@ thread_local char t_error[256] = "";
 std::mutex g_sm_mu;
 std::vector<unsigned> g_sm_counts;
 
+}  // namespace
+
 rng_status fail(rng_status st, const char *fmt, ...)
 {
     va_list ap;
@@ -42,6 +44,10 @@ rng_status cuda_fail(cudaError_t e, const char *what)
     if (e == cudaErrorMemoryAllocation) return fail(RNG_ENOMEM, "%s: %s", what, cudaGetErrorString(e));
     return fail(RNG_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+void clear_error() { t_error[0] = '\0'; }
+
+namespace {
 
 template <class T>
 rng_status check_out(const T *p, size_t n, const char *name)

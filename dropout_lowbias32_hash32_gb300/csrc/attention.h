@@ -1,0 +1,74 @@
+// attention.h -- what the attention kernels are launched with (host side of
+// attention.cu), and the device helpers that every one of them shares: the
+// position of a query, the mask, the buckets.
+#pragma once
+
+#include "element.cuh"
+#include "internal.h"
+
+namespace rngk {
+
+constexpr int kMaxBuckets = 128;
+constexpr int kMaxDistance = 1024;
+
+// One direction's buckets by the distances at which bucket 1, 2, ... begin
+// (count - 1 of them, ascending); `past` is added for keys past the query.
+struct Buckets {
+    int32_t total, count, past, max_distance;
+    int32_t starts[kMaxBuckets];
+};
+
+struct Strides {
+    int64_t batch, len, head;
+};
+
+struct Attention {
+    int32_t batch, len_q, len_k, heads, heads_kv, dim, group;
+    const void *q, *k, *v, *o, *d_o;
+    void *out, *dq, *dk, *dv;
+    Strides qs, ks, vs, os, dos, dqs, dks, dvs;
+    float *lse;
+    const int32_t *key_lengths;
+    bool causal, last;
+    float scale;
+    const void *table;
+    void *dtable;
+    Buckets buckets;
+    Mask mask;
+    uint32_t first;
+    void *workspace;
+};
+
+rng_status relative_buckets(const char *what, int32_t num_buckets, int32_t max_distance, bool bidirectional,
+                            Buckets *out);
+
+size_t attention_fwd_workspace(const Attention &a);
+size_t attention_bwd_workspace(const Attention &a);
+template <class T>
+cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s);
+template <class T>
+cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s);
+
+__host__ __device__ __forceinline__ int32_t bucket_of(const Buckets &b, int64_t rel)
+{
+    int64_t d = rel > 0 ? (b.past ? rel : 0) : -rel;
+    if (d > b.max_distance) d = b.max_distance;
+    int lo = 0, hi = b.count - 1;  // the number of starts at or below d
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (b.starts[mid] <= d) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo + (rel > 0 ? b.past : 0);
+}
+
+// The number of keys of a batch entry, and the position of its query 0.
+__device__ __forceinline__ int32_t keys_of(const Attention &a, int32_t b)
+{
+    if (!a.key_lengths) return a.len_k;
+    const int32_t n = a.key_lengths[b];
+    return n < 0 ? 0 : n > a.len_k ? a.len_k : n;
+}
+__device__ __forceinline__ int32_t first_position(const Attention &a, int32_t keys) { return a.last ? keys - a.len_q : 0; }
+
+}  // namespace rngk

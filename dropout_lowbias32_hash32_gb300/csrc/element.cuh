@@ -1,0 +1,130 @@
+// element.cuh -- element types of the layer kernels (f32, f16, bf16) and their
+// vector accesses: V elements as one 16-byte access, or one element.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "hash32.cuh"
+
+namespace rngk {
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Two f32 rounded to a pair of 16-bit values in one register, a in the low half.
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b)
+{
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b)
+{
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+    return d;
+}
+
+// The bits of V elements of T as they travel: whole 32-bit registers, or one
+// element.
+template <class T, int V>
+struct Raw {
+    static_assert(V * sizeof(T) % 4 == 0, "whole registers");
+    uint32_t w[V * sizeof(T) / 4];
+};
+template <>
+struct Raw<__half, 1> {
+    __half w;
+};
+template <>
+struct Raw<__nv_bfloat16, 1> {
+    __nv_bfloat16 w;
+};
+
+// V elements at p: 16-byte accesses (p aligned to them), or one element.  Streaming (evict-first) for activations,
+// which are read once; plain for weights, which every row reads.
+template <bool kStream, class T, int V>
+__device__ __forceinline__ Raw<T, V> load(const T *p)
+{
+    Raw<T, V> r;
+    if constexpr (V == 1) {
+        *reinterpret_cast<T *>(&r) = kStream ? __ldcs(p) : *p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(V * sizeof(T) / 16); ++i) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(p) + i;
+            const uint4 a = kStream ? __ldcs(q) : *q;
+            r.w[4 * i] = a.x, r.w[4 * i + 1] = a.y, r.w[4 * i + 2] = a.z, r.w[4 * i + 3] = a.w;
+        }
+    }
+    return r;
+}
+
+template <class T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V> &r, float (&o)[V])
+{
+    if constexpr (V == 1) {
+        o[0] = to_f32(*reinterpret_cast<const T *>(&r));
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = __uint_as_float(r.w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                const T *h = reinterpret_cast<const T *>(&r.w[i]);
+                o[2 * i] = to_f32(h[0]), o[2 * i + 1] = to_f32(h[1]);
+            }
+        }
+    }
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store(T *p, const float (&v)[V])
+{
+    if constexpr (V == 1) {
+        *p = from_f32<T>(v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i)
+            __stcs(reinterpret_cast<float4 *>(p) + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 8; ++i)
+            __stcs(reinterpret_cast<uint4 *>(p) + i,
+                   make_uint4(pack2<T>(v[8 * i], v[8 * i + 1]), pack2<T>(v[8 * i + 2], v[8 * i + 3]),
+                              pack2<T>(v[8 * i + 4], v[8 * i + 5]), pack2<T>(v[8 * i + 6], v[8 * i + 7])));
+    }
+}
+
+// Dropout as the layer kernels apply it: keep iff the draw's low 23 bits reach
+// the threshold ceil(p 2^23); the scale 1 / (1 - p) is multiplied by the
+// caller.  threshold 0 (p = 0) keeps everything.
+struct Mask {
+    uint32_t key, threshold;
+    float scale;
+};
+
+__device__ __forceinline__ bool keeps(const Mask &m, uint32_t c)
+{
+    return (draw32(m.key, c) & 0x7FFFFFu) >= m.threshold;
+}
+
+}  // namespace rngk

@@ -7,7 +7,14 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "rng.h"
+
 namespace rngk {
+
+// Record the calling thread's message (rng_last_error) and return the status.
+rng_status fail(rng_status st, const char *fmt, ...);
+rng_status cuda_fail(cudaError_t e, const char *what);
+void clear_error();
 
 // Threads per block of the streaming fill kernels.
 constexpr unsigned kFillThreads = 256;

@@ -1,0 +1,58 @@
+// layer_norm.h -- what the layer-norm kernels are launched with (host side of
+// layer_norm.cu, kernels in layer_norm_kernels.cuh).
+#pragma once
+
+#include "element.cuh"
+#include "internal.h"
+
+namespace rngk {
+
+template <class T>
+struct Rows {
+    T *p;
+    size_t stride;
+};
+
+struct NormFwd {
+    Rows<const void> x, residual;
+    Rows<void> y, h;
+    const void *bias, *gamma, *beta;
+    float *mean, *rstd;
+    size_t rows;
+    uint32_t cols;
+    float eps;
+    uint32_t first;
+    Mask mask;
+};
+
+struct NormBwd {
+    Rows<const void> dy, h, dh;
+    Rows<void> dx, dresidual;
+    const void *gamma;
+    const float *mean, *rstd;
+    void *dgamma, *dbeta, *dbias;
+    size_t rows;
+    uint32_t cols;
+    uint32_t first;
+    Mask mask;
+    float *workspace;
+};
+
+// Elements of one vector access of the rows: 16 bytes, or 1 when a row or an
+// address is not on that boundary.
+template <class T, class W>
+cudaError_t launch_norm_fwd(const NormFwd &a, bool vectors, cudaStream_t s);
+template <class T, class W>
+cudaError_t launch_norm_bwd(const NormBwd &a, bool vectors, cudaStream_t s);
+
+// How the backward pass is cut: the fused kernel's blocks (threads threads
+// share a row of cols columns, per_block rows at a time), or for long rows the
+// two-kernel form's chunks of rows.
+struct NormBwdPlan {
+    bool fused;
+    unsigned group, per_block, blocks;
+    size_t workspace_floats;
+};
+NormBwdPlan norm_bwd_plan(size_t rows, size_t cols);
+
+}  // namespace rngk

@@ -248,6 +248,149 @@ rng_status rng_dropout_fwd(const float *x, float *y, float p, uint32_t seed,
 rng_status rng_dropout_bwd(const float *dy, float *dx, float p, uint32_t seed,
                            uint32_t first_counter, size_t n, void *stream);
 
+/* ---- a transformer layer's dropout, fused with what surrounds it ----------- */
+/* The mask is dropout's above and is stored in neither direction: element e of
+ * a masked array, e its flat index, is kept iff uniform(seed, first_counter +
+ * e) >= p, and a kept value is scaled by the binary32 value of 1 / (1 - p).
+ * p = 0 draws nothing.  All arithmetic is binary32; an output is rounded once
+ * to its type. */
+
+/* Element types. */
+typedef int rng_dtype;
+#define RNG_F32 0
+#define RNG_F16 1
+#define RNG_BF16 2
+
+/* Bias, dropout, residual and layer norm of a [rows, cols] array:
+ *
+ *   h = residual + dropout(x + bias)           e = row * cols + column
+ *   mean, rstd = mean of h's row, 1 / sqrt(variance + eps)
+ *   y = (h - mean) * rstd * gamma + beta
+ *
+ * x, residual, y and h have type `dtype`; bias, gamma and beta (cols each)
+ * have type `param_dtype`, which is dtype or RNG_F32; mean and rstd (rows
+ * each) are f32.  bias, residual, gamma, beta, h, mean and rstd may be NULL
+ * (0, 0, 1, 0, not stored, not stored, not stored).  The norm is taken of the
+ * unrounded h.  Rows start x_stride, ... elements apart (a stride is not
+ * looked at for a NULL array); columns are adjacent.
+ * y and h may each be x's or residual's own array (same address and stride);
+ * any other overlap of an output with another array is RNG_EINVAL, as are a
+ * stride below cols (with rows > 1), a missing x or y, p outside [0, 1) and a
+ * negative or non-finite eps.  rows == 0 or cols == 0 is a no-op. */
+rng_status rng_dropout_layer_norm_fwd(const void *x, size_t x_stride, const void *bias, const void *residual,
+                                      size_t residual_stride, const void *gamma, const void *beta, void *y,
+                                      size_t y_stride, void *h, size_t h_stride, float *mean, float *rstd,
+                                      size_t rows, size_t cols, rng_dtype dtype, rng_dtype param_dtype, float p,
+                                      uint32_t seed, uint32_t first_counter, float eps, void *stream);
+
+/* Its gradient.  From dy, the stored h, mean and rstd, and dh (NULL: 0), the
+ * gradient that reaches h past the norm:
+ *
+ *   g  = dy * gamma,  n = (h - mean) * rstd
+ *   dz = rstd * (g - mean(g) - n * mean(g * n)) + dh
+ *   dresidual = dz,   dx = dropout(dz)  (the forward mask, redrawn)
+ *   dgamma = sum over rows of dy * n,  dbeta = of dy,  dbias = of dx
+ *
+ * dresidual, dgamma, dbeta and dbias may be NULL (not wanted); dgamma, dbeta
+ * and dbias have type param_dtype, are summed in f32 in an order that depends
+ * on the sizes and alignment alone, and are written (not added to): zeros for rows == 0.
+ * dx and dresidual may each be dy's or dh's own array.  `workspace` holds
+ * rng_dropout_layer_norm_bwd_workspace(rows, cols) bytes at a 16-byte
+ * boundary (NULL where that is 0); it belongs to the call until its work is
+ * done.  Other errors as above; a workspace that is too small is RNG_EINVAL. */
+rng_status rng_dropout_layer_norm_bwd(const void *dy, size_t dy_stride, const void *h, size_t h_stride,
+                                      const void *dh, size_t dh_stride, const void *gamma, const float *mean,
+                                      const float *rstd, void *dx, size_t dx_stride, void *dresidual,
+                                      size_t dresidual_stride, void *dgamma, void *dbeta, void *dbias, size_t rows,
+                                      size_t cols, rng_dtype dtype, rng_dtype param_dtype, float p, uint32_t seed,
+                                      uint32_t first_counter, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that rng_dropout_layer_norm_bwd needs on the current device. */
+size_t rng_dropout_layer_norm_bwd_workspace(size_t rows, size_t cols);
+
+/* Attention with a learned relative position bias by buckets and dropout on
+ * its probabilities.  For batch b, query i, head a (of heads_q; it reads key
+ * head a / (heads_q / heads_kv)) and key j:
+ *
+ *   s = scale * <q, k> + bias_table[rng_relative_bucket(j - pos(i)), a]
+ *   P = softmax over the visible j of s,  lse = log of the sum of exp(s)
+ *   o = sum over j of dropout(P) v,       e = ((b heads_q + a) len_q + i) len_k + j
+ *
+ * pos(i) = i, or with queries_last i + n(b) - len_q (the queries are the last
+ * len_q of the keys: a decoding step, a later piece of a prompt).  Key j is
+ * visible iff j < n(b) and, when causal, j <= pos(i).  n(b) is
+ * key_lengths[b], taken into [0, len_k], or len_k without key_lengths.  Keys
+ * at or past n(b) have no influence, whatever their bits.  A query that sees
+ * no key gets o = 0, lse = -inf and passes no gradient.
+ *
+ * The struct holds device pointers and sizes; it is read during the call
+ * only.  q, k, v, o (and their gradients) are [batch, length, heads,
+ * head_dim] arrays of type dtype (RNG_F16 or RNG_BF16) whose strides are
+ * given in elements in the order batch, length, head; head_dim is adjacent.
+ * Each address is a multiple of 16 bytes and each stride of 8 elements (of a
+ * dimension of size 1, any); head_dim is a multiple of 8 up to 128; heads_q
+ * is a multiple of heads_kv.  bias_table (NULL: none) is [num_buckets,
+ * heads_q] of type dtype, contiguous.  lse is [batch, heads_q, len_q] f32.
+ *
+ * s, the softmax statistics and all sums are f32; P (before its division by
+ * the row's sum) and, in the backward pass, P and dS are rounded to dtype as
+ * the operands of the matrix products that follow. */
+typedef struct rng_attention_args {
+    rng_dtype dtype;
+    int32_t batch, len_q, len_k, heads_q, heads_kv, head_dim;
+    const void *q, *k, *v;
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    void *o; /* backward: read */
+    int64_t o_stride[3];
+    float *lse; /* forward: may be NULL; backward: read */
+    const int32_t *key_lengths; /* [batch] or NULL */
+    int32_t causal, queries_last;
+    float scale;
+    const void *bias_table; /* or NULL */
+    int32_t num_buckets, max_distance, bidirectional;
+    float p;
+    uint32_t seed, first_counter;
+    /* backward only */
+    const void *d_o;
+    void *dq, *dk, *dv;
+    int64_t do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+    void *dbias_table; /* [num_buckets, heads_q] of type dtype, written; or NULL */
+    /* both: rng_attention_{fwd,bwd}_workspace(args) bytes at a 16-byte boundary */
+    void *workspace;
+    size_t workspace_bytes;
+} rng_attention_args;
+
+/* Forward: o and lse.  RNG_EINVAL: what the struct's description rules out, p
+ * outside [0, 1), a scale that is not finite, num_buckets and max_distance
+ * that rng_relative_bucket refuses (with a table), 2^31 or more of a length,
+ * an output that overlaps an input.  An empty output is a no-op; len_k == 0
+ * with queries gives o = 0. */
+rng_status rng_attention_fwd(const rng_attention_args *args, void *stream);
+
+/* Backward: dq, dk, dv and dbias_table from d_o and the forward's o and lse;
+ * with delta = <d_o, o> and dP = dropout of <d_o, v>,
+ *   dS = P (dP - delta),  dq = scale sum_j dS k,  dk = scale sum_i dS q,
+ *   dv = sum_i dropout(P) d_o,  dbias_table[n, a] = sum of dS in bucket n.
+ * dk and dv of a key head are summed over its query heads.  No atomics: the
+ * results are the same bits every time. */
+rng_status rng_attention_bwd(const rng_attention_args *args, void *stream);
+
+/* Bytes of workspace on the current device (pointers are not looked at,
+ * except whether bias_table and dbias_table are NULL). */
+size_t rng_attention_fwd_workspace(const rng_attention_args *args);
+size_t rng_attention_bwd_workspace(const rng_attention_args *args);
+
+/* The bucket of a relative position (key's minus query's).  With one
+ * direction's count m = num_buckets / 2 when bidirectional, else num_buckets:
+ * distance d < m / 2 has its own bucket d; above, bucket m / 2 + floor((m -
+ * m / 2) ln(d / (m / 2)) / ln(max_distance / (m / 2))), at most m - 1, by
+ * whole-number arithmetic.  Bidirectional: keys past the query use buckets m
+ * and up; otherwise their distance is 0.  RNG_EINVAL: num_buckets outside
+ * 2 (4 when bidirectional) .. 128 or odd when bidirectional, max_distance
+ * outside m / 2 + 1 .. 1024, bucket == NULL. */
+rng_status rng_relative_bucket(int64_t relative_position, int32_t num_buckets, int32_t max_distance,
+                               int32_t bidirectional, int32_t *bucket);
+
 /* ---- status -------------------------------------------------------------- */
 
 /* A static string naming the status code. */
