@@ -63,6 +63,7 @@ _FILL_SIGS = {
     "rng_relative_bucket": [_i64, _i32, _i32, _i32, C.POINTER(_i32)],
     "rng_debug_set_miss_capacity": [_sz],
     "rng_debug_last_miss_count": [C.POINTER(_u64)],
+    "rng_debug_stalled_waits": [C.POINTER(_u64)],
     "rng_debug_eval_f64": [_int, _p, _p, _sz, _p],
     "rng_debug_write_ceiling": [_int, _p, _sz, _p],
 }
@@ -530,6 +531,12 @@ def rng_debug_set_miss_capacity(capacity: int | None) -> None:
 def rng_debug_last_miss_count() -> int:
     c = _u64()
     _check(_lib.rng_debug_last_miss_count(C.byref(c)), "rng_debug_last_miss_count")
+    return c.value
+
+
+def rng_debug_stalled_waits() -> int:
+    c = _u64()
+    _check(_lib.rng_debug_stalled_waits(C.byref(c)), "rng_debug_stalled_waits")
     return c.value
 
 

@@ -292,4 +292,12 @@ rng_status rng_attention_bwd(const rng_attention_args *args, void *stream)
     return e == cudaSuccess ? RNG_OK : cuda_fail(e, what);
 }
 
+rng_status rng_debug_stalled_waits(uint64_t *count)
+{
+    if (!count) return fail(RNG_EINVAL, "rng_debug_stalled_waits: count is NULL");
+    clear_error();
+    const cudaError_t e = stalled_waits_fwd(count);
+    return e == cudaSuccess ? RNG_OK : cuda_fail(e, "rng_debug_stalled_waits");
+}
+
 }  // extern "C"

@@ -42,6 +42,9 @@ struct Attention {
 rng_status relative_buckets(const char *what, int32_t num_buckets, int32_t max_distance, bool bidirectional,
                             Buckets *out);
 
+// Waits that ran out in the forward and the backward kernels, on the current device.
+cudaError_t stalled_waits_fwd(uint64_t *count);
+
 size_t attention_fwd_workspace(const Attention &a);
 size_t attention_bwd_workspace(const Attention &a);
 template <class T>

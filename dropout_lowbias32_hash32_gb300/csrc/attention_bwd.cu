@@ -1,5 +1,4 @@
-// attention_kernels.cu -- attention with bucketed bias and dropout, forward
-// and backward (include/rng.h, rng_attention_*): one warp to a query (or key),
+// attention_bwd.cu -- attention backward (include/rng.h, rng_attention_bwd): one warp to a query (or key),
 // 32 keys (queries) at a time, a lane to each for the scores and a lane to
 // every 32nd column of the head dimension for the products.
 #include "attention.h"
@@ -54,12 +53,6 @@ __device__ __forceinline__ float warp_sum(float v)
     for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v)
-{
-    for (int m = 16; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
-    return v;
-}
-
 // The score of a visible pair.
 template <class T>
 __device__ float score(const Attention &a, const T *q, const T *k, int32_t head, int32_t rel)
@@ -72,37 +65,6 @@ __device__ float score(const Attention &a, const T *q, const T *k, int32_t head,
 __device__ __forceinline__ uint32_t counter(const Attention &a, const Place &x, uint32_t j)
 {
     return a.first + ((static_cast<uint32_t>(x.b) * a.heads + x.a) * a.len_q + x.i) * static_cast<uint32_t>(a.len_k) + j;
-}
-
-template <class T>
-__global__ void __launch_bounds__(128) fwd_kernel(const __grid_constant__ Attention a)
-{
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.y;
-    if (row >= static_cast<int64_t>(a.batch) * a.heads * a.len_q) return;
-    const uint32_t lane = threadIdx.x;
-    const Place x = place_of(row, a.heads, a.len_q);
-    const int32_t keys = keys_of(a, x.b), pos = first_position(a, keys) + x.i, hk = x.a / a.group;
-    const int32_t end = a.causal && pos + 1 < keys ? pos + 1 : keys;
-    const T *q = at<T>(a.q, a.qs, x.b, x.i, x.a);
-    float acc[kCols] = {}, top = -INFINITY, sum = 0.0f;
-    for (int32_t j0 = 0; j0 < end; j0 += 32) {
-        const int32_t j = j0 + lane;
-        const float s = j < end ? score(a, q, at<T>(a.k, a.ks, x.b, j, hk), x.a, j - pos) : -INFINITY;
-        const float next = fmaxf(top, warp_max(s));
-        const float base = next == -INFINITY ? 0.0f : next;
-        const float fade = __expf(top - base);
-        float p = __expf(s - base);
-        sum = sum * fade + warp_sum(p);
-        top = next;
-        if (a.mask.threshold && !keeps(a.mask, counter(a, x, j))) p = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) acc[k] *= fade;
-        for (int k = 0; k < 32 && j0 + k < end; ++k)
-            add_row(acc, __shfl_sync(0xFFFFFFFFu, p, k), at<T>(a.v, a.vs, x.b, j0 + k, hk), a.dim, lane);
-    }
-    T *o = static_cast<T *>(a.out) + x.b * a.os.batch + x.i * a.os.len + x.a * a.os.head;
-    put_row(o, acc, sum != 0.0f ? a.mask.scale / sum : 0.0f, a.dim, lane);
-    if (a.lse && lane == 0) a.lse[row] = sum != 0.0f ? top + logf(sum) : -INFINITY;
 }
 
 // Workspace of the backward pass: delta of every query, then each query's
@@ -221,19 +183,9 @@ __global__ void __launch_bounds__(256) dtable_kernel(const __grid_constant__ Att
 
 }  // namespace
 
-size_t attention_fwd_workspace(const Attention &) { return 0; }
-
 size_t attention_bwd_workspace(const Attention &a)
 {
     return static_cast<size_t>(queries(a)) * (1 + (a.dtable ? a.buckets.total : 0)) * sizeof(float);
-}
-
-template <class T>
-cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s)
-{
-    fwd_kernel<T><<<static_cast<unsigned>((queries(a) + 3) / 4), dim3(32, 4), 0, s>>>(a);
-    note_launch();
-    return cudaGetLastError();
 }
 
 template <class T>
@@ -255,8 +207,6 @@ cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template cudaError_t launch_attention_fwd<__half>(const Attention &, cudaStream_t);
-template cudaError_t launch_attention_fwd<__nv_bfloat16>(const Attention &, cudaStream_t);
 template cudaError_t launch_attention_bwd<__half>(const Attention &, cudaStream_t);
 template cudaError_t launch_attention_bwd<__nv_bfloat16>(const Attention &, cudaStream_t);
 

@@ -480,3 +480,8 @@ def test_python_refusals(torch, rng):
         call(q.float(), q.float(), q.float(), o.float())
     with pytest.raises(ValueError):
         rng.rng_attention_bwd(o, q, q, q, o, torch.zeros(2, 2, 4, device="cuda"), o, o, o, dbias_table=o)
+
+
+@pytest.mark.gpu
+def test_no_wait_ran_out(rng):
+    assert rng.rng_debug_stalled_waits() == 0
