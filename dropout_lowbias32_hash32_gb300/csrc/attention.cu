@@ -296,7 +296,10 @@ rng_status rng_debug_stalled_waits(uint64_t *count)
 {
     if (!count) return fail(RNG_EINVAL, "rng_debug_stalled_waits: count is NULL");
     clear_error();
-    const cudaError_t e = stalled_waits_fwd(count);
+    uint64_t forward = 0, backward = 0;
+    cudaError_t e = stalled_waits_fwd(&forward);
+    if (e == cudaSuccess) e = stalled_waits_bwd(&backward);
+    *count = forward + backward;
     return e == cudaSuccess ? RNG_OK : cuda_fail(e, "rng_debug_stalled_waits");
 }
 

@@ -44,6 +44,7 @@ rng_status relative_buckets(const char *what, int32_t num_buckets, int32_t max_d
 
 // Waits that ran out in the forward and the backward kernels, on the current device.
 cudaError_t stalled_waits_fwd(uint64_t *count);
+cudaError_t stalled_waits_bwd(uint64_t *count);
 
 size_t attention_fwd_workspace(const Attention &a);
 size_t attention_bwd_workspace(const Attention &a);
@@ -73,5 +74,18 @@ __device__ __forceinline__ int32_t keys_of(const Attention &a, int32_t b)
     return n < 0 ? 0 : n > a.len_k ? a.len_k : n;
 }
 __device__ __forceinline__ int32_t first_position(const Attention &a, int32_t keys) { return a.last ? keys - a.len_q : 0; }
+
+// The bias by relative position is tabulated for -reach .. reach - 1, which
+// covers the 159 positions of 32 queries by 128 keys that reach past the last
+// bucket's start.
+__host__ __device__ __forceinline__ int32_t bias_reach(const Buckets &b) { return b.max_distance + 160; }
+
+// Heads of one key head that lie side by side in a tile of 128 rows, so that
+// they read its keys once: all of them, where a tile is a whole number of
+// them and no head has a bias of its own.
+inline int32_t packed_heads(const Attention &a)
+{
+    return !a.table && a.group <= 64 && (a.group & (a.group - 1)) == 0 ? a.group : 1;
+}
 
 }  // namespace rngk

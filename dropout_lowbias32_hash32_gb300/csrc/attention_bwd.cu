@@ -1,178 +1,677 @@
-// attention_bwd.cu -- attention backward (include/rng.h, rng_attention_bwd): one warp to a query (or key),
-// 32 keys (queries) at a time, a lane to each for the scores and a lane to
-// every 32nd column of the head dimension for the products.
-#include "attention.h"
+// attention_bwd.cu -- attention backward (include/rng.h, rng_attention_bwd) on
+// the tensor cores.
+//
+// Two kernels, each of which draws the probabilities and the mask again, so
+// that every sum has one owner and no atomics: query_kernel (a block per 256
+// queries, over the keys) gives dq, the bias table's gradient and each query's
+// (lse, delta); key_kernel (a block per 128 keys, over the queries of all heads
+// of the key head) gives dk and dv.  S and dP come from two products into TMEM
+// by tiles of 128 x 64; the threads of one of two slots turn them into dS (and
+// P), written back over S in 16 bits as the TMEM operand of the products
+// that accumulate dq (dk, dv), while the tensor core works for the other slot.
+// The tile of 64 lets both slots' scores and both accumulators of a head
+// dimension of 128 fit the 512 TMEM columns.
+#include "tensor_core.cuh"
+#include "tensor_map.h"
 
 namespace rngk {
 namespace {
 
-constexpr int kCols = 4;  // columns of a head (up to 128) in a lane
+constexpr int kRows = 128, kCols = 64;  // a slot's tile
+constexpr int kThreads = 384;           // 2 x 128 for the slots, then a TMA warp, an MMA warp, two that only fill the warpgroup
+// registers: 384 threads start with 168 each; 2 x 208 + 88 = 3 x 168
+constexpr int kSlotRegisters = 208, kOtherRegisters = 88;
+constexpr uint32_t kRowsBox = 16384, kColsBox = 8192;  // bytes of 128 and of 64 rows of 64 elements
+constexpr float kLog2e = 1.4426950408889634f;
 
-struct Place {
-    int32_t b, a, i;  // batch, head, position
+// P's scale as the 16-bit operand of dv: f16 would lose the probabilities of
+// long rows to its smallest step (2^-24), so they are held times 2^10; they are
+// at most 1.
+template <class T>
+constexpr float kLift = 0.0f;
+template <>
+constexpr float kLift<__half> = 10.0f;
+
+struct BwdParams {
+    CUtensorMap q_rows, do_rows, k_cols, v_cols;  // query_kernel's
+    CUtensorMap k_rows, v_rows, q_cols, do_cols;  // key_kernel's
+    Attention a;
+    int32_t pack, units, q_tiles, len_pad;
+    // [batch heads][len_pad]: lse (in base two unless there is a bias; +inf for a query that sees nothing) and
+    // delta; [heads][2 reach]: the bias by relative position; [batch heads][q_tiles][buckets]: sums of dS
+    float2 *stats;
+    float *bias, *sums;
 };
 
-__device__ __forceinline__ Place place_of(int64_t row, int32_t heads, int32_t len)
-{
-    const int64_t ba = row / len;
-    return Place{static_cast<int32_t>(ba / heads), static_cast<int32_t>(ba % heads), static_cast<int32_t>(row % len)};
-}
+__device__ __forceinline__ bool is_plain(const Attention &a) { return a.table == nullptr; }
 
-template <class T>
-__device__ __forceinline__ const T *at(const void *p, const Strides &s, int64_t b, int64_t l, int64_t h)
-{
-    return static_cast<const T *>(p) + b * s.batch + l * s.len + h * s.head;
-}
+// ---- dq ------------------------------------------------------------------------
 
-template <class T>
-__device__ float dot(const T *x, const T *y, int32_t n)
-{
-    float s = 0.0f;
-    for (int32_t d = 0; d < n; ++d) s += to_f32(x[d]) * to_f32(y[d]);
-    return s;
-}
+template <int kDim, bool kSplitKeys>
+struct QueryShape {
+    static constexpr int kBoxes = kDim / 64;
+    static constexpr int kTiles = kSplitKeys ? 1 : 2;
+    static constexpr uint32_t kRowsBytes = kBoxes * kRowsBox, kColsBytes = kBoxes * kColsBox;
+    static constexpr int kKeyStages = kDim == 64 ? 6 : kSplitKeys ? 5 : 3, kValueStages = kDim == 64 ? 4 : kSplitKeys ? 3 : 2;
+    static constexpr uint32_t kDo = kTiles * kRowsBytes, kKeys = 2 * kDo, kValues = kKeys + kKeyStages * kColsBytes;
+    static constexpr uint32_t kTable = kValues + kValueStages * kColsBytes;
+};
 
-template <class T>
-__device__ __forceinline__ void add_row(float (&acc)[kCols], float w, const T *row, int32_t dim, uint32_t lane)
+// The relative positions of a bucket, lo .. hi (empty: lo > hi).
+__device__ __forceinline__ void bucket_range(const Buckets &b, int32_t n, int32_t &lo, int32_t &hi)
 {
-#pragma unroll
-    for (int k = 0; k < kCols; ++k)
-        if (lane + 32 * k < dim) acc[k] += w * to_f32(row[lane + 32 * k]);
-}
-
-template <class T>
-__device__ __forceinline__ void put_row(T *row, const float (&acc)[kCols], float w, int32_t dim, uint32_t lane)
-{
-#pragma unroll
-    for (int k = 0; k < kCols; ++k)
-        if (lane + 32 * k < dim) row[lane + 32 * k] = from_f32<T>(acc[k] * w);
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-    return v;
-}
-// The score of a visible pair.
-template <class T>
-__device__ float score(const Attention &a, const T *q, const T *k, int32_t head, int32_t rel)
-{
-    float s = dot(q, k, a.dim) * a.scale;
-    if (a.table) s += to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, rel) * a.heads + head]);
-    return s;
-}
-
-__device__ __forceinline__ uint32_t counter(const Attention &a, const Place &x, uint32_t j)
-{
-    return a.first + ((static_cast<uint32_t>(x.b) * a.heads + x.a) * a.len_q + x.i) * static_cast<uint32_t>(a.len_k) + j;
-}
-
-// Workspace of the backward pass: delta of every query, then each query's
-// sums of dS by bucket.
-__host__ __device__ __forceinline__ int64_t queries(const Attention &a)
-{
-    return static_cast<int64_t>(a.batch) * a.heads * a.len_q;
-}
-
-// The probability of a visible pair and its dS.
-template <class T>
-__device__ __forceinline__ void gradient(const Attention &a, const T *q, const T *k, const T *v, const T *d_o, float lse,
-                                         float delta, const Place &x, int32_t j, int32_t pos, float &kept, float &ds)
-{
-    // a query that sees no key, or only scores of -inf, has lse = -inf
-    const float p = lse == -INFINITY ? 0.0f : __expf(score(a, q, k, x.a, j - pos) - lse);
-    float dp = dot(d_o, v, a.dim);
-    kept = p;
-    if (a.mask.threshold) {
-        const float keep = keeps(a.mask, counter(a, x, j)) ? a.mask.scale : 0.0f;
-        kept *= keep, dp *= keep;
+    constexpr int32_t kFar = 1 << 30;
+    const bool past = b.past && n >= b.past;
+    const int32_t k = past ? n - b.past : n;
+    const int32_t near = k == 0 ? 0 : b.starts[k - 1], far = k == b.count - 1 ? kFar : b.starts[k] - 1;
+    if (n >= b.total) {
+        lo = 1, hi = 0;
+    } else if (past) {
+        lo = max(near, 1), hi = far;
+    } else {
+        lo = -far, hi = -near;
+        if (!b.past && k == 0) hi = kFar;  // one way: every key past the query
     }
-    ds = p * (dp - delta);
 }
 
-template <class T>
-__global__ void __launch_bounds__(128) dq_kernel(const __grid_constant__ Attention a)
+template <class T, int kDim, bool kSplitKeys>
+__global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constant__ BwdParams p)
 {
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.y;
-    if (row >= queries(a)) return;
-    const uint32_t lane = threadIdx.x;
-    const Place x = place_of(row, a.heads, a.len_q);
-    const int32_t keys = keys_of(a, x.b), pos = first_position(a, keys) + x.i, hk = x.a / a.group;
-    const int32_t end = a.causal && pos + 1 < keys ? pos + 1 : keys;
-    const T *q = at<T>(a.q, a.qs, x.b, x.i, x.a), *o = at<T>(a.o, a.os, x.b, x.i, x.a);
-    const T *d_o = at<T>(a.d_o, a.dos, x.b, x.i, x.a);
-    float *ws = static_cast<float *>(a.workspace);
-    float delta = 0.0f, lse = a.lse[row], acc[kCols] = {}, by_bucket[kMaxBuckets / 32] = {};
-    for (int32_t d = lane; d < a.dim; d += 32) delta += to_f32(o[d]) * to_f32(d_o[d]);
-    delta = warp_sum(delta);
-    if (lane == 0) ws[row] = delta;
-    for (int32_t j0 = 0; j0 < end; j0 += 32) {
-        const int32_t j = j0 + lane;
-        float kept, ds = 0.0f;
-        if (j < end)
-            gradient(a, q, at<T>(a.k, a.ks, x.b, j, hk), at<T>(a.v, a.vs, x.b, j, hk), d_o, lse, delta, x, j, pos, kept, ds);
-        const int32_t bucket = a.dtable ? bucket_of(a.buckets, j - pos) : 0;
-        for (int k = 0; k < 32 && j0 + k < end; ++k) {
-            const float w = __shfl_sync(0xFFFFFFFFu, ds, k);
-            add_row(acc, w, at<T>(a.k, a.ks, x.b, j0 + k, hk), a.dim, lane);
-            const uint32_t n = __shfl_sync(0xFFFFFFFFu, bucket, k);
-#pragma unroll
-            for (uint32_t m = 0; m < kMaxBuckets / 32; ++m)
-                if (n == lane + 32 * m) by_bucket[m] += w;
+    using S = QueryShape<kDim, kSplitKeys>;
+    extern __shared__ uint8_t dynamic[];
+    __shared__ alignas(8) uint64_t bars[2 * (S::kKeyStages + S::kValueStages) + 8];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile uint32_t stalled;
+    __shared__ float diagonals[8][96], by_bucket[8][kMaxBuckets];
+    const Attention &a = p.a;
+    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+    uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
+    const uint32_t base = smem_address(smem);
+    float *table = reinterpret_cast<float *>(smem + S::kTable);
+
+    // ---- the block's work
+    int32_t unit, q_tile;
+    if (a.causal) {  // the longest first
+        unit = blockIdx.x % p.units, q_tile = p.q_tiles - 1 - blockIdx.x / p.units;
+    } else {
+        q_tile = blockIdx.x % p.q_tiles, unit = blockIdx.x / p.q_tiles;
+    }
+    const int32_t packs = a.heads / p.pack, b = unit / packs, pack = unit % packs;
+    const int32_t head0 = pack * p.pack, head_kv = head0 / a.group;
+    const int32_t rows_per = kRows / p.pack;
+    const int32_t i0 = q_tile * S::kTiles * rows_per;
+    const int32_t keys = keys_of(a, b), pos0 = first_position(a, keys);
+    int32_t count[2];
+    for (int s = 0; s < 2; ++s) {
+        const int32_t last = min(i0 + (kSplitKeys ? 1 : s + 1) * rows_per, a.len_q) - 1;  // the slot's last query
+        int32_t end = a.causal ? min(keys, pos0 + last + 1) : keys;
+        if (!kSplitKeys && i0 + s * rows_per >= a.len_q) end = 0;
+        count[s] = max(0, (end + kCols - 1) / kCols);
+    }
+    const int32_t tiles = max(count[0], count[1]);
+
+    const uint32_t k_full = smem_address(bars), k_empty = k_full + 8 * S::kKeyStages, v_full = k_empty + 8 * S::kKeyStages,
+                   v_empty = v_full + 8 * S::kValueStages, scored = v_empty + 8 * S::kValueStages, ready = scored + 16,
+                   done = ready + 16, q_full = done + 8, tail = q_full + 8;
+    if (threadIdx.x == 0) {
+        stalled = 0;
+        for (int s = 0; s < S::kKeyStages; ++s) barrier_init(k_full + 8 * s, 1), barrier_init(k_empty + 8 * s, 1);
+        for (int s = 0; s < S::kValueStages; ++s) barrier_init(v_full + 8 * s, 1), barrier_init(v_empty + 8 * s, 1);
+        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4);
+        barrier_init(done, 1), barrier_init(q_full, 1), barrier_init(tail, 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) tmem_alloc<512>(smem_address(&tmem_base));
+    if (a.table) {  // the bias by relative position, head head0 (pack is 1)
+        const int32_t reach = bias_reach(a.buckets);
+        for (int32_t t = threadIdx.x; t < 2 * reach; t += kThreads) {
+            table[t] = to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, t - reach) * a.heads + head0]);
+            if (b == 0 && q_tile == 0) p.bias[static_cast<int64_t>(head0) * 2 * reach + t] = table[t];
         }
     }
-    put_row(static_cast<T *>(a.dq) + x.b * a.dqs.batch + x.i * a.dqs.len + x.a * a.dqs.head, acc, a.scale, a.dim, lane);
-    if (a.dtable)
-        for (uint32_t m = 0; m < kMaxBuckets / 32; ++m)
-            if (lane + 32 * m < a.buckets.total)
-                ws[queries(a) + row * a.buckets.total + lane + 32 * m] = by_bucket[m];
-}
-
-template <class T>
-__global__ void __launch_bounds__(128) dkv_kernel(const __grid_constant__ Attention a)
-{
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.y;
-    if (row >= static_cast<int64_t>(a.batch) * a.heads_kv * a.len_k) return;
-    const uint32_t lane = threadIdx.x;
-    const Place y = place_of(row, a.heads_kv, a.len_k);
-    const int32_t keys = keys_of(a, y.b), pos0 = first_position(a, keys), j = y.i;
-    const T *k = at<T>(a.k, a.ks, y.b, j, y.a), *v = at<T>(a.v, a.vs, y.b, j, y.a);
-    const float *ws = static_cast<const float *>(a.workspace);
-    float dk[kCols] = {}, dv[kCols] = {};
-    int32_t begin = a.causal && j > pos0 ? j - pos0 : 0;  // the first query that sees key j
-    if (j >= keys) begin = a.len_q;
-    for (int32_t h = y.a * a.group; h < (y.a + 1) * a.group; ++h) {
-        for (int32_t i0 = begin; i0 < a.len_q; i0 += 32) {
-            const int32_t i = i0 + lane;
-            const Place x{y.b, h, i};
-            float kept = 0.0f, ds = 0.0f;
-            if (i < a.len_q) {
-                const int64_t r = (static_cast<int64_t>(y.b) * a.heads + h) * a.len_q + i;
-                gradient(a, at<T>(a.q, a.qs, y.b, i, h), k, v, at<T>(a.d_o, a.dos, y.b, i, h), a.lse[r], ws[r], x, j,
-                         pos0 + i, kept, ds);
+    if (q_tile == p.q_tiles - 1)  // what key_kernel reads past the last query
+        for (int32_t t = threadIdx.x; t < p.pack * (p.len_pad - a.len_q); t += kThreads)
+            p.stats[(static_cast<int64_t>(b) * a.heads + head0 + t % p.pack) * p.len_pad + a.len_q + t / p.pack] =
+                make_float2(INFINITY, 0.0f);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_base;
+    if (warp >= 8) {
+        give_registers<kOtherRegisters>();
+        if (warp == 8) {
+            // ---- TMA: q and do, then K_n and V_n
+            const bool one = elect_one();
+            if (one && tiles) {
+                barrier_expect(q_full, 2 * S::kDo);
+                for (int t = 0; t < S::kTiles; ++t)
+                    for (int c = 0; c < S::kBoxes; ++c) {
+                        const uint32_t o = t * S::kRowsBytes + c * kRowsBox;
+                        tma_load_5d(base + o, &p.q_rows, q_full, c * 64, 0, i0 + t * rows_per, pack, b);
+                        tma_load_5d(base + S::kDo + o, &p.do_rows, q_full, c * 64, 0, i0 + t * rows_per, pack, b);
+                    }
             }
-            for (int n = 0; n < 32 && i0 + n < a.len_q; ++n) {
-                add_row(dk, __shfl_sync(0xFFFFFFFFu, ds, n), at<T>(a.q, a.qs, y.b, i0 + n, h), a.dim, lane);
-                add_row(dv, __shfl_sync(0xFFFFFFFFu, kept, n), at<T>(a.d_o, a.dos, y.b, i0 + n, h), a.dim, lane);
+            for (int32_t n = 0; n < tiles; ++n) {
+                const int32_t j0 = n * kCols;
+                const uint32_t ks = n % S::kKeyStages, vs = n % S::kValueStages;
+                barrier_wait(k_empty + 8 * ks, (n / S::kKeyStages & 1u) ^ 1u, &stalled);
+                // keys past n(b) that the array holds: whatever they are, dS's zeros must meet zeros
+                const bool past = j0 + kCols > keys && keys < a.len_k;
+                const uint32_t on = past ? tail : k_full + 8 * ks, dst = base + S::kKeys + ks * S::kColsBytes;
+                if (one) {
+                    barrier_expect(on, S::kColsBytes);
+                    for (int c = 0; c < S::kBoxes; ++c) tma_load_5d(dst + c * kColsBox, &p.k_cols, on, c * 64, 0, j0, head_kv, b);
+                }
+                if (past) {
+                    barrier_wait(tail, 0, &stalled);
+                    uint8_t *rows = smem + S::kKeys + ks * S::kColsBytes;
+                    for (int c = 0; c < S::kBoxes; ++c)
+                        for (uint32_t o = max(0, keys - j0) * 128u + lane * 16u; o < kColsBox; o += 512u)
+                            *reinterpret_cast<uint4 *>(rows + c * kColsBox + o) = make_uint4(0, 0, 0, 0);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (one) barrier_arrive(k_full + 8 * ks);
+                }
+                barrier_wait(v_empty + 8 * vs, (n / S::kValueStages & 1u) ^ 1u, &stalled);
+                if (one) {
+                    barrier_expect(v_full + 8 * vs, S::kColsBytes);
+                    for (int c = 0; c < S::kBoxes; ++c)
+                        tma_load_5d(base + S::kValues + vs * S::kColsBytes + c * kColsBox, &p.v_cols, v_full + 8 * vs, c * 64, 0,
+                                    j0, head_kv, b);
+                }
+            }
+            if (stalled && one)  // nothing may land after the block has ended
+                for (int32_t n = max(0, tiles - S::kKeyStages); n < tiles; ++n)
+                    for (uint32_t tries = 0;
+                         tries < 100000 && !(barrier_try(k_full + 8 * (n % S::kKeyStages), n / S::kKeyStages & 1u) &&
+                                             barrier_try(v_full + 8 * (n % S::kValueStages), n / S::kValueStages & 1u));
+                         ++tries) {}
+        } else if (warp == 9) {
+            // ---- MMA
+            if (elect_one() && tiles) {
+                constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
+                uint32_t given0 = 0, given1 = 0;
+                auto scores = [&](int slot, int32_t n) {
+                    const uint32_t ks = n % S::kKeyStages, vs = n % S::kValueStages;
+                    const uint32_t q = base + (kSplitKeys ? 0 : slot) * S::kRowsBytes, k = base + S::kKeys + ks * S::kColsBytes,
+                                   v = base + S::kValues + vs * S::kColsBytes;
+                    barrier_wait(k_full + 8 * ks, n / S::kKeyStages & 1u, &stalled);
+                    tmem_fence_after();
+                    for (int i = 0; i < kDim / 16; ++i)
+                        mma_step(tmem + slot * 256, row_major_tile(q + i / 4 * kRowsBox + i % 4 * 32),
+                                 row_major_tile(k + i / 4 * kColsBox + i % 4 * 32), kScores, i > 0);
+                    barrier_wait(v_full + 8 * vs, n / S::kValueStages & 1u, &stalled);
+                    tmem_fence_after();
+                    for (int i = 0; i < kDim / 16; ++i)
+                        mma_step(tmem + slot * 256 + kCols, row_major_tile(q + S::kDo + i / 4 * kRowsBox + i % 4 * 32),
+                                 row_major_tile(v + i / 4 * kColsBox + i % 4 * 32), kScores, i > 0);
+                    mma_commit(scored + 8 * slot);
+                };
+                auto product = [&](int slot, int32_t n, bool first) {
+                    const uint32_t k = base + S::kKeys + n % S::kKeyStages * S::kColsBytes;
+                    barrier_wait(ready + 8 * slot, (slot ? given1++ : given0++) & 1u, &stalled);
+                    tmem_fence_after();
+                    for (int i = 0; i < kCols / 16; ++i)
+                        mma_step_tmem(tmem + slot * 256 + 2 * kCols, tmem + slot * 256 + i * 8,
+                                      column_major_tile(k + i * 2048, S::kBoxes > 1 ? kColsBox : 1024), kOut, !first || i > 0);
+                };
+                auto release_k = [&](int32_t n) { mma_commit(k_empty + 8 * (n % S::kKeyStages)); };
+                auto release_v = [&](int32_t n) { mma_commit(v_empty + 8 * (n % S::kValueStages)); };
+                barrier_wait(q_full, 0, &stalled);
+                if (kSplitKeys) {
+                    for (int32_t n = 0; n < 2 && n < tiles; ++n) scores(n, n), release_v(n);
+                    for (int32_t n = 0; n < tiles; ++n) {
+                        product(n & 1, n, n < 2), release_k(n);
+                        if (n + 2 < tiles) scores(n & 1, n + 2), release_v(n + 2);
+                    }
+                } else {
+                    for (int s = 0; s < 2; ++s)
+                        if (count[s]) scores(s, 0);
+                    release_v(0);
+                    for (int32_t n = 0; n < tiles; ++n) {
+                        for (int s = 0; s < 2; ++s) {
+                            if (n < count[s]) product(s, n, n == 0);
+                            if (n + 1 < count[s]) scores(s, n + 1);
+                        }
+                        release_k(n);
+                        if (n + 1 < tiles) release_v(n + 1);
+                    }
+                }
+                mma_commit(done);
             }
         }
+    } else {
+        take_registers<kSlotRegisters>();
+        // ---- the slots' rows
+        const int slot = warp / 4;
+        const int32_t r = (warp % 4) * 32 + lane;
+        const uint32_t mine = tmem + slot * 256 + ((warp % 4) * 32u << 16);
+        const uint32_t out = mine + 2 * kCols;
+        const int32_t row0 = kSplitKeys ? 0 : slot * kRows;
+        const int32_t warp_i = i0 + (row0 + (warp % 4) * 32) / p.pack;
+        const int32_t i = i0 + (row0 + r) / p.pack, head = head0 + r % p.pack;
+        const bool valid = i < a.len_q, any = warp_i < a.len_q, plain = is_plain(a);
+        const int32_t pos = pos0 + i;
+        const int64_t index = (static_cast<int64_t>(b) * a.heads + head);
+        const uint32_t counter = a.first + (static_cast<uint32_t>(index) * a.len_q + i) * static_cast<uint32_t>(a.len_k);
+        const int32_t visible = a.causal ? min(keys, pos + 1) : keys;
+        const int32_t warp_visible = a.causal ? min(keys, pos0 + warp_i + 1) : keys;
+        const int32_t reach = bias_reach(a.buckets);
+        const int32_t last_start = plain ? 0 : a.buckets.starts[a.buckets.count - 2];
+
+        float lse = INFINITY, delta = 0.0f;
+        if (valid) {
+            const T *o = static_cast<const T *>(a.o) + b * a.os.batch + i * a.os.len + head * a.os.head;
+            const T *d_o = static_cast<const T *>(a.d_o) + b * a.dos.batch + i * a.dos.len + head * a.dos.head;
+            for (int32_t d = 0; d < a.dim; d += 8) {
+                float x[8], y[8];
+                unpack<T, 8>(load<false, T, 8>(o + d), x);
+                unpack<T, 8>(load<false, T, 8>(d_o + d), y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) delta += x[e] * y[e];
+            }
+            lse = a.lse[index * a.len_q + i];
+            // a query that sees nothing: exp(s - inf) = 0 whatever its scores
+            lse = lse == -INFINITY ? INFINITY : plain ? lse * kLog2e : lse;
+            if (slot == 0 || !kSplitKeys) p.stats[index * p.len_pad + i] = make_float2(lse, delta);
+        }
+
+        float own[kMaxBuckets / 32] = {}, far_low = 0.0f, far_high = 0.0f;
+        const float scale = a.mask.scale;
+        uint32_t turn = 0;
+        for (int32_t n = kSplitKeys ? slot : 0; n < count[kSplitKeys ? 0 : slot]; n += kSplitKeys ? 2 : 1, ++turn) {
+            const int32_t j0 = n * kCols;
+            barrier_wait(scored + 8 * slot, turn & 1u, &stalled);
+            tmem_fence_after();
+            if (any) {
+                uint32_t v[4][32];  // S, then dP
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_load32(v[c], mine + 32 * c);
+                tmem_wait_load(v);
+                auto s = [&](int e) -> uint32_t & { return v[e / 32][e % 32]; };
+                auto dp = [&](int e) -> uint32_t & { return v[2 + e / 32][e % 32]; };
+                // P
+                const int32_t low = j0 - (pos0 + warp_i + 31), high = j0 + kCols - 1 - (pos0 + warp_i);
+                const bool far = high <= -last_start || low >= last_start;
+                if (plain) {
+                    const float to_base2 = a.scale * kLog2e;
+                    const float2 k2 = make_float2(to_base2, to_base2), l2 = make_float2(-lse, -lse);
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 2) {
+                        const float2 f = fma2(make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1))), k2, l2);
+                        s(e) = __float_as_uint(exp2_approx(f.x)), s(e + 1) = __float_as_uint(exp2_approx(f.y));
+                    }
+                } else {
+                    const float2 k2 = make_float2(a.scale, a.scale), l2 = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
+                    const float edge = far ? table[high <= -last_start ? 0 : 2 * reach - 1] : 0.0f;
+                    const float *t = table + (j0 - pos + reach);
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 2) {
+                        const float2 bias = far ? make_float2(edge, edge) : make_float2(t[e], t[e + 1]);
+                        float2 f = fma2(make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1))), k2, bias);
+                        f = mul2(add2(f, l2), b2);
+                        s(e) = __float_as_uint(exp2_approx(f.x)), s(e + 1) = __float_as_uint(exp2_approx(f.y));
+                    }
+                }
+                // dS = P (dP / (1 - p) - delta), dP dropped as P was
+                const uint32_t c0 = counter + j0;
+#pragma unroll
+                for (int e = 0; e < kCols; e += 2) {
+                    float2 d = fma2(make_float2(__uint_as_float(dp(e)), __uint_as_float(dp(e + 1))), make_float2(scale, scale),
+                                    make_float2(-delta, -delta));
+                    if (a.mask.threshold) {
+                        if (!keeps(a.mask, c0 + e)) d.x = -delta;
+                        if (!keeps(a.mask, c0 + e + 1)) d.y = -delta;
+                    }
+                    d = mul2(d, make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1))));
+                    s(e) = __float_as_uint(d.x), s(e + 1) = __float_as_uint(d.y);
+                }
+                if (j0 + kCols > warp_visible) {
+                    const int32_t seen = visible - j0;
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e)
+                        if (e >= seen) s(e) = 0;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e] = pack2<T>(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
+                    tmem_store16(mine + 16 * c, w);
+                }
+                tmem_wait_store();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(ready + 8 * slot);
+                if (a.dtable && far) {  // one bucket
+                    float2 total = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int e = 0; e < kCols; e += 2)
+                        total = add2(total, make_float2(valid ? __uint_as_float(s(e)) : 0.0f, valid ? __uint_as_float(s(e + 1)) : 0.0f));
+                    (high <= -last_start ? far_low : far_high) += total.x + total.y;
+                } else if (a.dtable) {
+                    // sums along the diagonals of the warp's 32 x 64 tile: a partial sum moves one row down with
+                    // each column; what leaves row 31, or is left in the last column, is a whole one
+                    float acc = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e) {
+                        acc = __shfl_up_sync(0xFFFFFFFFu, acc, 1);
+                        acc = (lane ? acc : 0.0f) + (valid ? __uint_as_float(s(e)) : 0.0f);
+                        if (lane == 31) diagonals[warp][e] = acc;
+                    }
+                    if (lane < 31) diagonals[warp][94 - lane] = acc;
+                    __syncwarp();
+                    // diagonal d is relative position low + d; a lane adds the buckets lane, lane + 32, ...
+#pragma unroll
+                    for (int m = 0; m < kMaxBuckets / 32; ++m) {
+                        if (32 * m < a.buckets.total) {
+                            int32_t from, to;
+                            bucket_range(a.buckets, lane + 32 * m, from, to);
+                            from = max(from - low, 0), to = min(to - low, 94);
+                            for (int32_t d = from; d <= to; ++d) own[m] += diagonals[warp][d];
+                        }
+                    }
+                    __syncwarp();
+                }
+            } else if (lane == 0) {
+                barrier_arrive(ready + 8 * slot);
+            }
+        }
+
+        // ---- the result
+        if (tiles) {
+            barrier_wait(done, 0, &stalled);
+            tmem_fence_after();
+        }
+        if (a.dtable) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) {
+                far_low += __shfl_xor_sync(0xFFFFFFFFu, far_low, m);
+                far_high += __shfl_xor_sync(0xFFFFFFFFu, far_high, m);
+            }
+#pragma unroll
+            for (int m = 0; m < kMaxBuckets / 32; ++m) {
+                const int32_t bucket = lane + 32 * m;
+                if (bucket == a.buckets.count - 1) own[m] += far_low;
+                if (bucket == (a.buckets.past ? a.buckets.total - 1 : 0)) own[m] += far_high;
+                by_bucket[warp][bucket] = own[m];
+            }
+        }
+        float *hand = reinterpret_cast<float *>(smem + S::kKeys);  // nothing reads the tiles any more
+        const bool two = kSplitKeys && tiles > 1;
+        if (two && slot == 1 && any) {
+#pragma unroll
+            for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t o[1][32];
+                tmem_load32(o[0], out + 32 * c);
+                tmem_wait_load(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) hand[(32 * c + e) * kRows + r] = __uint_as_float(o[0][e]);
+            }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (a.dtable && threadIdx.x < a.buckets.total) {
+            float s = 0.0f;
+            for (int w = 0; w < 8; ++w) s += by_bucket[w][threadIdx.x];
+            p.sums[((static_cast<int64_t>(b) * a.heads + head0) * p.q_tiles + q_tile) * a.buckets.total + threadIdx.x] = s;
+        }
+        if (any && (!kSplitKeys || slot == 0)) {
+            T *row = static_cast<T *>(a.dq) + b * a.dqs.batch + i * a.dqs.len + head * a.dqs.head;
+            const bool mine_has = count[kSplitKeys ? 0 : slot] > 0;
+#pragma unroll
+            for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t o[1][32] = {};
+                if (mine_has) {
+                    tmem_load32(o[0], out + 32 * c);
+                    tmem_wait_load(o);
+                }
+                if (valid) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float eight[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            eight[k] = __uint_as_float(o[0][e + k]);
+                            if (two) eight[k] += hand[(32 * c + e + k) * kRows + r];
+                            eight[k] *= a.scale;
+                        }
+                        if (32 * c + e < a.dim) store<T, 8>(row + 32 * c + e, eight);
+                    }
+                }
+            }
+        }
+        tmem_fence_before();
     }
-    put_row(static_cast<T *>(a.dk) + y.b * a.dks.batch + j * a.dks.len + y.a * a.dks.head, dk, a.scale, a.dim, lane);
-    put_row(static_cast<T *>(a.dv) + y.b * a.dvs.batch + j * a.dvs.len + y.a * a.dvs.head, dv, 1.0f, a.dim, lane);
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 9) tmem_free<512>(tmem);
 }
 
-// dtable[n, head] from every query's sums: a block to each, its threads' sums
-// added in a fixed order.
+// ---- dk, dv ----------------------------------------------------------------------
+
+template <int kDim>
+struct KeyShape {
+    static constexpr int kBoxes = kDim / 64;
+    static constexpr uint32_t kRowsBytes = kBoxes * kRowsBox, kColsBytes = kBoxes * kColsBox;
+    static constexpr int kStages = kDim == 64 ? 8 : 4;
+    static constexpr uint32_t kStageBytes = 2 * kColsBytes;          // q, do
+    static constexpr uint32_t kRing = 2 * kRowsBytes;                // after k, v
+    static constexpr uint32_t kStats = kRing + kStages * kStageBytes;  // kCols (lse, delta) a stage
+    static constexpr uint32_t kBytes = kStats + kStages * kCols * sizeof(float2);
+};
+
+template <class T, int kDim>
+__global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant__ BwdParams p)
+{
+    using S = KeyShape<kDim>;
+    extern __shared__ uint8_t dynamic[];
+    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 6];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile uint32_t stalled;
+    const Attention &a = p.a;
+    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+    uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
+    const uint32_t base = smem_address(smem);
+
+    // ---- the block's work: the first keys, whose causal part is the longest, first
+    const int32_t units = a.batch * a.heads_kv, unit = blockIdx.x % units;
+    const int32_t b = unit / a.heads_kv, head_kv = unit % a.heads_kv;
+    const int32_t j0 = blockIdx.x / units * kRows;
+    const int32_t keys = keys_of(a, b), pos0 = first_position(a, keys);
+    const int32_t q_tiles = (a.len_q + kCols - 1) / kCols;
+    const int32_t first_i = a.causal && j0 > pos0 ? j0 - pos0 : 0;  // the first query that sees any of the keys
+    const int32_t begin = min(first_i / kCols, q_tiles), per_head = j0 < keys ? q_tiles - begin : 0;
+    const int32_t tiles = per_head * a.group;
+
+    const uint32_t full = smem_address(bars), empty = full + 8 * S::kStages, scored = empty + 8 * S::kStages,
+                   ready = scored + 16, done = ready + 16, k_full = done + 8;
+    if (threadIdx.x == 0) {
+        stalled = 0;
+        for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1);
+        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4);
+        barrier_init(done, 1), barrier_init(k_full, 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) tmem_alloc<512>(smem_address(&tmem_base));
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_base, dv_at = tmem + 4 * kCols, dk_at = dv_at + 128;
+    if (warp >= 8) {
+        give_registers<kOtherRegisters>();
+        if (warp == 8) {
+            // ---- TMA: k and v, then the queries' tiles, head by head
+            if (elect_one() && tiles) {
+                barrier_expect(k_full, 2 * S::kRowsBytes);
+                for (int c = 0; c < S::kBoxes; ++c) {
+                    tma_load_5d(base + c * kRowsBox, &p.k_rows, k_full, c * 64, 0, j0, head_kv, b);
+                    tma_load_5d(base + S::kRowsBytes + c * kRowsBox, &p.v_rows, k_full, c * 64, 0, j0, head_kv, b);
+                }
+                for (int32_t n = 0; n < tiles; ++n) {
+                    const uint32_t stage = n % S::kStages, bar = full + 8 * stage;
+                    const int32_t head = head_kv * a.group + n / per_head, i0 = (begin + n % per_head) * kCols;
+                    barrier_wait(empty + 8 * stage, (n / S::kStages & 1u) ^ 1u, &stalled);
+                    barrier_expect(bar, S::kStageBytes + kCols * sizeof(float2));
+                    const uint32_t dst = base + S::kRing + stage * S::kStageBytes;
+                    for (int c = 0; c < S::kBoxes; ++c) {
+                        tma_load_5d(dst + c * kColsBox, &p.q_cols, bar, c * 64, 0, i0, head, b);
+                        tma_load_5d(dst + S::kColsBytes + c * kColsBox, &p.do_cols, bar, c * 64, 0, i0, head, b);
+                    }
+                    bulk_load(base + S::kStats + stage * kCols * sizeof(float2),
+                              p.stats + (static_cast<int64_t>(b) * a.heads + head) * p.len_pad + i0, kCols * sizeof(float2), bar);
+                }
+                if (stalled)  // nothing may land after the block has ended
+                    for (int32_t n = max(0, tiles - S::kStages); n < tiles; ++n)
+                        for (uint32_t tries = 0; tries < 100000 && !barrier_try(full + 8 * (n % S::kStages), n / S::kStages & 1u); ++tries) {}
+            }
+        } else if (warp == 9) {
+            // ---- MMA
+            if (elect_one() && tiles) {
+                constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
+                auto scores = [&](int32_t n) {
+                    const uint32_t stage = n % S::kStages, slot = n & 1, q = base + S::kRing + stage * S::kStageBytes;
+                    barrier_wait(full + 8 * stage, n / S::kStages & 1u, &stalled);
+                    tmem_fence_after();
+                    for (int x = 0; x < 2; ++x)  // S^T = K Q^T, dP^T = V dO^T
+                        for (int i = 0; i < kDim / 16; ++i)
+                            mma_step(tmem + slot * 2 * kCols + x * kCols,
+                                     row_major_tile(base + x * S::kRowsBytes + i / 4 * kRowsBox + i % 4 * 32),
+                                     row_major_tile(q + x * S::kColsBytes + i / 4 * kColsBox + i % 4 * 32), kScores, i > 0);
+                    mma_commit(scored + 8 * slot);
+                };
+                barrier_wait(k_full, 0, &stalled);
+                for (int32_t n = 0; n < 2 && n < tiles; ++n) scores(n);
+                for (int32_t n = 0; n < tiles; ++n) {
+                    const uint32_t stage = n % S::kStages, slot = n & 1, q = base + S::kRing + stage * S::kStageBytes;
+                    barrier_wait(ready + 8 * slot, n / 2 & 1u, &stalled);
+                    tmem_fence_after();
+                    for (int x = 0; x < 2; ++x)  // dV += P^T dO, dK += dS^T Q
+                        for (int i = 0; i < kCols / 16; ++i)
+                            mma_step_tmem(x ? dk_at : dv_at, tmem + slot * 2 * kCols + x * 32 + i * 8,
+                                          column_major_tile(q + (x ? 0 : S::kColsBytes) + i * 2048, S::kBoxes > 1 ? kColsBox : 1024),
+                                          kOut, n > 0 || i > 0);
+                    mma_commit(empty + 8 * stage);
+                    if (n + 2 < tiles) scores(n + 2);
+                }
+                mma_commit(done);
+            }
+        }
+    } else {
+        take_registers<kSlotRegisters>();
+        // ---- the slots' rows: a key each
+        const int slot = warp / 4;
+        const int32_t j = j0 + (warp % 4) * 32 + lane, warp_j = j0 + (warp % 4) * 32;
+        const uint32_t lanes = (warp % 4) * 32u << 16, mine = tmem + slot * 2 * kCols + lanes;
+        const bool plain = is_plain(a), any = warp_j < keys;
+        const int32_t reach = bias_reach(a.buckets);
+        const int32_t last_start = plain ? 0 : a.buckets.starts[a.buckets.count - 2];
+        constexpr float kUnlift = kLift<T> != 0.0f ? 1.0f / 1024.0f : 1.0f;
+        const float scale = a.mask.scale * kUnlift;
+        for (int32_t n = slot; n < tiles; n += 2) {
+            const int32_t head = head_kv * a.group + n / per_head, i0 = (begin + n % per_head) * kCols;
+            const float4 *stats = reinterpret_cast<const float4 *>(smem + S::kStats + n % S::kStages * kCols * sizeof(float2));
+            barrier_wait(scored + 8 * slot, n / 2 & 1u, &stalled);
+            tmem_fence_after();
+            if (any) {
+                uint32_t v[4][32];  // S^T, then dP^T
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_load32(v[c], mine + 32 * c);
+                tmem_wait_load(v);
+                auto s = [&](int e) -> uint32_t & { return v[e / 32][e % 32]; };
+                auto dp = [&](int e) -> uint32_t & { return v[2 + e / 32][e % 32]; };
+                const int32_t rel = j - pos0 - i0;  // to the tile's first query
+                const int32_t low = warp_j - pos0 - i0 - (kCols - 1), high = warp_j + 31 - pos0 - i0;
+                const bool far = high <= -last_start || low >= last_start;
+                const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
+                const float edge = !plain && far ? bias[high <= -last_start ? 0 : 2 * reach - 1] : 0.0f;
+                const uint32_t c0 = a.first + ((static_cast<uint32_t>(b) * a.heads + head) * a.len_q + i0) * static_cast<uint32_t>(a.len_k) + j;
+                // causal: query i0 + e sees key j from e = rel on
+                const int32_t unseen = a.causal && high > 0 ? rel : 0;
+#pragma unroll
+                for (int e = 0; e < kCols; e += 2) {
+                    const float4 st = stats[e / 2];  // two queries' lse, delta
+                    const float2 x = make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1)));
+                    float2 f;
+                    if (plain) {
+                        const float to_base2 = a.scale * kLog2e;
+                        f = fma2(x, make_float2(to_base2, to_base2), make_float2(kLift<T> - st.x, kLift<T> - st.z));
+                    } else {
+                        const float2 by = far ? make_float2(edge, edge) : make_float2(bias[rel + reach - e], bias[rel + reach - e - 1]);
+                        f = fma2(x, make_float2(a.scale, a.scale), by);
+                        f = fma2(add2(f, make_float2(-st.x, -st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>));
+                    }
+                    float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                    if (e < unseen) prob.x = 0.0f;
+                    if (e + 1 < unseen) prob.y = 0.0f;
+                    const float2 minus = make_float2(-st.y * kUnlift, -st.w * kUnlift);
+                    float2 d = fma2(make_float2(__uint_as_float(dp(e)), __uint_as_float(dp(e + 1))), make_float2(scale, scale), minus);
+                    float2 kept = prob;
+                    if (a.mask.threshold) {
+                        if (!keeps(a.mask, c0 + e * static_cast<uint32_t>(a.len_k))) kept.x = 0.0f, d.x = minus.x;
+                        if (!keeps(a.mask, c0 + (e + 1) * static_cast<uint32_t>(a.len_k))) kept.y = 0.0f, d.y = minus.y;
+                    }
+                    d = mul2(d, prob);
+                    s(e / 2) = pack2<T>(kept.x, kept.y);
+                    dp(e / 2) = pack2<T>(d.x, d.y);
+                }
+                tmem_store32(mine, v[0]);
+                tmem_store32(mine + 32, v[2]);
+                tmem_wait_store();
+            }
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0) barrier_arrive(ready + 8 * slot);
+        }
+
+        // ---- the result: slot 0's threads write dv, slot 1's dk
+        if (tiles) {
+            barrier_wait(done, 0, &stalled);
+            tmem_fence_after();
+        }
+        if (warp_j < a.len_k) {
+            const Strides &st = slot ? a.dks : a.dvs;
+            T *row = static_cast<T *>(slot ? a.dk : a.dv) + b * st.batch + j * st.len + head_kv * st.head;
+            const float weight = slot ? a.scale : scale;
+#pragma unroll
+            for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t o[1][32] = {};
+                if (tiles) {
+                    tmem_load32(o[0], (slot ? dk_at : dv_at) + lanes + 32 * c);
+                    tmem_wait_load(o);
+                }
+                if (j < a.len_k) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float eight[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) eight[k] = j < keys ? __uint_as_float(o[0][e + k]) * weight : 0.0f;
+                        if (32 * c + e < a.dim) store<T, 8>(row + 32 * c + e, eight);
+                    }
+                }
+            }
+        }
+        tmem_fence_before();
+    }
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 9) tmem_free<512>(tmem);
+}
+
+// ---- the table ---------------------------------------------------------------------
+
+// dtable[n, head]: a block to each, its threads' sums over batch and query
+// tiles added in a fixed order.
 template <class T>
-__global__ void __launch_bounds__(256) dtable_kernel(const __grid_constant__ Attention a)
+__global__ void __launch_bounds__(256) table_kernel(const __grid_constant__ BwdParams p)
 {
     __shared__ float sums[8];
+    const Attention &a = p.a;
     const int32_t n = blockIdx.x, head = blockIdx.y;
-    const float *ws = static_cast<const float *>(a.workspace) + queries(a);
     float s = 0.0f;
-    for (int64_t r = threadIdx.x; r < static_cast<int64_t>(a.batch) * a.len_q; r += 256)
-        s += ws[((r / a.len_q * a.heads + head) * a.len_q + r % a.len_q) * a.buckets.total + n];
-    s = warp_sum(s);
+    for (int64_t r = threadIdx.x; r < static_cast<int64_t>(a.batch) * p.q_tiles; r += 256)
+        s += p.sums[((r / p.q_tiles * a.heads + head) * p.q_tiles + r % p.q_tiles) * a.buckets.total + n];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
     if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -181,30 +680,103 @@ __global__ void __launch_bounds__(256) dtable_kernel(const __grid_constant__ Att
     }
 }
 
+// ---- launching ------------------------------------------------------------------------
+
+// How a call is cut, and where its workspace's parts begin (in floats).
+struct BwdPlan {
+    int32_t dim, pack, units, q_tiles, len_pad;
+    bool split_keys;
+    size_t bias, sums, floats;
+};
+
+BwdPlan bwd_plan(const Attention &a)
+{
+    BwdPlan f{};
+    f.dim = a.dim <= 64 ? 64 : 128;
+    f.pack = packed_heads(a);
+    f.units = a.batch * (a.heads / f.pack);
+    const int32_t rows_per = kRows / f.pack, tiles = (a.len_q + rows_per - 1) / rows_per;
+    // one tile of queries to a block where two would leave SMs idle
+    f.split_keys = tiles == 1 || static_cast<int64_t>(f.units) * ((tiles + 1) / 2) < sm_count();
+    f.q_tiles = f.split_keys ? tiles : (tiles + 1) / 2;
+    f.len_pad = (a.len_q + kCols - 1) / kCols * kCols;
+    const size_t heads = static_cast<size_t>(a.batch) * a.heads;
+    f.bias = 2 * heads * f.len_pad;
+    f.sums = f.bias + (a.table ? static_cast<size_t>(a.heads) * 2 * bias_reach(a.buckets) : 0);
+    f.floats = f.sums + (a.dtable ? heads * f.q_tiles * a.buckets.total : 0);
+    return f;
+}
+
+template <class T, int kDim, bool kSplitKeys>
+cudaError_t launch_queries(const BwdParams &p, cudaStream_t s)
+{
+    const auto kernel = query_kernel<T, kDim, kSplitKeys>;
+    const size_t bytes = 1024 + QueryShape<kDim, kSplitKeys>::kTable + (p.a.table ? 2 * bias_reach(p.a.buckets) * sizeof(float) : 0);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.units) * p.q_tiles), kThreads, bytes, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+}
+
+template <class T, int kDim>
+cudaError_t launch_keys(const BwdParams &p, cudaStream_t s)
+{
+    const auto kernel = key_kernel<T, kDim>;
+    const size_t bytes = 1024 + KeyShape<kDim>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = static_cast<int64_t>(p.a.batch) * p.a.heads_kv * ((p.a.len_k + kRows - 1) / kRows);
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    kernel<<<static_cast<unsigned>(blocks), kThreads, bytes, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+}
+
 }  // namespace
 
-size_t attention_bwd_workspace(const Attention &a)
+cudaError_t stalled_waits_bwd(uint64_t *count)
 {
-    return static_cast<size_t>(queries(a)) * (1 + (a.dtable ? a.buckets.total : 0)) * sizeof(float);
+    return cudaMemcpyFromSymbol(count, g_stalled_waits, sizeof(uint64_t));
 }
+
+size_t attention_bwd_workspace(const Attention &a) { return bwd_plan(a).floats * sizeof(float); }
 
 template <class T>
 cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s)
 {
-    const int64_t nq = queries(a), nk = static_cast<int64_t>(a.batch) * a.heads_kv * a.len_k;
-    if (nq) {
-        dq_kernel<T><<<static_cast<unsigned>((nq + 3) / 4), dim3(32, 4), 0, s>>>(a);
-        note_launch();
+    const BwdPlan f = bwd_plan(a);
+    BwdParams p{};
+    p.a = a;
+    p.pack = f.pack, p.units = f.units, p.q_tiles = f.q_tiles, p.len_pad = f.len_pad;
+    float *ws = static_cast<float *>(a.workspace);
+    p.stats = reinterpret_cast<float2 *>(ws), p.bias = ws + f.bias, p.sums = ws + f.sums;
+    const bool has_q = a.batch && a.heads && a.len_q, has_k = a.batch && a.heads_kv && a.len_k;
+    constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+    cudaError_t e = cudaSuccess;
+    auto map = [&](CUtensorMap *m, const void *x, const Strides &st, int32_t len, int32_t heads, int32_t pack, int32_t box) {
+        if (e == cudaSuccess) e = make_heads_map(m, bf16, x, st, a.batch, len, heads, a.dim, pack, box);
+    };
+    if (has_q) {
+        map(&p.q_rows, a.q, a.qs, a.len_q, a.heads, f.pack, kRows), map(&p.do_rows, a.d_o, a.dos, a.len_q, a.heads, f.pack, kRows);
+        map(&p.q_cols, a.q, a.qs, a.len_q, a.heads, 1, kCols), map(&p.do_cols, a.d_o, a.dos, a.len_q, a.heads, 1, kCols);
     }
-    if (nk) {
-        dkv_kernel<T><<<static_cast<unsigned>((nk + 3) / 4), dim3(32, 4), 0, s>>>(a);
-        note_launch();
+    if (has_k) {
+        map(&p.k_rows, a.k, a.ks, a.len_k, a.heads_kv, 1, kRows), map(&p.v_rows, a.v, a.vs, a.len_k, a.heads_kv, 1, kRows);
+        map(&p.k_cols, a.k, a.ks, a.len_k, a.heads_kv, 1, kCols), map(&p.v_cols, a.v, a.vs, a.len_k, a.heads_kv, 1, kCols);
     }
-    if (a.dtable && a.heads) {
-        dtable_kernel<T><<<dim3(a.buckets.total, a.heads), 256, 0, s>>>(a);
-        note_launch();
+    if (e == cudaSuccess && has_q) {
+        if (static_cast<int64_t>(f.units) * f.q_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        if (f.dim == 64) e = f.split_keys ? launch_queries<T, 64, true>(p, s) : launch_queries<T, 64, false>(p, s);
+        else e = f.split_keys ? launch_queries<T, 128, true>(p, s) : launch_queries<T, 128, false>(p, s);
     }
-    return cudaGetLastError();
+    if (e == cudaSuccess && has_k) e = f.dim == 64 ? launch_keys<T, 64>(p, s) : launch_keys<T, 128>(p, s);
+    if (e == cudaSuccess && a.dtable && a.heads) {
+        table_kernel<T><<<dim3(a.buckets.total, a.heads), 256, 0, s>>>(p);
+        note_launch();
+        e = cudaGetLastError();
+    }
+    return e;
 }
 
 template cudaError_t launch_attention_bwd<__half>(const Attention &, cudaStream_t);

@@ -48,8 +48,6 @@ struct Shape {
     static constexpr uint32_t kTable = kRing + kStages * kStageBytes;
 };
 
-__device__ __forceinline__ int32_t bias_reach(const Buckets &b) { return b.max_distance + 160; }
-
 // One slot's rows: the thread's row, its place and what it may see.
 struct Row {
     int32_t i, head;
@@ -487,8 +485,7 @@ FwdPlan fwd_plan(const Attention &a)
 {
     FwdPlan f;
     f.dim = a.dim <= 64 ? 64 : 128;
-    // the heads of a key head side by side, where a tile is a whole number of them and no head has a bias of its own
-    f.pack = !a.table && a.group <= 64 && (a.group & (a.group - 1)) == 0 ? a.group : 1;
+    f.pack = packed_heads(a);
     f.units = a.batch * (a.heads / f.pack);
     const int32_t rows_per = kTile / f.pack, tiles = (a.len_q + rows_per - 1) / rows_per;
     const int32_t key_tiles = (a.len_k + kTile - 1) / kTile;

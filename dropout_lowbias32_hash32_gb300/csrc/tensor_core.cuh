@@ -88,6 +88,13 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v)
         : "memory");
 }
+// bytes adjacent bytes, a multiple of 16 from a 16-byte boundary to one.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 // ---- tensor memory ---------------------------------------------------------------
 // 512 columns of 128 lanes x 32 bits; an address is lane << 16 | column.  A warp
