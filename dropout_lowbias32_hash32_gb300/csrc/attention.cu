@@ -186,8 +186,7 @@ rng_status make(const char *what, const rng_attention_args *args, bool sizes_onl
     auto strides = [](const int64_t *s) { return Strides{s[0], s[1], s[2]}; };
     t.q = a.q, t.k = a.k, t.v = a.v, t.lse = a.lse, t.key_lengths = a.key_lengths, t.scale = a.scale;
     t.qs = strides(a.q_stride), t.ks = strides(a.k_stride), t.vs = strides(a.v_stride), t.os = strides(a.o_stride);
-    t.mask = Mask{seed_key(a.seed), static_cast<uint32_t>(std::ceil(static_cast<double>(a.p) * 8388608.0)),
-                  1.0f / (1.0f - a.p)};
+    t.mask = make_mask(a.p, a.seed);
     t.first = a.first_counter;
     t.workspace = a.workspace;
     return RNG_OK;

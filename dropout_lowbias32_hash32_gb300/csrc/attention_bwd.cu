@@ -9,6 +9,8 @@
 // by tiles of 128 x 64; the threads of one of two slots turn them into dS (and
 // P), written back over S in 16 bits as the TMEM operand of the products
 // that accumulate dq (dk, dv), while the tensor core works for the other slot.
+// Two threads share a row, so that four warps a scheduler hide each other's
+// latencies.
 // The tile of 64 lets both slots' scores and both accumulators of a head
 // dimension of 128 fit the 512 TMEM columns.
 #include "tensor_core.cuh"
@@ -18,9 +20,12 @@ namespace rngk {
 namespace {
 
 constexpr int kRows = 128, kCols = 64;  // a slot's tile
-constexpr int kThreads = 384;           // 2 x 128 for the slots, then a TMA warp, an MMA warp, two that only fill the warpgroup
-// registers: 384 threads start with 168 each; 2 x 208 + 88 = 3 x 168
-constexpr int kSlotRegisters = 208, kOtherRegisters = 88;
+constexpr int kHalf = kCols / 2;        // columns of a thread
+// 2 x 256 for the slots, then a TMA warp, an MMA warp, two that only fill the warpgroup
+constexpr int kThreads = 640;
+constexpr uint32_t kTmaWarp = 16, kMmaWarp = 17;
+// registers: 640 threads start with 96 each; 4 x 104 + 64 = 5 x 96
+constexpr int kSlotRegisters = 104, kOtherRegisters = 64;
 constexpr uint32_t kRowsBox = 16384, kColsBox = 8192;  // bytes of 128 and of 64 rows of 64 elements
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -43,7 +48,8 @@ struct BwdParams {
     float *bias, *sums;
 };
 
-__device__ __forceinline__ bool is_plain(const Attention &a) { return a.table == nullptr; }
+// How far step i of 16 is into a row-major tile of boxes, as a descriptor counts.
+__host__ __device__ constexpr uint32_t row_step(int i, uint32_t box) { return (i / 4 * box + i % 4 * 32) / 16; }
 
 // ---- dq ------------------------------------------------------------------------
 
@@ -74,7 +80,7 @@ __device__ __forceinline__ void bucket_range(const Buckets &b, int32_t n, int32_
     }
 }
 
-template <class T, int kDim, bool kSplitKeys>
+template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constant__ BwdParams p)
 {
     using S = QueryShape<kDim, kSplitKeys>;
@@ -82,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
     __shared__ alignas(8) uint64_t bars[2 * (S::kKeyStages + S::kValueStages) + 8];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t stalled;
-    __shared__ float diagonals[8][96], by_bucket[8][kMaxBuckets];
+    __shared__ float diagonals[16][64];
     const Attention &a = p.a;
     const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
     uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
@@ -117,12 +123,12 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
         stalled = 0;
         for (int s = 0; s < S::kKeyStages; ++s) barrier_init(k_full + 8 * s, 1), barrier_init(k_empty + 8 * s, 1);
         for (int s = 0; s < S::kValueStages; ++s) barrier_init(v_full + 8 * s, 1), barrier_init(v_empty + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4);
+        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 8);
         barrier_init(done, 1), barrier_init(q_full, 1), barrier_init(tail, 1);
         fence_barrier_init();
     }
-    if (warp == 9) tmem_alloc<512>(smem_address(&tmem_base));
-    if (a.table) {  // the bias by relative position, head head0 (pack is 1)
+    if (warp == kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
+    if (kBias) {  // the bias by relative position, head head0 (pack is 1)
         const int32_t reach = bias_reach(a.buckets);
         for (int32_t t = threadIdx.x; t < 2 * reach; t += kThreads) {
             table[t] = to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, t - reach) * a.heads + head0]);
@@ -137,9 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
-    if (warp >= 8) {
+    if (warp >= kTmaWarp) {
         give_registers<kOtherRegisters>();
-        if (warp == 8) {
+        if (warp == kTmaWarp) {
             // ---- TMA: q and do, then K_n and V_n
             const bool one = elect_one();
             if (one && tiles) {
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                          tries < 100000 && !(barrier_try(k_full + 8 * (n % S::kKeyStages), n / S::kKeyStages & 1u) &&
                                              barrier_try(v_full + 8 * (n % S::kValueStages), n / S::kValueStages & 1u));
                          ++tries) {}
-        } else if (warp == 9) {
+        } else if (warp == kMmaWarp) {
             // ---- MMA
             if (elect_one() && tiles) {
                 constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
@@ -197,43 +203,45 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                                    v = base + S::kValues + vs * S::kColsBytes;
                     barrier_wait(k_full + 8 * ks, n / S::kKeyStages & 1u, &stalled);
                     tmem_fence_after();
+                    const uint64_t qd = row_major_tile(q), kd = row_major_tile(k), dd = row_major_tile(q + S::kDo), vd = row_major_tile(v);
+#pragma unroll
                     for (int i = 0; i < kDim / 16; ++i)
-                        mma_step(tmem + slot * 256, row_major_tile(q + i / 4 * kRowsBox + i % 4 * 32),
-                                 row_major_tile(k + i / 4 * kColsBox + i % 4 * 32), kScores, i > 0);
+                        mma_step(tmem + slot * 256, qd + row_step(i, kRowsBox), kd + row_step(i, kColsBox), kScores, i > 0);
                     barrier_wait(v_full + 8 * vs, n / S::kValueStages & 1u, &stalled);
                     tmem_fence_after();
+#pragma unroll
                     for (int i = 0; i < kDim / 16; ++i)
-                        mma_step(tmem + slot * 256 + kCols, row_major_tile(q + S::kDo + i / 4 * kRowsBox + i % 4 * 32),
-                                 row_major_tile(v + i / 4 * kColsBox + i % 4 * 32), kScores, i > 0);
+                        mma_step(tmem + slot * 256 + kCols, dd + row_step(i, kRowsBox), vd + row_step(i, kColsBox), kScores, i > 0);
                     mma_commit(scored + 8 * slot);
                 };
                 auto product = [&](int slot, int32_t n, bool first) {
                     const uint32_t k = base + S::kKeys + n % S::kKeyStages * S::kColsBytes;
                     barrier_wait(ready + 8 * slot, (slot ? given1++ : given0++) & 1u, &stalled);
                     tmem_fence_after();
+                    const uint64_t kd = column_major_tile(k, S::kBoxes > 1 ? kColsBox : 1024);
+#pragma unroll
                     for (int i = 0; i < kCols / 16; ++i)
-                        mma_step_tmem(tmem + slot * 256 + 2 * kCols, tmem + slot * 256 + i * 8,
-                                      column_major_tile(k + i * 2048, S::kBoxes > 1 ? kColsBox : 1024), kOut, !first || i > 0);
+                        mma_step_tmem(tmem + slot * 256 + 2 * kCols, tmem + slot * 256 + i / 2 * kHalf + i % 2 * 8, kd + i * (2048 / 16), kOut,
+                                      !first || i > 0);
                 };
                 auto release_k = [&](int32_t n) { mma_commit(k_empty + 8 * (n % S::kKeyStages)); };
                 auto release_v = [&](int32_t n) { mma_commit(v_empty + 8 * (n % S::kValueStages)); };
                 barrier_wait(q_full, 0, &stalled);
                 if (kSplitKeys) {
-                    for (int32_t n = 0; n < 2 && n < tiles; ++n) scores(n, n), release_v(n);
-                    for (int32_t n = 0; n < tiles; ++n) {
-                        product(n & 1, n, n < 2), release_k(n);
+#pragma unroll 1
+                    for (int32_t n = -2; n < tiles; ++n) {
+                        if (n >= 0) product(n & 1, n, n < 2), release_k(n);
                         if (n + 2 < tiles) scores(n & 1, n + 2), release_v(n + 2);
                     }
                 } else {
-                    for (int s = 0; s < 2; ++s)
-                        if (count[s]) scores(s, 0);
-                    release_v(0);
-                    for (int32_t n = 0; n < tiles; ++n) {
+#pragma unroll 1
+                    for (int32_t n = -1; n < tiles; ++n) {
+#pragma unroll 1
                         for (int s = 0; s < 2; ++s) {
-                            if (n < count[s]) product(s, n, n == 0);
+                            if (n >= 0 && n < count[s]) product(s, n, n == 0);
                             if (n + 1 < count[s]) scores(s, n + 1);
                         }
-                        release_k(n);
+                        if (n >= 0) release_k(n);
                         if (n + 1 < tiles) release_v(n + 1);
                     }
                 }
@@ -243,21 +251,22 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
     } else {
         take_registers<kSlotRegisters>();
         // ---- the slots' rows
-        const int slot = warp / 4;
+        const int slot = warp / 8, half = warp / 4 % 2;
         const int32_t r = (warp % 4) * 32 + lane;
-        const uint32_t mine = tmem + slot * 256 + ((warp % 4) * 32u << 16);
-        const uint32_t out = mine + 2 * kCols;
+        const uint32_t lanes = (warp % 4) * 32u << 16;
+        const uint32_t mine = tmem + slot * 256 + lanes + half * kHalf;  // the thread's scores, then its dS; dP kCols on
+        const uint32_t out = tmem + slot * 256 + lanes + 2 * kCols + half * (kDim / 2);
         const int32_t row0 = kSplitKeys ? 0 : slot * kRows;
         const int32_t warp_i = i0 + (row0 + (warp % 4) * 32) / p.pack;
         const int32_t i = i0 + (row0 + r) / p.pack, head = head0 + r % p.pack;
-        const bool valid = i < a.len_q, any = warp_i < a.len_q, plain = is_plain(a);
+        const bool valid = i < a.len_q, any = warp_i < a.len_q;
         const int32_t pos = pos0 + i;
         const int64_t index = (static_cast<int64_t>(b) * a.heads + head);
-        const uint32_t counter = a.first + (static_cast<uint32_t>(index) * a.len_q + i) * static_cast<uint32_t>(a.len_k);
+        const uint32_t counter = a.first + (static_cast<uint32_t>(index) * a.len_q + i) * static_cast<uint32_t>(a.len_k) + half * kHalf;
         const int32_t visible = a.causal ? min(keys, pos + 1) : keys;
         const int32_t warp_visible = a.causal ? min(keys, pos0 + warp_i + 1) : keys;
         const int32_t reach = bias_reach(a.buckets);
-        const int32_t last_start = plain ? 0 : a.buckets.starts[a.buckets.count - 2];
+        const int32_t last_start = !kBias ? 0 : a.buckets.starts[a.buckets.count - 2];
 
         float lse = INFINITY, delta = 0.0f;
         if (valid) {
@@ -272,118 +281,117 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
             }
             lse = a.lse[index * a.len_q + i];
             // a query that sees nothing: exp(s - inf) = 0 whatever its scores
-            lse = lse == -INFINITY ? INFINITY : plain ? lse * kLog2e : lse;
-            if (slot == 0 || !kSplitKeys) p.stats[index * p.len_pad + i] = make_float2(lse, delta);
+            lse = lse == -INFINITY ? INFINITY : kBias ? lse : lse * kLog2e;
+            if (half == 0 && (slot == 0 || !kSplitKeys)) p.stats[index * p.len_pad + i] = make_float2(lse, delta);
         }
 
         float own[kMaxBuckets / 32] = {}, far_low = 0.0f, far_high = 0.0f;
-        const float scale = a.mask.scale;
+        const float2 scale = make_float2(a.mask.scale, a.mask.scale), minus = make_float2(-delta, -delta);
         uint32_t turn = 0;
         for (int32_t n = kSplitKeys ? slot : 0; n < count[kSplitKeys ? 0 : slot]; n += kSplitKeys ? 2 : 1, ++turn) {
-            const int32_t j0 = n * kCols;
+            const int32_t j0 = n * kCols + half * kHalf;
             barrier_wait(scored + 8 * slot, turn & 1u, &stalled);
             tmem_fence_after();
             if (any) {
-                uint32_t v[4][32];  // S, then dP
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load32(v[c], mine + 32 * c);
+                uint32_t v[2][32];  // S, then dP
+                tmem_load32(v[0], mine);
+                tmem_load32(v[1], mine + kCols);
                 tmem_wait_load(v);
-                auto s = [&](int e) -> uint32_t & { return v[e / 32][e % 32]; };
-                auto dp = [&](int e) -> uint32_t & { return v[2 + e / 32][e % 32]; };
+                uint32_t(&s)[32] = v[0], (&dp)[32] = v[1];
                 // P
-                const int32_t low = j0 - (pos0 + warp_i + 31), high = j0 + kCols - 1 - (pos0 + warp_i);
+                const int32_t low = j0 - (pos0 + warp_i + 31), high = j0 + kHalf - 1 - (pos0 + warp_i);
                 const bool far = high <= -last_start || low >= last_start;
-                if (plain) {
+                if (!kBias) {
                     const float to_base2 = a.scale * kLog2e;
                     const float2 k2 = make_float2(to_base2, to_base2), l2 = make_float2(-lse, -lse);
 #pragma unroll
-                    for (int e = 0; e < kCols; e += 2) {
-                        const float2 f = fma2(make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1))), k2, l2);
-                        s(e) = __float_as_uint(exp2_approx(f.x)), s(e + 1) = __float_as_uint(exp2_approx(f.y));
+                    for (int e = 0; e < kHalf; e += 2) {
+                        const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, l2);
+                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
                     }
                 } else {
                     const float2 k2 = make_float2(a.scale, a.scale), l2 = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
                     const float edge = far ? table[high <= -last_start ? 0 : 2 * reach - 1] : 0.0f;
                     const float *t = table + (j0 - pos + reach);
 #pragma unroll
-                    for (int e = 0; e < kCols; e += 2) {
+                    for (int e = 0; e < kHalf; e += 2) {
                         const float2 bias = far ? make_float2(edge, edge) : make_float2(t[e], t[e + 1]);
-                        float2 f = fma2(make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1))), k2, bias);
+                        float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, bias);
                         f = mul2(add2(f, l2), b2);
-                        s(e) = __float_as_uint(exp2_approx(f.x)), s(e + 1) = __float_as_uint(exp2_approx(f.y));
+                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
                     }
                 }
                 // dS = P (dP / (1 - p) - delta), dP dropped as P was
-                const uint32_t c0 = counter + j0;
+                if (kDrop) drop32(a.mask, counter + n * kCols, dp);
 #pragma unroll
-                for (int e = 0; e < kCols; e += 2) {
-                    float2 d = fma2(make_float2(__uint_as_float(dp(e)), __uint_as_float(dp(e + 1))), make_float2(scale, scale),
-                                    make_float2(-delta, -delta));
-                    if (a.mask.threshold) {
-                        if (!keeps(a.mask, c0 + e)) d.x = -delta;
-                        if (!keeps(a.mask, c0 + e + 1)) d.y = -delta;
-                    }
-                    d = mul2(d, make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1))));
-                    s(e) = __float_as_uint(d.x), s(e + 1) = __float_as_uint(d.y);
+                for (int e = 0; e < kHalf; e += 2) {
+                    float2 d = fma2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), scale, minus);
+                    d = mul2(d, make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                    s[e] = __float_as_uint(d.x), s[e + 1] = __float_as_uint(d.y);
                 }
-                if (j0 + kCols > warp_visible) {
+                if (j0 + kHalf > warp_visible) {
                     const int32_t seen = visible - j0;
 #pragma unroll
-                    for (int e = 0; e < kCols; ++e)
-                        if (e >= seen) s(e) = 0;
+                    for (int e = 0; e < kHalf; ++e)
+                        if (e >= seen) s[e] = 0;
                 }
+                uint32_t w[16];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e] = pack2<T>(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1]));
-                    tmem_store16(mine + 16 * c, w);
-                }
+                for (int e = 0; e < 16; ++e) w[e] = pack2<T>(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+                tmem_store16(mine, w);
                 tmem_wait_store();
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) barrier_arrive(ready + 8 * slot);
-                if (a.dtable && far) {  // one bucket
-                    float2 total = make_float2(0.0f, 0.0f);
+                if (kBias && a.dtable) {
+                    if (!valid) {
 #pragma unroll
-                    for (int e = 0; e < kCols; e += 2)
-                        total = add2(total, make_float2(valid ? __uint_as_float(s(e)) : 0.0f, valid ? __uint_as_float(s(e + 1)) : 0.0f));
-                    (high <= -last_start ? far_low : far_high) += total.x + total.y;
-                } else if (a.dtable) {
-                    // sums along the diagonals of the warp's 32 x 64 tile: a partial sum moves one row down with
-                    // each column; what leaves row 31, or is left in the last column, is a whole one
-                    float acc = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < kCols; ++e) {
-                        acc = __shfl_up_sync(0xFFFFFFFFu, acc, 1);
-                        acc = (lane ? acc : 0.0f) + (valid ? __uint_as_float(s(e)) : 0.0f);
-                        if (lane == 31) diagonals[warp][e] = acc;
+                        for (int e = 0; e < kHalf; ++e) s[e] = 0;
                     }
-                    if (lane < 31) diagonals[warp][94 - lane] = acc;
-                    __syncwarp();
-                    // diagonal d is relative position low + d; a lane adds the buckets lane, lane + 32, ...
+                    if (far) {  // one bucket
+                        float2 total = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int m = 0; m < kMaxBuckets / 32; ++m) {
-                        if (32 * m < a.buckets.total) {
-                            int32_t from, to;
-                            bucket_range(a.buckets, lane + 32 * m, from, to);
-                            from = max(from - low, 0), to = min(to - low, 94);
-                            for (int32_t d = from; d <= to; ++d) own[m] += diagonals[warp][d];
+                        for (int e = 0; e < kHalf; e += 2) total = add2(total, make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                        (high <= -last_start ? far_low : far_high) += total.x + total.y;
+                    } else {
+                        // sums along the diagonals of the warp's 32 x 32 tile: a partial sum moves one row down with
+                        // each column; what leaves row 31, or is left in the last column, is a whole one
+                        float acc = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < kHalf; ++e) {
+                            acc = __shfl_up_sync(0xFFFFFFFFu, acc, 1);
+                            acc = (lane ? acc : 0.0f) + __uint_as_float(s[e]);
+                            if (lane == 31) diagonals[warp][e] = acc;
                         }
+                        if (lane < 31) diagonals[warp][62 - lane] = acc;
+                        __syncwarp();
+                        // diagonal d is relative position low + d; a lane adds the buckets lane, lane + 32, ...
+#pragma unroll
+                        for (int m = 0; m < kMaxBuckets / 32; ++m) {
+                            if (32 * m < a.buckets.total) {
+                                int32_t from, to;
+                                bucket_range(a.buckets, lane + 32 * m, from, to);
+                                from = max(from - low, 0), to = min(to - low, 62);
+#pragma unroll 1
+                                for (int32_t d = from; d <= to; ++d) own[m] += diagonals[warp][d];
+                            }
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             } else if (lane == 0) {
                 barrier_arrive(ready + 8 * slot);
             }
         }
 
-        // ---- the result
+        // ---- the result, through the tiles' memory, which nothing reads any more
         if (tiles) {
             barrier_wait(done, 0, &stalled);
             tmem_fence_after();
         }
-        if (a.dtable) {
+        float *hand = reinterpret_cast<float *>(smem + S::kKeys);
+        [[maybe_unused]] float *by_bucket = hand + kDim * kRows * (kSplitKeys ? 1 : 0);  // [16][kMaxBuckets]
+        if (kBias && a.dtable) {
 #pragma unroll
             for (int m = 16; m > 0; m >>= 1) {
                 far_low += __shfl_xor_sync(0xFFFFFFFFu, far_low, m);
@@ -394,34 +402,34 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                 const int32_t bucket = lane + 32 * m;
                 if (bucket == a.buckets.count - 1) own[m] += far_low;
                 if (bucket == (a.buckets.past ? a.buckets.total - 1 : 0)) own[m] += far_high;
-                by_bucket[warp][bucket] = own[m];
+                by_bucket[warp * kMaxBuckets + bucket] = own[m];
             }
         }
-        float *hand = reinterpret_cast<float *>(smem + S::kKeys);  // nothing reads the tiles any more
         const bool two = kSplitKeys && tiles > 1;
         if (two && slot == 1 && any) {
-#pragma unroll
-            for (int c = 0; c < kDim / 32; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < kDim / 64; ++c) {
                 uint32_t o[1][32];
                 tmem_load32(o[0], out + 32 * c);
                 tmem_wait_load(o);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) hand[(32 * c + e) * kRows + r] = __uint_as_float(o[0][e]);
+                for (int e = 0; e < 32; ++e) hand[(half * (kDim / 2) + 32 * c + e) * kRows + r] = __uint_as_float(o[0][e]);
             }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (a.dtable && threadIdx.x < a.buckets.total) {
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+        if (kBias && a.dtable && threadIdx.x < a.buckets.total) {
             float s = 0.0f;
-            for (int w = 0; w < 8; ++w) s += by_bucket[w][threadIdx.x];
+            for (int w = 0; w < 16; ++w) s += by_bucket[w * kMaxBuckets + threadIdx.x];
             p.sums[((static_cast<int64_t>(b) * a.heads + head0) * p.q_tiles + q_tile) * a.buckets.total + threadIdx.x] = s;
         }
         if (any && (!kSplitKeys || slot == 0)) {
             T *row = static_cast<T *>(a.dq) + b * a.dqs.batch + i * a.dqs.len + head * a.dqs.head;
-            const bool mine_has = count[kSplitKeys ? 0 : slot] > 0;
-#pragma unroll
-            for (int c = 0; c < kDim / 32; ++c) {
+            const bool has = count[kSplitKeys ? 0 : slot] > 0;
+#pragma unroll 1
+            for (int c = 0; c < kDim / 64; ++c) {
                 uint32_t o[1][32] = {};
-                if (mine_has) {
+                const int col = half * (kDim / 2) + 32 * c;
+                if (has) {
                     tmem_load32(o[0], out + 32 * c);
                     tmem_wait_load(o);
                 }
@@ -432,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             eight[k] = __uint_as_float(o[0][e + k]);
-                            if (two) eight[k] += hand[(32 * c + e + k) * kRows + r];
+                            if (two) eight[k] += hand[(col + e + k) * kRows + r];
                             eight[k] *= a.scale;
                         }
-                        if (32 * c + e < a.dim) store<T, 8>(row + 32 * c + e, eight);
+                        if (col + e < a.dim) store<T, 8>(row + col + e, eight);
                     }
                 }
             }
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
     }
     __syncthreads();
     tmem_fence_after();
-    if (warp == 9) tmem_free<512>(tmem);
+    if (warp == kMmaWarp) tmem_free<512>(tmem);
 }
 
 // ---- dk, dv ----------------------------------------------------------------------
@@ -460,7 +468,7 @@ struct KeyShape {
     static constexpr uint32_t kBytes = kStats + kStages * kCols * sizeof(float2);
 };
 
-template <class T, int kDim>
+template <class T, int kDim, bool kDrop, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant__ BwdParams p)
 {
     using S = KeyShape<kDim>;
@@ -488,18 +496,18 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
     if (threadIdx.x == 0) {
         stalled = 0;
         for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4);
+        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 8);
         barrier_init(done, 1), barrier_init(k_full, 1);
         fence_barrier_init();
     }
-    if (warp == 9) tmem_alloc<512>(smem_address(&tmem_base));
+    if (warp == kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_base, dv_at = tmem + 4 * kCols, dk_at = dv_at + 128;
-    if (warp >= 8) {
+    if (warp >= kTmaWarp) {
         give_registers<kOtherRegisters>();
-        if (warp == 8) {
+        if (warp == kTmaWarp) {
             // ---- TMA: k and v, then the queries' tiles, head by head
             if (elect_one() && tiles) {
                 barrier_expect(k_full, 2 * S::kRowsBytes);
@@ -524,34 +532,42 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
                     for (int32_t n = max(0, tiles - S::kStages); n < tiles; ++n)
                         for (uint32_t tries = 0; tries < 100000 && !barrier_try(full + 8 * (n % S::kStages), n / S::kStages & 1u); ++tries) {}
             }
-        } else if (warp == 9) {
+        } else if (warp == kMmaWarp) {
             // ---- MMA
             if (elect_one() && tiles) {
                 constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
-                auto scores = [&](int32_t n) {
-                    const uint32_t stage = n % S::kStages, slot = n & 1, q = base + S::kRing + stage * S::kStageBytes;
-                    barrier_wait(full + 8 * stage, n / S::kStages & 1u, &stalled);
-                    tmem_fence_after();
-                    for (int x = 0; x < 2; ++x)  // S^T = K Q^T, dP^T = V dO^T
-                        for (int i = 0; i < kDim / 16; ++i)
-                            mma_step(tmem + slot * 2 * kCols + x * kCols,
-                                     row_major_tile(base + x * S::kRowsBytes + i / 4 * kRowsBox + i % 4 * 32),
-                                     row_major_tile(q + x * S::kColsBytes + i / 4 * kColsBox + i % 4 * 32), kScores, i > 0);
-                    mma_commit(scored + 8 * slot);
-                };
                 barrier_wait(k_full, 0, &stalled);
-                for (int32_t n = 0; n < 2 && n < tiles; ++n) scores(n);
-                for (int32_t n = 0; n < tiles; ++n) {
-                    const uint32_t stage = n % S::kStages, slot = n & 1, q = base + S::kRing + stage * S::kStageBytes;
-                    barrier_wait(ready + 8 * slot, n / 2 & 1u, &stalled);
-                    tmem_fence_after();
-                    for (int x = 0; x < 2; ++x)  // dV += P^T dO, dK += dS^T Q
-                        for (int i = 0; i < kCols / 16; ++i)
-                            mma_step_tmem(x ? dk_at : dv_at, tmem + slot * 2 * kCols + x * 32 + i * 8,
-                                          column_major_tile(q + (x ? 0 : S::kColsBytes) + i * 2048, S::kBoxes > 1 ? kColsBox : 1024),
-                                          kOut, n > 0 || i > 0);
-                    mma_commit(empty + 8 * stage);
-                    if (n + 2 < tiles) scores(n + 2);
+#pragma unroll 1
+                for (int32_t n = -2; n < tiles; ++n) {
+                    const uint32_t slot = n & 1;
+                    if (n >= 0) {  // dV += P^T dO, dK += dS^T Q
+                        const uint32_t stage = n % S::kStages, q = base + S::kRing + stage * S::kStageBytes;
+                        barrier_wait(ready + 8 * slot, n / 2 & 1u, &stalled);
+                        tmem_fence_after();
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint64_t qd = column_major_tile(q + (x ? 0 : S::kColsBytes), S::kBoxes > 1 ? kColsBox : 1024);
+#pragma unroll
+                            for (int i = 0; i < kCols / 16; ++i)
+                                mma_step_tmem(x ? dk_at : dv_at, tmem + slot * 2 * kCols + x * 16 + i / 2 * kHalf + i % 2 * 8,
+                                              qd + i * (2048 / 16), kOut, n > 0 || i > 0);
+                        }
+                        mma_commit(empty + 8 * stage);
+                    }
+                    if (n + 2 < tiles) {  // S^T = K Q^T, dP^T = V dO^T
+                        const uint32_t stage = (n + 2) % S::kStages, q = base + S::kRing + stage * S::kStageBytes;
+                        barrier_wait(full + 8 * stage, (n + 2) / S::kStages & 1u, &stalled);
+                        tmem_fence_after();
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint64_t kd = row_major_tile(base + x * S::kRowsBytes), qd = row_major_tile(q + x * S::kColsBytes);
+#pragma unroll
+                            for (int i = 0; i < kDim / 16; ++i)
+                                mma_step(tmem + slot * 2 * kCols + x * kCols, kd + row_step(i, kRowsBox), qd + row_step(i, kColsBox), kScores,
+                                         i > 0);
+                        }
+                        mma_commit(scored + 8 * slot);
+                    }
                 }
                 mma_commit(done);
             }
@@ -559,63 +575,75 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
     } else {
         take_registers<kSlotRegisters>();
         // ---- the slots' rows: a key each
-        const int slot = warp / 4;
+        const int slot = warp / 8, half = warp / 4 % 2;
         const int32_t j = j0 + (warp % 4) * 32 + lane, warp_j = j0 + (warp % 4) * 32;
-        const uint32_t lanes = (warp % 4) * 32u << 16, mine = tmem + slot * 2 * kCols + lanes;
-        const bool plain = is_plain(a), any = warp_j < keys;
+        const uint32_t lanes = (warp % 4) * 32u << 16;
+        const uint32_t mine = tmem + slot * 2 * kCols + lanes + half * kHalf;  // S^T, then P^T and dS^T; dP^T kCols on
+        const bool any = warp_j < keys;
         const int32_t reach = bias_reach(a.buckets);
-        const int32_t last_start = plain ? 0 : a.buckets.starts[a.buckets.count - 2];
+        const int32_t last_start = !kBias ? 0 : a.buckets.starts[a.buckets.count - 2];
         constexpr float kUnlift = kLift<T> != 0.0f ? 1.0f / 1024.0f : 1.0f;
-        const float scale = a.mask.scale * kUnlift;
+        const float scale = a.mask.scale * kUnlift, to_base2 = a.scale * kLog2e;
         for (int32_t n = slot; n < tiles; n += 2) {
-            const int32_t head = head_kv * a.group + n / per_head, i0 = (begin + n % per_head) * kCols;
-            const float4 *stats = reinterpret_cast<const float4 *>(smem + S::kStats + n % S::kStages * kCols * sizeof(float2));
+            const int32_t head = head_kv * a.group + n / per_head, i0 = (begin + n % per_head) * kCols + half * kHalf;
+            const float4 *stats = reinterpret_cast<const float4 *>(smem + S::kStats + (n % S::kStages * kCols + half * kHalf) * sizeof(float2));
             barrier_wait(scored + 8 * slot, n / 2 & 1u, &stalled);
             tmem_fence_after();
             if (any) {
-                uint32_t v[4][32];  // S^T, then dP^T
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load32(v[c], mine + 32 * c);
+                uint32_t v[2][32];  // S^T, then dP^T
+                tmem_load32(v[0], mine);
+                tmem_load32(v[1], mine + kCols);
                 tmem_wait_load(v);
-                auto s = [&](int e) -> uint32_t & { return v[e / 32][e % 32]; };
-                auto dp = [&](int e) -> uint32_t & { return v[2 + e / 32][e % 32]; };
-                const int32_t rel = j - pos0 - i0;  // to the tile's first query
-                const int32_t low = warp_j - pos0 - i0 - (kCols - 1), high = warp_j + 31 - pos0 - i0;
-                const bool far = high <= -last_start || low >= last_start;
-                const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
-                const float edge = !plain && far ? bias[high <= -last_start ? 0 : 2 * reach - 1] : 0.0f;
-                const uint32_t c0 = a.first + ((static_cast<uint32_t>(b) * a.heads + head) * a.len_q + i0) * static_cast<uint32_t>(a.len_k) + j;
-                // causal: query i0 + e sees key j from e = rel on
-                const int32_t unseen = a.causal && high > 0 ? rel : 0;
+                uint32_t(&s)[32] = v[0], (&dp)[32] = v[1];
+                const int32_t rel = j - pos0 - i0;  // to the thread's first query
+                const int32_t low = warp_j - pos0 - i0 - (kHalf - 1), high = warp_j + 31 - pos0 - i0;
+                uint32_t c = a.first + ((static_cast<uint32_t>(b) * a.heads + head) * a.len_q + i0) * static_cast<uint32_t>(a.len_k) + j;
+                // P
+                if (!kBias) {
 #pragma unroll
-                for (int e = 0; e < kCols; e += 2) {
-                    const float4 st = stats[e / 2];  // two queries' lse, delta
-                    const float2 x = make_float2(__uint_as_float(s(e)), __uint_as_float(s(e + 1)));
-                    float2 f;
-                    if (plain) {
-                        const float to_base2 = a.scale * kLog2e;
-                        f = fma2(x, make_float2(to_base2, to_base2), make_float2(kLift<T> - st.x, kLift<T> - st.z));
-                    } else {
-                        const float2 by = far ? make_float2(edge, edge) : make_float2(bias[rel + reach - e], bias[rel + reach - e - 1]);
-                        f = fma2(x, make_float2(a.scale, a.scale), by);
+                    for (int e = 0; e < kHalf; e += 2) {
+                        const float4 st = stats[e / 2];  // two queries' lse, delta
+                        const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(to_base2, to_base2),
+                                              make_float2(kLift<T> - st.x, kLift<T> - st.z));
+                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
+                    }
+                } else {
+                    const bool far = high <= -last_start || low >= last_start;
+                    const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
+                    const float edge = far ? bias[high <= -last_start ? 0 : 2 * reach - 1] : 0.0f;
+                    bias += rel + reach;
+#pragma unroll
+                    for (int e = 0; e < kHalf; e += 2) {
+                        const float4 st = stats[e / 2];
+                        const float2 by = far ? make_float2(edge, edge) : make_float2(bias[-e], bias[-e - 1]);
+                        float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(a.scale, a.scale), by);
                         f = fma2(add2(f, make_float2(-st.x, -st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>));
+                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
                     }
-                    float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
-                    if (e < unseen) prob.x = 0.0f;
-                    if (e + 1 < unseen) prob.y = 0.0f;
-                    const float2 minus = make_float2(-st.y * kUnlift, -st.w * kUnlift);
-                    float2 d = fma2(make_float2(__uint_as_float(dp(e)), __uint_as_float(dp(e + 1))), make_float2(scale, scale), minus);
-                    float2 kept = prob;
-                    if (a.mask.threshold) {
-                        if (!keeps(a.mask, c0 + e * static_cast<uint32_t>(a.len_k))) kept.x = 0.0f, d.x = minus.x;
-                        if (!keeps(a.mask, c0 + (e + 1) * static_cast<uint32_t>(a.len_k))) kept.y = 0.0f, d.y = minus.y;
-                    }
-                    d = mul2(d, prob);
-                    s(e / 2) = pack2<T>(kept.x, kept.y);
-                    dp(e / 2) = pack2<T>(d.x, d.y);
                 }
-                tmem_store32(mine, v[0]);
-                tmem_store32(mine + 32, v[2]);
+                if (a.causal && high > 0) {  // query i0 + e sees key j from e = rel on
+#pragma unroll
+                    for (int e = 0; e < kHalf; ++e)
+                        if (e < rel) s[e] = 0;
+                }
+                // dropout(P) for dv, dS = P (dropout(dP) - delta) for dk
+#pragma unroll
+                for (int e = 0; e < kHalf; e += 2) {
+                    const float4 st = stats[e / 2];
+                    const float2 prob = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    float2 kept2 = prob, d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+                    if (kDrop) {
+                        const float2 k = make_float2(kept(a.mask, c), kept(a.mask, c + static_cast<uint32_t>(a.len_k)));
+                        c += 2 * static_cast<uint32_t>(a.len_k);
+                        kept2 = mul2(kept2, k), d = mul2(d, k);
+                    }
+                    d = fma2(d, make_float2(scale, scale), make_float2(-st.y * kUnlift, -st.w * kUnlift));
+                    d = mul2(d, prob);
+                    s[e / 2] = pack2<T>(kept2.x, kept2.y);
+                    dp[e / 2] = pack2<T>(d.x, d.y);
+                }
+                tmem_store16(mine, reinterpret_cast<const uint32_t(&)[16]>(v[0]));
+                tmem_store16(mine + 16, reinterpret_cast<const uint32_t(&)[16]>(v[1]));
                 tmem_wait_store();
             }
             tmem_fence_before();
@@ -632,11 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
             const Strides &st = slot ? a.dks : a.dvs;
             T *row = static_cast<T *>(slot ? a.dk : a.dv) + b * st.batch + j * st.len + head_kv * st.head;
             const float weight = slot ? a.scale : scale;
-#pragma unroll
-            for (int c = 0; c < kDim / 32; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < kDim / 64; ++c) {
                 uint32_t o[1][32] = {};
+                const int col = half * (kDim / 2) + 32 * c;
                 if (tiles) {
-                    tmem_load32(o[0], (slot ? dk_at : dv_at) + lanes + 32 * c);
+                    tmem_load32(o[0], (slot ? dk_at : dv_at) + lanes + col);
                     tmem_wait_load(o);
                 }
                 if (j < a.len_k) {
@@ -645,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
                         float eight[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) eight[k] = j < keys ? __uint_as_float(o[0][e + k]) * weight : 0.0f;
-                        if (32 * c + e < a.dim) store<T, 8>(row + 32 * c + e, eight);
+                        if (col + e < a.dim) store<T, 8>(row + col + e, eight);
                     }
                 }
             }
@@ -654,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
     }
     __syncthreads();
     tmem_fence_after();
-    if (warp == 9) tmem_free<512>(tmem);
+    if (warp == kMmaWarp) tmem_free<512>(tmem);
 }
 
 // ---- the table ---------------------------------------------------------------------
@@ -707,11 +736,11 @@ BwdPlan bwd_plan(const Attention &a)
     return f;
 }
 
-template <class T, int kDim, bool kSplitKeys>
+template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
 cudaError_t launch_queries(const BwdParams &p, cudaStream_t s)
 {
-    const auto kernel = query_kernel<T, kDim, kSplitKeys>;
-    const size_t bytes = 1024 + QueryShape<kDim, kSplitKeys>::kTable + (p.a.table ? 2 * bias_reach(p.a.buckets) * sizeof(float) : 0);
+    const auto kernel = query_kernel<T, kDim, kSplitKeys, kDrop, kBias>;
+    const size_t bytes = 1024 + QueryShape<kDim, kSplitKeys>::kTable + (kBias ? 2 * bias_reach(p.a.buckets) * sizeof(float) : 0);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.units) * p.q_tiles), kThreads, bytes, s>>>(p);
@@ -719,10 +748,10 @@ cudaError_t launch_queries(const BwdParams &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <class T, int kDim>
+template <class T, int kDim, bool kDrop, bool kBias>
 cudaError_t launch_keys(const BwdParams &p, cudaStream_t s)
 {
-    const auto kernel = key_kernel<T, kDim>;
+    const auto kernel = key_kernel<T, kDim, kDrop, kBias>;
     const size_t bytes = 1024 + KeyShape<kDim>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
@@ -731,6 +760,26 @@ cudaError_t launch_keys(const BwdParams &p, cudaStream_t s)
     kernel<<<static_cast<unsigned>(blocks), kThreads, bytes, s>>>(p);
     note_launch();
     return cudaGetLastError();
+}
+
+template <class T, int kDim, bool kDrop, bool kBias>
+cudaError_t launch_both(const BwdParams &p, bool queries, bool keys, bool split_keys, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    if (queries) e = split_keys ? launch_queries<T, kDim, true, kDrop, kBias>(p, s) : launch_queries<T, kDim, false, kDrop, kBias>(p, s);
+    if (e == cudaSuccess && keys) e = launch_keys<T, kDim, kDrop, kBias>(p, s);
+    return e;
+}
+
+template <class T, int kDim>
+cudaError_t launch_both(const BwdParams &p, bool queries, bool keys, bool split_keys, cudaStream_t s)
+{
+    const bool drop = p.a.mask.threshold != 0, bias = p.a.table != nullptr;
+    if (drop)
+        return bias ? launch_both<T, kDim, true, true>(p, queries, keys, split_keys, s)
+                    : launch_both<T, kDim, true, false>(p, queries, keys, split_keys, s);
+    return bias ? launch_both<T, kDim, false, true>(p, queries, keys, split_keys, s)
+                : launch_both<T, kDim, false, false>(p, queries, keys, split_keys, s);
 }
 
 }  // namespace
@@ -765,12 +814,9 @@ cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s)
         map(&p.k_rows, a.k, a.ks, a.len_k, a.heads_kv, 1, kRows), map(&p.v_rows, a.v, a.vs, a.len_k, a.heads_kv, 1, kRows);
         map(&p.k_cols, a.k, a.ks, a.len_k, a.heads_kv, 1, kCols), map(&p.v_cols, a.v, a.vs, a.len_k, a.heads_kv, 1, kCols);
     }
-    if (e == cudaSuccess && has_q) {
-        if (static_cast<int64_t>(f.units) * f.q_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-        if (f.dim == 64) e = f.split_keys ? launch_queries<T, 64, true>(p, s) : launch_queries<T, 64, false>(p, s);
-        else e = f.split_keys ? launch_queries<T, 128, true>(p, s) : launch_queries<T, 128, false>(p, s);
-    }
-    if (e == cudaSuccess && has_k) e = f.dim == 64 ? launch_keys<T, 64>(p, s) : launch_keys<T, 128>(p, s);
+    if (static_cast<int64_t>(f.units) * f.q_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (e == cudaSuccess)
+        e = f.dim == 64 ? launch_both<T, 64>(p, has_q, has_k, f.split_keys, s) : launch_both<T, 128>(p, has_q, has_k, f.split_keys, s);
     if (e == cudaSuccess && a.dtable && a.heads) {
         table_kernel<T><<<dim3(a.buckets.total, a.heads), 256, 0, s>>>(p);
         note_launch();

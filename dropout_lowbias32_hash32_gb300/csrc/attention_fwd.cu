@@ -2,12 +2,14 @@
 // the tensor cores.
 //
 // A block works on two "slots" of 128 query rows by 128 keys.  For a slot's key
-// tile, S = Q K^T goes to TMEM; each of the slot's 128 threads takes one row of
-// S, updates the row's running maximum and sum, and writes P = exp(S - max)
-// back over S in 16 bits; O += P V accumulates in TMEM with P as the
-// TMEM operand.  One thread issues all products (warp 9), one warp the TMA loads of
-// the key and value tiles (warp 8), and while a slot's threads work on its
-// scores the tensor core works for the other slot.
+// tile, S = Q K^T goes to TMEM; the slot's threads take the rows of S,
+// update the row's running maximum and sum, and write P = exp(S - max)
+// back over S in 16 bits; O += P V accumulates in TMEM with P as the TMEM
+// operand.  Two threads share a row, 64 keys each, so that four warps a
+// scheduler hide each other's latencies; they agree on the row's maximum only
+// when one of them has to raise it.  One thread issues all products, one warp
+// the TMA loads of the key and value tiles, and while a slot's threads work on
+// its scores the tensor core works for the other slot.
 //   kSplitKeys = false: the slots are two tiles of queries that share the key
 //     and value tiles (halving their traffic from L2);
 //   kSplitKeys = true: one tile of queries, the slots take every other key
@@ -25,9 +27,12 @@ namespace rngk {
 namespace {
 
 constexpr int kTile = 128;          // rows of a slot, keys of a tile
-constexpr int kThreads = 384;       // 2 x 128 for the slots, then a TMA warp, an MMA warp, two that only fill the warpgroup
-// registers: 384 threads start with 168 each; 2 x 208 + 88 = 3 x 168
-constexpr int kSlotRegisters = 208, kOtherRegisters = 88;
+constexpr int kHalf = kTile / 2;    // keys of a thread
+// 2 x 256 for the slots, then a TMA warp, an MMA warp, two that only fill the warpgroup
+constexpr int kThreads = 640;
+constexpr uint32_t kTmaWarp = 16, kMmaWarp = 17;
+// registers: 640 threads start with 96 each; 4 x 104 + 64 = 5 x 96
+constexpr int kSlotRegisters = 104, kOtherRegisters = 64;
 constexpr uint32_t kBox = 16384;    // bytes of 128 rows of 64 elements
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -48,15 +53,22 @@ struct Shape {
     static constexpr uint32_t kTable = kRing + kStages * kStageBytes;
 };
 
-// One slot's rows: the thread's row, its place and what it may see.
-struct Row {
-    int32_t i, head;
-    bool valid;
-    int32_t pos;
-    uint32_t counter;  // of key 0
-};
+// Barriers of a slot's 256 threads; slot_any also tells whether any of them
+// asked.
+__device__ __forceinline__ void slot_sync(int slot) { asm volatile("bar.sync %0, 256;" ::"r"(2 + slot) : "memory"); }
+__device__ __forceinline__ bool slot_any(int slot, bool ask)
+{
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(yes)
+        : "r"(static_cast<uint32_t>(ask)), "r"(2 + slot)
+        : "memory");
+    return yes != 0;
+}
 
-template <class T, int kDim, bool kSplitKeys>
+template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid_constant__ FwdParams p)
 {
     using S = Shape<kDim, kSplitKeys>;
@@ -64,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     __shared__ alignas(8) uint64_t bars[2 * S::kStages + 8];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t stalled;
-    __shared__ float join[2 * kTile];
+    __shared__ float tops[2][2][2][kTile], sums[2][2][kTile];  // [turn's parity][slot][half][row], [slot][half][row]
     const Attention &a = p.a;
     const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
     uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
@@ -104,12 +116,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     if (threadIdx.x == 0) {
         stalled = 0;
         for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4);
+        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 8);
         barrier_init(done, 1), barrier_init(q_full, 1), barrier_init(tail, 1);
         fence_barrier_init();
     }
-    if (warp == 9) tmem_alloc<512>(smem_address(&tmem_base));
-    if (a.table) {  // the bias by relative position, head head0 (pack is 1)
+    if (warp == kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
+    if (kBias) {  // the bias by relative position, head head0 (pack is 1)
         const int32_t reach = bias_reach(a.buckets);
         for (int32_t t = threadIdx.x; t < 2 * reach; t += kThreads)
             table[t] = to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, t - reach) * a.heads + head0]);
@@ -118,9 +130,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
-    if (warp >= 8) {
+    if (warp >= kTmaWarp) {
       give_registers<kOtherRegisters>();
-      if (warp == 8) {
+      if (warp == kTmaWarp) {
         // ---- TMA: the queries, then K_0 .. K_{lead-1} and alternately V_n, K_{n+lead}
         constexpr int kLead = kSplitKeys ? 2 : 1;
         const bool one = elect_one();
@@ -164,11 +176,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         if (stalled && one)  // nothing may land after the block has ended
             for (uint32_t u = use > S::kStages ? use - S::kStages : 0; u < use; ++u)
                 for (uint32_t tries = 0; tries < 100000 && !barrier_try(full + 8 * (u % S::kStages), u / S::kStages & 1u); ++tries) {}
-      } else if (warp == 9) {
+      } else if (warp == kMmaWarp) {
         // ---- MMA
         if (elect_one() && tiles) {
             constexpr uint32_t kScores = mma_shape<T>(kTile, false), kOut = mma_shape<T>(kDim, true);
-            uint32_t use = 0, given[2] = {0, 0};
+            uint32_t use = 0, given0 = 0, given1 = 0;
             auto acquire = [&] {
                 const uint32_t stage = use % S::kStages;
                 barrier_wait(full + 8 * stage, use / S::kStages & 1u, &stalled);
@@ -181,48 +193,51 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             };
             auto scores = [&](int slot, uint32_t stage) {
                 const uint32_t q = base + (kSplitKeys ? 0 : slot) * S::kStageBytes, k = base + S::kRing + stage * S::kStageBytes;
+                const uint64_t qd = row_major_tile(q), kd = row_major_tile(k);
+#pragma unroll
                 for (int i = 0; i < kDim / 16; ++i) {
-                    const uint32_t o = i / 4 * kBox + i % 4 * 32;
-                    mma_step(tmem + slot * 256, row_major_tile(q + o), row_major_tile(k + o), kScores, i > 0);
+                    constexpr uint32_t kStep = 16;  // descriptors count 16 bytes
+                    const uint32_t o = (i / 4 * kBox + i % 4 * 32) / kStep;
+                    mma_step(tmem + slot * 256, qd + o, kd + o, kScores, i > 0);
                 }
                 mma_commit(scored + 8 * slot);
             };
             auto products = [&](int slot, uint32_t stage, bool first) {
                 const uint32_t v = base + S::kRing + stage * S::kStageBytes;
-                barrier_wait(ready + 8 * slot, given[slot]++ & 1u, &stalled);
+                barrier_wait(ready + 8 * slot, (slot ? given1++ : given0++) & 1u, &stalled);
                 tmem_fence_after();
+                const uint64_t vd = column_major_tile(v, S::kBoxes > 1 ? kBox : 1024);
+#pragma unroll
                 for (int i = 0; i < kTile / 16; ++i)
-                    mma_step_tmem(tmem + slot * 256 + kTile, tmem + slot * 256 + i * 8, column_major_tile(v + i * 2048, S::kBoxes > 1 ? kBox : 1024),
-                                  kOut, !first || i > 0);
+                    mma_step_tmem(tmem + slot * 256 + kTile, tmem + slot * 256 + i / 4 * kHalf + i % 4 * 8, vd + i * (2048 / 16), kOut,
+                                  !first || i > 0);
             };
             barrier_wait(q_full, 0, &stalled);
             if (kSplitKeys) {
-                for (int32_t n = 0; n < 2 && n < tiles; ++n) scores(n, acquire()), release();
-                for (int32_t n = 0; n < tiles; ++n) {
-                    products(n & 1, acquire(), n < 2), release();
+#pragma unroll 1
+                for (int32_t n = -2; n < tiles; ++n) {
+                    if (n >= 0) products(n & 1, acquire(), n < 2), release();
                     if (n + 2 < tiles) scores(n & 1, acquire()), release();
                 }
             } else {
-                const uint32_t k0 = acquire();
-                for (int s = 0; s < 2; ++s)
-                    if (count[s]) scores(s, k0);
-                release();
-                for (int32_t n = 0; n < tiles; ++n) {
-                    // the stages of V_n and K_{n+1}, each released when both slots have used it
-                    const uint32_t vs = acquire();
-                    uint32_t ks = 0;
+                // the stages of V_n and K_{n+1}, each released when both slots have used it
+#pragma unroll 1
+                for (int32_t n = -1; n < tiles; ++n) {
+                    const uint32_t vs = n >= 0 ? acquire() : 0;
+                    uint32_t ks = S::kStages;
+#pragma unroll 1
                     for (int s = 0; s < 2; ++s) {
-                        if (n < count[s]) products(s, vs, n == 0);
+                        if (n >= 0 && n < count[s]) products(s, vs, n == 0);
                         if (n + 1 < count[s]) {
-                            if (s == 0 || n + 1 >= count[0]) {
-                                ++use;
+                            if (ks == S::kStages) {
+                                if (n >= 0) ++use;
                                 ks = acquire();
-                                --use;
+                                if (n >= 0) --use;
                             }
                             scores(s, ks);
                         }
                     }
-                    release();
+                    if (n >= 0) release();
                     if (n + 1 < tiles) release();
                 }
             }
@@ -232,54 +247,53 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     } else {
         take_registers<kSlotRegisters>();
         // ---- the slots' rows
-        const int slot = warp / 4;
+        const int slot = warp / 8, half = warp / 4 % 2;
         const int32_t r = (warp % 4) * 32 + lane;
-        const uint32_t mine = tmem + slot * 256 + ((warp % 4) * 32u << 16);
-        const uint32_t out = mine + kTile;
-        const int32_t warp_i = i0 + ((kSplitKeys ? 0 : slot * kTile) + (warp % 4) * 32) / p.pack;  // the warp's first query
-        Row row;
-        row.i = i0 + ((kSplitKeys ? 0 : slot * kTile) + r) / p.pack;
-        row.head = head0 + r % p.pack;
-        row.valid = row.i < a.len_q;
-        row.pos = pos0 + row.i;
-        row.counter = a.first + ((static_cast<uint32_t>(b) * a.heads + row.head) * a.len_q + row.i) * static_cast<uint32_t>(a.len_k);
-        const bool any = warp_i < a.len_q;  // whether the warp has a query at all
-        const int32_t visible = a.causal ? min(keys, row.pos + 1) : keys;
+        const uint32_t lanes = (warp % 4) * 32u << 16;
+        const uint32_t mine = tmem + slot * 256 + lanes + half * kHalf;              // the thread's scores, then its P
+        const uint32_t out = tmem + slot * 256 + lanes + kTile + half * (kDim / 2);  // its half of O's columns
+        const int32_t row0 = (kSplitKeys ? 0 : slot * kTile);
+        const int32_t warp_i = i0 + (row0 + (warp % 4) * 32) / p.pack;  // the warp's first query
+        const int32_t i = i0 + (row0 + r) / p.pack, head = head0 + r % p.pack, pos = pos0 + i;
+        const bool valid = i < a.len_q, any = warp_i < a.len_q;
+        const int64_t index = (static_cast<int64_t>(b) * a.heads + head) * a.len_q + i;
+        const uint32_t counter = a.first + static_cast<uint32_t>(index) * static_cast<uint32_t>(a.len_k) + half * kHalf;
+        const int32_t visible = a.causal ? min(keys, pos + 1) : keys;
         const int32_t warp_visible = a.causal ? min(keys, pos0 + warp_i + 1) : keys;  // the least of the warp's
-        const bool biased = a.table != nullptr, plain = !biased && a.scale > 0.0f;
+        const bool plain = !kBias && a.scale > 0.0f;
         // scores are held before (plain) or after their scaling and bias; base two is for the exponential
         const float to_base2 = plain ? a.scale * kLog2e : kLog2e, to_natural = plain ? a.scale : 1.0f;
-        const int32_t reach = biased ? bias_reach(a.buckets) : 0;
-        const float bias_low = biased ? table[0] : 0.0f, bias_high = biased ? table[2 * reach - 1] : 0.0f;
+        const int32_t reach = kBias ? bias_reach(a.buckets) : 0;
+        const float bias_low = kBias ? table[0] : 0.0f, bias_high = kBias ? table[2 * reach - 1] : 0.0f;
         float top = -INFINITY, sum = 0.0f;
-        int32_t n = kSplitKeys ? slot : 0;
         uint32_t turn = 0;
-        for (; n < count[kSplitKeys ? 0 : slot]; n += kSplitKeys ? 2 : 1, ++turn) {
-            const int32_t j0 = (tile0 + n) * kTile;
+        for (int32_t n = kSplitKeys ? slot : 0; n < count[kSplitKeys ? 0 : slot]; n += kSplitKeys ? 2 : 1, ++turn) {
+            const int32_t j0 = (tile0 + n) * kTile + half * kHalf;
             barrier_wait(scored + 8 * slot, turn & 1u, &stalled);
             tmem_fence_after();
+            uint32_t s[2][32];
+            float tile_top = -INFINITY;
             if (any) {
-                uint32_t s[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_load32(s[c], mine + 32 * c);
+                for (int c = 0; c < 2; ++c) tmem_load32(s[c], mine + 32 * c);
                 tmem_wait_load(s);
-                if (biased) {
+                if (kBias) {
                     // relative positions of the warp's pairs: beyond the last bucket's start on one side, or by the table
-                    const int32_t low = j0 - (pos0 + warp_i + 31), high = j0 + kTile - 1 - (pos0 + warp_i);
+                    const int32_t low = j0 - (pos0 + warp_i + 31), high = j0 + kHalf - 1 - (pos0 + warp_i);
                     const float2 scale = make_float2(a.scale, a.scale);
                     if (high <= -a.buckets.max_distance || low >= a.buckets.max_distance) {
                         const float v = high < 0 ? bias_low : bias_high;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int e = 0; e < 32; e += 2) {
                                 const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale, make_float2(v, v));
                                 s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
                             }
                     } else {
-                        const float *t = table + (j0 - row.pos + reach);
+                        const float *t = table + (j0 - pos + reach);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int e = 0; e < 32; e += 2) {
                                 const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale,
@@ -289,14 +303,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     }
                 } else if (!plain) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) * a.scale);
                 }
-                if (j0 + kTile > warp_visible) {
+                if (j0 + kHalf > warp_visible) {
                     const int32_t seen = visible - j0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (32 * c + e >= seen) s[c][e] = __float_as_uint(-INFINITY);
@@ -304,54 +318,63 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                 float most[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    most[c] = __uint_as_float(s[c][0]);
+                    const uint32_t(&q)[16] = *reinterpret_cast<const uint32_t(*)[16]>(&s[c / 2][c % 2 * 16]);
+                    most[c] = __uint_as_float(q[0]);
 #pragma unroll
-                    for (int e = 1; e < 31; e += 2)
-                        most[c] = max3(most[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                    most[c] = fmaxf(most[c], __uint_as_float(s[c][31]));
+                    for (int e = 1; e < 15; e += 2) most[c] = max3(most[c], __uint_as_float(q[e]), __uint_as_float(q[e + 1]));
+                    most[c] = fmaxf(most[c], __uint_as_float(q[15]));
                 }
-                const float tile_top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-                // a new maximum, and O and the sum brought to it: at the first finite score, or 2^8 above the old one
-                const bool raise = tile_top > top && (top == -INFINITY || (tile_top - top) * to_base2 > 8.0f);
-                if (__any_sync(0xFFFFFFFFu, raise)) {
-                    const float next = raise ? tile_top : top;
+                tile_top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+            }
+            // A new maximum, and O and the sums brought to it: at the first finite score, or 2^8 above the old one.
+            // Where one of the slot's threads needs it, its rows' halves meet.
+            const bool want = tile_top > top && (top == -INFINITY || (tile_top - top) * to_base2 > 8.0f);
+            if (slot_any(slot, want)) {
+                float(&meet)[2][kTile] = tops[turn & 1u][slot];
+                meet[half][r] = tile_top;
+                slot_sync(slot);
+                const float most = fmaxf(meet[0][r], meet[1][r]);
+                const bool raise = most > top && (top == -INFINITY || (most - top) * to_base2 > 8.0f);
+                if (any && __any_sync(0xFFFFFFFFu, raise)) {
+                    const float next = raise ? most : top;
                     const float fade = raise ? exp2_approx((top - next) * to_base2) : 1.0f;
                     sum *= fade;
                     top = next;
                     if (turn) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < kDim / 32; ++c) {
-                            uint32_t o[1][32];
-                            tmem_load32(o[0], out + 32 * c);
-                            tmem_wait_load(o);
+                            uint32_t o[16];
+                            tmem_load16(o, out + 16 * c);
+                            tmem_wait_load16(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[0][e] = __float_as_uint(__uint_as_float(o[0][e]) * fade);
-                            tmem_store32(out + 32 * c, o[0]);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                            tmem_store16(out + 16 * c, o);
                         }
                     }
                 }
+            }
+            if (any) {
                 // exp2((s - top) to_base2): as one multiply-add, or, where a bias may be the type's
                 // lowest value, with the difference taken first
                 const float from = top == -INFINITY ? 0.0f : -top, shift = from * to_base2;
                 const float2 from2 = make_float2(from, from), shift2 = make_float2(shift, shift);
                 const float2 base2 = make_float2(to_base2, to_base2);
                 float2 total = make_float2(0.0f, 0.0f);
-                const uint32_t c0 = row.counter + j0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[16];
+                for (int c = 0; c < 2; ++c) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
                         const float2 v = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
                         const float2 f = plain ? fma2(v, base2, shift2) : mul2(add2(v, from2), base2);
-                        float2 q = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                        const float2 q = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                         total = add2(total, q);
-                        if (a.mask.threshold) {
-                            if (!keeps(a.mask, c0 + 32 * c + e)) q.x = 0.0f;
-                            if (!keeps(a.mask, c0 + 32 * c + e + 1)) q.y = 0.0f;
-                        }
-                        w[e / 2] = pack2<T>(q.x, q.y);
+                        s[c][e] = __float_as_uint(q.x), s[c][e + 1] = __float_as_uint(q.y);
                     }
+                    if (kDrop) drop32(a.mask, counter + (tile0 + n) * kTile + 32 * c, s[c]);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2)
+                        w[e / 2] = pack2<T>(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
                     tmem_store16(mine + 16 * c, w);
                 }
                 sum += total.x + total.y;
@@ -367,54 +390,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             barrier_wait(done, 0, &stalled);
             tmem_fence_after();
         }
-        if (kSplitKeys) {  // slot 1 hands its part to slot 0 through the ring, which nothing reads any more
-            float *hand = reinterpret_cast<float *>(smem + S::kRing);
-            const bool has = tiles > 1;
-            if (slot == 1 && has && any) {
-                join[r] = top, join[kTile + r] = sum;
+        sums[slot][half][r] = sum;
+        if (kSplitKeys && half == 0) tops[0][slot][0][r] = top;
+        float *hand = reinterpret_cast<float *>(smem + S::kRing);  // the ring, which nothing reads any more
+        const bool two = kSplitKeys && tiles > 1;
+        if (two && slot == 1 && any) {  // slot 1 hands its part to slot 0
 #pragma unroll
-                for (int c = 0; c < kDim / 32; ++c) {
-                    uint32_t o[1][32];
-                    tmem_load32(o[0], out + 32 * c);
-                    tmem_wait_load(o);
+            for (int c = 0; c < kDim / 64; ++c) {
+                uint32_t o[1][32];
+                tmem_load32(o[0], out + 32 * c);
+                tmem_wait_load(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) hand[(32 * c + e) * kTile + r] = __uint_as_float(o[0][e]);
-                }
+                for (int e = 0; e < 32; ++e) hand[(half * (kDim / 2) + 32 * c + e) * kTile + r] = __uint_as_float(o[0][e]);
             }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
         }
+        asm volatile("bar.sync 1, 512;" ::: "memory");
         if (any && (!kSplitKeys || slot == 0)) {
             float weight = 1.0f, other = 0.0f;
-            const float *hand = reinterpret_cast<const float *>(smem + S::kRing);
-            const bool two = kSplitKeys && tiles > 1;
+            sum = sums[slot][0][r] + sums[slot][1][r];
             if (two) {
-                const float top1 = join[r], sum1 = join[kTile + r], most = fmaxf(top, top1);
+                const float top1 = tops[0][1][0][r], sum1 = sums[1][0][r] + sums[1][1][r], most = fmaxf(top, top1);
                 weight = top == -INFINITY ? 0.0f : exp2_approx((top - most) * to_base2);
                 other = top1 == -INFINITY ? 0.0f : exp2_approx((top1 - most) * to_base2);
                 sum = sum * weight + sum1 * other;
                 top = most;
             }
             const bool whole = p.splits == 1;
-            const int64_t index = (static_cast<int64_t>(b) * a.heads + row.head) * a.len_q + row.i;
             float *part = p.part + (static_cast<int64_t>(split) * a.batch * a.heads * a.len_q + index) * (kDim + 2);
             const float scale = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.mask.scale / sum;
-            T *o_row = static_cast<T *>(a.out) + b * a.os.batch + row.i * a.os.len + row.head * a.os.head;
+            T *o_row = static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head;
 #pragma unroll
-            for (int c = 0; c < kDim / 32; ++c) {
-                uint32_t o[1][32];
+            for (int c = 0; c < kDim / 64; ++c) {
+                uint32_t o[1][32] = {};
+                const int col = half * (kDim / 2) + 32 * c;
                 if (tiles) {
                     tmem_load32(o[0], out + 32 * c);
                     tmem_wait_load(o);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[0][e] = 0;
                 }
-                if (row.valid) {
+                if (valid) {
                     float v[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         v[e] = __uint_as_float(o[0][e]);
-                        if (two) v[e] = v[e] * weight + hand[(32 * c + e) * kTile + r] * other;
+                        if (two) v[e] = v[e] * weight + hand[(col + e) * kTile + r] * other;
                         if (sum == 0.0f) v[e] = 0.0f;  // nothing seen
                         v[e] *= scale;
                     }
@@ -422,15 +440,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             const float(&eight)[8] = *reinterpret_cast<const float(*)[8]>(&v[e]);
-                            if (32 * c + e < a.dim) store<T, 8>(o_row + 32 * c + e, eight);
+                            if (col + e < a.dim) store<T, 8>(o_row + col + e, eight);
                         }
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2 *>(part + 32 * c + e) = make_float2(v[e], v[e + 1]);
+                        for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2 *>(part + col + e) = make_float2(v[e], v[e + 1]);
                     }
                 }
             }
-            if (row.valid) {
+            if (valid && half == 0) {
                 if (!whole)
                     part[kDim] = top * to_natural, part[kDim + 1] = sum;
                 else if (a.lse)
@@ -441,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     }
     __syncthreads();
     tmem_fence_after();
-    if (warp == 9) tmem_free<512>(tmem);
+    if (warp == kMmaWarp) tmem_free<512>(tmem);
 }
 
 // Joins the key axis's splits: a warp to a row.
@@ -503,13 +521,12 @@ FwdPlan fwd_plan(const Attention &a)
     return f;
 }
 
-template <class T, int kDim, bool kSplitKeys>
+template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
 cudaError_t launch(const FwdParams &p, cudaStream_t s)
 {
     using S = Shape<kDim, kSplitKeys>;
-    const auto kernel = attention_fwd_kernel<T, kDim, kSplitKeys>;
-    const size_t table = p.a.table ? 2 * (p.a.buckets.max_distance + 160) * sizeof(float) : 0;
-    const size_t bytes = 1024 + S::kTable + table;
+    const auto kernel = attention_fwd_kernel<T, kDim, kSplitKeys, kDrop, kBias>;
+    const size_t bytes = 1024 + S::kTable + (kBias ? 2 * bias_reach(p.a.buckets) * sizeof(float) : 0);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.units) * p.q_tiles * p.splits), kThreads, bytes, s>>>(p);
@@ -520,6 +537,14 @@ cudaError_t launch(const FwdParams &p, cudaStream_t s)
         note_launch();
     }
     return cudaGetLastError();
+}
+
+template <class T, int kDim, bool kSplitKeys>
+cudaError_t launch(const FwdParams &p, cudaStream_t s)
+{
+    const bool drop = p.a.mask.threshold != 0, bias = p.a.table != nullptr;
+    if (drop) return bias ? launch<T, kDim, kSplitKeys, true, true>(p, s) : launch<T, kDim, kSplitKeys, true, false>(p, s);
+    return bias ? launch<T, kDim, kSplitKeys, false, true>(p, s) : launch<T, kDim, kSplitKeys, false, false>(p, s);
 }
 
 }  // namespace

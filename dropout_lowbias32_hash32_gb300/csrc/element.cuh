@@ -5,9 +5,11 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "hash32.cuh"
+#include "internal.h"
 
 namespace rngk {
 
@@ -114,17 +116,74 @@ __device__ __forceinline__ void store(T *p, const float (&v)[V])
     }
 }
 
-// Dropout as the layer kernels apply it: keep iff the draw's low 23 bits reach
-// the threshold ceil(p 2^23); the scale 1 / (1 - p) is multiplied by the
-// caller.  threshold 0 (p = 0) keeps everything.
+// Dropout as the layer kernels apply it: keep iff the draw's low 23 bits m
+// reach the threshold T = ceil(p 2^23); the scale 1 / (1 - p) is multiplied by
+// the caller.  threshold 0 (p = 0) keeps everything.
+//
+// The kernels are bound by the hash's logic operations (the ALU pipe takes one
+// warp instruction in two cycles), so the decision is made on the FMA pipe:
+// 1 + m 2^-23 is put together from the draw by one byte permutation and one
+// logic operation, and 2^30 (1 + m 2^-23) - (2^30 + 2^7 (T - 1)) = 2^7 (m - T +
+// 1), which a multiply-add gives exactly, saturates to 1 for m >= T and to 0
+// below.
 struct Mask {
     uint32_t key, threshold;
     float scale;
+    float bar;  // -(2^30 + 2^7 (T - 1)), exact for T >= 1
 };
 
-__device__ __forceinline__ bool keeps(const Mask &m, uint32_t c)
+inline Mask make_mask(float p, uint32_t seed)
 {
-    return (draw32(m.key, c) & 0x7FFFFFu) >= m.threshold;
+    // keep iff m 2^-23 >= p  <=>  m >= ceil(p 2^23), exact in binary64
+    const uint32_t t = static_cast<uint32_t>(std::ceil(static_cast<double>(p) * 8388608.0));
+    return Mask{seed_key(seed), t, 1.0f / (1.0f - p), -(1073741824.0f + 128.0f * (static_cast<float>(t) - 1.0f))};
+}
+
+// 1 for a kept element, 0 for a dropped one, from hash32 after its first
+// xorshift with the key.
+__device__ __forceinline__ float kept_of(const Mask &m, uint32_t x)
+{
+    x *= 0x7FEB352Du;
+    x ^= x >> 15;
+    x *= 0x846CA68Bu;
+    const uint32_t high = __byte_perm(x, 0x3F800000u, 0x7632);  // x >> 16 under the exponent of 1.0
+    float k;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(k) : "f"(__uint_as_float(high ^ (x & 0x7FFFFFu))), "f"(1073741824.0f), "f"(m.bar));
+    return k;
+}
+__device__ __forceinline__ float kept(const Mask &m, uint32_t c) { return kept_of(m, c ^ (c >> 16) ^ m.key); }
+
+// Bit e: whether c + e is kept, e < 32.  A loop, for the rare rows whose
+// counters cross a multiple of 2^16.
+__device__ __forceinline__ uint32_t kept_bits(const Mask &m, uint32_t c)
+{
+    uint32_t bits = 0;
+#pragma unroll 1
+    for (uint32_t e = 0; e < 32; ++e) bits |= kept(m, c + e) != 0.0f ? 1u << e : 0u;
+    return bits;
+}
+
+// Whether the counters c .. c + n - 1 share their high halves, in every lane of
+// the warp: then kept_of(m, (c + e) ^ high_key(m, c)) is kept(m, c + e).
+__device__ __forceinline__ bool one_high_half(uint32_t c, uint32_t n)
+{
+    return __all_sync(0xFFFFFFFFu, ((c ^ (c + (n - 1u))) >> 16) == 0u);
+}
+__device__ __forceinline__ uint32_t high_key(const Mask &m, uint32_t c) { return m.key ^ (c >> 16); }
+
+// Drops of 32 f32 values those whose counters c, c + 1, ... say so.
+__device__ __forceinline__ void drop32(const Mask &m, uint32_t c, uint32_t (&v)[32])
+{
+    if (one_high_half(c, 32)) {
+        const uint32_t key = high_key(m, c);
+#pragma unroll
+        for (uint32_t e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kept_of(m, (c + e) ^ key));
+    } else {
+        const uint32_t bits = kept_bits(m, c);
+#pragma unroll
+        for (uint32_t e = 0; e < 32; ++e)
+            if (!(bits >> e & 1u)) v[e] = 0;
+    }
 }
 
 }  // namespace rngk

@@ -124,11 +124,6 @@ rng_status check_probability(const char *what, float p)
     return RNG_OK;
 }
 
-Mask make_mask(float p, uint32_t seed)
-{
-    return Mask{seed_key(seed), static_cast<uint32_t>(std::ceil(static_cast<double>(p) * 8388608.0)), 1.0f / (1.0f - p)};
-}
-
 // f(T, W) for the element types' tags.
 template <class F>
 cudaError_t with_types(rng_dtype dtype, rng_dtype param, F &&f)

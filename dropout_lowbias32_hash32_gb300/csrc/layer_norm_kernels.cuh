@@ -66,7 +66,7 @@ __device__ __forceinline__ void hidden(const NormFwd &a, const Raw<T, V> &x, con
     }
     if (a.mask.threshold) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) h[k] = keeps(a.mask, c + k) ? h[k] * a.mask.scale : 0.0f;
+        for (int k = 0; k < V; ++k) h[k] = kept(a.mask, c + k) != 0.0f ? h[k] * a.mask.scale : 0.0f;
     }
     if (a.residual.p) {
         float r[V];
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_bwd_kernel(const __gr
                 if (a.mask.threshold) {
 #pragma unroll
                     for (int k = 0; k < V; ++k)
-                        dz[k] = keeps(a.mask, c0 + v * V + k) ? dz[k] * a.mask.scale : 0.0f;
+                        dz[k] = kept(a.mask, c0 + v * V + k) != 0.0f ? dz[k] * a.mask.scale : 0.0f;
                 }
 #pragma unroll
                 for (int k = 0; k < V; ++k) dbias[i][k] += dz[k];
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(const __grid_cons
         if (a.dh.p) dz += to_f32(row_of<T>(a.dh, row)[j]);
         if (a.dresidual.p) row_of<T>(a.dresidual, row)[j] = from_f32<T>(dz);
         if (a.mask.threshold)
-            dz = keeps(a.mask, a.first + static_cast<uint32_t>(row) * a.cols + j) ? dz * a.mask.scale : 0.0f;
+            dz = kept(a.mask, a.first + static_cast<uint32_t>(row) * a.cols + j) != 0.0f ? dz * a.mask.scale : 0.0f;
         row_of<T>(a.dx, row)[j] = from_f32<T>(dz);
         dgamma += dy * n, dbeta += dy, dbias += dz;
     }

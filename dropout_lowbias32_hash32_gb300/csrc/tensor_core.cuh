@@ -61,13 +61,15 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity)
 // and ends, and the host can read that it happened.
 __device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t *stalled)
 {
-    if (barrier_try(bar, parity)) return;
-    for (uint32_t tries = 0; tries < (1u << 20); ++tries) {
-        if (barrier_try(bar, parity)) return;
+#pragma unroll 1
+    for (uint32_t tries = 0; !barrier_try(bar, parity); ++tries) {
         if (*stalled) return;
+        if (tries == 1u << 20) {
+            *stalled = 1;
+            atomicAdd(&g_stalled_waits, 1ull);
+            return;
+        }
     }
-    *stalled = 1;
-    atomicAdd(&g_stalled_waits, 1ull);
 }
 
 __device__ __forceinline__ void fence_barrier_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
@@ -128,6 +130,23 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t address)
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(address));
+}
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t address)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(address));
+}
+__device__ __forceinline__ void tmem_wait_load16(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 // Ends the warp's loads so far; the registers pass through it, so that nothing
 // that uses them moves ahead of it.
