@@ -164,7 +164,7 @@ rng_status make(const char *what, const rng_attention_args *args, bool sizes_onl
     t.batch = a.batch, t.len_q = a.len_q, t.len_k = a.len_k, t.heads = a.heads_q, t.heads_kv = a.heads_kv;
     t.dim = a.head_dim, t.group = a.heads_kv ? a.heads_q / a.heads_kv : 1;
     t.causal = a.causal != 0, t.last = a.queries_last != 0;
-    t.table = a.bias_table, t.dtable = a.dbias_table;
+    t.table = a.bias_table, t.dtable = a.dbias_table, t.scale = a.scale;
     if (a.bias_table || a.dbias_table) {
         if (rng_status st = relative_buckets(what, a.num_buckets, a.max_distance, a.bidirectional != 0, &t.buckets))
             return st;
@@ -184,7 +184,7 @@ rng_status make(const char *what, const rng_attention_args *args, bool sizes_onl
         if (reinterpret_cast<uintptr_t>(x.p) % x.size)
             return fail(RNG_EINVAL, "%s: %s is not aligned to its %zu-byte element", what, x.name, x.size);
     auto strides = [](const int64_t *s) { return Strides{s[0], s[1], s[2]}; };
-    t.q = a.q, t.k = a.k, t.v = a.v, t.lse = a.lse, t.key_lengths = a.key_lengths, t.scale = a.scale;
+    t.q = a.q, t.k = a.k, t.v = a.v, t.lse = a.lse, t.key_lengths = a.key_lengths;
     t.qs = strides(a.q_stride), t.ks = strides(a.k_stride), t.vs = strides(a.v_stride), t.os = strides(a.o_stride);
     t.mask = make_mask(a.p, a.seed);
     t.first = a.first_counter;

@@ -80,12 +80,16 @@ __device__ __forceinline__ int32_t first_position(const Attention &a, int32_t ke
 // bucket's start.
 __host__ __device__ __forceinline__ int32_t bias_reach(const Buckets &b) { return b.max_distance + 160; }
 
+// Whether the forward kernels with a bias are needed: those without take the
+// maximum before the scores are scaled, and so want a scale above 0.
+inline bool has_bias(const Attention &a) { return a.table != nullptr || !(a.scale > 0.0f); }
+
 // Heads of one key head that lie side by side in a tile of 128 rows, so that
 // they read its keys once: all of them, where a tile is a whole number of
 // them and no head has a bias of its own.
 inline int32_t packed_heads(const Attention &a)
 {
-    return !a.table && a.group <= 64 && (a.group & (a.group - 1)) == 0 ? a.group : 1;
+    return !has_bias(a) && a.group <= 64 && (a.group & (a.group - 1)) == 0 ? a.group : 1;
 }
 
 }  // namespace rngk

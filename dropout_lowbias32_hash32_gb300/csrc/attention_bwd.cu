@@ -48,9 +48,6 @@ struct BwdParams {
     float *bias, *sums;
 };
 
-// How far step i of 16 is into a row-major tile of boxes, as a descriptor counts.
-__host__ __device__ constexpr uint32_t row_step(int i, uint32_t box) { return (i / 4 * box + i % 4 * 32) / 16; }
-
 // ---- dq ------------------------------------------------------------------------
 
 template <int kDim, bool kSplitKeys>
@@ -160,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
             for (int32_t n = 0; n < tiles; ++n) {
                 const int32_t j0 = n * kCols;
                 const uint32_t ks = n % S::kKeyStages, vs = n % S::kValueStages;
-                barrier_wait(k_empty + 8 * ks, (n / S::kKeyStages & 1u) ^ 1u, &stalled);
+                if (!barrier_wait(k_empty + 8 * ks, (n / S::kKeyStages & 1u) ^ 1u, &stalled)) break;
                 // keys past n(b) that the array holds: whatever they are, dS's zeros must meet zeros
                 const bool past = j0 + kCols > keys && keys < a.len_k;
                 const uint32_t on = past ? tail : k_full + 8 * ks, dst = base + S::kKeys + ks * S::kColsBytes;
@@ -169,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                     for (int c = 0; c < S::kBoxes; ++c) tma_load_5d(dst + c * kColsBox, &p.k_cols, on, c * 64, 0, j0, head_kv, b);
                 }
                 if (past) {
-                    barrier_wait(tail, 0, &stalled);
+                    if (!barrier_wait(tail, 0, &stalled)) barrier_drain(tail, 0);
                     uint8_t *rows = smem + S::kKeys + ks * S::kColsBytes;
                     for (int c = 0; c < S::kBoxes; ++c)
                         for (uint32_t o = max(0, keys - j0) * 128u + lane * 16u; o < kColsBox; o += 512u)
@@ -178,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                     __syncwarp();
                     if (one) barrier_arrive(k_full + 8 * ks);
                 }
-                barrier_wait(v_empty + 8 * vs, (n / S::kValueStages & 1u) ^ 1u, &stalled);
+                if (!barrier_wait(v_empty + 8 * vs, (n / S::kValueStages & 1u) ^ 1u, &stalled)) break;
                 if (one) {
                     barrier_expect(v_full + 8 * vs, S::kColsBytes);
                     for (int c = 0; c < S::kBoxes; ++c)
@@ -201,13 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                     const uint32_t ks = n % S::kKeyStages, vs = n % S::kValueStages;
                     const uint32_t q = base + (kSplitKeys ? 0 : slot) * S::kRowsBytes, k = base + S::kKeys + ks * S::kColsBytes,
                                    v = base + S::kValues + vs * S::kColsBytes;
-                    barrier_wait(k_full + 8 * ks, n / S::kKeyStages & 1u, &stalled);
+                    barrier_wait_one(k_full + 8 * ks, n / S::kKeyStages & 1u, &stalled);
                     tmem_fence_after();
                     const uint64_t qd = row_major_tile(q), kd = row_major_tile(k), dd = row_major_tile(q + S::kDo), vd = row_major_tile(v);
 #pragma unroll
                     for (int i = 0; i < kDim / 16; ++i)
                         mma_step(tmem + slot * 256, qd + row_step(i, kRowsBox), kd + row_step(i, kColsBox), kScores, i > 0);
-                    barrier_wait(v_full + 8 * vs, n / S::kValueStages & 1u, &stalled);
+                    barrier_wait_one(v_full + 8 * vs, n / S::kValueStages & 1u, &stalled);
                     tmem_fence_after();
 #pragma unroll
                     for (int i = 0; i < kDim / 16; ++i)
@@ -216,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                 };
                 auto product = [&](int slot, int32_t n, bool first) {
                     const uint32_t k = base + S::kKeys + n % S::kKeyStages * S::kColsBytes;
-                    barrier_wait(ready + 8 * slot, (slot ? given1++ : given0++) & 1u, &stalled);
+                    barrier_wait_one(ready + 8 * slot, (slot ? given1++ : given0++) & 1u, &stalled);
                     tmem_fence_after();
                     const uint64_t kd = column_major_tile(k, S::kBoxes > 1 ? kColsBox : 1024);
 #pragma unroll
@@ -226,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                 };
                 auto release_k = [&](int32_t n) { mma_commit(k_empty + 8 * (n % S::kKeyStages)); };
                 auto release_v = [&](int32_t n) { mma_commit(v_empty + 8 * (n % S::kValueStages)); };
-                barrier_wait(q_full, 0, &stalled);
+                barrier_wait_one(q_full, 0, &stalled);
                 if (kSplitKeys) {
 #pragma unroll 1
                     for (int32_t n = -2; n < tiles; ++n) {
@@ -298,37 +295,38 @@ __global__ void __launch_bounds__(kThreads, 1) query_kernel(const __grid_constan
                 tmem_load32(v[1], mine + kCols);
                 tmem_wait_load(v);
                 uint32_t(&s)[32] = v[0], (&dp)[32] = v[1];
-                // P
                 const int32_t low = j0 - (pos0 + warp_i + 31), high = j0 + kHalf - 1 - (pos0 + warp_i);
                 const bool far = high <= -last_start || low >= last_start;
-                if (!kBias) {
-                    const float to_base2 = a.scale * kLog2e;
-                    const float2 k2 = make_float2(to_base2, to_base2), l2 = make_float2(-lse, -lse);
+                if (kBias) {
+                    const float2 k2 = make_float2(a.scale, a.scale);
+                    if (far) {
+                        const float edge = table[high <= -last_start ? 0 : 2 * reach - 1];
 #pragma unroll
-                    for (int e = 0; e < kHalf; e += 2) {
-                        const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, l2);
-                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
-                    }
-                } else {
-                    const float2 k2 = make_float2(a.scale, a.scale), l2 = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
-                    const float edge = far ? table[high <= -last_start ? 0 : 2 * reach - 1] : 0.0f;
-                    const float *t = table + (j0 - pos + reach);
+                        for (int e = 0; e < kHalf; e += 2) {
+                            const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, make_float2(edge, edge));
+                            s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
+                        }
+                    } else {
+                        const float *t = table + (j0 - pos + reach);
 #pragma unroll
-                    for (int e = 0; e < kHalf; e += 2) {
-                        const float2 bias = far ? make_float2(edge, edge) : make_float2(t[e], t[e + 1]);
-                        float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, bias);
-                        f = mul2(add2(f, l2), b2);
-                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
+                        for (int e = 0; e < kHalf; e += 2) {
+                            const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, make_float2(t[e], t[e + 1]));
+                            s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
+                        }
                     }
                 }
-                // dS = P (dP / (1 - p) - delta), dP dropped as P was
-                if (kDrop) drop32(a.mask, counter + n * kCols, dp);
-#pragma unroll
-                for (int e = 0; e < kHalf; e += 2) {
-                    float2 d = fma2(make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1])), scale, minus);
-                    d = mul2(d, make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                // P = exp(S - lse); dS = P (dP / (1 - p) - delta), dP dropped as P was
+                const float2 to_base2 = kBias ? make_float2(kLog2e, kLog2e) : make_float2(a.scale * kLog2e, a.scale * kLog2e);
+                const float2 l2 = make_float2(-lse, -lse);
+                for_pairs32<kDrop>(a.mask, counter + n * kCols, [&](uint32_t e, float2 k) {
+                    float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    f = kBias ? mul2(add2(f, l2), to_base2) : fma2(f, to_base2, l2);
+                    const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                    float2 d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+                    if (kDrop) d = mul2(d, k);
+                    d = mul2(fma2(d, scale, minus), prob);
                     s[e] = __float_as_uint(d.x), s[e + 1] = __float_as_uint(d.y);
-                }
+                });
                 if (j0 + kHalf > warp_visible) {
                     const int32_t seen = visible - j0;
 #pragma unroll
@@ -518,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
                 for (int32_t n = 0; n < tiles; ++n) {
                     const uint32_t stage = n % S::kStages, bar = full + 8 * stage;
                     const int32_t head = head_kv * a.group + n / per_head, i0 = (begin + n % per_head) * kCols;
-                    barrier_wait(empty + 8 * stage, (n / S::kStages & 1u) ^ 1u, &stalled);
+                    barrier_wait_one(empty + 8 * stage, (n / S::kStages & 1u) ^ 1u, &stalled);
                     barrier_expect(bar, S::kStageBytes + kCols * sizeof(float2));
                     const uint32_t dst = base + S::kRing + stage * S::kStageBytes;
                     for (int c = 0; c < S::kBoxes; ++c) {
@@ -536,13 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
             // ---- MMA
             if (elect_one() && tiles) {
                 constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
-                barrier_wait(k_full, 0, &stalled);
+                barrier_wait_one(k_full, 0, &stalled);
 #pragma unroll 1
                 for (int32_t n = -2; n < tiles; ++n) {
                     const uint32_t slot = n & 1;
                     if (n >= 0) {  // dV += P^T dO, dK += dS^T Q
                         const uint32_t stage = n % S::kStages, q = base + S::kRing + stage * S::kStageBytes;
-                        barrier_wait(ready + 8 * slot, n / 2 & 1u, &stalled);
+                        barrier_wait_one(ready + 8 * slot, n / 2 & 1u, &stalled);
                         tmem_fence_after();
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -556,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
                     }
                     if (n + 2 < tiles) {  // S^T = K Q^T, dP^T = V dO^T
                         const uint32_t stage = (n + 2) % S::kStages, q = base + S::kRing + stage * S::kStageBytes;
-                        barrier_wait(full + 8 * stage, (n + 2) / S::kStages & 1u, &stalled);
+                        barrier_wait_one(full + 8 * stage, (n + 2) / S::kStages & 1u, &stalled);
                         tmem_fence_after();
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
@@ -598,47 +596,46 @@ __global__ void __launch_bounds__(kThreads, 1) key_kernel(const __grid_constant_
                 const int32_t rel = j - pos0 - i0;  // to the thread's first query
                 const int32_t low = warp_j - pos0 - i0 - (kHalf - 1), high = warp_j + 31 - pos0 - i0;
                 uint32_t c = a.first + ((static_cast<uint32_t>(b) * a.heads + head) * a.len_q + i0) * static_cast<uint32_t>(a.len_k) + j;
-                // P
-                if (!kBias) {
-#pragma unroll
-                    for (int e = 0; e < kHalf; e += 2) {
-                        const float4 st = stats[e / 2];  // two queries' lse, delta
-                        const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(to_base2, to_base2),
-                                              make_float2(kLift<T> - st.x, kLift<T> - st.z));
-                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
-                    }
-                } else {
+                if (kBias) {
                     const bool far = high <= -last_start || low >= last_start;
                     const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
-                    const float edge = far ? bias[high <= -last_start ? 0 : 2 * reach - 1] : 0.0f;
-                    bias += rel + reach;
+                    const float2 k2 = make_float2(a.scale, a.scale);
+                    if (far) {
+                        const float edge = bias[high <= -last_start ? 0 : 2 * reach - 1];
 #pragma unroll
-                    for (int e = 0; e < kHalf; e += 2) {
-                        const float4 st = stats[e / 2];
-                        const float2 by = far ? make_float2(edge, edge) : make_float2(bias[-e], bias[-e - 1]);
-                        float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(a.scale, a.scale), by);
-                        f = fma2(add2(f, make_float2(-st.x, -st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>));
-                        s[e] = __float_as_uint(exp2_approx(f.x)), s[e + 1] = __float_as_uint(exp2_approx(f.y));
+                        for (int e = 0; e < kHalf; e += 2) {
+                            const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, make_float2(edge, edge));
+                            s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
+                        }
+                    } else {
+                        bias += rel + reach;
+#pragma unroll
+                        for (int e = 0; e < kHalf; e += 2) {
+                            const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, make_float2(bias[-e], bias[-e - 1]));
+                            s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
+                        }
                     }
                 }
                 if (a.causal && high > 0) {  // query i0 + e sees key j from e = rel on
 #pragma unroll
                     for (int e = 0; e < kHalf; ++e)
-                        if (e < rel) s[e] = 0;
+                        if (e < rel) s[e] = __float_as_uint(-INFINITY);
                 }
-                // dropout(P) for dv, dS = P (dropout(dP) - delta) for dk
+                // P = exp(S - lse), dropped for dv; dS = P (dropout(dP) - delta) for dk
 #pragma unroll
                 for (int e = 0; e < kHalf; e += 2) {
-                    const float4 st = stats[e / 2];
-                    const float2 prob = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    const float4 st = stats[e / 2];  // two queries' lse, delta
+                    float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    f = kBias ? fma2(add2(f, make_float2(-st.x, -st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>))
+                              : fma2(f, make_float2(to_base2, to_base2), make_float2(kLift<T> - st.x, kLift<T> - st.z));
+                    const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                     float2 kept2 = prob, d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
                     if (kDrop) {
                         const float2 k = make_float2(kept(a.mask, c), kept(a.mask, c + static_cast<uint32_t>(a.len_k)));
                         c += 2 * static_cast<uint32_t>(a.len_k);
                         kept2 = mul2(kept2, k), d = mul2(d, k);
                     }
-                    d = fma2(d, make_float2(scale, scale), make_float2(-st.y * kUnlift, -st.w * kUnlift));
-                    d = mul2(d, prob);
+                    d = mul2(fma2(d, make_float2(scale, scale), make_float2(-st.y * kUnlift, -st.w * kUnlift)), prob);
                     s[e / 2] = pack2<T>(kept2.x, kept2.y);
                     dp[e / 2] = pack2<T>(d.x, d.y);
                 }

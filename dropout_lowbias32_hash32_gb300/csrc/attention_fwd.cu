@@ -1,39 +1,40 @@
 // attention_fwd.cu -- attention forward (include/rng.h, rng_attention_fwd) on
 // the tensor cores.
 //
-// A block works on two "slots" of 128 query rows by 128 keys.  For a slot's key
-// tile, S = Q K^T goes to TMEM; the slot's threads take the rows of S,
-// update the row's running maximum and sum, and write P = exp(S - max)
-// back over S in 16 bits; O += P V accumulates in TMEM with P as the TMEM
-// operand.  Two threads share a row, 64 keys each, so that four warps a
-// scheduler hide each other's latencies; they agree on the row's maximum only
-// when one of them has to raise it.  One thread issues all products, one warp
-// the TMA loads of the key and value tiles, and while a slot's threads work on
-// its scores the tensor core works for the other slot.
-//   kSplitKeys = false: the slots are two tiles of queries that share the key
+// A block works on two units, each of 128 query rows with an O in TMEM.  A unit
+// goes through tiles of 64 keys: S = Q K^T to TMEM, P = exp(S - max) written
+// back over S in 16 bits, O += P V with P as the TMEM operand.  Two warpgroups
+// take a unit's tiles in turn, a thread to a row, each with an S of its own: so
+// four chains of product, exponential, product are under way, the tensor core
+// works for three while the fourth computes, and four warps a scheduler hide each
+// other's latencies.  One thread a unit issues its products, one warp the TMA loads; a
+// stage of their ring holds a value tile and the key tile `kLead` after it.
+//   kSplitKeys = false: the units are two tiles of queries that share the key
 //     and value tiles (halving their traffic from L2);
-//   kSplitKeys = true: one tile of queries, the slots take every other key
+//   kSplitKeys = true: one tile of queries, the units take every other key
 //     tile and are joined at the end.  For few rows, where the key axis is also
 //     split over blocks, and joined by join_kernel.
 // The query heads of one key head are `pack` adjacent rows of a tile, so that
-// they read its keys once.
+// they read its keys once.  A block that has finished takes over the work of one
+// that has not started, so that its loads and first products run under the last
+// of its previous work.
 //
-// O is rescaled only when a row's maximum has grown by more than 2^8 since its
-// last rescaling: P then stays below 2^8, which 16 bits hold as well as 1.
+// A row's maximum passes from tile to tile through shared memory.  It is raised,
+// and O rescaled, only when it has grown by more than 2^8: P then stays below
+// 2^8, which 16 bits hold as well as 1.
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 
 namespace rngk {
 namespace {
 
-constexpr int kTile = 128;          // rows of a slot, keys of a tile
-constexpr int kHalf = kTile / 2;    // keys of a thread
-// 2 x 256 for the slots, then a TMA warp, an MMA warp, two that only fill the warpgroup
+constexpr int kRows = 128, kKeys = 64;  // a unit's tile
+// 2 x 2 warpgroups for the units, then a TMA warp, an MMA warp a unit, one that asks for work
 constexpr int kThreads = 640;
-constexpr uint32_t kTmaWarp = 16, kMmaWarp = 17;
+constexpr uint32_t kTmaWarp = 16, kMmaWarp = 17, kAskWarp = 19;
 // registers: 640 threads start with 96 each; 4 x 104 + 64 = 5 x 96
-constexpr int kSlotRegisters = 104, kOtherRegisters = 64;
-constexpr uint32_t kBox = 16384;    // bytes of 128 rows of 64 elements
+constexpr int kUnitRegisters = 104, kOtherRegisters = 64;
+constexpr uint32_t kRowsBox = 16384, kKeysBox = 8192;  // bytes of 128 and of 64 rows of 64 elements
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct FwdParams {
@@ -47,45 +48,47 @@ template <int kDim, bool kSplitKeys>
 struct Shape {
     static constexpr int kBoxes = kDim / 64;
     static constexpr int kQTiles = kSplitKeys ? 1 : 2;
-    static constexpr int kStages = kDim == 64 ? 8 : kSplitKeys ? 5 : 4;
-    static constexpr uint32_t kStageBytes = kBoxes * kBox;
-    static constexpr uint32_t kRing = kQTiles * kStageBytes;  // where the ring begins
-    static constexpr uint32_t kTable = kRing + kStages * kStageBytes;
+    static constexpr int kLead = kSplitKeys ? 4 : 2;  // tiles whose S there is room for
+    static constexpr int kStages = kDim == 64 ? 8 : 4;
+    static constexpr uint32_t kRowsBytes = kBoxes * kRowsBox, kTileBytes = kBoxes * kKeysBox, kStageBytes = 2 * kTileBytes;
+    static constexpr uint32_t kRing = kQTiles * kRowsBytes;                               // where the ring begins
+    static constexpr uint32_t kHand = kRing + kStages * kStageBytes;                      // unit 1's O for unit 0, 64 columns at a time
+    static constexpr uint32_t kTable = kHand + (kSplitKeys ? 64 * kRows * 4 : 0);  // a bias table a unit
 };
 
-// Barriers of a slot's 256 threads; slot_any also tells whether any of them
-// asked.
-__device__ __forceinline__ void slot_sync(int slot) { asm volatile("bar.sync %0, 256;" ::"r"(2 + slot) : "memory"); }
-__device__ __forceinline__ bool slot_any(int slot, bool ask)
+// Barriers of the block's units, or of one; all_of also tells whether every one
+// of their threads agrees.
+template <bool kBoth>
+__device__ __forceinline__ void sync_units(int unit)
+{
+    if (kBoth) asm volatile("bar.sync 1, 512;" ::: "memory");
+    else asm volatile("bar.sync %0, 256;" ::"r"(2 + unit) : "memory");
+}
+template <bool kBoth>
+__device__ __forceinline__ bool all_of(int unit, bool agree)
 {
     uint32_t yes;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
         : "=r"(yes)
-        : "r"(static_cast<uint32_t>(ask)), "r"(2 + slot)
+        : "r"(static_cast<uint32_t>(agree)), "r"(kBoth ? 1 : 2 + unit), "n"(kBoth ? 512 : 256)
         : "memory");
     return yes != 0;
 }
 
-template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid_constant__ FwdParams p)
-{
-    using S = Shape<kDim, kSplitKeys>;
-    extern __shared__ uint8_t dynamic[];
-    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 8];
-    __shared__ uint32_t tmem_base;
-    __shared__ volatile uint32_t stalled;
-    __shared__ float tops[2][2][2][kTile], sums[2][2][kTile];  // [turn's parity][slot][half][row], [slot][half][row]
-    const Attention &a = p.a;
-    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
-    uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
-    const uint32_t base = smem_address(smem);
-    float *table = reinterpret_cast<float *>(smem + S::kTable);
+// One item of work: a pack of heads of a batch entry, its query tiles, a range
+// of key tiles.
+struct Item {
+    int32_t b, pack, head0, head_kv, i0, keys, pos0, split, tile0, count[2], tiles;
+};
 
-    // ---- the block's work
-    uint32_t x = blockIdx.x;
-    const int32_t split = x % p.splits;
+template <bool kSplitKeys>
+__device__ __forceinline__ Item item_at(const FwdParams &p, uint32_t x)
+{
+    const Attention &a = p.a;
+    Item w;
+    w.split = x % p.splits;
     x /= p.splits;
     int32_t unit, q_tile;
     if (a.causal) {  // the longest first
@@ -93,346 +96,417 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     } else {
         q_tile = x % p.q_tiles, unit = x / p.q_tiles;
     }
-    const int32_t packs = a.heads / p.pack, b = unit / packs, pack = unit % packs;
-    const int32_t head0 = pack * p.pack, head_kv = head0 / a.group;
-    const int32_t rows_per = kTile / p.pack;  // positions of a tile
-    const int32_t i0 = q_tile * S::kQTiles * rows_per;
-    const int32_t keys = keys_of(a, b), pos0 = first_position(a, keys);
-    // key tiles of each slot (both slots' are the block's when the keys are split)
-    int32_t tile0 = split * p.split_tiles, count[2];
-    for (int s = 0; s < 2; ++s) {
-        const int32_t last = min(i0 + (kSplitKeys ? 1 : s + 1) * rows_per, a.len_q) - 1;  // the slot's last query
-        int32_t end = a.causal ? min(keys, pos0 + last + 1) : keys;
-        if (!kSplitKeys && i0 + s * rows_per >= a.len_q) end = 0;
-        end = max(0, min((end + kTile - 1) / kTile - tile0, p.split_tiles));
-        count[s] = end;
+    const int32_t packs = a.heads / p.pack, rows_per = kRows / p.pack;  // positions of a tile
+    w.b = unit / packs, w.pack = unit % packs;
+    w.head0 = w.pack * p.pack, w.head_kv = w.head0 / a.group;
+    w.i0 = q_tile * (kSplitKeys ? 1 : 2) * rows_per;
+    w.keys = keys_of(a, w.b), w.pos0 = first_position(a, w.keys);
+    w.tile0 = w.split * p.split_tiles;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {  // key tiles of each unit (the item's, when the units share them out)
+        const int32_t last = min(w.i0 + (kSplitKeys ? 1 : s + 1) * rows_per, a.len_q) - 1;  // the unit's last query
+        int32_t end = a.causal ? min(w.keys, w.pos0 + last + 1) : w.keys;
+        if (!kSplitKeys && w.i0 + s * rows_per >= a.len_q) end = 0;
+        w.count[s] = max(0, min((end + kKeys - 1) / kKeys - w.tile0, p.split_tiles));
     }
-    const int32_t tiles = max(count[0], count[1]);
+    w.tiles = max(w.count[0], w.count[1]);
+    return w;
+}
 
-    // ---- barriers, TMEM
-    const uint32_t bar0 = smem_address(bars);
-    const uint32_t full = bar0, empty = bar0 + 8 * S::kStages, scored = empty + 8 * S::kStages, ready = scored + 16,
-                   done = ready + 16, q_full = done + 8, tail = q_full + 8;
+template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid_constant__ FwdParams p)
+{
+    using S = Shape<kDim, kSplitKeys>;
+    extern __shared__ uint8_t dynamic[];
+    __shared__ alignas(16) uint4 response;
+    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 37];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile uint32_t stalled;
+    __shared__ float tops[2][2][kRows];                          // [unit][warpgroup][row], of its last tile
+    __shared__ float last_tops[2][2][2][kRows], sums[2][2][2][kRows];  // [item's parity][unit][warpgroup][row]
+    const Attention &a = p.a;
+    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+    uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
+    const uint32_t base = smem_address(smem);
+
+    // scored, ready: [unit][warpgroup]; passed: [unit][warpgroup][quarter]
+    const uint32_t full = smem_address(bars), empty = full + 8 * S::kStages, scored = empty + 8 * S::kStages,
+                   ready = scored + 32, passed = ready + 32, added = passed + 128, done = added + 16, q_full = done + 16, q_empty = q_full + 8,
+                   tail = q_empty + 8, answered = tail + 8, heard = answered + 8, drained = heard + 8;
     if (threadIdx.x == 0) {
+        prefetch_map(&p.q), prefetch_map(&p.k), prefetch_map(&p.v);
         stalled = 0;
-        for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 8);
-        barrier_init(done, 1), barrier_init(q_full, 1), barrier_init(tail, 1);
+        for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 2);
+        for (int s = 0; s < 4; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4);
+        for (int s = 0; s < 16; ++s) barrier_init(passed + 8 * s, 1);
+        for (int s = 0; s < 2; ++s) barrier_init(added + 8 * s, 1), barrier_init(done + 8 * s, 1);
+        barrier_init(q_full, 1), barrier_init(q_empty, 2), barrier_init(tail, 1);
+        barrier_init(answered, 1), barrier_init(heard, 19);
+        for (int s = 0; s < 2; ++s) barrier_init(drained + 8 * s, 1);
         fence_barrier_init();
     }
     if (warp == kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
-    if (kBias) {  // the bias by relative position, head head0 (pack is 1)
-        const int32_t reach = bias_reach(a.buckets);
-        for (int32_t t = threadIdx.x; t < 2 * reach; t += kThreads)
-            table[t] = to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, t - reach) * a.heads + head0]);
-    }
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
-    if (warp >= kTmaWarp) {
-      give_registers<kOtherRegisters>();
-      if (warp == kTmaWarp) {
-        // ---- TMA: the queries, then K_0 .. K_{lead-1} and alternately V_n, K_{n+lead}
-        constexpr int kLead = kSplitKeys ? 2 : 1;
-        const bool one = elect_one();
-        if (one && tiles) {
-            prefetch_map(&p.k), prefetch_map(&p.v);
-            barrier_expect(q_full, S::kQTiles * S::kStageBytes);
-            for (int t = 0; t < S::kQTiles; ++t)
-                for (int c = 0; c < S::kBoxes; ++c)
-                    tma_load_5d(base + t * S::kStageBytes + c * kBox, &p.q, q_full, c * 64, 0, i0 + t * rows_per, pack, b);
-        }
-        uint32_t use = 0;
-        auto load = [&](const CUtensorMap *map, int32_t n, bool values) {
-            const uint32_t stage = use % S::kStages, dst = base + S::kRing + stage * S::kStageBytes;
-            const uint32_t bar = full + 8 * stage;
-            barrier_wait(empty + 8 * stage, (use / S::kStages & 1u) ^ 1u, &stalled);
-            const int32_t j0 = (tile0 + n) * kTile;
-            // keys past n(b) that the array holds: whatever they are, P's zeros must meet zeros
-            const bool past = values && j0 + kTile > keys && keys < a.len_k;
-            const uint32_t on = past ? tail : bar;
-            if (one) {
-                barrier_expect(on, S::kStageBytes);
-                for (int c = 0; c < S::kBoxes; ++c) tma_load_5d(dst + c * kBox, map, on, c * 64, 0, j0, head_kv, b);
-            }
-            if (past) {
-                barrier_wait(tail, 0, &stalled);
-                uint8_t *rows = smem + S::kRing + stage * S::kStageBytes;
-                for (int c = 0; c < S::kBoxes; ++c)
-                    for (uint32_t o = max(0, keys - j0) * 128u + lane * 16u; o < kBox; o += 512u)
-                        *reinterpret_cast<uint4 *>(rows + c * kBox + o) = make_uint4(0, 0, 0, 0);
-                fence_async_shared();
-                __syncwarp();
-                if (one) barrier_arrive(bar);
-            }
-            ++use;
-        };
-        for (int32_t n = 0; n < kLead && n < tiles; ++n) load(&p.k, n, false);
-        for (int32_t n = 0; n < tiles; ++n) {
-            load(&p.v, n, true);
-            if (n + kLead < tiles) load(&p.k, n + kLead, false);
-        }
-        if (stalled && one)  // nothing may land after the block has ended
-            for (uint32_t u = use > S::kStages ? use - S::kStages : 0; u < use; ++u)
-                for (uint32_t tries = 0; tries < 100000 && !barrier_try(full + 8 * (u % S::kStages), u / S::kStages & 1u); ++tries) {}
-      } else if (warp == kMmaWarp) {
-        // ---- MMA
-        if (elect_one() && tiles) {
-            constexpr uint32_t kScores = mma_shape<T>(kTile, false), kOut = mma_shape<T>(kDim, true);
-            uint32_t use = 0, given0 = 0, given1 = 0;
-            auto acquire = [&] {
-                const uint32_t stage = use % S::kStages;
-                barrier_wait(full + 8 * stage, use / S::kStages & 1u, &stalled);
-                tmem_fence_after();
-                return stage;
-            };
-            auto release = [&] {
-                mma_commit(empty + 8 * (use % S::kStages));
-                ++use;
-            };
-            auto scores = [&](int slot, uint32_t stage) {
-                const uint32_t q = base + (kSplitKeys ? 0 : slot) * S::kStageBytes, k = base + S::kRing + stage * S::kStageBytes;
-                const uint64_t qd = row_major_tile(q), kd = row_major_tile(k);
-#pragma unroll
-                for (int i = 0; i < kDim / 16; ++i) {
-                    constexpr uint32_t kStep = 16;  // descriptors count 16 bytes
-                    const uint32_t o = (i / 4 * kBox + i % 4 * 32) / kStep;
-                    mma_step(tmem + slot * 256, qd + o, kd + o, kScores, i > 0);
-                }
-                mma_commit(scored + 8 * slot);
-            };
-            auto products = [&](int slot, uint32_t stage, bool first) {
-                const uint32_t v = base + S::kRing + stage * S::kStageBytes;
-                barrier_wait(ready + 8 * slot, (slot ? given1++ : given0++) & 1u, &stalled);
-                tmem_fence_after();
-                const uint64_t vd = column_major_tile(v, S::kBoxes > 1 ? kBox : 1024);
-#pragma unroll
-                for (int i = 0; i < kTile / 16; ++i)
-                    mma_step_tmem(tmem + slot * 256 + kTile, tmem + slot * 256 + i / 4 * kHalf + i % 4 * 8, vd + i * (2048 / 16), kOut,
-                                  !first || i > 0);
-            };
-            barrier_wait(q_full, 0, &stalled);
-            if (kSplitKeys) {
-#pragma unroll 1
-                for (int32_t n = -2; n < tiles; ++n) {
-                    if (n >= 0) products(n & 1, acquire(), n < 2), release();
-                    if (n + 2 < tiles) scores(n & 1, acquire()), release();
-                }
-            } else {
-                // the stages of V_n and K_{n+1}, each released when both slots have used it
-#pragma unroll 1
-                for (int32_t n = -1; n < tiles; ++n) {
-                    const uint32_t vs = n >= 0 ? acquire() : 0;
-                    uint32_t ks = S::kStages;
-#pragma unroll 1
-                    for (int s = 0; s < 2; ++s) {
-                        if (n >= 0 && n < count[s]) products(s, vs, n == 0);
-                        if (n + 1 < count[s]) {
-                            if (ks == S::kStages) {
-                                if (n >= 0) ++use;
-                                ks = acquire();
-                                if (n >= 0) --use;
-                            }
-                            scores(s, ks);
-                        }
-                    }
-                    if (n >= 0) release();
-                    if (n + 1 < tiles) release();
-                }
-            }
-            mma_commit(done);
-        }
-      }
-    } else {
-        take_registers<kSlotRegisters>();
-        // ---- the slots' rows
-        const int slot = warp / 8, half = warp / 4 % 2;
-        const int32_t r = (warp % 4) * 32 + lane;
-        const uint32_t lanes = (warp % 4) * 32u << 16;
-        const uint32_t mine = tmem + slot * 256 + lanes + half * kHalf;              // the thread's scores, then its P
-        const uint32_t out = tmem + slot * 256 + lanes + kTile + half * (kDim / 2);  // its half of O's columns
-        const int32_t row0 = (kSplitKeys ? 0 : slot * kTile);
-        const int32_t warp_i = i0 + (row0 + (warp % 4) * 32) / p.pack;  // the warp's first query
-        const int32_t i = i0 + (row0 + r) / p.pack, head = head0 + r % p.pack, pos = pos0 + i;
-        const bool valid = i < a.len_q, any = warp_i < a.len_q;
-        const int64_t index = (static_cast<int64_t>(b) * a.heads + head) * a.len_q + i;
-        const uint32_t counter = a.first + static_cast<uint32_t>(index) * static_cast<uint32_t>(a.len_k) + half * kHalf;
-        const int32_t visible = a.causal ? min(keys, pos + 1) : keys;
-        const int32_t warp_visible = a.causal ? min(keys, pos0 + warp_i + 1) : keys;  // the least of the warp's
-        const bool plain = !kBias && a.scale > 0.0f;
-        // scores are held before (plain) or after their scaling and bias; base two is for the exponential
-        const float to_base2 = plain ? a.scale * kLog2e : kLog2e, to_natural = plain ? a.scale : 1.0f;
-        const int32_t reach = kBias ? bias_reach(a.buckets) : 0;
-        const float bias_low = kBias ? table[0] : 0.0f, bias_high = kBias ? table[2 * reach - 1] : 0.0f;
-        float top = -INFINITY, sum = 0.0f;
-        uint32_t turn = 0;
-        for (int32_t n = kSplitKeys ? slot : 0; n < count[kSplitKeys ? 0 : slot]; n += kSplitKeys ? 2 : 1, ++turn) {
-            const int32_t j0 = (tile0 + n) * kTile + half * kHalf;
-            barrier_wait(scored + 8 * slot, turn & 1u, &stalled);
-            tmem_fence_after();
-            uint32_t s[2][32];
-            float tile_top = -INFINITY;
-            if (any) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) tmem_load32(s[c], mine + 32 * c);
-                tmem_wait_load(s);
-                if (kBias) {
-                    // relative positions of the warp's pairs: beyond the last bucket's start on one side, or by the table
-                    const int32_t low = j0 - (pos0 + warp_i + 31), high = j0 + kHalf - 1 - (pos0 + warp_i);
-                    const float2 scale = make_float2(a.scale, a.scale);
-                    if (high <= -a.buckets.max_distance || low >= a.buckets.max_distance) {
-                        const float v = high < 0 ? bias_low : bias_high;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale, make_float2(v, v));
-                                s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
-                            }
-                    } else {
-                        const float *t = table + (j0 - pos + reach);
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale,
-                                                      make_float2(t[32 * c + e], t[32 * c + e + 1]));
-                                s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
-                            }
-                    }
-                } else if (!plain) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) * a.scale);
-                }
-                if (j0 + kHalf > warp_visible) {
-                    const int32_t seen = visible - j0;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e >= seen) s[c][e] = __float_as_uint(-INFINITY);
-                }
-                float most[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t(&q)[16] = *reinterpret_cast<const uint32_t(*)[16]>(&s[c / 2][c % 2 * 16]);
-                    most[c] = __uint_as_float(q[0]);
-#pragma unroll
-                    for (int e = 1; e < 15; e += 2) most[c] = max3(most[c], __uint_as_float(q[e]), __uint_as_float(q[e + 1]));
-                    most[c] = fmaxf(most[c], __uint_as_float(q[15]));
-                }
-                tile_top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-            }
-            // A new maximum, and O and the sums brought to it: at the first finite score, or 2^8 above the old one.
-            // Where one of the slot's threads needs it, its rows' halves meet.
-            const bool want = tile_top > top && (top == -INFINITY || (tile_top - top) * to_base2 > 8.0f);
-            if (slot_any(slot, want)) {
-                float(&meet)[2][kTile] = tops[turn & 1u][slot];
-                meet[half][r] = tile_top;
-                slot_sync(slot);
-                const float most = fmaxf(meet[0][r], meet[1][r]);
-                const bool raise = most > top && (top == -INFINITY || (most - top) * to_base2 > 8.0f);
-                if (any && __any_sync(0xFFFFFFFFu, raise)) {
-                    const float next = raise ? most : top;
-                    const float fade = raise ? exp2_approx((top - next) * to_base2) : 1.0f;
-                    sum *= fade;
-                    top = next;
-                    if (turn) {
-#pragma unroll 1
-                        for (int c = 0; c < kDim / 32; ++c) {
-                            uint32_t o[16];
-                            tmem_load16(o, out + 16 * c);
-                            tmem_wait_load16(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-                            tmem_store16(out + 16 * c, o);
-                        }
-                    }
-                }
-            }
-            if (any) {
-                // exp2((s - top) to_base2): as one multiply-add, or, where a bias may be the type's
-                // lowest value, with the difference taken first
-                const float from = top == -INFINITY ? 0.0f : -top, shift = from * to_base2;
-                const float2 from2 = make_float2(from, from), shift2 = make_float2(shift, shift);
-                const float2 base2 = make_float2(to_base2, to_base2);
-                float2 total = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 v = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                        const float2 f = plain ? fma2(v, base2, shift2) : mul2(add2(v, from2), base2);
-                        const float2 q = make_float2(exp2_approx(f.x), exp2_approx(f.y));
-                        total = add2(total, q);
-                        s[c][e] = __float_as_uint(q.x), s[c][e + 1] = __float_as_uint(q.y);
-                    }
-                    if (kDrop) drop32(a.mask, counter + (tile0 + n) * kTile + 32 * c, s[c]);
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2)
-                        w[e / 2] = pack2<T>(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                    tmem_store16(mine + 16 * c, w);
-                }
-                sum += total.x + total.y;
-                tmem_wait_store();
-            }
-            tmem_fence_before();
-            __syncwarp();
-            if (lane == 0) barrier_arrive(ready + 8 * slot);
-        }
 
-        // ---- the result
-        if (tiles) {
-            barrier_wait(done, 0, &stalled);
-            tmem_fence_after();
-        }
-        sums[slot][half][r] = sum;
-        if (kSplitKeys && half == 0) tops[0][slot][0][r] = top;
-        float *hand = reinterpret_cast<float *>(smem + S::kRing);  // the ring, which nothing reads any more
-        const bool two = kSplitKeys && tiles > 1;
-        if (two && slot == 1 && any) {  // slot 1 hands its part to slot 0
-#pragma unroll
-            for (int c = 0; c < kDim / 64; ++c) {
-                uint32_t o[1][32];
-                tmem_load32(o[0], out + 32 * c);
-                tmem_wait_load(o);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) hand[(half * (kDim / 2) + 32 * c + e) * kTile + r] = __uint_as_float(o[0][e]);
+    // Every role goes through the block's items: its own first, then those of blocks that need not start any more.
+    // The asking warp asks for the next one when all have heard the last answer.
+    uint32_t items = 0;
+    auto next_item = [&]() -> int32_t {
+        if (!barrier_wait(answered, items++ & 1u, &stalled)) return -1;
+        const int32_t next = taken_work(smem_address(&response));
+        fence_async_shared();
+        __syncwarp();
+        if (elect_one()) barrier_arrive(heard);
+        return next;
+    };
+
+    if (warp >= kTmaWarp) {
+        give_registers<kOtherRegisters>();
+        if (warp == kAskWarp) {
+            if (elect_one()) {
+                int32_t next = 0;
+                while (next >= 0 && (!items || barrier_wait_one(heard, (items - 1) & 1u, &stalled))) {
+                    ask_for_work(smem_address(&response), answered);
+                    if (!barrier_wait_one(answered, items++ & 1u, &stalled)) {
+                        barrier_drain(answered, (items - 1) & 1u);
+                        break;
+                    }
+                    next = taken_work(smem_address(&response));
+                }
             }
+        } else if (warp == kTmaWarp) {
+            // ---- TMA: the queries, then K_0 .. K_{lead-1} and alternately V_n, K_{n+lead}
+            const bool one = elect_one();
+            uint32_t use = 0, loaded = 0, tails = 0;
+            bool fine = true;
+            for (int32_t x = blockIdx.x; x >= 0 && fine; x = fine ? next_item() : -1) {
+                const Item w = item_at<kSplitKeys>(p, x);
+                if (w.tiles) {
+                    if (loaded) fine = barrier_wait(q_empty, (loaded - 1) & 1u, &stalled);
+                    if (!fine) break;
+                    ++loaded;
+                    if (one) {
+                        barrier_expect(q_full, S::kQTiles * S::kRowsBytes);
+                        for (int t = 0; t < S::kQTiles; ++t)
+                            for (int c = 0; c < S::kBoxes; ++c)
+                                tma_load_5d(base + t * S::kRowsBytes + c * kRowsBox, &p.q, q_full, c * 64, 0,
+                                            w.i0 + t * (kRows / p.pack), w.pack, w.b);
+                    }
+                }
+#pragma unroll 1
+                for (int32_t n = -S::kLead; n < w.tiles; ++n) {
+                    const bool has_v = n >= 0, has_k = n + S::kLead < w.tiles;
+                    if (!has_v && !has_k) continue;
+                    const uint32_t stage = use % S::kStages, dst = base + S::kRing + stage * S::kStageBytes, bar = full + 8 * stage;
+                    fine = barrier_wait(empty + 8 * stage, (use / S::kStages & 1u) ^ 1u, &stalled);
+                    if (!fine) break;
+                    ++use;
+                    // values past n(b) that the array holds: whatever they are, P's zeros must meet zeros (the last
+                    // tile's, which has no keys beside it)
+                    const bool past = has_v && (w.tile0 + n + 1) * kKeys > w.keys && w.keys < a.len_k;
+                    const uint32_t on = past ? tail : bar;
+                    if (one) {
+                        barrier_expect(on, (has_v && has_k ? 2 : 1) * S::kTileBytes);
+#pragma unroll
+                        for (int c = 0; c < S::kBoxes; ++c) {
+                            if (has_v) tma_load_5d(dst + c * kKeysBox, &p.v, on, c * 64, 0, (w.tile0 + n) * kKeys, w.head_kv, w.b);
+                            if (has_k)
+                                tma_load_5d(dst + S::kTileBytes + c * kKeysBox, &p.k, on, c * 64, 0, (w.tile0 + n + S::kLead) * kKeys, w.head_kv, w.b);
+                        }
+                    }
+                    if (past) {
+                        if (!barrier_wait(tail, tails++ & 1u, &stalled)) barrier_drain(tail, (tails - 1) & 1u);
+                        uint8_t *rows = smem + S::kRing + stage * S::kStageBytes;
+                        for (int c = 0; c < S::kBoxes; ++c)
+#pragma unroll 1
+                            for (uint32_t o = (w.keys - (w.tile0 + n) * kKeys) * 128u + lane * 16u; o < kKeysBox; o += 512u)
+                                *reinterpret_cast<uint4 *>(rows + c * kKeysBox + o) = make_uint4(0, 0, 0, 0);
+                        fence_async_shared();
+                        __syncwarp();
+                        if (one) barrier_arrive(bar);
+                    }
+                }
+            }
+            if (stalled) {  // nothing may land after the block has ended
+                if (loaded) barrier_drain(q_full, (loaded - 1) & 1u);
+                for (uint32_t u = use > S::kStages ? use - S::kStages : 0; u < use; ++u) barrier_drain(full + 8 * (u % S::kStages), u / S::kStages & 1u);
+            }
+        } else {
+            // ---- MMA, a warp to a unit.  Both go through every stage, whether or not it holds something for their unit,
+            // so that neither falls a whole phase behind.
+            constexpr uint32_t kScores = mma_shape<T>(kKeys, false), kOut = mma_shape<T>(kDim, true);
+            const uint32_t unit = warp - kMmaWarp, at = tmem + unit * 256;
+            const uint64_t qd = row_major_tile(base + (kSplitKeys ? 0 : unit) * S::kRowsBytes);
+            const uint64_t ring_v = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kKeysBox : 1024);
+            const uint64_t ring_k = row_major_tile(base + S::kRing + S::kTileBytes);
+            const bool one = elect_one();
+            uint32_t use = 0, given = 0, loaded = 0;  // given: bit g, the parity of warpgroup g's next P
+            bool fine = true;
+            for (int32_t x = blockIdx.x; x >= 0; x = fine ? next_item() : -1) {
+                const Item w = item_at<kSplitKeys>(p, x);
+                if (!w.tiles) continue;
+                const int32_t count = kSplitKeys ? w.tiles : unit ? w.count[1] : w.count[0];
+                const uint32_t lead = min(w.tiles, S::kLead);
+                fine = barrier_wait(q_full, loaded++ & 1u, &stalled);
+                tmem_fence_after();
+                bool scored_any = false;
+#pragma unroll 1
+                for (int32_t n = -S::kLead; n < w.tiles && fine; ++n) {
+                    const int32_t next = n + S::kLead;
+                    if (n < 0 && next >= w.tiles) continue;
+                    const uint32_t u = use + (next < static_cast<int32_t>(lead) ? next : n + lead), stage = u % S::kStages;
+                    const uint32_t group = (kSplitKeys ? next >> 1 : n) & 1u;  // tile n's and tile n + lead's
+                    const bool mine = !kSplitKeys || (n & 1) == static_cast<int32_t>(unit), v_mine = mine && n >= 0 && n < count,
+                               k_mine = mine && next < count;
+                    fine = barrier_wait(full + 8 * stage, u / S::kStages & 1u, &stalled);
+                    if (v_mine) {  // O += P V
+                        fine = fine && barrier_wait(ready + 8 * (2 * unit + group), given >> group & 1u, &stalled);
+                        given ^= 1u << group;
+                    }
+                    if (!fine) break;
+                    tmem_fence_after();
+                    if (one) {
+                        if (v_mine) {
+                            const uint64_t vd = ring_v + stage * (S::kStageBytes / 16);
+#pragma unroll
+                            for (int i = 0; i < kKeys / 16; ++i)
+                                mma_step_tmem(at + 2 * kKeys, at + group * kKeys + i * 8, vd + i * (2048 / 16), kOut,
+                                              n >= (kSplitKeys ? 2 : 1) || i > 0);
+                            if (next >= count) mma_commit(added + 8 * unit);
+                            if (n + (kSplitKeys ? 2 : 1) >= count) mma_commit(done + 8 * unit);
+                        }
+                        if (k_mine) {  // S = Q K^T
+                            const uint64_t kd = ring_k + stage * (S::kStageBytes / 16);
+#pragma unroll
+                            for (int i = 0; i < kDim / 16; ++i)
+                                mma_step(at + group * kKeys, qd + row_step(i, kRowsBox), kd + row_step(i, kKeysBox), kScores, i > 0);
+                            mma_commit(scored + 8 * (2 * unit + group));
+                        }
+                        if (v_mine || k_mine) mma_commit(empty + 8 * stage);
+                        else barrier_arrive(empty + 8 * stage);
+                        if (k_mine && next + (kSplitKeys ? 2 : 1) >= count) mma_commit(q_empty);
+                    }
+                    scored_any = scored_any || k_mine;
+                }
+                if (!scored_any && one) barrier_arrive(q_empty);
+                use += w.tiles + lead;
+            }
+            if (stalled && one) mma_commit(drained + 8 * unit), barrier_drain(drained + 8 * unit, 0);
         }
-        asm volatile("bar.sync 1, 512;" ::: "memory");
-        if (any && (!kSplitKeys || slot == 0)) {
+    } else {
+        take_registers<kUnitRegisters>();
+        // ---- the units' rows
+        const int unit = warp / 8, group = warp / 4 % 2;
+        const int32_t r = (warp % 4) * 32 + lane;
+        const uint32_t lanes = (warp % 4) * 32u << 16, chain = 2 * unit + group;
+        const uint32_t mine = tmem + unit * 256 + lanes + group * kKeys;              // the thread's scores, then its P
+        const uint32_t out = tmem + unit * 256 + lanes + 2 * kKeys;
+        const uint32_t pass = passed + 8 * (4 * chain + warp % 4), take = passed + 8 * (4 * (chain ^ 1) + warp % 4);
+        const int32_t row0 = (kSplitKeys ? 0 : unit * kRows);
+                // scores are held before or, with a bias, after their scaling; base two is for the exponential
+        const float to_base2 = kBias ? kLog2e : a.scale * kLog2e;
+        const int32_t reach = kBias ? bias_reach(a.buckets) : 0;
+        float *table = reinterpret_cast<float *>(smem + S::kTable) + unit * 2 * reach;
+        int32_t table_head = -1;
+        uint32_t turn = 0, turns_of_other = 0, taken = 0, additions = 0, finished = 0, item = 0;
+        for (int32_t x = blockIdx.x;; ++item) {
+            const Item w = item_at<kSplitKeys>(p, x);
+            const int32_t warp_i = w.i0 + (row0 + (warp % 4) * 32) / p.pack;  // the warp's first query
+            const int32_t i = w.i0 + (row0 + r) / p.pack, head = w.head0 + r % p.pack, pos = w.pos0 + i;
+            const bool valid = i < a.len_q, any = warp_i < a.len_q;
+            const int64_t index = (static_cast<int64_t>(w.b) * a.heads + head) * a.len_q + i;
+            const uint32_t counter = a.first + static_cast<uint32_t>(index) * static_cast<uint32_t>(a.len_k);
+            const int32_t visible = a.causal ? min(w.keys, pos + 1) : w.keys;
+            const int32_t warp_visible = a.causal ? min(w.keys, w.pos0 + warp_i + 1) : w.keys;  // the least of the warp's
+            if (kBias && w.head0 != table_head) {  // the bias by relative position (pack is 1)
+                table_head = w.head0;
+                sync_units<false>(unit);
+                for (int32_t t = threadIdx.x % 256u; t < 2 * reach; t += 256)
+                    table[t] = a.table ? to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, t - reach) * a.heads + w.head0]) : 0.0f;
+                sync_units<false>(unit);
+            }
+            float top = -INFINITY, sum = 0.0f;
+            // the unit's tiles; this warpgroup's are group, group + 2, ...
+            const int32_t count = kSplitKeys ? (w.tiles + 1 - unit) / 2 : unit ? w.count[1] : w.count[0];
+#pragma unroll 1
+            for (int32_t j = group; j < count; j += 2, ++turn) {
+                const int32_t j0 = (w.tile0 + (kSplitKeys ? 2 * j + unit : j)) * kKeys;
+                barrier_wait(scored + 8 * chain, turn & 1u, &stalled);
+                tmem_fence_after();
+                if (any) {
+                    uint32_t s[2][32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tmem_load32(s[c], mine + 32 * c);
+                    tmem_wait_load(s);
+                    if (kBias) {
+                        // relative positions of the warp's pairs: beyond the last bucket's start on one side, or by the table
+                        const int32_t low = j0 - (w.pos0 + warp_i + 31), high = j0 + kKeys - 1 - (w.pos0 + warp_i);
+                        const float2 scale = make_float2(a.scale, a.scale);
+                        if (high <= -a.buckets.max_distance || low >= a.buckets.max_distance) {
+                            const float v = table[high < 0 ? 0 : 2 * reach - 1];
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale, make_float2(v, v));
+                                    s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
+                                }
+                        } else {
+                            const float *t = table + (j0 - pos + reach);
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale,
+                                                          make_float2(t[32 * c + e], t[32 * c + e + 1]));
+                                    s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
+                                }
+                        }
+                    }
+                    if (j0 + kKeys > warp_visible) {
+                        const int32_t seen = visible - j0;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * c + e >= seen) s[c][e] = __float_as_uint(-INFINITY);
+                    }
+                    float most[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t(&q)[16] = *reinterpret_cast<const uint32_t(*)[16]>(&s[c / 2][c % 2 * 16]);
+                        most[c] = __uint_as_float(q[0]);
+#pragma unroll
+                        for (int e = 1; e < 15; e += 2) most[c] = max3(most[c], __uint_as_float(q[e]), __uint_as_float(q[e + 1]));
+                        most[c] = fmaxf(most[c], __uint_as_float(q[15]));
+                    }
+                    const float tile_top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                    // the maximum after the unit's previous tile, to which this warpgroup's sum is brought
+                    if (j > 0) {
+                        barrier_wait(take, taken++ & 1u, &stalled);
+                        const float given = tops[unit][group ^ 1][r];
+                        if (given > top) {
+                            sum *= exp2_approx((top - given) * to_base2);
+                            top = given;
+                        }
+                    }
+                    // a new one, and O and the sum brought to it: at the first finite score, or 2^8 above the old one
+                    const bool raise = tile_top > top && (top == -INFINITY || (tile_top - top) * to_base2 > 8.0f);
+                    if (__any_sync(0xFFFFFFFFu, raise)) {
+                        const float fade = raise ? exp2_approx((top - tile_top) * to_base2) : 1.0f;
+                        sum *= fade;
+                        if (raise) top = tile_top;
+                        if (j > 0) {
+                            // O up to the previous tile: what was issued after its product tells (the one before
+                            // that was added before this S was made)
+                            if (j + 1 < count) barrier_wait(scored + 8 * (chain ^ 1), (turns_of_other + (j + 1) / 2) & 1u, &stalled);
+                            else barrier_wait(added + 8 * unit, (additions + j - 1 - max(count - 2, 0)) & 1u, &stalled);
+                            tmem_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < kDim / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_load16(o, out + 16 * c);
+                                tmem_wait_load16(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                                tmem_store16(out + 16 * c, o);
+                            }
+                        }
+                    }
+                    tops[unit][group][r] = top;
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(pass);
+                    // exp2((s - top) to_base2): as one multiply-add, or, where a bias may be the type's
+                    // lowest value, with the difference taken first
+                    const float from = top == -INFINITY ? 0.0f : -top, shift = from * to_base2;
+                    const float2 from2 = make_float2(from, from), shift2 = make_float2(shift, shift);
+                    const float2 base2 = make_float2(to_base2, to_base2);
+                    float2 total = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t q[16];
+                        for_pairs32<kDrop>(a.mask, counter + j0 + 32 * c, [&](uint32_t e, float2 k) {
+                            const float2 v = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                            const float2 f = kBias ? mul2(add2(v, from2), base2) : fma2(v, base2, shift2);
+                            float2 x = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                            total = add2(total, x);
+                            if (kDrop) x = mul2(x, k);
+                            q[e / 2] = pack2<T>(x.x, x.y);
+                        });
+                        tmem_store16(mine + 16 * c, q);
+                    }
+                    sum += total.x + total.y;
+                    tmem_wait_store();
+                }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(ready + 8 * chain);
+            }
+            // the other warpgroup's maxima that this one had no tile for
+            if (any) taken += group ? 0 : (count > 0 ? count / 2 - (count - 1) / 2 : 0);
+            if (any && group) taken += (count + 1) / 2 - count / 2;
+
+            // ---- the result
+            const bool two = kSplitKeys && w.tiles > 1;
+            if (count) {
+                barrier_wait(done + 8 * unit, finished++ & 1u, &stalled);
+                tmem_fence_after();
+            }
+            additions += min(count, 2);
+            turns_of_other += group ? (count + 1) / 2 : count / 2;
+            float(&all_tops)[2][2][kRows] = last_tops[item & 1u], (&all_sums)[2][2][kRows] = sums[item & 1u];
+            all_tops[unit][group][r] = top, all_sums[unit][group][r] = sum;
+            sync_units<kSplitKeys>(unit);
+            // the warpgroups' maxima only grow, so O is relative to the larger
+            auto whole_unit = [&](int u, float &most, float &total) {
+                const float t0 = all_tops[u][0][r], t1 = all_tops[u][1][r];
+                most = fmaxf(t0, t1);
+                // (without a maximum, the sum is 0, or NaN where the scores are)
+                total = all_sums[u][0][r] * (t0 == -INFINITY ? 1.0f : exp2_approx((t0 - most) * to_base2)) +
+                        all_sums[u][1][r] * (t1 == -INFINITY ? 1.0f : exp2_approx((t1 - most) * to_base2));
+            };
             float weight = 1.0f, other = 0.0f;
-            sum = sums[slot][0][r] + sums[slot][1][r];
+            whole_unit(kSplitKeys ? 0 : unit, top, sum);
             if (two) {
-                const float top1 = tops[0][1][0][r], sum1 = sums[1][0][r] + sums[1][1][r], most = fmaxf(top, top1);
+                float top1, sum1;
+                whole_unit(1, top1, sum1);
+                const float most = fmaxf(top, top1);
                 weight = top == -INFINITY ? 0.0f : exp2_approx((top - most) * to_base2);
                 other = top1 == -INFINITY ? 0.0f : exp2_approx((top1 - most) * to_base2);
                 sum = sum * weight + sum1 * other;
                 top = most;
             }
-            const bool whole = p.splits == 1;
-            float *part = p.part + (static_cast<int64_t>(split) * a.batch * a.heads * a.len_q + index) * (kDim + 2);
+            const float to_natural = kBias ? 1.0f : a.scale;
+            const bool whole = p.splits == 1, mine_to_write = !kSplitKeys || unit == 0;
+            float *part = p.part + (static_cast<int64_t>(w.split) * a.batch * a.heads * a.len_q + index) * (kDim + 2);
             const float scale = !whole ? 1.0f : sum == 0.0f ? 0.0f : a.mask.scale / sum;
-            T *o_row = static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head;
-#pragma unroll
+            T *o_row = static_cast<T *>(a.out) + w.b * a.os.batch + i * a.os.len + head * a.os.head;
+            float *hand = reinterpret_cast<float *>(smem + S::kHand) + group * 32 * kRows + r;
+#pragma unroll 1
             for (int c = 0; c < kDim / 64; ++c) {
                 uint32_t o[1][32] = {};
-                const int col = half * (kDim / 2) + 32 * c;
-                if (tiles) {
-                    tmem_load32(o[0], out + 32 * c);
+                const int col = group * (kDim / 2) + 32 * c;
+                if (count && any) {
+                    tmem_load32(o[0], out + col);
                     tmem_wait_load(o);
                 }
-                if (valid) {
+                if (two) {  // unit 1 hands its part to unit 0
+                    if (c) sync_units<true>(unit);
+                    if (unit == 1 && any) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) hand[e * kRows] = __uint_as_float(o[0][e]);
+                    }
+                    sync_units<true>(unit);
+                }
+                if (valid && mine_to_write) {
                     float v[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         v[e] = __uint_as_float(o[0][e]);
-                        if (two) v[e] = v[e] * weight + hand[(col + e) * kTile + r] * other;
+                        if (two) v[e] = v[e] * weight + hand[e * kRows] * other;
                         if (sum == 0.0f) v[e] = 0.0f;  // nothing seen
                         v[e] *= scale;
                     }
@@ -448,14 +522,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     }
                 }
             }
-            if (valid && half == 0) {
+            if (valid && mine_to_write && group == 0) {
                 if (!whole)
                     part[kDim] = top * to_natural, part[kDim + 1] = sum;
                 else if (a.lse)
                     a.lse[index] = sum == 0.0f ? -INFINITY : top * to_natural + logf(sum);
             }
+            // Both warpgroups have read O before the next item's first P is announced; and they leave together, also
+            // when a wait of one of them ran out.
+            tmem_fence_before();
+            x = next_item();
+            if (!all_of<kSplitKeys>(unit, x >= 0)) break;
         }
-        tmem_fence_before();
     }
     __syncthreads();
     tmem_fence_after();
@@ -505,15 +583,15 @@ FwdPlan fwd_plan(const Attention &a)
     f.dim = a.dim <= 64 ? 64 : 128;
     f.pack = packed_heads(a);
     f.units = a.batch * (a.heads / f.pack);
-    const int32_t rows_per = kTile / f.pack, tiles = (a.len_q + rows_per - 1) / rows_per;
-    const int32_t key_tiles = (a.len_k + kTile - 1) / kTile;
+    const int32_t rows_per = kRows / f.pack, tiles = (a.len_q + rows_per - 1) / rows_per;
+    const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
     f.split_keys = tiles == 1;
     f.q_tiles = f.split_keys ? 1 : (tiles + 1) / 2;
     f.splits = 1, f.split_tiles = key_tiles < 1 ? 1 : key_tiles;
-    if (f.split_keys && key_tiles > 2) {
-        // about four blocks to an SM, of two key tiles or more
+    if (f.split_keys && key_tiles > 4) {
+        // about four blocks to an SM, of four key tiles or more
         const int64_t want = (4ll * sm_count() + f.units - 1) / f.units;
-        const int64_t most = (key_tiles + 1) / 2;
+        const int64_t most = (key_tiles + 3) / 4;
         const int64_t splits = want < most ? want : most;
         f.split_tiles = static_cast<int32_t>((key_tiles + splits - 1) / splits);
         f.splits = (key_tiles + f.split_tiles - 1) / f.split_tiles;
@@ -526,7 +604,7 @@ cudaError_t launch(const FwdParams &p, cudaStream_t s)
 {
     using S = Shape<kDim, kSplitKeys>;
     const auto kernel = attention_fwd_kernel<T, kDim, kSplitKeys, kDrop, kBias>;
-    const size_t bytes = 1024 + S::kTable + (kBias ? 2 * bias_reach(p.a.buckets) * sizeof(float) : 0);
+    const size_t bytes = 1024 + S::kTable + (kBias ? 4 * bias_reach(p.a.buckets) * sizeof(float) : 0);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.units) * p.q_tiles * p.splits), kThreads, bytes, s>>>(p);
@@ -542,7 +620,7 @@ cudaError_t launch(const FwdParams &p, cudaStream_t s)
 template <class T, int kDim, bool kSplitKeys>
 cudaError_t launch(const FwdParams &p, cudaStream_t s)
 {
-    const bool drop = p.a.mask.threshold != 0, bias = p.a.table != nullptr;
+    const bool drop = p.a.mask.threshold != 0, bias = has_bias(p.a);
     if (drop) return bias ? launch<T, kDim, kSplitKeys, true, true>(p, s) : launch<T, kDim, kSplitKeys, true, false>(p, s);
     return bias ? launch<T, kDim, kSplitKeys, false, true>(p, s) : launch<T, kDim, kSplitKeys, false, false>(p, s);
 }
@@ -572,10 +650,10 @@ cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s)
     p.part = static_cast<float *>(a.workspace);
     if (static_cast<int64_t>(f.units) * f.q_tiles * f.splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-    cudaError_t e = make_heads_map(&p.q, bf16, a.q, a.qs, a.batch, a.len_q, a.heads, a.dim, f.pack, kTile);
+    cudaError_t e = make_heads_map(&p.q, bf16, a.q, a.qs, a.batch, a.len_q, a.heads, a.dim, f.pack, kRows);
     if (a.len_k > 0) {
-        if (e == cudaSuccess) e = make_heads_map(&p.k, bf16, a.k, a.ks, a.batch, a.len_k, a.heads_kv, a.dim, 1, kTile);
-        if (e == cudaSuccess) e = make_heads_map(&p.v, bf16, a.v, a.vs, a.batch, a.len_k, a.heads_kv, a.dim, 1, kTile);
+        if (e == cudaSuccess) e = make_heads_map(&p.k, bf16, a.k, a.ks, a.batch, a.len_k, a.heads_kv, a.dim, 1, kKeys);
+        if (e == cudaSuccess) e = make_heads_map(&p.v, bf16, a.v, a.vs, a.batch, a.len_k, a.heads_kv, a.dim, 1, kKeys);
     } else {
         p.k = p.v = p.q;  // not read
     }

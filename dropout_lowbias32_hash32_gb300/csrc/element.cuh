@@ -153,16 +153,6 @@ __device__ __forceinline__ float kept_of(const Mask &m, uint32_t x)
 }
 __device__ __forceinline__ float kept(const Mask &m, uint32_t c) { return kept_of(m, c ^ (c >> 16) ^ m.key); }
 
-// Bit e: whether c + e is kept, e < 32.  A loop, for the rare rows whose
-// counters cross a multiple of 2^16.
-__device__ __forceinline__ uint32_t kept_bits(const Mask &m, uint32_t c)
-{
-    uint32_t bits = 0;
-#pragma unroll 1
-    for (uint32_t e = 0; e < 32; ++e) bits |= kept(m, c + e) != 0.0f ? 1u << e : 0u;
-    return bits;
-}
-
 // Whether the counters c .. c + n - 1 share their high halves, in every lane of
 // the warp: then kept_of(m, (c + e) ^ high_key(m, c)) is kept(m, c + e).
 __device__ __forceinline__ bool one_high_half(uint32_t c, uint32_t n)
@@ -171,18 +161,22 @@ __device__ __forceinline__ bool one_high_half(uint32_t c, uint32_t n)
 }
 __device__ __forceinline__ uint32_t high_key(const Mask &m, uint32_t c) { return m.key ^ (c >> 16); }
 
-// Drops of 32 f32 values those whose counters c, c + 1, ... say so.
-__device__ __forceinline__ void drop32(const Mask &m, uint32_t c, uint32_t (&v)[32])
+// f(e, k) for e = 0 .. 31 in steps of 2, k the pair of factors (1 kept, 0
+// dropped) of the counters c + e and c + e + 1.
+template <bool kDrop, class F>
+__device__ __forceinline__ void for_pairs32(const Mask &m, uint32_t c, F &&f)
 {
-    if (one_high_half(c, 32)) {
+    if (!kDrop) {
+#pragma unroll
+        for (uint32_t e = 0; e < 32; e += 2) f(e, make_float2(1.0f, 1.0f));
+    } else if (one_high_half(c, 32)) {
         const uint32_t key = high_key(m, c);
 #pragma unroll
-        for (uint32_t e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kept_of(m, (c + e) ^ key));
-    } else {
-        const uint32_t bits = kept_bits(m, c);
+        for (uint32_t e = 0; e < 32; e += 2)
+            f(e, make_float2(kept_of(m, (c + e) ^ key), kept_of(m, (c + e + 1) ^ key)));
+    } else {  // the high half changes on the way
 #pragma unroll
-        for (uint32_t e = 0; e < 32; ++e)
-            if (!(bits >> e & 1u)) v[e] = 0;
+        for (uint32_t e = 0; e < 32; e += 2) f(e, make_float2(kept(m, c + e), kept(m, c + e + 1)));
     }
 }
 

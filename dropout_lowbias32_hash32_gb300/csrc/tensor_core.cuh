@@ -55,21 +55,34 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity)
     return done != 0;
 }
 
-// Waits for the phase of the given parity to end, about two seconds at most.
-// After a wait that ran out, `stalled` (shared by the block) makes every later
-// wait return at once: the block goes on over what it has, frees what it holds
-// and ends, and the host can read that it happened.
-__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t *stalled)
+// Waits for the phase of the given parity to end, about two seconds at most;
+// false when that ran out.  `stalled` (shared by the block) then makes every
+// later wait return false at once: the block issues nothing more, waits for
+// what it has in flight, frees what it holds and ends, and the host can read
+// that it happened.  barrier_wait is for a whole warp, which it leaves
+// converged; barrier_wait_one for a single thread.
+__device__ __forceinline__ bool barrier_wait_one(uint32_t bar, uint32_t parity, volatile uint32_t *stalled)
 {
 #pragma unroll 1
     for (uint32_t tries = 0; !barrier_try(bar, parity); ++tries) {
-        if (*stalled) return;
+        if (*stalled) return false;
         if (tries == 1u << 20) {
             *stalled = 1;
             atomicAdd(&g_stalled_waits, 1ull);
-            return;
+            return false;
         }
     }
+    return true;
+}
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile uint32_t *stalled)
+{
+    return __all_sync(0xFFFFFFFFu, barrier_wait_one(bar, parity, stalled));
+}
+// The end of a block's role that gave up: waits, with a limit, for a phase.
+__device__ __forceinline__ void barrier_drain(uint32_t bar, uint32_t parity)
+{
+#pragma unroll 1
+    for (uint32_t tries = 0; tries < 100000 && !barrier_try(bar, parity); ++tries) {}
 }
 
 __device__ __forceinline__ void fence_barrier_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
@@ -96,6 +109,34 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// ---- work from blocks that have not started ------------------------------------------
+// A running block takes over the work of one that the launch still has to
+// start (cluster launch control): 16 bytes of answer to `response`, counted by
+// the barrier.  After an answer that there is none, nobody asks again.
+__device__ __forceinline__ void ask_for_work(uint32_t response, uint32_t bar)
+{
+    barrier_expect(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 ::"r"(response), "r"(bar)
+                 : "memory");
+}
+// The index of the block whose work was taken over; -1 for none.
+__device__ __forceinline__ int32_t taken_work(uint32_t response)
+{
+    int32_t taken, index;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.s32 %0, 1, 0, p;\n\t"
+        "mov.b32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, _, _, _}, r;\n\t}"
+        : "=r"(taken), "=r"(index)
+        : "r"(response)
+        : "memory");
+    return taken ? index : -1;
 }
 
 // ---- tensor memory ---------------------------------------------------------------
@@ -208,6 +249,9 @@ __device__ __forceinline__ uint64_t column_major_tile(uint32_t address, uint32_t
     return kDescriptorBase | ((address >> 4) & 0x3FFFu) | (uint64_t((chunk >> 4) & 0x3FFFu) << 16) |
            (uint64_t(1024 >> 4) << 32);
 }
+
+// How far step i of 16 is into a row-major tile of boxes, as a descriptor counts.
+__host__ __device__ constexpr uint32_t row_step(int i, uint32_t box) { return (i / 4 * box + i % 4 * 32) / 16; }
 
 // 16-bit operands of type T, f32 accumulators, M = 128 rows by N columns.
 template <class T>

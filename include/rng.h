@@ -375,8 +375,8 @@ rng_status rng_attention_fwd(const rng_attention_args *args, void *stream);
  * results are the same bits every time. */
 rng_status rng_attention_bwd(const rng_attention_args *args, void *stream);
 
-/* Bytes of workspace on the current device (pointers are not looked at,
- * except whether bias_table and dbias_table are NULL). */
+/* Bytes of workspace on the current device (sizes, scale and
+ * whether bias_table and dbias_table are NULL are looked at). */
 size_t rng_attention_fwd_workspace(const rng_attention_args *args);
 size_t rng_attention_bwd_workspace(const rng_attention_args *args);
 
