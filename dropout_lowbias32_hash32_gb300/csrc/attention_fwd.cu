@@ -56,27 +56,6 @@ struct Shape {
     static constexpr uint32_t kTable = kHand + (kSplitKeys ? 64 * kRows * 4 : 0);  // a bias table a unit
 };
 
-// Barriers of the block's units, or of one; all_of also tells whether every one
-// of their threads agrees.
-template <bool kBoth>
-__device__ __forceinline__ void sync_units(int unit)
-{
-    if (kBoth) asm volatile("bar.sync 1, 512;" ::: "memory");
-    else asm volatile("bar.sync %0, 256;" ::"r"(2 + unit) : "memory");
-}
-template <bool kBoth>
-__device__ __forceinline__ bool all_of(int unit, bool agree)
-{
-    uint32_t yes;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-        : "=r"(yes)
-        : "r"(static_cast<uint32_t>(agree)), "r"(kBoth ? 1 : 2 + unit), "n"(kBoth ? 512 : 256)
-        : "memory");
-    return yes != 0;
-}
-
 // One item of work: a pack of heads of a batch entry, its query tiles, a range
 // of key tiles.
 struct Item {
@@ -151,38 +130,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     tmem_fence_after();
     const uint32_t tmem = tmem_base;
 
-    // Every role goes through the block's items: its own first, then those of blocks that need not start any more.
-    // The asking warp asks for the next one when all have heard the last answer.
-    uint32_t items = 0;
-    auto next_item = [&]() -> int32_t {
-        if (!barrier_wait(answered, items++ & 1u, &stalled)) return -1;
-        const int32_t next = taken_work(smem_address(&response));
-        fence_async_shared();
-        __syncwarp();
-        if (elect_one()) barrier_arrive(heard);
-        return next;
-    };
+    WorkQueue work{smem_address(&response), answered, heard, &stalled};
 
     if (warp >= kTmaWarp) {
         give_registers<kOtherRegisters>();
         if (warp == kAskWarp) {
-            if (elect_one()) {
-                int32_t next = 0;
-                while (next >= 0 && (!items || barrier_wait_one(heard, (items - 1) & 1u, &stalled))) {
-                    ask_for_work(smem_address(&response), answered);
-                    if (!barrier_wait_one(answered, items++ & 1u, &stalled)) {
-                        barrier_drain(answered, (items - 1) & 1u);
-                        break;
-                    }
-                    next = taken_work(smem_address(&response));
-                }
-            }
+            if (elect_one()) work.serve();
         } else if (warp == kTmaWarp) {
             // ---- TMA: the queries, then K_0 .. K_{lead-1} and alternately V_n, K_{n+lead}
             const bool one = elect_one();
             uint32_t use = 0, loaded = 0, tails = 0;
             bool fine = true;
-            for (int32_t x = blockIdx.x; x >= 0 && fine; x = fine ? next_item() : -1) {
+            for (int32_t x = blockIdx.x; x >= 0 && fine; x = fine ? work.next_warp() : -1) {
                 const Item w = item_at<kSplitKeys>(p, x);
                 if (w.tiles) {
                     if (loaded) fine = barrier_wait(q_empty, (loaded - 1) & 1u, &stalled);
@@ -245,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             const bool one = elect_one();
             uint32_t use = 0, given = 0, loaded = 0;  // given: bit g, the parity of warpgroup g's next P
             bool fine = true;
-            for (int32_t x = blockIdx.x; x >= 0; x = fine ? next_item() : -1) {
+            for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_warp() : -1) {
                 const Item w = item_at<kSplitKeys>(p, x);
                 if (!w.tiles) continue;
                 const int32_t count = kSplitKeys ? w.tiles : unit ? w.count[1] : w.count[0];
@@ -299,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     } else {
         take_registers<kUnitRegisters>();
         // ---- the units' rows
+        constexpr int kTogether = kSplitKeys ? 512 : 256;  // threads that work on an item's rows
         const int unit = warp / 8, group = warp / 4 % 2;
         const int32_t r = (warp % 4) * 32 + lane;
         const uint32_t lanes = (warp % 4) * 32u << 16, chain = 2 * unit + group;
@@ -323,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             const int32_t warp_visible = a.causal ? min(w.keys, w.pos0 + warp_i + 1) : w.keys;  // the least of the warp's
             if (kBias && w.head0 != table_head) {  // the bias by relative position (pack is 1)
                 table_head = w.head0;
-                sync_units<false>(unit);
+                sync_threads<256>(2 + unit);
                 for (int32_t t = threadIdx.x % 256u; t < 2 * reach; t += 256)
                     table[t] = a.table ? to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, t - reach) * a.heads + w.head0]) : 0.0f;
-                sync_units<false>(unit);
+                sync_threads<256>(2 + unit);
             }
             float top = -INFINITY, sum = 0.0f;
             // the unit's tiles; this warpgroup's are group, group + 2, ...
@@ -459,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             turns_of_other += group ? (count + 1) / 2 : count / 2;
             float(&all_tops)[2][2][kRows] = last_tops[item & 1u], (&all_sums)[2][2][kRows] = sums[item & 1u];
             all_tops[unit][group][r] = top, all_sums[unit][group][r] = sum;
-            sync_units<kSplitKeys>(unit);
+            sync_threads<kTogether>(kSplitKeys ? 1 : 2 + unit);
             // the warpgroups' maxima only grow, so O is relative to the larger
             auto whole_unit = [&](int u, float &most, float &total) {
                 const float t0 = all_tops[u][0][r], t1 = all_tops[u][1][r];
@@ -494,12 +454,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     tmem_wait_load(o);
                 }
                 if (two) {  // unit 1 hands its part to unit 0
-                    if (c) sync_units<true>(unit);
+                    if (c) sync_threads<512>(1);
                     if (unit == 1 && any) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) hand[e * kRows] = __uint_as_float(o[0][e]);
                     }
-                    sync_units<true>(unit);
+                    sync_threads<512>(1);
                 }
                 if (valid && mine_to_write) {
                     float v[32];
@@ -531,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             // Both warpgroups have read O before the next item's first P is announced; and they leave together, also
             // when a wait of one of them ran out.
             tmem_fence_before();
-            x = next_item();
-            if (!all_of<kSplitKeys>(unit, x >= 0)) break;
+            x = work.next_warp();
+            if (!all_of<kTogether>(kSplitKeys ? 1 : 2 + unit, x >= 0)) break;
         }
     }
     __syncthreads();

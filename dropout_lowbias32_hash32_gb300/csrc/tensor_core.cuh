@@ -139,6 +139,69 @@ __device__ __forceinline__ int32_t taken_work(uint32_t response)
     return taken ? index : -1;
 }
 
+// A block's items of work: its own first, then those of blocks that need not
+// start any more.  Every role goes through them; the asking warp asks for the
+// next one when all have heard the last answer, so nobody is more than one item
+// ahead.
+struct WorkQueue {
+    uint32_t response, answered, heard;  // shared-memory addresses: 16 bytes, and two barriers
+    volatile uint32_t *stalled;
+    uint32_t items = 0;
+
+    // The next item, for a whole warp or for a role of one thread; -1 when there
+    // is none, or after a wait that ran out.
+    __device__ __forceinline__ int32_t next_warp()
+    {
+        if (!barrier_wait(answered, items++ & 1u, stalled)) return -1;
+        const int32_t next = taken_work(response);
+        fence_async_shared();
+        __syncwarp();
+        if (elect_one()) barrier_arrive(heard);
+        return next;
+    }
+    __device__ __forceinline__ int32_t next_one()
+    {
+        if (!barrier_wait_one(answered, items++ & 1u, stalled)) return -1;
+        const int32_t next = taken_work(response);
+        fence_async_shared();
+        barrier_arrive(heard);
+        return next;
+    }
+    // The asking warp's thread.
+    __device__ __forceinline__ void serve()
+    {
+        int32_t next = 0;
+        while (next >= 0 && (!items || barrier_wait_one(heard, (items - 1) & 1u, stalled))) {
+            ask_for_work(response, answered);
+            if (!barrier_wait_one(answered, items++ & 1u, stalled)) {
+                barrier_drain(answered, (items - 1) & 1u);
+                break;
+            }
+            next = taken_work(response);
+        }
+    }
+};
+
+// A named barrier of kThreads threads; all_of also tells whether every one of
+// them agrees.
+template <int kThreads>
+__device__ __forceinline__ void sync_threads(int id)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(kThreads) : "memory");
+}
+template <int kThreads>
+__device__ __forceinline__ bool all_of(int id, bool agree)
+{
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(yes)
+        : "r"(static_cast<uint32_t>(agree)), "r"(id), "n"(kThreads)
+        : "memory");
+    return yes != 0;
+}
+
 // ---- tensor memory ---------------------------------------------------------------
 // 512 columns of 128 lanes x 32 bits; an address is lane << 16 | column.  A warp
 // reaches the 32 lanes of its rank in its group of four.
