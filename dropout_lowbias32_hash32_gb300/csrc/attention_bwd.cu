@@ -26,12 +26,12 @@ namespace {
 constexpr int kRows = 128, kCols = 64;  // a tile
 
 // The warpgroups of a block, and their registers: it starts with 65536 / threads
-// a thread, the last warpgroup (a TMA warp, an MMA warp, one that asks for work,
-// one that only fills it) gives some to the others.
+// a thread, the last warpgroup (a TMA warp, an MMA warp,
+// two that only fill it) gives some to the others.
 template <int kChains, int kShare>  // warpgroups of a tile
 struct Crew {
     static constexpr int kGroups = kChains * kShare, kWorkers = 128 * kGroups, kThreads = kWorkers + 128;
-    static constexpr uint32_t kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1, kAskWarp = kTmaWarp + 2;
+    static constexpr uint32_t kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1;
     // 512 threads start with 128 each, 3 x 152 + 56 = 4 x 128; 640 with 96, 4 x 104 + 64 = 5 x 96
     static constexpr int kWorkerRegisters = kGroups == 3 ? 152 : 104, kOtherRegisters = kGroups == 3 ? 56 : 64;
     static_assert(kGroups == 3 || kGroups == 4, "");
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
         for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1);
         for (int s = 0; s < kChains; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4);
         barrier_init(done, 1), barrier_init(q_full, 1), barrier_init(q_empty, 1), barrier_init(tail, 1);
-        barrier_init(answered, 1), barrier_init(heard, 2 + 4 * kChains), barrier_init(drained, 1);
+        barrier_init(answered, 1), barrier_init(heard, 1 + 4 * kChains), barrier_init(drained, 1);
         fence_barrier_init();
     }
     if (warp == Team::kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
@@ -177,14 +177,12 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
     WorkQueue work{smem_address(&response), answered, heard, &stalled};
     if (warp >= Team::kTmaWarp) {
         give_registers<Team::kOtherRegisters>();
-        if (warp == Team::kAskWarp) {
-            if (elect_one()) work.serve();
-        } else if (warp == Team::kTmaWarp) {
+        if (warp == Team::kTmaWarp) {
             // ---- TMA: q and do, then K_n and V_n
             const bool one = elect_one();
             uint32_t use = 0, loaded = 0, tails = 0;
             bool fine = true;
-            for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_warp() : -1) {
+            for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.ask_warp() : -1) {
                 const QueryItem w = query_item(p, x);
                 if (!w.tiles) continue;
                 if (loaded) fine = barrier_wait(q_empty, (loaded - 1) & 1u, &stalled);
@@ -552,7 +550,7 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
         for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1);
         for (int s = 0; s < kChains; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4 * S::kShare);
         barrier_init(done, 1), barrier_init(k_full, 1), barrier_init(k_empty, 1);
-        barrier_init(answered, 1), barrier_init(heard, 2 + 4 * Team::kGroups), barrier_init(drained, 1);
+        barrier_init(answered, 1), barrier_init(heard, 1 + 4 * Team::kGroups), barrier_init(drained, 1);
         fence_barrier_init();
     }
     if (warp == Team::kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
@@ -563,14 +561,12 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
     WorkQueue work{smem_address(&response), answered, heard, &stalled};
     if (warp >= Team::kTmaWarp) {
         give_registers<Team::kOtherRegisters>();
-        if (warp == Team::kAskWarp) {
-            if (elect_one()) work.serve();
-        } else if (warp == Team::kTmaWarp) {
+        if (warp == Team::kTmaWarp) {
             // ---- TMA: k and v, then the queries' tiles, head by head
             if (elect_one()) {
                 uint32_t use = 0, loaded = 0;
                 bool fine = true;
-                for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_one() : -1) {
+                for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.ask_one() : -1) {
                     const KeyItem w = key_item(p, x);
                     if (!w.tiles) continue;
                     if (loaded) fine = barrier_wait_one(k_empty, (loaded - 1) & 1u, &stalled);

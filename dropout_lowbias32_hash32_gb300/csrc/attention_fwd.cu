@@ -29,9 +29,9 @@ namespace rngk {
 namespace {
 
 constexpr int kRows = 128, kKeys = 64;  // a unit's tile
-// 2 x 2 warpgroups for the units, then a TMA warp, an MMA warp a unit, one that asks for work
+// 2 x 2 warpgroups for the units, then a TMA warp, an MMA warp a unit, one that only fills the warpgroup
 constexpr int kThreads = 640;
-constexpr uint32_t kTmaWarp = 16, kMmaWarp = 17, kAskWarp = 19;
+constexpr uint32_t kTmaWarp = 16, kMmaWarp = 17;
 // registers: 640 threads start with 96 each; 4 x 104 + 64 = 5 x 96
 constexpr int kUnitRegisters = 104, kOtherRegisters = 64;
 constexpr uint32_t kRowsBox = 16384, kKeysBox = 8192;  // bytes of 128 and of 64 rows of 64 elements
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         for (int s = 0; s < 16; ++s) barrier_init(passed + 8 * s, 1);
         for (int s = 0; s < 2; ++s) barrier_init(added + 8 * s, 1), barrier_init(done + 8 * s, 1);
         barrier_init(q_full, 1), barrier_init(q_empty, 2), barrier_init(tail, 1);
-        barrier_init(answered, 1), barrier_init(heard, 19);
+        barrier_init(answered, 1), barrier_init(heard, 18);
         for (int s = 0; s < 2; ++s) barrier_init(drained + 8 * s, 1);
         fence_barrier_init();
     }
@@ -134,14 +134,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
 
     if (warp >= kTmaWarp) {
         give_registers<kOtherRegisters>();
-        if (warp == kAskWarp) {
-            if (elect_one()) work.serve();
-        } else if (warp == kTmaWarp) {
+        if (warp == kTmaWarp) {
             // ---- TMA: the queries, then K_0 .. K_{lead-1} and alternately V_n, K_{n+lead}
             const bool one = elect_one();
             uint32_t use = 0, loaded = 0, tails = 0;
             bool fine = true;
-            for (int32_t x = blockIdx.x; x >= 0 && fine; x = fine ? work.next_warp() : -1) {
+            for (int32_t x = blockIdx.x; x >= 0 && fine; x = fine ? work.ask_warp() : -1) {
                 const Item w = item_at<kSplitKeys>(p, x);
                 if (w.tiles) {
                     if (loaded) fine = barrier_wait(q_empty, (loaded - 1) & 1u, &stalled);
@@ -193,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                 if (loaded) barrier_drain(q_full, (loaded - 1) & 1u);
                 for (uint32_t u = use > S::kStages ? use - S::kStages : 0; u < use; ++u) barrier_drain(full + 8 * (u % S::kStages), u / S::kStages & 1u);
             }
-        } else {
+        } else if (warp < kMmaWarp + 2) {
             // ---- MMA, a warp to a unit.  Both go through every stage, whether or not it holds something for their unit,
             // so that neither falls a whole phase behind.
             constexpr uint32_t kScores = mma_shape<T>(kKeys, false), kOut = mma_shape<T>(kDim, true);

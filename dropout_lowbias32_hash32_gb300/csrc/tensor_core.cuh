@@ -140,9 +140,9 @@ __device__ __forceinline__ int32_t taken_work(uint32_t response)
 }
 
 // A block's items of work: its own first, then those of blocks that need not
-// start any more.  Every role goes through them; the asking warp asks for the
-// next one when all have heard the last answer, so nobody is more than one item
-// ahead.
+// start any more.  Every role goes through them.  The loading role asks for the
+// next one when it has asked for all of an item's tiles, not before: an item
+// that is taken too early waits while blocks that have finished go without.
 struct WorkQueue {
     uint32_t response, answered, heard;  // shared-memory addresses: 16 bytes, and two barriers
     volatile uint32_t *stalled;
@@ -167,18 +167,28 @@ struct WorkQueue {
         barrier_arrive(heard);
         return next;
     }
-    // The asking warp's thread.
-    __device__ __forceinline__ void serve()
+    // The loading role's: asks, once all others have heard the last answer.
+    __device__ __forceinline__ int32_t ask_warp()
     {
-        int32_t next = 0;
-        while (next >= 0 && (!items || barrier_wait_one(heard, (items - 1) & 1u, stalled))) {
-            ask_for_work(response, answered);
-            if (!barrier_wait_one(answered, items++ & 1u, stalled)) {
-                barrier_drain(answered, (items - 1) & 1u);
-                break;
-            }
-            next = taken_work(response);
+        if (items && !barrier_wait(heard, (items - 1) & 1u, stalled)) return -1;
+        if (elect_one()) ask_for_work(response, answered);
+        if (!barrier_wait(answered, items & 1u, stalled)) {
+            barrier_drain(answered, items & 1u);
+            return -1;
         }
+        ++items;
+        return taken_work(response);
+    }
+    __device__ __forceinline__ int32_t ask_one()
+    {
+        if (items && !barrier_wait_one(heard, (items - 1) & 1u, stalled)) return -1;
+        ask_for_work(response, answered);
+        if (!barrier_wait_one(answered, items & 1u, stalled)) {
+            barrier_drain(answered, items & 1u);
+            return -1;
+        }
+        ++items;
+        return taken_work(response);
     }
 };
 
