@@ -18,6 +18,28 @@ struct Buckets {
     int32_t starts[kMaxBuckets];
 };
 
+// Division by a number that a launch fixes: a product's high half and a shift
+// (the multiplier rounded up is exact for dividends below 2^31).  The kernels
+// cut an item's index with it, which their roles all wait for.
+struct Divider {
+    uint32_t by, multiplier, shift;
+    Divider() = default;
+    explicit Divider(uint32_t d) : by(d), multiplier(0), shift(0)
+    {
+        if (d < 2) return;
+        uint32_t log = 1;
+        while ((uint64_t(1) << log) < d) ++log;
+        multiplier = static_cast<uint32_t>(((uint64_t(1) << (31 + log)) + d - 1) / d);
+        shift = log - 1;
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return by < 2 ? n : __umulhi(n, multiplier) >> shift; }
+    __device__ __forceinline__ void divide(uint32_t n, int32_t &q, int32_t &r) const
+    {
+        q = static_cast<int32_t>(quotient(n));
+        r = static_cast<int32_t>(n) - q * static_cast<int32_t>(by);
+    }
+};
+
 struct Strides {
     int64_t batch, len, head;
 };
@@ -83,6 +105,13 @@ __host__ __device__ __forceinline__ int32_t bias_reach(const Buckets &b) { retur
 // Whether the forward kernels with a bias are needed: those without take the
 // maximum before the scores are scaled, and so want a scale above 0.
 inline bool has_bias(const Attention &a) { return a.table != nullptr || !(a.scale > 0.0f); }
+
+inline int32_t log2_of(int32_t power)
+{
+    int32_t n = 0;
+    while ((1 << n) < power) ++n;
+    return n;
+}
 
 // Heads of one key head that lie side by side in a tile of 128 rows, so that
 // they read its keys once: all of them, where a tile is a whole number of

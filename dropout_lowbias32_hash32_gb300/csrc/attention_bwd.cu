@@ -47,14 +47,17 @@ template <class T>
 constexpr float kLift = 0.0f;
 template <>
 constexpr float kLift<__half> = 10.0f;
+template <class T>
+constexpr float kUnlift = kLift<T> != 0.0f ? 1.0f / 1024.0f : 1.0f;
 
 struct BwdParams {
     CUtensorMap q_rows, do_rows, k_cols, v_cols;  // query_kernel's
     CUtensorMap k_rows, v_rows, q_cols, do_cols;  // key_kernel's
     Attention a;
-    int32_t pack, units, q_tiles, len_pad;
-    // [batch heads][len_pad]: lse (in base two unless there is a bias; +inf for a query that sees nothing) and
-    // delta; [heads][2 reach]: the bias by relative position; [batch heads][q_tiles][buckets]: sums of dS
+    int32_t pack, pack_log, units, q_tiles, len_pad;
+    Divider by_units, by_q_tiles, by_packs, by_group, by_key_units, by_heads_kv;
+    // [batch heads][len_pad]: what key_kernel adds to a query's scores in base two, kLift - lse (with a bias, -lse
+    // in the natural base; -inf for a query that sees nothing), and to its scaled dP, -delta; [heads][2 reach]: the bias by relative position; [batch heads][q_tiles][buckets]: sums of dS
     float2 *stats;
     float *bias, *sums;
 };
@@ -97,23 +100,6 @@ struct QueryShape {
     static constexpr uint32_t kTable = kRing + kStages * kStageBytes;
 };
 
-// The relative positions of a bucket, lo .. hi (empty: lo > hi).
-__device__ __forceinline__ void bucket_range(const Buckets &b, int32_t n, int32_t &lo, int32_t &hi)
-{
-    constexpr int32_t kFar = 1 << 30;
-    const bool past = b.past && n >= b.past;
-    const int32_t k = past ? n - b.past : n;
-    const int32_t near = k == 0 ? 0 : b.starts[k - 1], far = k == b.count - 1 ? kFar : b.starts[k] - 1;
-    if (n >= b.total) {
-        lo = 1, hi = 0;
-    } else if (past) {
-        lo = max(near, 1), hi = far;
-    } else {
-        lo = -far, hi = -near;
-        if (!b.past && k == 0) hi = kFar;  // one way: every key past the query
-    }
-}
-
 struct QueryItem {
     int32_t b, pack, head0, head_kv, q_tile, i0, keys, pos0, tiles;
 };
@@ -124,13 +110,14 @@ __device__ __forceinline__ QueryItem query_item(const BwdParams &p, uint32_t x)
     QueryItem w;
     int32_t unit;
     if (a.causal) {  // the longest first
-        unit = x % p.units, w.q_tile = p.q_tiles - 1 - x / p.units;
+        p.by_units.divide(x, w.q_tile, unit);
+        w.q_tile = p.q_tiles - 1 - w.q_tile;
     } else {
-        w.q_tile = x % p.q_tiles, unit = x / p.q_tiles;
+        p.by_q_tiles.divide(x, unit, w.q_tile);
     }
-    const int32_t packs = a.heads / p.pack, rows_per = kRows / p.pack;
-    w.b = unit / packs, w.pack = unit % packs;
-    w.head0 = w.pack * p.pack, w.head_kv = w.head0 / a.group;
+    const int32_t rows_per = kRows >> p.pack_log;
+    p.by_packs.divide(unit, w.b, w.pack);
+    w.head0 = w.pack << p.pack_log, w.head_kv = p.by_group.quotient(w.head0);
     w.i0 = w.q_tile * rows_per;
     w.keys = keys_of(a, w.b), w.pos0 = first_position(a, w.keys);
     const int32_t last = min(w.i0 + rows_per, a.len_q) - 1, end = a.causal ? min(w.keys, w.pos0 + last + 1) : w.keys;
@@ -291,47 +278,65 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
         const int32_t last_start = kBias ? a.buckets.starts[a.buckets.count - 2] : 0;
         const float2 scale = make_float2(a.mask.scale, a.mask.scale);
         int32_t table_head = -1;
+        // the bucket of every relative position that is tabulated (read after the item's first barrier)
+        uint8_t *bucket_at = reinterpret_cast<uint8_t *>(table + 2 * reach) + reach;
+        if (kBias)
+            for (int32_t t = threadIdx.x; t < 2 * reach; t += Team::kWorkers) bucket_at[t - reach] = bucket_of(a.buckets, t - reach);
+        const float above = lane ? 1.0f : 0.0f;
         uint32_t turn = 0, finished = 0;
-        for (int32_t x = blockIdx.x;;) {
-            const QueryItem w = query_item(p, x);
-            const int32_t warp_i = w.i0 + (warp % 4) * 32 / p.pack;
-            const int32_t i = w.i0 + r / p.pack, head = w.head0 + r % p.pack, pos = w.pos0 + i;
+        // A row's o, do (the warpgroups take parts of it) and lse are asked for before the previous item's result is
+        // written, which takes longer than they do.
+        constexpr int kParts = (kDim / 8 + kChains - 1) / kChains;
+        Raw<T, 8> part_o[kParts], part_do[kParts];
+        float next_lse;
+        auto fetch_row = [&](const QueryItem &w) {
+            const int32_t i = min(w.i0 + (r >> p.pack_log), a.len_q - 1), head = w.head0 + (r & (p.pack - 1));
+            const T *o = static_cast<const T *>(a.o) + w.b * a.os.batch + i * a.os.len + head * a.os.head;
+            const T *d_o = static_cast<const T *>(a.d_o) + w.b * a.dos.batch + i * a.dos.len + head * a.dos.head;
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+                const int32_t at = min(8 * (k * kChains + static_cast<int32_t>(chain)), a.dim - 8);
+                part_o[k] = load<false, T, 8>(o + at), part_do[k] = load<false, T, 8>(d_o + at);
+            }
+            next_lse = a.lse[(static_cast<int64_t>(w.b) * a.heads + head) * a.len_q + i];
+        };
+        QueryItem w = query_item(p, blockIdx.x);
+        fetch_row(w);
+        for (;;) {
+            const int32_t warp_i = w.i0 + ((warp % 4) * 32 >> p.pack_log);
+            const int32_t i = w.i0 + (r >> p.pack_log), head = w.head0 + (r & (p.pack - 1)), pos = w.pos0 + i;
             const bool valid = i < a.len_q, any = warp_i < a.len_q;
             const int64_t index = static_cast<int64_t>(w.b) * a.heads + head;
             const uint32_t counter = a.first + (static_cast<uint32_t>(index) * a.len_q + i) * static_cast<uint32_t>(a.len_k);
             const int32_t visible = a.causal ? min(w.keys, pos + 1) : w.keys;
             const int32_t warp_visible = a.causal ? min(w.keys, w.pos0 + warp_i + 1) : w.keys;
 
-            // lse and delta = sum of o do (the warpgroups take parts of a row)
+            // lse and delta = sum of o do
             float lse = INFINITY, delta = 0.0f;
             if (valid) {
-                const T *o = static_cast<const T *>(a.o) + w.b * a.os.batch + i * a.os.len + head * a.os.head;
-                const T *d_o = static_cast<const T *>(a.d_o) + w.b * a.dos.batch + i * a.dos.len + head * a.dos.head;
 #pragma unroll
-                for (int d = 0; d < kDim; d += 8 * kChains) {
-                    const int32_t at = d + 8 * chain;
-                    if (at < a.dim) {
+                for (int k = 0; k < kParts; ++k) {
+                    if (8 * (k * kChains + static_cast<int32_t>(chain)) < a.dim) {
                         float u[8], v[8];
-                        unpack<T, 8>(load<false, T, 8>(o + at), u);
-                        unpack<T, 8>(load<false, T, 8>(d_o + at), v);
+                        unpack<T, 8>(part_o[k], u);
+                        unpack<T, 8>(part_do[k], v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) delta += u[e] * v[e];
                     }
                 }
-                lse = a.lse[index * a.len_q + i];
                 // a query that sees nothing: exp(s - inf) = 0 whatever its scores
-                lse = lse == -INFINITY ? INFINITY : kBias ? lse : lse * kLog2e;
+                lse = next_lse == -INFINITY ? INFINITY : kBias ? next_lse : next_lse * kLog2e;
             }
             deltas[chain][r] = delta;
             sync_threads<Team::kWorkers>(1);
             delta = 0.0f;
 #pragma unroll
             for (int c = 0; c < kChains; ++c) delta += deltas[c][r];
-            if (valid && chain == 0) p.stats[index * p.len_pad + i] = make_float2(lse, delta);
+            if (valid && chain == 0) p.stats[index * p.len_pad + i] = make_float2(kBias ? -lse : kLift<T> - lse, -delta * kUnlift<T>);
             if (w.q_tile == p.q_tiles - 1)  // what key_kernel reads past the last query
                 for (int32_t t = threadIdx.x; t < p.pack * (p.len_pad - a.len_q); t += Team::kWorkers)
-                    p.stats[(static_cast<int64_t>(w.b) * a.heads + w.head0 + t % p.pack) * p.len_pad + a.len_q + t / p.pack] =
-                        make_float2(INFINITY, 0.0f);
+                    p.stats[(static_cast<int64_t>(w.b) * a.heads + w.head0 + (t & (p.pack - 1))) * p.len_pad + a.len_q + (t >> p.pack_log)] =
+                        make_float2(-INFINITY, 0.0f);
             if (kBias && w.head0 != table_head) {  // the bias by relative position (pack is 1)
                 table_head = w.head0;
                 for (int32_t t = threadIdx.x; t < 2 * reach; t += Team::kWorkers)
@@ -345,7 +350,11 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
             const float2 minus = make_float2(-delta, -delta), l2 = make_float2(-lse, -lse);
             const float to_base2 = kBias ? kLog2e : a.scale * kLog2e;
             const float2 b2 = make_float2(to_base2, to_base2);
-            float own[kMaxBuckets / 32] = {}, far_low = 0.0f, far_high = 0.0f;
+            float far_low = 0.0f, far_high = 0.0f;
+            if (kBias && a.dtable) {
+                for (uint32_t m = lane; m < kMaxBuckets; m += 32) by_bucket[warp][m] = 0.0f;
+                __syncwarp();
+            }
 #pragma unroll 1
             for (int32_t n = chain; n < w.tiles; n += kChains, ++turn) {
                 barrier_wait(scored + 8 * chain, turn & 1u, &stalled);
@@ -389,39 +398,39 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                             if (lane == 0) barrier_arrive(ready + 8 * chain);
                         }
                         if (kBias && a.dtable) {
-                            if (!valid) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) s[e] = 0;
-                            }
                             if (far) {  // one bucket
                                 float2 total = make_float2(0.0f, 0.0f);
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) total = add2(total, make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
                                 (high <= -last_start ? far_low : far_high) += total.x + total.y;
                             } else {
-                                // sums along the diagonals of the warp's 32 x 32 pairs: a partial sum moves one row down
-                                // with each column; what leaves row 31, or is left in the last column, is a whole one
+                                // Sums along the diagonals of the warp's 32 x 32 pairs: a partial sum moves one row down
+                                // with each column; what leaves row 31, or is left in the last column, is a whole one.
+                                // Diagonal d = 0 .. 62 is relative position low + d.
                                 float acc = 0.0f;
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) {
-                                    acc = __shfl_up_sync(0xFFFFFFFFu, acc, 1);
-                                    acc = (lane ? acc : 0.0f) + __uint_as_float(s[e]);
+                                    acc = __fmaf_rn(__shfl_up_sync(0xFFFFFFFFu, acc, 1), above, __uint_as_float(s[e]));
                                     if (lane == 31) diagonals[warp][e] = acc;
                                 }
-                                if (lane < 31) diagonals[warp][62 - lane] = acc;
+                                diagonals[warp][63 - (lane + 1) % 32] = lane < 31 ? acc : 0.0f;
                                 __syncwarp();
-                                // diagonal d is relative position low + d; a lane adds the buckets lane, lane + 32, ...
-#pragma unroll
-                                for (int m = 0; m < kMaxBuckets / 32; ++m) {
-                                    if (32 * m < a.buckets.total) {
-                                        int32_t from, to;
-                                        bucket_range(a.buckets, lane + 32 * m, from, to);
-                                        from = max(from - low, 0), to = min(to - low, 62);
+                                // A bucket's positions follow each other, so sums over runs of one bucket: half of the
+                                // diagonals at a time, the last lane of a run adds it.
 #pragma unroll 1
-                                        for (int32_t d = from; d <= to; ++d) own[m] += diagonals[warp][d];
+                                for (int32_t d = lane; d < 64; d += 32) {
+                                    const int32_t bucket = bucket_at[low + d];
+                                    float run = diagonals[warp][d];
+#pragma unroll
+                                    for (int m = 1; m < 32; m *= 2) {
+                                        const float before = __shfl_up_sync(0xFFFFFFFFu, run, m);
+                                        const int32_t its = __shfl_up_sync(0xFFFFFFFFu, bucket, m);
+                                        if (static_cast<int>(lane) >= m && its == bucket) run += before;
                                     }
+                                    const int32_t after = __shfl_down_sync(0xFFFFFFFFu, bucket, 1);
+                                    if (lane == 31 || after != bucket) by_bucket[warp][bucket] += run;
+                                    __syncwarp();
                                 }
-                                __syncwarp();
                             }
                         }
                     }
@@ -430,19 +439,22 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                 }
             }
 
-            // ---- the result
+            // ---- the next item, and this one's result
+            const int32_t x = work.next_warp();
+            QueryItem next = w;
+            if (x >= 0) {
+                next = query_item(p, x);
+                fetch_row(next);
+            }
             if (kBias && a.dtable) {
 #pragma unroll
                 for (int m = 16; m > 0; m >>= 1) {
                     far_low += __shfl_xor_sync(0xFFFFFFFFu, far_low, m);
                     far_high += __shfl_xor_sync(0xFFFFFFFFu, far_high, m);
                 }
-#pragma unroll
-                for (int m = 0; m < kMaxBuckets / 32; ++m) {
-                    const int32_t bucket = lane + 32 * m;
-                    if (bucket == a.buckets.count - 1) own[m] += far_low;
-                    if (bucket == (a.buckets.past ? a.buckets.total - 1 : 0)) own[m] += far_high;
-                    by_bucket[warp][bucket] = own[m];
+                if (lane == 0) {
+                    by_bucket[warp][a.buckets.count - 1] += far_low;
+                    by_bucket[warp][a.buckets.past ? a.buckets.total - 1 : 0] += far_high;
                 }
                 sync_threads<Team::kWorkers>(1);
                 if (threadIdx.x < a.buckets.total) {
@@ -479,8 +491,8 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
             // dq has been read before the next item's first dS is announced; and all leave together, also when a
             // wait of one of them ran out
             tmem_fence_before();
-            x = work.next_warp();
             if (!all_of<Team::kWorkers>(1, x >= 0)) break;
+            w = next;
         }
     }
     __syncthreads();
@@ -514,9 +526,10 @@ __device__ __forceinline__ KeyItem key_item(const BwdParams &p, uint32_t x)
 {
     const Attention &a = p.a;
     KeyItem w;
-    const int32_t units = a.batch * a.heads_kv, unit = x % units;  // the first keys, whose causal part is the longest, first
-    w.b = unit / a.heads_kv, w.head_kv = unit % a.heads_kv;
-    w.j0 = x / units * kRows;
+    int32_t tile, unit;
+    p.by_key_units.divide(x, tile, unit);  // the first keys, whose causal part is the longest, first
+    p.by_heads_kv.divide(unit, w.b, w.head_kv);
+    w.j0 = tile * kRows;
     w.keys = keys_of(a, w.b), w.pos0 = first_position(a, w.keys);
     const int32_t q_tiles = (a.len_q + kCols - 1) / kCols;
     const int32_t first_i = a.causal && w.j0 > w.pos0 ? w.j0 - w.pos0 : 0;  // the first query that sees any of the keys
@@ -663,16 +676,17 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
         const uint32_t mine = scores_at + lanes + chain * 2 * kCols;  // S^T, then P^T; kCols on, dP^T, then dS^T
         const int32_t reach = bias_reach(a.buckets);
         const int32_t last_start = kBias ? a.buckets.starts[a.buckets.count - 2] : 0;
-        constexpr float kUnlift = kLift<T> != 0.0f ? 1.0f / 1024.0f : 1.0f;
-        const float scale = a.mask.scale * kUnlift, to_base2 = a.scale * kLog2e;
+        const float scale = a.mask.scale * kUnlift<T>, to_base2 = a.scale * kLog2e;
         uint32_t turn = 0, use = 0, finished = 0;
-        for (int32_t x = blockIdx.x;;) {
-            const KeyItem w = key_item(p, x);
+        KeyItem w = key_item(p, blockIdx.x);
+        for (;;) {
             const int32_t j = w.j0 + r, warp_j = w.j0 + (warp % 4) * 32;
             const bool any = warp_j < w.keys;
+            int32_t head = w.head_kv * a.group, t = chain;  // tile n is tile t of a head's
 #pragma unroll 1
-            for (int32_t n = chain; n < w.tiles; n += kChains, ++turn) {
-                const int32_t head = w.head_kv * a.group + n / w.per_head, i0 = (w.begin + n % w.per_head) * kCols;
+            for (int32_t n = chain; n < w.tiles; n += kChains, t += kChains, ++turn) {
+                while (t >= w.per_head) t -= w.per_head, ++head;
+                const int32_t i0 = (w.begin + t) * kCols;
                 const float4 *tile_stats = reinterpret_cast<const float4 *>(smem + S::kStats + (use + n) % S::kStages * kCols * sizeof(float2));
                 barrier_wait(scored + 8 * chain, turn & 1u, &stalled);
                 tmem_fence_after();
@@ -687,7 +701,7 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                         uint32_t(&s)[32] = v[0], (&dp)[32] = v[1];
                         const int32_t ic = i0 + 32 * c, rel = j - w.pos0 - ic;  // to the first of 32 queries
                         const int32_t low = warp_j - w.pos0 - ic - 31, high = warp_j + 31 - w.pos0 - ic;
-                        uint32_t counter = a.first + ((static_cast<uint32_t>(w.b) * a.heads + head) * a.len_q + ic) * static_cast<uint32_t>(a.len_k) + j;
+                        const uint32_t counter = a.first + ((static_cast<uint32_t>(w.b) * a.heads + head) * a.len_q + ic) * static_cast<uint32_t>(a.len_k) + j;
                         if (kBias) {
                             const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
                             const bool far = high <= -last_start || low >= last_start;
@@ -701,18 +715,18 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                         // P = exp(S - lse), dropped for dv; dS = P (dropout(dP) - delta) for dk
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float4 st = stats[e / 2];  // two queries' lse, delta
+                            const float4 st = stats[e / 2];  // two queries' -lse, -delta
                             float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                            f = kBias ? fma2(add2(f, make_float2(-st.x, -st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>))
-                                      : fma2(f, make_float2(to_base2, to_base2), make_float2(kLift<T> - st.x, kLift<T> - st.z));
+                            f = kBias ? fma2(add2(f, make_float2(st.x, st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>))
+                                      : fma2(f, make_float2(to_base2, to_base2), make_float2(st.x, st.z));
                             const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                             float2 kept2 = prob, d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
                             if (kDrop) {
-                                const float2 k = make_float2(kept(a.mask, counter), kept(a.mask, counter + static_cast<uint32_t>(a.len_k)));
-                                counter += 2 * static_cast<uint32_t>(a.len_k);
+                                const uint32_t step = a.len_k;
+                                const float2 k = make_float2(kept(a.mask, mad_lo(e, step, counter)), kept(a.mask, mad_lo(e + 1, step, counter)));
                                 kept2 = mul2(kept2, k), d = mul2(d, k);
                             }
-                            d = mul2(fma2(d, make_float2(scale, scale), make_float2(-st.y * kUnlift, -st.w * kUnlift)), prob);
+                            d = mul2(fma2(d, make_float2(scale, scale), make_float2(st.y, st.w)), prob);
                             s[e / 2] = pack2<T>(kept2.x, kept2.y);
                             dp[e / 2] = pack2<T>(d.x, d.y);
                         }
@@ -727,7 +741,9 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
             }
             use += w.tiles;
 
-            // ---- the result: chain 0's threads write dv, chain 1's dk
+            // ---- the next item, and this one's result: chain 0's threads write dv, chain 1's dk
+            const int32_t x = work.next_warp();
+            const KeyItem next = x >= 0 ? key_item(p, x) : w;
             if (w.tiles) {
                 barrier_wait(done, finished++ & 1u, &stalled);
                 tmem_fence_after();
@@ -759,8 +775,8 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
             // dv and dk have been read before the next item's first P is announced; and all leave together, also
             // when a wait of one of them ran out
             tmem_fence_before();
-            x = work.next_warp();
             if (!all_of<Team::kWorkers>(1, x >= 0)) break;
+            w = next;
         }
     }
     __syncthreads();
@@ -819,7 +835,7 @@ template <class T, int kDim, bool kDrop, bool kBias>
 cudaError_t launch_queries(const BwdParams &p, cudaStream_t s)
 {
     const auto kernel = query_kernel<T, kDim, kDrop, kBias>;
-    const size_t bytes = 1024 + QueryShape<kDim>::kTable + (kBias ? 2 * bias_reach(p.a.buckets) * sizeof(float) : 0);
+    const size_t bytes = 1024 + QueryShape<kDim>::kTable + (kBias ? 2 * bias_reach(p.a.buckets) * (sizeof(float) + 1) : 0);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.units) * p.q_tiles), QueryShape<kDim>::Team::kThreads, bytes, s>>>(p);
@@ -876,7 +892,9 @@ cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s)
     const BwdPlan f = bwd_plan(a);
     BwdParams p{};
     p.a = a;
-    p.pack = f.pack, p.units = f.units, p.q_tiles = f.q_tiles, p.len_pad = f.len_pad;
+    p.pack = f.pack, p.pack_log = log2_of(f.pack), p.units = f.units, p.q_tiles = f.q_tiles, p.len_pad = f.len_pad;
+    p.by_units = Divider(f.units), p.by_q_tiles = Divider(f.q_tiles), p.by_packs = Divider(a.heads / f.pack);
+    p.by_group = Divider(a.group), p.by_key_units = Divider(a.batch * a.heads_kv), p.by_heads_kv = Divider(a.heads_kv);
     float *ws = static_cast<float *>(a.workspace);
     p.stats = reinterpret_cast<float2 *>(ws), p.bias = ws + f.bias, p.sums = ws + f.sums;
     const bool has_q = a.batch && a.heads && a.len_q, has_k = a.batch && a.heads_kv && a.len_k;

@@ -40,7 +40,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct FwdParams {
     CUtensorMap q, k, v;
     Attention a;
-    int32_t pack, units, q_tiles, splits, split_tiles;
+    int32_t pack, pack_log, units, q_tiles, splits, split_tiles;
+    Divider by_splits, by_units, by_q_tiles, by_packs, by_group;
     float *part;  // [splits][rows][dim padded + 2]: O, max, sum
 };
 
@@ -67,17 +68,17 @@ __device__ __forceinline__ Item item_at(const FwdParams &p, uint32_t x)
 {
     const Attention &a = p.a;
     Item w;
-    w.split = x % p.splits;
-    x /= p.splits;
-    int32_t unit, q_tile;
+    int32_t rest, unit, q_tile;
+    p.by_splits.divide(x, rest, w.split);
     if (a.causal) {  // the longest first
-        unit = x % p.units, q_tile = p.q_tiles - 1 - x / p.units;
+        p.by_units.divide(rest, q_tile, unit);
+        q_tile = p.q_tiles - 1 - q_tile;
     } else {
-        q_tile = x % p.q_tiles, unit = x / p.q_tiles;
+        p.by_q_tiles.divide(rest, unit, q_tile);
     }
-    const int32_t packs = a.heads / p.pack, rows_per = kRows / p.pack;  // positions of a tile
-    w.b = unit / packs, w.pack = unit % packs;
-    w.head0 = w.pack * p.pack, w.head_kv = w.head0 / a.group;
+    const int32_t rows_per = kRows >> p.pack_log;  // positions of a tile
+    p.by_packs.divide(unit, w.b, w.pack);
+    w.head0 = w.pack << p.pack_log, w.head_kv = p.by_group.quotient(w.head0);
     w.i0 = q_tile * (kSplitKeys ? 1 : 2) * rows_per;
     w.keys = keys_of(a, w.b), w.pos0 = first_position(a, w.keys);
     w.tile0 = w.split * p.split_tiles;
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                         for (int t = 0; t < S::kQTiles; ++t)
                             for (int c = 0; c < S::kBoxes; ++c)
                                 tma_load_5d(base + t * S::kRowsBytes + c * kRowsBox, &p.q, q_full, c * 64, 0,
-                                            w.i0 + t * (kRows / p.pack), w.pack, w.b);
+                                            w.i0 + t * (kRows >> p.pack_log), w.pack, w.b);
                     }
                 }
 #pragma unroll 1
@@ -270,10 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         float *table = reinterpret_cast<float *>(smem + S::kTable) + unit * 2 * reach;
         int32_t table_head = -1;
         uint32_t turn = 0, turns_of_other = 0, taken = 0, additions = 0, finished = 0, item = 0;
-        for (int32_t x = blockIdx.x;; ++item) {
-            const Item w = item_at<kSplitKeys>(p, x);
-            const int32_t warp_i = w.i0 + (row0 + (warp % 4) * 32) / p.pack;  // the warp's first query
-            const int32_t i = w.i0 + (row0 + r) / p.pack, head = w.head0 + r % p.pack, pos = w.pos0 + i;
+        Item w = item_at<kSplitKeys>(p, blockIdx.x);
+        for (;; ++item) {
+            const int32_t warp_i = w.i0 + ((row0 + (warp % 4) * 32) >> p.pack_log);  // the warp's first query
+            const int32_t i = w.i0 + ((row0 + r) >> p.pack_log), head = w.head0 + (r & (p.pack - 1)), pos = w.pos0 + i;
             const bool valid = i < a.len_q, any = warp_i < a.len_q;
             const int64_t index = (static_cast<int64_t>(w.b) * a.heads + head) * a.len_q + i;
             const uint32_t counter = a.first + static_cast<uint32_t>(index) * static_cast<uint32_t>(a.len_k);
@@ -407,7 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             if (any) taken += group ? 0 : (count > 0 ? count / 2 - (count - 1) / 2 : 0);
             if (any && group) taken += (count + 1) / 2 - count / 2;
 
-            // ---- the result
+            // ---- the next item, and this one's result
+            const int32_t x = work.next_warp();
+            const Item next = x >= 0 ? item_at<kSplitKeys>(p, x) : w;
             const bool two = kSplitKeys && w.tiles > 1;
             if (count) {
                 barrier_wait(done + 8 * unit, finished++ & 1u, &stalled);
@@ -489,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             // Both warpgroups have read O before the next item's first P is announced; and they leave together, also
             // when a wait of one of them ran out.
             tmem_fence_before();
-            x = work.next_warp();
             if (!all_of<kTogether>(kSplitKeys ? 1 : 2 + unit, x >= 0)) break;
+            w = next;
         }
     }
     __syncthreads();
@@ -605,6 +608,9 @@ cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s)
     FwdParams p;
     p.a = a;
     p.pack = f.pack, p.units = f.units, p.q_tiles = f.q_tiles, p.splits = f.splits, p.split_tiles = f.split_tiles;
+    p.pack_log = log2_of(f.pack);
+    p.by_splits = Divider(f.splits), p.by_units = Divider(f.units), p.by_q_tiles = Divider(f.q_tiles);
+    p.by_packs = Divider(a.heads / f.pack), p.by_group = Divider(a.group);
     p.part = static_cast<float *>(a.workspace);
     if (static_cast<int64_t>(f.units) * f.q_tiles * f.splits > 0x7FFFFFFF) return cudaErrorInvalidValue;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
