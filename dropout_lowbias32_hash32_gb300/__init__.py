@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 from . import sharding  # noqa: F401  (counter ranges for multi-process fills)
 
@@ -261,39 +262,56 @@ class AttentionArgs(C.Structure):
                 ("workspace", _p), ("workspace_bytes", _sz)]
 
 
-_codes: dict = {}  # torch dtype -> rng_dtype, made at the first use of torch
+# The same struct as bytes, which a small call fills in less time than the
+# struct's fields one by one (native alignment, as the C struct's).
+_pack_attention = struct.Struct("@7i3P9qP3q2P2if1P3if2I4P12q2PN").pack
+assert struct.calcsize("@7i3P9qP3q2P2if1P3if2I4P12q2PN") == C.sizeof(AttentionArgs)
+
+_torch = None  # torch, from the first call on (importing this package does not import it)
+_codes: dict = {}  # torch dtype -> rng_dtype
+_raw_stream = None  # device index -> the current stream's handle
 
 
-def _dtype_code(t, name: str) -> int:
-    if not _codes:
-        import torch
-        _codes.update({torch.float32: RNG_F32, torch.float16: RNG_F16, torch.bfloat16: RNG_BF16})
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _codes.update({torch.float32: RNG_F32, torch.float16: RNG_F16, torch.bfloat16: RNG_BF16})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+
+
+def _first(t, name: str) -> int:
+    """The rng_dtype of the tensor whose device and dtype the others follow."""
+    if _torch is None:
+        _load_torch()
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{name} must be a CUDA tensor")
     code = _codes.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must have dtype float32, float16 or bfloat16, not {t.dtype}")
     return code
 
 
-def _same(t, name: str, like, like_name: str, dtype=None) -> None:
-    """t lies on like's device and has its dtype (or the given one)."""
+def _same(t, name: str, like, like_name: str, dtype) -> None:
+    """t lies on like's device and has the dtype."""
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, {like_name} on {like.device}")
-    if t.dtype != (dtype or like.dtype):
-        raise TypeError(f"{name} must have dtype {dtype or like.dtype}, not {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, not {t.dtype}")
 
 
-def _row_array(t, name: str, like, like_name: str) -> tuple:
-    """(pointer, elements between rows) of a [..., cols] tensor whose leading
-    dimensions lie one row stride apart; (None, 0) for None."""
+def _rows(t, name: str, like, like_name: str) -> tuple:
+    """(pointer, elements between rows) of a [..., cols] tensor of like's shape
+    whose leading dimensions lie one row stride apart; (None, 0) for None."""
     if t is None:
         return None, 0
     if t is not like:
-        _same(t, name, like, like_name)
+        if t.dtype is not like.dtype or t.device != like.device:
+            _same(t, name, like, like_name, like.dtype)
         if t.shape != like.shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, {like_name} {tuple(like.shape)}")
-    if t.is_contiguous():
-        return t.data_ptr(), t.shape[-1]
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return t.data_ptr(), t.shape[-1]
     stride, rows = None, 1  # from the last leading dimension out
     for n, s in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
@@ -313,54 +331,66 @@ def _flat(t, name: str, n: int, like, like_name: str, dtype) -> int | None:
     """Pointer of a contiguous tensor of n elements; None for None."""
     if t is None:
         return None
-    _same(t, name, like, like_name, dtype)
+    if t.dtype is not dtype or t.device != like.device:
+        _same(t, name, like, like_name, dtype)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements")
     return t.data_ptr()
 
 
-def _cuda_rows(t, name: str) -> tuple:
-    if not getattr(t, "is_cuda", False):
-        raise TypeError(f"{name} must be a CUDA tensor")
+def _size(t, name: str) -> tuple:
+    """(rows, columns) of a [..., cols] tensor."""
     if t.dim() == 0:
         raise ValueError(f"{name} must have at least one dimension")
     cols = t.shape[-1]
     return (t.numel() // cols if cols else 0), cols
 
 
-def _param_dtype(weights, like):
+def _weight_dtype(like, *weights):
     """The weights' common dtype (the activations' when there are none)."""
     for w in weights:
         if w is not None:
-            return w.dtype, _dtype_code(w, "a weight")
-    return like.dtype, _dtype_code(like, "x")
+            if w.dtype not in _codes:
+                raise TypeError(f"a weight must have dtype float32, float16 or bfloat16, not {w.dtype}")
+            return w.dtype, _codes[w.dtype]
+    return like.dtype, _codes[like.dtype]
 
 
 def _scratch(workspace, need: int, like, stream):
-    """The caller's workspace, or one of the caching allocator's."""
+    """(pointer, bytes, tensor) of the caller's workspace, or of one of the
+    caching allocator's; (None, 0, None) where none is needed."""
     if need == 0:
         return None, 0, None
-    import torch
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = _torch.empty(need, dtype=_torch.uint8, device=like.device)
         if stream is not None:  # its memory may be reused only after that stream's work
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+            if not isinstance(stream, _torch.cuda.Stream):
+                stream = _torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
             workspace.record_stream(stream)
     elif workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _call(name: str, t, stream, *args):
-    """The entry point on t's device and stream, the stream its last argument."""
-    import torch
-    fn = getattr(_lib, name)
-    if torch.cuda.current_device() == t.device.index:
-        _check(fn(*args, _stream(stream, t)), name)
-    else:
-        with _on_device(t):
-            _check(fn(*args, _stream(stream, t)), name)
+def _handle(stream, index: int) -> int | None:
+    return (_raw_stream(index) if stream is None else int(getattr(stream, "cuda_stream", stream))) or None
+
+
+class _Current:
+    """Makes a device the current one, where it is not."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.before = _torch.cuda.current_device()
+        if self.before != self.index:
+            _torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.before != self.index:
+            _torch.cuda.set_device(self.before)
 
 
 def rng_dropout_layer_norm_fwd(x, gamma, beta, y, mean=None, rstd=None, *, bias=None, residual=None, h=None, p=0.0,
@@ -368,17 +398,23 @@ def rng_dropout_layer_norm_fwd(x, gamma, beta, y, mean=None, rstd=None, *, bias=
     """h = residual + dropout(x + bias); y = (h - mean) * rstd * gamma + beta
     over the last dimension; see rng.h.  Writes y and, where given, h, mean
     and rstd; returns y."""
-    name = "rng_dropout_layer_norm_fwd"
-    rows, cols = _cuda_rows(x, "x")
-    code = _dtype_code(x, "x")
-    wd, wcode = _param_dtype((gamma, beta, bias), x)
-    import torch
-    f32 = torch.float32
-    _call(name, x, stream, *_row_array(x, "x", x, "x"), _flat(bias, "bias", cols, x, "x", wd),
-          *_row_array(residual, "residual", x, "x"), _flat(gamma, "gamma", cols, x, "x", wd),
-          _flat(beta, "beta", cols, x, "x", wd), *_row_array(y, "y", x, "x"), *_row_array(h, "h", x, "x"),
-          _flat(mean, "mean", rows, x, "x", f32), _flat(rstd, "rstd", rows, x, "x", f32), rows, cols, code, wcode,
-          p, seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF, eps)
+    code = _first(x, "x")
+    rows, cols = _size(x, "x")
+    wd, wcode = _weight_dtype(x, gamma, beta, bias)
+    f32, index = _torch.float32, x.get_device()
+    px, sx = _rows(x, "x", x, "x")
+    pr, sr = _rows(residual, "residual", x, "x")
+    py, sy = _rows(y, "y", x, "x")
+    ph, sh = _rows(h, "h", x, "x")
+    pb = _flat(bias, "bias", cols, x, "x", wd)
+    pg, pe = _flat(gamma, "gamma", cols, x, "x", wd), _flat(beta, "beta", cols, x, "x", wd)
+    pm, ps = _flat(mean, "mean", rows, x, "x", f32), _flat(rstd, "rstd", rows, x, "x", f32)
+    with _Current(index):
+        status = _lib.rng_dropout_layer_norm_fwd(px, sx, pb, pr, sr, pg, pe, py, sy, ph, sh, pm, ps, rows, cols, code,
+                                                 wcode, p, seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF, eps,
+                                                 _handle(stream, index))
+    if status:
+        _check(status, "rng_dropout_layer_norm_fwd")
     return y
 
 
@@ -392,67 +428,88 @@ def rng_dropout_layer_norm_bwd(dy, h, gamma, mean, rstd, dx, dgamma=None, dbeta=
     """The gradient of rng_dropout_layer_norm_fwd from its h, mean and rstd;
     dh is the gradient that reaches h past the norm.  Writes dx and, where
     given, dresidual, dgamma, dbeta and dbias; returns dx."""
-    name = "rng_dropout_layer_norm_bwd"
-    rows, cols = _cuda_rows(dy, "dy")
-    code = _dtype_code(dy, "dy")
-    wd, wcode = _param_dtype((gamma, dgamma, dbeta, dbias), dy)
-    import torch
-    f32 = torch.float32
-    with _on_device(dy):
-        need = _lib.rng_dropout_layer_norm_bwd_workspace(rows, cols)
-    ws, ws_bytes, hold = _scratch(workspace, need, dy, stream)
-    _call(name, dy, stream, *_row_array(dy, "dy", dy, "dy"), *_row_array(h, "h", dy, "dy"),
-          *_row_array(dh, "dh", dy, "dy"), _flat(gamma, "gamma", cols, dy, "dy", wd),
-          _flat(mean, "mean", rows, dy, "dy", f32), _flat(rstd, "rstd", rows, dy, "dy", f32),
-          *_row_array(dx, "dx", dy, "dy"), *_row_array(dresidual, "dresidual", dy, "dy"),
-          _flat(dgamma, "dgamma", cols, dy, "dy", wd), _flat(dbeta, "dbeta", cols, dy, "dy", wd),
-          _flat(dbias, "dbias", cols, dy, "dy", wd), rows, cols, code, wcode, p, seed & 0xFFFFFFFF,
-          first_counter & 0xFFFFFFFF, ws, ws_bytes)
+    code = _first(dy, "dy")
+    rows, cols = _size(dy, "dy")
+    wd, wcode = _weight_dtype(dy, gamma, dgamma, dbeta, dbias)
+    f32, index = _torch.float32, dy.get_device()
+    py, sy = _rows(dy, "dy", dy, "dy")
+    ph, sh = _rows(h, "h", dy, "dy")
+    pd, sd = _rows(dh, "dh", dy, "dy")
+    px, sx = _rows(dx, "dx", dy, "dy")
+    pr, sr = _rows(dresidual, "dresidual", dy, "dy")
+    pg, pm = _flat(gamma, "gamma", cols, dy, "dy", wd), _flat(mean, "mean", rows, dy, "dy", f32)
+    ps, pdg = _flat(rstd, "rstd", rows, dy, "dy", f32), _flat(dgamma, "dgamma", cols, dy, "dy", wd)
+    pde, pdb = _flat(dbeta, "dbeta", cols, dy, "dy", wd), _flat(dbias, "dbias", cols, dy, "dy", wd)
+    with _Current(index):
+        ws, ws_bytes, hold = _scratch(workspace, _lib.rng_dropout_layer_norm_bwd_workspace(rows, cols), dy, stream)
+        status = _lib.rng_dropout_layer_norm_bwd(py, sy, ph, sh, pd, sd, pg, pm, ps, px, sx, pr, sr, pdg, pde, pdb,
+                                                 rows, cols, code, wcode, p, seed & 0xFFFFFFFF,
+                                                 first_counter & 0xFFFFFFFF, ws, ws_bytes, _handle(stream, index))
+    if status:
+        _check(status, "rng_dropout_layer_norm_bwd")
     del hold
     return dx
 
 
-def _heads_array(args, field: str, t, name: str, shape, like) -> None:
-    if t is not like:
-        _same(t, name, like, "q")
+def _heads(t, name: str, shape, like) -> tuple:
+    """Pointer and strides of a [batch, length, heads, head_dim] tensor."""
+    if t.dtype is not like.dtype or t.device != like.device:
+        _same(t, name, like, "q", like.dtype)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     b, l, h, d = t.stride()
     if d != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    setattr(args, field, t.data_ptr())
-    setattr(args, "do_stride" if field == "d_o" else field + "_stride", (b, l, h))
+    return t.data_ptr(), b, l, h
 
 
-def _attention_args(q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table, max_distance, bidirectional,
-                    p, seed, first_counter) -> AttentionArgs:
-    if not getattr(q, "is_cuda", False):
-        raise TypeError("q must be a CUDA tensor")
+_NO_GRADIENT = (0, 0, 0, 0)  # pointer, strides
+
+
+def _attention(name, q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table, max_distance,
+               bidirectional, p, seed, first_counter, gradients, dbias_table, workspace, stream):
+    code = _first(q, "q")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must be [batch, length, heads, head_dim]")
-    import torch
-    a = AttentionArgs()
-    a.dtype = _dtype_code(q, "q")
-    a.batch, a.len_q, a.heads_q, a.head_dim = q.shape
-    a.len_k, a.heads_kv = k.shape[1], k.shape[2]
-    keys = (q.shape[0], k.shape[1], k.shape[2], q.shape[3])
-    _heads_array(a, "q", q, "q", q.shape, q)
-    _heads_array(a, "k", k, "k", keys, q)
-    _heads_array(a, "v", v, "v", keys, q)
-    _heads_array(a, "o", o, "o", q.shape, q)
-    if lse is not None and lse.shape != (a.batch, a.heads_q, a.len_q):
+    shape = q.shape
+    batch, len_q, heads, dim = shape
+    key_shape = (batch, k.shape[1], k.shape[2], dim)
+    pq, qb, ql, qh = _heads(q, "q", shape, q)
+    pk, kb, kl, kh = _heads(k, "k", key_shape, q)
+    pv, vb, vl, vh = _heads(v, "v", key_shape, q)
+    po, ob, ol, oh = _heads(o, "o", shape, q)
+    if lse is not None and lse.shape != (batch, heads, len_q):
         raise ValueError(f"lse has shape {tuple(lse.shape)}, not [batch, heads, len_q]")
-    a.lse = _flat(lse, "lse", a.batch * a.heads_q * a.len_q, q, "q", torch.float32)
-    a.key_lengths = _flat(key_lengths, "key_lengths", a.batch, q, "q", torch.int32)
-    a.causal, a.queries_last = bool(causal), bool(queries_last)
-    a.scale = q.shape[3] ** -0.5 if scale is None else scale
+    plse = _flat(lse, "lse", batch * heads * len_q, q, "q", _torch.float32)
+    plen = _flat(key_lengths, "key_lengths", batch, q, "q", _torch.int32)
+    buckets = 0
     if bias_table is not None:
-        if bias_table.dim() != 2 or bias_table.shape[1] != a.heads_q:
+        if bias_table.dim() != 2 or bias_table.shape[1] != heads:
             raise ValueError(f"bias_table has shape {tuple(bias_table.shape)}, not [num_buckets, heads]")
-        a.bias_table = _flat(bias_table, "bias_table", bias_table.numel(), q, "q", q.dtype)
-        a.num_buckets, a.max_distance, a.bidirectional = bias_table.shape[0], max_distance, bool(bidirectional)
-    a.p, a.seed, a.first_counter = p, seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF
-    return a
+        buckets = bias_table.shape[0]
+    elif dbias_table is not None:
+        raise ValueError("dbias_table without a bias_table")
+    pt = _flat(bias_table, "bias_table", buckets * heads, q, "q", q.dtype)
+    pdt = _flat(dbias_table, "dbias_table", buckets * heads, q, "q", q.dtype)
+    do, dq, dk, dv = _NO_GRADIENT, _NO_GRADIENT, _NO_GRADIENT, _NO_GRADIENT
+    if gradients is not None:
+        do, dq = _heads(gradients[0], "do", shape, q), _heads(gradients[1], "dq", shape, q)
+        dk, dv = _heads(gradients[2], "dk", key_shape, q), _heads(gradients[3], "dv", key_shape, q)
+    fields = (code, batch, len_q, key_shape[1], heads, key_shape[2], dim, pq, pk, pv, qb, ql, qh, kb, kl, kh, vb, vl,
+              vh, po, ob, ol, oh, plse or 0, plen or 0, bool(causal), bool(queries_last),
+              dim ** -0.5 if scale is None else scale, pt or 0, buckets, max_distance if buckets else 0,
+              bool(bidirectional), p, seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF, do[0], dq[0], dk[0], dv[0],
+              *do[1:], *dq[1:], *dk[1:], *dv[1:], pdt or 0)
+    index = q.get_device()
+    with _Current(index):
+        args = _pack_attention(*fields, 0, 0)
+        ws, ws_bytes, hold = _scratch(workspace, getattr(_lib, name + "_workspace")(args), q, stream)
+        if ws_bytes:
+            args = _pack_attention(*fields, ws, ws_bytes)
+        status = getattr(_lib, name)(args, _handle(stream, index))
+    if status:
+        _check(status, name)
+    del hold
 
 
 def rng_attention_fwd_workspace(args: AttentionArgs) -> int:
@@ -465,14 +522,6 @@ def rng_attention_bwd_workspace(args: AttentionArgs) -> int:
     return _lib.rng_attention_bwd_workspace(C.byref(args))
 
 
-def _attention(name, a, like, workspace, stream):
-    with _on_device(like):
-        need = getattr(_lib, name + "_workspace")(C.byref(a))
-    a.workspace, a.workspace_bytes, hold = _scratch(workspace, need, like, stream)
-    _call(name, like, stream, C.byref(a))
-    del hold
-
-
 def rng_attention_fwd(q, k, v, o, *, lse=None, key_lengths=None, causal=False, queries_last=False, scale=None,
                       bias_table=None, max_distance=128, bidirectional=True, p=0.0, seed=0, first_counter=0,
                       workspace=None, stream=None):
@@ -481,9 +530,8 @@ def rng_attention_fwd(q, k, v, o, *, lse=None, key_lengths=None, causal=False, q
     [batch, len_k, key heads, head_dim] (any strides, the last dimension
     contiguous); scale None: head_dim ** -0.5; see rng.h.  Writes o and, where
     given, lse [batch, heads, len_q]; returns o."""
-    a = _attention_args(q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table, max_distance,
-                        bidirectional, p, seed, first_counter)
-    _attention("rng_attention_fwd", a, q, workspace, stream)
+    _attention("rng_attention_fwd", q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table,
+               max_distance, bidirectional, p, seed, first_counter, None, None, workspace, stream)
     return o
 
 
@@ -492,17 +540,8 @@ def rng_attention_bwd(do, q, k, v, o, lse, dq, dk, dv, *, dbias_table=None, key_
                       seed=0, first_counter=0, workspace=None, stream=None):
     """The gradient of rng_attention_fwd from its o and lse and the same
     options.  Writes dq, dk, dv and, where given, dbias_table; returns dq, dk, dv."""
-    a = _attention_args(q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table, max_distance,
-                        bidirectional, p, seed, first_counter)
-    _heads_array(a, "d_o", do, "do", q.shape, q)
-    _heads_array(a, "dq", dq, "dq", q.shape, q)
-    _heads_array(a, "dk", dk, "dk", k.shape, q)
-    _heads_array(a, "dv", dv, "dv", k.shape, q)
-    if dbias_table is not None:
-        if bias_table is None:
-            raise ValueError("dbias_table without a bias_table")
-        a.dbias_table = _flat(dbias_table, "dbias_table", bias_table.numel(), q, "q", q.dtype)
-    _attention("rng_attention_bwd", a, q, workspace, stream)
+    _attention("rng_attention_bwd", q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table,
+               max_distance, bidirectional, p, seed, first_counter, (do, dq, dk, dv), dbias_table, workspace, stream)
     return dq, dk, dv
 
 
