@@ -1,6 +1,7 @@
 // attention.cu -- the extern "C" entry points of attention (include/rng.h):
 // argument checks and the bucket boundaries.
 #include "attention.h"
+#include "layer_norm.h"
 
 #include <cmath>
 #include <cstring>
@@ -295,10 +296,15 @@ rng_status rng_debug_stalled_waits(uint64_t *count)
 {
     if (!count) return fail(RNG_EINVAL, "rng_debug_stalled_waits: count is NULL");
     clear_error();
-    uint64_t forward = 0, backward = 0;
-    cudaError_t e = stalled_waits_fwd(&forward);
-    if (e == cudaSuccess) e = stalled_waits_bwd(&backward);
-    *count = forward + backward;
+    cudaError_t (*const kernels[])(uint64_t *) = {stalled_waits_fwd, stalled_waits_bwd, stalled_waits_norm<float>,
+                                                  stalled_waits_norm<__half>, stalled_waits_norm<__nv_bfloat16>};
+    *count = 0;
+    cudaError_t e = cudaSuccess;
+    for (const auto kernel : kernels) {
+        uint64_t n = 0;
+        if (e == cudaSuccess) e = kernel(&n);
+        *count += n;
+    }
     return e == cudaSuccess ? RNG_OK : cuda_fail(e, "rng_debug_stalled_waits");
 }
 

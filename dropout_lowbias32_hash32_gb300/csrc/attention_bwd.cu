@@ -836,7 +836,8 @@ cudaError_t launch_queries(const BwdParams &p, cudaStream_t s)
 {
     const auto kernel = query_kernel<T, kDim, kDrop, kBias>;
     const size_t bytes = 1024 + QueryShape<kDim>::kTable + (kBias ? 2 * bias_reach(p.a.buckets) * (sizeof(float) + 1) : 0);
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    static std::atomic<bool> done[16];
+    const cudaError_t e = allow_shared(kernel, done);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.units) * p.q_tiles), QueryShape<kDim>::Team::kThreads, bytes, s>>>(p);
     note_launch();
@@ -848,7 +849,8 @@ cudaError_t launch_keys(const BwdParams &p, cudaStream_t s)
 {
     const auto kernel = key_kernel<T, kDim, kDrop, kBias>;
     const size_t bytes = 1024 + KeyShape<kDim>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    static std::atomic<bool> done[16];
+    const cudaError_t e = allow_shared(kernel, done);
     if (e != cudaSuccess) return e;
     const int64_t blocks = static_cast<int64_t>(p.a.batch) * p.a.heads_kv * ((p.a.len_k + kRows - 1) / kRows);
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;

@@ -549,10 +549,11 @@ FwdPlan fwd_plan(const Attention &a)
     f.split_keys = tiles == 1;
     f.q_tiles = f.split_keys ? 1 : (tiles + 1) / 2;
     f.splits = 1, f.split_tiles = key_tiles < 1 ? 1 : key_tiles;
-    if (f.split_keys && key_tiles > 4) {
-        // about four blocks to an SM, of four key tiles or more
+    if (f.split_keys && key_tiles > 8) {
+        // about four blocks to an SM, of eight key tiles or more (the second launch that joins them costs as much as
+        // some six tiles)
         const int64_t want = (4ll * sm_count() + f.units - 1) / f.units;
-        const int64_t most = (key_tiles + 3) / 4;
+        const int64_t most = (key_tiles + 7) / 8;
         const int64_t splits = want < most ? want : most;
         f.split_tiles = static_cast<int32_t>((key_tiles + splits - 1) / splits);
         f.splits = (key_tiles + f.split_tiles - 1) / f.split_tiles;
@@ -566,7 +567,8 @@ cudaError_t launch(const FwdParams &p, cudaStream_t s)
     using S = Shape<kDim, kSplitKeys>;
     const auto kernel = attention_fwd_kernel<T, kDim, kSplitKeys, kDrop, kBias>;
     const size_t bytes = 1024 + S::kTable + (kBias ? 4 * bias_reach(p.a.buckets) * sizeof(float) : 0);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    static std::atomic<bool> done[16];
+    const cudaError_t e = allow_shared(kernel, done);
     if (e != cudaSuccess) return e;
     kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.units) * p.q_tiles * p.splits), kThreads, bytes, s>>>(p);
     note_launch();

@@ -7,6 +7,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "hash32.cuh"
 #include "internal.h"
@@ -91,8 +92,12 @@ __device__ __forceinline__ void unpack(const Raw<T, V> &r, float (&o)[V])
 #pragma unroll
         for (int i = 0; i < V / 2; ++i) {
             if constexpr (sizeof(T) == 2) {
-                const T *h = reinterpret_cast<const T *>(&r.w[i]);
-                o[2 * i] = to_f32(h[0]), o[2 * i + 1] = to_f32(h[1]);
+                if constexpr (std::is_same<T, __nv_bfloat16>::value) {  // a bfloat16 is the high half of its f32
+                    o[2 * i] = __uint_as_float(r.w[i] << 16), o[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[i]));
+                    o[2 * i] = f.x, o[2 * i + 1] = f.y;
+                }
             }
         }
     }
@@ -116,12 +121,120 @@ __device__ __forceinline__ void store(T *p, const float (&v)[V])
     }
 }
 
+// Two f32 at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+          "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return d;
+}
+
+// The same over V elements (one by one for V = 1): d = a b + c, d = a + b.
+template <int V>
+__device__ __forceinline__ void fma_all(float (&d)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V])
+{
+    if constexpr (V == 1) {
+        d[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float2 r = fma2(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]), make_float2(c[k], c[k + 1]));
+            d[k] = r.x, d[k + 1] = r.y;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void fma_all(float (&d)[V], const float (&a)[V], float b, float c)
+{
+    if constexpr (V == 1) {
+        d[0] = fmaf(a[0], b, c);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float2 r = fma2(make_float2(a[k], a[k + 1]), make_float2(b, b), make_float2(c, c));
+            d[k] = r.x, d[k + 1] = r.y;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void fma_all(float (&d)[V], const float (&a)[V], float b, const float (&c)[V])
+{
+    if constexpr (V == 1) {
+        d[0] = fmaf(a[0], b, c[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float2 r = fma2(make_float2(a[k], a[k + 1]), make_float2(b, b), make_float2(c[k], c[k + 1]));
+            d[k] = r.x, d[k + 1] = r.y;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void add_all(float (&d)[V], const float (&a)[V], const float (&b)[V])
+{
+    if constexpr (V == 1) {
+        d[0] = a[0] + b[0];
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float2 r = add2(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]));
+            d[k] = r.x, d[k + 1] = r.y;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ void mul_all(float (&d)[V], const float (&a)[V], const float (&b)[V])
+{
+    if constexpr (V == 1) {
+        d[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+            const float2 r = mul2(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]));
+            d[k] = r.x, d[k + 1] = r.y;
+        }
+    }
+}
+
+// V weights, ones where there are none.
+template <class W, int V>
+__device__ __forceinline__ Raw<W, V> load_or_one(const void *p, uint32_t at)
+{
+    if (p) return load<false, W, V>(static_cast<const W *>(p) + at);
+    Raw<W, V> r;
+    W *w = reinterpret_cast<W *>(&r);
+#pragma unroll
+    for (int k = 0; k < V; ++k) w[k] = from_f32<W>(1.0f);
+    return r;
+}
+
 // Dropout as the layer kernels apply it: keep iff the draw's low 23 bits m
 // reach the threshold T = ceil(p 2^23); the scale 1 / (1 - p) is multiplied by
 // the caller.  threshold 0 (p = 0) keeps everything.
 //
-// The kernels are bound by the hash's logic operations (the ALU pipe takes one
-// warp instruction in two cycles), so the decision is made on the FMA pipe:
+// The attention kernels are bound by the hash's logic operations (the ALU pipe
+// takes one warp instruction in two cycles), so there the decision is made on
+// the FMA pipe (11.9 cycles a warp and scheduler for 32 decisions and products,
+// against 14.3 with a compare and a select):
 // 1 + m 2^-23 is put together from the draw by one byte permutation and one
 // logic operation, and 2^30 (1 + m 2^-23) - (2^30 + 2^7 (T - 1)) = 2^7 (m - T +
 // 1), which a multiply-add gives exactly, saturates to 1 for m >= T and to 0
@@ -137,6 +250,29 @@ inline Mask make_mask(float p, uint32_t seed)
     // keep iff m 2^-23 >= p  <=>  m >= ceil(p 2^23), exact in binary64
     const uint32_t t = static_cast<uint32_t>(std::ceil(static_cast<double>(p) * 8388608.0));
     return Mask{seed_key(seed), t, 1.0f / (1.0f - p), -(1073741824.0f + 128.0f * (static_cast<float>(t) - 1.0f))};
+}
+
+// The decision itself, for kernels that HBM bounds and whose dropped values
+// may be infinite or NaN (a product with 0 would keep those).
+__device__ __forceinline__ bool keeps(const Mask &m, uint32_t c)
+{
+    return (draw32(m.key, c) & 0x7FFFFFu) >= m.threshold;
+}
+
+// V adjacent elements dropped or scaled by 1 / (1 - p).  Their counters c, c + 1,
+// ... share the high half but for one group in 2^16 / V.
+template <int V>
+__device__ __forceinline__ void drop_all(const Mask &m, uint32_t c, float (&v)[V])
+{
+    if (V > 1 && ((c ^ (c + (V - 1u))) >> 16) == 0u) {
+        const uint32_t key = m.key ^ (c >> 16);
+#pragma unroll
+        for (uint32_t k = 0; k < V; ++k)
+            v[k] = (lowbias32::hash32_rounds((c + k) ^ key) & 0x7FFFFFu) >= m.threshold ? v[k] * m.scale : 0.0f;
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < V; ++k) v[k] = keeps(m, c + k) ? v[k] * m.scale : 0.0f;
+    }
 }
 
 // 1 for a kept element, 0 for a dropped one, from hash32 after its first

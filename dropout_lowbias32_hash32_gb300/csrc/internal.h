@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -34,6 +35,24 @@ constexpr size_t kChunk = size_t(1) << 31;
 
 // Streaming multiprocessor count of the current device (cached per device).
 unsigned sm_count();
+
+// Lets a kernel use all the dynamic shared memory that its static shared
+// memory leaves of a block's 227 KB.  `done` remembers the devices (the first
+// 16) where that is so.
+template <class Kernel>
+cudaError_t allow_shared(Kernel kernel, std::atomic<bool> (&done)[16])
+{
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess || (device < 16 && done[device].load(std::memory_order_acquire))) return e;
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(227 * 1024 - f.sharedSizeBytes));
+    if (e == cudaSuccess && device < 16) done[device].store(true, std::memory_order_release);
+    return e;
+}
 
 // Accounting of kernel launches (rng_debug_launch_count).
 void note_launch();

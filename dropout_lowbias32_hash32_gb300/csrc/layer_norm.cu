@@ -7,24 +7,31 @@
 
 namespace rngk {
 
-// The fused kernel holds 8 elements a thread, so up to 8192 columns; 1024
-// threads an SM are resident (64 registers each), all of them at work.  For
-// longer rows, chunks of rows such that about 8 blocks of 256 columns an SM
-// run.
+// The fused kernel holds 8 elements a thread, 1024 threads to an SM (64
+// registers each), the one with a ring 16, 512 to an SM (128 registers): both up
+// to 8192 columns.  Every block writes a row of partial sums, so few rows are
+// not spread over all blocks: two to a block, where that still gives every SM
+// one.  For longer rows, chunks of rows such that about 8 blocks of 256 columns
+// an SM run.
 NormBwdPlan norm_bwd_plan(size_t rows, size_t cols)
 {
     NormBwdPlan p{};
     const size_t sms = sm_count();
+    auto spread = [&](size_t groups, size_t per_sm) {  // blocks for that many groups of rows
+        const size_t blocks = groups / 2 > sms ? groups / 2 : groups < sms ? groups : sms;
+        return static_cast<unsigned>(blocks < sms * per_sm ? blocks : sms * per_sm);
+    };
+    auto per_sm = [](size_t all, size_t threads) { return static_cast<unsigned>(all / threads < 16 ? all / threads : 16); };
     if (cols <= 8192) {
         p.fused = true;
-        const size_t threads = (cols + 7) / 8;
+        const size_t threads = (cols + 7) / 8, ring = (cols + 15) / 16;
         p.group = static_cast<unsigned>(threads <= 32 ? 32 : (threads + 31) / 32 * 32);
         p.per_block = p.group == 32 ? 8 : 1;
-        size_t per_sm = 1024 / (p.group * p.per_block);
-        if (per_sm > 16) per_sm = 16;
-        const size_t need = (rows + p.per_block - 1) / p.per_block;
-        p.blocks = static_cast<unsigned>(need < sms * per_sm ? need : sms * per_sm);
-        p.workspace_floats = size_t(p.blocks) * 3 * cols;
+        p.blocks = spread((rows + p.per_block - 1) / p.per_block, per_sm(1024, p.group * p.per_block));
+        p.ring_group = static_cast<unsigned>((ring + 31) / 32 * 32);
+        p.ring_per_sm = per_sm(512, p.ring_group);
+        p.ring_blocks = spread(rows, p.ring_per_sm);
+        p.workspace_floats = size_t(p.blocks > p.ring_blocks ? p.blocks : p.ring_blocks) * 3 * cols;
     } else {
         const size_t tiles = (cols + 255) / 256;
         size_t chunks = (sms * 8 + tiles - 1) / tiles;

@@ -45,12 +45,17 @@ cudaError_t launch_norm_fwd(const NormFwd &a, bool vectors, cudaStream_t s);
 template <class T, class W>
 cudaError_t launch_norm_bwd(const NormBwd &a, bool vectors, cudaStream_t s);
 
-// How the backward pass is cut: the fused kernel's blocks (threads threads
-// share a row of cols columns, per_block rows at a time), or for long rows the
-// two-kernel form's chunks of rows.
+// Waits that ran out in the kernels for T, on the current device.
+template <class T>
+cudaError_t stalled_waits_norm(uint64_t *count);
+
+// How the backward pass is cut: the fused kernel's blocks (group threads share
+// a row of cols columns, per_block rows at a time), its form with a ring's
+// (ring_group threads to a row, ring_per_sm blocks to an SM), or for long rows
+// the two-kernel form's chunks of rows.
 struct NormBwdPlan {
     bool fused;
-    unsigned group, per_block, blocks;
+    unsigned group, per_block, blocks, ring_group, ring_per_sm, ring_blocks;
     size_t workspace_floats;
 };
 NormBwdPlan norm_bwd_plan(size_t rows, size_t cols);

@@ -6,4 +6,5 @@ template cudaError_t launch_norm_fwd<__nv_bfloat16, __nv_bfloat16>(const NormFwd
 template cudaError_t launch_norm_bwd<__nv_bfloat16, __nv_bfloat16>(const NormBwd &, bool, cudaStream_t);
 template cudaError_t launch_norm_fwd<__nv_bfloat16, float>(const NormFwd &, bool, cudaStream_t);
 template cudaError_t launch_norm_bwd<__nv_bfloat16, float>(const NormBwd &, bool, cudaStream_t);
+template cudaError_t stalled_waits_norm<__nv_bfloat16>(uint64_t *);
 }  // namespace rngk

@@ -6,4 +6,5 @@ template cudaError_t launch_norm_fwd<__half, __half>(const NormFwd &, bool, cuda
 template cudaError_t launch_norm_bwd<__half, __half>(const NormBwd &, bool, cudaStream_t);
 template cudaError_t launch_norm_fwd<__half, float>(const NormFwd &, bool, cudaStream_t);
 template cudaError_t launch_norm_bwd<__half, float>(const NormBwd &, bool, cudaStream_t);
+template cudaError_t stalled_waits_norm<__half>(uint64_t *);
 }  // namespace rngk

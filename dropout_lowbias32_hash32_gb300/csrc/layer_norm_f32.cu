@@ -4,4 +4,5 @@
 namespace rngk {
 template cudaError_t launch_norm_fwd<float, float>(const NormFwd &, bool, cudaStream_t);
 template cudaError_t launch_norm_bwd<float, float>(const NormBwd &, bool, cudaStream_t);
+template cudaError_t stalled_waits_norm<float>(uint64_t *);
 }  // namespace rngk

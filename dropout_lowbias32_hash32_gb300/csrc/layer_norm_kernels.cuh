@@ -9,6 +9,7 @@
 // between its reductions; the mask is redrawn from the element's flat index.
 #pragma once
 
+#include "barrier.cuh"
 #include "layer_norm.h"
 
 namespace rngk {
@@ -61,18 +62,13 @@ __device__ __forceinline__ void hidden(const NormFwd &a, const Raw<T, V> &x, con
     if (a.bias) {
         float b[V];
         unpack<W, V>(load<false, W, V>(static_cast<const W *>(a.bias) + col), b);
-#pragma unroll
-        for (int k = 0; k < V; ++k) h[k] += b[k];
+        add_all<V>(h, h, b);
     }
-    if (a.mask.threshold) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) h[k] = kept(a.mask, c + k) != 0.0f ? h[k] * a.mask.scale : 0.0f;
-    }
+    if (a.mask.threshold) drop_all<V>(a.mask, c, h);
     if (a.residual.p) {
         float r[V];
         unpack<T, V>(res, r);
-#pragma unroll
-        for (int k = 0; k < V; ++k) h[k] += r[k];
+        add_all<V>(h, h, r);
     }
 }
 
@@ -81,31 +77,81 @@ template <class W, int V>
 __device__ __forceinline__ void normalised(const NormFwd &a, const float (&h)[V], float mean, float rstd, uint32_t col,
                                            float (&y)[V])
 {
+    // h rstd - mean rstd would cancel where the mean is far above the deviations: the difference first
+    fma_all<V>(y, h, 1.0f, -mean);
+    float g[V];
+    unpack<W, V>(load_or_one<W, V>(a.gamma, col), g);
 #pragma unroll
-    for (int k = 0; k < V; ++k) y[k] = (h[k] - mean) * rstd;
-    if (a.gamma) {
-        float g[V];
-        unpack<W, V>(load<false, W, V>(static_cast<const W *>(a.gamma) + col), g);
-#pragma unroll
-        for (int k = 0; k < V; ++k) y[k] *= g[k];
-    }
+    for (int k = 0; k < V; ++k) g[k] *= rstd;
     if (a.beta) {
         float b[V];
         unpack<W, V>(load<false, W, V>(static_cast<const W *>(a.beta) + col), b);
-#pragma unroll
-        for (int k = 0; k < V; ++k) y[k] += b[k];
+        fma_all<V>(y, y, g, b);
+    } else {
+        mul_all<V>(y, y, g);
     }
 }
 
+// Mean and sum of squared deviations of a row of n elements, of which the
+// thread has e[0 .. count).  A warp takes both over its own elements, the
+// deviations from its own mean, in two rounds of shuffles; the block's warps
+// are then joined with one barrier: with m the mean of the whole, a part of n_w
+// elements contributes n_w (m_w - m)^2 to the deviations beside its own sum.
+struct Moments {
+    float mean, deviations;
+};
+template <bool kWarp, int V, int P>
+__device__ __forceinline__ Moments row_moments(const float (&h)[P][V], uint32_t vectors, float2 *scratch)
+{
+    const uint32_t group = blockDim.x, t = threadIdx.x;
+    auto share = [&](uint32_t warp) {  // elements of a warp of the row's
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint32_t first = 32u * warp + i * group;
+            n += first < vectors ? min(vectors - first, 32u) : 0u;
+        }
+        return static_cast<float>(n * V);
+    };
+    auto warp_sum = [](float v) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+        return v;
+    };
+    const uint32_t warp = kWarp ? 0u : t / 32u;
+    const float mine = share(warp);
+    float sum = 0.0f, squares = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (t + i * group < vectors)
+#pragma unroll
+            for (int k = 0; k < V; ++k) sum += h[i][k];
+    Moments m;
+    m.mean = mine > 0.0f ? warp_sum(sum) / mine : 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (t + i * group < vectors)
+#pragma unroll
+            for (int k = 0; k < V; ++k) squares += (h[i][k] - m.mean) * (h[i][k] - m.mean);
+    m.deviations = warp_sum(squares);
+    if constexpr (!kWarp) {
+        const uint32_t lane = t % 32u;
+        if (lane == 0) scratch[warp] = make_float2(m.mean, m.deviations);
+        __syncthreads();
+        const float n = lane < group / 32u ? share(lane) : 0.0f;
+        const float2 part = n > 0.0f ? scratch[lane] : make_float2(0.0f, 0.0f);
+        m.mean = warp_sum(n * part.x) / static_cast<float>(vectors * V);
+        m.deviations = warp_sum(part.y + n * (part.x - m.mean) * (part.x - m.mean));
+    }
+    return m;
+}
+
 // Rows held in registers: blockDim.x threads share a row (kWarp: a warp, and
-// blockDim.y rows to a block), each with P vectors of V elements.  The
-// variance is taken of the deviations from the mean, in a second reduction
-// over the same registers.
+// blockDim.y rows to a block), each with P vectors of V elements.
 template <class T, class W, int V, int P, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_fwd_kernel(const __grid_constant__ NormFwd a)
 {
-    __shared__ float scratch[kWarp ? 1 : 64];
-    uint32_t phase = 0;
+    __shared__ float2 scratch[32];
     const size_t row = static_cast<size_t>(blockIdx.x) * blockDim.y + threadIdx.y;
     if (kWarp && row >= a.rows) return;
     const uint32_t group = blockDim.x, vectors = a.cols / V, t = threadIdx.x;
@@ -125,28 +171,13 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_fwd_kernel(const __gr
         }
     }
     float h[P][V];
-    float sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const uint32_t v = t + i * group;
-        if (v < vectors) {
-            hidden<T, W, V>(a, x[i], res[i], v * V, c0 + v * V, h[i]);
-#pragma unroll
-            for (int k = 0; k < V; ++k) sum[0] += h[i][k];
-        }
+        if (v < vectors) hidden<T, W, V>(a, x[i], res[i], v * V, c0 + v * V, h[i]);
     }
-    row_sum<kWarp, 1>(sum, scratch, phase);
-    const float mean = sum[0] / static_cast<float>(a.cols);
-    float square[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        if (t + i * group < vectors) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) square[0] += (h[i][k] - mean) * (h[i][k] - mean);
-        }
-    }
-    row_sum<kWarp, 1>(square, scratch, phase);
-    const float rstd = 1.0f / sqrtf(square[0] / static_cast<float>(a.cols) + a.eps);
+    const Moments m = row_moments<kWarp, V, P>(h, vectors, scratch);
+    const float mean = m.mean, rstd = 1.0f / sqrtf(m.deviations / static_cast<float>(a.cols) + a.eps);
     if (t == 0) {
         if (a.mean) a.mean[row] = mean;
         if (a.rstd) a.rstd[row] = rstd;
@@ -214,6 +245,9 @@ constexpr int kBwdElems = 8;  // elements of a row in one thread's registers
 // the threads' registers over the walk, so dy, h and dh are read once; a block
 // writes one row of partial sums, which column_sum_kernel adds up in a fixed
 // order.
+constexpr uint32_t kRingStages = 8;
+constexpr int kRingElems = 16;
+
 template <class T, class W, int V, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_bwd_kernel(const __grid_constant__ NormBwd a)
 {
@@ -274,11 +308,7 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_bwd_kernel(const __gr
                     for (int k = 0; k < V; ++k) dz[k] += d[k];
                 }
                 if (a.dresidual.p) store<T, V>(row_of<T>(a.dresidual, row) + v * V, dz);
-                if (a.mask.threshold) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        dz[k] = kept(a.mask, c0 + v * V + k) != 0.0f ? dz[k] * a.mask.scale : 0.0f;
-                }
+                if (a.mask.threshold) drop_all<V>(a.mask, c0 + v * V, dz);
 #pragma unroll
                 for (int k = 0; k < V; ++k) dbias[i][k] += dz[k];
                 store<T, V>(row_of<T>(a.dx, row) + v * V, dz);
@@ -314,6 +344,128 @@ __global__ void __launch_bounds__(kWarp ? 256 : 1024) norm_bwd_kernel(const __gr
     put(dgamma, part);
     put(dbeta, part + a.cols);
     put(dbias, part + 2u * a.cols);
+}
+
+// The same for rows of whole 16-byte vectors that a block shares: rows to come
+// are copied to a ring in shared memory by bulk copies, so that the loads of
+// some rows are under way behind the reduction of one (a row's own loads,
+// then its barrier, then its stores left HBM idle).  Sixteen elements to a thread:
+// a thread's share of the reduction and the addresses costs as much as ten.
+template <class T, class W, int V>
+__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const __grid_constant__ NormBwd a, uint32_t stages)
+{
+    constexpr int P = kRingElems / V;
+    extern __shared__ uint4 ring[];  // [stages][dy, h, dh]
+    __shared__ alignas(8) uint64_t bars[kRingStages];
+    __shared__ float scratch[128];
+    __shared__ volatile uint32_t stalled;
+    uint32_t phase = 0;
+    const uint32_t group = blockDim.x, vectors = a.cols / V, t = threadIdx.x, full = smem_address(bars);
+    const uint32_t row_bytes = a.cols * sizeof(T), arrays = a.dh.p ? 3u : 2u, stage_bytes = arrays * row_bytes;
+    const float inv = 1.0f / static_cast<float>(a.cols);
+    auto fetch = [&](uint32_t n, uint32_t stage) {  // the block's n-th row, by one thread
+        const size_t row = blockIdx.x + static_cast<size_t>(n) * gridDim.x;
+        if (row >= a.rows || stalled) return;
+        const uint32_t bar = full + 8 * stage, dst = smem_address(ring) + stage * stage_bytes;
+        barrier_expect(bar, stage_bytes);
+        bulk_load(dst, row_of<T>(a.dy, row), row_bytes, bar);
+        bulk_load(dst + row_bytes, row_of<T>(a.h, row), row_bytes, bar);
+        if (a.dh.p) bulk_load(dst + 2 * row_bytes, row_of<T>(a.dh, row), row_bytes, bar);
+    };
+    if (t == 0) {
+        stalled = 0;
+        for (uint32_t s = 0; s < stages; ++s) barrier_init(full + 8 * s, 1);
+        fence_barrier_init();
+        for (uint32_t s = 0; s < stages; ++s) fetch(s, s);
+    }
+    Raw<W, V> gamma[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        if (t + i * group < vectors) gamma[i] = load_or_one<W, V>(a.gamma, (t + i * group) * V);
+    float dgamma[P][V] = {}, dbeta[P][V] = {}, dbias[P][V] = {};
+    __syncthreads();
+
+    size_t row = blockIdx.x;
+    float mean = a.mean[row], rstd = a.rstd[row];
+    uint32_t stage = 0, parity = 0;
+    for (uint32_t n = 0; row < a.rows; ++n) {
+        const size_t next_row = row + gridDim.x;
+        const size_t peek = next_row < a.rows ? next_row : row;
+        const float next_mean = a.mean[peek], next_rstd = a.rstd[peek];
+        barrier_wait_one(full + 8 * stage, parity, &stalled);
+        const T *in = reinterpret_cast<const T *>(reinterpret_cast<const uint8_t *>(ring) + stage * stage_bytes);
+        // dy, dy gamma and (h - mean) rstd of a vector
+        auto inputs = [&](int i, uint32_t v, float (&dy)[V], float (&g)[V], float (&x)[V]) {
+            unpack<T, V>(load<false, T, V>(in + v * V), dy);
+            unpack<T, V>(load<false, T, V>(in + a.cols + v * V), x);
+            unpack<W, V>(gamma[i], g);
+            fma_all<V>(x, x, 1.0f, -mean);
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[k] *= rstd;
+            mul_all<V>(g, g, dy);
+        };
+        float part0[V] = {}, part1[V] = {};
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint32_t v = t + i * group;
+            if (v < vectors) {
+                float dy[V], g[V], x[V];
+                inputs(i, v, dy, g, x);
+                fma_all<V>(dgamma[i], dy, x, dgamma[i]);
+                add_all<V>(dbeta[i], dbeta[i], dy);
+                add_all<V>(part0, part0, g);
+                fma_all<V>(part1, g, x, part1);
+            }
+        }
+        float sums[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < V; ++k) sums[0] += part0[k], sums[1] += part1[k];
+        row_sum<false, 2>(sums, scratch, phase);
+        // every thread has left the previous row behind
+        if (t == 0 && n > 0) fence_async_shared(), fetch(n - 1 + stages, stage ? stage - 1 : stages - 1);
+        const float m0 = sums[0] * inv, m1 = sums[1] * inv;
+        const uint32_t c0 = a.first + static_cast<uint32_t>(row) * a.cols;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const uint32_t v = t + i * group;
+            if (v < vectors) {
+                float dy[V], g[V], x[V], dz[V];
+                inputs(i, v, dy, g, x);
+                fma_all<V>(g, x, -m1, g);
+                fma_all<V>(dz, g, 1.0f, -m0);
+                if (a.dh.p) {
+                    float d[V];
+                    unpack<T, V>(load<false, T, V>(in + 2 * a.cols + v * V), d);
+                    fma_all<V>(dz, dz, rstd, d);
+                } else {
+                    fma_all<V>(dz, dz, rstd, 0.0f);
+                }
+                if (a.dresidual.p) store<T, V>(row_of<T>(a.dresidual, row) + v * V, dz);
+                if (a.mask.threshold) drop_all<V>(a.mask, c0 + v * V, dz);
+                add_all<V>(dbias[i], dbias[i], dz);
+                store<T, V>(row_of<T>(a.dx, row) + v * V, dz);
+            }
+        }
+        row = next_row, mean = next_mean, rstd = next_rstd;
+        if (++stage == stages) stage = 0, parity ^= 1u;
+    }
+    if (stalled && t == 0)  // nothing may land after the block has ended
+        for (uint32_t s = 0; s < stages; ++s) barrier_drain(full + 8 * s, 0), barrier_drain(full + 8 * s, 1);
+
+    float *part = a.workspace + static_cast<size_t>(blockIdx.x) * 3u * a.cols;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const uint32_t v = t + i * group;
+        if (v < vectors) {
+#pragma unroll
+            for (int k = 0; k < V; k += 4) {
+                float *out = part + v * V + k;
+                *reinterpret_cast<float4 *>(out) = make_float4(dgamma[i][k], dgamma[i][k + 1], dgamma[i][k + 2], dgamma[i][k + 3]);
+                *reinterpret_cast<float4 *>(out + a.cols) = make_float4(dbeta[i][k], dbeta[i][k + 1], dbeta[i][k + 2], dbeta[i][k + 3]);
+                *reinterpret_cast<float4 *>(out + 2 * a.cols) = make_float4(dbias[i][k], dbias[i][k + 1], dbias[i][k + 2], dbias[i][k + 3]);
+            }
+        }
+    }
 }
 
 // Rows too long for the fused kernel, first half: the two means of every row.
@@ -355,7 +507,7 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(const __grid_cons
         if (a.dh.p) dz += to_f32(row_of<T>(a.dh, row)[j]);
         if (a.dresidual.p) row_of<T>(a.dresidual, row)[j] = from_f32<T>(dz);
         if (a.mask.threshold)
-            dz = kept(a.mask, a.first + static_cast<uint32_t>(row) * a.cols + j) != 0.0f ? dz * a.mask.scale : 0.0f;
+            dz = keeps(a.mask, a.first + static_cast<uint32_t>(row) * a.cols + j) ? dz * a.mask.scale : 0.0f;
         row_of<T>(a.dx, row)[j] = from_f32<T>(dz);
         dgamma += dy * n, dbeta += dy, dbias += dz;
     }
@@ -376,6 +528,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, uin
     const uint32_t j = blockIdx.x * 32u + threadIdx.x;
     float s = 0.0f;
     if (j < cols)
+#pragma unroll 8
         for (uint32_t b = threadIdx.y; b < blocks; b += 32u)
             s += part[(static_cast<size_t>(b) * 3u + blockIdx.y) * cols + j];
     sums[threadIdx.y][threadIdx.x] = s;
@@ -414,15 +567,22 @@ void launch_column_sum(const NormBwd &a, const float *part, unsigned blocks, cud
 
 }  // namespace
 
+template <class T>
+cudaError_t stalled_waits_norm(uint64_t *count)
+{
+    return cudaMemcpyFromSymbol(count, g_stalled_waits, sizeof(uint64_t));
+}
+
 template <class T, class W>
 cudaError_t launch_norm_fwd(const NormFwd &a, bool vectors, cudaStream_t s)
 {
     constexpr int V = 16 / sizeof(T);
-    if (vectors && a.cols <= 1024u * V) {
-        if (a.cols <= 128u * V)
-            fwd_in_registers<T, W, V, 1>(a, s);
-        else
-            fwd_in_registers<T, W, V, 2>(a, s);
+    // Four vectors to a thread: the reductions' shuffles and the addresses cost a thread as much as ten of its elements
+    // (16384 x 4096 in bf16: 94 us, 100 with two, 124 with one).  Up to 128 vectors, a warp holds a row, with no barrier.
+    if (vectors && a.cols <= 32u * V) {
+        fwd_in_registers<T, W, V, 1>(a, s);
+    } else if (vectors && a.cols <= 64u * V) {
+        fwd_in_registers<T, W, V, 2>(a, s);
     } else if (vectors && a.cols <= 4096u * V) {
         fwd_in_registers<T, W, V, 4>(a, s);
     } else if (!vectors && a.cols <= 4096u) {
@@ -443,20 +603,32 @@ cudaError_t launch_norm_bwd(const NormBwd &a, bool vectors, cudaStream_t s)
     const NormBwdPlan plan = norm_bwd_plan(a.rows, a.cols);
     const bool weights = a.dgamma || a.dbeta || a.dbias;
     if (plan.fused) {
+        unsigned blocks = plan.blocks;
         const dim3 block(plan.group, plan.per_block);
         const bool warp = plan.group == 32u;
         if (plan.blocks) {
-            if (vectors && warp)
+            if (vectors && warp) {
                 norm_bwd_kernel<T, W, V, true><<<plan.blocks, block, 0, s>>>(a);
-            else if (vectors)
-                norm_bwd_kernel<T, W, V, false><<<plan.blocks, block, 0, s>>>(a);
-            else if (warp)
+            } else if (vectors) {
+                blocks = plan.ring_blocks;
+                const auto kernel = norm_bwd_ring_kernel<T, W, V>;
+                static std::atomic<bool> done[16];
+                if (const cudaError_t e = allow_shared(kernel, done)) return e;
+                // the block's part of the SM's shared memory, and no more stages than rows
+                const size_t stage = (a.dh.p ? 3u : 2u) * a.cols * sizeof(T), room = (226u * 1024u) / plan.ring_per_sm - 2048u;
+                const size_t rows = (a.rows + blocks - 1) / blocks;
+                size_t stages = room / stage < kRingStages ? room / stage : kRingStages;
+                if (stages > rows) stages = rows;
+                if (stages < 2) stages = 2;
+                kernel<<<blocks, plan.ring_group, stages * stage, s>>>(a, static_cast<uint32_t>(stages));
+            } else if (warp) {
                 norm_bwd_kernel<T, W, 1, true><<<plan.blocks, block, 0, s>>>(a);
-            else
+            } else {
                 norm_bwd_kernel<T, W, 1, false><<<plan.blocks, block, 0, s>>>(a);
+            }
             note_launch();
         }
-        if (weights) launch_column_sum<T, W>(a, a.workspace, plan.blocks, s);
+        if (weights) launch_column_sum<T, W>(a, a.workspace, blocks, s);
     } else {
         if (plan.blocks) {
             norm_bwd_means_kernel<T, W><<<static_cast<unsigned>(a.rows), 1024, 0, s>>>(a);

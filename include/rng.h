@@ -431,7 +431,7 @@ uint64_t rng_debug_launch_count(void);
  * chosen inputs; which outside 0 .. 4 is RNG_EINVAL. */
 rng_status rng_debug_eval_f64(int which, const double *in, double *out, size_t n, void *stream);
 
-/* Number of waits inside the attention kernels that ran out on the current
+/* Number of waits inside the layer kernels (attention, layer norm) that ran out on the current
  * device since the library was loaded.  Every wait of theirs (for a tile, for
  * a product) ends after about two seconds at most, so that a fault of theirs
  * never holds the GPU; a count above 0 says that outputs are not to be
