@@ -205,6 +205,36 @@ def test_new_tokens_against_a_cache(torch, rng, orc, group, lq, lk, b, dtype, d)
     r.check_forward(*r.forward())
 
 
+# More work than there are SMs: every block takes several pieces, of unequal lengths, one after the other.
+MANY = {
+    "encoder": case(b=24, lq=300, lk=333, h=16, buckets=32, far=128, p=0.1),
+    "causal": case(b=12, lq=385, h=24, hk=6, d=128, causal=True, p=0.1, dtype="float16"),
+    "one_tile": case(b=64, lq=40, lk=30, h=12, d=40, dtype="float16", buckets=20, p=0.2),
+    "odd_tiles": case(b=40, lq=130, lk=129, h=8, hk=4, d=128),
+    "ragged": case(b=40, lq=150, lk=260, h=16, hk=8, lengths=[0, 260, 1, 64, 65, 128, 200, 7] * 5, causal=True, p=0.1),
+    "ragged_bias": case(b=30, lq=70, lk=500, h=12, d=96, lengths=[500, 3, 0, 450, 129] * 6, causal=True, last=True,
+                        buckets=32, dtype="float16"),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", MANY)
+def test_many_heads(torch, rng, orc, name):
+    Run(torch, rng, orc, MANY[name]).check()
+    assert rng.rng_debug_stalled_waits() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("b,h,hk,lk,d,dtype", ((64, 16, 16, 1100, 128, "bfloat16"), (80, 32, 8, 1301, 64, "float16"),
+                                               (200, 8, 2, 577, 128, "float16"), (7, 8, 4, 20000, 128, "bfloat16"),
+                                               (300, 4, 4, 100, 64, "bfloat16")))
+def test_many_new_tokens_against_a_cache(torch, rng, orc, b, h, hk, lk, d, dtype):
+    lengths = [[lk, max(1, lk // 3), 0, 7, lk - 1, lk // 2][i % 6] for i in range(b)]
+    r = Run(torch, rng, orc, case(b=b, lq=1, lk=lk, h=h, hk=hk, d=d, dtype=dtype, lengths=lengths, causal=True, last=True))
+    r.check_forward(*r.forward())
+    assert rng.rng_debug_stalled_waits() == 0
+
+
 @pytest.mark.gpu
 def test_layouts(torch, rng, orc):
     """[B, H, L, D] storage, one packed q, k, v array, gradients into one packed

@@ -194,6 +194,19 @@ def test_backward_of_many_rows_and_twice_the_same_bits(torch, rng, orc):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,dtype,wtype", ((9001, 256, "float32", "float32"), (5003, 520, "bfloat16", "float32"),
+                                                   (3001, 1000, "float16", "float16"), (1201, 8192, "float32", "float32"),
+                                                   (801, 8184, "bfloat16", "bfloat16"), (7001, 24, "bfloat16", "bfloat16"),
+                                                   (2001, 777, "float16", "float32")))
+def test_many_rows_a_block(torch, rng, orc, rows, cols, dtype, wtype):
+    t = make(torch, rows, cols, dtype, wtype, seed=cols)
+    check_fwd(torch, orc, t, 0.1, 3, 1, *run_fwd(torch, rng, t, 0.1, 3, 1))
+    check_bwd(torch, orc, t, 0.1, 3, 1, *run_bwd(torch, rng, t, 0.1, 3, 1))
+    t["dh"] = None
+    check_bwd(torch, orc, t, 0.0, 3, 1, *run_bwd(torch, rng, t, 0.0, 3, 1, dresidual=False))
+
+
+@pytest.mark.gpu
 def test_no_rows_give_zero_gradients(torch, rng):
     z = torch.empty(0, 48, device="cuda")
     stat = torch.empty(0, device="cuda")
