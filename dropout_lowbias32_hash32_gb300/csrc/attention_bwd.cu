@@ -62,23 +62,23 @@ struct BwdParams {
     float *bias, *sums;
 };
 
-// The bias added to 32 scaled scores whose relative positions go by step from
+// The bias added to N scaled scores whose relative positions go by step from
 // that of `at` on: from the table by relative position, or one value beyond
 // the last bucket's start on either side.
-template <int kStep>
-__device__ __forceinline__ void add_bias32(uint32_t (&s)[32], float scale, const float *table, int32_t at, bool far, float edge)
+template <int kStep, int N>
+__device__ __forceinline__ void add_bias(uint32_t (&s)[N], float scale, const float *table, int32_t at, bool far, float edge)
 {
     const float2 k2 = make_float2(scale, scale);
     if (far) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < N; e += 2) {
             const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, make_float2(edge, edge));
             s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
         }
     } else {
         const float *t = table + at;
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int e = 0; e < N; e += 2) {
             const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2,
                                   make_float2(t[kStep * e], t[kStep * (e + 1)]));
             s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
@@ -363,14 +363,13 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         const int32_t j0 = n * kCols + 32 * c;
-                        uint32_t v[2][32];  // S, then dP
-                        tmem_load32(v[0], mine + 32 * c);
-                        tmem_load32(v[1], mine + kCols + 32 * c);
-                        tmem_wait_load(v);
-                        uint32_t(&s)[32] = v[0], (&dp)[32] = v[1];
+                        uint32_t s[32], dp[32];
+                        tmem_load(s, mine + 32 * c);
+                        tmem_load(dp, mine + kCols + 32 * c);
+                        tmem_wait_load(s, dp);
                         const int32_t low = j0 - (w.pos0 + warp_i + 31), high = j0 + 31 - (w.pos0 + warp_i);
                         const bool far = high <= -last_start || low >= last_start;
-                        if (kBias) add_bias32<1>(s, a.scale, table, j0 - pos + reach, far, table[high < 0 ? 0 : 2 * reach - 1]);
+                        if (kBias) add_bias<1>(s, a.scale, table, j0 - pos + reach, far, table[high < 0 ? 0 : 2 * reach - 1]);
                         // P = exp(S - lse); dS = P (dP / (1 - p) - delta), dP dropped as P was
                         for_pairs32<kDrop>(a.mask, counter + j0, [&](uint32_t e, float2 k) {
                             float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
@@ -390,7 +389,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                         uint32_t ds[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) ds[e] = pack2<T>(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                        tmem_store16(mine + 16 * c, ds);
+                        tmem_store(mine + 16 * c, ds);
                         if (c) {
                             tmem_wait_store();
                             tmem_fence_before();
@@ -471,10 +470,10 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                 T *row = static_cast<T *>(a.dq) + w.b * a.dqs.batch + i * a.dqs.len + head * a.dqs.head;
 #pragma unroll 1
                 for (int c = 0; c < kDim / 64; ++c) {
-                    uint32_t o[1][32] = {};
+                    uint32_t o[32] = {};
                     const int col = chain * (kDim / 2) + 32 * c;
                     if (w.tiles) {
-                        tmem_load32(o[0], tmem + lanes + col);
+                        tmem_load(o, tmem + lanes + col);
                         tmem_wait_load(o);
                     }
                     if (valid) {
@@ -482,7 +481,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                         for (int e = 0; e < 32; e += 8) {
                             float eight[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) eight[k] = __uint_as_float(o[0][e + k]) * a.scale;
+                            for (int k = 0; k < 8; ++k) eight[k] = __uint_as_float(o[e + k]) * a.scale;
                             if (col + e < a.dim) store<T, 8>(row + col + e, eight);
                         }
                     }
@@ -677,6 +676,10 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
         const int32_t reach = bias_reach(a.buckets);
         const int32_t last_start = kBias ? a.buckets.starts[a.buckets.count - 2] : 0;
         const float scale = a.mask.scale * kUnlift<T>, to_base2 = a.scale * kLog2e;
+        // Columns at a time: with 104 registers a thread, 32 of S and dP spill (2 x 4096 causal queries of 16 heads of
+        // 128: 522 us with 16, 567 with 32); with 152, 16 only wait for TMEM more often (16 x 1024 of 16 heads of 64:
+        // 577 us with 32, 611 with 16).
+        constexpr int kPiece = S::kShare == 1 ? 32 : 16;
         uint32_t turn = 0, use = 0, finished = 0;
         KeyItem w = key_item(p, blockIdx.x);
         for (;;) {
@@ -692,29 +695,28 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                 tmem_fence_after();
                 if (any) {
 #pragma unroll 1
-                    for (int c = half; c < (S::kShare == 1 ? 2 : half + 1); ++c) {
-                        const float4 *stats = tile_stats + 16 * c;
-                        uint32_t v[2][32];  // S^T, then dP^T
-                        tmem_load32(v[0], mine + 32 * c);
-                        tmem_load32(v[1], mine + kCols + 32 * c);
-                        tmem_wait_load(v);
-                        uint32_t(&s)[32] = v[0], (&dp)[32] = v[1];
-                        const int32_t ic = i0 + 32 * c, rel = j - w.pos0 - ic;  // to the first of 32 queries
-                        const int32_t low = warp_j - w.pos0 - ic - 31, high = warp_j + 31 - w.pos0 - ic;
+                    for (int at = half * kCols / S::kShare; at < (half + 1) * kCols / S::kShare; at += kPiece) {
+                        const float4 *stats = tile_stats + at / 2;
+                        uint32_t s[kPiece], dp[kPiece];  // S^T, dP^T
+                        tmem_load(s, mine + at);
+                        tmem_load(dp, mine + kCols + at);
+                        tmem_wait_load(s, dp);
+                        const int32_t ic = i0 + at, rel = j - w.pos0 - ic;  // to the first of kPiece queries
+                        const int32_t low = warp_j - w.pos0 - ic - kPiece + 1, high = warp_j + 31 - w.pos0 - ic;
                         const uint32_t counter = a.first + ((static_cast<uint32_t>(w.b) * a.heads + head) * a.len_q + ic) * static_cast<uint32_t>(a.len_k) + j;
                         if (kBias) {
                             const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
                             const bool far = high <= -last_start || low >= last_start;
-                            add_bias32<-1>(s, a.scale, bias, rel + reach, far, far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f);
+                            add_bias<-1>(s, a.scale, bias, rel + reach, far, far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f);
                         }
                         if (a.causal && high > 0) {  // query ic + e sees key j from e = rel on
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < kPiece; ++e)
                                 if (e < rel) s[e] = __float_as_uint(-INFINITY);
                         }
                         // P = exp(S - lse), dropped for dv; dS = P (dropout(dP) - delta) for dk
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < kPiece; e += 2) {
                             const float4 st = stats[e / 2];  // two queries' -lse, -delta
                             float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                             f = kBias ? fma2(add2(f, make_float2(st.x, st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>))
@@ -730,8 +732,9 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                             s[e / 2] = pack2<T>(kept2.x, kept2.y);
                             dp[e / 2] = pack2<T>(d.x, d.y);
                         }
-                        tmem_store16(mine + S::kPitch * c, reinterpret_cast<const uint32_t(&)[16]>(v[0]));
-                        tmem_store16(mine + kCols + S::kPitch * c, reinterpret_cast<const uint32_t(&)[16]>(v[1]));
+                        const uint32_t to = mine + at / 32 * S::kPitch + at % 32 / 2;
+                        tmem_store(to, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(s));
+                        tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(dp));
                     }
                     tmem_wait_store();
                 }
@@ -755,10 +758,10 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                 constexpr int kParts = kDim / 32 / S::kShare;
 #pragma unroll 1
                 for (int c = 0; c < kParts; ++c) {
-                    uint32_t o[1][32] = {};
+                    uint32_t o[32] = {};
                     const int col = 32 * (half * kParts + c);
                     if (w.tiles) {
-                        tmem_load32(o[0], (chain ? dk_at : dv_at) + lanes + col);
+                        tmem_load(o, (chain ? dk_at : dv_at) + lanes + col);
                         tmem_wait_load(o);
                     }
                     if (j < a.len_k) {
@@ -766,7 +769,7 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                         for (int e = 0; e < 32; e += 8) {
                             float eight[8];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) eight[k] = j < w.keys ? __uint_as_float(o[0][e + k]) * weight : 0.0f;
+                            for (int k = 0; k < 8; ++k) eight[k] = j < w.keys ? __uint_as_float(o[e + k]) * weight : 0.0f;
                             if (col + e < a.dim) store<T, 8>(row + col + e, eight);
                         }
                     }

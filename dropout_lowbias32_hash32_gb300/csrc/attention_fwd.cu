@@ -298,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                 if (any) {
                     uint32_t s[2][32];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_load32(s[c], mine + 32 * c);
-                    tmem_wait_load(s);
+                    for (int c = 0; c < 2; ++c) tmem_load(s[c], mine + 32 * c);
+                    tmem_wait_load(s[0], s[1]);
                     if (kBias) {
                         // relative positions of the warp's pairs: beyond the last bucket's start on one side, or by the table
                         const int32_t low = j0 - (w.pos0 + warp_i + 31), high = j0 + kKeys - 1 - (w.pos0 + warp_i);
@@ -367,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
 #pragma unroll 1
                             for (int c = 0; c < kDim / 16; ++c) {
                                 uint32_t o[16];
-                                tmem_load16(o, out + 16 * c);
-                                tmem_wait_load16(o);
+                                tmem_load(o, out + 16 * c);
+                                tmem_wait_load(o);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
-                                tmem_store16(out + 16 * c, o);
+                                tmem_store(out + 16 * c, o);
                             }
                         }
                     }
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                             if (kDrop) x = mul2(x, k);
                             q[e / 2] = pack2<T>(x.x, x.y);
                         });
-                        tmem_store16(mine + 16 * c, q);
+                        tmem_store(mine + 16 * c, q);
                     }
                     sum += total.x + total.y;
                     tmem_wait_store();
@@ -448,17 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             float *hand = reinterpret_cast<float *>(smem + S::kHand) + group * 32 * kRows + r;
 #pragma unroll 1
             for (int c = 0; c < kDim / 64; ++c) {
-                uint32_t o[1][32] = {};
+                uint32_t o[32] = {};
                 const int col = group * (kDim / 2) + 32 * c;
                 if (count && any) {
-                    tmem_load32(o[0], out + col);
+                    tmem_load(o, out + col);
                     tmem_wait_load(o);
                 }
                 if (two) {  // unit 1 hands its part to unit 0
                     if (c) sync_threads<512>(1);
                     if (unit == 1 && any) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) hand[e * kRows] = __uint_as_float(o[0][e]);
+                        for (int e = 0; e < 32; ++e) hand[e * kRows] = __uint_as_float(o[e]);
                     }
                     sync_threads<512>(1);
                 }
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     float v[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        v[e] = __uint_as_float(o[0][e]);
+                        v[e] = __uint_as_float(o[e]);
                         if (two) v[e] = v[e] * weight + hand[e * kRows] * other;
                         if (sum == 0.0f) v[e] = 0.0f;  // nothing seen
                         v[e] *= scale;

@@ -156,8 +156,8 @@ __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fenc
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// 32 (or 16) adjacent columns of the warp's lanes, a lane to a thread.
-__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t address)
+// 32 (or 16, 8) adjacent columns of the warp's lanes, a lane to a thread.
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[32], uint32_t address)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -169,7 +169,7 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t address)
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(address));
 }
-__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t address)
+__device__ __forceinline__ void tmem_load(uint32_t (&r)[16], uint32_t address)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -178,33 +178,25 @@ __device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t address)
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(address));
 }
-__device__ __forceinline__ void tmem_wait_load16(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
 // Ends the warp's loads so far; the registers pass through it, so that nothing
 // that uses them moves ahead of it.
-__device__ __forceinline__ void pin32(uint32_t (&r)[32])
-{
-    asm volatile(""
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31]));
-}
 template <int N>
-__device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[N][32])
+__device__ __forceinline__ void pin(uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+        asm volatile(""
+                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]),
+                       "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]), "+r"(r[i + 12]),
+                       "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+}
+template <int... N>
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&...r)[N])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < N; ++i) pin32(r[i]);
+    (pin(r), ...);
 }
-__device__ __forceinline__ void tmem_store32(uint32_t address, const uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_store(uint32_t address, const uint32_t (&r)[32])
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -216,7 +208,7 @@ __device__ __forceinline__ void tmem_store32(uint32_t address, const uint32_t (&
           "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(address)
         : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t address, const uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_store(uint32_t address, const uint32_t (&r)[16])
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -224,6 +216,13 @@ __device__ __forceinline__ void tmem_store16(uint32_t address, const uint32_t (&
         ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
           "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(address)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_store(uint32_t address, const uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
+                 ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(address)
+                 : "memory");
 }
 
 // ---- tcgen05.mma -------------------------------------------------------------------
