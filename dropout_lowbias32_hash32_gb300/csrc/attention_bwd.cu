@@ -119,7 +119,7 @@ __device__ __forceinline__ QueryItem query_item(const BwdParams &p, uint32_t x)
     p.by_packs.divide(unit, w.b, w.pack);
     w.head0 = w.pack << p.pack_log, w.head_kv = p.by_group.quotient(w.head0);
     w.i0 = w.q_tile * rows_per;
-    w.keys = keys_of(a, w.b), w.pos0 = first_position(a, w.keys);
+    w.keys = uniform(keys_of(a, w.b)), w.pos0 = first_position(a, w.keys);
     const int32_t last = min(w.i0 + rows_per, a.len_q) - 1, end = a.causal ? min(w.keys, w.pos0 + last + 1) : w.keys;
     w.tiles = max(0, (end + kCols - 1) / kCols);
     return w;
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
     __shared__ float deltas[kChains][kRows];
     __shared__ float diagonals[kBias ? 4 * kChains : 1][64], by_bucket[kBias ? 4 * kChains : 1][kMaxBuckets];
     const Attention &a = p.a;
-    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+    const uint32_t warp = uniform(threadIdx.x / 32u), lane = threadIdx.x % 32u;
     uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
     const uint32_t base = smem_address(smem);
     float *table = reinterpret_cast<float *>(smem + S::kTable);
@@ -166,7 +166,6 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
         give_registers<Team::kOtherRegisters>();
         if (warp == Team::kTmaWarp) {
             // ---- TMA: q and do, then K_n and V_n
-            const bool one = elect_one();
             uint32_t use = 0, loaded = 0, tails = 0;
             bool fine = true;
             for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.ask_warp() : -1) {
@@ -175,7 +174,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                 if (loaded) fine = barrier_wait(q_empty, (loaded - 1) & 1u, &stalled);
                 if (!fine) break;
                 ++loaded;
-                if (one) {
+                if (elect_one()) {
                     barrier_expect(q_full, 2 * S::kRowsBytes);
                     for (int c = 0; c < S::kBoxes; ++c) {
                         tma_load_5d(base + c * kRowsBox, &p.q_rows, q_full, c * 64, 0, w.i0, w.pack, w.b);
@@ -192,7 +191,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                     // keys past n(b) that the array holds: whatever they are, dS's zeros must meet zeros
                     const bool past = j0 + kCols > w.keys && w.keys < a.len_k;
                     const uint32_t on = past ? tail : bar;
-                    if (one) {
+                    if (elect_one()) {
                         barrier_expect(on, S::kStageBytes);
                         for (int c = 0; c < S::kBoxes; ++c) {
                             tma_load_5d(dst + c * kColsBox, &p.k_cols, on, c * 64, 0, j0, w.head_kv, w.b);
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                                 *reinterpret_cast<uint4 *>(rows + c * kColsBox + o) = make_uint4(0, 0, 0, 0);
                         fence_async_shared();
                         __syncwarp();
-                        if (one) barrier_arrive(bar);
+                        if (elect_one()) barrier_arrive(bar);
                     }
                 }
             }
@@ -218,54 +217,52 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
             }
         } else if (warp == Team::kMmaWarp) {
             // ---- MMA
-            if (elect_one()) {
-                constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
-                const uint64_t qd = row_major_tile(base), dd = row_major_tile(base + S::kRowsBytes);
-                const uint64_t ring_k = row_major_tile(base + S::kRing), ring_v = row_major_tile(base + S::kRing + S::kColsBytes);
-                const uint64_t ring_kt = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kColsBox : 1024);
-                // tile counters over all items: made is kChains ahead of added within an item
-                uint32_t use_made = 0, use_added = 0, loaded = 0, turns = 0;  // turns: bit c, the parity of chain c's next dS
-                bool fine = true;
-                for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_one() : -1) {
-                    const QueryItem w = query_item(p, x);
-                    if (!w.tiles) continue;
-                    fine = barrier_wait_one(q_full, loaded++ & 1u, &stalled);
-                    uint32_t chain = 0;
+            constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
+            const uint64_t qd = row_major_tile(base), dd = row_major_tile(base + S::kRowsBytes);
+            const uint64_t ring_k = row_major_tile(base + S::kRing), ring_v = row_major_tile(base + S::kRing + S::kColsBytes);
+            const uint64_t ring_kt = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kColsBox : 1024);
+            // tile counters over all items: made is kChains ahead of added within an item
+            uint32_t use_made = 0, use_added = 0, loaded = 0, turns = 0;  // turns: bit c, the parity of chain c's next dS
+            bool fine = true;
+            for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_warp() : -1) {
+                const int32_t tiles = query_item(p, x).tiles;
+                if (!tiles) continue;
+                fine = barrier_wait(q_full, loaded++ & 1u, &stalled);
+                uint32_t chain = 0;
 #pragma unroll 1
-                    for (int32_t n = -kChains; n < w.tiles && fine; ++n) {
-                        const uint32_t at = scores_at + chain * 2 * kCols;
-                        if (n >= 0) {  // dQ += dS K
-                            const uint32_t stage = use_added++ % S::kStages;
-                            fine = barrier_wait_one(ready + 8 * chain, turns >> chain & 1u, &stalled);
-                            if (!fine) break;
-                            turns ^= 1u << chain;
-                            tmem_fence_after();
-                            const uint64_t kd = ring_kt + stage * (S::kStageBytes / 16);
+                for (int32_t n = -kChains; n < tiles && fine; ++n) {
+                    const bool add = n >= 0, make = n + kChains < tiles;
+                    const uint32_t at = scores_at + chain * 2 * kCols, stage = use_added % S::kStages, next = use_made % S::kStages;
+                    if (add) fine = barrier_wait(ready + 8 * chain, turns >> chain & 1u, &stalled);
+                    if (!fine) break;
+                    tmem_fence_after();
+                    if (add && elect_one()) {  // dQ += dS K
+                        const uint64_t kd = ring_kt + stage * (S::kStageBytes / 16);
 #pragma unroll
-                            for (int i = 0; i < kCols / 16; ++i) mma_step_tmem(tmem, at + i * 8, kd + i * (2048 / 16), kOut, n > 0 || i > 0);
-                            mma_commit(empty + 8 * stage);
-                            if (n + 1 == w.tiles) mma_commit(done);
-                        }
-                        if (n + kChains < w.tiles) {  // S = Q K^T, dP = dO V^T
-                            const uint32_t stage = use_made % S::kStages;
-                            fine = barrier_wait_one(full + 8 * stage, use_made / S::kStages & 1u, &stalled);
-                            if (!fine) break;
-                            ++use_made;
-                            tmem_fence_after();
-                            const uint64_t kd = ring_k + stage * (S::kStageBytes / 16), vd = ring_v + stage * (S::kStageBytes / 16);
-#pragma unroll
-                            for (int i = 0; i < kDim / 16; ++i) mma_step(at, qd + row_step(i, kRowsBox), kd + row_step(i, kColsBox), kScores, i > 0);
-#pragma unroll
-                            for (int i = 0; i < kDim / 16; ++i)
-                                mma_step(at + kCols, dd + row_step(i, kRowsBox), vd + row_step(i, kColsBox), kScores, i > 0);
-                            mma_commit(scored + 8 * chain);
-                            if (n + kChains + 1 == w.tiles) mma_commit(q_empty);
-                        }
-                        chain = chain + 1 == kChains ? 0 : chain + 1;
+                        for (int i = 0; i < kCols / 16; ++i) mma_step_tmem(tmem, at + i * 8, kd + i * (2048 / 16), kOut, n > 0 || i > 0);
+                        mma_commit(empty + 8 * stage);
+                        if (n + 1 == tiles) mma_commit(done);
                     }
+                    if (make) fine = barrier_wait(full + 8 * next, use_made / S::kStages & 1u, &stalled);
+                    if (!fine) break;
+                    tmem_fence_after();
+                    if (make && elect_one()) {  // S = Q K^T, dP = dO V^T
+                        const uint64_t kd = ring_k + next * (S::kStageBytes / 16), vd = ring_v + next * (S::kStageBytes / 16);
+#pragma unroll
+                        for (int i = 0; i < kDim / 16; ++i) mma_step(at, qd + row_step(i, kRowsBox), kd + row_step(i, kColsBox), kScores, i > 0);
+#pragma unroll
+                        for (int i = 0; i < kDim / 16; ++i)
+                            mma_step(at + kCols, dd + row_step(i, kRowsBox), vd + row_step(i, kColsBox), kScores, i > 0);
+                        mma_commit(scored + 8 * chain);
+                        if (n + kChains + 1 == tiles) mma_commit(q_empty);
+                    }
+                    __syncwarp();
+                    if (add) ++use_added, turns ^= 1u << chain;
+                    use_made += make;
+                    chain = chain + 1 == kChains ? 0 : chain + 1;
                 }
-                if (stalled) mma_commit(drained), barrier_drain(drained, 0);
             }
+            if (stalled && elect_one()) mma_commit(drained), barrier_drain(drained, 0);
         }
     } else {
         take_registers<Team::kWorkerRegisters>();
@@ -529,7 +526,7 @@ __device__ __forceinline__ KeyItem key_item(const BwdParams &p, uint32_t x)
     p.by_key_units.divide(x, tile, unit);  // the first keys, whose causal part is the longest, first
     p.by_heads_kv.divide(unit, w.b, w.head_kv);
     w.j0 = tile * kRows;
-    w.keys = keys_of(a, w.b), w.pos0 = first_position(a, w.keys);
+    w.keys = uniform(keys_of(a, w.b)), w.pos0 = first_position(a, w.keys);
     const int32_t q_tiles = (a.len_q + kCols - 1) / kCols;
     const int32_t first_i = a.causal && w.j0 > w.pos0 ? w.j0 - w.pos0 : 0;  // the first query that sees any of the keys
     w.begin = min(first_i / kCols, q_tiles), w.per_head = w.j0 < w.keys ? q_tiles - w.begin : 0;
@@ -549,7 +546,7 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t stalled;
     const Attention &a = p.a;
-    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+    const uint32_t warp = uniform(threadIdx.x / 32u), lane = threadIdx.x % 32u;
     uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
     const uint32_t base = smem_address(smem);
 
@@ -575,27 +572,29 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
         give_registers<Team::kOtherRegisters>();
         if (warp == Team::kTmaWarp) {
             // ---- TMA: k and v, then the queries' tiles, head by head
-            if (elect_one()) {
-                uint32_t use = 0, loaded = 0;
-                bool fine = true;
-                for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.ask_one() : -1) {
-                    const KeyItem w = key_item(p, x);
-                    if (!w.tiles) continue;
-                    if (loaded) fine = barrier_wait_one(k_empty, (loaded - 1) & 1u, &stalled);
-                    if (!fine) break;
-                    ++loaded;
+            uint32_t use = 0, loaded = 0;
+            bool fine = true;
+            for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.ask_warp() : -1) {
+                const KeyItem w = key_item(p, x);
+                if (!w.tiles) continue;
+                if (loaded) fine = barrier_wait(k_empty, (loaded - 1) & 1u, &stalled);
+                if (!fine) break;
+                ++loaded;
+                if (elect_one()) {
                     barrier_expect(k_full, 2 * S::kRowsBytes);
                     for (int c = 0; c < S::kBoxes; ++c) {
                         tma_load_5d(base + c * kRowsBox, &p.k_rows, k_full, c * 64, 0, w.j0, w.head_kv, w.b);
                         tma_load_5d(base + S::kRowsBytes + c * kRowsBox, &p.v_rows, k_full, c * 64, 0, w.j0, w.head_kv, w.b);
                     }
-                    int32_t head = w.head_kv * a.group, t = w.begin;
+                }
+                int32_t head = w.head_kv * a.group, t = w.begin;
 #pragma unroll 1
-                    for (int32_t n = 0; n < w.tiles; ++n) {
-                        const uint32_t stage = use % S::kStages, bar = full + 8 * stage, dst = base + S::kRing + stage * S::kStageBytes;
-                        fine = barrier_wait_one(empty + 8 * stage, (use / S::kStages & 1u) ^ 1u, &stalled);
-                        if (!fine) break;
-                        ++use;
+                for (int32_t n = 0; n < w.tiles; ++n) {
+                    const uint32_t stage = use % S::kStages, bar = full + 8 * stage, dst = base + S::kRing + stage * S::kStageBytes;
+                    fine = barrier_wait(empty + 8 * stage, (use / S::kStages & 1u) ^ 1u, &stalled);
+                    if (!fine) break;
+                    ++use;
+                    if (elect_one()) {
                         barrier_expect(bar, S::kStageBytes + kCols * sizeof(float2));
                         for (int c = 0; c < S::kBoxes; ++c) {
                             tma_load_5d(dst + c * kColsBox, &p.q_cols, bar, c * 64, 0, t * kCols, head, w.b);
@@ -603,68 +602,66 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                         }
                         bulk_load(base + S::kStats + stage * kCols * sizeof(float2),
                                   p.stats + (static_cast<int64_t>(w.b) * a.heads + head) * p.len_pad + t * kCols, kCols * sizeof(float2), bar);
-                        if (++t == w.begin + w.per_head) t = w.begin, ++head;
                     }
+                    if (++t == w.begin + w.per_head) t = w.begin, ++head;
                 }
-                if (stalled) {  // nothing may land after the block has ended
-                    if (loaded) barrier_drain(k_full, (loaded - 1) & 1u);
-                    for (uint32_t u = use > S::kStages ? use - S::kStages : 0; u < use; ++u)
-                        barrier_drain(full + 8 * (u % S::kStages), u / S::kStages & 1u);
-                }
+            }
+            if (stalled && elect_one()) {  // nothing may land after the block has ended
+                if (loaded) barrier_drain(k_full, (loaded - 1) & 1u);
+                for (uint32_t u = use > S::kStages ? use - S::kStages : 0; u < use; ++u)
+                    barrier_drain(full + 8 * (u % S::kStages), u / S::kStages & 1u);
             }
         } else if (warp == Team::kMmaWarp) {
             // ---- MMA
-            if (elect_one()) {
-                constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
-                const uint64_t kd = row_major_tile(base), vd = row_major_tile(base + S::kRowsBytes);
-                const uint64_t ring_q = row_major_tile(base + S::kRing), ring_do = row_major_tile(base + S::kRing + S::kColsBytes);
-                const uint64_t ring_qt = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kColsBox : 1024);
-                uint32_t use_made = 0, use_added = 0, loaded = 0, turns = 0;  // turns: bit c, the parity of chain c's next P, dS
-                bool fine = true;
-                for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_one() : -1) {
-                    const KeyItem w = key_item(p, x);
-                    if (!w.tiles) continue;
-                    fine = barrier_wait_one(k_full, loaded++ & 1u, &stalled);
-                    uint32_t chain = 0;
+            constexpr uint32_t kScores = mma_shape<T>(kCols, false), kOut = mma_shape<T>(kDim, true);
+            const uint64_t kd = row_major_tile(base), vd = row_major_tile(base + S::kRowsBytes);
+            const uint64_t ring_q = row_major_tile(base + S::kRing), ring_do = row_major_tile(base + S::kRing + S::kColsBytes);
+            const uint64_t ring_qt = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kColsBox : 1024);
+            uint32_t use_made = 0, use_added = 0, loaded = 0, turns = 0;  // turns: bit c, the parity of chain c's next P, dS
+            bool fine = true;
+            for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_warp() : -1) {
+                const int32_t tiles = key_item(p, x).tiles;
+                if (!tiles) continue;
+                fine = barrier_wait(k_full, loaded++ & 1u, &stalled);
+                uint32_t chain = 0;
 #pragma unroll 1
-                    for (int32_t n = -kChains; n < w.tiles && fine; ++n) {
-                        const uint32_t at = scores_at + chain * 2 * kCols;
-                        if (n >= 0) {  // dV += P^T dO, dK += dS^T Q
-                            const uint32_t stage = use_added++ % S::kStages;
-                            fine = barrier_wait_one(ready + 8 * chain, turns >> chain & 1u, &stalled);
-                            if (!fine) break;
-                            turns ^= 1u << chain;
-                            tmem_fence_after();
-                            const uint64_t qt = ring_qt + stage * (S::kStageBytes / 16);
+                for (int32_t n = -kChains; n < tiles && fine; ++n) {
+                    const bool add = n >= 0, make = n + kChains < tiles;
+                    const uint32_t at = scores_at + chain * 2 * kCols, stage = use_added % S::kStages, next = use_made % S::kStages;
+                    if (add) fine = barrier_wait(ready + 8 * chain, turns >> chain & 1u, &stalled);
+                    if (!fine) break;
+                    tmem_fence_after();
+                    if (add && elect_one()) {  // dV += P^T dO, dK += dS^T Q
+                        const uint64_t qt = ring_qt + stage * (S::kStageBytes / 16);
 #pragma unroll
-                            for (int i = 0; i < kCols / 16; ++i)
-                                mma_step_tmem(dv_at, at + i / 2 * S::kPitch + i % 2 * 8, qt + (S::kColsBytes + i * 2048) / 16, kOut, n > 0 || i > 0);
+                        for (int i = 0; i < kCols / 16; ++i)
+                            mma_step_tmem(dv_at, at + i / 2 * S::kPitch + i % 2 * 8, qt + (S::kColsBytes + i * 2048) / 16, kOut, n > 0 || i > 0);
 #pragma unroll
-                            for (int i = 0; i < kCols / 16; ++i)
-                                mma_step_tmem(dk_at, at + kCols + i / 2 * S::kPitch + i % 2 * 8, qt + i * 2048 / 16, kOut, n > 0 || i > 0);
-                            mma_commit(empty + 8 * stage);
-                            if (n + 1 == w.tiles) mma_commit(done);
-                        }
-                        if (n + kChains < w.tiles) {  // S^T = K Q^T, dP^T = V dO^T
-                            const uint32_t stage = use_made % S::kStages;
-                            fine = barrier_wait_one(full + 8 * stage, use_made / S::kStages & 1u, &stalled);
-                            if (!fine) break;
-                            ++use_made;
-                            tmem_fence_after();
-                            const uint64_t qd = ring_q + stage * (S::kStageBytes / 16), dd = ring_do + stage * (S::kStageBytes / 16);
-#pragma unroll
-                            for (int i = 0; i < kDim / 16; ++i) mma_step(at, kd + row_step(i, kRowsBox), qd + row_step(i, kColsBox), kScores, i > 0);
-#pragma unroll
-                            for (int i = 0; i < kDim / 16; ++i)
-                                mma_step(at + kCols, vd + row_step(i, kRowsBox), dd + row_step(i, kColsBox), kScores, i > 0);
-                            mma_commit(scored + 8 * chain);
-                            if (n + kChains + 1 == w.tiles) mma_commit(k_empty);
-                        }
-                        chain = chain + 1 == kChains ? 0 : chain + 1;
+                        for (int i = 0; i < kCols / 16; ++i)
+                            mma_step_tmem(dk_at, at + kCols + i / 2 * S::kPitch + i % 2 * 8, qt + i * 2048 / 16, kOut, n > 0 || i > 0);
+                        mma_commit(empty + 8 * stage);
+                        if (n + 1 == tiles) mma_commit(done);
                     }
+                    if (make) fine = barrier_wait(full + 8 * next, use_made / S::kStages & 1u, &stalled);
+                    if (!fine) break;
+                    tmem_fence_after();
+                    if (make && elect_one()) {  // S^T = K Q^T, dP^T = V dO^T
+                        const uint64_t qd = ring_q + next * (S::kStageBytes / 16), dd = ring_do + next * (S::kStageBytes / 16);
+#pragma unroll
+                        for (int i = 0; i < kDim / 16; ++i) mma_step(at, kd + row_step(i, kRowsBox), qd + row_step(i, kColsBox), kScores, i > 0);
+#pragma unroll
+                        for (int i = 0; i < kDim / 16; ++i)
+                            mma_step(at + kCols, vd + row_step(i, kRowsBox), dd + row_step(i, kColsBox), kScores, i > 0);
+                        mma_commit(scored + 8 * chain);
+                        if (n + kChains + 1 == tiles) mma_commit(k_empty);
+                    }
+                    __syncwarp();
+                    if (add) ++use_added, turns ^= 1u << chain;
+                    use_made += make;
+                    chain = chain + 1 == kChains ? 0 : chain + 1;
                 }
-                if (stalled) mma_commit(drained), barrier_drain(drained, 0);
             }
+            if (stalled && elect_one()) mma_commit(drained), barrier_drain(drained, 0);
         }
     } else {
         take_registers<Team::kWorkerRegisters>();

@@ -80,7 +80,7 @@ __device__ __forceinline__ Item item_at(const FwdParams &p, uint32_t x)
     p.by_packs.divide(unit, w.b, w.pack);
     w.head0 = w.pack << p.pack_log, w.head_kv = p.by_group.quotient(w.head0);
     w.i0 = q_tile * (kSplitKeys ? 1 : 2) * rows_per;
-    w.keys = keys_of(a, w.b), w.pos0 = first_position(a, w.keys);
+    w.keys = uniform(keys_of(a, w.b)), w.pos0 = first_position(a, w.keys);
     w.tile0 = w.split * p.split_tiles;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {  // key tiles of each unit (the item's, when the units share them out)
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     __shared__ float tops[2][2][kRows];                          // [unit][warpgroup][row], of its last tile
     __shared__ float last_tops[2][2][2][kRows], sums[2][2][2][kRows];  // [item's parity][unit][warpgroup][row]
     const Attention &a = p.a;
-    const uint32_t warp = threadIdx.x / 32u, lane = threadIdx.x % 32u;
+    const uint32_t warp = uniform(threadIdx.x / 32u), lane = threadIdx.x % 32u;
     uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
     const uint32_t base = smem_address(smem);
 
@@ -137,7 +137,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         give_registers<kOtherRegisters>();
         if (warp == kTmaWarp) {
             // ---- TMA: the queries, then K_0 .. K_{lead-1} and alternately V_n, K_{n+lead}
-            const bool one = elect_one();
             uint32_t use = 0, loaded = 0, tails = 0;
             bool fine = true;
             for (int32_t x = blockIdx.x; x >= 0 && fine; x = fine ? work.ask_warp() : -1) {
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     if (loaded) fine = barrier_wait(q_empty, (loaded - 1) & 1u, &stalled);
                     if (!fine) break;
                     ++loaded;
-                    if (one) {
+                    if (elect_one()) {
                         barrier_expect(q_full, S::kQTiles * S::kRowsBytes);
                         for (int t = 0; t < S::kQTiles; ++t)
                             for (int c = 0; c < S::kBoxes; ++c)
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     // tile's, which has no keys beside it)
                     const bool past = has_v && (w.tile0 + n + 1) * kKeys > w.keys && w.keys < a.len_k;
                     const uint32_t on = past ? tail : bar;
-                    if (one) {
+                    if (elect_one()) {
                         barrier_expect(on, (has_v && has_k ? 2 : 1) * S::kTileBytes);
 #pragma unroll
                         for (int c = 0; c < S::kBoxes; ++c) {
@@ -184,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                                 *reinterpret_cast<uint4 *>(rows + c * kKeysBox + o) = make_uint4(0, 0, 0, 0);
                         fence_async_shared();
                         __syncwarp();
-                        if (one) barrier_arrive(bar);
+                        if (elect_one()) barrier_arrive(bar);
                     }
                 }
             }
@@ -200,7 +199,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
             const uint64_t qd = row_major_tile(base + (kSplitKeys ? 0 : unit) * S::kRowsBytes);
             const uint64_t ring_v = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kKeysBox : 1024);
             const uint64_t ring_k = row_major_tile(base + S::kRing + S::kTileBytes);
-            const bool one = elect_one();
             uint32_t use = 0, given = 0, loaded = 0;  // given: bit g, the parity of warpgroup g's next P
             bool fine = true;
             for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.next_warp() : -1) {
@@ -226,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     }
                     if (!fine) break;
                     tmem_fence_after();
-                    if (one) {
+                    if (elect_one()) {
                         if (v_mine) {
                             const uint64_t vd = ring_v + stage * (S::kStageBytes / 16);
 #pragma unroll
@@ -249,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     }
                     scored_any = scored_any || k_mine;
                 }
-                if (!scored_any && one) barrier_arrive(q_empty);
+                if (!scored_any && elect_one()) barrier_arrive(q_empty);
                 use += w.tiles + lead;
             }
-            if (stalled && one) mma_commit(drained + 8 * unit), barrier_drain(drained + 8 * unit, 0);
+            if (stalled && elect_one()) mma_commit(drained + 8 * unit), barrier_drain(drained + 8 * unit, 0);
         }
     } else {
         take_registers<kUnitRegisters>();
@@ -265,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
         const uint32_t out = tmem + unit * 256 + lanes + 2 * kKeys;
         const uint32_t pass = passed + 8 * (4 * chain + warp % 4), take = passed + 8 * (4 * (chain ^ 1) + warp % 4);
         const int32_t row0 = (kSplitKeys ? 0 : unit * kRows);
-                // scores are held before or, with a bias, after their scaling; base two is for the exponential
+        // scores are held before or, with a bias, after their scaling; base two is for the exponential
         const float to_base2 = kBias ? kLog2e : a.scale * kLog2e;
         const int32_t reach = kBias ? bias_reach(a.buckets) : 0;
         float *table = reinterpret_cast<float *>(smem + S::kTable) + unit * 2 * reach;

@@ -21,6 +21,14 @@ __device__ __forceinline__ bool elect_one()
     return yes != 0;
 }
 
+// A value that all lanes of the warp have, for the compiler to know it: what
+// follows from it is computed once a warp.
+template <class T>
+__device__ __forceinline__ T uniform(T v)
+{
+    return __shfl_sync(0xFFFFFFFFu, v, 0);
+}
+
 // ---- TMA ------------------------------------------------------------------------
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
@@ -81,7 +89,7 @@ struct WorkQueue {
         fence_async_shared();
         __syncwarp();
         if (elect_one()) barrier_arrive(heard);
-        return next;
+        return uniform(next);
     }
     __device__ __forceinline__ int32_t next_one()
     {
