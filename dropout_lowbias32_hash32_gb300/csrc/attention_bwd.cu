@@ -62,10 +62,10 @@ struct BwdParams {
     float *bias, *sums;
 };
 
-// The bias added to N scaled scores whose relative positions go by step from
-// that of `at` on: from the table by relative position, or one value beyond
-// the last bucket's start on either side.
-template <int kStep, int N>
+// The bias added to N scaled scores whose relative positions descend from that
+// of `at`: from the table by relative position, or one value beyond the last
+// bucket's start on either side.
+template <int N>
 __device__ __forceinline__ void add_bias(uint32_t (&s)[N], float scale, const float *table, int32_t at, bool far, float edge)
 {
     const float2 k2 = make_float2(scale, scale);
@@ -79,8 +79,7 @@ __device__ __forceinline__ void add_bias(uint32_t (&s)[N], float scale, const fl
         const float *t = table + at;
 #pragma unroll
         for (int e = 0; e < N; e += 2) {
-            const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2,
-                                  make_float2(t[kStep * e], t[kStep * (e + 1)]));
+            const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, make_float2(t[-e], t[-e - 1]));
             s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
         }
     }
@@ -344,9 +343,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                 for (int32_t t = threadIdx.x; t < 2 * reach; t += Team::kWorkers)
                     p.bias[static_cast<int64_t>(w.head0) * 2 * reach + t] = table[t];
 
-            const float2 minus = make_float2(-delta, -delta), l2 = make_float2(-lse, -lse);
-            const float to_base2 = kBias ? kLog2e : a.scale * kLog2e;
-            const float2 b2 = make_float2(to_base2, to_base2);
+            const float2 minus = make_float2(-delta, -delta);
             float far_low = 0.0f, far_high = 0.0f;
             if (kBias && a.dtable) {
                 for (uint32_t m = lane; m < kMaxBuckets; m += 32) by_bucket[warp][m] = 0.0f;
@@ -366,11 +363,28 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                         tmem_wait_load(s, dp);
                         const int32_t low = j0 - (w.pos0 + warp_i + 31), high = j0 + 31 - (w.pos0 + warp_i);
                         const bool far = high <= -last_start || low >= last_start;
-                        if (kBias) add_bias<1>(s, a.scale, table, j0 - pos + reach, far, table[high < 0 ? 0 : 2 * reach - 1]);
+                        // the exponential's argument in base two is s by + at: of the score, with one bias for all pairs,
+                        // or of what has become of it.  A bias as large as a type's lowest value leaves nothing of s.
+                        float by = a.scale * kLog2e, at = -lse;
+                        if (kBias && far) {
+                            const float edge = table[high < 0 ? 0 : 2 * reach - 1];
+                            by = fabsf(edge) < 0x1p100f ? by : 0.0f, at = (edge - lse) * kLog2e;
+                        } else if (kBias) {
+                            by = 1.0f, at = 0.0f;
+                            const float *t = table + (j0 - pos + reach);
+                            const float2 scale = make_float2(a.scale, a.scale), from = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                                f = mul2(add2(fma2(f, scale, make_float2(t[e], t[e + 1])), from), b2);
+                                s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
+                            }
+                        }
+                        const float2 by2 = make_float2(by, by), at2 = make_float2(at, at);
                         // P = exp(S - lse); dS = P (dP / (1 - p) - delta), dP dropped as P was
                         for_pairs32<kDrop>(a.mask, counter + j0, [&](uint32_t e, float2 k) {
                             float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                            f = kBias ? mul2(add2(f, l2), b2) : fma2(f, b2, l2);
+                            f = fma2(f, by2, at2);
                             const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                             float2 d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
                             if (kDrop) d = mul2(d, k);
@@ -704,7 +718,7 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                         if (kBias) {
                             const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
                             const bool far = high <= -last_start || low >= last_start;
-                            add_bias<-1>(s, a.scale, bias, rel + reach, far, far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f);
+                            add_bias(s, a.scale, bias, rel + reach, far, far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f);
                         }
                         if (a.causal && high > 0) {  // query ic + e sees key j from e = rel on
 #pragma unroll
