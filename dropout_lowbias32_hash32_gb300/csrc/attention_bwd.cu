@@ -87,6 +87,11 @@ __device__ __forceinline__ void add_bias(uint32_t (&s)[N], float scale, const fl
 
 // ---- dq ------------------------------------------------------------------------
 
+// Sums along the diagonals of a warp's 32 x 32 pairs are walked in that many
+// parts of the columns at once: a step waits for a shuffle (16 x 1024 of 16
+// heads of 64, 32 buckets: 519 us with two, 525 with one, 521 with four).
+constexpr int kWalks = 2;
+
 template <int kDim>
 struct QueryShape {
     using Team = Crew<3, 1>;
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t stalled;
     __shared__ float deltas[kChains][kRows];
-    __shared__ float diagonals[kBias ? 4 * kChains : 1][64], by_bucket[kBias ? 4 * kChains : 1][kMaxBuckets];
+    __shared__ float diagonals[kBias ? 4 * kChains : 1][kWalks][64], by_bucket[kBias ? 4 * kChains : 1][kMaxBuckets];
     const Attention &a = p.a;
     const uint32_t warp = uniform(threadIdx.x / 32u), lane = threadIdx.x % 32u;
     uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
@@ -279,6 +284,10 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
         if (kBias)
             for (int32_t t = threadIdx.x; t < 2 * reach; t += Team::kWorkers) bucket_at[t - reach] = bucket_of(a.buckets, t - reach);
         const float above = lane ? 1.0f : 0.0f;
+        if (kBias) {  // the diagonals that a walk does not reach stay 0
+            for (int k = 0; k < kWalks; ++k) diagonals[warp][k][lane] = diagonals[warp][k][lane + 32] = 0.0f;
+            __syncwarp();
+        }
         uint32_t turn = 0, finished = 0;
         // A row's o, do (the warpgroups take parts of it) and lse are asked for before the previous item's result is
         // written, which takes longer than they do.
@@ -415,30 +424,43 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                                 (high <= -last_start ? far_low : far_high) += total.x + total.y;
                             } else {
                                 // Sums along the diagonals of the warp's 32 x 32 pairs: a partial sum moves one row down
-                                // with each column; what leaves row 31, or is left in the last column, is a whole one.
-                                // Diagonal d = 0 .. 62 is relative position low + d.
-                                float acc = 0.0f;
+                                // with each column; what leaves row 31, or is left in a walk's last column, is a walk's
+                                // part.  Diagonal d = 0 .. 62 is relative position low + d.
+                                constexpr int kSteps = 32 / kWalks;
+                                float acc[kWalks] = {};
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    acc = __fmaf_rn(__shfl_up_sync(0xFFFFFFFFu, acc, 1), above, __uint_as_float(s[e]));
-                                    if (lane == 31) diagonals[warp][e] = acc;
-                                }
-                                diagonals[warp][63 - (lane + 1) % 32] = lane < 31 ? acc : 0.0f;
+                                for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+                                    for (int k = 0; k < kWalks; ++k) {
+                                        acc[k] = __fmaf_rn(__shfl_up_sync(0xFFFFFFFFu, acc[k], 1), above, __uint_as_float(s[k * kSteps + e]));
+                                        if (lane == 31) diagonals[warp][k][k * kSteps + e] = acc[k];
+                                    }
+#pragma unroll
+                                for (int k = 0; k < kWalks; ++k)
+                                    if (lane < 31) diagonals[warp][k][(k + 1) * kSteps + 30 - lane] = acc[k];
                                 __syncwarp();
                                 // A bucket's positions follow each other, so sums over runs of one bucket: half of the
                                 // diagonals at a time, the last lane of a run adds it.
-#pragma unroll 1
-                                for (int32_t d = lane; d < 64; d += 32) {
-                                    const int32_t bucket = bucket_at[low + d];
-                                    float run = diagonals[warp][d];
+                                int32_t bucket[2];
+                                float run[2] = {};
 #pragma unroll
-                                    for (int m = 1; m < 32; m *= 2) {
-                                        const float before = __shfl_up_sync(0xFFFFFFFFu, run, m);
-                                        const int32_t its = __shfl_up_sync(0xFFFFFFFFu, bucket, m);
-                                        if (static_cast<int>(lane) >= m && its == bucket) run += before;
+                                for (int d = 0; d < 2; ++d) {
+                                    bucket[d] = bucket_at[low + 32 * d + lane];
+#pragma unroll
+                                    for (int k = 0; k < kWalks; ++k) run[d] += diagonals[warp][k][32 * d + lane];
+                                }
+#pragma unroll
+                                for (int m = 1; m < 32; m *= 2)
+#pragma unroll
+                                    for (int d = 0; d < 2; ++d) {
+                                        const float before = __shfl_up_sync(0xFFFFFFFFu, run[d], m);
+                                        const int32_t its = __shfl_up_sync(0xFFFFFFFFu, bucket[d], m);
+                                        if (static_cast<int>(lane) >= m && its == bucket[d]) run[d] += before;
                                     }
-                                    const int32_t after = __shfl_down_sync(0xFFFFFFFFu, bucket, 1);
-                                    if (lane == 31 || after != bucket) by_bucket[warp][bucket] += run;
+#pragma unroll
+                                for (int d = 0; d < 2; ++d) {
+                                    const int32_t after = __shfl_down_sync(0xFFFFFFFFu, bucket[d], 1);
+                                    if (lane == 31 || after != bucket[d]) by_bucket[warp][bucket[d]] += run[d];
                                     __syncwarp();
                                 }
                             }
