@@ -742,11 +742,6 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                             const bool far = high <= -last_start || low >= last_start;
                             add_bias(s, a.scale, bias, rel + reach, far, far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f);
                         }
-                        if (a.causal && high > 0) {  // query ic + e sees key j from e = rel on
-#pragma unroll
-                            for (int e = 0; e < kPiece; ++e)
-                                if (e < rel) s[e] = __float_as_uint(-INFINITY);
-                        }
                         // P = exp(S - lse), dropped for dv; dS = P (dropout(dP) - delta) for dk
 #pragma unroll
                         for (int e = 0; e < kPiece; e += 2) {
@@ -764,6 +759,13 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                             d = mul2(fma2(d, make_float2(scale, scale), make_float2(st.y, st.w)), prob);
                             s[e / 2] = pack2<T>(kept2.x, kept2.y);
                             dp[e / 2] = pack2<T>(d.x, d.y);
+                        }
+                        if (a.causal && high > 0) {  // query ic + e sees key j from e = rel on
+#pragma unroll
+                            for (int e = 0; e < kPiece; e += 2) {
+                                const uint32_t seen = (e < rel ? 0u : 0xFFFFu) | (e + 1 < rel ? 0u : 0xFFFF0000u);
+                                s[e / 2] &= seen, dp[e / 2] &= seen;
+                            }
                         }
                         const uint32_t to = mine + at / 32 * S::kPitch + at % 32 / 2;
                         tmem_store(to, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(s));

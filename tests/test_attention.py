@@ -108,7 +108,7 @@ class Run:
         import layer_reference as ref
         k, _ = self.clean()
         big = ref.heads_first(self.q.abs()) @ ref.heads_first(k.abs(), self.c["h"] // self.c["hk"]).transpose(2, 3)
-        big = big * self.scale
+        big = big * abs(self.scale)
         bias = 0.0 if self.table is None else float(self.table.double().abs().max())
         err = (self.c["d"] + 8) * 2 * U * big + 2.0 ** -21 * (big + bias)
         err = err.masked_fill(~self.pairs.visible, 0)
@@ -140,8 +140,8 @@ class Run:
         err = (c["d"] + 8) * 2 * U * (ado @ av.transpose(2, 3) / (1 - c["p"]) + (ado * ao).sum(-1, keepdim=True))
         step = 2.0 ** -25 if c["dtype"] == "float16" else 0.0
         w = (ut + 4 * e) * ds.abs() + 2 * prob * err + step * self.pairs.visible
-        assert_within("dq", out["dq"], dq, (w @ ak * self.scale).transpose(1, 2) + ut * dq.abs() + tiny)
-        assert_within("dk", out["dk"], dk, ref.shared(w.transpose(2, 3) @ aq * self.scale, c["hk"]) + ut * dk.abs() + tiny)
+        assert_within("dq", out["dq"], dq, (w @ ak * abs(self.scale)).transpose(1, 2) + ut * dq.abs() + tiny)
+        assert_within("dk", out["dk"], dk, ref.shared(w.transpose(2, 3) @ aq * abs(self.scale), c["hk"]) + ut * dk.abs() + tiny)
         wv = (ut + 4 * e) * kept + step / (1 - c["p"]) * self.pairs.visible
         assert_within("dv", out["dv"], dv, ref.shared(wv.transpose(2, 3) @ ado, c["hk"]) + ut * dv.abs() + tiny)
         if self.table is not None:
@@ -203,6 +203,17 @@ def test_new_tokens_against_a_cache(torch, rng, orc, group, lq, lk, b, dtype, d)
     r = Run(torch, rng, orc, case(b=b, lq=lq, lk=lk, h=2 * group, hk=2, d=d, dtype=dtype, lengths=lengths, causal=True,
                                   last=True))
     r.check_forward(*r.forward())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", (1.0, 0.0, -0.2))
+@pytest.mark.parametrize("buckets,lk", ((0, 200), (32, 200), (0, 900)))
+def test_scales(torch, rng, orc, scale, buckets, lk):
+    """Of either sign: the maximum is then another score's; 0: every visible key counts alike."""
+    for lq in (1, 150):
+        r = Run(torch, rng, orc, case(lq=lq, lk=lk, h=4, hk=2, buckets=buckets, p=0.1, causal=True, last=True, spread=0.5))
+        r.scale = r.options["scale"] = scale
+        r.check()
 
 
 # More work than there are SMs: every block takes several pieces, of unequal lengths, one after the other.
