@@ -499,7 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
     if (warp == kMmaWarp) tmem_free<512>(tmem);
 }
 
-// Joins the key axis's splits: a warp to a row.
+// Joins the key axis's splits: a warp to a row, the loads of four splits at
+// once (one that saw no key has the maximum -inf and zeros).
 template <class T, int kDim>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ FwdParams p)
 {
@@ -508,18 +509,27 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ FwdPa
     const int64_t index = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.y;
     if (index >= rows) return;
     const uint32_t lane = threadIdx.x;
-    constexpr int kEach = kDim / 32;
+    constexpr int kEach = kDim / 32, kAtOnce = 4;
     float top = -INFINITY, sum = 0.0f, o[kEach] = {};
-    for (int32_t s = 0; s < p.splits; ++s) {
-        const float *part = p.part + (s * rows + index) * (kDim + 2);
-        const float t = part[kDim], l = part[kDim + 1];
-        if (l == 0.0f) continue;  // saw nothing
-        const float next = fmaxf(top, t), fade = exp2_approx((top - next) * kLog2e);
-        const float weight = exp2_approx((t - next) * kLog2e);
-        sum = sum * fade + l * weight;
-        top = next;
+    for (int32_t s = 0; s < p.splits; s += kAtOnce) {
+        float2 stats[kAtOnce], part[kAtOnce][kEach / 2];
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) o[k] = o[k] * fade + part[lane * kEach + k] * weight;
+        for (int u = 0; u < kAtOnce; ++u) {
+            const float2 *at = reinterpret_cast<const float2 *>(p.part + (min(s + u, p.splits - 1) * rows + index) * (kDim + 2));
+            stats[u] = at[kDim / 2];
+#pragma unroll
+            for (int k = 0; k < kEach / 2; ++k) part[u][k] = at[lane * (kEach / 2) + k];
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (s + u >= p.splits || stats[u].y == 0.0f) continue;
+            const float next = fmaxf(top, stats[u].x), fade = exp2_approx((top - next) * kLog2e);
+            const float weight = exp2_approx((stats[u].x - next) * kLog2e);
+            sum = sum * fade + stats[u].y * weight;
+            top = next;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) o[k] = o[k] * fade + (k % 2 ? part[u][k / 2].y : part[u][k / 2].x) * weight;
+        }
     }
     const int64_t i = index % a.len_q, h = index / a.len_q % a.heads, b = index / a.len_q / a.heads;
     const float scale = sum == 0.0f ? 0.0f : a.mask.scale / sum;

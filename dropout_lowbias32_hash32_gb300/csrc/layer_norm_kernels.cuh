@@ -516,28 +516,28 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(const __grid_cons
 }
 
 // The weights' gradients from `blocks` rows of [3][cols] partial sums: a warp
-// of adjacent columns adds every 32nd row from its own on, then the block's 32
-// warps are added in order.
+// of adjacent columns adds every 16th row from its own on, then the block's 16
+// warps are added in a fixed order.
+constexpr uint32_t kSumWarps = 16;
 template <class W>
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, uint32_t blocks, uint32_t cols, W *dgamma,
-                                                          W *dbeta, W *dbias)
+__global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const float *part, uint32_t blocks, uint32_t cols, W *dgamma,
+                                                                    W *dbeta, W *dbias)
 {
-    __shared__ float sums[32][33];
+    __shared__ float sums[kSumWarps][32];
     W *out = blockIdx.y == 0 ? dgamma : blockIdx.y == 1 ? dbeta : dbias;
     if (out == nullptr) return;
     const uint32_t j = blockIdx.x * 32u + threadIdx.x;
     float s = 0.0f;
     if (j < cols)
 #pragma unroll 8
-        for (uint32_t b = threadIdx.y; b < blocks; b += 32u)
+        for (uint32_t b = threadIdx.y; b < blocks; b += kSumWarps)
             s += part[(static_cast<size_t>(b) * 3u + blockIdx.y) * cols + j];
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    s = sums[threadIdx.x][threadIdx.y];
+    if (threadIdx.y != 0 || j >= cols) return;
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-    const uint32_t k = blockIdx.x * 32u + threadIdx.y;
-    if (threadIdx.x == 0 && k < cols) out[k] = from_f32<W>(s);
+    for (uint32_t k = 1; k < kSumWarps; ++k) s += sums[k][threadIdx.x];
+    out[j] = from_f32<W>(s);
 }
 
 unsigned round_up(unsigned v, unsigned m) { return (v + m - 1u) / m * m; }
@@ -560,7 +560,7 @@ void fwd_in_registers(const NormFwd &a, cudaStream_t s)
 template <class T, class W>
 void launch_column_sum(const NormBwd &a, const float *part, unsigned blocks, cudaStream_t s)
 {
-    column_sum_kernel<W><<<dim3((a.cols + 31u) / 32u, 3), dim3(32, 32), 0, s>>>(
+    column_sum_kernel<W><<<dim3((a.cols + 31u) / 32u, 3), dim3(32, kSumWarps), 0, s>>>(
         part, blocks, a.cols, static_cast<W *>(a.dgamma), static_cast<W *>(a.dbeta), static_cast<W *>(a.dbias));
     note_launch();
 }
