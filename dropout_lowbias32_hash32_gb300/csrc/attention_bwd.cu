@@ -17,6 +17,14 @@
 // thread to a row; where there are two chains only, two warpgroups share a tile,
 // 32 columns a thread, for as many warps.  A block that has finished takes over
 // the work of one that has not started.
+//
+// What bounds them, measured (bf16, p = 0.1): both draw the mask, so instruction
+// issue, 20 to 23 instructions a pair each.
+//   16 x 1024 positions, 16 heads of 64, 32 buckets: query_kernel 252 us (issue slots
+//     60 % busy, ALU pipe 40 %, tensor core 18 %), key_kernel 255 us (65, 46, 23 %),
+//     table_kernel 5 us.
+//   2 x 4096 causal positions, 16 heads of 128 over 4 key heads: query_kernel 239 us
+//     (55, 39, 37 %), key_kernel 263 us (68, 47, 51 %).
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 

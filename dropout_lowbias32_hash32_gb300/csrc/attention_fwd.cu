@@ -7,7 +7,7 @@
 // take a unit's tiles in turn, a thread to a row, each with an S of its own: so
 // four chains of product, exponential, product are under way, the tensor core
 // works for three while the fourth computes, and four warps a scheduler hide each
-// other's latencies.  One thread a unit issues its products, one warp the TMA loads; a
+// other's latencies.  One warp a unit issues its products, another the TMA loads; a
 // stage of their ring holds a value tile and the key tile `kLead` after it.
 //   kSplitKeys = false: the units are two tiles of queries that share the key
 //     and value tiles (halving their traffic from L2);
@@ -22,6 +22,16 @@
 // A row's maximum passes from tile to tile through shared memory.  It is raised,
 // and O rescaled, only when it has grown by more than 2^8: P then stays below
 // 2^8, which 16 bits hold as well as 1.
+//
+// What bounds it, measured (bf16):
+//   with dropout, the mask's hash: 10 of 17 instructions a pair (19 with a bias).
+//     16 x 1024 positions, 16 heads of 64, 32 buckets, p = 0.1: 201 us, issue slots
+//     71 % busy, ALU pipe 54 %, tensor core 15 %; without bias and dropout 97 us.
+//   without it, the tensor core and what feeds it: 4099 causal positions, 32 heads
+//     of 128 over 8 key heads: 106 us, 1.30 PFLOP/s of the visible pairs, tensor
+//     core 60 %, exponentials 30 %.
+//   for new tokens, HBM: 32 of them, 32 heads over 8 key heads of 128, 8192 cached
+//     keys at most: 537 MB in 97.5 us, 5.5 TB/s, of which 5 us are join_kernel.
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 

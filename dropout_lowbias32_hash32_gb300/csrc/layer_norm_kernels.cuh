@@ -4,9 +4,13 @@
 //
 // Bound by HBM: the forward pass reads x and residual and writes y and h (8
 // bytes an element in 16-bit types), the backward pass reads dy, h, dh and
-// writes dx, dresidual (10 bytes), for 15 to 35 instructions an element, about
-// ten of them the mask's hash.  So a row is read once and stays in registers
-// between its reductions; the mask is redrawn from the element's flat index.
+// writes dx, dresidual (10 bytes), for 40 instructions an element, about ten of
+// them the mask's hash.  So a row is read once and stays in registers (or shared
+// memory) between its reductions; the mask is redrawn from the element's flat
+// index.  Measured, 16384 x 4096 in bf16, p = 0.1: forward 94 us, 537 MB at 5.7
+// TB/s, issue slots 79 % busy; backward 127 us, 671 MB at 5.3 TB/s, of which the
+// sums of the weights' gradients 7 us.  2^20 x 256 in f32, forward: 610 us, 4.3 GB
+// at 7.0 TB/s.
 #pragma once
 
 #include "barrier.cuh"
