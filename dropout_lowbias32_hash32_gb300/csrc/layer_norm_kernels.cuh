@@ -85,8 +85,7 @@ __device__ __forceinline__ void normalised(const NormFwd &a, const float (&h)[V]
     fma_all<V>(y, h, 1.0f, -mean);
     float g[V];
     unpack<W, V>(load_or_one<W, V>(a.gamma, col), g);
-#pragma unroll
-    for (int k = 0; k < V; ++k) g[k] *= rstd;
+    fma_all<V>(g, g, rstd, 0.0f);
     if (a.beta) {
         float b[V];
         unpack<W, V>(load<false, W, V>(static_cast<const W *>(a.beta) + col), b);
@@ -124,20 +123,24 @@ __device__ __forceinline__ Moments row_moments(const float (&h)[P][V], uint32_t 
     };
     const uint32_t warp = kWarp ? 0u : t / 32u;
     const float mine = share(warp);
-    float sum = 0.0f, squares = 0.0f;
+    float sum[V] = {}, squares[V] = {};
 #pragma unroll
     for (int i = 0; i < P; ++i)
-        if (t + i * group < vectors)
+        if (t + i * group < vectors) add_all<V>(sum, sum, h[i]);
 #pragma unroll
-            for (int k = 0; k < V; ++k) sum += h[i][k];
+    for (int k = 1; k < V; ++k) sum[0] += sum[k];
     Moments m;
-    m.mean = mine > 0.0f ? warp_sum(sum) / mine : 0.0f;
+    m.mean = mine > 0.0f ? warp_sum(sum[0]) / mine : 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i)
-        if (t + i * group < vectors)
+        if (t + i * group < vectors) {
+            float d[V];
+            fma_all<V>(d, h[i], 1.0f, -m.mean);
+            fma_all<V>(squares, d, d, squares);
+        }
 #pragma unroll
-            for (int k = 0; k < V; ++k) squares += (h[i][k] - m.mean) * (h[i][k] - m.mean);
-    m.deviations = warp_sum(squares);
+    for (int k = 1; k < V; ++k) squares[0] += squares[k];
+    m.deviations = warp_sum(squares[0]);
     if constexpr (!kWarp) {
         const uint32_t lane = t % 32u;
         if (lane == 0) scratch[warp] = make_float2(m.mean, m.deviations);
