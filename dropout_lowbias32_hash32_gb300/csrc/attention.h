@@ -106,6 +106,14 @@ __host__ __device__ __forceinline__ int32_t bias_reach(const Buckets &b) { retur
 // maximum before the scores are scaled, and so want a scale above 0.
 inline bool has_bias(const Attention &a) { return a.table != nullptr || !(a.scale > 0.0f); }
 
+// Whether P and dS enter the products that follow as two 16-bit terms, the
+// rounded value and what rounding left.  One rounding adds an error as large as
+// the output's own: 1.4 of it together over many rows, but up to 1.7 over few,
+// where chance decides.  Few rows are bound by latency, which the second term
+// adds nothing to (one query of 8 heads, 301 keys: 17 us either way); with
+// 1024 rows it already costs (32 x 8192 cached keys: 112 us, 97 without).
+inline bool two_terms(const Attention &a, int64_t length) { return length * a.batch * a.heads <= 512; }
+
 inline int32_t log2_of(int32_t power)
 {
     int32_t n = 0;

@@ -137,7 +137,7 @@ __device__ __forceinline__ QueryItem query_item(const BwdParams &p, uint32_t x)
     return w;
 }
 
-template <class T, int kDim, bool kDrop, bool kBias>
+template <class T, int kDim, bool kDrop, bool kBias, bool kTwoTerms>
 __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_kernel(const __grid_constant__ BwdParams p)
 {
     using S = QueryShape<kDim>;
@@ -252,6 +252,9 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                         const uint64_t kd = ring_kt + stage * (S::kStageBytes / 16);
 #pragma unroll
                         for (int i = 0; i < kCols / 16; ++i) mma_step_tmem(tmem, at + i * 8, kd + i * (2048 / 16), kOut, n > 0 || i > 0);
+                        if (kTwoTerms)
+#pragma unroll
+                            for (int i = 0; i < kCols / 16; ++i) mma_step_tmem(tmem, at + kCols + i * 8, kd + i * (2048 / 16), kOut, true);
                         mma_commit(empty + 8 * stage);
                         if (n + 1 == tiles) mma_commit(done);
                     }
@@ -418,6 +421,13 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
 #pragma unroll
                         for (int e = 0; e < 16; ++e) ds[e] = pack2<T>(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
                         tmem_store(mine + 16 * c, ds);
+                        if (kTwoTerms) {  // the second, over dP
+                            uint32_t rest[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                rest[e] = rest2<T>(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), ds[e]);
+                            tmem_store(mine + kCols + 16 * c, rest);
+                        }
                         if (c) {
                             tmem_wait_store();
                             tmem_fence_before();
@@ -578,7 +588,7 @@ __device__ __forceinline__ KeyItem key_item(const BwdParams &p, uint32_t x)
     return w;
 }
 
-template <class T, int kDim, bool kDrop, bool kBias>
+template <class T, int kDim, bool kDrop, bool kBias, bool kTwoTerms>
 __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(const __grid_constant__ BwdParams p)
 {
     using S = KeyShape<kDim>;
@@ -678,11 +688,17 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                     if (add && elect_one()) {  // dV += P^T dO, dK += dS^T Q
                         const uint64_t qt = ring_qt + stage * (S::kStageBytes / 16);
 #pragma unroll
-                        for (int i = 0; i < kCols / 16; ++i)
-                            mma_step_tmem(dv_at, at + i / 2 * S::kPitch + i % 2 * 8, qt + (S::kColsBytes + i * 2048) / 16, kOut, n > 0 || i > 0);
+                        for (int i = 0; i < kCols / 16; ++i) {
+                            const uint32_t from = kTwoTerms ? i * 16 : i / 2 * S::kPitch + i % 2 * 8;
+                            mma_step_tmem(dv_at, at + from, qt + (S::kColsBytes + i * 2048) / 16, kOut, n > 0 || i > 0);
+                            if (kTwoTerms) mma_step_tmem(dv_at, at + from + 8, qt + (S::kColsBytes + i * 2048) / 16, kOut, true);
+                        }
 #pragma unroll
-                        for (int i = 0; i < kCols / 16; ++i)
-                            mma_step_tmem(dk_at, at + kCols + i / 2 * S::kPitch + i % 2 * 8, qt + i * 2048 / 16, kOut, n > 0 || i > 0);
+                        for (int i = 0; i < kCols / 16; ++i) {
+                            const uint32_t from = kCols + (kTwoTerms ? i * 16 : i / 2 * S::kPitch + i % 2 * 8);
+                            mma_step_tmem(dk_at, at + from, qt + i * 2048 / 16, kOut, n > 0 || i > 0);
+                            if (kTwoTerms) mma_step_tmem(dk_at, at + from + 8, qt + i * 2048 / 16, kOut, true);
+                        }
                         mma_commit(empty + 8 * stage);
                         if (n + 1 == tiles) mma_commit(done);
                     }
@@ -751,33 +767,55 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                             add_bias(s, a.scale, bias, rel + reach, far, far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f);
                         }
                         // P = exp(S - lse), dropped for dv; dS = P (dropout(dP) - delta) for dk
-#pragma unroll
-                        for (int e = 0; e < kPiece; e += 2) {
+                        auto pair = [&](int e, float2 &kept2, float2 &d) {
                             const float4 st = stats[e / 2];  // two queries' -lse, -delta
                             float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                             f = kBias ? fma2(add2(f, make_float2(st.x, st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>))
                                       : fma2(f, make_float2(to_base2, to_base2), make_float2(st.x, st.z));
                             const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
-                            float2 kept2 = prob, d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+                            kept2 = prob, d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
                             if (kDrop) {
                                 const uint32_t step = a.len_k;
                                 const float2 k = make_float2(kept(a.mask, mad_lo(e, step, counter)), kept(a.mask, mad_lo(e + 1, step, counter)));
                                 kept2 = mul2(kept2, k), d = mul2(d, k);
                             }
                             d = mul2(fma2(d, make_float2(scale, scale), make_float2(st.y, st.w)), prob);
-                            s[e / 2] = pack2<T>(kept2.x, kept2.y);
-                            dp[e / 2] = pack2<T>(d.x, d.y);
-                        }
-                        if (a.causal && high > 0) {  // query ic + e sees key j from e = rel on
+                        };
+                        // query ic + e sees key j from e = rel on
+                        auto seen = [&](int e) { return (e < rel ? 0u : 0xFFFFu) | (e + 1 < rel ? 0u : 0xFFFF0000u); };
+                        if (kTwoTerms) {  // of 16 columns, the second term's 8 after the first's
+                            uint32_t rest_p[kPiece / 2], rest_d[kPiece / 2];
 #pragma unroll
                             for (int e = 0; e < kPiece; e += 2) {
-                                const uint32_t seen = (e < rel ? 0u : 0xFFFFu) | (e + 1 < rel ? 0u : 0xFFFF0000u);
-                                s[e / 2] &= seen, dp[e / 2] &= seen;
+                                float2 kept2, d;
+                                pair(e, kept2, d);
+                                const uint32_t mask = a.causal ? seen(e) : ~0u;
+                                s[e / 2] = pack2<T>(kept2.x, kept2.y), dp[e / 2] = pack2<T>(d.x, d.y);
+                                rest_p[e / 2] = rest2<T>(kept2, s[e / 2]) & mask, rest_d[e / 2] = rest2<T>(d, dp[e / 2]) & mask;
+                                s[e / 2] &= mask, dp[e / 2] &= mask;
                             }
+#pragma unroll
+                            for (int e = 0; e < kPiece / 2; e += 8) {
+                                const uint32_t to = mine + at + 2 * e;
+                                tmem_store(to, reinterpret_cast<const uint32_t(&)[8]>(s[e]));
+                                tmem_store(to + 8, reinterpret_cast<const uint32_t(&)[8]>(rest_p[e]));
+                                tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[8]>(dp[e]));
+                                tmem_store(to + kCols + 8, reinterpret_cast<const uint32_t(&)[8]>(rest_d[e]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < kPiece; e += 2) {
+                                float2 kept2, d;
+                                pair(e, kept2, d);
+                                s[e / 2] = pack2<T>(kept2.x, kept2.y), dp[e / 2] = pack2<T>(d.x, d.y);
+                            }
+                            if (a.causal && high > 0)
+#pragma unroll
+                                for (int e = 0; e < kPiece; e += 2) s[e / 2] &= seen(e), dp[e / 2] &= seen(e);
+                            const uint32_t to = mine + at / 32 * S::kPitch + at % 32 / 2;
+                            tmem_store(to, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(s));
+                            tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(dp));
                         }
-                        const uint32_t to = mine + at / 32 * S::kPitch + at % 32 / 2;
-                        tmem_store(to, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(s));
-                        tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(dp));
                     }
                     tmem_wait_store();
                 }
@@ -877,10 +915,10 @@ BwdPlan bwd_plan(const Attention &a)
     return f;
 }
 
-template <class T, int kDim, bool kDrop, bool kBias>
+template <class T, int kDim, bool kDrop, bool kBias, bool kTwoTerms>
 cudaError_t launch_queries(const BwdParams &p, cudaStream_t s)
 {
-    const auto kernel = query_kernel<T, kDim, kDrop, kBias>;
+    const auto kernel = query_kernel<T, kDim, kDrop, kBias, kTwoTerms>;
     const size_t bytes = 1024 + QueryShape<kDim>::kTable + (kBias ? 2 * bias_reach(p.a.buckets) * (sizeof(float) + 1) : 0);
     static std::atomic<bool> done[16];
     const cudaError_t e = allow_shared(kernel, done);
@@ -890,10 +928,10 @@ cudaError_t launch_queries(const BwdParams &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <class T, int kDim, bool kDrop, bool kBias>
+template <class T, int kDim, bool kDrop, bool kBias, bool kTwoTerms>
 cudaError_t launch_keys(const BwdParams &p, cudaStream_t s)
 {
-    const auto kernel = key_kernel<T, kDim, kDrop, kBias>;
+    const auto kernel = key_kernel<T, kDim, kDrop, kBias, kTwoTerms>;
     const size_t bytes = 1024 + KeyShape<kDim>::kBytes;
     static std::atomic<bool> done[16];
     const cudaError_t e = allow_shared(kernel, done);
@@ -905,13 +943,21 @@ cudaError_t launch_keys(const BwdParams &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <class T, int kDim, bool kDrop, bool kBias>
+template <class T, int kDim, bool kDrop, bool kBias, bool kTwoTerms>
 cudaError_t launch_both(const BwdParams &p, bool queries, bool keys, cudaStream_t s)
 {
     cudaError_t e = cudaSuccess;
-    if (queries) e = launch_queries<T, kDim, kDrop, kBias>(p, s);
-    if (e == cudaSuccess && keys) e = launch_keys<T, kDim, kDrop, kBias>(p, s);
+    if (queries) e = launch_queries<T, kDim, kDrop, kBias, kTwoTerms>(p, s);
+    if (e == cudaSuccess && keys) e = launch_keys<T, kDim, kDrop, kBias, kTwoTerms>(p, s);
     return e;
+}
+
+template <class T, int kDim, bool kDrop, bool kBias>
+cudaError_t launch_both(const BwdParams &p, bool queries, bool keys, cudaStream_t s)
+{
+    return two_terms(p.a, p.a.len_q > p.a.len_k ? p.a.len_q : p.a.len_k)
+               ? launch_both<T, kDim, kDrop, kBias, true>(p, queries, keys, s)
+               : launch_both<T, kDim, kDrop, kBias, false>(p, queries, keys, s);
 }
 
 template <class T, int kDim>

@@ -12,8 +12,8 @@
 //   kSplitKeys = false: the units are two tiles of queries that share the key
 //     and value tiles (halving their traffic from L2);
 //   kSplitKeys = true: one tile of queries, the units take every other key
-//     tile and are joined at the end.  For few rows, where the key axis is also
-//     split over blocks, and joined by join_kernel.
+//     tile and are joined at the end.  For one tile a head and for few rows,
+//     where the key axis is also split over blocks, and joined by join_kernel.
 // The query heads of one key head are `pack` adjacent rows of a tile, so that
 // they read its keys once.  A block that has finished takes over the work of one
 // that has not started, so that its loads and first products run under the last
@@ -52,6 +52,7 @@ struct FwdParams {
     Attention a;
     int32_t pack, pack_log, units, q_tiles, splits, split_tiles;
     Divider by_splits, by_units, by_q_tiles, by_packs, by_group;
+    bool two_terms;
     float *part;  // [splits][rows][dim padded + 2]: O, max, sum
 };
 
@@ -241,6 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                             for (int i = 0; i < kKeys / 16; ++i)
                                 mma_step_tmem(at + 2 * kKeys, at + group * kKeys + i * 8, vd + i * (2048 / 16), kOut,
                                               n >= (kSplitKeys ? 2 : 1) || i > 0);
+                            if (kSplitKeys && p.two_terms)
+#pragma unroll
+                                for (int i = 0; i < kKeys / 16; ++i)
+                                    mma_step_tmem(at + 2 * kKeys, at + group * kKeys + kKeys / 2 + i * 8, vd + i * (2048 / 16), kOut, true);
                             if (next >= count) mma_commit(added + 8 * unit);
                             if (n + (kSplitKeys ? 2 : 1) >= count) mma_commit(done + 8 * unit);
                         }
@@ -391,14 +396,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                     const float from = top == -INFINITY ? 0.0f : -top, shift = from * to_base2;
                     const float2 from2 = make_float2(from, from), shift2 = make_float2(shift, shift);
                     const float2 base2 = make_float2(to_base2, to_base2);
+                    auto exponentials = [&](int c, uint32_t e) {
+                        const float2 v = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                        const float2 f = kBias ? mul2(add2(v, from2), base2) : fma2(v, base2, shift2);
+                        return make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                    };
+                    if (kSplitKeys && p.two_terms)  // the second, beside where the first goes
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t q[16];
+                            for_pairs32<kDrop>(a.mask, counter + j0 + 32 * c, [&](uint32_t e, float2 k) {
+                                const float2 x = mul2(exponentials(c, e), k);
+                                q[e / 2] = rest2<T>(x, pack2<T>(x.x, x.y));
+                            });
+                            tmem_store(mine + kKeys / 2 + 16 * c, q);
+                        }
                     float2 total = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t q[16];
                         for_pairs32<kDrop>(a.mask, counter + j0 + 32 * c, [&](uint32_t e, float2 k) {
-                            const float2 v = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                            const float2 f = kBias ? mul2(add2(v, from2), base2) : fma2(v, base2, shift2);
-                            float2 x = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                            float2 x = exponentials(c, e);
                             total = add2(total, x);
                             if (kDrop) x = mul2(x, k);
                             q[e / 2] = pack2<T>(x.x, x.y);
@@ -564,13 +582,13 @@ FwdPlan fwd_plan(const Attention &a)
     f.units = a.batch * (a.heads / f.pack);
     const int32_t rows_per = kRows / f.pack, tiles = (a.len_q + rows_per - 1) / rows_per;
     const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
-    f.split_keys = tiles == 1;
-    f.q_tiles = f.split_keys ? 1 : (tiles + 1) / 2;
+    f.split_keys = tiles == 1 || two_terms(a, a.len_q);  // whose kernel knows two terms
+    f.q_tiles = f.split_keys ? tiles : (tiles + 1) / 2;
     f.splits = 1, f.split_tiles = key_tiles < 1 ? 1 : key_tiles;
     if (f.split_keys && key_tiles > 8) {
         // about four blocks to an SM, of eight key tiles or more (the second launch that joins them costs as much as
         // some six tiles)
-        const int64_t want = (4ll * sm_count() + f.units - 1) / f.units;
+        const int64_t blocks = static_cast<int64_t>(f.units) * f.q_tiles, want = (4ll * sm_count() + blocks - 1) / blocks;
         const int64_t most = (key_tiles + 7) / 8;
         const int64_t splits = want < most ? want : most;
         f.split_tiles = static_cast<int32_t>((key_tiles + splits - 1) / splits);
@@ -628,7 +646,7 @@ cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s)
     FwdParams p;
     p.a = a;
     p.pack = f.pack, p.units = f.units, p.q_tiles = f.q_tiles, p.splits = f.splits, p.split_tiles = f.split_tiles;
-    p.pack_log = log2_of(f.pack);
+    p.pack_log = log2_of(f.pack), p.two_terms = two_terms(a, a.len_q);
     p.by_splits = Divider(f.splits), p.by_units = Divider(f.units), p.by_q_tiles = Divider(f.q_tiles);
     p.by_packs = Divider(a.heads / f.pack), p.by_group = Divider(a.group);
     p.part = static_cast<float *>(a.workspace);

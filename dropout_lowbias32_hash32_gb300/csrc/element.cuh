@@ -121,6 +121,17 @@ __device__ __forceinline__ void store(T *p, const float (&v)[V])
     }
 }
 
+// What rounding a pair to T's packed h has left of it, rounded likewise.
+template <class T>
+__device__ __forceinline__ uint32_t rest2(float2 v, uint32_t h)
+{
+    Raw<T, 8> r;
+    r.w[0] = h, r.w[1] = r.w[2] = r.w[3] = 0;
+    float o[8];
+    unpack<T, 8>(r, o);
+    return pack2<T>(v.x - o[0], v.y - o[1]);
+}
+
 // Two f32 at a time.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {

@@ -16,6 +16,7 @@ dP - delta: dS is rounded to ut, so each dS is within ut|dS| + 4 e |dS| + 2 P E
 |q|; dv within (ut + 4 e) sum P'|do| + ut |dv|; the table's gradient is not
 rounded before its sum of n terms: 4 e sum|dS| + 2 sum P E + 4096 u sum|dS| +
 ut |dtable| (a chain is at most 4096 terms long here).
+Where P and dS are two terms (few rows), their part of this is ut^2, not ut.
 """
 import ctypes as C
 import math
@@ -78,6 +79,7 @@ class Run:
                     n = min(max(n, 0), c["lk"])
                     self.k[b, n:], self.v[b, n:] = float("nan"), float("inf")
         self.scale = c["d"] ** -0.5
+        self.term = UT[c["dtype"]]  # what rounding P and dS may change of them
         self.pairs = ref.Pairs(orc, self.q, self.k, self.lengths, c["causal"], c["last"], c["buckets"], c["far"],
                                c["two_way"], c["p"], c["seed"], c["first"])
         self.options = dict(key_lengths=self.lengths, causal=c["causal"], queries_last=c["last"], bias_table=self.table,
@@ -120,7 +122,7 @@ class Run:
         k, v = self.clean()
         want, wlse, prob = ref.attention_fwd(self.q, k, v, self.table, self.pairs, self.scale)
         e, hv = self.score_error(), ref.heads_first(v, group).abs()
-        tol = (ut + 4 * e + 2.0 ** -19) * ((prob * self.pairs.keep) @ hv)
+        tol = (self.term + 4 * e + 2.0 ** -19) * ((prob * self.pairs.keep) @ hv)
         if self.c["dtype"] == "float16":
             tol = tol + 2.0 ** -25 / (1 - self.c["p"]) * hv.sum(2, keepdim=True)
         assert_within("lse", lse, wlse, (e + 2.0 ** -20 * (1 + wlse.abs())).nan_to_num(posinf=0.0))
@@ -139,10 +141,10 @@ class Run:
         kept = prob * self.pairs.keep
         err = (c["d"] + 8) * 2 * U * (ado @ av.transpose(2, 3) / (1 - c["p"]) + (ado * ao).sum(-1, keepdim=True))
         step = 2.0 ** -25 if c["dtype"] == "float16" else 0.0
-        w = (ut + 4 * e) * ds.abs() + 2 * prob * err + step * self.pairs.visible
+        w = (self.term + 4 * e) * ds.abs() + 2 * prob * err + step * self.pairs.visible
         assert_within("dq", out["dq"], dq, (w @ ak * abs(self.scale)).transpose(1, 2) + ut * dq.abs() + tiny)
         assert_within("dk", out["dk"], dk, ref.shared(w.transpose(2, 3) @ aq * abs(self.scale), c["hk"]) + ut * dk.abs() + tiny)
-        wv = (ut + 4 * e) * kept + step / (1 - c["p"]) * self.pairs.visible
+        wv = (self.term + 4 * e) * kept + step / (1 - c["p"]) * self.pairs.visible
         assert_within("dv", out["dv"], dv, ref.shared(wv.transpose(2, 3) @ ado, c["hk"]) + ut * dv.abs() + tiny)
         if self.table is not None:
             tol = ref.by_bucket((4 * e + 4096 * U) * ds.abs() + 2 * prob * err, self.table, self.pairs)
@@ -203,6 +205,28 @@ def test_new_tokens_against_a_cache(torch, rng, orc, group, lq, lk, b, dtype, d)
     r = Run(torch, rng, orc, case(b=b, lq=lq, lk=lk, h=2 * group, hk=2, d=d, dtype=dtype, lengths=lengths, causal=True,
                                   last=True))
     r.check_forward(*r.forward())
+
+
+FEW = {
+    "one_token": case(b=1, lq=1, lk=301, h=8, causal=True, last=True, buckets=32),
+    "one_token_128": case(b=2, lq=1, lk=2500, h=16, hk=2, d=128, causal=True, last=True, dtype="float16"),
+    "five": case(b=2, lq=5, h=6, d=8, buckets=32), "six": case(lq=6, h=9, hk=3, dtype="float16", p=0.1, buckets=32),
+    "causal_128": case(lq=100, h=2, hk=1, d=128, causal=True, p=0.1), "tiles": case(b=1, lq=120, lk=250, h=2, p=0.2),
+    "tiles_f16": case(b=1, lq=70, lk=128, h=4, hk=4, d=96, causal=True, last=True, dtype="float16", buckets=16),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", FEW)
+def test_few_rows_take_two_terms(torch, rng, orc, name):
+    """The forward pass for at most 512 queries of all heads; the backward pass for 512 queries, and keys, of all heads."""
+    c = FEW[name]
+    r = Run(torch, rng, orc, c)
+    r.term = UT[c["dtype"]] ** 2
+    o, lse = r.forward()
+    prob = r.check_forward(o, lse)
+    if c["b"] * c["h"] * max(c["lq"], c["lk"]) <= 512:
+        r.check_backward(o, prob, r.backward(o, lse))
 
 
 @pytest.mark.gpu
