@@ -107,7 +107,8 @@ __host__ __device__ __forceinline__ int32_t bias_reach(const Buckets &b) { retur
 inline bool has_bias(const Attention &a) { return a.table != nullptr || !(a.scale > 0.0f); }
 
 // Whether P and dS enter the products that follow as two 16-bit terms, the
-// rounded value and what rounding left.  One rounding adds an error as large as
+// rounded value and what rounding left; length is the queries' (backward: the
+// shorter one).  One rounding adds an error as large as
 // the output's own: 1.4 of it together over many rows, but up to 1.7 over few,
 // where chance decides.  Few rows are bound by latency, which the second term
 // adds nothing to (one query of 8 heads, 301 keys: 17 us either way); with

@@ -334,8 +334,9 @@ size_t rng_dropout_layer_norm_bwd_workspace(size_t rows, size_t cols);
  *
  * s, the softmax statistics and all sums are f32; P (before its division by
  * the row's sum) and, in the backward pass, P and dS are rounded to dtype as
- * the operands of the matrix products that follow, where there are at most 512
- * rows as two terms each (the value and what its rounding left). */
+ * the operands of the matrix products that follow; with at most 512 queries of
+ * all batch entries and heads (backward: or keys) as two terms each, the value
+ * and what its rounding left. */
 typedef struct rng_attention_args {
     rng_dtype dtype;
     int32_t batch, len_q, len_k, heads_q, heads_kv, head_dim;
