@@ -294,7 +294,6 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
         uint8_t *bucket_at = reinterpret_cast<uint8_t *>(table + 2 * reach) + reach;
         if (kBias)
             for (int32_t t = threadIdx.x; t < 2 * reach; t += Team::kWorkers) bucket_at[t - reach] = bucket_of(a.buckets, t - reach);
-        const float above = lane ? 1.0f : 0.0f;
         if (kBias) {  // the diagonals that a walk does not reach stay 0
             for (int k = 0; k < kWalks; ++k) diagonals[warp][k][lane] = diagonals[warp][k][lane + 32] = 0.0f;
             __syncwarp();
@@ -450,7 +449,8 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                                 for (int e = 0; e < kSteps; ++e)
 #pragma unroll
                                     for (int k = 0; k < kWalks; ++k) {
-                                        acc[k] = __fmaf_rn(__shfl_up_sync(0xFFFFFFFFu, acc[k], 1), above, __uint_as_float(s[k * kSteps + e]));
+                                        const float before = __shfl_up_sync(0xFFFFFFFFu, acc[k], 1);
+                                        acc[k] = (lane ? before : 0.0f) + __uint_as_float(s[k * kSteps + e]);
                                         if (lane == 31) diagonals[warp][k][k * kSteps + e] = acc[k];
                                     }
 #pragma unroll

@@ -365,6 +365,18 @@ def test_scores_that_are_not_finite(torch, rng, orc):
 
 
 @pytest.mark.gpu
+def test_gradients_that_are_not_finite_stay_in_their_bucket(torch, rng, orc):
+    """Query 0 sees key 0 alone: what its gradient holds reaches bucket 0 and its own row of dq."""
+    r = Run(torch, rng, orc, case(lq=150, h=2, b=1, causal=True, buckets=16, two_way=False))
+    o, lse = r.forward()
+    clean = r.backward(o, lse)
+    r.do[0, 0] = float("inf")
+    out = r.backward(o, lse)
+    assert bool(out["dtable"][0].isnan().all()) and torch.equal(out["dtable"][1:], clean["dtable"][1:])
+    assert bool(out["dq"][0, 0].isnan().all()) and torch.equal(out["dq"][0, 1:], clean["dq"][0, 1:])
+
+
+@pytest.mark.gpu
 def test_twice_the_same_bits_and_another_stream(torch, rng, orc):
     r = Run(torch, rng, orc, case(lq=300, h=4, hk=2, buckets=32, p=0.1, causal=True))
     o, lse = r.forward()
