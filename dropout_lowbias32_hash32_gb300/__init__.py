@@ -362,11 +362,17 @@ def _scratch(workspace, need: int, like, stream):
     if need == 0:
         return None, 0, None
     if workspace is None:
-        workspace = _torch.empty(need, dtype=_torch.uint8, device=like.device)
-        if stream is not None:  # its memory may be reused only after that stream's work
+        # From the pool of the stream that the kernels run on: a block that another stream has given back may still
+        # be used by that stream's queued work.
+        if stream is None:
+            workspace = _torch.empty(need, dtype=_torch.uint8, device=like.device)
+        else:
             if not isinstance(stream, _torch.cuda.Stream):
-                stream = _torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
-            workspace.record_stream(stream)
+                handle = int(getattr(stream, "cuda_stream", stream))
+                stream = (_torch.cuda.ExternalStream(handle, device=like.device) if handle
+                          else _torch.cuda.default_stream(like.device))
+            with _torch.cuda.stream(stream):
+                workspace = _torch.empty(need, dtype=_torch.uint8, device=like.device)
     elif workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace

@@ -1,0 +1,130 @@
+"""How the layer operators are called: the stream and the workspace of a call."""
+import contextlib
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    return torch
+
+
+@pytest.fixture(scope="module")
+def rng():
+    import dropout_lowbias32_hash32_gb300 as rng
+    return rng
+
+
+# ---- the workspace's stream ----------------------------------------------------------
+
+
+class FakeTorch:
+    """As much of torch as takes a workspace; `allocated` lists the streams that
+    were current when it was."""
+
+    uint8 = "uint8"
+
+    def __init__(self):
+        self.current, self.allocated = "current", []
+        fake = self
+
+        class Stream:
+            def __init__(self, handle):
+                self.cuda_stream = handle
+
+        class Cuda:
+            pass
+
+        @contextlib.contextmanager
+        def stream(s):
+            before, fake.current = fake.current, s.cuda_stream
+            yield
+            fake.current = before
+
+        self.cuda = Cuda()
+        self.cuda.Stream, self.cuda.stream = Stream, stream
+        self.cuda.ExternalStream = lambda handle, device=None: Stream(handle)
+        self.cuda.default_stream = lambda device=None: Stream(0)
+
+    def empty(self, n, dtype, device):
+        self.allocated.append(self.current)
+
+        class Tensor:
+            record_stream = staticmethod(lambda s: None)
+            data_ptr, numel, element_size = (staticmethod(lambda: 1 << 20), staticmethod(lambda: n),
+                                             staticmethod(lambda: 1))
+        return Tensor()
+
+
+def test_a_workspace_is_taken_from_the_stream_that_the_kernels_run_on(rng, monkeypatch):
+    """The allocator hands a block of the current stream's pool out again while
+    the current stream's earlier work still uses it: right for that stream
+    alone."""
+    fake = FakeTorch()
+    monkeypatch.setattr(rng, "_torch", fake)
+    like = type("Like", (), {"device": "cuda:0"})()
+
+    class Handle:  # a stream of another library
+        cuda_stream = 77
+
+    for stream, want in ((None, "current"), (fake.cuda.Stream(55), 55), (66, 66), (Handle(), 77), (0, 0),
+                         (fake.cuda.Stream(0), 0)):
+        pointer, size, hold = rng._scratch(None, 4096, like, stream)
+        assert (fake.allocated.pop(), fake.current) == (want, "current") and pointer and size == 4096 and hold
+    assert rng._scratch(None, 0, like, 55) == (None, 0, None) and not fake.allocated
+
+
+def busy(torch):
+    """Work that the current stream is at for some milliseconds."""
+    a = torch.randn(8192, 8192, device="cuda")
+    for _ in range(6):
+        a = a @ a * 1e-3
+    return a
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("operator", ("attention_bwd", "attention_fwd", "norm_bwd"))
+def test_a_call_on_another_stream_keeps_off_the_current_ones_workspace(torch, rng, operator):
+    """Two calls of one size, the second on another stream while the first, and
+    the workspace that it has given back, are still to be used: each gives what
+    it gives alone."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def normal(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+    def call():
+        if operator == "norm_bwd":
+            dy, h, gamma, mean, rstd = (normal(4096, 1024), normal(4096, 1024), normal(1024),
+                                        normal(4096, dtype=torch.float32), normal(4096, dtype=torch.float32))
+            out = [torch.empty_like(t) for t in (dy, gamma, gamma)]
+            return out, lambda **o: rng.rng_dropout_layer_norm_bwd(dy, h, gamma, mean, rstd, out[0], out[1], out[2],
+                                                                   p=0.1, seed=3, **o)
+        lq, lk = (1, 8192) if operator == "attention_fwd" else (512, 512)
+        q, do = normal(2, lq, 8, 64), normal(2, lq, 8, 64)
+        k, v = normal(2, lk, 8, 64), normal(2, lk, 8, 64)
+        o, lse = torch.empty_like(q), torch.empty(2, 8, lq, device="cuda")
+        if operator == "attention_fwd":
+            return [o, lse], lambda **s: rng.rng_attention_fwd(q, k, v, o, lse=lse, **s)
+        rng.rng_attention_fwd(q, k, v, o, lse=lse, p=0.1, seed=3)
+        out = [torch.empty_like(t) for t in (q, k, v)]
+        return out, lambda **s: rng.rng_attention_bwd(do, q, k, v, o, lse, *out, p=0.1, seed=3, **s)
+
+    calls = [call() for _ in range(2)]
+    want = []
+    for out, run in calls:
+        run()
+        want.append([t.clone() for t in out])
+        for t in out:
+            t.zero_()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        torch.cuda.synchronize()
+        busy(torch)
+        calls[0][1]()
+        calls[1][1](stream=stream)
+        torch.cuda.synchronize()
+        for (out, _), w in zip(calls, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, w))
+            for t in out:
+                t.zero_()
