@@ -124,10 +124,10 @@ inline int32_t log2_of(int32_t power)
 
 // Heads of one key head that lie side by side in a tile of 128 rows, so that
 // they read its keys once: all of them, where a tile is a whole number of
-// them and no head has a bias of its own.
+// them and no head has a bias of its own.  At least 1, also without query heads.
 inline int32_t packed_heads(const Attention &a)
 {
-    return !has_bias(a) && a.group <= 64 && (a.group & (a.group - 1)) == 0 ? a.group : 1;
+    return !has_bias(a) && a.group >= 1 && a.group <= 64 && (a.group & (a.group - 1)) == 0 ? a.group : 1;
 }
 
 }  // namespace rngk

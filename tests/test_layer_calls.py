@@ -1,7 +1,12 @@
-"""How the layer operators are called: the stream and the workspace of a call."""
+"""How the layer operators are called: the stream and the workspace of a call,
+sizes at the ends of what it accepts."""
 import contextlib
+import subprocess
+import sys
 
 import pytest
+
+from conftest import ROOT
 
 
 @pytest.fixture(scope="module")
@@ -128,3 +133,20 @@ def test_a_call_on_another_stream_keeps_off_the_current_ones_workspace(torch, rn
             assert all(torch.equal(a, b) for a, b in zip(out, w))
             for t in out:
                 t.zero_()
+
+
+# ---- sizes ---------------------------------------------------------------------------
+
+
+def test_workspaces_without_query_heads():
+    """In a process of its own: what it guards against ends the process."""
+    code = """
+import ctypes as C
+import dropout_lowbias32_hash32_gb300 as rng
+for causal in (0, 1):
+    for scale in (0.125, 0.0):
+        a = rng.AttentionArgs(dtype=rng.RNG_BF16, batch=2, len_q=4, len_k=4, heads_q=0, heads_kv=2, head_dim=64, scale=scale,
+                              causal=causal)
+        assert rng.rng_attention_fwd_workspace(a) == 0 and rng.rng_attention_bwd_workspace(a) == 0
+"""
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, timeout=120)
