@@ -1005,6 +1005,9 @@ cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s)
         map(&p.k_rows, a.k, a.ks, a.len_k, a.heads_kv, 1, kRows), map(&p.v_rows, a.v, a.vs, a.len_k, a.heads_kv, 1, kRows);
         map(&p.k_cols, a.k, a.ks, a.len_k, a.heads_kv, 1, kCols), map(&p.v_cols, a.v, a.vs, a.len_k, a.heads_kv, 1, kCols);
     }
+    // what is missing has no tile that is loaded, but a kernel prefetches its maps
+    if (!has_q) p.q_cols = p.do_cols = p.k_cols;
+    if (!has_k) p.k_cols = p.v_cols = p.q_cols;
     if (static_cast<int64_t>(f.units) * f.q_tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
     if (e == cudaSuccess)
         e = f.dim == 64 ? launch_both<T, 64>(p, has_q, has_k, s) : launch_both<T, 128>(p, has_q, has_k, s);

@@ -150,3 +150,27 @@ for causal in (0, 1):
         assert rng.rng_attention_fwd_workspace(a) == 0 and rng.rng_attention_bwd_workspace(a) == 0
 """
     subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True, timeout=120)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", (64, 128))
+def test_without_query_heads_the_keys_gradients_are_zeros(torch, rng, dim):
+    q = torch.empty(2, 5, 0, dim, device="cuda", dtype=torch.bfloat16)
+    k, v, dk, dv = (torch.full((2, 150, 2, dim), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    lse = torch.empty(2, 0, 5, device="cuda")
+    rng.rng_attention_fwd(q, k, v, q.clone(), lse=lse)
+    rng.rng_attention_bwd(q, q, k, v, q, lse, q.clone(), dk, dv, causal=True, p=0.1)
+    assert bool((dk == 0).all()) and bool((dv == 0).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", (64, 128))
+def test_without_keys_or_queries_the_gradients_are_zeros(torch, rng, dim):
+    some, none = (torch.randn(2, n, 2, dim, device="cuda").bfloat16() for n in (150, 0))
+    table = torch.randn(8, 2, device="cuda").bfloat16()
+    for q, k, lse in ((some, none, torch.full((2, 2, 150), -float("inf"), device="cuda")),
+                      (none, some, torch.empty(2, 2, 0, device="cuda"))):
+        dq, dk, dv, dtable = (torch.full_like(t, float("nan")) for t in (q, k, k, table))
+        rng.rng_attention_bwd(q, q, k, k, torch.zeros_like(q), lse, dq, dk, dv, bias_table=table, dbias_table=dtable,
+                              causal=True, p=0.1)
+        assert all(bool((t == 0).all()) for t in (dq, dk, dv, dtable))
