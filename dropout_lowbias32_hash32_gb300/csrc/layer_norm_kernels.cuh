@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(256) norm_bwd_columns_kernel(const __grid_cons
         dgamma += dy * n, dbeta += dy, dbias += dz;
     }
     float *part = a.workspace + 2 * a.rows + static_cast<size_t>(blockIdx.y) * 3u * a.cols;
-    part[j] = dgamma, part[a.cols + j] = dbeta, part[2u * a.cols + j] = dbias;
+    part[j] = dgamma, part[static_cast<size_t>(a.cols) + j] = dbeta, part[size_t(2) * a.cols + j] = dbias;
 }
 
 // The weights' gradients from `blocks` rows of [3][cols] partial sums: a warp

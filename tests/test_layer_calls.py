@@ -174,3 +174,18 @@ def test_without_keys_or_queries_the_gradients_are_zeros(torch, rng, dim):
         rng.rng_attention_bwd(q, q, k, k, torch.zeros_like(q), lse, dq, dk, dv, bias_table=table, dbias_table=dtable,
                               causal=True, p=0.1)
         assert all(bool((t == 0).all()) for t in (dq, dk, dv, dtable))
+
+
+@pytest.mark.gpu
+def test_rows_whose_three_sums_pass_2_to_32(torch, rng):
+    """One row: dbias is dx, dbeta is dy and, as the statistics are 0 and 1, dgamma dy h, each rounded once."""
+    cols = 1_440_000_007
+    g = torch.Generator(device="cuda").manual_seed(6)
+    dy, h = (torch.empty(1, cols, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(2))
+    mean, rstd = torch.zeros(1, device="cuda"), torch.ones(1, device="cuda")
+    dx = torch.empty_like(dy)
+    dgamma, dbeta, dbias = (torch.full((cols,), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    rng.rng_dropout_layer_norm_bwd(dy, h, None, mean, rstd, dx, dgamma, dbeta, dbias=dbias)
+    assert torch.equal(dbias, dx[0]) and torch.equal(dbeta, dy[0]) and torch.equal(dgamma, dy[0] * h[0])
+    del dy, h, dx, dgamma, dbeta, dbias
+    torch.cuda.empty_cache()
