@@ -114,6 +114,46 @@ rng_status check_rows(const char *what, const Array (&a)[N], int in_place, size_
     return RNG_OK;
 }
 
+// A contiguous array beside them: a weight, a row's statistic, the workspace.
+struct Flat {
+    const char *name;
+    const void *p;
+    size_t bytes;
+    bool output;
+};
+
+// Whether a flat array shares a byte with a row: with the first one that ends
+// past its beginning.
+bool overlap(const Array &a, const Flat &f, size_t rows, size_t cols, size_t size)
+{
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), f0 = reinterpret_cast<uintptr_t>(f.p);
+    const size_t used = cols * size, step = a.stride * size;
+    const size_t row = f0 < a0 + used ? 0 : rows == 1 ? 1 : (f0 - a0 - used) / step + 1;
+    return row < rows && a0 + row * step < f0 + f.bytes;
+}
+
+// Outputs share no byte with anything else (the [rows, cols] arrays among
+// themselves are check_rows's).
+template <size_t N, size_t M>
+rng_status check_flat(const char *what, const Flat (&f)[M], const Array (&a)[N], size_t rows, size_t cols, size_t size)
+{
+    for (size_t i = 0; i < M; ++i) {
+        if (!f[i].p || f[i].bytes == 0) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(f[i].p);
+        if (f[i].bytes > UINTPTR_MAX - at)
+            return fail(RNG_EINVAL, "%s: %s runs past the end of the address space", what, f[i].name);
+        for (const Array &x : a)
+            if (rows && x.p && (x.output || f[i].output) && overlap(x, f[i], rows, cols, size))
+                return fail(RNG_EINVAL, "%s: %s and %s overlap", what, x.name, f[i].name);
+        for (size_t j = 0; j < i; ++j) {
+            const uintptr_t other = reinterpret_cast<uintptr_t>(f[j].p);
+            if (f[j].p && (f[i].output || f[j].output) && at < other + f[j].bytes && other < at + f[i].bytes)
+                return fail(RNG_EINVAL, "%s: %s and %s overlap", what, f[j].name, f[i].name);
+        }
+    }
+    return RNG_OK;
+}
+
 template <size_t N>
 bool whole_vectors(const Array (&a)[N], size_t rows, size_t cols, size_t size)
 {
@@ -171,6 +211,12 @@ rng_status rng_dropout_layer_norm_fwd(const void *x, size_t x_stride, const void
         if (rng_status st = check_vector(what, "a weight", w, psize)) return st;
     if (rng_status st = check_vector(what, "mean", mean, 4)) return st;
     if (rng_status st = check_vector(what, "rstd", rstd, 4)) return st;
+    const Flat flat[] = {{"bias", bias, cols * psize, false},
+                         {"gamma", gamma, cols * psize, false},
+                         {"beta", beta, cols * psize, false},
+                         {"mean", mean, rows * sizeof(float), true},
+                         {"rstd", rstd, rows * sizeof(float), true}};
+    if (rng_status st = check_flat(what, flat, arrays, rows, cols, size)) return st;
     clear_error();
     NormFwd a{};
     a.x = {x, x_stride}, a.residual = {residual, residual_stride}, a.y = {y, y_stride}, a.h = {h, h_stride};
@@ -219,6 +265,14 @@ rng_status rng_dropout_layer_norm_bwd(const void *dy, size_t dy_stride, const vo
     } else if (cols > 0x7FFFFFFF) {
         return fail(RNG_EINVAL, "%s: %zu columns exceed 2^31 - 1", what, cols);
     }
+    const Flat flat[] = {{"gamma", gamma, cols * psize, false},
+                         {"mean", mean, rows * sizeof(float), false},
+                         {"rstd", rstd, rows * sizeof(float), false},
+                         {"dgamma", dgamma, cols * psize, true},
+                         {"dbeta", dbeta, cols * psize, true},
+                         {"dbias", dbias, cols * psize, true},
+                         {"workspace", workspace, rows ? rng_dropout_layer_norm_bwd_workspace(rows, cols) : 0, true}};
+    if (rng_status st = check_flat(what, flat, arrays, rows, cols, size)) return st;
     clear_error();
     NormBwd a{};
     a.dy = {dy, dy_stride}, a.h = {h, h_stride}, a.dh = {dh, dh_stride};

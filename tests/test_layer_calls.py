@@ -189,3 +189,59 @@ def test_rows_whose_three_sums_pass_2_to_32(torch, rng):
     assert torch.equal(dbias, dx[0]) and torch.equal(dbeta, dy[0]) and torch.equal(dgamma, dy[0] * h[0])
     del dy, h, dx, dgamma, dbeta, dbias
     torch.cuda.empty_cache()
+
+
+# ---- overlaps (nothing below reaches the GPU) -----------------------------------------
+
+A = 0x10000000  # an address that is never dereferenced
+
+
+def norm_fwd(rng, x=A, bias=2 * A, residual=3 * A, gamma=4 * A, beta=5 * A, y=6 * A, h=7 * A, mean=8 * A, rstd=9 * A,
+             stride=100, rows=4, cols=64):
+    return rng.raw("rng_dropout_layer_norm_fwd")(x, stride, bias, residual, stride, gamma, beta, y, stride, h, stride,
+                                                 mean, rstd, rows, cols, rng.RNG_BF16, rng.RNG_F32, 0.1, 1, 0, 1e-5,
+                                                 None)
+
+
+def norm_bwd(rng, dy=A, h=2 * A, dh=3 * A, gamma=4 * A, mean=5 * A, rstd=6 * A, dx=7 * A, dresidual=8 * A,
+             dgamma=9 * A, dbeta=10 * A, dbias=11 * A, ws=12 * A, stride=100, rows=4, cols=64):
+    need = rng.rng_dropout_layer_norm_bwd_workspace(rows, cols)
+    return rng.raw("rng_dropout_layer_norm_bwd")(dy, stride, h, stride, dh, stride, gamma, mean, rstd, dx, stride,
+                                                 dresidual, stride, dgamma, dbeta, dbias, rows, cols, rng.RNG_BF16,
+                                                 rng.RNG_F32, 0.1, 1, 0, ws, need, None)
+
+
+# rows of 128 bytes, 200 apart; weights of 256 bytes, statistics of 16
+@pytest.mark.parametrize("bad,says", [
+    ({"gamma": 6 * A}, "y and gamma"), ({"beta": 6 * A - 252}, "y and beta"), ({"bias": 7 * A + 600 + 124}, "h and bias"),
+    ({"mean": 6 * A}, "y and mean"), ({"rstd": A}, "x and rstd"), ({"mean": 3 * A + 200}, "residual and mean"),
+    ({"rstd": 8 * A + 12}, "mean and rstd"), ({"mean": 4 * A + 252}, "gamma and mean"),
+    ({"mean": 6 * A, "rows": 1}, "y and mean"), ({"gamma": 6 * A + 124, "rows": 1}, "y and gamma")])
+def test_norm_forward_refuses_overlaps(rng, bad, says):
+    assert norm_fwd(rng, **bad) == rng.RNG_EINVAL
+    assert says in rng.rng_last_error() and "overlap" in rng.rng_last_error()
+
+
+@pytest.mark.parametrize("bad,says", [
+    ({"dgamma": 4 * A}, "gamma and dgamma"), ({"dbeta": 9 * A + 252}, "dgamma and dbeta"),
+    ({"dbias": 2 * A + 200}, "h and dbias"), ({"dx": 5 * A}, "dx and mean"), ({"dresidual": 6 * A + 8}, "dresidual and rstd"),
+    ({"ws": A}, "dy and workspace"), ({"ws": 9 * A}, "dgamma and workspace"), ({"ws": 5 * A}, "mean and workspace"),
+    ({"ws": 7 * A}, "dx and workspace"), ({"dgamma": 10 * A, "rows": 0}, "dgamma and dbeta")])
+def test_norm_backward_refuses_overlaps(rng, bad, says):
+    assert norm_bwd(rng, **bad) == rng.RNG_EINVAL
+    assert says in rng.rng_last_error() and "overlap" in rng.rng_last_error()
+
+
+@pytest.mark.gpu
+def test_norm_beside_its_rows_is_fine(torch, rng):
+    """Statistics and weights in the gaps of a wider array, and one after the
+    other in one allocation."""
+    rows, cols = 3, 64
+    store = torch.zeros(rows, 512, device="cuda")
+    x = torch.randn(rows, cols, device="cuda")
+    y, gamma, mean, rstd = store[:, :cols], store[0, 64:128], store[1, 64:64 + rows], store[1, 64 + rows:64 + 2 * rows]
+    gamma.fill_(2.0)
+    rng.rng_dropout_layer_norm_fwd(x, gamma, None, y, mean, rstd)
+    want = torch.empty_like(x)
+    rng.rng_dropout_layer_norm_fwd(x, gamma.clone(), None, want)
+    assert torch.equal(y, want) and bool((gamma == 2.0).all()) and bool((mean - x.mean(1)).abs().max() < 1e-6)
