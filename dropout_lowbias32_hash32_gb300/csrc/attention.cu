@@ -144,6 +144,82 @@ bool overlap(const rng_attention_args &a, const Tensor &x, const Tensor &y)
     return true;
 }
 
+// A contiguous array beside the tensors; output: written.
+struct Flat {
+    const char *name;
+    const void *p;
+    uint64_t bytes;
+    bool output;
+};
+
+// A tensor's dimensions from the largest stride to the smallest, in bytes, and
+// what one entry of the dimensions before reaches.
+struct Nest {
+    int32_t n[3];
+    uint64_t step[3], reach[4];
+};
+
+Nest nest_of(const rng_attention_args &a, const Tensor &t)
+{
+    const int32_t n[3] = {a.batch, t.len, t.heads};
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (t.stride[order[j]] > t.stride[order[i]]) std::swap(order[i], order[j]);
+    Nest x;
+    x.reach[3] = 2 * static_cast<uint64_t>(a.head_dim);
+    for (int k = 2; k >= 0; --k) {
+        x.n[k] = n[order[k]], x.step[k] = 2 * static_cast<uint64_t>(t.stride[order[k]]);
+        x.reach[k] = x.reach[k + 1] + (x.n[k] - 1) * x.step[k];
+    }
+    return x;
+}
+
+// Whether [f0, f1) shares a byte with the tensor's part at `at` of the
+// dimensions from k on: with its first or its last entry there, or it holds one
+// between them.  Entries that overlap each other (an input's may) count as
+// without gaps.
+bool meets(const Nest &x, int k, uintptr_t at, uintptr_t f0, uintptr_t f1)
+{
+    if (f1 <= at || at + x.reach[k] <= f0) return false;
+    if (k == 3) return true;
+    if (x.n[k] == 1) return meets(x, k + 1, at, f0, f1);
+    const uint64_t step = x.step[k], inside = x.reach[k + 1], last = x.n[k] - 1;
+    if (step < inside) return true;
+    const uint64_t first = f0 < at + inside ? 0 : (f0 - at - inside) / step + 1, end = (f1 - 1 - at) / step;
+    const uint64_t to = end < last ? end : last;
+    if (first > to) return false;
+    return to - first > 1 || meets(x, k + 1, at + first * step, f0, f1) || meets(x, k + 1, at + to * step, f0, f1);
+}
+
+// Outputs share no byte with anything else (the tensors among themselves are
+// check_tensors's).
+template <size_t N, size_t M>
+rng_status check_flat(const char *what, const rng_attention_args &a, const Flat (&f)[M], const Tensor (&t)[N])
+{
+    for (size_t i = 0; i < M; ++i) {
+        if (!f[i].p || f[i].bytes == 0) continue;
+        const uintptr_t f0 = reinterpret_cast<uintptr_t>(f[i].p), f1 = f0 + f[i].bytes;
+        if (f1 < f0) return fail(RNG_EINVAL, "%s: %s runs past the end of the address space", what, f[i].name);
+        for (const Tensor &x : t) {
+            const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p);
+            if (!(x.output || f[i].output) || empty(a, x) || f1 <= x0 || x0 + extent(a, x) <= f0) continue;
+            if (meets(nest_of(a, x), 0, x0, f0, f1))
+                return fail(RNG_EINVAL, "%s: %s and %s overlap", what, x.name, f[i].name);
+        }
+        for (size_t j = 0; j < i; ++j) {
+            const uintptr_t other = reinterpret_cast<uintptr_t>(f[j].p);
+            if (f[j].p && (f[i].output || f[j].output) && f0 < other + f[j].bytes && other < f1)
+                return fail(RNG_EINVAL, "%s: %s and %s overlap", what, f[j].name, f[i].name);
+        }
+    }
+    return RNG_OK;
+}
+
+// Bytes of lse, and of the table or its gradient.
+uint64_t lse_bytes(const Attention &t) { return uint64_t(4) * t.batch * t.heads * t.len_q; }
+uint64_t table_bytes(const Attention &t) { return uint64_t(2) * t.buckets.total * t.heads; }
+
 // The sizes and options, without the pointers.
 rng_status make(const char *what, const rng_attention_args *args, bool sizes_only, Attention *out)
 {
@@ -257,7 +333,13 @@ rng_status rng_attention_fwd(const rng_attention_args *args, void *stream)
                               {"v", a.v, a.v_stride, a.len_k, a.heads_kv, false},
                               {"o", a.o, a.o_stride, a.len_q, a.heads_q, true}};
     if (rng_status st = check_tensors(what, a, tensors)) return st;
-    if (rng_status st = check_workspace(what, a, attention_fwd_workspace(t))) return st;
+    const size_t need = attention_fwd_workspace(t);
+    if (rng_status st = check_workspace(what, a, need)) return st;
+    const Flat flat[] = {{"key_lengths", a.key_lengths, uint64_t(4) * t.batch, false},
+                         {"bias_table", a.bias_table, table_bytes(t), false},
+                         {"lse", a.lse, lse_bytes(t), true},
+                         {"workspace", a.workspace, need, true}};
+    if (rng_status st = check_flat(what, a, flat, tensors)) return st;
     t.out = a.o;
     clear_error();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -282,7 +364,14 @@ rng_status rng_attention_bwd(const rng_attention_args *args, void *stream)
                               {"dv", a.dv, a.dv_stride, a.len_k, a.heads_kv, true}};
     if (rng_status st = check_tensors(what, a, tensors)) return st;
     if (!a.lse && t.batch && t.len_q && t.heads) return fail(RNG_EINVAL, "%s: lse is NULL", what);
-    if (rng_status st = check_workspace(what, a, attention_bwd_workspace(t))) return st;
+    const size_t need = attention_bwd_workspace(t);
+    if (rng_status st = check_workspace(what, a, need)) return st;
+    const Flat flat[] = {{"key_lengths", a.key_lengths, uint64_t(4) * t.batch, false},
+                         {"bias_table", a.bias_table, table_bytes(t), false},
+                         {"lse", a.lse, lse_bytes(t), false},
+                         {"dbias_table", a.dbias_table, table_bytes(t), true},
+                         {"workspace", a.workspace, need, true}};
+    if (rng_status st = check_flat(what, a, flat, tensors)) return st;
     t.o = a.o, t.d_o = a.d_o, t.dq = a.dq, t.dk = a.dk, t.dv = a.dv;
     auto strides = [](const int64_t *s) { return Strides{s[0], s[1], s[2]}; };
     t.dos = strides(a.do_stride), t.dqs = strides(a.dq_stride), t.dks = strides(a.dk_stride), t.dvs = strides(a.dv_stride);

@@ -1,6 +1,7 @@
 """How the layer operators are called: the stream and the workspace of a call,
 sizes at the ends of what it accepts."""
 import contextlib
+import ctypes as C
 import subprocess
 import sys
 
@@ -245,3 +246,77 @@ def test_norm_beside_its_rows_is_fine(torch, rng):
     want = torch.empty_like(x)
     rng.rng_dropout_layer_norm_fwd(x, gamma.clone(), None, want)
     assert torch.equal(y, want) and bool((gamma == 2.0).all()) and bool((mean - x.mean(1)).abs().max() < 1e-6)
+
+
+def attention_args(rng, strides=(1024, 256, 64), **change):
+    """[2, 4, 2, 64] arrays, a position's two heads side by side and a gap of 128 elements after them."""
+    a = rng.AttentionArgs(dtype=rng.RNG_BF16, batch=2, len_q=4, len_k=4, heads_q=2, heads_kv=2, head_dim=64, scale=0.125,
+                          num_buckets=32, max_distance=128, bidirectional=1, workspace_bytes=1 << 20)
+    names = ("q", "k", "v", "o", "d_o", "dq", "dk", "dv", "lse", "key_lengths", "bias_table", "dbias_table", "workspace")
+    for i, n in enumerate(names):
+        setattr(a, n, (i + 1) * A)
+        if i < 8:
+            setattr(a, "do_stride" if n == "d_o" else n + "_stride", strides)
+    for n, v in change.items():
+        setattr(a, n, v)
+    return C.byref(a)
+
+
+# lse: 64 bytes, key_lengths 8, tables 128; a position's heads use 256 of 512 bytes
+@pytest.mark.parametrize("bad,says", [
+    ({"lse": A}, "q and lse"), ({"lse": 4 * A + 128}, "o and lse"), ({"lse": 2 * A + 2048 + 512 * 3 + 252}, "k and lse"),
+    ({"lse": 4 * A - 60}, "o and lse"), ({"bias_table": 4 * A + 1024}, "o and bias_table"),
+    ({"key_lengths": 4 * A + 512 + 252}, "o and key_lengths"), ({"lse": 11 * A + 124}, "bias_table and lse"),
+    ({"lse": 10 * A}, "key_lengths and lse"), ({"lse": 4 * A + 208}, "o and lse")])
+def test_attention_forward_refuses_overlaps(rng, bad, says):
+    assert rng.raw("rng_attention_fwd")(attention_args(rng, **bad), None) == rng.RNG_EINVAL
+    assert says in rng.rng_last_error() and "overlap" in rng.rng_last_error()
+
+
+@pytest.mark.gpu
+def test_attention_forward_refuses_a_workspace_that_overlaps(torch, rng):
+    """(How the key axis is split, and so whether there is a workspace, goes by the device.)"""
+    q = torch.randn(1, 1, 8, 64, device="cuda").bfloat16()
+    k = torch.randn(1, 8192, 8, 64, device="cuda").bfloat16()
+    o, lse = torch.empty_like(q), torch.empty(1, 8, 1, device="cuda")
+    with pytest.raises(rng.RngError, match="k and workspace overlap"):
+        rng.rng_attention_fwd(q, k, k, o, lse=lse, workspace=k.view(-1))
+
+
+@pytest.mark.parametrize("bad,says", [
+    ({"lse": 6 * A}, "dq and lse"), ({"dbias_table": 6 * A}, "dq and dbias_table"), ({"dbias_table": 11 * A}, "bias_table and dbias_table"),
+    ({"dbias_table": 4 * A + 256 - 16}, "o and dbias_table"), ({"bias_table": 8 * A}, "dv and bias_table"),
+    ({"key_lengths": 7 * A}, "dk and key_lengths"), ({"dbias_table": 9 * A + 60}, "lse and dbias_table"),
+    ({"workspace": 6 * A}, "dq and workspace"), ({"workspace": A - 64}, "q and workspace"),
+    ({"workspace": 9 * A}, "lse and workspace"), ({"workspace": 12 * A + 112}, "dbias_table and workspace")])
+def test_attention_backward_refuses_overlaps(rng, bad, says):
+    assert rng.raw("rng_attention_bwd")(attention_args(rng, **bad), None) == rng.RNG_EINVAL
+    assert says in rng.rng_last_error() and "overlap" in rng.rng_last_error()
+
+
+@pytest.mark.gpu
+def test_attention_beside_its_heads_is_fine(torch, rng):
+    """lse, lengths, the table and its gradient in the gaps of the arrays."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    wide = {n: torch.zeros(2, 4, 4, 64, device="cuda").bfloat16() for n in ("q", "k", "v", "o", "do", "dq", "dk", "dv")}
+    part = {n: t[:, :, 1:3] for n, t in wide.items()}
+    for n in ("q", "k", "v", "do"):
+        part[n].copy_(torch.randn(2, 4, 2, 64, generator=g, device="cuda"))
+    lse = wide["o"][0, 1, 0].view(torch.float32)[:16].view(2, 2, 4)
+    lengths = wide["dk"][1, 2, 3].view(torch.int32)[:2]
+    lengths.copy_(torch.tensor([4, 3]))
+    table, dtable = wide["dv"][0, 0, 3].view(32, 2), wide["dq"][1, 3, 0].view(32, 2)
+    table.copy_(torch.randn(32, 2, generator=g, device="cuda"))
+    options = dict(key_lengths=lengths, bias_table=table, p=0.1, seed=3)
+    rng.rng_attention_fwd(part["q"], part["k"], part["v"], part["o"], lse=lse, **options)
+    rng.rng_attention_bwd(part["do"], part["q"], part["k"], part["v"], part["o"], lse, part["dq"], part["dk"], part["dv"],
+                          dbias_table=dtable, **options)
+    own = {n: t.contiguous() for n, t in part.items()}
+    options.update(key_lengths=lengths.clone(), bias_table=table.clone())
+    lse2, dtable2 = torch.empty(2, 2, 4, device="cuda"), torch.empty(32, 2, device="cuda").bfloat16()
+    out = {n: torch.empty_like(own[n]) for n in ("o", "dq", "dk", "dv")}
+    rng.rng_attention_fwd(own["q"], own["k"], own["v"], out["o"], lse=lse2, **options)
+    rng.rng_attention_bwd(own["do"], own["q"], own["k"], own["v"], out["o"], lse2, out["dq"], out["dk"], out["dv"],
+                          dbias_table=dtable2, **options)
+    assert all(torch.equal(out[n], part[n]) for n in out)
+    assert torch.equal(lse, lse2) and torch.equal(dtable, dtable2)
