@@ -877,7 +877,7 @@ __global__ void __launch_bounds__(256) table_kernel(const __grid_constant__ BwdP
 {
     __shared__ float sums[8];
     const Attention &a = p.a;
-    const int32_t n = blockIdx.x, head = blockIdx.y;
+    const int32_t n = blockIdx.y, head = blockIdx.x;
     float s = 0.0f;
     for (int64_t r = threadIdx.x; r < static_cast<int64_t>(a.batch) * p.q_tiles; r += 256)
         s += p.sums[((r / p.q_tiles * a.heads + head) * p.q_tiles + r % p.q_tiles) * a.buckets.total + n];
@@ -1012,7 +1012,7 @@ cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s)
     if (e == cudaSuccess)
         e = f.dim == 64 ? launch_both<T, 64>(p, has_q, has_k, s) : launch_both<T, 128>(p, has_q, has_k, s);
     if (e == cudaSuccess && a.dtable && a.heads) {
-        table_kernel<T><<<dim3(a.buckets.total, a.heads), 256, 0, s>>>(p);
+        table_kernel<T><<<dim3(a.heads, a.buckets.total), 256, 0, s>>>(p);
         note_launch();
         e = cudaGetLastError();
     }

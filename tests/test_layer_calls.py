@@ -192,6 +192,27 @@ def test_rows_whose_three_sums_pass_2_to_32(torch, rng):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.gpu
+def test_more_heads_than_a_grids_second_dimension(torch, rng):
+    """The table's gradient of 70000 heads: the same bits as of two halves."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, k, v, do = (torch.randn(1, 2, 70000, 8, generator=g, device="cuda").bfloat16() for _ in range(4))
+    table = torch.randn(4, 70000, generator=g, device="cuda").bfloat16()
+
+    def gradient(heads):
+        part = [t[:, :, heads].contiguous() for t in (q, k, v, do)]
+        bias = table[:, heads].contiguous()
+        o, lse = torch.empty_like(part[0]), torch.empty(1, part[0].shape[2], 2, device="cuda")
+        rng.rng_attention_fwd(*part[:3], o, lse=lse, bias_table=bias, max_distance=2)
+        out = [torch.full_like(t, float("nan")) for t in (*part[:3], bias)]
+        rng.rng_attention_bwd(part[3], *part[:3], o, lse, *out[:3], bias_table=bias, dbias_table=out[3], max_distance=2)
+        return out[3]
+
+    whole = gradient(slice(0, 70000))
+    assert bool(whole.isfinite().all()) and float(whole.abs().max()) > 0.1
+    assert torch.equal(whole, torch.cat([gradient(slice(0, 35000)), gradient(slice(35000, 70000))], 1))
+
+
 # ---- overlaps (nothing below reaches the GPU) -----------------------------------------
 
 A = 0x10000000  # an address that is never dereferenced
