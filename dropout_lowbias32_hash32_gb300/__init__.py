@@ -493,6 +493,8 @@ def _attention(name, q, k, v, o, lse, key_lengths, causal, queries_last, scale, 
         if bias_table.dim() != 2 or bias_table.shape[1] != heads:
             raise ValueError(f"bias_table has shape {tuple(bias_table.shape)}, not [num_buckets, heads]")
         buckets = bias_table.shape[0]
+        if buckets == 0:  # whose null pointer would say that there is no table
+            raise ValueError("bias_table has no buckets")
     elif dbias_table is not None:
         raise ValueError("dbias_table without a bias_table")
     pt = _flat(bias_table, "bias_table", buckets * heads, q, "q", q.dtype)

@@ -213,6 +213,18 @@ def test_more_heads_than_a_grids_second_dimension(torch, rng):
     assert torch.equal(whole, torch.cat([gradient(slice(0, 35000)), gradient(slice(35000, 70000))], 1))
 
 
+@pytest.mark.gpu
+def test_a_table_without_buckets_is_refused(torch, rng):
+    q = torch.randn(1, 4, 2, 64, device="cuda").bfloat16()
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 4, device="cuda")
+    none = torch.empty(0, 2, device="cuda").bfloat16()
+    with pytest.raises(ValueError, match="no buckets"):
+        rng.rng_attention_fwd(q, q, q, o, bias_table=none)
+    rng.rng_attention_fwd(q, q, q, o, lse=lse)
+    with pytest.raises(ValueError, match="no buckets"):
+        rng.rng_attention_bwd(q, q, q, q, o, lse, *(torch.empty_like(q) for _ in range(3)), bias_table=none)
+
+
 # ---- overlaps (nothing below reaches the GPU) -----------------------------------------
 
 A = 0x10000000  # an address that is never dereferenced
