@@ -107,13 +107,16 @@ __host__ __device__ __forceinline__ int32_t bias_reach(const Buckets &b) { retur
 inline bool has_bias(const Attention &a) { return a.table != nullptr || !(a.scale > 0.0f); }
 
 // Whether P and dS enter the products that follow as two 16-bit terms, the
-// rounded value and what rounding left; length is the queries' (backward: the
-// shorter one).  One rounding adds an error as large as
-// the output's own: 1.4 of it together over many rows, but up to 1.7 over few,
-// where chance decides.  Few rows are bound by latency, which the second term
-// adds nothing to (one query of 8 heads, 301 keys: 17 us either way); with
-// 1024 rows it already costs (32 x 8192 cached keys: 112 us, 97 without).
-inline bool two_terms(const Attention &a, int64_t length) { return length * a.batch * a.heads <= 512; }
+// rounded value and what rounding left.  One rounding adds an error as large as
+// the output's own: 1.4 of it together over many pairs, but up to 1.7 over few,
+// where chance decides.  The rule looks at a single batch entry, so that what a
+// request is batched with does not change its rounding.  So few pairs alone are
+// bound by latency (a token of 8 heads, 301 keys: 8.9 us, 8.6 with one term); in
+// large batches the second term costs (512 entries of 60 x 60 positions, 8 heads,
+// p = 0.1: forward 105 and 99 us, backward 160 and 136; 16 tokens of 16 heads,
+// 4096 keys, which are the bound: 45 and 38), and above the bound it would cost
+// as much at any size.
+inline bool two_terms(const Attention &a) { return static_cast<int64_t>(a.len_q) * a.len_k * a.heads <= 65536; }
 
 inline int32_t log2_of(int32_t power)
 {

@@ -955,9 +955,8 @@ cudaError_t launch_both(const BwdParams &p, bool queries, bool keys, cudaStream_
 template <class T, int kDim, bool kDrop, bool kBias>
 cudaError_t launch_both(const BwdParams &p, bool queries, bool keys, cudaStream_t s)
 {
-    return two_terms(p.a, p.a.len_q < p.a.len_k ? p.a.len_q : p.a.len_k)
-               ? launch_both<T, kDim, kDrop, kBias, true>(p, queries, keys, s)
-               : launch_both<T, kDim, kDrop, kBias, false>(p, queries, keys, s);
+    return two_terms(p.a) ? launch_both<T, kDim, kDrop, kBias, true>(p, queries, keys, s)
+                          : launch_both<T, kDim, kDrop, kBias, false>(p, queries, keys, s);
 }
 
 template <class T, int kDim>

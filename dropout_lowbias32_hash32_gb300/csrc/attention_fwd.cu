@@ -52,7 +52,6 @@ struct FwdParams {
     Attention a;
     int32_t pack, pack_log, units, q_tiles, splits, split_tiles;
     Divider by_splits, by_units, by_q_tiles, by_packs, by_group;
-    bool two_terms;
     float *part;  // [splits][rows][dim padded + 2]: O, max, sum
 };
 
@@ -104,7 +103,7 @@ __device__ __forceinline__ Item item_at(const FwdParams &p, uint32_t x)
     return w;
 }
 
-template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
+template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias, bool kTwoTerms>
 __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid_constant__ FwdParams p)
 {
     using S = Shape<kDim, kSplitKeys>;
@@ -242,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                             for (int i = 0; i < kKeys / 16; ++i)
                                 mma_step_tmem(at + 2 * kKeys, at + group * kKeys + i * 8, vd + i * (2048 / 16), kOut,
                                               n >= (kSplitKeys ? 2 : 1) || i > 0);
-                            if (kSplitKeys && p.two_terms)
+                            if (kTwoTerms)
 #pragma unroll
                                 for (int i = 0; i < kKeys / 16; ++i)
                                     mma_step_tmem(at + 2 * kKeys, at + group * kKeys + kKeys / 2 + i * 8, vd + i * (2048 / 16), kOut, true);
@@ -401,25 +400,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_fwd_kernel(const __grid
                         const float2 f = kBias ? mul2(add2(v, from2), base2) : fma2(v, base2, shift2);
                         return make_float2(exp2_approx(f.x), exp2_approx(f.y));
                     };
-                    if (kSplitKeys && p.two_terms)  // the second, beside where the first goes
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t q[16];
-                            for_pairs32<kDrop>(a.mask, counter + j0 + 32 * c, [&](uint32_t e, float2 k) {
-                                const float2 x = mul2(exponentials(c, e), k);
-                                q[e / 2] = rest2<T>(x, pack2<T>(x.x, x.y));
-                            });
-                            tmem_store(mine + kKeys / 2 + 16 * c, q);
-                        }
                     float2 total = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        uint32_t q[16];
+                        uint32_t q[16], rest[8];  // (which rounding left, 16 columns at a time)
                         for_pairs32<kDrop>(a.mask, counter + j0 + 32 * c, [&](uint32_t e, float2 k) {
                             float2 x = exponentials(c, e);
                             total = add2(total, x);
                             if (kDrop) x = mul2(x, k);
                             q[e / 2] = pack2<T>(x.x, x.y);
+                            if constexpr (kTwoTerms) {
+                                rest[e / 2 % 8] = rest2<T>(x, q[e / 2]);
+                                if (e % 16 == 14) tmem_store(mine + kKeys / 2 + 16 * c + e / 16 * 8, rest);  // beside P
+                            }
                         });
                         tmem_store(mine + 16 * c, q);
                     }
@@ -582,7 +575,7 @@ FwdPlan fwd_plan(const Attention &a)
     f.units = a.batch * (a.heads / f.pack);
     const int32_t rows_per = kRows / f.pack, tiles = (a.len_q + rows_per - 1) / rows_per;
     const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
-    f.split_keys = tiles == 1 || two_terms(a, a.len_q);  // whose kernel knows two terms
+    f.split_keys = tiles == 1 || two_terms(a);  // whose kernel knows two terms
     f.q_tiles = f.split_keys ? tiles : (tiles + 1) / 2;
     f.splits = 1, f.split_tiles = key_tiles < 1 ? 1 : key_tiles;
     if (f.split_keys && key_tiles > 8) {
@@ -597,11 +590,11 @@ FwdPlan fwd_plan(const Attention &a)
     return f;
 }
 
-template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias>
+template <class T, int kDim, bool kSplitKeys, bool kDrop, bool kBias, bool kTwoTerms>
 cudaError_t launch(const FwdParams &p, cudaStream_t s)
 {
     using S = Shape<kDim, kSplitKeys>;
-    const auto kernel = attention_fwd_kernel<T, kDim, kSplitKeys, kDrop, kBias>;
+    const auto kernel = attention_fwd_kernel<T, kDim, kSplitKeys, kDrop, kBias, kTwoTerms>;
     const size_t bytes = 1024 + S::kTable + (kBias ? 4 * bias_reach(p.a.buckets) * sizeof(float) : 0);
     static std::atomic<bool> done[16];
     const cudaError_t e = allow_shared(kernel, done);
@@ -616,12 +609,22 @@ cudaError_t launch(const FwdParams &p, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <class T, int kDim, bool kSplitKeys>
+template <class T, int kDim, bool kSplitKeys, bool kTwoTerms>
 cudaError_t launch(const FwdParams &p, cudaStream_t s)
 {
     const bool drop = p.a.mask.threshold != 0, bias = has_bias(p.a);
-    if (drop) return bias ? launch<T, kDim, kSplitKeys, true, true>(p, s) : launch<T, kDim, kSplitKeys, true, false>(p, s);
-    return bias ? launch<T, kDim, kSplitKeys, false, true>(p, s) : launch<T, kDim, kSplitKeys, false, false>(p, s);
+    if (drop)
+        return bias ? launch<T, kDim, kSplitKeys, true, true, kTwoTerms>(p, s)
+                    : launch<T, kDim, kSplitKeys, true, false, kTwoTerms>(p, s);
+    return bias ? launch<T, kDim, kSplitKeys, false, true, kTwoTerms>(p, s)
+                : launch<T, kDim, kSplitKeys, false, false, kTwoTerms>(p, s);
+}
+
+template <class T, int kDim>
+cudaError_t launch(const FwdParams &p, bool split_keys, cudaStream_t s)
+{
+    if (two_terms(p.a)) return launch<T, kDim, true, true>(p, s);
+    return split_keys ? launch<T, kDim, true, false>(p, s) : launch<T, kDim, false, false>(p, s);
 }
 
 }  // namespace
@@ -646,7 +649,7 @@ cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s)
     FwdParams p;
     p.a = a;
     p.pack = f.pack, p.units = f.units, p.q_tiles = f.q_tiles, p.splits = f.splits, p.split_tiles = f.split_tiles;
-    p.pack_log = log2_of(f.pack), p.two_terms = two_terms(a, a.len_q);
+    p.pack_log = log2_of(f.pack);
     p.by_splits = Divider(f.splits), p.by_units = Divider(f.units), p.by_q_tiles = Divider(f.q_tiles);
     p.by_packs = Divider(a.heads / f.pack), p.by_group = Divider(a.group);
     p.part = static_cast<float *>(a.workspace);
@@ -660,8 +663,7 @@ cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s)
         p.k = p.v = p.q;  // not read
     }
     if (e != cudaSuccess) return e;
-    if (f.dim == 64) return f.split_keys ? launch<T, 64, true>(p, s) : launch<T, 64, false>(p, s);
-    return f.split_keys ? launch<T, 128, true>(p, s) : launch<T, 128, false>(p, s);
+    return f.dim == 64 ? launch<T, 64>(p, f.split_keys, s) : launch<T, 128>(p, f.split_keys, s);
 }
 
 template cudaError_t launch_attention_fwd<__half>(const Attention &, cudaStream_t);

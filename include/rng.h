@@ -334,9 +334,10 @@ size_t rng_dropout_layer_norm_bwd_workspace(size_t rows, size_t cols);
  *
  * s, the softmax statistics and all sums are f32; P (before its division by
  * the row's sum) and, in the backward pass, P and dS are rounded to dtype as
- * the operands of the matrix products that follow; with at most 512 queries of
- * all batch entries and heads (backward: or keys) as two terms each, the value
- * and what its rounding left. */
+ * the operands of the matrix products that follow; where len_q * len_k *
+ * heads_q is at most 65536, as two terms each, the value and what its rounding
+ * left (whatever the batch).  The forward pass may split a long key axis by the
+ * number of batch entries, which changes the order of its f32 sums. */
 typedef struct rng_attention_args {
     rng_dtype dtype;
     int32_t batch, len_q, len_k, heads_q, heads_kv, head_dim;

@@ -225,6 +225,32 @@ def test_a_table_without_buckets_is_refused(torch, rng):
         rng.rng_attention_bwd(q, q, q, q, o, lse, *(torch.empty_like(q) for _ in range(3)), bias_table=none)
 
 
+# ---- what a request is batched with -----------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk,h,hk,d,p,buckets", (
+    (1, 300, 8, 8, 64, 0.0, 32), (1, 512, 16, 2, 128, 0.0, 0), (40, 40, 8, 8, 64, 0.1, 32), (77, 115, 6, 3, 40, 0.1, 0),
+    (300, 20, 8, 8, 64, 0.0, 0), (150, 200, 4, 2, 128, 0.1, 16)))
+def test_a_request_gets_the_same_bits_in_any_batch(torch, rng, lq, lk, h, hk, d, p, buckets):
+    """Entry 0 alone, of 9 and of 65 (few enough keys that their axis is not split, whose parts go by the batch)."""
+    g = torch.Generator(device="cuda").manual_seed(lq + lk)
+    q, do = (torch.randn(65, lq, h, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k, v = (torch.randn(65, lk, hk, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    table = torch.randn(buckets, h, generator=g, device="cuda").bfloat16() if buckets else None
+    results = []
+    for batch in (1, 9, 65):
+        part = [t[:batch] for t in (q, k, v)]
+        o, lse = torch.empty_like(part[0]), torch.empty(batch, h, lq, device="cuda")
+        options = dict(bias_table=table, causal=True, queries_last=lq < lk, p=p, seed=2)
+        rng.rng_attention_fwd(*part, o, lse=lse, **options)
+        out = [torch.empty_like(t) for t in part]
+        rng.rng_attention_bwd(do[:batch], *part, o, lse, *out, **options)
+        results.append([t[0].clone() for t in (o, lse, *out)])
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
 # ---- overlaps (nothing below reaches the GPU) -----------------------------------------
 
 A = 0x10000000  # an address that is never dereferenced
