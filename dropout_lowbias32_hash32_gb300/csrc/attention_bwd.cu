@@ -68,7 +68,49 @@ struct BwdParams {
     // in the natural base; -inf for a query that sees nothing), and to its scaled dP, -delta; [heads][2 reach]: the bias by relative position; [batch heads][q_tiles][buckets]: sums of dS
     float2 *stats;
     float *bias, *sums;
+    uint8_t *lost;  // [batch heads][len_pad / 32]: whether 32 queries have one whose lse is too large (below)
 };
+
+// Above 2^17 an f32 lse is 2^-7 and more off.  With a bias of the type's lowest
+// value (or highest, or the 1e9 of additive masks) for all that a query sees,
+// nothing is left in it of the logarithm of the sum of exp(s - largest s), and
+// P = exp(s - lse) would be too large by the number of such keys.  Only bf16 has
+// such values.  The sum of such a row's P is then taken again from its scores,
+// and divides them: in query_kernel with the factors of dP and delta, in
+// key_kernel by the row's first statistic, -log of the sum, after lse has been
+// taken from the scores of a tile that has such rows.  Seldom, so as simply as
+// can be; a byte for 32 queries is all that it costs others.
+template <class T, bool kBias>
+constexpr bool kMayLose = kBias && std::is_same<T, __nv_bfloat16>::value;
+constexpr float kLostFrom = 131072.0f;
+__device__ __forceinline__ bool loses(float lse) { return fabsf(lse) >= kLostFrom && fabsf(lse) < INFINITY; }
+// (Sums in another order may round a score up past lse, by a step that is not
+// small here.)  A NaN stays.
+__device__ __forceinline__ float at_most_0(float x) { return x > 0.0f ? 0.0f : x; }
+
+template <class T>
+__device__ __noinline__ float sum_again(const Attention &a, int32_t b, int32_t head, int32_t i, int32_t pos, int32_t visible,
+                                        float lse)
+{
+    const T *q = static_cast<const T *>(a.q) + b * a.qs.batch + i * a.qs.len + head * a.qs.head;
+    const T *k = static_cast<const T *>(a.k) + b * a.ks.batch + head / a.group * a.ks.head;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int32_t j = 0; j < visible; ++j, k += a.ks.len) {
+        float dot = 0.0f;
+#pragma unroll 4
+        for (int32_t d = 0; d < a.dim; d += 8) {
+            float u[8], v[8];
+            unpack<T, 8>(load<false, T, 8>(q + d), u);
+            unpack<T, 8>(load<false, T, 8>(k + d), v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(u[e], v[e], dot);
+        }
+        const float bias = to_f32(static_cast<const T *>(a.table)[bucket_of(a.buckets, static_cast<int64_t>(j) - pos) * a.heads + head]);
+        sum += exp2_approx(at_most_0(fmaf(dot, a.scale, bias) - lse) * kLog2e);
+    }
+    return sum;
+}
 
 // The bias added to N scaled scores whose relative positions descend from that
 // of `at`: from the table by relative position, or one value beyond the last
@@ -288,7 +330,6 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
         const uint32_t mine = scores_at + lanes + chain * 2 * kCols;  // S, then dS; dP kCols on
         const int32_t reach = bias_reach(a.buckets);
         const int32_t last_start = kBias ? a.buckets.starts[a.buckets.count - 2] : 0;
-        const float2 scale = make_float2(a.mask.scale, a.mask.scale);
         int32_t table_head = -1;
         // the bucket of every relative position that is tabulated (read after the item's first barrier)
         uint8_t *bucket_at = reinterpret_cast<uint8_t *>(table + 2 * reach) + reach;
@@ -347,7 +388,19 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
             delta = 0.0f;
 #pragma unroll
             for (int c = 0; c < kChains; ++c) delta += deltas[c][r];
-            if (valid && chain == 0) p.stats[index * p.len_pad + i] = make_float2(kBias ? -lse : kLift<T> - lse, -delta * kUnlift<T>);
+            const float minus_delta = -delta;
+            float share = a.mask.scale, to_key = kBias ? -lse : kLift<T> - lse;
+            bool some = false;  // of the warp's queries have too large an lse
+            if constexpr (kMayLose<T, kBias>) {
+                const bool lost = valid && loses(next_lse);
+                some = __any_sync(0xFFFFFFFFu, lost);
+                if (lost) {
+                    const float sum = sum_again<T>(a, w.b, head, i, pos, visible, lse);
+                    share /= sum, delta /= sum, to_key = -logf(sum);
+                }
+                if (chain == 0 && lane == 0 && warp_i < p.len_pad) p.lost[index * (p.len_pad / 32) + warp_i / 32] = some;
+            }
+            if (valid && chain == 0) p.stats[index * p.len_pad + i] = make_float2(to_key, minus_delta * kUnlift<T>);
             if (w.q_tile == p.q_tiles - 1)  // what key_kernel reads past the last query
                 for (int32_t t = threadIdx.x; t < p.pack * (p.len_pad - a.len_q); t += Team::kWorkers)
                     p.stats[(static_cast<int64_t>(w.b) * a.heads + w.head0 + (t & (p.pack - 1))) * p.len_pad + a.len_q + (t >> p.pack_log)] =
@@ -362,132 +415,143 @@ __global__ void __launch_bounds__(QueryShape<kDim>::Team::kThreads, 1) query_ker
                 for (int32_t t = threadIdx.x; t < 2 * reach; t += Team::kWorkers)
                     p.bias[static_cast<int64_t>(w.head0) * 2 * reach + t] = table[t];
 
-            const float2 minus = make_float2(-delta, -delta);
             float far_low = 0.0f, far_high = 0.0f;
             if (kBias && a.dtable) {
                 for (uint32_t m = lane; m < kMaxBuckets; m += 32) by_bucket[warp][m] = 0.0f;
                 __syncwarp();
             }
+            auto tiles = [&](auto lose) {
+                const float of_dp = decltype(lose)::value ? share : a.mask.scale;
+                const float2 scale = make_float2(of_dp, of_dp), minus = make_float2(-delta, -delta);
 #pragma unroll 1
-            for (int32_t n = chain; n < w.tiles; n += kChains, ++turn) {
-                barrier_wait(scored + 8 * chain, turn & 1u, &stalled);
-                tmem_fence_after();
-                if (any) {
+                for (int32_t n = chain; n < w.tiles; n += kChains, ++turn) {
+                    barrier_wait(scored + 8 * chain, turn & 1u, &stalled);
+                    tmem_fence_after();
+                    if (any) {
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        const int32_t j0 = n * kCols + 32 * c;
-                        uint32_t s[32], dp[32];
-                        tmem_load(s, mine + 32 * c);
-                        tmem_load(dp, mine + kCols + 32 * c);
-                        tmem_wait_load(s, dp);
-                        const int32_t low = j0 - (w.pos0 + warp_i + 31), high = j0 + 31 - (w.pos0 + warp_i);
-                        const bool far = high <= -last_start || low >= last_start;
-                        // the exponential's argument in base two is s by + at: of the score, with one bias for all pairs,
-                        // or of what has become of it.  A bias as large as a type's lowest value leaves nothing of s.
-                        float by = a.scale * kLog2e, at = -lse;
-                        if (kBias && far) {
-                            const float edge = table[high < 0 ? 0 : 2 * reach - 1];
-                            by = fabsf(edge) < 0x1p100f ? by : 0.0f, at = (edge - lse) * kLog2e;
-                        } else if (kBias) {
-                            by = 1.0f, at = 0.0f;
-                            const float *t = table + (j0 - pos + reach);
-                            const float2 scale = make_float2(a.scale, a.scale), from = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
+                        for (int c = 0; c < 2; ++c) {
+                            const int32_t j0 = n * kCols + 32 * c;
+                            uint32_t s[32], dp[32];
+                            tmem_load(s, mine + 32 * c);
+                            tmem_load(dp, mine + kCols + 32 * c);
+                            tmem_wait_load(s, dp);
+                            const int32_t low = j0 - (w.pos0 + warp_i + 31), high = j0 + 31 - (w.pos0 + warp_i);
+                            const bool far = high <= -last_start || low >= last_start;
+                            // the exponential's argument in base two is s by + at: of the score, with one bias for all pairs,
+                            // or of what has become of it.  A bias as large as a type's lowest value leaves nothing of s.
+                            float by = a.scale * kLog2e, at = -lse;
+                            if constexpr (decltype(lose)::value) {
+                                const float edge = table[high < 0 ? 0 : 2 * reach - 1], *t = table + (j0 - pos + reach);
+                                by = kLog2e, at = 0.0f;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                                f = mul2(add2(fma2(f, scale, make_float2(t[e], t[e + 1])), from), b2);
-                                s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
-                            }
-                        }
-                        const float2 by2 = make_float2(by, by), at2 = make_float2(at, at);
-                        // P = exp(S - lse); dS = P (dP / (1 - p) - delta), dP dropped as P was
-                        for_pairs32<kDrop>(a.mask, counter + j0, [&](uint32_t e, float2 k) {
-                            float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                            f = fma2(f, by2, at2);
-                            const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
-                            float2 d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
-                            if (kDrop) d = mul2(d, k);
-                            d = mul2(fma2(d, scale, minus), prob);
-                            s[e] = __float_as_uint(d.x), s[e + 1] = __float_as_uint(d.y);
-                        });
-                        if (j0 + 32 > warp_visible) {
-                            const int32_t seen = visible - j0;
+                                for (int e = 0; e < 32; ++e)
+                                    s[e] = __float_as_uint(at_most_0(fmaf(__uint_as_float(s[e]), a.scale, far ? edge : t[e]) - lse));
+                            } else if (kBias && far) {
+                                const float edge = table[high < 0 ? 0 : 2 * reach - 1];
+                                by = fabsf(edge) < 0x1p100f ? by : 0.0f, at = (edge - lse) * kLog2e;
+                            } else if (kBias) {
+                                by = 1.0f, at = 0.0f;
+                                const float *t = table + (j0 - pos + reach);
+                                const float2 scale = make_float2(a.scale, a.scale), from = make_float2(-lse, -lse), b2 = make_float2(kLog2e, kLog2e);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (e >= seen) s[e] = 0;
-                        }
-                        uint32_t ds[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) ds[e] = pack2<T>(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                        tmem_store(mine + 16 * c, ds);
-                        if (kTwoTerms) {  // the second, over dP
-                            uint32_t rest[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                rest[e] = rest2<T>(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), ds[e]);
-                            tmem_store(mine + kCols + 16 * c, rest);
-                        }
-                        if (c) {
-                            tmem_wait_store();
-                            tmem_fence_before();
-                            __syncwarp();
-                            if (lane == 0) barrier_arrive(ready + 8 * chain);
-                        }
-                        if (kBias && a.dtable) {
-                            if (far) {  // one bucket
-                                float2 total = make_float2(0.0f, 0.0f);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) total = add2(total, make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-                                (high <= -last_start ? far_low : far_high) += total.x + total.y;
-                            } else {
-                                // Sums along the diagonals of the warp's 32 x 32 pairs: a partial sum moves one row down
-                                // with each column; what leaves row 31, or is left in a walk's last column, is a walk's
-                                // part.  Diagonal d = 0 .. 62 is relative position low + d.
-                                constexpr int kSteps = 32 / kWalks;
-                                float acc[kWalks] = {};
-#pragma unroll
-                                for (int e = 0; e < kSteps; ++e)
-#pragma unroll
-                                    for (int k = 0; k < kWalks; ++k) {
-                                        const float before = __shfl_up_sync(0xFFFFFFFFu, acc[k], 1);
-                                        acc[k] = (lane ? before : 0.0f) + __uint_as_float(s[k * kSteps + e]);
-                                        if (lane == 31) diagonals[warp][k][k * kSteps + e] = acc[k];
-                                    }
-#pragma unroll
-                                for (int k = 0; k < kWalks; ++k)
-                                    if (lane < 31) diagonals[warp][k][(k + 1) * kSteps + 30 - lane] = acc[k];
-                                __syncwarp();
-                                // A bucket's positions follow each other, so sums over runs of one bucket: half of the
-                                // diagonals at a time, the last lane of a run adds it.
-                                int32_t bucket[2];
-                                float run[2] = {};
-#pragma unroll
-                                for (int d = 0; d < 2; ++d) {
-                                    bucket[d] = bucket_at[low + 32 * d + lane];
-#pragma unroll
-                                    for (int k = 0; k < kWalks; ++k) run[d] += diagonals[warp][k][32 * d + lane];
+                                for (int e = 0; e < 32; e += 2) {
+                                    float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                                    f = mul2(add2(fma2(f, scale, make_float2(t[e], t[e + 1])), from), b2);
+                                    s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
                                 }
+                            }
+                            const float2 by2 = make_float2(by, by), at2 = make_float2(at, at);
+                            // P = exp(S - lse); dS = P (dP / (1 - p) - delta), dP dropped as P was
+                            for_pairs32<kDrop>(a.mask, counter + j0, [&](uint32_t e, float2 k) {
+                                float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                                f = fma2(f, by2, at2);
+                                const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                                float2 d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+                                if (kDrop) d = mul2(d, k);
+                                d = mul2(fma2(d, scale, minus), prob);
+                                s[e] = __float_as_uint(d.x), s[e + 1] = __float_as_uint(d.y);
+                            });
+                            if (j0 + 32 > warp_visible) {
+                                const int32_t seen = visible - j0;
 #pragma unroll
-                                for (int m = 1; m < 32; m *= 2)
+                                for (int e = 0; e < 32; ++e)
+                                    if (e >= seen) s[e] = 0;
+                            }
+                            uint32_t ds[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) ds[e] = pack2<T>(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+                            tmem_store(mine + 16 * c, ds);
+                            if (kTwoTerms) {  // the second, over dP
+                                uint32_t rest[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    rest[e] = rest2<T>(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), ds[e]);
+                                tmem_store(mine + kCols + 16 * c, rest);
+                            }
+                            if (c) {
+                                tmem_wait_store();
+                                tmem_fence_before();
+                                __syncwarp();
+                                if (lane == 0) barrier_arrive(ready + 8 * chain);
+                            }
+                            if (kBias && a.dtable) {
+                                if (far) {  // one bucket
+                                    float2 total = make_float2(0.0f, 0.0f);
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) total = add2(total, make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                                    (high <= -last_start ? far_low : far_high) += total.x + total.y;
+                                } else {
+                                    // Sums along the diagonals of the warp's 32 x 32 pairs: a partial sum moves one row down
+                                    // with each column; what leaves row 31, or is left in a walk's last column, is a walk's
+                                    // part.  Diagonal d = 0 .. 62 is relative position low + d.
+                                    constexpr int kSteps = 32 / kWalks;
+                                    float acc[kWalks] = {};
+#pragma unroll
+                                    for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+                                        for (int k = 0; k < kWalks; ++k) {
+                                            const float before = __shfl_up_sync(0xFFFFFFFFu, acc[k], 1);
+                                            acc[k] = (lane ? before : 0.0f) + __uint_as_float(s[k * kSteps + e]);
+                                            if (lane == 31) diagonals[warp][k][k * kSteps + e] = acc[k];
+                                        }
+#pragma unroll
+                                    for (int k = 0; k < kWalks; ++k)
+                                        if (lane < 31) diagonals[warp][k][(k + 1) * kSteps + 30 - lane] = acc[k];
+                                    __syncwarp();
+                                    // A bucket's positions follow each other, so sums over runs of one bucket: half of the
+                                    // diagonals at a time, the last lane of a run adds it.
+                                    int32_t bucket[2];
+                                    float run[2] = {};
 #pragma unroll
                                     for (int d = 0; d < 2; ++d) {
-                                        const float before = __shfl_up_sync(0xFFFFFFFFu, run[d], m);
-                                        const int32_t its = __shfl_up_sync(0xFFFFFFFFu, bucket[d], m);
-                                        if (static_cast<int>(lane) >= m && its == bucket[d]) run[d] += before;
+                                        bucket[d] = bucket_at[low + 32 * d + lane];
+#pragma unroll
+                                        for (int k = 0; k < kWalks; ++k) run[d] += diagonals[warp][k][32 * d + lane];
                                     }
 #pragma unroll
-                                for (int d = 0; d < 2; ++d) {
-                                    const int32_t after = __shfl_down_sync(0xFFFFFFFFu, bucket[d], 1);
-                                    if (lane == 31 || after != bucket[d]) by_bucket[warp][bucket[d]] += run[d];
-                                    __syncwarp();
+                                    for (int m = 1; m < 32; m *= 2)
+#pragma unroll
+                                        for (int d = 0; d < 2; ++d) {
+                                            const float before = __shfl_up_sync(0xFFFFFFFFu, run[d], m);
+                                            const int32_t its = __shfl_up_sync(0xFFFFFFFFu, bucket[d], m);
+                                            if (static_cast<int>(lane) >= m && its == bucket[d]) run[d] += before;
+                                        }
+#pragma unroll
+                                    for (int d = 0; d < 2; ++d) {
+                                        const int32_t after = __shfl_down_sync(0xFFFFFFFFu, bucket[d], 1);
+                                        if (lane == 31 || after != bucket[d]) by_bucket[warp][bucket[d]] += run[d];
+                                        __syncwarp();
+                                    }
                                 }
                             }
                         }
+                    } else if (lane == 0) {
+                        barrier_arrive(ready + 8 * chain);
                     }
-                } else if (lane == 0) {
-                    barrier_arrive(ready + 8 * chain);
                 }
-            }
+            };
+            if (!some) tiles(std::false_type{});
+            else tiles(std::true_type{});
 
             // ---- the next item, and this one's result
             const int32_t x = work.next_warp();
@@ -738,96 +802,128 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
         // 577 us with 32, 611 with 16).
         constexpr int kPiece = S::kShare == 1 ? 32 : 16;
         uint32_t turn = 0, use = 0, finished = 0;
+        // Whether queries of the item have too large an lse: asked for before the previous item's result is written,
+        // which takes longer.  A lane's part of the answer.
+        auto fetch_lost = [&](const KeyItem &w) {
+            uint32_t any = 0;
+            if constexpr (kMayLose<T, kBias>) {
+                const int32_t words = p.len_pad / kCols * a.group;  // of two bytes, the heads' one after the other (a q of 2^31 would be 2 TB)
+                const uint16_t *of_heads = reinterpret_cast<const uint16_t *>(p.lost) +
+                                           (static_cast<int64_t>(w.b) * a.heads_kv + w.head_kv) * words;
+#pragma unroll 1
+                for (int32_t x = lane + 32; x < words; x += 32) any |= of_heads[x];
+                if (lane < words) any |= of_heads[lane];
+            }
+            return any;
+        };
         KeyItem w = key_item(p, blockIdx.x);
+        uint32_t lost = fetch_lost(w);
         for (;;) {
             const int32_t j = w.j0 + r, warp_j = w.j0 + (warp % 4) * 32;
             const bool any = warp_j < w.keys;
-            int32_t head = w.head_kv * a.group, t = chain;  // tile n is tile t of a head's
+            const bool some = kMayLose<T, kBias> && __any_sync(0xFFFFFFFFu, lost != 0u);
+            auto tiles = [&](auto lose) {
+                int32_t head = w.head_kv * a.group, t = chain;  // tile n is tile t of a head's
 #pragma unroll 1
-            for (int32_t n = chain; n < w.tiles; n += kChains, t += kChains, ++turn) {
-                while (t >= w.per_head) t -= w.per_head, ++head;
-                const int32_t i0 = (w.begin + t) * kCols;
-                const float4 *tile_stats = reinterpret_cast<const float4 *>(smem + S::kStats + (use + n) % S::kStages * kCols * sizeof(float2));
-                barrier_wait(scored + 8 * chain, turn & 1u, &stalled);
-                tmem_fence_after();
-                if (any) {
+                for (int32_t n = chain; n < w.tiles; n += kChains, t += kChains, ++turn) {
+                    while (t >= w.per_head) t -= w.per_head, ++head;
+                    const int32_t i0 = (w.begin + t) * kCols;
+                    const float4 *tile_stats = reinterpret_cast<const float4 *>(smem + S::kStats + (use + n) % S::kStages * kCols * sizeof(float2));
+                    barrier_wait(scored + 8 * chain, turn & 1u, &stalled);
+                    tmem_fence_after();
+                    if (any) {
 #pragma unroll 1
-                    for (int at = half * kCols / S::kShare; at < (half + 1) * kCols / S::kShare; at += kPiece) {
-                        const float4 *stats = tile_stats + at / 2;
-                        uint32_t s[kPiece], dp[kPiece];  // S^T, dP^T
-                        tmem_load(s, mine + at);
-                        tmem_load(dp, mine + kCols + at);
-                        tmem_wait_load(s, dp);
-                        const int32_t ic = i0 + at, rel = j - w.pos0 - ic;  // to the first of kPiece queries
-                        const int32_t low = warp_j - w.pos0 - ic - kPiece + 1, high = warp_j + 31 - w.pos0 - ic;
-                        const uint32_t counter = a.first + ((static_cast<uint32_t>(w.b) * a.heads + head) * a.len_q + ic) * static_cast<uint32_t>(a.len_k) + j;
-                        if (kBias) {
-                            const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
-                            const bool far = high <= -last_start || low >= last_start;
-                            add_bias(s, a.scale, bias, rel + reach, far, far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f);
+                        for (int at = half * kCols / S::kShare; at < (half + 1) * kCols / S::kShare; at += kPiece) {
+                            const float4 *stats = tile_stats + at / 2;
+                            uint32_t s[kPiece], dp[kPiece];  // S^T, dP^T
+                            tmem_load(s, mine + at);
+                            tmem_load(dp, mine + kCols + at);
+                            tmem_wait_load(s, dp);
+                            const int32_t ic = i0 + at, rel = j - w.pos0 - ic;  // to the first of kPiece queries
+                            const int32_t low = warp_j - w.pos0 - ic - kPiece + 1, high = warp_j + 31 - w.pos0 - ic;
+                            const uint32_t counter = a.first + ((static_cast<uint32_t>(w.b) * a.heads + head) * a.len_q + ic) * static_cast<uint32_t>(a.len_k) + j;
+                            if (kBias) {
+                                const float *bias = p.bias + static_cast<int64_t>(head) * 2 * reach;
+                                const bool far = high <= -last_start || low >= last_start;
+                                const float edge = far ? bias[high < 0 ? 0 : 2 * reach - 1] : 0.0f;
+                                if constexpr (decltype(lose)::value) {
+                                    const float *lse = a.lse + (static_cast<int64_t>(w.b) * a.heads + head) * a.len_q;
+#pragma unroll
+                                    for (int e = 0; e < kPiece; ++e) {
+                                        const float x = fmaf(__uint_as_float(s[e]), a.scale, far ? edge : bias[rel + reach - e]);
+                                        const float shift = lse[min(ic + e, a.len_q - 1)];
+                                        s[e] = __float_as_uint(loses(shift) ? at_most_0(x - shift) : x);
+                                    }
+                                } else {
+                                    add_bias(s, a.scale, bias, rel + reach, far, edge);
+                                }
+                            }
+                            // P = exp(S - lse), dropped for dv; dS = P (dropout(dP) - delta) for dk
+                            auto pair = [&](int e, float2 &kept2, float2 &d) {
+                                const float4 st = stats[e / 2];  // two queries' -lse, -delta
+                                float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                                f = kBias ? fma2(add2(f, make_float2(st.x, st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>))
+                                          : fma2(f, make_float2(to_base2, to_base2), make_float2(st.x, st.z));
+                                const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                                kept2 = prob, d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
+                                if (kDrop) {
+                                    const uint32_t step = a.len_k;
+                                    const float2 k = make_float2(kept(a.mask, mad_lo(e, step, counter)), kept(a.mask, mad_lo(e + 1, step, counter)));
+                                    kept2 = mul2(kept2, k), d = mul2(d, k);
+                                }
+                                d = mul2(fma2(d, make_float2(scale, scale), make_float2(st.y, st.w)), prob);
+                            };
+                            // query ic + e sees key j from e = rel on
+                            auto seen = [&](int e) { return (e < rel ? 0u : 0xFFFFu) | (e + 1 < rel ? 0u : 0xFFFF0000u); };
+                            if (kTwoTerms) {  // of 16 columns, the second term's 8 after the first's
+                                uint32_t rest_p[kPiece / 2], rest_d[kPiece / 2];
+#pragma unroll
+                                for (int e = 0; e < kPiece; e += 2) {
+                                    float2 kept2, d;
+                                    pair(e, kept2, d);
+                                    const uint32_t mask = a.causal ? seen(e) : ~0u;
+                                    s[e / 2] = pack2<T>(kept2.x, kept2.y), dp[e / 2] = pack2<T>(d.x, d.y);
+                                    rest_p[e / 2] = rest2<T>(kept2, s[e / 2]) & mask, rest_d[e / 2] = rest2<T>(d, dp[e / 2]) & mask;
+                                    s[e / 2] &= mask, dp[e / 2] &= mask;
+                                }
+#pragma unroll
+                                for (int e = 0; e < kPiece / 2; e += 8) {
+                                    const uint32_t to = mine + at + 2 * e;
+                                    tmem_store(to, reinterpret_cast<const uint32_t(&)[8]>(s[e]));
+                                    tmem_store(to + 8, reinterpret_cast<const uint32_t(&)[8]>(rest_p[e]));
+                                    tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[8]>(dp[e]));
+                                    tmem_store(to + kCols + 8, reinterpret_cast<const uint32_t(&)[8]>(rest_d[e]));
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < kPiece; e += 2) {
+                                    float2 kept2, d;
+                                    pair(e, kept2, d);
+                                    s[e / 2] = pack2<T>(kept2.x, kept2.y), dp[e / 2] = pack2<T>(d.x, d.y);
+                                }
+                                if (a.causal && high > 0)
+#pragma unroll
+                                    for (int e = 0; e < kPiece; e += 2) s[e / 2] &= seen(e), dp[e / 2] &= seen(e);
+                                const uint32_t to = mine + at / 32 * S::kPitch + at % 32 / 2;
+                                tmem_store(to, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(s));
+                                tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(dp));
+                            }
                         }
-                        // P = exp(S - lse), dropped for dv; dS = P (dropout(dP) - delta) for dk
-                        auto pair = [&](int e, float2 &kept2, float2 &d) {
-                            const float4 st = stats[e / 2];  // two queries' -lse, -delta
-                            float2 f = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                            f = kBias ? fma2(add2(f, make_float2(st.x, st.z)), make_float2(kLog2e, kLog2e), make_float2(kLift<T>, kLift<T>))
-                                      : fma2(f, make_float2(to_base2, to_base2), make_float2(st.x, st.z));
-                            const float2 prob = make_float2(exp2_approx(f.x), exp2_approx(f.y));
-                            kept2 = prob, d = make_float2(__uint_as_float(dp[e]), __uint_as_float(dp[e + 1]));
-                            if (kDrop) {
-                                const uint32_t step = a.len_k;
-                                const float2 k = make_float2(kept(a.mask, mad_lo(e, step, counter)), kept(a.mask, mad_lo(e + 1, step, counter)));
-                                kept2 = mul2(kept2, k), d = mul2(d, k);
-                            }
-                            d = mul2(fma2(d, make_float2(scale, scale), make_float2(st.y, st.w)), prob);
-                        };
-                        // query ic + e sees key j from e = rel on
-                        auto seen = [&](int e) { return (e < rel ? 0u : 0xFFFFu) | (e + 1 < rel ? 0u : 0xFFFF0000u); };
-                        if (kTwoTerms) {  // of 16 columns, the second term's 8 after the first's
-                            uint32_t rest_p[kPiece / 2], rest_d[kPiece / 2];
-#pragma unroll
-                            for (int e = 0; e < kPiece; e += 2) {
-                                float2 kept2, d;
-                                pair(e, kept2, d);
-                                const uint32_t mask = a.causal ? seen(e) : ~0u;
-                                s[e / 2] = pack2<T>(kept2.x, kept2.y), dp[e / 2] = pack2<T>(d.x, d.y);
-                                rest_p[e / 2] = rest2<T>(kept2, s[e / 2]) & mask, rest_d[e / 2] = rest2<T>(d, dp[e / 2]) & mask;
-                                s[e / 2] &= mask, dp[e / 2] &= mask;
-                            }
-#pragma unroll
-                            for (int e = 0; e < kPiece / 2; e += 8) {
-                                const uint32_t to = mine + at + 2 * e;
-                                tmem_store(to, reinterpret_cast<const uint32_t(&)[8]>(s[e]));
-                                tmem_store(to + 8, reinterpret_cast<const uint32_t(&)[8]>(rest_p[e]));
-                                tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[8]>(dp[e]));
-                                tmem_store(to + kCols + 8, reinterpret_cast<const uint32_t(&)[8]>(rest_d[e]));
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < kPiece; e += 2) {
-                                float2 kept2, d;
-                                pair(e, kept2, d);
-                                s[e / 2] = pack2<T>(kept2.x, kept2.y), dp[e / 2] = pack2<T>(d.x, d.y);
-                            }
-                            if (a.causal && high > 0)
-#pragma unroll
-                                for (int e = 0; e < kPiece; e += 2) s[e / 2] &= seen(e), dp[e / 2] &= seen(e);
-                            const uint32_t to = mine + at / 32 * S::kPitch + at % 32 / 2;
-                            tmem_store(to, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(s));
-                            tmem_store(to + kCols, reinterpret_cast<const uint32_t(&)[kPiece / 2]>(dp));
-                        }
+                        tmem_wait_store();
                     }
-                    tmem_wait_store();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(ready + 8 * chain);
                 }
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) barrier_arrive(ready + 8 * chain);
-            }
+            };
+            if (some) tiles(std::true_type{});
+            else tiles(std::false_type{});
             use += w.tiles;
 
             // ---- the next item, and this one's result: chain 0's threads write dv, chain 1's dk
             const int32_t x = work.next_warp();
             const KeyItem next = x >= 0 ? key_item(p, x) : w;
+            lost = fetch_lost(next);
             if (w.tiles) {
                 barrier_wait(done, finished++ & 1u, &stalled);
                 tmem_fence_after();
@@ -896,7 +992,7 @@ __global__ void __launch_bounds__(256) table_kernel(const __grid_constant__ BwdP
 // How a call is cut, and where its workspace's parts begin (in floats).
 struct BwdPlan {
     int32_t dim, pack, units, q_tiles, len_pad;
-    size_t bias, sums, floats;
+    size_t bias, sums, lost, floats;
 };
 
 BwdPlan bwd_plan(const Attention &a)
@@ -911,7 +1007,8 @@ BwdPlan bwd_plan(const Attention &a)
     const size_t heads = static_cast<size_t>(a.batch) * a.heads;
     f.bias = 2 * heads * f.len_pad;
     f.sums = f.bias + (a.table ? static_cast<size_t>(a.heads) * 2 * bias_reach(a.buckets) : 0);
-    f.floats = f.sums + (a.dtable ? heads * f.q_tiles * a.buckets.total : 0);
+    f.lost = f.sums + (a.dtable ? heads * f.q_tiles * a.buckets.total : 0);
+    f.floats = f.lost + (a.table ? (heads * (f.len_pad / 32) + 3) / 4 : 0);
     return f;
 }
 
@@ -990,6 +1087,7 @@ cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s)
     p.by_group = Divider(a.group), p.by_key_units = Divider(a.batch * a.heads_kv), p.by_heads_kv = Divider(a.heads_kv);
     float *ws = static_cast<float *>(a.workspace);
     p.stats = reinterpret_cast<float2 *>(ws), p.bias = ws + f.bias, p.sums = ws + f.sums;
+    p.lost = reinterpret_cast<uint8_t *>(ws + f.lost);
     const bool has_q = a.batch && a.heads && a.len_q, has_k = a.batch && a.heads_kv && a.len_k;
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     cudaError_t e = cudaSuccess;

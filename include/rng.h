@@ -375,7 +375,10 @@ rng_status rng_attention_fwd(const rng_attention_args *args, void *stream);
  *   dS = P (dP - delta),  dq = scale sum_j dS k,  dk = scale sum_i dS q,
  *   dv = sum_i dropout(P) d_o,  dbias_table[n, a] = sum of dS in bucket n.
  * dk and dv of a key head are summed over its query heads.  No atomics: the
- * results are the same bits every time. */
+ * results are the same bits every time.  P = exp(s - lse); where biases leave
+ * nothing of the sum in an f32 lse (above 2^17, which bf16 has), the sum is
+ * taken again, so that a row's P add up to 1 there too (slowly: one thread a
+ * query). */
 rng_status rng_attention_bwd(const rng_attention_args *args, void *stream);
 
 /* Bytes of workspace on the current device (sizes, scale and

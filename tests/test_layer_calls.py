@@ -379,3 +379,58 @@ def test_attention_beside_its_heads_is_fine(torch, rng):
                           dbias_table=dtable2, **options)
     assert all(torch.equal(out[n], part[n]) for n in out)
     assert torch.equal(lse, lse2) and torch.equal(dtable, dtable2)
+
+
+# ---- biases that a score is lost beside -------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("value", (-3.3895313892515355e38, -1e9, 3e38))
+@pytest.mark.parametrize("lq,lk,hk,d,causal,p", ((90, 90, 3, 64, False, 0.0), (200, 150, 3, 128, True, 0.1),
+                                                 (150, 700, 1, 64, True, 0.0), (9, 70, 1, 64, False, 0.0),
+                                                 (300, 270, 1, 72, False, 0.1)))
+def test_gradients_of_rows_whose_biases_are_all_as_large(torch, rng, orc, lq, lk, hk, d, causal, p, value):
+    """Head 0 has such an entry in every bucket, head 1 in the first few alone
+    (so some of its rows see nothing else), head 2 has none.  An f32 score keeps
+    nothing (or, beside 1e9, some) of q and k; a row's probabilities still add up
+    to 1.  Where nothing is left they are one over the number of keys with the
+    entry that wins, and the gradients are the formulas' with them."""
+    import layer_reference as ref
+    g = torch.Generator(device="cuda").manual_seed(lq)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+    q, do = normal(2, lq, 3, d), normal(2, lq, 3, d)
+    k, v, table = normal(2, lk, hk, d), normal(2, lk, hk, d), normal(16, 3)
+    table[:, 0] = value
+    table[:5, 1] = value
+    o, lse = torch.empty_like(q), torch.empty(2, 3, lq, device="cuda")
+    options = dict(bias_table=table, max_distance=64, bidirectional=False, causal=causal, p=p, seed=4)
+    rng.rng_attention_fwd(q, k, v, o, lse=lse, **options)
+    out = [torch.full_like(t, float("nan")) for t in (q, k, v, table)]
+    rng.rng_attention_bwd(do, q, k, v, o, lse, *out[:3], dbias_table=out[3], **options)
+    pairs = ref.Pairs(orc, q, k, None, causal, False, 16, 64, False, p, 4, 0)
+    if p == 0.0:  # sum over j of dv = sum over i of (sum over j of P) do, with P rounded to 2^-8 of itself
+        heads = do.double().unflatten(2, (hk, -1))
+        assert bool(((out[2].double().sum(1) - heads.sum((1, 3))).abs() <= 2.0 ** -7 * heads.abs().sum((1, 3))).all())
+    if abs(value) < 1e30:
+        return
+    # (64 bits would lose the sum's logarithm beside such a score as well)
+    prob = ref.scores(q, k, table, pairs, d ** -0.5).softmax(-1)
+    want = ((prob * pairs.keep) @ ref.heads_first(v, 3 // hk)).transpose(1, 2)
+    ut, av = 2.0 ** -8, ref.heads_first(v, 3 // hk).abs()
+    # two roundings of P, 2^-19 for its exponential (whose argument is exact here, or a score's), and one of o
+    tol = ((2 * ut + 2.0 ** -17) * (prob * pairs.keep) @ av).transpose(1, 2) + ut * want.abs() + 2.0 ** -20
+    assert bool(((o.double() - want).abs() <= tol).all())
+    dq, dk, dv, dtable, ds = ref.attention_bwd(do, q, k, v, o, table, pairs, prob, d ** -0.5)
+    # dS and P rounded once, the f32 sums behind dP - delta, the result rounded once
+    ado, ao, aq, ak = *(ref.heads_first(t).abs() for t in (do, o, q)), ref.heads_first(k, 3 // hk).abs()
+    err = (d + 8) * 2.0 ** -23 * (ado @ av.transpose(2, 3) / (1 - p) + (ado * ao).sum(-1, keepdim=True))
+    w = (ut + 2.0 ** -17) * ds.abs() + 2 * prob * err
+    assert bool(((out[0].double() - dq).abs() <= (w @ ak * d ** -0.5).transpose(1, 2) + ut * dq.abs() + 1e-30).all())
+    assert bool(((out[1].double() - dk).abs() <= ref.shared(w.transpose(2, 3) @ aq * d ** -0.5, hk) + ut * dk.abs() + 1e-30).all())
+    wv = (ut + 2.0 ** -17) * prob * pairs.keep
+    assert bool(((out[2].double() - dv).abs() <= ref.shared(wv.transpose(2, 3) @ ado, hk) + ut * dv.abs() + 1e-30).all())
+    tol = ref.by_bucket((2.0 ** -17 + 2.0 ** -12) * ds.abs() + 2 * prob * err, table, pairs)
+    assert bool(((out[3].double() - dtable).abs() <= tol + ut * dtable.abs() + 1e-30).all())
