@@ -520,14 +520,36 @@ def _attention(name, q, k, v, o, lse, key_lengths, causal, queries_last, scale, 
     del hold
 
 
-def rng_attention_fwd_workspace(args: AttentionArgs) -> int:
-    """Bytes of workspace of rng_attention_fwd on the current device."""
-    return _lib.rng_attention_fwd_workspace(C.byref(args))
+def _attention_workspace(name, q, k, scale, bias_table, dbias_table, max_distance, bidirectional) -> int:
+    if isinstance(q, AttentionArgs):
+        return getattr(_lib, name)(C.byref(q))
+    code = _first(q, "q")
+    if q.dim() != 4 or k is None or k.dim() != 4:
+        raise ValueError("q and k must be [batch, length, heads, head_dim]")
+    batch, len_q, heads, dim = q.shape
+    table = 0 if bias_table is None else bias_table.data_ptr()
+    buckets = bias_table.shape[0] if table else 0
+    args = _pack_attention(code, batch, len_q, k.shape[1], heads, k.shape[2], dim, 0, 0, 0, *(0,) * 9, 0, 0, 0, 0, 0, 0,
+                           False, False, dim ** -0.5 if scale is None else scale, table, buckets,
+                           max_distance if buckets else 0, bool(bidirectional), 0.0, 0, 0, *(0,) * 16,
+                           0 if dbias_table is None else dbias_table.data_ptr(), 0, 0)
+    with _Current(q.get_device()):
+        return getattr(_lib, name)(args)
 
 
-def rng_attention_bwd_workspace(args: AttentionArgs) -> int:
-    """Bytes of workspace of rng_attention_bwd on the current device."""
-    return _lib.rng_attention_bwd_workspace(C.byref(args))
+def rng_attention_fwd_workspace(q, k=None, *, scale=None, bias_table=None, max_distance=128, bidirectional=True) -> int:
+    """Bytes of workspace of rng_attention_fwd for q and k on their device (or
+    of an AttentionArgs on the current one); 0 also where the call itself would
+    be refused."""
+    return _attention_workspace("rng_attention_fwd_workspace", q, k, scale, bias_table, None, max_distance,
+                                bidirectional)
+
+
+def rng_attention_bwd_workspace(q, k=None, *, scale=None, bias_table=None, dbias_table=None, max_distance=128,
+                                bidirectional=True) -> int:
+    """Bytes of workspace of rng_attention_bwd, likewise."""
+    return _attention_workspace("rng_attention_bwd_workspace", q, k, scale, bias_table, dbias_table, max_distance,
+                                bidirectional)
 
 
 def rng_attention_fwd(q, k, v, o, *, lse=None, key_lengths=None, causal=False, queries_last=False, scale=None,

@@ -136,6 +136,91 @@ def test_a_call_on_another_stream_keeps_off_the_current_ones_workspace(torch, rn
                 t.zero_()
 
 
+# ---- the caller's workspace ------------------------------------------------------------
+
+
+def guarded(torch, size):
+    """A workspace of that many bytes, all of them NaN in every type, and what lies around it."""
+    store = torch.full((size + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    return store[256:256 + size], lambda: bool((store[:256] == 0xFF).all() and (store[256 + size:] == 0xFF).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk,h,hk,d,dtype,buckets", ((1, 9000, 8, 2, 128, "bfloat16", 0), (3, 4000, 4, 4, 64, "float16", 32),
+                                                        (130, 700, 6, 3, 72, "bfloat16", 16), (257, 257, 4, 1, 64, "float16", 0)))
+def test_attention_in_a_workspace_of_the_callers(torch, rng, lq, lk, h, hk, d, dtype, buckets):
+    g = torch.Generator(device="cuda").manual_seed(lq)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(getattr(torch, dtype))
+
+    q, do, k, v = normal(2, lq, h, d), normal(2, lq, h, d), normal(2, lk, hk, d), normal(2, lk, hk, d)
+    table = normal(buckets, h) if buckets else None
+    options = dict(bias_table=table, max_distance=100)
+    results = []
+    for own in (False, True):
+        o, lse = torch.full_like(q, float("nan")), torch.full((2, h, lq), float("nan"), device="cuda")
+        out = [torch.full_like(t, float("nan")) for t in (q, k, v)]
+        dtable = None if table is None else torch.full_like(table, float("nan"))
+        fwd, bwd, beside = {}, {}, []
+        if own:
+            sizes = (rng.rng_attention_fwd_workspace(q, k, **options),
+                     rng.rng_attention_bwd_workspace(q, k, dbias_table=dtable, **options))
+            assert sizes[1] > 0 and (sizes[0] > 0) == (lq < 5)
+            (fwd["workspace"], a), (bwd["workspace"], b) = (guarded(torch, n) for n in sizes)
+            beside = [a, b]
+            if sizes[0]:
+                with pytest.raises(rng.RngError, match="workspace"):
+                    rng.rng_attention_fwd(q, k, v, o, lse=lse, workspace=fwd["workspace"][:-4], **options)
+            with pytest.raises(rng.RngError, match="workspace"):
+                rng.rng_attention_bwd(do, q, k, v, o, lse, *out, dbias_table=dtable, workspace=bwd["workspace"][:-4], **options)
+        common = dict(causal=True, queries_last=True, p=0.1, seed=5, **options)
+        rng.rng_attention_fwd(q, k, v, o, lse=lse, **common, **fwd)
+        rng.rng_attention_bwd(do, q, k, v, o, lse, *out, dbias_table=dtable, **common, **bwd)
+        assert all(untouched() for untouched in beside)
+        results.append([o, lse, *out] + ([] if table is None else [dtable]))
+    assert all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(*results))
+
+
+@pytest.mark.gpu
+def test_workspace_sizes_of_tensors_and_of_the_struct(torch, rng):
+    q = torch.empty(2, 300, 4, 64, device="cuda", dtype=torch.float16)
+    k = torch.empty(2, 77, 2, 64, device="cuda", dtype=torch.float16)
+    table = torch.empty(32, 4, device="cuda", dtype=torch.float16)
+    a = rng.AttentionArgs(dtype=rng.RNG_F16, batch=2, len_q=300, len_k=77, heads_q=4, heads_kv=2, head_dim=64, scale=0.125)
+    assert rng.rng_attention_bwd_workspace(q, k) == rng.rng_attention_bwd_workspace(a)
+    assert rng.rng_attention_fwd_workspace(q, k) == rng.rng_attention_fwd_workspace(a)
+    a.bias_table, a.num_buckets, a.max_distance, a.bidirectional = table.data_ptr(), 32, 64, 1
+    assert rng.rng_attention_bwd_workspace(q, k, bias_table=table, max_distance=64) == rng.rng_attention_bwd_workspace(a)
+    a.dbias_table = table.data_ptr()
+    size = rng.rng_attention_bwd_workspace(q, k, bias_table=table, dbias_table=table, max_distance=64)
+    assert size == rng.rng_attention_bwd_workspace(a) > 0
+    with pytest.raises(ValueError):
+        rng.rng_attention_fwd_workspace(q)
+    with pytest.raises(TypeError):
+        rng.rng_attention_fwd_workspace(q.cpu(), k.cpu())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,cols,dtype", ((700, 1024, "bfloat16"), (70, 769, "float16"), (40, 9000, "float32"),
+                                             (3000, 64, "bfloat16")))
+def test_norm_backward_in_a_workspace_of_the_callers(torch, rng, rows, cols, dtype):
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    dy, h = (torch.randn(rows, cols, generator=g, device="cuda").to(getattr(torch, dtype)) for _ in range(2))
+    mean, rstd = torch.randn(rows, generator=g, device="cuda"), torch.rand(rows, generator=g, device="cuda") + 0.5
+    size = rng.rng_dropout_layer_norm_bwd_workspace(rows, cols)
+    workspace, untouched = guarded(torch, size)
+    results = []
+    for more in ({}, {"workspace": workspace}):
+        dx = torch.full_like(dy, float("nan"))
+        grads = [torch.full((cols,), float("nan"), device="cuda", dtype=dy.dtype) for _ in range(3)]
+        rng.rng_dropout_layer_norm_bwd(dy, h, None, mean, rstd, dx, *grads[:2], dbias=grads[2], p=0.2, seed=8, **more)
+        results.append([dx, *grads])
+    assert untouched() and all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(*results))
+    with pytest.raises(rng.RngError, match="workspace"):
+        rng.rng_dropout_layer_norm_bwd(dy, h, None, mean, rstd, dx, *grads[:2], workspace=workspace[:-4])
+
+
 # ---- sizes ---------------------------------------------------------------------------
 
 
