@@ -519,3 +519,45 @@ def test_gradients_of_rows_whose_biases_are_all_as_large(torch, rng, orc, lq, lk
     assert bool(((out[2].double() - dv).abs() <= ref.shared(wv.transpose(2, 3) @ ado, hk) + ut * dv.abs() + 1e-30).all())
     tol = ref.by_bucket((2.0 ** -17 + 2.0 ** -12) * ds.abs() + 2 * prob * err, table, pairs)
     assert bool(((out[3].double() - dtable).abs() <= tol + ut * dtable.abs() + 1e-30).all())
+
+
+# ---- captured, and again -----------------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lq,lk,buckets", ((150, 150, 32), (1, 5000, 0), (600, 600, 0)))
+def test_a_captured_training_step(torch, rng, lq, lk, buckets):
+    """Forward and backward of both operators in one graph, replayed with new inputs, against plain calls."""
+    g = torch.Generator(device="cuda").manual_seed(lq)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+    q, x, do = normal(2, lq, 4, 64), normal(2, lq, 256), normal(2, lq, 256)
+    k, v, gamma = normal(2, lk, 2, 64), normal(2, lk, 2, 64), normal(256)
+    table = normal(buckets, 4) if buckets else None
+    options = dict(bias_table=table, causal=True, queries_last=True, p=0.1, seed=7)
+
+    def step():
+        o, lse, y, h = torch.empty_like(q), torch.empty(2, 4, lq, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+        mean, rstd = (torch.empty(2, lq, device="cuda") for _ in range(2))
+        rng.rng_attention_fwd(q, k, v, o, lse=lse, **options)
+        rng.rng_dropout_layer_norm_fwd(o.view(2, lq, 256), gamma, None, y, mean, rstd, residual=x, h=h, p=0.1, seed=8)
+        dx, dres, dgamma = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gamma)
+        rng.rng_dropout_layer_norm_bwd(do, h, gamma, mean, rstd, dx, dgamma, dresidual=dres, p=0.1, seed=8)
+        out = [torch.empty_like(t) for t in (q, k, v)]
+        dtable = torch.empty_like(table) if buckets else None
+        rng.rng_attention_bwd(dx.view(2, lq, 4, 64), q, k, v, o, lse, *out, dbias_table=dtable, **options)
+        return [o, lse, y, h, dx, dres, dgamma, *out] + ([dtable] if buckets else [])
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(2):
+        for t in (q, k, v, x, do):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        for t in captured:
+            t.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(captured, step()))

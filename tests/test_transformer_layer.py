@@ -40,3 +40,16 @@ def test_the_same_steps_give_the_same_bits(example):
     (a, u), (b, v) = once(), once()
     # (the embedding's gradient is summed by atomics, in the library)
     assert a[0] == b[0] and all(torch.isfinite(p).all() for p in u + v)
+
+
+@pytest.mark.gpu
+def test_the_same_steps_give_the_same_losses_and_weights(example):
+    import torch
+
+    def once():
+        torch.manual_seed(0)
+        model = example.Decoder().cuda().bfloat16()
+        return example.train(model, 20), [p.detach().clone() for p in model.parameters()]
+
+    (a, u), (b, v) = once(), once()
+    assert a == b and all(torch.equal(p, q) for p, q in zip(u, v))
