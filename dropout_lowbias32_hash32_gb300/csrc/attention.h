@@ -97,9 +97,9 @@ __device__ __forceinline__ int32_t keys_of(const Attention &a, int32_t b)
 }
 __device__ __forceinline__ int32_t first_position(const Attention &a, int32_t keys) { return a.last ? keys - a.len_q : 0; }
 
-// The bias by relative position is tabulated for -reach .. reach - 1, which
-// covers the 159 positions of 32 queries by 128 keys that reach past the last
-// bucket's start.
+// The bias by relative position is tabulated for -reach .. reach - 1.  A piece of
+// 32 queries by 64 keys (backward: 32 by 32) has 95 positions; one that is not
+// past the last bucket's start as a whole reaches at most 94 past it.
 __host__ __device__ __forceinline__ int32_t bias_reach(const Buckets &b) { return b.max_distance + 160; }
 
 // Whether the forward kernels with a bias are needed: those without take the

@@ -80,8 +80,8 @@ struct WorkQueue {
     volatile uint32_t *stalled;
     uint32_t items = 0;
 
-    // The next item, for a whole warp or for a role of one thread; -1 when there
-    // is none, or after a wait that ran out.
+    // The next item, for a whole warp; -1 when there is none, or after a wait
+    // that ran out.
     __device__ __forceinline__ int32_t next_warp()
     {
         if (!barrier_wait(answered, items++ & 1u, stalled)) return -1;
@@ -91,31 +91,12 @@ struct WorkQueue {
         if (elect_one()) barrier_arrive(heard);
         return uniform(next);
     }
-    __device__ __forceinline__ int32_t next_one()
-    {
-        if (!barrier_wait_one(answered, items++ & 1u, stalled)) return -1;
-        const int32_t next = taken_work(response);
-        fence_async_shared();
-        barrier_arrive(heard);
-        return next;
-    }
     // The loading role's: asks, once all others have heard the last answer.
     __device__ __forceinline__ int32_t ask_warp()
     {
         if (items && !barrier_wait(heard, (items - 1) & 1u, stalled)) return -1;
         if (elect_one()) ask_for_work(response, answered);
         if (!barrier_wait(answered, items & 1u, stalled)) {
-            barrier_drain(answered, items & 1u);
-            return -1;
-        }
-        ++items;
-        return taken_work(response);
-    }
-    __device__ __forceinline__ int32_t ask_one()
-    {
-        if (items && !barrier_wait_one(heard, (items - 1) & 1u, stalled)) return -1;
-        ask_for_work(response, answered);
-        if (!barrier_wait_one(answered, items & 1u, stalled)) {
             barrier_drain(answered, items & 1u);
             return -1;
         }
