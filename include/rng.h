@@ -251,9 +251,10 @@ rng_status rng_dropout_bwd(const float *dy, float *dx, float p, uint32_t seed,
 /* ---- a transformer layer's dropout, fused with what surrounds it ----------- */
 /* The mask is dropout's above and is stored in neither direction: element e of
  * a masked array, e its flat index, is kept iff uniform(seed, first_counter +
- * e) >= p, and a kept value is scaled by the binary32 value of 1 / (1 - p).
- * p = 0 draws nothing.  All arithmetic is binary32; an output is rounded once
- * to its type. */
+ * e) >= p, and a kept value is multiplied by the binary32 value of 1 / (1 - p)
+ * (rng_dropout_fwd divides by 1 - p: the last bit may differ).  p = 0 draws
+ * nothing.  Sums and statistics are binary32, and an output is rounded once to
+ * its type; attention also rounds the operands of its products, as said there. */
 
 /* Element types. */
 typedef int rng_dtype;
@@ -274,9 +275,10 @@ typedef int rng_dtype;
  * unrounded h.  Rows start x_stride, ... elements apart (a stride is not
  * looked at for a NULL array); columns are adjacent.
  * y and h may each be x's or residual's own array (same address and stride);
- * any other overlap of an output with another array is RNG_EINVAL, as are a
- * stride below cols (with rows > 1), a missing x or y, p outside [0, 1) and a
- * negative or non-finite eps.  rows == 0 or cols == 0 is a no-op. */
+ * any other overlap of an output (mean and rstd among them) with another array
+ * is RNG_EINVAL, as are a stride below cols (with rows > 1), a missing x or y, p
+ * outside [0, 1) and a negative or non-finite eps.  rows == 0 or cols == 0 is a
+ * no-op. */
 rng_status rng_dropout_layer_norm_fwd(const void *x, size_t x_stride, const void *bias, const void *residual,
                                       size_t residual_stride, const void *gamma, const void *beta, void *y,
                                       size_t y_stride, void *h, size_t h_stride, float *mean, float *rstd,
@@ -337,7 +339,14 @@ size_t rng_dropout_layer_norm_bwd_workspace(size_t rows, size_t cols);
  * the operands of the matrix products that follow; where len_q * len_k *
  * heads_q is at most 65536, as two terms each, the value and what its rounding
  * left (whatever the batch).  The forward pass may split a long key axis by the
- * number of batch entries, which changes the order of its f32 sums. */
+ * number of batch entries, which changes the order of its f32 sums.  In f16, dS
+ * has f16's range: it is in steps of 2^-24 below 2^-14 and infinite above 65504,
+ * so gradients that small or large want their loss scaled, as f16 outputs do.
+ *
+ * A NaN or an infinity in k or v of a visible key, or in q or d_o, reaches what
+ * sees it; where a causal mask ends inside a tile (128 queries or keys by 64) it
+ * may also reach what is beside it there: the mask gives a weight of 0, and 0
+ * times it is NaN. */
 typedef struct rng_attention_args {
     rng_dtype dtype;
     int32_t batch, len_q, len_k, heads_q, heads_kv, head_dim;
@@ -365,9 +374,9 @@ typedef struct rng_attention_args {
 
 /* Forward: o and lse.  RNG_EINVAL: what the struct's description rules out, p
  * outside [0, 1), a scale that is not finite, num_buckets and max_distance
- * that rng_relative_bucket refuses (with a table), 2^31 or more of a length,
- * an output that overlaps an input.  An empty output is a no-op; len_k == 0
- * with queries gives o = 0. */
+ * that rng_relative_bucket refuses (with a table), a length or batch * heads_q
+ * above 2^30, an output (or the workspace) that overlaps any other array.  An
+ * empty output is a no-op; len_k == 0 with queries gives o = 0. */
 rng_status rng_attention_fwd(const rng_attention_args *args, void *stream);
 
 /* Backward: dq, dk, dv and dbias_table from d_o and the forward's o and lse;
