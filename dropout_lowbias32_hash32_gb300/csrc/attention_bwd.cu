@@ -19,12 +19,14 @@
 // the work of one that has not started.
 //
 // What bounds them, measured (bf16, p = 0.1): both draw the mask, so instruction
-// issue, 20 to 23 instructions a pair each.
-//   16 x 1024 positions, 16 heads of 64, 32 buckets: query_kernel 252 us (issue slots
-//     60 % busy, ALU pipe 40 %, tensor core 18 %), key_kernel 255 us (65, 46, 23 %),
+// issue, 18 to 23 instructions a pair each.
+//   16 x 1024 positions, 16 heads of 64, 32 buckets: query_kernel 254 us (issue slots
+//     61 % busy, ALU pipe 41 %, tensor core 18 %), key_kernel 250 us (67, 47, 24 %),
 //     table_kernel 5 us.
-//   2 x 4096 causal positions, 16 heads of 128 over 4 key heads: query_kernel 239 us
-//     (55, 39, 37 %), key_kernel 263 us (68, 47, 51 %).
+//   2 x 4096 causal positions, 16 heads of 128 over 4 key heads: query_kernel 238 us
+//     (55, 39, 37 %), key_kernel 264 us (68, 47, 51 %).
+//   24 x 77 x 115 ragged, 6 heads of 40, 20 buckets, f16: 12, 12 and 4 us, one after
+//     the other and each mostly its own set-up.
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 

@@ -25,13 +25,13 @@
 //
 // What bounds it, measured (bf16):
 //   with dropout, the mask's hash: 10 of 17 instructions a pair (19 with a bias).
-//     16 x 1024 positions, 16 heads of 64, 32 buckets, p = 0.1: 201 us, issue slots
-//     71 % busy, ALU pipe 54 %, tensor core 15 %; without bias and dropout 97 us.
+//     16 x 1024 positions, 16 heads of 64, 32 buckets, p = 0.1: 198 us, issue slots
+//     72 % busy, ALU pipe 54 %, tensor core 15 %; without bias and dropout 97 us.
 //   without it, the tensor core and what feeds it: 4099 causal positions, 32 heads
 //     of 128 over 8 key heads: 106 us, 1.30 PFLOP/s of the visible pairs, tensor
 //     core 60 %, exponentials 30 %.
 //   for new tokens, HBM: 32 of them, 32 heads over 8 key heads of 128, 8192 cached
-//     keys at most: 537 MB in 97.5 us, 5.5 TB/s, of which 5 us are join_kernel.
+//     keys at most: 537 MB in 96 us, 5.6 TB/s, of which 5 us are join_kernel.
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 

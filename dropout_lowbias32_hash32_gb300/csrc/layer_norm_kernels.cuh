@@ -7,10 +7,11 @@
 // writes dx, dresidual (10 bytes), for 40 instructions an element, about ten of
 // them the mask's hash.  So a row is read once and stays in registers (or shared
 // memory) between its reductions; the mask is redrawn from the element's flat
-// index.  Measured, 16384 x 4096 in bf16, p = 0.1: forward 94 us, 537 MB at 5.7
-// TB/s, issue slots 79 % busy; backward 127 us, 671 MB at 5.3 TB/s, of which the
-// sums of the weights' gradients 7 us.  2^20 x 256 in f32, forward: 610 us, 4.3 GB
-// at 7.0 TB/s.
+// index.  Measured, 16384 x 4096 in bf16, p = 0.1: forward 92 us, 537 MB at 5.9
+// TB/s, issue slots 77 % busy; backward 123 us, 671 MB at 5.4 TB/s, of which the
+// sums of the weights' gradients 7 us.  2^20 x 256 in f32, forward: 615 us, 4.3 GB
+// at 7.0 TB/s.  Rows off a vector boundary and, backward, of more than 8192
+// columns take an element an access: 1531 x 769 in f16, backward, 24 us for 11.8 MB.
 #pragma once
 
 #include "barrier.cuh"
@@ -585,7 +586,7 @@ cudaError_t launch_norm_fwd(const NormFwd &a, bool vectors, cudaStream_t s)
 {
     constexpr int V = 16 / sizeof(T);
     // Four vectors to a thread: the reductions' shuffles and the addresses cost a thread as much as ten of its elements
-    // (16384 x 4096 in bf16: 94 us, 100 with two, 124 with one).  Up to 128 vectors, a warp holds a row, with no barrier.
+    // (16384 x 4096 in bf16: 92 us, 100 with two, 124 with one).  Up to 128 vectors, a warp holds a row, with no barrier.
     if (vectors && a.cols <= 32u * V) {
         fwd_in_registers<T, W, V, 1>(a, s);
     } else if (vectors && a.cols <= 64u * V) {
