@@ -12,8 +12,8 @@
 //   kSplitKeys = false: the units are two tiles of queries that share the key
 //     and value tiles (halving their traffic from L2);
 //   kSplitKeys = true: one tile of queries, the units take every other key
-//     tile and are joined at the end.  For one tile a head and for few rows,
-//     where the key axis is also split over blocks, and joined by join_kernel.
+//     tile and are joined at the end.  For one tile a head, where
+//     the key axis may also be split over blocks, and is joined by join_kernel.
 // The query heads of one key head are `pack` adjacent rows of a tile, so that
 // they read its keys once.  A block that has finished takes over the work of one
 // that has not started, so that its loads and first products run under the last
@@ -575,7 +575,7 @@ FwdPlan fwd_plan(const Attention &a)
     f.units = a.batch * (a.heads / f.pack);
     const int32_t rows_per = kRows / f.pack, tiles = (a.len_q + rows_per - 1) / rows_per;
     const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
-    f.split_keys = tiles == 1 || two_terms(a);  // whose kernel knows two terms
+    f.split_keys = tiles == 1;
     f.q_tiles = f.split_keys ? tiles : (tiles + 1) / 2;
     f.splits = 1, f.split_tiles = key_tiles < 1 ? 1 : key_tiles;
     if (f.split_keys && key_tiles > 8) {
@@ -623,7 +623,7 @@ cudaError_t launch(const FwdParams &p, cudaStream_t s)
 template <class T, int kDim>
 cudaError_t launch(const FwdParams &p, bool split_keys, cudaStream_t s)
 {
-    if (two_terms(p.a)) return launch<T, kDim, true, true>(p, s);
+    if (two_terms(p.a)) return split_keys ? launch<T, kDim, true, true>(p, s) : launch<T, kDim, false, true>(p, s);
     return split_keys ? launch<T, kDim, true, false>(p, s) : launch<T, kDim, false, false>(p, s);
 }
 
