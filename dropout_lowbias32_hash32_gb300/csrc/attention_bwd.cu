@@ -638,6 +638,12 @@ struct KeyItem {
     int32_t b, head_kv, j0, keys, pos0, begin, per_head, tiles;
 };
 
+// The first query that sees any of the keys from j0 on.
+__device__ __forceinline__ int32_t first_query(const Attention &a, int32_t j0, int32_t pos0)
+{
+    return a.causal && j0 > pos0 ? j0 - pos0 : 0;
+}
+
 __device__ __forceinline__ KeyItem key_item(const BwdParams &p, uint32_t x)
 {
     const Attention &a = p.a;
@@ -648,8 +654,7 @@ __device__ __forceinline__ KeyItem key_item(const BwdParams &p, uint32_t x)
     w.j0 = tile * kRows;
     w.keys = uniform(keys_of(a, w.b)), w.pos0 = first_position(a, w.keys);
     const int32_t q_tiles = (a.len_q + kCols - 1) / kCols;
-    const int32_t first_i = a.causal && w.j0 > w.pos0 ? w.j0 - w.pos0 : 0;  // the first query that sees any of the keys
-    w.begin = min(first_i / kCols, q_tiles), w.per_head = w.j0 < w.keys ? q_tiles - w.begin : 0;
+    w.begin = min(first_query(a, w.j0, w.pos0) / kCols, q_tiles), w.per_head = w.j0 < w.keys ? q_tiles - w.begin : 0;
     w.tiles = w.per_head * a.group;
     return w;
 }
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
     constexpr int kChains = S::kChains;
     extern __shared__ uint8_t dynamic[];
     __shared__ alignas(16) uint4 response;
-    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 2 * kChains + 6];
+    __shared__ alignas(8) uint64_t bars[2 * S::kStages + 2 * kChains + 7];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t stalled;
     const Attention &a = p.a;
@@ -672,14 +677,14 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
 
     const uint32_t full = smem_address(bars), empty = full + 8 * S::kStages, scored = empty + 8 * S::kStages,
                    ready = scored + 8 * kChains, done = ready + 8 * kChains, k_full = done + 8, k_empty = k_full + 8,
-                   answered = k_empty + 8, heard = answered + 8, drained = heard + 8;
+                   answered = k_empty + 8, heard = answered + 8, drained = heard + 8, tail = drained + 8;
     if (threadIdx.x == 0) {
         prefetch_map(&p.k_rows), prefetch_map(&p.v_rows), prefetch_map(&p.q_cols), prefetch_map(&p.do_cols);
         stalled = 0;
         for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1);
         for (int s = 0; s < kChains; ++s) barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4 * S::kShare);
         barrier_init(done, 1), barrier_init(k_full, 1), barrier_init(k_empty, 1);
-        barrier_init(answered, 1), barrier_init(heard, 1 + 4 * Team::kGroups), barrier_init(drained, 1);
+        barrier_init(answered, 1), barrier_init(heard, 1 + 4 * Team::kGroups), barrier_init(drained, 1), barrier_init(tail, 1);
         fence_barrier_init();
     }
     if (warp == Team::kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
         give_registers<Team::kOtherRegisters>();
         if (warp == Team::kTmaWarp) {
             // ---- TMA: k and v, then the queries' tiles, head by head
-            uint32_t use = 0, loaded = 0;
+            uint32_t use = 0, loaded = 0, tails = 0;
             bool fine = true;
             for (int32_t x = blockIdx.x; x >= 0; x = fine ? work.ask_warp() : -1) {
                 const KeyItem w = key_item(p, x);
@@ -707,6 +712,9 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                         tma_load_5d(base + S::kRowsBytes + c * kRowsBox, &p.v_rows, k_full, c * 64, 0, w.j0, w.head_kv, w.b);
                     }
                 }
+                // Queries of the first tile that see none of the keys (before the first key, perhaps, where what q and
+                // do hold is nobody's gradient): whatever they are, the zeros of P and dS must meet zeros.
+                const uint32_t hidden = first_query(a, w.j0, w.pos0) % kCols;
                 int32_t head = w.head_kv * a.group, t = w.begin;
 #pragma unroll 1
                 for (int32_t n = 0; n < w.tiles; ++n) {
@@ -714,14 +722,28 @@ __global__ void __launch_bounds__(KeyShape<kDim>::Team::kThreads, 1) key_kernel(
                     fine = barrier_wait(empty + 8 * stage, (use / S::kStages & 1u) ^ 1u, &stalled);
                     if (!fine) break;
                     ++use;
+                    const bool clears = hidden > 0 && t == w.begin;
+                    const uint32_t on = clears ? tail : bar;
                     if (elect_one()) {
-                        barrier_expect(bar, S::kStageBytes + kCols * sizeof(float2));
+                        barrier_expect(on, S::kStageBytes + kCols * sizeof(float2));
                         for (int c = 0; c < S::kBoxes; ++c) {
-                            tma_load_5d(dst + c * kColsBox, &p.q_cols, bar, c * 64, 0, t * kCols, head, w.b);
-                            tma_load_5d(dst + S::kColsBytes + c * kColsBox, &p.do_cols, bar, c * 64, 0, t * kCols, head, w.b);
+                            tma_load_5d(dst + c * kColsBox, &p.q_cols, on, c * 64, 0, t * kCols, head, w.b);
+                            tma_load_5d(dst + S::kColsBytes + c * kColsBox, &p.do_cols, on, c * 64, 0, t * kCols, head, w.b);
                         }
                         bulk_load(base + S::kStats + stage * kCols * sizeof(float2),
-                                  p.stats + (static_cast<int64_t>(w.b) * a.heads + head) * p.len_pad + t * kCols, kCols * sizeof(float2), bar);
+                                  p.stats + (static_cast<int64_t>(w.b) * a.heads + head) * p.len_pad + t * kCols, kCols * sizeof(float2), on);
+                    }
+                    if (clears) {
+                        if (!barrier_wait(tail, tails++ & 1u, &stalled)) barrier_drain(tail, (tails - 1) & 1u);
+                        uint8_t *rows = smem + S::kRing + stage * S::kStageBytes;
+#pragma unroll 1
+                        for (int c = 0; c < 2 * S::kBoxes; ++c)  // q's, then do's
+#pragma unroll 1
+                            for (uint32_t o = lane * 16u; o < hidden * 128u; o += 512u)
+                                *reinterpret_cast<uint4 *>(rows + c * kColsBox + o) = make_uint4(0, 0, 0, 0);
+                        fence_async_shared();
+                        __syncwarp();
+                        if (elect_one()) barrier_arrive(bar);
                     }
                     if (++t == w.begin + w.per_head) t = w.begin, ++head;
                 }

@@ -323,7 +323,8 @@ size_t rng_dropout_layer_norm_bwd_workspace(size_t rows, size_t cols);
  * visible iff j < n(b) and, when causal, j <= pos(i).  n(b) is
  * key_lengths[b], taken into [0, len_k], or len_k without key_lengths.  Keys
  * at or past n(b) have no influence, whatever their bits.  A query that sees
- * no key gets o = 0, lse = -inf and passes no gradient.
+ * no key gets o = 0, lse = -inf and passes no gradient, whatever q and d_o hold
+ * there.
  *
  * The struct holds device pointers and sizes; it is read during the call
  * only.  q, k, v, o (and their gradients) are [batch, length, heads,
@@ -343,8 +344,7 @@ size_t rng_dropout_layer_norm_bwd_workspace(size_t rows, size_t cols);
  * has f16's range: it is in steps of 2^-24 below 2^-14 and infinite above 65504,
  * so gradients that small or large want their loss scaled, as f16 outputs do.
  *
- * A NaN or an infinity in k or v of a visible key, or in q or d_o, reaches what
- * sees it; where a causal mask ends inside a tile (128 queries or keys by 64) it
+ * Any other NaN or infinity in q, k, v or d_o reaches what sees it; where a causal mask ends inside a tile (128 queries or keys by 64) it
  * may also reach what is beside it there: the mask gives a weight of 0, and 0
  * times it is NaN. */
 typedef struct rng_attention_args {

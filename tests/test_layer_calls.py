@@ -561,3 +561,38 @@ def test_a_captured_training_step(torch, rng, lq, lk, buckets):
             t.fill_(float("nan"))
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(captured, step()))
+
+
+# ---- queries that see nothing --------------------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
+@pytest.mark.parametrize("lq,lk,h,hk,d,buckets,p", ((300, 200, 4, 2, 64, 0, 0.1), (200, 180, 2, 1, 128, 16, 0.0),
+                                                    (70, 30, 2, 2, 64, 32, 0.1), (150, 149, 6, 2, 72, 0, 0.0)))
+def test_queries_that_see_nothing_pass_no_gradient_whatever_they_hold(torch, rng, dtype, lq, lk, h, hk, d, buckets, p):
+    """The last queries of caches that are shorter than they: those before the
+    first key hold NaN and infinities, or zeros; the rest has the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(lq)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(getattr(torch, dtype))
+
+    q, do, k, v = normal(4, lq, h, d), normal(4, lq, h, d), normal(4, lk, hk, d), normal(4, lk, hk, d)
+    table = normal(buckets, h) if buckets else None
+    lengths = torch.tensor([lk, 0, lk // 2, 1], dtype=torch.int32, device="cuda")
+    unseen = (torch.arange(lq, device="cuda")[None, :] < lq - lengths[:, None])[:, :, None, None]
+    results = []
+    for fill in (0.0, float("nan"), float("inf")):
+        a, b = q.masked_fill(unseen, fill), do.masked_fill(unseen, fill)
+        o, lse = torch.empty_like(q), torch.empty(4, h, lq, device="cuda")
+        options = dict(key_lengths=lengths, causal=True, queries_last=True, bias_table=table, p=p, seed=6)
+        rng.rng_attention_fwd(a, k, v, o, lse=lse, **options)
+        out = [torch.full_like(t, float("nan")) for t in (q, k, v)]
+        dtable = torch.full_like(table, float("nan")) if buckets else None
+        rng.rng_attention_bwd(b, a, k, v, o, lse, *out, dbias_table=dtable, **options)
+        results.append([o, lse, *out] + ([dtable] if buckets else []))
+    assert all(bool(t.isfinite().all()) for t in results[0][2:])
+    assert bool((results[0][2].masked_select(unseen) == 0).all())
+    for other in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(results[0], other))
