@@ -344,9 +344,9 @@ size_t rng_dropout_layer_norm_bwd_workspace(size_t rows, size_t cols);
  * has f16's range: it is in steps of 2^-24 below 2^-14 and infinite above 65504,
  * so gradients that small or large want their loss scaled, as f16 outputs do.
  *
- * Any other NaN or infinity in q, k, v or d_o reaches what sees it; where a causal mask ends inside a tile (128 queries or keys by 64) it
- * may also reach what is beside it there: the mask gives a weight of 0, and 0
- * times it is NaN. */
+ * Any other NaN or infinity in q, k, v or d_o reaches what sees it; where a
+ * causal mask ends inside a tile (128 queries or keys by 64) it may also reach
+ * what is beside it there: the mask gives a weight of 0, and 0 times it is NaN. */
 typedef struct rng_attention_args {
     rng_dtype dtype;
     int32_t batch, len_q, len_k, heads_q, heads_kv, head_dim;
