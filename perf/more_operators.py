@@ -35,7 +35,7 @@ def _verify(name, batch, nodes, vocab, dtype, **more):
 
 def _keep(name, caches, batch, nodes, len_k, kv_heads, dim, dtype, **more):
     case = {"op": "keep", "caches": caches, "batch": batch, "nodes": nodes, "len_k": len_k, "kv_heads": kv_heads,
-            "dim": dim, "dtype": dtype}
+            "dim": dim, "dtype": dtype, "stacked": True}
     return {**({"name": name} if name else {}), **case, **more}
 
 
@@ -61,9 +61,9 @@ def listed():
         _verify("verify_odd_bf16", 33, 9, 50001, "bf16", given=False),
         # drafts without probabilities of their own (looked up, or taken greedily)
         _verify("verify_point_drafts", 64, 24, 131072, "f32", draft=False),
-        # one request of a decoder of two layers
-        _keep("keep_one_request", 4, 1, 8, 309, 2, 64, "bf16"),
-        # all layers' caches of a served batch
+        # one request of a decoder of two layers, its caches in a list
+        _keep("keep_one_request", 4, 1, 8, 309, 2, 64, "bf16", stacked=False),
+        # all layers' caches of a served batch, in one tensor
         _keep("keep_serving", 64, 32, 16, 256, 8, 128, "bf16"),
     ]
 
@@ -96,7 +96,8 @@ def draw(rng):
     kv_heads, caches, nodes = rng.randint(1, 8), 2 * _spread(rng, 1, 40), _spread(rng, 1, 64)
     len_k = nodes + rng.randint(0, 256)
     batch = _spread(rng, 1, max(1, min(64, (1 << 29) // (caches * len_k * kv_heads * dim))))
-    return _keep("", caches, batch, nodes, len_k, kv_heads, dim, rng.choice(["bf16", "bf16", "f16"]))
+    return _keep("", caches, batch, nodes, len_k, kv_heads, dim, rng.choice(["bf16", "bf16", "f16"]),
+                 stacked=rng.random() < 0.5)
 
 
 # ---- what a program holds before the call ---------------------------------------
@@ -181,7 +182,7 @@ def prepare(case, seed):
         return state
     # all caches in one tensor, a cache (a layer's keys or values) to an entry
     state["caches"] = normal(case["caches"], b, case["len_k"], case["kv_heads"], case["dim"])
-    state["list"] = list(state["caches"])
+    state["given"] = state["caches"] if case["stacked"] else list(state["caches"])
     state["lengths"] = torch.tensor(_cache_lengths(case), dtype=torch.int32, device="cuda")
     paths = _paths(case)
     state["path"] = torch.tensor([p + [-1] * (n - len(p)) for p in paths], dtype=torch.int32, device="cuda")
@@ -364,7 +365,7 @@ def _own_verify(state):
 
 def _own_keep(state):
     import dropout_lowbias32_hash32_gb300 as rng
-    rng.rng_cache_keep(state["list"], state["path"], state["accepted"], state["lengths"], state["new_lengths"])
+    rng.rng_cache_keep(state["given"], state["path"], state["accepted"], state["lengths"], state["new_lengths"])
     return {"caches": state["caches"], "new_lengths": state["new_lengths"]}
 
 
