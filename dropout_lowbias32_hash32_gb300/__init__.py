@@ -61,6 +61,9 @@ _FILL_SIGS = {
                                    _int, _f32, _u32, _u32, _p, _sz, _p],
     "rng_attention_fwd": [_p, _p],
     "rng_attention_bwd": [_p, _p],
+    "rng_tree_attention_fwd": [_p, _p],
+    "rng_verify_drafts": [_p, _p],
+    "rng_cache_keep": [_p, _p],
     "rng_relative_bucket": [_i64, _i32, _i32, _i32, C.POINTER(_i32)],
     "rng_debug_set_miss_capacity": [_sz],
     "rng_debug_last_miss_count": [C.POINTER(_u64)],
@@ -73,7 +76,7 @@ for _name, _args in _FILL_SIGS.items():
     _fn.argtypes = _args
     _fn.restype = _int
 for _name, _args in {"rng_dropout_layer_norm_bwd_workspace": [_sz, _sz], "rng_attention_fwd_workspace": [_p],
-                     "rng_attention_bwd_workspace": [_p]}.items():
+                     "rng_attention_bwd_workspace": [_p], "rng_tree_attention_fwd_workspace": [_p]}.items():
     getattr(_lib, _name).argtypes = _args
     getattr(_lib, _name).restype = _sz
 _lib.rng_status_string.argtypes = [_int]
@@ -573,6 +576,200 @@ def rng_attention_bwd(do, q, k, v, o, lse, dq, dk, dv, *, dbias_table=None, key_
     _attention("rng_attention_bwd", q, k, v, o, lse, key_lengths, causal, queries_last, scale, bias_table,
                max_distance, bidirectional, p, seed, first_counter, (do, dq, dk, dv), dbias_table, workspace, stream)
     return dq, dk, dv
+
+
+# ---- drafted tokens ---------------------------------------------------------------
+RNG_MAX_TREE_NODES = 128
+
+
+class TreeAttentionArgs(C.Structure):
+    """rng_tree_attention_args of include/rng.h."""
+    _fields_ = [("dtype", _int), ("batch", _i32), ("nodes", _i32), ("len_k", _i32), ("heads_q", _i32),
+                ("heads_kv", _i32), ("head_dim", _i32), ("q", _p), ("k", _p), ("v", _p), ("q_stride", _i64 * 3),
+                ("k_stride", _i64 * 3), ("v_stride", _i64 * 3), ("o", _p), ("o_stride", _i64 * 3), ("lse", _p),
+                ("cache_lengths", _p), ("parents", _p), ("scale", _f32), ("bias_table", _p), ("num_buckets", _i32),
+                ("max_distance", _i32), ("bidirectional", _i32), ("workspace", _p), ("workspace_bytes", _sz)]
+
+
+class VerifyDraftsArgs(C.Structure):
+    """rng_verify_drafts_args of include/rng.h."""
+    _fields_ = [("dtype", _int), ("batch", _i32), ("nodes", _i32), ("vocab", _i32), ("target", _p), ("draft", _p),
+                ("target_stride", _i64 * 2), ("draft_stride", _i64 * 2), ("tokens", _p), ("parents", _p),
+                ("uniforms", _p), ("seed", _u32), ("first_counter", _u32), ("path", _p), ("accepted", _p),
+                ("out_tokens", _p)]
+
+
+class CacheKeepArgs(C.Structure):
+    """rng_cache_keep_args of include/rng.h."""
+    _fields_ = [("caches", _p), ("count", _i32), ("batch", _i32), ("nodes", _i32), ("len_k", _i32), ("heads", _i32),
+                ("head_dim", _i32), ("stride", _i64 * 3), ("cache_lengths", _p), ("path", _p), ("accepted", _p),
+                ("new_lengths", _p)]
+
+
+# The structs as bytes, as for attention.
+_pack_tree = struct.Struct("@7i3P9qP3q3PfP3iPN").pack
+_pack_verify = struct.Struct("@4i2P4q3P2I3P").pack
+_pack_keep = struct.Struct("@P6i3q4P").pack
+for _form, _args in (("@7i3P9qP3q3PfP3iPN", TreeAttentionArgs), ("@4i2P4q3P2I3P", VerifyDraftsArgs),
+                     ("@P6i3q4P", CacheKeepArgs)):
+    assert struct.calcsize(_form) == C.sizeof(_args)
+
+
+def _tree(q, k, v, o, lse, cache_lengths, parents, scale, bias_table, max_distance, bidirectional):
+    """The fields of a TreeAttentionArgs before its workspace; without o, of sizes alone."""
+    code = _first(q, "q")
+    if q.dim() != 4 or k is None or k.dim() != 4:
+        raise ValueError("q, k and v must be [batch, nodes or length, heads, head_dim]")
+    shape = q.shape
+    batch, nodes, heads, dim = shape
+    key_shape = (batch, k.shape[1], k.shape[2], dim)
+    buckets = 0
+    if bias_table is not None:
+        if bias_table.dim() != 2 or bias_table.shape[1] != heads:
+            raise ValueError(f"bias_table has shape {tuple(bias_table.shape)}, not [num_buckets, heads]")
+        buckets = bias_table.shape[0]
+        if buckets == 0:  # whose null pointer would say that there is no table
+            raise ValueError("bias_table has no buckets")
+    if o is None:
+        tensors = (0, 0, 0, *(0,) * 9, 0, 0, 0, 0, 0, 0, 0)
+    else:
+        pq, *sq = _heads(q, "q", shape, q)
+        pk, *sk = _heads(k, "k", key_shape, q)
+        pv, *sv = _heads(v, "v", key_shape, q)
+        po, *so = _heads(o, "o", shape, q)
+        if lse is not None and lse.shape != (batch, heads, nodes):
+            raise ValueError(f"lse has shape {tuple(lse.shape)}, not [batch, heads, nodes]")
+        plse = _flat(lse, "lse", batch * heads * nodes, q, "q", _torch.float32)
+        plen = _flat(cache_lengths, "cache_lengths", batch, q, "q", _torch.int32)
+        pp = _flat(parents, "parents", batch * nodes, q, "q", _torch.int32)
+        tensors = (pq, pk, pv, *sq, *sk, *sv, po, *so, plse or 0, plen or 0, pp or 0)
+    pt = _flat(bias_table, "bias_table", buckets * heads, q, "q", q.dtype)
+    return (code, batch, nodes, key_shape[1], heads, key_shape[2], dim, *tensors,
+            dim ** -0.5 if scale is None else scale, pt or 0, buckets, max_distance if buckets else 0,
+            bool(bidirectional))
+
+
+def rng_tree_attention_fwd_workspace(q, k=None, *, scale=None, bias_table=None, max_distance=128,
+                                     bidirectional=True) -> int:
+    """Bytes of workspace of rng_tree_attention_fwd for q and k on their device (or of a TreeAttentionArgs on the
+    current one); 0 also where the call itself would be refused."""
+    if isinstance(q, TreeAttentionArgs):
+        return _lib.rng_tree_attention_fwd_workspace(C.byref(q))
+    args = _pack_tree(*_tree(q, k, None, None, None, None, None, scale, bias_table, max_distance, bidirectional), 0, 0)
+    with _Current(q.get_device()):
+        return _lib.rng_tree_attention_fwd_workspace(args)
+
+
+def rng_tree_attention_fwd(q, k, v, o, *, lse=None, cache_lengths=None, parents=None, scale=None, bias_table=None,
+                           max_distance=128, bidirectional=True, workspace=None, stream=None):
+    """Attention of a tree of tokens over a cache that holds the nodes' own keys and values behind its cache_lengths
+    (None: at its end); q and o are [batch, nodes, heads, head_dim], k and v [batch, length, key heads, head_dim] (any
+    strides, the last dimension contiguous), parents [batch, nodes] int32 (None: a chain); scale None:
+    head_dim ** -0.5; see rng.h.  Writes o and, where given, lse [batch, heads, nodes]; returns o."""
+    fields = _tree(q, k, v, o, lse, cache_lengths, parents, scale, bias_table, max_distance, bidirectional)
+    index = q.get_device()
+    with _Current(index):
+        args = _pack_tree(*fields, 0, 0)
+        ws, ws_bytes, hold = _scratch(workspace, _lib.rng_tree_attention_fwd_workspace(args), q, stream)
+        if ws_bytes:
+            args = _pack_tree(*fields, ws, ws_bytes)
+        status = _lib.rng_tree_attention_fwd(args, _handle(stream, index))
+    if status:
+        _check(status, "rng_tree_attention_fwd")
+    del hold
+    return o
+
+
+def _probabilities(t, name: str, like) -> tuple:
+    """(pointer, batch stride, node stride) of a [batch, nodes, vocab] tensor; (0, 0, 0) for None."""
+    if t is None:
+        return 0, 0, 0
+    if t.dtype is not like.dtype or t.device != like.device:
+        _same(t, name, like, "target", like.dtype)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, target {tuple(like.shape)}")
+    b, n, v = t.stride()
+    if v != 1 and t.shape[2] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), b, n
+
+
+def rng_verify_drafts(target, tokens, path, accepted, out_tokens, *, draft=None, parents=None, uniforms=None, seed=0,
+                      first_counter=0, stream=None):
+    """Verifies drafted tokens [batch, nodes] (node 0 the known one) against the target's probabilities
+    [batch, nodes, vocab] after each node; draft: the probabilities that each node's children were drawn from (None:
+    they were chosen), parents int32 (None: a chain), uniforms [batch, nodes] f32 (None: drawn from seed and
+    first_counter); see rng.h.  Writes path [batch, nodes], accepted [batch] and out_tokens [batch, nodes], all int32;
+    returns out_tokens."""
+    code = _first(target, "target")
+    if target.dim() != 3:
+        raise ValueError("target must be [batch, nodes, vocab]")
+    batch, nodes, vocab = target.shape
+    i32, n = _torch.int32, batch * nodes
+    pt, tb, tn = _probabilities(target, "target", target)
+    pd, db, dn = _probabilities(draft, "draft", target)
+    ptok = _flat(tokens, "tokens", n, target, "target", i32)
+    ppar = _flat(parents, "parents", n, target, "target", i32)
+    pu = _flat(uniforms, "uniforms", n, target, "target", _torch.float32)
+    ppath, pacc = _flat(path, "path", n, target, "target", i32), _flat(accepted, "accepted", batch, target, "target", i32)
+    pout = _flat(out_tokens, "out_tokens", n, target, "target", i32)
+    args = _pack_verify(code, batch, nodes, vocab, pt, pd, tb, tn, db, dn, ptok or 0, ppar or 0, pu or 0,
+                        seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF, ppath or 0, pacc or 0, pout or 0)
+    index = target.get_device()
+    with _Current(index):
+        status = _lib.rng_verify_drafts(args, _handle(stream, index))
+    if status:
+        _check(status, "rng_verify_drafts")
+    return out_tokens
+
+
+def _caches(caches) -> tuple:
+    """(a cache, the pointers of all) of a list of caches, or of one tensor with the caches along its first dimension."""
+    if getattr(caches, "dim", None) is not None:
+        if caches.dim() != 5:
+            raise ValueError("caches must be a list of [batch, length, heads, head_dim] tensors, or a tensor of them")
+        _first(caches, "caches")
+        count, base = caches.shape[0], caches.data_ptr()
+        step = caches.stride(0) * caches.element_size()
+        if count == 0:
+            raise ValueError("caches must hold at least one cache")
+        return caches[0], [base + i * step for i in range(count)]
+    if len(caches) == 0:
+        raise ValueError("caches must hold at least one cache")
+    first = caches[0]
+    _first(first, "a cache")
+    shape, stride, device, dtype = first.shape, first.stride(), first.device, first.dtype
+    for t in caches:
+        if t.shape != shape or t.stride() != stride or t.dtype is not dtype or t.device != device:
+            raise ValueError("all caches must have the same shape, strides, dtype and device")
+    return first, [t.data_ptr() for t in caches]
+
+
+def rng_cache_keep(caches, path, accepted, cache_lengths=None, new_lengths=None, *, stream=None):
+    """Moves the accepted nodes' rows together in every cache of a list of [batch, length, heads, head_dim] tensors of
+    the same shape and strides (or of one tensor with the caches along its first dimension), from path [batch, nodes]
+    and accepted [batch] as rng_verify_drafts writes them; see rng.h.  Writes the caches and, where given, new_lengths
+    [batch]; returns new_lengths."""
+    like, pointers = _caches(caches)
+    if like.dim() != 4 or like.element_size() != 2:
+        raise ValueError("a cache must be [batch, length, heads, head_dim] of a 2-byte type")
+    batch, length, heads, dim = like.shape
+    if path.dim() != 2 or path.shape[0] != batch:
+        raise ValueError(f"path has shape {tuple(path.shape)}, not [batch, nodes]")
+    nodes, i32 = path.shape[1], _torch.int32
+    _, sb, sl, sh = _heads(like, "a cache", like.shape, like)
+    small = [_flat(t, name, n, like, "a cache", i32) or 0
+             for t, name, n in ((cache_lengths, "cache_lengths", batch), (path, "path", batch * nodes),
+                                (accepted, "accepted", batch), (new_lengths, "new_lengths", batch))]
+    array = struct.pack(f"@{len(pointers)}P", *pointers)
+    hold = C.c_char_p(array)
+    args = _pack_keep(C.cast(hold, _p).value, len(pointers), batch, nodes, length, heads, dim, sb, sl, sh, *small)
+    index = like.get_device()
+    with _Current(index):
+        status = _lib.rng_cache_keep(args, _handle(stream, index))
+    if status:
+        _check(status, "rng_cache_keep")
+    return new_lengths
 
 
 def rng_relative_bucket(relative_position: int, num_buckets: int, max_distance: int = 128,

@@ -3,6 +3,7 @@
 #include "attention.h"
 #include "layer_norm.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -289,6 +290,35 @@ rng_status check_workspace(const char *what, const rng_attention_args &a, size_t
     return RNG_OK;
 }
 
+// A tree's call as attention's: its nodes are the queries, the rows cached before them the key lengths.
+rng_attention_args as_attention(const rng_tree_attention_args &t)
+{
+    rng_attention_args a{};
+    a.dtype = t.dtype, a.batch = t.batch, a.len_q = t.nodes, a.len_k = t.len_k;
+    a.heads_q = t.heads_q, a.heads_kv = t.heads_kv, a.head_dim = t.head_dim;
+    a.q = t.q, a.k = t.k, a.v = t.v, a.o = t.o, a.lse = t.lse, a.key_lengths = t.cache_lengths;
+    std::memcpy(a.q_stride, t.q_stride, sizeof a.q_stride), std::memcpy(a.k_stride, t.k_stride, sizeof a.k_stride);
+    std::memcpy(a.v_stride, t.v_stride, sizeof a.v_stride), std::memcpy(a.o_stride, t.o_stride, sizeof a.o_stride);
+    a.scale = t.scale, a.bias_table = t.bias_table;
+    a.num_buckets = t.num_buckets, a.max_distance = t.max_distance, a.bidirectional = t.bidirectional;
+    a.workspace = t.workspace, a.workspace_bytes = t.workspace_bytes;
+    return a;
+}
+
+rng_status make_tree(const char *what, const rng_tree_attention_args *args, bool sizes_only, rng_attention_args *plain,
+                     TreeAttention *out)
+{
+    if (!args) return fail(RNG_EINVAL, "%s: args is NULL", what);
+    *plain = as_attention(*args);
+    if (rng_status st = make(what, plain, sizes_only, &out->a)) return st;
+    if (args->nodes > RNG_MAX_TREE_NODES)
+        return fail(RNG_EINVAL, "%s: nodes = %d exceeds %d", what, args->nodes, RNG_MAX_TREE_NODES);
+    if (args->nodes > args->len_k)
+        return fail(RNG_EINVAL, "%s: nodes = %d exceeds len_k = %d", what, args->nodes, args->len_k);
+    out->parents = args->parents;
+    return RNG_OK;
+}
+
 }  // namespace
 }  // namespace rngk
 
@@ -381,11 +411,105 @@ rng_status rng_attention_bwd(const rng_attention_args *args, void *stream)
     return e == cudaSuccess ? RNG_OK : cuda_fail(e, what);
 }
 
+size_t rng_tree_attention_fwd_workspace(const rng_tree_attention_args *args)
+{
+    rng_attention_args plain;
+    TreeAttention t;
+    return make_tree("rng_tree_attention_fwd_workspace", args, true, &plain, &t) == RNG_OK ? tree_attention_workspace(t) : 0;
+}
+
+rng_status rng_tree_attention_fwd(const rng_tree_attention_args *args, void *stream)
+{
+    static const char what[] = "rng_tree_attention_fwd";
+    rng_attention_args a;
+    TreeAttention t;
+    if (rng_status st = make_tree(what, args, false, &a, &t)) return st;
+    if (t.a.batch == 0 || t.a.len_q == 0 || t.a.heads == 0) return RNG_OK;
+    if (reinterpret_cast<uintptr_t>(t.parents) % 4)
+        return fail(RNG_EINVAL, "%s: parents is not aligned to its 4-byte element", what);
+    const Tensor tensors[] = {{"q", a.q, a.q_stride, a.len_q, a.heads_q, false},
+                              {"k", a.k, a.k_stride, a.len_k, a.heads_kv, false},
+                              {"v", a.v, a.v_stride, a.len_k, a.heads_kv, false},
+                              {"o", a.o, a.o_stride, a.len_q, a.heads_q, true}};
+    if (rng_status st = check_tensors(what, a, tensors)) return st;
+    const size_t need = tree_attention_workspace(t);
+    if (rng_status st = check_workspace(what, a, need)) return st;
+    const Flat flat[] = {{"cache_lengths", a.key_lengths, uint64_t(4) * t.a.batch, false},
+                         {"parents", t.parents, uint64_t(4) * t.a.batch * t.a.len_q, false},
+                         {"bias_table", a.bias_table, table_bytes(t.a), false},
+                         {"lse", a.lse, lse_bytes(t.a), true},
+                         {"workspace", a.workspace, need, true}};
+    if (rng_status st = check_flat(what, a, flat, tensors)) return st;
+    t.a.out = a.o;
+    clear_error();
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a.dtype == RNG_F16 ? launch_tree_attention<__half>(t, s) : launch_tree_attention<__nv_bfloat16>(t, s);
+    return e == cudaSuccess ? RNG_OK : cuda_fail(e, what);
+}
+
+rng_status rng_cache_keep(const rng_cache_keep_args *args, void *stream)
+{
+    static const char what[] = "rng_cache_keep";
+    constexpr int32_t kMaxCaches = 4096;
+    if (!args) return fail(RNG_EINVAL, "%s: args is NULL", what);
+    const rng_cache_keep_args &a = *args;
+    if (a.batch < 0 || a.heads < 0 || a.count < 0) return fail(RNG_EINVAL, "%s: a size is negative", what);
+    if (a.count > kMaxCaches) return fail(RNG_EINVAL, "%s: %d caches exceed %d", what, a.count, kMaxCaches);
+    if (a.head_dim < 8 || a.head_dim > 128 || a.head_dim % 8)
+        return fail(RNG_EINVAL, "%s: head_dim = %d is not a multiple of 8 in 8 .. 128", what, a.head_dim);
+    if (a.nodes < 1 || a.nodes > RNG_MAX_TREE_NODES || a.nodes > a.len_k)
+        return fail(RNG_EINVAL, "%s: nodes = %d is outside 1 .. %d or above len_k = %d", what, a.nodes, RNG_MAX_TREE_NODES, a.len_k);
+    if (a.len_k > (1 << 30) || static_cast<int64_t>(a.batch) * a.heads > 0x7FFFFFFF / 2)
+        return fail(RNG_EINVAL, "%s: len_k or batch * heads exceeds 2^30", what);
+    if (a.batch == 0) return RNG_OK;
+    const struct {
+        const char *name;
+        const void *p;
+        bool needed;
+    } small[] = {{"cache_lengths", a.cache_lengths, false}, {"path", a.path, true}, {"accepted", a.accepted, true},
+                 {"new_lengths", a.new_lengths, false}};
+    for (const auto &x : small) {
+        if (x.needed && !x.p) return fail(RNG_EINVAL, "%s: %s is NULL", what, x.name);
+        if (reinterpret_cast<uintptr_t>(x.p) % 4)
+            return fail(RNG_EINVAL, "%s: %s is not aligned to its 4-byte element", what, x.name);
+    }
+    if (a.count && !a.caches) return fail(RNG_EINVAL, "%s: caches is NULL", what);
+    rng_attention_args shape{};
+    shape.batch = a.batch, shape.head_dim = a.head_dim;
+    const uint64_t each = uint64_t(4) * a.batch;
+    const Flat flat[] = {{"cache_lengths", a.cache_lengths, each, false}, {"path", a.path, each * a.nodes, false},
+                         {"accepted", a.accepted, each, false}, {"new_lengths", a.new_lengths, each, true}};
+    auto cache = [&](const void *p) { return Tensor{"a cache", p, a.stride, a.len_k, a.heads, true}; };
+    const Tensor none[] = {{"", nullptr, a.stride, 0, 0, false}};
+    if (rng_status st = check_flat(what, shape, flat, none)) return st;
+    const void *sorted[kMaxCaches];
+    for (int32_t i = 0; i < a.count; ++i) {
+        const Tensor t[] = {cache(a.caches[i])};
+        if (rng_status st = check_tensor(what, shape, t[0])) return st;
+        if (rng_status st = check_flat(what, shape, flat, t)) return st;
+        sorted[i] = a.caches[i];
+    }
+    std::sort(sorted, sorted + a.count);
+    for (int32_t i = 1; a.heads && i < a.count; ++i) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(sorted[i]);
+        for (int32_t j = i - 1; j >= 0; --j) {
+            const Tensor x = cache(sorted[j]), y = cache(sorted[i]);
+            if (reinterpret_cast<uintptr_t>(sorted[j]) + extent(shape, x) <= at) break;
+            if (overlap(shape, x, y)) return fail(RNG_EINVAL, "%s: two caches overlap", what);
+        }
+    }
+    const CacheKeep c{a.batch, a.nodes, a.len_k, a.heads, a.head_dim, Strides{a.stride[0], a.stride[1], a.stride[2]},
+                      a.cache_lengths, a.path, a.accepted, a.new_lengths};
+    clear_error();
+    const cudaError_t e = launch_cache_keep(c, a.caches, a.count, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RNG_OK : cuda_fail(e, what);
+}
+
 rng_status rng_debug_stalled_waits(uint64_t *count)
 {
     if (!count) return fail(RNG_EINVAL, "rng_debug_stalled_waits: count is NULL");
     clear_error();
-    cudaError_t (*const kernels[])(uint64_t *) = {stalled_waits_fwd, stalled_waits_bwd, stalled_waits_norm<float>,
+    cudaError_t (*const kernels[])(uint64_t *) = {stalled_waits_fwd, stalled_waits_bwd, stalled_waits_tree, stalled_waits_norm<float>,
                                                   stalled_waits_norm<__half>, stalled_waits_norm<__nv_bfloat16>};
     *count = 0;
     cudaError_t e = cudaSuccess;

@@ -61,12 +61,28 @@ struct Attention {
     void *workspace;
 };
 
+// Attention of a tree of tokens over a cache: len_q nodes, key_lengths the rows cached before them.
+struct TreeAttention {
+    Attention a;
+    const int32_t *parents;
+};
+
+// The move of accepted tokens' rows in caches of the same sizes and strides.
+struct CacheKeep {
+    int32_t batch, nodes, len_k, heads, dim;
+    Strides strides;
+    const int32_t *lengths, *path, *accepted;
+    int32_t *new_lengths;
+};
+cudaError_t launch_cache_keep(const CacheKeep &c, void *const *caches, int32_t count, cudaStream_t s);
+
 rng_status relative_buckets(const char *what, int32_t num_buckets, int32_t max_distance, bool bidirectional,
                             Buckets *out);
 
-// Waits that ran out in the forward and the backward kernels, on the current device.
+// Waits that ran out in the forward, the backward and the tree's kernels, on the current device.
 cudaError_t stalled_waits_fwd(uint64_t *count);
 cudaError_t stalled_waits_bwd(uint64_t *count);
+cudaError_t stalled_waits_tree(uint64_t *count);
 
 size_t attention_fwd_workspace(const Attention &a);
 size_t attention_bwd_workspace(const Attention &a);
@@ -74,6 +90,9 @@ template <class T>
 cudaError_t launch_attention_fwd(const Attention &a, cudaStream_t s);
 template <class T>
 cudaError_t launch_attention_bwd(const Attention &a, cudaStream_t s);
+size_t tree_attention_workspace(const TreeAttention &t);
+template <class T>
+cudaError_t launch_tree_attention(const TreeAttention &t, cudaStream_t s);
 
 __host__ __device__ __forceinline__ int32_t bucket_of(const Buckets &b, int64_t rel)
 {

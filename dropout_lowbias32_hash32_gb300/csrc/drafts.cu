@@ -1,0 +1,451 @@
+// drafts.cu -- drafted tokens after the model has run (include/rng.h): their
+// verification against the target's probabilities, and the move of the accepted
+// ones' cache rows.
+//
+// Verification.  A cluster of blocks has a batch entry, each block a slice of the
+// vocabulary, each warp a run of the slice.  What the walk needs of the drafts
+// (their probabilities at their parents) is fetched by one block for all at once,
+// so that walking down accepted drafts reads shared memory only; every block walks
+// for itself, from the same numbers.  A row is read when a draft has been rejected:
+// all blocks sum what is left, max(p - c q, 0), and share their sums.  The last
+// token's place is then looked for within the one warp's run where the sum passes
+// u[0] of the whole.
+//
+// The sums decide whole numbers, so they are kept in pairs of f32 (48 bits): f64
+// would be slower than HBM here (2 operations a cycle and SM), and f32 sums would
+// pick a neighbouring token about once in a thousand draws of a large vocabulary.
+#include <cooperative_groups.h>
+
+#include "attention.h"
+
+namespace cg = cooperative_groups;
+
+namespace rngk {
+namespace {
+
+constexpr int kMaxNodes = RNG_MAX_TREE_NODES;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
+
+struct VerifyParams {
+    int32_t batch, nodes, vocab;
+    const void *target, *draft;
+    int64_t target_batch, target_node, draft_batch, draft_node;
+    const int32_t *tokens, *parents;
+    const float *uniforms;
+    uint32_t key, first;
+    int32_t *path, *accepted, *out;
+    int32_t run;  // tokens of a warp, a multiple of 32
+};
+
+// A sum of f32 values as a pair, error-free additions (Knuth's two-sum) with
+// intrinsics, which the compiler leaves as they are.
+struct Pair {
+    float hi, lo;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+};
+
+// max(p - c q, 0) as a pair, c = chi + clo: the product's error by a fused
+// multiply-add, the difference's by two-sum.
+__device__ __forceinline__ Pair left_of(float p, float q, float chi, float clo)
+{
+    const float t = __fmul_rn(chi, q), te = __fmaf_rn(chi, q, -t);
+    const float s = __fsub_rn(p, t), b = __fsub_rn(s, p);
+    const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(s, b)), __fadd_rn(t, b));
+    const float lo = __fsub_rn(__fsub_rn(e, te), __fmul_rn(clo, q));
+    const float hi = __fadd_rn(s, lo);
+    const bool some = hi > 0.0f;  // (not for NaN)
+    return Pair{some ? hi : 0.0f, some ? __fsub_rn(lo, __fsub_rn(hi, s)) : 0.0f};
+}
+
+// What the walk needs, the same in every block of a cluster.
+struct Nodes {
+    int32_t parent[kMaxNodes], token[kMaxNodes];
+    float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // probabilities at the parent's row
+};
+
+template <class T, bool kDraft>
+__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams v)
+{
+    extern __shared__ uint32_t removed[];  // without draft probabilities: a bit to a token of the block's slice
+    __shared__ Nodes n;
+    __shared__ double totals[2][kMaxCluster], sums[kWarps];
+    __shared__ int32_t path[kMaxNodes];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int32_t rank = static_cast<int32_t>(cluster.block_rank()), blocks = static_cast<int32_t>(cluster.num_blocks());
+    const int32_t entry = static_cast<int32_t>(blockIdx.x) / blocks, x = threadIdx.x, warp = x / 32, lane = x % 32;
+    const T *target = static_cast<const T *>(v.target) + entry * v.target_batch;
+    const T *draft = static_cast<const T *>(v.draft) + entry * v.draft_batch;
+    const int64_t at0 = static_cast<int64_t>(entry) * v.nodes;
+
+    if (rank == 0 && x < kMaxNodes) {
+        int32_t parent = -2, token = -1;
+        float u = 0.0f, p = 0.0f, q = 0.0f;
+        if (x < v.nodes) {
+            parent = x == 0 ? -1 : v.parents ? v.parents[at0 + x] : x - 1, token = v.tokens[at0 + x];
+            u = v.uniforms ? v.uniforms[at0 + x] : lowbias32::uniform_of(draw32(v.key, v.first + static_cast<uint32_t>(at0) + x));
+            if (parent < 0 || parent >= x || token < 0 || token >= v.vocab) {
+                parent = -2;  // never stands
+            } else {
+                p = to_f32(target[parent * v.target_node + token]);
+                if (kDraft) q = to_f32(draft[parent * v.draft_node + token]);
+            }
+        }
+        for (int32_t r = 0; r < blocks; ++r) {
+            Nodes &to = *cluster.map_shared_rank(&n, r);
+            to.parent[x] = parent, to.token[x] = token, to.u[x] = u, to.p[x] = p, to.q[x] = q;
+        }
+    }
+    const int32_t slice = v.run * kWarps, begin = (rank * kWarps + warp) * v.run, end = min(begin + v.run, v.vocab);
+    auto forget = [&] {
+        if (!kDraft)
+            for (int32_t w = x; w < slice / 32; w += kThreads) removed[w] = 0;
+    };
+    forget();
+    cluster.sync();
+
+    // The sum over the whole vocabulary of what is left of a row; each warp's and block's parts stay in `sums` and `totals`.
+    uint32_t parity = 0;
+    auto left_at = [&](int32_t node, int32_t t, float chi, float clo) {
+        const float p = to_f32(target[node * v.target_node + t]);
+        if (kDraft) return left_of(p, to_f32(draft[node * v.draft_node + t]), chi, clo);
+        const uint32_t place = t - rank * slice;
+        return Pair{p > 0.0f && !(removed[place / 32] >> place % 32 & 1u) ? p : 0.0f, 0.0f};
+    };
+    auto mass_of = [&](int32_t node, double c) {
+        const float chi = static_cast<float>(c), clo = static_cast<float>(c - chi);
+        Pair sum{0.0f, 0.0f};
+#pragma unroll 8
+        for (int32_t t = begin + lane; t < end; t += 32) {
+            const Pair w = left_at(node, t, chi, clo);
+            sum.add(w.hi);
+            if (kDraft) sum.lo = __fadd_rn(sum.lo, w.lo);
+        }
+        double s = sum.value();
+#pragma unroll
+        for (int d = 16; d; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        if (lane == 0) sums[warp] = s;
+        __syncthreads();
+        parity ^= 1u;
+        if (x < blocks) {
+            double block = 0.0;
+            for (int w = 0; w < kWarps; ++w) block += sums[w];
+            cluster.map_shared_rank(&totals[0][0], x)[parity * kMaxCluster + rank] = block;
+        }
+        cluster.sync();
+        double all = 0.0;
+        for (int32_t r = 0; r < blocks; ++r) all += totals[parity][r];
+        return all;
+    };
+
+    // ---- the walk
+    int32_t at = 0, stood = 0;
+    double c = 0.0, mass = 1.0;
+    if (x == 0) path[0] = 0;
+    for (bool further = true; further;) {
+        further = false;
+        bool known = true;  // whether mass is the present w's
+        for (int32_t i = at + 1; i < v.nodes; ++i) {
+            if (n.parent[i] != at) continue;
+            const int32_t t = n.token[i];
+            if (kDraft && !known) mass = mass_of(at, c), known = true;
+            double w = n.p[i], bar = n.u[i] * mass;
+            if (kDraft) {
+                w = fma(-c, static_cast<double>(n.q[i]), w);
+                bar *= static_cast<double>(n.q[i]);
+            } else if (__syncthreads_or(x > at && x < i && n.parent[x & (kMaxNodes - 1)] == at && n.token[x & (kMaxNodes - 1)] == t)) {
+                w = 0.0;  // rejected once already
+            }
+            if (!(w > 0.0)) w = 0.0;
+            if (bar < w) {
+                at = i, c = 0.0, mass = 1.0, further = true;
+                if (x == 0) path[++stood] = i;
+                else ++stood;
+                break;
+            }
+            if (kDraft) {
+                c += mass, known = false;
+            } else {
+                mass -= w;
+                const int32_t place = t - rank * slice;
+                if (x == 0 && place >= 0 && place < slice) removed[place / 32] |= 1u << place % 32;
+            }
+        }
+        if (!kDraft && further) {  // another row: nothing is removed there
+            __syncthreads();
+            forget();
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+
+    // ---- the last token
+    double whole = mass_of(at, c);
+    if (!(whole > 0.0)) {
+        c = 0.0;
+        forget();
+        __syncthreads();
+        whole = mass_of(at, c);
+    }
+    int32_t *out = v.out + at0, *out_path = v.path + at0;
+    if (rank == 0) {
+        if (x == 0) v.accepted[entry] = stood;
+        for (int32_t k = x; k < v.nodes; k += kThreads) {
+            out_path[k] = k <= stood ? path[k] : -1;
+            if (k != stood) out[k] = k < stood ? n.token[path[k + 1]] : -1;
+        }
+    }
+    if (!(whole > 0.0)) {
+        if (rank == 0 && x == 0) out[stood] = -1;
+        return;
+    }
+    // The first of some parts for which the sum up to it exceeds the bar; the last that has any where rounding
+    // leaves none.  before: the sum up to it.
+    const double bar = n.u[0] * whole;
+    double before = 0.0;
+    auto pick = [&](const double *part, int32_t count) {
+        int32_t last = -1;
+        double up_to = before, at_last = before;
+        for (int32_t r = 0; r < count; ++r) {
+            if (part[r] > 0.0) last = r, at_last = up_to;
+            up_to += part[r];
+            if (part[r] > 0.0 && up_to > bar) break;
+        }
+        before = at_last;
+        return last;
+    };
+    if (pick(totals[parity], blocks) != rank) return;
+    if (pick(sums, kWarps) != warp) return;
+    // within a warp's run: the lane's part of it, then a token of that part
+    const float chi = static_cast<float>(c), clo = static_cast<float>(c - chi);
+    const int32_t each = v.run / 32, from = begin + lane * each, to = min(from + each, v.vocab);
+    Pair sum{0.0f, 0.0f};
+#pragma unroll 8
+    for (int32_t t = from; t < to; ++t) {
+        const Pair w = left_at(at, t, chi, clo);
+        sum.add(w.hi);
+        if (kDraft) sum.lo = __fadd_rn(sum.lo, w.lo);
+    }
+    auto up_to_lane = [&](double w) {
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const double y = __shfl_up_sync(0xFFFFFFFFu, w, d);
+            if (lane >= d) w += y;
+        }
+        return w;
+    };
+    const double part = sum.value(), up_to = up_to_lane(part);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, part > 0.0), over = __ballot_sync(0xFFFFFFFFu, part > 0.0 && before + up_to > bar);
+    const int32_t which = over ? __ffs(over) - 1 : 31 - __clz(some);  // (the warp's sum is above 0: some lane's is)
+    before += __shfl_sync(0xFFFFFFFFu, up_to - part, which);
+    const int32_t first = begin + which * each, past = min(first + each, v.vocab);
+    int32_t token = -1;
+    for (int32_t t0 = first; t0 < past; t0 += 32) {
+        const double w = t0 + lane < past ? left_at(at, t0 + lane, chi, clo).value() : 0.0, so_far = before + up_to_lane(w);
+        const uint32_t any = __ballot_sync(0xFFFFFFFFu, w > 0.0), enough = __ballot_sync(0xFFFFFFFFu, w > 0.0 && so_far > bar);
+        if (enough) {
+            token = t0 + __ffs(enough) - 1;
+            break;
+        }
+        if (any) token = t0 + 31 - __clz(any);
+        before = __shfl_sync(0xFFFFFFFFu, so_far, 31);
+    }
+    if (lane == 0) out[stood] = token;
+}
+
+// ---- the accepted rows' move
+
+constexpr int kKeepThreads = 256, kCachesAtOnce = 128, kRowsAtOnce = 8;
+
+struct KeepParams {
+    uint4 *cache[kCachesAtOnce];
+    int32_t batch, nodes, len_k, vectors, head_vectors, chunks, blocks;  // 16-byte vectors of a row and of a head
+    int64_t stride_batch, stride_row, stride_head;                       // in vectors
+    const int32_t *lengths, *path, *accepted;
+    int32_t *new_lengths;
+};
+
+__device__ __forceinline__ int32_t within(int32_t v, int32_t most) { return min(max(v, 0), most); }
+
+// A thread moves one vector of every row, kRowsAtOnce rows' loads at a time: row
+// path[k] > k is read before a later step may write it, since path ascends.  The
+// blocks after the caches' write the new lengths.
+__global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams p)
+{
+    const int32_t room = p.len_k - p.nodes;
+    if (static_cast<int32_t>(blockIdx.x) >= p.blocks) {
+        const int32_t b = (blockIdx.x - p.blocks) * kKeepThreads + threadIdx.x;
+        if (b < p.batch) p.new_lengths[b] = (p.lengths ? within(p.lengths[b], room) : room) + within(p.accepted[b], p.nodes - 1) + 1;
+        return;
+    }
+    const int32_t chunk = blockIdx.x % p.chunks, rest = blockIdx.x / p.chunks, b = rest % p.batch;
+    const int32_t at = chunk * kKeepThreads + threadIdx.x;
+    if (at >= p.vectors) return;
+    const int32_t kept = within(p.accepted[b], p.nodes - 1), cached = p.lengths ? within(p.lengths[b], room) : room;
+    const int32_t *path = p.path + static_cast<int64_t>(b) * p.nodes;
+    uint4 *row = p.cache[rest / p.batch] + b * p.stride_batch + cached * p.stride_row + at / p.head_vectors * p.stride_head +
+                 at % p.head_vectors;
+    for (int32_t k0 = 1; k0 <= kept; k0 += kRowsAtOnce) {
+        uint4 value[kRowsAtOnce];
+        bool moves[kRowsAtOnce];
+#pragma unroll
+        for (int32_t r = 0; r < kRowsAtOnce; ++r) {
+            const int32_t from = k0 + r <= kept ? path[k0 + r] : 0;
+            moves[r] = from > k0 + r && from < p.nodes;
+            if (moves[r]) value[r] = row[from * p.stride_row];
+        }
+#pragma unroll
+        for (int32_t r = 0; r < kRowsAtOnce; ++r)
+            if (moves[r]) row[(k0 + r) * p.stride_row] = value[r];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_keep(const CacheKeep &c, void *const *caches, int32_t count, cudaStream_t s)
+{
+    KeepParams p;
+    p.batch = c.batch, p.nodes = c.nodes, p.len_k = c.len_k;
+    p.head_vectors = c.dim / 8;
+    p.stride_batch = c.strides.batch / 8, p.stride_row = c.strides.len / 8, p.stride_head = c.strides.head / 8;
+    p.lengths = c.lengths, p.path = c.path, p.accepted = c.accepted, p.new_lengths = c.new_lengths;
+    if (static_cast<int64_t>(c.heads) * p.head_vectors > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    p.vectors = c.heads * p.head_vectors;
+    p.chunks = (p.vectors + kKeepThreads - 1) / kKeepThreads;
+    const int64_t each = static_cast<int64_t>(p.chunks) * c.batch, lengths = c.new_lengths ? (c.batch + kKeepThreads - 1) / kKeepThreads : 0;
+    if (each * kCachesAtOnce + lengths > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    for (int32_t at = 0; at == 0 || at < count; at += kCachesAtOnce) {
+        const int32_t some = count - at < kCachesAtOnce ? count - at : kCachesAtOnce;
+        for (int32_t i = 0; i < some; ++i) p.cache[i] = static_cast<uint4 *>(caches[at + i]);
+        p.blocks = static_cast<int32_t>(each * some);
+        const unsigned blocks = static_cast<unsigned>(p.blocks + (at == 0 ? lengths : 0));
+        if (blocks == 0) continue;
+        keep_kernel<<<blocks, kKeepThreads, 0, s>>>(p);
+        note_launch();
+    }
+    return cudaGetLastError();
+}
+
+namespace {
+
+// ---- argument checks
+
+struct Range {
+    const char *name;
+    const void *p;
+    uint64_t bytes;
+    size_t element;
+    bool output, optional;
+};
+
+template <size_t N>
+rng_status check_ranges(const char *what, const Range (&r)[N])
+{
+    for (size_t i = 0; i < N; ++i) {
+        if (!r[i].p) {
+            if (!r[i].optional) return fail(RNG_EINVAL, "%s: %s is NULL", what, r[i].name);
+            continue;
+        }
+        const uintptr_t at = reinterpret_cast<uintptr_t>(r[i].p);
+        if (at % r[i].element) return fail(RNG_EINVAL, "%s: %s is not aligned to its %zu-byte element", what, r[i].name, r[i].element);
+        if (r[i].bytes > UINTPTR_MAX - at) return fail(RNG_EINVAL, "%s: %s runs past the end of the address space", what, r[i].name);
+        for (size_t j = 0; j < i; ++j) {
+            const uintptr_t other = reinterpret_cast<uintptr_t>(r[j].p);
+            if (r[j].p && (r[i].output || r[j].output) && at < other + r[j].bytes && other < at + r[i].bytes)
+                return fail(RNG_EINVAL, "%s: %s and %s overlap", what, r[j].name, r[i].name);
+        }
+    }
+    return RNG_OK;
+}
+
+// Bytes from a [batch, nodes, vocab] array's address to its end; false for a stride that it cannot have.
+bool extent(const int64_t (&stride)[2], const rng_verify_drafts_args &a, size_t size, uint64_t *bytes)
+{
+    const double most = static_cast<double>(a.batch - 1) * stride[0] + static_cast<double>(a.nodes - 1) * stride[1] + a.vocab;
+    if (stride[0] < 0 || stride[1] < 0 || most * size > static_cast<double>(INT64_MAX)) return false;
+    *bytes = size * (static_cast<uint64_t>(a.batch - 1) * stride[0] + static_cast<uint64_t>(a.nodes - 1) * stride[1] + a.vocab);
+    return true;
+}
+
+template <class T, bool kDraft>
+cudaError_t launch_verify(const VerifyParams &v, int cluster, cudaStream_t s)
+{
+    const auto kernel = verify_kernel<T, kDraft>;
+    static std::atomic<bool> done[16];
+    cudaError_t e = allow_shared(kernel, done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(static_cast<unsigned>(v.batch) * cluster);
+    config.blockDim = dim3(kThreads);
+    config.dynamicSmemBytes = kDraft ? 0 : v.run * kWarps / 8;
+    config.stream = s;
+    cudaLaunchAttribute shape;
+    shape.id = cudaLaunchAttributeClusterDimension;
+    shape.val.clusterDim.x = cluster, shape.val.clusterDim.y = shape.val.clusterDim.z = 1;
+    config.attrs = &shape, config.numAttrs = 1;
+    e = cudaLaunchKernelEx(&config, kernel, v);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t launch_verify(const VerifyParams &v, int cluster, cudaStream_t s)
+{
+    return v.draft ? launch_verify<T, true>(v, cluster, s) : launch_verify<T, false>(v, cluster, s);
+}
+
+}  // namespace
+}  // namespace rngk
+
+using namespace rngk;
+
+extern "C" {
+
+rng_status rng_verify_drafts(const rng_verify_drafts_args *args, void *stream)
+{
+    static const char what[] = "rng_verify_drafts";
+    if (!args) return fail(RNG_EINVAL, "%s: args is NULL", what);
+    const rng_verify_drafts_args &a = *args;
+    if (a.dtype != RNG_F32 && a.dtype != RNG_F16 && a.dtype != RNG_BF16)
+        return fail(RNG_EINVAL, "%s: unknown dtype %d", what, a.dtype);
+    if (a.batch < 0 || a.batch > 1 << 24) return fail(RNG_EINVAL, "%s: batch = %d is outside 0 .. 2^24", what, a.batch);
+    if (a.nodes < 1 || a.nodes > RNG_MAX_TREE_NODES)
+        return fail(RNG_EINVAL, "%s: nodes = %d is outside 1 .. %d", what, a.nodes, RNG_MAX_TREE_NODES);
+    if (a.vocab < 1 || a.vocab > 1 << 23) return fail(RNG_EINVAL, "%s: vocab = %d is outside 1 .. 2^23", what, a.vocab);
+    if (a.batch == 0) return RNG_OK;
+    const size_t size = a.dtype == RNG_F32 ? 4 : 2;
+    const uint64_t flat = uint64_t(4) * a.batch * a.nodes;
+    uint64_t target = 0, draft = 0;
+    if (!extent(a.target_stride, a, size, &target) || (a.draft && !extent(a.draft_stride, a, size, &draft)))
+        return fail(RNG_EINVAL, "%s: a stride is negative or too large", what);
+    const Range ranges[] = {{"target", a.target, target, size, false, false},
+                            {"draft", a.draft, draft, size, false, true},
+                            {"tokens", a.tokens, flat, 4, false, false},
+                            {"parents", a.parents, flat, 4, false, true},
+                            {"uniforms", a.uniforms, flat, 4, false, true},
+                            {"path", a.path, flat, 4, true, false},
+                            {"accepted", a.accepted, uint64_t(4) * a.batch, 4, true, false},
+                            {"out_tokens", a.out_tokens, flat, 4, true, false}};
+    if (rng_status st = check_ranges(what, ranges)) return st;
+    VerifyParams v{a.batch, a.nodes, a.vocab, a.target, a.draft, a.target_stride[0], a.target_stride[1], a.draft_stride[0],
+                   a.draft_stride[1], a.tokens, a.parents, a.uniforms, seed_key(a.seed), a.first_counter, a.path, a.accepted,
+                   a.out_tokens, 0};
+    int cluster = 1;
+    while (cluster < kMaxCluster && a.vocab > cluster * 2048) cluster *= 2;
+    const int32_t warps = cluster * kWarps;
+    v.run = ((a.vocab + warps - 1) / warps + 31) / 32 * 32;
+    clear_error();
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a.dtype == RNG_F32   ? launch_verify<float>(v, cluster, s)
+                          : a.dtype == RNG_F16 ? launch_verify<__half>(v, cluster, s)
+                                               : launch_verify<__nv_bfloat16>(v, cluster, s);
+    return e == cudaSuccess ? RNG_OK : cuda_fail(e, what);
+}
+
+}  // extern "C"

@@ -406,6 +406,139 @@ size_t rng_attention_bwd_workspace(const rng_attention_args *args);
 rng_status rng_relative_bucket(int64_t relative_position, int32_t num_buckets, int32_t max_distance,
                                int32_t bidirectional, int32_t *bucket);
 
+/* ---- drafted tokens --------------------------------------------------------- */
+/* A step of serving that tries several drafted tokens at once: attention of a
+ * tree of them over the cache, then, from the probabilities that come of it,
+ * the verification that says which of them stand, then the move of their rows
+ * in the caches.
+ *
+ * A tree is `nodes` tokens, each after its parent.  Node 0 is the newest token
+ * that is known, whose key and value are not cached yet; the others are drafts.
+ * parents is [batch, nodes], contiguous: parents[i] is the node before node i,
+ * or -1 for one that follows the cache.  Any other value outside 0 .. i - 1 says
+ * that the node is absent (an entry with a smaller tree), and with it all nodes
+ * below it.  parents == NULL is a chain: parents[i] = i - 1. */
+
+/* Nodes of a tree at most. */
+#define RNG_MAX_TREE_NODES 128
+
+/* Attention of a tree of tokens over a cache.  With C(b) = cache_lengths[b],
+ * taken into [0, len_k - nodes] (without cache_lengths, len_k - nodes), the key
+ * and value of node t are row C(b) + t.  Node i sees the rows below C(b), itself
+ * and the nodes before it in the tree:
+ *
+ *   s = scale * <q, k> + bias_table[rng_relative_bucket(position's difference), head]
+ *   P = softmax over what it sees of s,  lse = log of the sum of exp(s),  o = sum P v
+ *
+ * A cached row's position is its index, a node's C(b) + the number of nodes
+ * before it.  Heads share keys as in rng_attention_fwd.  An absent node gets
+ * o = 0, lse = -inf.
+ *
+ * The struct holds device pointers and sizes; it is read during the call only.
+ * q and o are [batch, nodes, heads_q, head_dim], k and v [batch, len_k, heads_kv,
+ * head_dim], of type dtype (RNG_F16 or RNG_BF16), with strides, alignment,
+ * head_dim and heads as in rng_attention_args; bias_table (NULL: none) is
+ * [num_buckets, heads_q] of type dtype, contiguous; lse (NULL: not wanted) is
+ * [batch, heads_q, nodes] f32.
+ *
+ * Rows at or past C(b) + nodes, and those of absent nodes, have no influence,
+ * whatever their bits; a node's key and value have none on nodes that do not see
+ * it, infinities and NaN among them.  s, the statistics and all sums are f32; P is
+ * rounded to dtype as the operand of the product with v, as two terms (the value
+ * and what its rounding left) where a key head's rows, nodes * heads_q / heads_kv,
+ * are at most 128.  The key axis is split by the lengths of the whole batch, which
+ * changes the order of the f32 sums. */
+typedef struct rng_tree_attention_args {
+    rng_dtype dtype;
+    int32_t batch, nodes, len_k, heads_q, heads_kv, head_dim;
+    const void *q, *k, *v;
+    int64_t q_stride[3], k_stride[3], v_stride[3]; /* batch, node or row, head */
+    void *o;
+    int64_t o_stride[3];
+    float *lse;
+    const int32_t *cache_lengths; /* [batch] or NULL */
+    const int32_t *parents;       /* [batch, nodes] or NULL */
+    float scale;
+    const void *bias_table;
+    int32_t num_buckets, max_distance, bidirectional;
+    void *workspace; /* rng_tree_attention_fwd_workspace(args) bytes at a 16-byte boundary */
+    size_t workspace_bytes;
+} rng_tree_attention_args;
+
+/* RNG_EINVAL: as rng_attention_fwd; nodes above RNG_MAX_TREE_NODES or above
+ * len_k.  Without batch entries, nodes or query heads a no-op. */
+rng_status rng_tree_attention_fwd(const rng_tree_attention_args *args, void *stream);
+
+/* Bytes of workspace on the current device (sizes alone are looked at); it
+ * belongs to the call until its work is done. */
+size_t rng_tree_attention_fwd_workspace(const rng_tree_attention_args *args);
+
+/* Which drafts stand, and the token after them, such that what comes out has
+ * the target's distribution.  target[b, i] holds the target's probabilities of
+ * the token after node i (of a sum near 1), draft[b, i] those that node i's
+ * children were drawn from, each of its own draw; tokens[b, i] is node i's
+ * token.  The walk begins at node 0.  At a node with probabilities p, and q of
+ * the draft, its children are tried in their order: with w = p, W = 1, c = 0,
+ *
+ *   child i with token t stands iff u[i] W q(t) < w(t);
+ *   else c = c + W,  w = max(p - c q, 0),  W = the sum of w.
+ *
+ * The first that stands is the walk's next node.  Where none does, the last
+ * token is drawn from what is left: the first v for which the sum of w up to v
+ * exceeds u[0] times the whole sum; from p where w has no sum, and -1 where p
+ * has none either.  draft == NULL: each draft was chosen, not drawn; child i
+ * stands iff u[i] W < w(t), else W = W - w(t), w(t) = 0.  A child whose token is
+ * outside 0 .. vocab - 1 does not stand and changes nothing.
+ *
+ * u[i] of entry b is uniforms[b * nodes + i], in [0, 1), or, where uniforms is
+ * NULL, uniform(seed, first_counter + b * nodes + i).
+ *
+ * Written, each [batch, nodes] or [batch]: accepted[b], the number of drafts
+ * that stand; path[b], node 0 and those drafts' nodes, then -1; out_tokens[b],
+ * their tokens and the last one, then -1.  All comparisons are made to 2^-46 of
+ * the sums or better (products and sums of f32 pairs or f64), the sums in an
+ * order that depends on the sizes alone. */
+typedef struct rng_verify_drafts_args {
+    rng_dtype dtype; /* of target and draft: RNG_F32, RNG_F16 or RNG_BF16 */
+    int32_t batch, nodes, vocab;
+    const void *target, *draft;                /* [batch, nodes, vocab], the last dimension adjacent; draft may be NULL */
+    int64_t target_stride[2], draft_stride[2]; /* batch, node, in elements; at least 0 */
+    const int32_t *tokens;                     /* [batch, nodes] */
+    const int32_t *parents;                    /* [batch, nodes] or NULL */
+    const float *uniforms;                     /* [batch, nodes] or NULL */
+    uint32_t seed, first_counter;
+    int32_t *path, *accepted, *out_tokens;
+} rng_verify_drafts_args;
+
+/* RNG_EINVAL: a missing or misaligned pointer, nodes outside 1 ..
+ * RNG_MAX_TREE_NODES, vocab outside 1 .. 2^23, batch above 2^24, a negative
+ * stride, an output that overlaps another array (from its first element to its
+ * last).  batch == 0 is a no-op. */
+rng_status rng_verify_drafts(const rng_verify_drafts_args *args, void *stream);
+
+/* Moves the accepted nodes' rows together: in every cache, for each entry b and
+ * k = 1 .. accepted[b], row C(b) + path[b, k] becomes row C(b) + k (C(b) as in
+ * rng_tree_attention_fwd; accepted is taken into [0, nodes - 1]).  path's entries
+ * ascend, as verification writes them; one that is not in k + 1 .. nodes - 1 is
+ * not moved.  new_lengths[b] (NULL: not wanted) becomes C(b) + accepted[b] + 1.
+ * Caches are [batch, len_k, heads, head_dim] arrays of 2-byte elements (a layer's
+ * keys, a layer's values, ...) of the same sizes and strides, the latter in
+ * elements; addresses, strides and head_dim as in rng_attention_args. */
+typedef struct rng_cache_keep_args {
+    void *const *caches; /* host array of `count` device pointers, read during the call */
+    int32_t count, batch, nodes, len_k, heads, head_dim;
+    int64_t stride[3];            /* batch, row, head */
+    const int32_t *cache_lengths; /* [batch] or NULL */
+    const int32_t *path;          /* [batch, nodes] */
+    const int32_t *accepted;      /* [batch] */
+    int32_t *new_lengths;         /* [batch] or NULL; not cache_lengths's own array */
+} rng_cache_keep_args;
+
+/* RNG_EINVAL: a missing or misaligned pointer, nodes outside 1 .. len_k or above
+ * RNG_MAX_TREE_NODES, more than 4096 caches, two that share an element, an output
+ * that overlaps another array.  batch == 0 is a no-op. */
+rng_status rng_cache_keep(const rng_cache_keep_args *args, void *stream);
+
 /* ---- status -------------------------------------------------------------- */
 
 /* A static string naming the status code. */
