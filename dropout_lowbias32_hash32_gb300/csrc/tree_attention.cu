@@ -341,24 +341,34 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             while (fine && cursor.next<kTiles>(p, w)) {
                 uint32_t(&odd_nodes)[4] = odd[piece++ % kOddBuffers];
                 const int32_t *parents = p.t.parents ? p.t.parents + static_cast<int64_t>(w.b) * a.len_q : nullptr;
+                uint32_t there[4];  // (a node below an absent one may count: its values are seen by nobody, and stay finite)
                 bool begun = false;
                 for (int32_t n = max(0, w.cached / kKeys - w.tile0); n < w.tiles && fine; ++n) {
                     const uint32_t at = use + (kTiles == 2 ? 2 * n + 1 : w.tiles == 1 ? 1 : n < w.tiles - 1 ? 2 * n + 2 : 2 * n + 1);
                     const uint32_t stage = at % S::kStages;
-                    if (!begun && lane < 4) odd_nodes[lane] = 0;
-                    __syncwarp();
-                    begun = true;
+                    if (!begun) {
+                        begun = true;
+                        if (lane < 4) odd_nodes[lane] = 0;
+                        int32_t parent[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int32_t node = 32 * c + static_cast<int32_t>(lane);
+                            parent[c] = node >= a.len_q ? -2 : parents ? __ldg(parents + node) : node - 1;
+                        }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            there[c] = __ballot_sync(0xFFFFFFFFu, parent[c] >= -1 && parent[c] < 32 * c + static_cast<int32_t>(lane));
+                    }
                     fine = barrier_wait(tail + 8 * stage, turns >> stage & 1u, &stalled);
                     turns ^= 1u << stage;
                     if (!fine) break;
                     const int32_t j0 = (w.tile0 + n) * kKeys;
                     uint8_t *rows = smem + S::kRing + stage * S::kTileBytes;
-#pragma unroll 1
+#pragma unroll 2
                     for (int32_t j = max(0, w.cached - j0) + static_cast<int32_t>(lane / 8); j < kKeys; j += 4) {  // a row to 8 lanes
                         const int32_t node = j0 + j - w.cached;
-                        // (a node below an absent one is absent too, and seen by nobody that counts: its values stay, finite)
-                        const int32_t parent = node >= a.len_q ? -2 : parents ? parents[node] : node - 1;
-                        const bool gone = parent < -1 || parent >= node;
+                        const uint32_t word = node < 64 ? node < 32 ? there[0] : there[1] : node < 96 ? there[2] : there[3];
+                        const bool gone = node >= kMaxNodes || !(word >> node % 32 & 1u);
                         bool infinite = false;
 #pragma unroll
                         for (int c = 0; c < S::kBoxes; ++c) {
