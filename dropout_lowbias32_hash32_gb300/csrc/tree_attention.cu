@@ -10,7 +10,8 @@
 // A unit's step is S = Q K^T, P = exp(S - max) written back over S in 16 bits, O +=
 // P V; one warp issues both units' products in turn, so that one unit's
 // exponentials run under the other's products.  One warp issues the TMA loads, one
-// clears value rows that nobody may look at.
+// clears value rows that nobody may look at, one has the next pieces of work ready:
+// the nodes' lines, the biases.
 //
 // The work is the list of all (batch entry, key head, rows) and their key tiles,
 // cut evenly among the blocks by the lengths found on the device.  A block's first
@@ -25,8 +26,8 @@ namespace rngk {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;  // a unit's tile
-constexpr int kThreads = 384;            // a warpgroup a unit, and one of the TMA, MMA and clearing warps
-constexpr uint32_t kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10;
+constexpr int kThreads = 384;            // a warpgroup a unit, and one of the other roles' warps
+constexpr uint32_t kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10;  // and one for the pieces
 // registers: 384 threads start with 168 each; 2 x 208 + 80 <= 3 x 168
 constexpr int kUnitRegisters = 208, kOtherRegisters = 80;
 constexpr uint32_t kBox = 16384;  // bytes of 128 rows of 64 elements
@@ -45,6 +46,7 @@ struct TreeParams {
     // heads side by side in a tile, nodes of a tile, packs of heads, pairs (kTiles = 1: single ones) of tiles of a pack,
     // packs x pairs, rows of a part
     int32_t pack, nodes_per, packs, pairs, units, part_rows;
+    Divider by_pack, by_pairs, by_group, by_blocks;
     float *part;  // [blocks][2][part_rows][dim padded + 2]: O, max, sum
     int4 *meta;   // [blocks][2]: batch entry, unit, first key tile, state
 };
@@ -60,7 +62,7 @@ struct Shape {
     static constexpr uint32_t kTileBytes = kBoxes * kBox;
     static constexpr uint32_t kRing = 2 * kTileBytes;                                     // after two tiles of queries
     static constexpr uint32_t kHand = kRing + kStages * kTileBytes;                       // unit 1's O for unit 0, 32 columns at a time
-    static constexpr uint32_t kTable = kHand + (kTiles == 1 ? 32 * kRows * 4 : 0);        // bias values a unit
+    static constexpr uint32_t kTable = kHand + (kTiles == 1 ? 32 * kRows * 4 : 0);        // bias values of two pieces
     static constexpr uint32_t kBuckets = kTable + 2 * kTableValues * 4;                   // bucket by distance
 };
 
@@ -69,40 +71,39 @@ __device__ __forceinline__ int32_t cached_of(const Attention &a, int32_t b)
     const int32_t room = a.len_k - a.len_q;
     return a.key_lengths ? min(max(a.key_lengths[b], 0), room) : room;
 }
-__device__ __forceinline__ int32_t tiles_of(const Attention &a, int32_t b) { return (cached_of(a, b) + a.len_q + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int32_t tiles_for(const Attention &a, int32_t cached) { return (cached + a.len_q + kKeys - 1) / kKeys; }
 
 // A run of one unit's key tiles.
 struct Piece {
     int32_t b, unit, tile0, tiles, all;  // all: of the unit
     int32_t cached, pack, head0, head_kv, node0;
-    bool second;  // (kTiles = 2) whether the second tile has rows
+    int32_t second;  // (kTiles = 2) whether the second tile has rows
 };
 
 // A block's pieces, one after the other.
 struct Cursor {
-    int64_t at, end, base;  // in the list of all key tiles; base: where the batch entry's begin
-    int32_t b, tiles;       // its key tiles of one unit
+    uint32_t at, end, base;  // in the list of all key tiles; base: where the batch entry's begin
+    int32_t b, cached, tiles;  // its cached rows, and key tiles of one unit
 
     template <int kTiles>
     __device__ __forceinline__ bool next(const TreeParams &p, Piece &w)
     {
         if (at >= end) return false;
         const Attention &a = p.t.a;
-        while (at >= base + static_cast<int64_t>(tiles) * p.units) {
-            base += static_cast<int64_t>(tiles) * p.units;
-            tiles = uniform(tiles_of(a, ++b));
+        while (at >= base + static_cast<uint32_t>(tiles) * p.units) {
+            base += static_cast<uint32_t>(tiles) * p.units;
+            cached = uniform(cached_of(a, ++b));
+            tiles = tiles_for(a, cached);
         }
-        const uint64_t local = at - base;
-        w.b = b, w.all = tiles;
+        const uint32_t local = at - base;
+        w.b = b, w.all = tiles, w.cached = cached;
         w.unit = static_cast<int32_t>(local / static_cast<uint32_t>(tiles));
-        w.tile0 = static_cast<int32_t>(local - static_cast<uint64_t>(w.unit) * tiles);
-        const int64_t left = end - at;
-        w.tiles = w.all - w.tile0 < left ? w.all - w.tile0 : static_cast<int32_t>(left);
+        w.tile0 = static_cast<int32_t>(local) - w.unit * tiles;
+        w.tiles = min(w.all - w.tile0, static_cast<int32_t>(end - at));
         at += w.tiles;
-        w.cached = uniform(cached_of(a, b));
-        const int32_t pair = w.unit % p.pairs;
-        w.pack = w.unit / p.pairs;
-        w.head0 = w.pack * p.pack, w.head_kv = w.head0 / a.group;
+        int32_t pair;
+        p.by_pairs.divide(w.unit, w.pack, pair);
+        w.head0 = w.pack * p.pack, w.head_kv = p.by_group.quotient(w.head0);
         w.node0 = pair * kTiles * p.nodes_per;
         w.second = kTiles == 2 && w.node0 + p.nodes_per < a.len_q;
         return true;
@@ -110,10 +111,55 @@ struct Cursor {
 };
 
 // Where the list is cut at x: at a unit's own beginning or end rather than less than kLeastPart tiles from it.
-__device__ __forceinline__ int64_t snapped(int64_t x, int64_t base, int32_t tiles)
+__device__ __forceinline__ uint32_t snapped(uint32_t x, uint32_t base, uint32_t tiles)
 {
-    const int32_t o = static_cast<int32_t>(static_cast<uint64_t>(x - base) % static_cast<uint32_t>(tiles));
+    const uint32_t o = (x - base) % tiles;
     return o < kLeastPart ? x - o : tiles - o < kLeastPart ? x - o + tiles : x;
+}
+
+// The lines of a tree's nodes (the node and those before it; none for an absent one) and the number of nodes before
+// each, by a warp: each step doubles how far up a line reaches.
+__device__ __forceinline__ void find_lines(const TreeAttention &t, int32_t b, Bits (&seen)[kMaxNodes], int16_t (&depth)[kMaxNodes],
+                                           int16_t (&jump)[kMaxNodes], uint32_t lane)
+{
+    constexpr int kEach = kMaxNodes / 32;
+    const int32_t nodes = t.a.len_q;
+    const int32_t *parents = t.parents ? t.parents + static_cast<int64_t>(b) * nodes : nullptr;
+    Bits line[kEach];
+    int32_t up[kEach];
+#pragma unroll
+    for (int c = 0; c < kEach; ++c) {
+        const int32_t node = 32 * c + static_cast<int32_t>(lane);
+        if (parents) {
+            up[c] = node < nodes ? __ldg(parents + node) : -2;
+            if (up[c] < -1 || up[c] >= node) up[c] = -2;
+            line[c] = up[c] == -2 ? Bits(0) : Bits(1) << node;
+        } else {
+            up[c] = -1, line[c] = ~Bits(0) >> (kMaxNodes - 1 - node);
+        }
+    }
+    bool further = parents != nullptr;
+#pragma unroll 1
+    while (further) {
+        further = false;
+#pragma unroll
+        for (int c = 0; c < kEach; ++c) seen[32 * c + lane] = line[c], jump[32 * c + lane] = static_cast<int16_t>(up[c]);
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < kEach; ++c) {
+            if (up[c] < 0) continue;
+            const Bits more = seen[up[c]];
+            line[c] = more ? line[c] | more : Bits(0);
+            up[c] = jump[up[c]];
+            further = further || up[c] >= 0;
+        }
+        further = __any_sync(0xFFFFFFFFu, further);
+    }
+#pragma unroll
+    for (int c = 0; c < kEach; ++c) {
+        seen[32 * c + lane] = line[c];
+        depth[32 * c + lane] = static_cast<int16_t>(__popcll(static_cast<uint64_t>(line[c])) + __popcll(static_cast<uint64_t>(line[c] >> 64)) - 1);
+    }
 }
 
 template <class T, int kDim, int kTiles, bool kBias>
@@ -121,17 +167,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
 {
     using S = Shape<kDim, kTiles>;
     constexpr bool kTwoTerms = kTiles == 1;
+    constexpr int kTogether = kTiles == 1 ? 256 : 128;  // threads that work on a piece's rows
     // f16 holds 2^15: P below 2^8 is lifted, so that long rows' small ones keep their bits
     constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+    constexpr uint32_t kBars = 3 * S::kStages + 11;  // that one arrival completes
     extern __shared__ uint8_t dynamic[];
-    __shared__ alignas(8) uint64_t bars[3 * S::kStages + 12];
+    __shared__ alignas(8) uint64_t bars[kBars + 4];
     __shared__ uint32_t tmem_base;
     __shared__ volatile uint32_t stalled;
     __shared__ Cursor shared_cursor;
-    __shared__ int64_t scan[kThreads / 32 + 1], cut_end;
-    __shared__ Bits seen_by[2][kMaxNodes];      // [unit][node]: the nodes of its line, none for an absent one
-    __shared__ int16_t depth_by[2][kMaxNodes];  // nodes before it
-    __shared__ uint32_t odd[kOddBuffers][4];    // nodes with an infinity or NaN among their values
+    __shared__ uint32_t scan[kThreads / 32], cut_end;
+    __shared__ Piece pieces[2];
+    __shared__ Bits seen[2][kMaxNodes];                      // [piece's parity][node]: the nodes of its line
+    __shared__ int16_t depth[2][kMaxNodes], jump[kMaxNodes];  // nodes before it
+    __shared__ uint32_t odd[kOddBuffers][4];                 // nodes with an infinity or NaN among their values
     __shared__ float tops[2][kRows], sums[2][kRows];
     const Attention &a = p.t.a;
     const uint32_t warp = uniform(threadIdx.x / 32u), lane = threadIdx.x % 32u;
@@ -139,17 +188,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     const uint32_t base = smem_address(smem);
 
     const uint32_t full = smem_address(bars), empty = full + 8 * S::kStages, tail = empty + 8 * S::kStages,
-                   scored = tail + 8 * S::kStages, ready = scored + 16, done = ready + 16, q_full = done + 16,
-                   q_empty = q_full + 16, drained = q_empty + 16;
-    if (threadIdx.x == 0) {
-        prefetch_map(&p.q), prefetch_map(&p.k), prefetch_map(&p.v);
-        stalled = 0;
-        for (int s = 0; s < S::kStages; ++s) barrier_init(full + 8 * s, 1), barrier_init(empty + 8 * s, 1), barrier_init(tail + 8 * s, 1);
-        for (int s = 0; s < 2; ++s)
-            barrier_init(scored + 8 * s, 1), barrier_init(ready + 8 * s, 4), barrier_init(done + 8 * s, 1),
-                barrier_init(q_full + 8 * s, 1), barrier_init(q_empty + 8 * s, 1);
-        barrier_init(drained, 1);
+                   scored = tail + 8 * S::kStages, done = scored + 16, q_full = done + 16, q_empty = q_full + 16,
+                   drained = q_empty + 16, prepared = drained + 8, ready = prepared + 16, taken = ready + 16;
+    if (threadIdx.x < kBars + 4) {
+        barrier_init(full + 8 * threadIdx.x, threadIdx.x < kBars ? 1 : threadIdx.x < kBars + 2 ? 4 : 8);
         fence_barrier_init();
+    } else if (threadIdx.x == 64) {
+        stalled = 0;
+        prefetch_map(&p.q), prefetch_map(&p.k), prefetch_map(&p.v);
     }
     if (warp == kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
     if (kBias && a.table) {
@@ -158,38 +204,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     }
 
     // ---- the block's share of the list
-    auto block_sum = [&](int64_t v, int64_t &before) {  // over the threads; before: over those before this one
-        int64_t up_to = v;
+    auto block_sum = [&](uint32_t v, uint32_t &before) {  // over the threads; before: over those before this one
+        uint32_t up_to = v;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
-            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, up_to, d);
+            const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, up_to, d);
             if (lane >= static_cast<uint32_t>(d)) up_to += y;
         }
         __syncthreads();
         if (lane == 31) scan[warp] = up_to;
         __syncthreads();
-        before = up_to - v;
-        int64_t all = 0;
-        for (uint32_t w = 0; w < kThreads / 32; ++w) {
-            if (w == warp) before += all;
-            all += scan[w];
-        }
-        return all;
+        uint32_t w = lane < kThreads / 32 ? scan[lane] : 0;
+        before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0) + up_to - v;
+        return __reduce_add_sync(0xFFFFFFFFu, w);
     };
     {
-        int64_t mine = 0, before;
-        for (int32_t b = threadIdx.x; b < a.batch; b += kThreads) mine += tiles_of(a, b);
-        const int64_t all = block_sum(mine, before) * p.units;
-        const int64_t from = all * blockIdx.x / gridDim.x, to = all * (blockIdx.x + 1) / gridDim.x;
-        if (threadIdx.x == 0) shared_cursor = Cursor{all, all, all, a.batch - 1, 1}, cut_end = all;
-        int64_t so_far = 0;
+        const int32_t mine = threadIdx.x;
+        uint32_t sum = 0, before, so_far = 0;
+        int32_t cached = 0;
+        for (int32_t b = mine; b < a.batch; b += kThreads) cached = cached_of(a, b), sum += tiles_for(a, cached);
+        const uint32_t all = block_sum(sum, before) * p.units;
+        const uint32_t share = p.by_blocks.quotient(all), left = all - share * p.by_blocks.by;
+        const uint32_t from = blockIdx.x * share + min(blockIdx.x, left), to = from + share + (blockIdx.x < left ? 1 : 0);
+        if (threadIdx.x == 0) shared_cursor = Cursor{all, all, all, a.batch - 1, 0, 1}, cut_end = all;
         for (int32_t b0 = 0; b0 < a.batch; b0 += kThreads) {
-            const int32_t b = b0 + static_cast<int32_t>(threadIdx.x), n = b < a.batch ? tiles_of(a, b) : 0;
-            const int64_t part = block_sum(static_cast<int64_t>(n) * p.units, before), begin = so_far + before,
-                          past = begin + static_cast<int64_t>(n) * p.units;
-            if (from >= begin && from < past) shared_cursor = Cursor{snapped(from, begin, n), 0, begin, b, n};
-            if (to >= begin && to < past) cut_end = snapped(to, begin, n);
-            so_far += part;
+            const int32_t b = b0 + mine;
+            if (a.batch > kThreads) {  // (else the first sum had one entry to a thread)
+                sum = b < a.batch ? cached = cached_of(a, b), tiles_for(a, cached) : 0;
+                const uint32_t part = block_sum(sum, before);
+                before += so_far, so_far += part;
+            } else {
+                __syncthreads();
+            }
+            const uint32_t begin = before * p.units, past = begin + sum * p.units;
+            if (from >= begin && from < past) shared_cursor = Cursor{snapped(from, begin, sum), 0, begin, b, cached, static_cast<int32_t>(sum)};
+            if (to >= begin && to < past) cut_end = snapped(to, begin, sum);
         }
     }
     tmem_fence_before();
@@ -221,13 +270,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             tma_load_5d(base + (kTiles == 2 ? t : buffer) * S::kTileBytes + c * kBox, &p.q, q_full + 8 * buffer, c * 64, 0,
                                         w.node0 + t * p.nodes_per, w.pack, w.b);
                 }
-                auto tile = [&](bool value, int32_t n) {
+                constexpr int32_t kLead = kTiles == 1 ? 2 : 1;  // K_0 .. K_{lead-1}, then V_n and K_{n+lead}
+#pragma unroll 1
+                for (int32_t n = -2 * kLead; n < 2 * w.tiles; ++n) {
+                    const bool value = n >= 0 && n % 2 == 0;
+                    const int32_t tile = value ? n / 2 : n < 0 ? n / 2 + kLead : n / 2 + kLead;
+                    if ((n < 0 && n % 2 != 0) || tile >= w.tiles) continue;
                     const uint32_t stage = use % S::kStages, dst = base + S::kRing + stage * S::kTileBytes;
                     fine = barrier_wait(empty + 8 * stage, (use / S::kStages & 1u) ^ 1u, &stalled);
-                    if (!fine) return;
+                    if (!fine) break;
                     ++use;
                     // value rows from the tree on are looked through before the products see them
-                    const bool looked_through = value && (w.tile0 + n + 1) * kKeys > w.cached;
+                    const bool looked_through = value && (w.tile0 + tile + 1) * kKeys > w.cached;
                     const uint32_t bar = (looked_through ? tail : full) + 8 * stage;
                     on_tail = looked_through ? on_tail | 1u << stage : on_tail & ~(1u << stage);
                     tail_turns ^= looked_through ? 1u << stage : 0u;
@@ -235,14 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         barrier_expect(bar, S::kTileBytes);
 #pragma unroll
                         for (int c = 0; c < S::kBoxes; ++c)
-                            tma_load_5d(dst + c * kBox, value ? &p.v : &p.k, bar, c * 64, 0, (w.tile0 + n) * kKeys, w.head_kv, w.b);
+                            tma_load_5d(dst + c * kBox, value ? &p.v : &p.k, bar, c * 64, 0, (w.tile0 + tile) * kKeys, w.head_kv, w.b);
                     }
-                };
-                constexpr int32_t kLead = kTiles == 1 ? 2 : 1;
-                for (int32_t n = 0; n < kLead && n < w.tiles && fine; ++n) tile(false, n);
-                for (int32_t n = 0; n < w.tiles && fine; ++n) {
-                    tile(true, n);
-                    if (fine && n + kLead < w.tiles) tile(false, n + kLead);
                 }
             }
             if (stalled) {  // nothing may land after the block has ended
@@ -282,16 +330,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 }
                 __syncwarp();
             };
-            // O += P V of a unit
+            // O += P V of a unit; P lies where the scores were, 16 columns for 32 keys, and beside them its second term
             auto add = [&](uint32_t unit, uint32_t u, bool first, bool frees, bool last) {
                 if (fine && elect_one()) {
                     const uint64_t vd = ring_v + (u % S::kStages) * (S::kTileBytes / 16);
                     const uint32_t at = tmem + unit * 256;
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i) mma_step_tmem(at + kKeys, at + i * 8, vd + i * (2048 / 16), kOut, !first || i > 0);
-                    if (kTwoTerms)
-#pragma unroll
-                        for (int i = 0; i < kKeys / 16; ++i) mma_step_tmem(at + kKeys, at + kKeys / 2 + i * 8, vd + i * (2048 / 16), kOut, true);
+                    for (int i = 0; i < kKeys / 16; ++i) {
+                        const uint32_t from = at + (i / 2) * 32 + i % 2 * 8;
+                        mma_step_tmem(at + kKeys, from, vd + i * (2048 / 16), kOut, !first || i > 0);
+                        if (kTwoTerms) mma_step_tmem(at + kKeys, from + 16, vd + i * (2048 / 16), kOut, true);
+                    }
                     if (frees) mma_commit(empty + 8 * (u % S::kStages));
                     if (last) mma_commit(done + 8 * unit);
                 }
@@ -302,34 +351,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 fine = barrier_wait(q_full + 8 * buffer, piece / S::kQBuffers & 1u, &stalled);
                 ++piece;
                 tmem_fence_after();
-                if (kTiles == 1) {
-                    for (int32_t n = 0; n < 2 && n < w.tiles && fine; ++n) {
-                        loaded(use);
-                        score(n, buffer, use++, true, n == w.tiles - 1, buffer);
-                    }
-                    for (int32_t n = 0; n < w.tiles && fine; ++n) {
-                        loaded(use);
-                        written(n & 1);
-                        add(n & 1, use++, n < 2, true, n + 2 >= w.tiles);
-                        if (n + 2 >= w.tiles) continue;
-                        loaded(use);
-                        score(n & 1, buffer, use++, true, n + 2 == w.tiles - 1, buffer);
-                    }
-                } else {
-                    const uint32_t last = w.second ? 1 : 0;
-                    loaded(use);
-                    for (uint32_t u = 0; u <= last; ++u) score(u, u, use, u == last, u == last && w.tiles == 1, buffer);
-                    for (int32_t n = 0; n < w.tiles && fine; ++n) {
-                        for (uint32_t u = 0; u <= last && fine; ++u) {
-                            if (u == 0) loaded(use + 1);
-                            written(u);
-                            add(u, use + 1, n == 0, u == last, n == w.tiles - 1);
-                            if (n + 1 == w.tiles) continue;
-                            if (u == 0) loaded(use + 2);
-                            score(u, u, use + 2, u == last, u == last && n + 2 == w.tiles, buffer);
+                // a step: the sums of tile n (from 0 on), then the scores of the one that takes their place
+                const uint32_t last = kTiles == 1 ? 0 : w.second ? 1 : 0;
+                constexpr int32_t kLead = kTiles == 1 ? 2 : 1;
+#pragma unroll 1
+                for (int32_t n = -kLead; n < w.tiles && fine; ++n) {
+                    const int32_t next = n + kLead;
+                    const uint32_t value = use, key = use + (n >= 0 ? 1 : 0);
+                    if (n < 0 && next >= w.tiles) continue;
+#pragma unroll 1
+                    for (uint32_t u = 0; u <= last && fine; ++u) {
+                        const uint32_t unit = kTiles == 1 ? n & 1 : u;
+                        if (n >= 0) {
+                            if (u == 0) loaded(value);
+                            written(unit);
+                            add(unit, value, n < kLead, u == last, n + kLead >= w.tiles);
                         }
-                        use += 2;
+                        if (next >= w.tiles) continue;
+                        if (u == 0) loaded(key);
+                        score(unit, kTiles == 1 ? buffer : u, key, u == last, u == last && next == w.tiles - 1, buffer);
                     }
+                    use += (n >= 0 ? 1 : 0) + (next < w.tiles ? 1 : 0);
                 }
             }
             if (stalled && elect_one()) mma_commit(drained), barrier_drain(drained, 0);
@@ -364,27 +406,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     if (!fine) break;
                     const int32_t j0 = (w.tile0 + n) * kKeys;
                     uint8_t *rows = smem + S::kRing + stage * S::kTileBytes;
-#pragma unroll 2
+                    // a finite number's bits without its sign, plus this, stay below 2^15
+                    constexpr uint32_t kToSign = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+#pragma unroll 4
                     for (int32_t j = max(0, w.cached - j0) + static_cast<int32_t>(lane / 8); j < kKeys; j += 4) {  // a row to 8 lanes
                         const int32_t node = j0 + j - w.cached;
                         const uint32_t word = node < 64 ? node < 32 ? there[0] : there[1] : node < 96 ? there[2] : there[3];
                         const bool gone = node >= kMaxNodes || !(word >> node % 32 & 1u);
-                        bool infinite = false;
 #pragma unroll
                         for (int c = 0; c < S::kBoxes; ++c) {
                             uint4 *at16 = reinterpret_cast<uint4 *>(rows + c * kBox + j * 128 + lane % 8 * 16);
-                            uint4 x = gone ? make_uint4(0, 0, 0, 0) : *at16;
-                            constexpr uint32_t kExponent = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-                            uint32_t *half = &x.x;
-                            bool change = gone;
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                if ((half[h] & kExponent) == kExponent) half[h] &= 0xFFFF0000u, change = infinite = true;
-                                if ((half[h] >> 16 & kExponent) == kExponent) half[h] &= 0xFFFFu, change = infinite = true;
+                            if (gone) {
+                                *at16 = make_uint4(0, 0, 0, 0);
+                                continue;
                             }
-                            if (change) *at16 = x;
+                            uint4 x = *at16;
+                            auto over = [&](uint32_t y) { return (y & 0x7FFF7FFFu) + kToSign; };
+                            if ((over(x.x) | over(x.y) | over(x.z) | over(x.w)) & 0x80008000u) {
+                                auto finite = [&](uint32_t y) {
+                                    const uint32_t o = over(y);
+                                    return y & ~((o & 0x8000u ? 0xFFFFu : 0u) | (o & 0x80000000u ? 0xFFFF0000u : 0u));
+                                };
+                                *at16 = make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w));
+                                atomicOr(&odd_nodes[node / 32], 1u << node % 32);
+                            }
                         }
-                        if (infinite) atomicOr(&odd_nodes[node / 32], 1u << node % 32);
                     }
                     fence_async_shared();
                     __syncwarp();
@@ -392,63 +438,70 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 }
                 use += 2 * w.tiles;
             }
+        } else {
+            // ---- the next pieces: two are ready
+            const bool has_bias = kBias && a.table;
+            int32_t lines_of[2] = {-1, -1}, values_of[2] = {-1, -1};
+            for (uint32_t piece = 0;; ++piece) {
+                const uint32_t buffer = piece & 1u;
+                const bool more = cursor.next<kTiles>(p, w);
+                if (piece >= 2 && !barrier_wait(taken + 8 * buffer, (piece / 2 - 1) & 1u, &stalled)) break;
+                if (!more) w.tiles = 0;
+                if (lane == 0) pieces[buffer] = w;
+                const bool tree = (w.tile0 + w.tiles) * kKeys > w.cached;  // whether the piece has rows of the tree
+                if (more && (tree || has_bias) && (buffer ? lines_of[1] : lines_of[0]) != w.b) {
+                    if (buffer) lines_of[1] = w.b;
+                    else lines_of[0] = w.b;
+                    find_lines(p.t, w.b, seen[buffer], depth[buffer], jump, lane);
+                }
+                if (more && has_bias && (buffer ? values_of[1] : values_of[0]) != w.pack) {
+                    if (buffer) values_of[1] = w.pack;
+                    else values_of[0] = w.pack;
+                    float *values = reinterpret_cast<float *>(smem + S::kTable) + buffer * kTableValues;
+                    for (int32_t t = lane; t < a.buckets.total * p.pack; t += 32) {
+                        int32_t n, head;
+                        p.by_pack.divide(t, n, head);
+                        values[t] = to_f32(static_cast<const T *>(a.table)[n * a.heads + w.head0 + head]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) barrier_arrive(prepared + 8 * buffer);
+                if (!more) break;
+            }
         }
     } else {
         take_registers<kUnitRegisters>();
         // ---- the units' rows
         const int unit = warp / 4;
-        const int32_t r = (warp % 4) * 32 + lane, local_node = r / p.pack, head_at = r - local_node * p.pack;
+        const int32_t r = (warp % 4) * 32 + lane;
+        int32_t local_node, head_at;
+        p.by_pack.divide(r, local_node, head_at);
         const uint32_t mine = tmem + unit * 256 + ((warp % 4) * 32u << 16), out = mine + kKeys;
         const float to_base2 = kBias ? kLog2e : a.scale * kLog2e;
-        Bits(&seen)[kMaxNodes] = seen_by[unit];
-        int16_t(&depth)[kMaxNodes] = depth_by[unit];
-        float *values = reinterpret_cast<float *>(smem + S::kTable) + unit * kTableValues;
         const uint8_t *bucket = smem + S::kBuckets;
-        const int32_t far = a.table ? a.buckets.max_distance : 0;
-        int32_t tree_of = -1, values_of = -1;  // whose `seen` and `values` are there
-        uint32_t turn = 0, finished = 0, piece = 0, parts = 0;
         const bool has_bias = kBias && a.table;
-        while (cursor.next<kTiles>(p, w)) {
-            const int32_t node0 = w.node0 + (kTiles == 2 ? unit * p.nodes_per : 0), i = node0 + local_node, head = w.head0 + head_at;
+        const int32_t far = has_bias ? a.buckets.max_distance : 0;
+        uint32_t turn = 0, finished = 0, parts = 0;
+#pragma unroll 1
+        for (uint32_t piece = 0;; ++piece) {
+            // Both units have read O before the next piece's first P is announced; and they leave together, also when a
+            // wait of one of them ran out.
+            tmem_fence_before();
+            const uint32_t buffer = piece & 1u;
+            const bool fine = barrier_wait(prepared + 8 * buffer, piece / 2 & 1u, &stalled);
+            if (!all_of<kTogether>(kTiles == 1 ? 1 : 2 + unit, fine && !stalled)) break;
+            w = pieces[buffer];
+            if (w.tiles == 0) break;
+            const int32_t i = w.node0 + (kTiles == 2 ? unit * p.nodes_per : 0) + local_node, head = w.head0 + head_at;
             const bool valid = local_node < p.nodes_per && i < a.len_q;
             const bool any = __any_sync(0xFFFFFFFFu, valid);
             const bool tree = (w.tile0 + w.tiles) * kKeys > w.cached;  // whether the piece has rows of the tree
             const int64_t index = (static_cast<int64_t>(w.b) * a.heads + head) * a.len_q + i;
-            if ((tree || has_bias) && tree_of != w.b) {
-                tree_of = w.b;
-                sync_threads<128>(2 + unit);
-                if (r < a.len_q) {
-                    const int32_t *parents = p.t.parents ? p.t.parents + static_cast<int64_t>(w.b) * a.len_q : nullptr;
-                    Bits line = 0;
-                    int32_t n = -1;
-                    if (parents) {
-                        for (int32_t at = r; at >= 0; ++n) {
-                            line |= Bits(1) << at;
-                            const int32_t up = __ldg(parents + at);
-                            if (up < -1 || up >= at) {
-                                line = 0;
-                                break;
-                            }
-                            at = up;
-                        }
-                    } else {
-                        line = ~Bits(0) >> (kMaxNodes - 1 - r), n = r;
-                    }
-                    seen[r] = line, depth[r] = static_cast<int16_t>(n);
-                }
-                sync_threads<128>(2 + unit);
-            }
-            if (has_bias && values_of != w.pack) {
-                values_of = w.pack;
-                sync_threads<128>(2 + unit);
-                for (int32_t t = r; t < a.buckets.total * p.pack; t += kRows)
-                    values[t] = to_f32(static_cast<const T *>(a.table)[t / p.pack * a.heads + w.head0 + t % p.pack]);
-                sync_threads<128>(2 + unit);
-            }
-            const Bits line = (tree || has_bias) && valid ? seen[i] : 0;
+            const float *values = reinterpret_cast<const float *>(smem + S::kTable) + buffer * kTableValues + (valid ? head_at : 0);
+            const Bits line = (tree || has_bias) && valid ? seen[buffer][i] : 0;
             const bool absent = (tree || has_bias) && line == 0;
-            const int32_t my_depth = has_bias && valid && !absent ? depth[i] : 0;
-            const float far_bias = has_bias && valid ? values[bucket[far] * p.pack + head_at] : 0.0f;
+            const int32_t my_depth = has_bias && valid ? depth[buffer][i] : 0;
+            const float far_bias = has_bias ? values[bucket[far] * p.pack] : 0.0f;
             float top = -INFINITY, sum = 0.0f;
             const int32_t count = kTiles == 1 ? (w.tiles + 1 - unit) / 2 : unit == 0 || w.second ? w.tiles : 0;
 #pragma unroll 1
@@ -457,53 +510,50 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 barrier_wait(scored + 8 * unit, turn & 1u, &stalled);
                 tmem_fence_after();
                 if (any) {
-                    uint32_t s[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_load(s[c], mine + 32 * c);
-                    tmem_wait_load(s[0], s[1], s[2], s[3]);
-                    if (kBias) {
-                        const float2 scale = make_float2(a.scale, a.scale);
-                        if (!has_bias || w.cached - (j0 + kKeys - 1) >= far) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
+                    const bool near = has_bias && w.cached - (j0 + kKeys - 1) < far, masked = j0 + kKeys > w.cached;
+                    const int32_t shift = w.cached - j0;  // the tree's first row in the tile
+                    const Bits visible = !masked ? ~Bits(0) : absent ? Bits(0) : shift >= 0 ? ((Bits(1) << shift) - 1) | line << shift : line >> -shift;
+                    float tile_top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t s[32];
+                        tmem_load(s, mine + 32 * c);
+                        tmem_wait_load(s);
+                        if (kBias) {
+                            const float2 scale = make_float2(a.scale, a.scale);
+                            if (!near) {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale,
+                                    const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale,
                                                           make_float2(far_bias, far_bias));
-                                    s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
+                                    s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
                                 }
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
+                            } else {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) {
-                                    const int32_t node = j0 + 32 * c + e - w.cached;
-                                    const int32_t d = my_depth - (node < 0 ? node : static_cast<int32_t>(depth[min(node, a.len_q - 1)]));
-                                    s[c][e] = __float_as_uint(fmaf(__uint_as_float(s[c][e]), a.scale,
-                                                                   values[bucket[min(max(d, 0), far)] * p.pack + (valid ? head_at : 0)]));
+                                    const int32_t node = 32 * c + e - shift;
+                                    const int32_t d = my_depth - (node < 0 ? node : static_cast<int32_t>(depth[buffer][min(node, a.len_q - 1)]));
+                                    s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), a.scale, values[bucket[min(max(d, 0), far)] * p.pack]));
                                 }
+                            }
                         }
-                    }
-                    if (j0 + kKeys > w.cached) {
-                        const int32_t shift = w.cached - j0;  // the tree's first row
-                        const Bits visible = absent ? Bits(0) : shift >= 0 ? (Bits(1) << shift) - 1 | line << shift : line >> -shift;
-                        const uint32_t word[4] = {static_cast<uint32_t>(visible), static_cast<uint32_t>(visible >> 32),
-                                                  static_cast<uint32_t>(visible >> 64), static_cast<uint32_t>(visible >> 96)};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
+                        if (masked) {
+                            const uint32_t word = static_cast<uint32_t>(visible >> 32 * c);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!(word[c] >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);
-                    }
-                    float most[4];
+                                if (!(word >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
+                        }
+                        if (kBias || masked) tmem_store(mine + 32 * c, s);
+                        float most[2] = {__uint_as_float(s[0]), __uint_as_float(s[1])};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        most[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                        for (int e = 1; e < 31; e += 2) most[c] = max3(most[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                        most[c] = fmaxf(most[c], __uint_as_float(s[c][31]));
+                        for (int e = 2; e < 30; e += 4) {
+                            most[0] = max3(most[0], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                            most[1] = max3(most[1], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                        }
+                        most[0] = max3(most[0], __uint_as_float(s[30]), __uint_as_float(s[31]));
+                        tile_top = max3(tile_top, most[0], most[1]);
                     }
-                    const float tile_top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                    if (kBias || masked) tmem_wait_store();
                     // a new maximum, and O and the sum brought to it: at the first finite score, or 2^8 above the old one
                     const bool raise = tile_top > top && (top == -INFINITY || (tile_top - top) * to_base2 > 8.0f);
                     if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -524,24 +574,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     }
                     // exp2((s - top) to_base2): as one multiply-add, or, where a bias may be the type's
                     // lowest value, with the difference taken first
-                    const float from = top == -INFINITY ? 0.0f : -top, shift = kBias ? kLift : fmaf(from, to_base2, kLift);
-                    const float2 from2 = make_float2(from, from), shift2 = make_float2(shift, shift);
+                    const float from = top == -INFINITY ? 0.0f : -top, add = kBias ? kLift : fmaf(from, to_base2, kLift);
+                    const float2 from2 = make_float2(from, from), add_2 = make_float2(add, add);
                     const float2 base2 = make_float2(to_base2, to_base2);
                     float2 total = make_float2(0.0f, 0.0f);
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t q[16], rest[16];
+                        uint32_t s[32], q[16], rest[16];
+                        tmem_load(s, mine + 32 * c);
+                        tmem_wait_load(s);
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            float2 v = make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                            float2 v = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                             if (kBias) v = add2(v, from2);
-                            const float2 f = fma2(v, base2, shift2), x = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                            const float2 f = fma2(v, base2, add_2), x = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                             total = add2(total, x);
                             q[e / 2] = pack2<T>(x.x, x.y);
                             if (kTwoTerms) rest[e / 2] = rest2<T>(x, q[e / 2]);
                         }
-                        tmem_store(mine + 16 * c, q);
-                        if (kTwoTerms) tmem_store(mine + kKeys / 2 + 16 * c, rest);
+                        tmem_store(mine + 32 * c, q);
+                        if (kTwoTerms) tmem_store(mine + 32 * c + 16, rest);
                     }
                     sum += total.x + total.y;
                     tmem_wait_store();
@@ -550,6 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 __syncwarp();
                 if (lane == 0) barrier_arrive(ready + 8 * unit);
             }
+            if (lane == 0) barrier_arrive(taken + 8 * buffer);
 
             // ---- the piece's result
             if (count) {
@@ -639,11 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 p.meta[blockIdx.x * 2 + slot] = make_int4(w.b, w.unit, w.tile0, kIsThere | (whole ? 0 : kIsPart) | (w.tile0 == 0 ? kStarts : 0) |
                                                                                        (w.tile0 + w.tiles == w.all ? kEnds : 0));
             if (threadIdx.x == 0 && parts == 0) p.meta[blockIdx.x * 2 + 1] = make_int4(0, 0, 0, 0);
-            ++parts, ++piece;
-            // Both units have read O before the next piece's first P is announced; and they leave together, also when a
-            // wait of one of them ran out.
-            tmem_fence_before();
-            if (!(kTiles == 1 ? all_of<256>(1, !stalled) : all_of<128>(2 + unit, !stalled))) break;
+            ++parts;
         }
         if (threadIdx.x == 0 && parts == 0) p.meta[blockIdx.x * 2] = p.meta[blockIdx.x * 2 + 1] = make_int4(0, 0, 0, 0);
     }
@@ -721,8 +770,9 @@ TreePlan tree_plan(const Attention &a)
     f.part_rows = f.tiles * f.pack * f.nodes_per;
     const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
     f.parts = key_tiles >= 2 * kLeastPart;
-    const int64_t most = static_cast<int64_t>(a.batch) * f.packs * f.pairs * key_tiles;
-    f.blocks = most < sm_count() ? static_cast<int32_t>(most) : static_cast<int32_t>(sm_count());
+    // the list of key tiles has less than 2^31 entries: more would be 2^38 rows of keys
+    const double most = static_cast<double>(a.batch) * f.packs * f.pairs * key_tiles;
+    f.blocks = most > 0x7FFFFFFF ? 0 : most < sm_count() ? static_cast<int32_t>(most) : static_cast<int32_t>(sm_count());
     return f;
 }
 
@@ -778,8 +828,9 @@ cudaError_t launch_tree_attention(const TreeAttention &t, cudaStream_t s)
     TreeParams p;
     p.t = t;
     p.pack = f.pack, p.nodes_per = f.nodes_per, p.packs = f.packs, p.pairs = f.pairs, p.part_rows = f.part_rows;
-    if (static_cast<int64_t>(f.packs) * f.pairs > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (!f.blocks) return cudaErrorInvalidValue;
     p.units = f.packs * f.pairs;
+    p.by_pack = Divider(f.pack), p.by_pairs = Divider(f.pairs), p.by_group = Divider(a.group), p.by_blocks = Divider(f.blocks);
     p.meta = static_cast<int4 *>(a.workspace);
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + meta_bytes(f));
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
