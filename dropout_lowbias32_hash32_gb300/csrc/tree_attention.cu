@@ -2,16 +2,16 @@
 // (include/rng.h, rng_tree_attention_fwd) on the tensor cores.
 //
 // The rows of a key head, its query heads' nodes, are packed into tiles of 128,
-// so that its keys are read once; two units a block, each with a tile of rows, an S
-// and an O in TMEM and a warpgroup, a row to a thread:
-//   kTiles = 1 (at most 128 rows): the units take every other tile of 128 keys
-//     and are joined at the end;
-//   kTiles = 2: the units have two tiles of rows and share the key tiles.
+// so that its keys are read once.  A unit is such a tile with an O in TMEM and two
+// warpgroups: two threads to a row, each with half of a tile's 128 keys; they
+// exchange the row's maximum of a tile through shared memory.
+//   kTiles = 1 (at most 128 rows): one unit with two S, so that a tile's products
+//     run under the next one's exponentials;
+//   kTiles = 2: two units that share the key tiles, with an S each.
 // A unit's step is S = Q K^T, P = exp(S - max) written back over S in 16 bits, O +=
-// P V; one warp issues both units' products in turn, so that one unit's
-// exponentials run under the other's products.  One warp issues the TMA loads, one
-// clears value rows that nobody may look at, one has the next pieces of work ready:
-// the nodes' lines, the biases.
+// P V.  One warp issues all products, one the TMA loads, one clears value rows that
+// nobody may look at, one has the next pieces of work ready: the nodes' lines, the
+// biases.
 //
 // The work is the list of all (batch entry, key head, rows) and their key tiles,
 // cut evenly among the blocks by the lengths found on the device.  A block's first
@@ -26,10 +26,6 @@ namespace rngk {
 namespace {
 
 constexpr int kRows = 128, kKeys = 128;  // a unit's tile
-constexpr int kThreads = 384;            // a warpgroup a unit, and one of the other roles' warps
-constexpr uint32_t kTmaWarp = 8, kMmaWarp = 9, kClearWarp = 10;  // and one for the pieces
-// registers: 384 threads start with 168 each; 2 x 208 + 80 <= 3 x 168
-constexpr int kUnitRegisters = 208, kOtherRegisters = 80;
 constexpr uint32_t kBox = 16384;  // bytes of 128 rows of 64 elements
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxNodes = RNG_MAX_TREE_NODES;
@@ -58,12 +54,15 @@ template <int kDim, int kTiles>
 struct Shape {
     static constexpr int kBoxes = kDim / 64;
     static constexpr int kQBuffers = 3 - kTiles;
+    static constexpr int kThreads = 256 * kTiles + 128;  // two warpgroups a unit, and one of the other roles' warps
+    // registers: 384 threads start with 168 each, 2 x 208 + 80 <= 3 x 168; 640 with 96, 4 x 104 + 64 = 5 x 96
+    static constexpr int kUnitRegisters = kTiles == 1 ? 208 : 104, kOtherRegisters = kTiles == 1 ? 80 : 64;
+    static constexpr uint32_t kTmaWarp = 8 * kTiles, kMmaWarp = kTmaWarp + 1, kClearWarp = kTmaWarp + 2;  // and one for the pieces
     static constexpr int kStages = kDim == 64 ? 8 : 4;
     static constexpr uint32_t kTileBytes = kBoxes * kBox;
-    static constexpr uint32_t kRing = 2 * kTileBytes;                                     // after two tiles of queries
-    static constexpr uint32_t kHand = kRing + kStages * kTileBytes;                       // unit 1's O for unit 0, 32 columns at a time
-    static constexpr uint32_t kTable = kHand + (kTiles == 1 ? 32 * kRows * 4 : 0);        // bias values of two pieces
-    static constexpr uint32_t kBuckets = kTable + 2 * kTableValues * 4;                   // bucket by distance
+    static constexpr uint32_t kRing = 2 * kTileBytes;                    // after two tiles of queries
+    static constexpr uint32_t kTable = kRing + kStages * kTileBytes;     // bias values of two pieces
+    static constexpr uint32_t kBuckets = kTable + 2 * kTableValues * 4;  // bucket by distance
 };
 
 __device__ __forceinline__ int32_t cached_of(const Attention &a, int32_t b)
@@ -163,11 +162,12 @@ __device__ __forceinline__ void find_lines(const TreeAttention &t, int32_t b, Bi
 }
 
 template <class T, int kDim, int kTiles, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __grid_constant__ TreeParams p)
+__global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attention_kernel(const __grid_constant__ TreeParams p)
 {
     using S = Shape<kDim, kTiles>;
     constexpr bool kTwoTerms = kTiles == 1;
-    constexpr int kTogether = kTiles == 1 ? 256 : 128;  // threads that work on a piece's rows
+    constexpr int kThreads = S::kThreads;
+    constexpr int kLead = kTiles == 1 ? 2 : 1;  // tiles whose S there is room for
     // f16 holds 2^15: P below 2^8 is lifted, so that long rows' small ones keep their bits
     constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
     constexpr uint32_t kBars = 3 * S::kStages + 11;  // that one arrival completes
@@ -181,23 +181,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     __shared__ Bits seen[2][kMaxNodes];                      // [piece's parity][node]: the nodes of its line
     __shared__ int16_t depth[2][kMaxNodes], jump[kMaxNodes];  // nodes before it
     __shared__ uint32_t odd[kOddBuffers][4];                 // nodes with an infinity or NaN among their values
-    __shared__ float tops[2][kRows], sums[2][kRows];
+    __shared__ float tops[2][kTiles][2][kRows], sums[kTiles][2][kRows];  // [tile's parity][unit][half][row]
     const Attention &a = p.t.a;
     const uint32_t warp = uniform(threadIdx.x / 32u), lane = threadIdx.x % 32u;
     uint8_t *smem = dynamic + ((1024u - (smem_address(dynamic) & 1023u)) & 1023u);
     const uint32_t base = smem_address(smem);
 
     const uint32_t full = smem_address(bars), empty = full + 8 * S::kStages, tail = empty + 8 * S::kStages,
-                   scored = tail + 8 * S::kStages, done = scored + 16, q_full = done + 16, q_empty = q_full + 16,
+                   scored = tail + 8 * S::kStages, added = scored + 16, q_full = added + 16, q_empty = q_full + 16,
                    drained = q_empty + 16, prepared = drained + 8, ready = prepared + 16, taken = ready + 16;
     if (threadIdx.x < kBars + 4) {
-        barrier_init(full + 8 * threadIdx.x, threadIdx.x < kBars ? 1 : threadIdx.x < kBars + 2 ? 4 : 8);
+        barrier_init(full + 8 * threadIdx.x, threadIdx.x < kBars ? 1 : 8 * (threadIdx.x < kBars + 2 ? 1 : kTiles));
         fence_barrier_init();
     } else if (threadIdx.x == 64) {
         stalled = 0;
         prefetch_map(&p.q), prefetch_map(&p.k), prefetch_map(&p.v);
     }
-    if (warp == kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
+    if (warp == S::kMmaWarp) tmem_alloc<512>(smem_address(&tmem_base));
     if (kBias && a.table) {
         uint8_t *bucket = smem + S::kBuckets;
         for (int32_t d = threadIdx.x; d <= a.buckets.max_distance; d += kThreads) bucket[d] = static_cast<uint8_t>(bucket_of(a.buckets, -d));
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
         __syncthreads();
         if (lane == 31) scan[warp] = up_to;
         __syncthreads();
-        uint32_t w = lane < kThreads / 32 ? scan[lane] : 0;
+        const uint32_t w = lane < kThreads / 32 ? scan[lane] : 0;
         before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0) + up_to - v;
         return __reduce_add_sync(0xFFFFFFFFu, w);
     };
@@ -249,9 +249,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     cursor.end = cut_end;
     Piece w;
 
-    if (warp >= kTmaWarp) {
-        give_registers<kOtherRegisters>();
-        if (warp == kTmaWarp) {
+    if (warp >= S::kTmaWarp) {
+        give_registers<S::kOtherRegisters>();
+        if (warp == S::kTmaWarp) {
             // ---- TMA: a piece's queries, then its keys and values in the order in which the products take them
             uint32_t use = 0, piece = 0, on_tail = 0, tail_turns = 0;  // bit s: stage s's last tile, the parity of its next
             bool fine = true;
@@ -270,8 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                             tma_load_5d(base + (kTiles == 2 ? t : buffer) * S::kTileBytes + c * kBox, &p.q, q_full + 8 * buffer, c * 64, 0,
                                         w.node0 + t * p.nodes_per, w.pack, w.b);
                 }
-                constexpr int32_t kLead = kTiles == 1 ? 2 : 1;  // K_0 .. K_{lead-1}, then V_n and K_{n+lead}
-#pragma unroll 1
+#pragma unroll 1  // K_0 .. K_{lead-1}, then V_n and K_{n+lead}
                 for (int32_t n = -2 * kLead; n < 2 * w.tiles; ++n) {
                     const bool value = n >= 0 && n % 2 == 0;
                     const int32_t tile = value ? n / 2 : n < 0 ? n / 2 + kLead : n / 2 + kLead;
@@ -302,47 +301,44 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     else barrier_drain(full + 8 * stage, u / S::kStages & 1u);
                 }
             }
-        } else if (warp == kMmaWarp) {
+        } else if (warp == S::kMmaWarp) {
             // ---- MMA
             constexpr uint32_t kScores = mma_shape<T>(kKeys, false), kOut = mma_shape<T>(kDim, true);
             const uint64_t ring_v = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kBox : 1024);
             const uint64_t ring_k = row_major_tile(base + S::kRing), qd = row_major_tile(base);
-            uint32_t use = 0, piece = 0, given = 0;  // given: bit u, the parity of unit u's next P
+            uint32_t use = 0, piece = 0, given = 0;  // given: bit s, the parity of S s's next P
             bool fine = true;
             auto loaded = [&](uint32_t u) {
                 fine = fine && barrier_wait(full + 8 * (u % S::kStages), u / S::kStages & 1u, &stalled);
                 tmem_fence_after();
             };
-            auto written = [&](uint32_t unit) {
-                fine = fine && barrier_wait(ready + 8 * unit, given >> unit & 1u, &stalled);
-                given ^= 1u << unit;
-                tmem_fence_after();
-            };
-            // S = Q K^T of a unit; frees: whether this was the key tile's last use
-            auto score = [&](uint32_t unit, uint32_t queries, uint32_t u, bool frees, bool frees_q, uint32_t buffer) {
+            // S = Q K^T
+            auto score = [&](uint32_t which, uint32_t queries, uint32_t u, bool frees, bool frees_q, uint32_t buffer) {
                 if (fine && elect_one()) {
                     const uint64_t kd = ring_k + (u % S::kStages) * (S::kTileBytes / 16), q = qd + queries * (S::kTileBytes / 16);
 #pragma unroll
-                    for (int i = 0; i < kDim / 16; ++i) mma_step(tmem + unit * 256, q + row_step(i, kBox), kd + row_step(i, kBox), kScores, i > 0);
-                    mma_commit(scored + 8 * unit);
+                    for (int i = 0; i < kDim / 16; ++i) mma_step(tmem + which * kKeys, q + row_step(i, kBox), kd + row_step(i, kBox), kScores, i > 0);
+                    mma_commit(scored + 8 * which);
                     if (frees) mma_commit(empty + 8 * (u % S::kStages));
                     if (frees_q) mma_commit(q_empty + 8 * buffer);
                 }
                 __syncwarp();
             };
-            // O += P V of a unit; P lies where the scores were, 16 columns for 32 keys, and beside them its second term
-            auto add = [&](uint32_t unit, uint32_t u, bool first, bool frees, bool last) {
+            // O += P V over `steps` of 16 keys; P lies where the scores were, 16 columns for 32 keys, and beside them its
+            // second term
+            auto add = [&](uint32_t which, uint32_t unit, uint32_t u, int32_t steps, bool first, bool frees) {
                 if (fine && elect_one()) {
                     const uint64_t vd = ring_v + (u % S::kStages) * (S::kTileBytes / 16);
-                    const uint32_t at = tmem + unit * 256;
+                    const uint32_t at = tmem + which * kKeys, o = tmem + (2 + unit) * kKeys;
 #pragma unroll
                     for (int i = 0; i < kKeys / 16; ++i) {
+                        if (i >= steps) break;
                         const uint32_t from = at + (i / 2) * 32 + i % 2 * 8;
-                        mma_step_tmem(at + kKeys, from, vd + i * (2048 / 16), kOut, !first || i > 0);
-                        if (kTwoTerms) mma_step_tmem(at + kKeys, from + 16, vd + i * (2048 / 16), kOut, true);
+                        mma_step_tmem(o, from, vd + i * (2048 / 16), kOut, !first || i > 0);
+                        if (kTwoTerms) mma_step_tmem(o, from + 16, vd + i * (2048 / 16), kOut, true);
                     }
                     if (frees) mma_commit(empty + 8 * (u % S::kStages));
-                    if (last) mma_commit(done + 8 * unit);
+                    mma_commit(added + 8 * unit);
                 }
                 __syncwarp();
             };
@@ -351,9 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 fine = barrier_wait(q_full + 8 * buffer, piece / S::kQBuffers & 1u, &stalled);
                 ++piece;
                 tmem_fence_after();
-                // a step: the sums of tile n (from 0 on), then the scores of the one that takes their place
-                const uint32_t last = kTiles == 1 ? 0 : w.second ? 1 : 0;
-                constexpr int32_t kLead = kTiles == 1 ? 2 : 1;
+                // a step: the sums of tile n (from 0 on), then the scores of the one that takes its place
+                const uint32_t last = w.second ? 1 : 0;
+                const int32_t keys = w.cached + a.len_q - w.tile0 * kKeys;
 #pragma unroll 1
                 for (int32_t n = -kLead; n < w.tiles && fine; ++n) {
                     const int32_t next = n + kLead;
@@ -361,21 +357,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     if (n < 0 && next >= w.tiles) continue;
 #pragma unroll 1
                     for (uint32_t u = 0; u <= last && fine; ++u) {
-                        const uint32_t unit = kTiles == 1 ? n & 1 : u;
+                        const uint32_t which = kTiles == 1 ? n & 1 : u;
                         if (n >= 0) {
                             if (u == 0) loaded(value);
-                            written(unit);
-                            add(unit, value, n < kLead, u == last, n + kLead >= w.tiles);
+                            fine = fine && barrier_wait(ready + 8 * which, given >> which & 1u, &stalled);
+                            given ^= 1u << which;
+                            tmem_fence_after();
+                            add(which, u, value, (keys - n * kKeys + 15) / 16, n == 0, u == last);
                         }
                         if (next >= w.tiles) continue;
                         if (u == 0) loaded(key);
-                        score(unit, kTiles == 1 ? buffer : u, key, u == last, u == last && next == w.tiles - 1, buffer);
+                        score(which, kTiles == 1 ? buffer : u, key, u == last, u == last && next == w.tiles - 1, buffer);
                     }
                     use += (n >= 0 ? 1 : 0) + (next < w.tiles ? 1 : 0);
                 }
             }
             if (stalled && elect_one()) mma_commit(drained), barrier_drain(drained, 0);
-        } else if (warp == kClearWarp) {
+        } else if (warp == S::kClearWarp) {
             // ---- value rows of the tree: those past it and of absent nodes become zeros, as P's zeros want it;
             // infinities and NaN of the others too, which the rows that see them add at the end
             uint32_t use = 0, piece = 0, turns = 0;  // turns: bit s, the parity of stage s's next tile
@@ -404,12 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     fine = barrier_wait(tail + 8 * stage, turns >> stage & 1u, &stalled);
                     turns ^= 1u << stage;
                     if (!fine) break;
-                    const int32_t j0 = (w.tile0 + n) * kKeys;
+                    const int32_t j0 = (w.tile0 + n) * kKeys, end = min(kKeys, (w.cached + a.len_q - j0 + 15) / 16 * 16);  // what the products take
                     uint8_t *rows = smem + S::kRing + stage * S::kTileBytes;
                     // a finite number's bits without its sign, plus this, stay below 2^15
                     constexpr uint32_t kToSign = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
 #pragma unroll 4
-                    for (int32_t j = max(0, w.cached - j0) + static_cast<int32_t>(lane / 8); j < kKeys; j += 4) {  // a row to 8 lanes
+                    for (int32_t j = max(0, w.cached - j0) + static_cast<int32_t>(lane / 8); j < end; j += 4) {  // a row to 8 lanes
                         const int32_t node = j0 + j - w.cached;
                         const uint32_t word = node < 64 ? node < 32 ? there[0] : there[1] : node < 96 ? there[2] : there[3];
                         const bool gone = node >= kMaxNodes || !(word >> node % 32 & 1u);
@@ -470,26 +468,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             }
         }
     } else {
-        take_registers<kUnitRegisters>();
+        take_registers<S::kUnitRegisters>();
         // ---- the units' rows
-        const int unit = warp / 4;
+        const int unit = warp / 8, half = warp / 4 % 2;
         const int32_t r = (warp % 4) * 32 + lane;
         int32_t local_node, head_at;
         p.by_pack.divide(r, local_node, head_at);
-        const uint32_t mine = tmem + unit * 256 + ((warp % 4) * 32u << 16), out = mine + kKeys;
+        const uint32_t lanes = tmem + ((warp % 4) * 32u << 16), out = lanes + (2 + unit) * kKeys + half * (kDim / 2);
+        const int pair = 1 + kTiles + unit * 4 + warp % 4;  // the barrier of the two warps that share rows
         const float to_base2 = kBias ? kLog2e : a.scale * kLog2e;
         const uint8_t *bucket = smem + S::kBuckets;
         const bool has_bias = kBias && a.table;
         const int32_t far = has_bias ? a.buckets.max_distance : 0;
-        uint32_t turn = 0, finished = 0, parts = 0;
+        uint32_t turns = 0, additions = 0, parts = 0;  // turns: bit s, the parity of S s's next tile
 #pragma unroll 1
         for (uint32_t piece = 0;; ++piece) {
-            // Both units have read O before the next piece's first P is announced; and they leave together, also when a
-            // wait of one of them ran out.
+            // They leave together, also when a wait of one of them ran out.
             tmem_fence_before();
             const uint32_t buffer = piece & 1u;
             const bool fine = barrier_wait(prepared + 8 * buffer, piece / 2 & 1u, &stalled);
-            if (!all_of<kTogether>(kTiles == 1 ? 1 : 2 + unit, fine && !stalled)) break;
+            if (!all_of<256>(1 + unit, fine && !stalled)) break;
             w = pieces[buffer];
             if (w.tiles == 0) break;
             const int32_t i = w.node0 + (kTiles == 2 ? unit * p.nodes_per : 0) + local_node, head = w.head0 + head_at;
@@ -503,19 +501,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             const int32_t my_depth = has_bias && valid ? depth[buffer][i] : 0;
             const float far_bias = has_bias ? values[bucket[far] * p.pack] : 0.0f;
             float top = -INFINITY, sum = 0.0f;
-            const int32_t count = kTiles == 1 ? (w.tiles + 1 - unit) / 2 : unit == 0 || w.second ? w.tiles : 0;
+            const int32_t count = unit == 0 || w.second ? w.tiles : 0;
 #pragma unroll 1
-            for (int32_t n = 0; n < count; ++n, ++turn) {
-                const int32_t j0 = (w.tile0 + (kTiles == 1 ? 2 * n + unit : n)) * kKeys;
-                barrier_wait(scored + 8 * unit, turn & 1u, &stalled);
+            for (int32_t n = 0; n < count; ++n) {
+                const uint32_t which = kTiles == 1 ? n & 1 : unit;
+                const uint32_t mine = lanes + which * kKeys + half * (kKeys / 2);
+                const int32_t j0 = (w.tile0 + n) * kKeys + half * (kKeys / 2);  // this half's
+                barrier_wait(scored + 8 * which, turns >> which & 1u, &stalled);
+                turns ^= 1u << which;
                 tmem_fence_after();
                 if (any) {
-                    const bool near = has_bias && w.cached - (j0 + kKeys - 1) < far, masked = j0 + kKeys > w.cached;
-                    const int32_t shift = w.cached - j0;  // the tree's first row in the tile
-                    const Bits visible = !masked ? ~Bits(0) : absent ? Bits(0) : shift >= 0 ? ((Bits(1) << shift) - 1) | line << shift : line >> -shift;
-                    float tile_top = -INFINITY;
+                    const bool near = has_bias && w.cached - (j0 + kKeys / 2 - 1) < far, masked = j0 + kKeys / 2 > w.cached;
+                    const int32_t shift = w.cached - j0;  // the tree's first row
+                    uint64_t visible = ~uint64_t(0);
+                    if (masked)
+                        visible = static_cast<uint64_t>(absent ? Bits(0) : shift >= 0 ? ((Bits(1) << shift) - 1) | line << shift : shift > -kMaxNodes ? line >> -shift : Bits(0));
+                    float most[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t s[32];
                         tmem_load(s, mine + 32 * c);
                         tmem_wait_load(s);
@@ -544,25 +547,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                                 if (!(word >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
                         }
                         if (kBias || masked) tmem_store(mine + 32 * c, s);
-                        float most[2] = {__uint_as_float(s[0]), __uint_as_float(s[1])};
 #pragma unroll
-                        for (int e = 2; e < 30; e += 4) {
+                        for (int e = 0; e < 32; e += 4) {
                             most[0] = max3(most[0], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                             most[1] = max3(most[1], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
                         }
-                        most[0] = max3(most[0], __uint_as_float(s[30]), __uint_as_float(s[31]));
-                        tile_top = max3(tile_top, most[0], most[1]);
                     }
                     if (kBias || masked) tmem_wait_store();
+                    // the row's maximum, of both halves
+                    float(&shared_tops)[2][kRows] = tops[n & 1][unit];
+                    float tile_top = fmaxf(most[0], most[1]);
+                    shared_tops[half][r] = tile_top;
+                    sync_threads<64>(pair);
+                    tile_top = fmaxf(tile_top, shared_tops[half ^ 1][r]);
                     // a new maximum, and O and the sum brought to it: at the first finite score, or 2^8 above the old one
                     const bool raise = tile_top > top && (top == -INFINITY || (tile_top - top) * to_base2 > 8.0f);
                     if (__any_sync(0xFFFFFFFFu, raise)) {
                         const float fade = raise ? exp2_approx((top - tile_top) * to_base2) : 1.0f;
                         sum *= fade;
                         if (raise) top = tile_top;
-                        if (n > 0) {  // (the products that O is made of were issued before this S)
+                        if (n > 0) {
+                            // O up to the previous tile (kTiles = 2: its products were issued before this S)
+                            if (kTiles == 1) barrier_wait(added, (additions + n - 1) & 1u, &stalled);
+                            tmem_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < kDim / 16; ++c) {
+                            for (int c = 0; c < kDim / 32; ++c) {
                                 uint32_t o[16];
                                 tmem_load(o, out + 16 * c);
                                 tmem_wait_load(o);
@@ -574,12 +583,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                     }
                     // exp2((s - top) to_base2): as one multiply-add, or, where a bias may be the type's
                     // lowest value, with the difference taken first
-                    const float from = top == -INFINITY ? 0.0f : -top, add = kBias ? kLift : fmaf(from, to_base2, kLift);
-                    const float2 from2 = make_float2(from, from), add_2 = make_float2(add, add);
+                    const float from = top == -INFINITY ? 0.0f : -top, shift_2 = kBias ? kLift : fmaf(from, to_base2, kLift);
+                    const float2 from2 = make_float2(from, from), shift2 = make_float2(shift_2, shift_2);
                     const float2 base2 = make_float2(to_base2, to_base2);
                     float2 total = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t s[32], q[16], rest[16];
                         tmem_load(s, mine + 32 * c);
                         tmem_wait_load(s);
@@ -587,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                         for (int e = 0; e < 32; e += 2) {
                             float2 v = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
                             if (kBias) v = add2(v, from2);
-                            const float2 f = fma2(v, base2, add_2), x = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                            const float2 f = fma2(v, base2, shift2), x = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                             total = add2(total, x);
                             q[e / 2] = pack2<T>(x.x, x.y);
                             if (kTwoTerms) rest[e / 2] = rest2<T>(x, q[e / 2]);
@@ -600,27 +609,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
                 }
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) barrier_arrive(ready + 8 * unit);
+                if (lane == 0) barrier_arrive(ready + 8 * which);
             }
             if (lane == 0) barrier_arrive(taken + 8 * buffer);
 
             // ---- the piece's result
+            sums[unit][half][r] = sum;
+            sync_threads<64>(pair);
+            sum += sums[unit][half ^ 1][r];
             if (count) {
-                barrier_wait(done + 8 * unit, finished++ & 1u, &stalled);
+                additions += count;
+                // (one after the other: a wait tells a phase from the next one only)
+                if (kTiles == 1 && count > 1) barrier_wait(added, (additions - 2) & 1u, &stalled);
+                barrier_wait(added + 8 * unit, (additions - 1) & 1u, &stalled);
                 tmem_fence_after();
             }
-            const bool whole = w.tiles == w.all, two = kTiles == 1 && w.tiles > 1, writes = kTiles == 2 || unit == 0;
-            float weight = 1.0f, other = 0.0f;
-            if (two) {
-                tops[unit][r] = top, sums[unit][r] = sum;
-                sync_threads<256>(1);
-                const float top1 = tops[unit ^ 1][r], sum1 = sums[unit ^ 1][r], most = fmaxf(top, top1);
-                weight = top == -INFINITY ? 0.0f : exp2_approx((top - most) * to_base2);
-                other = top1 == -INFINITY ? 0.0f : exp2_approx((top1 - most) * to_base2);
-                // (without a maximum, the sum is 0, or NaN where the scores are)
-                sum = (top == -INFINITY ? sum : sum * weight) + (top1 == -INFINITY ? sum1 : sum1 * other);
-                top = most;
-            }
+            const bool whole = w.tiles == w.all;
             // whether it sees values that the products did not
             const uint32_t(&odd_nodes)[4] = odd[piece % kOddBuffers];
             bool some_odd = false;
@@ -633,56 +637,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
             float *part = p.part + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.part_rows + (kTiles == 2 ? unit * p.pack * p.nodes_per : 0) + r) * (kDim + 2);
             const float scale = !whole ? 1.0f : sum == 0.0f || absent ? 0.0f : 1.0f / sum;
             T *o_row = static_cast<T *>(a.out) + w.b * a.os.batch + i * a.os.len + head * a.os.head;
-            float *hand = reinterpret_cast<float *>(smem + S::kHand) + r;
 #pragma unroll 1
-            for (int c = 0; c < kDim / 32; ++c) {
+            for (int c = 0; c < kDim / 64; ++c) {
+                const int col = half * (kDim / 2) + 32 * c;
                 uint32_t o[32] = {};
                 if (count && any) {
                     tmem_load(o, out + 32 * c);
                     tmem_wait_load(o);
                 }
-                if (two) {  // unit 1 hands its part to unit 0
-                    if (c) sync_threads<256>(1);
-                    if (unit == 1 && any) {
+                if (!valid) continue;
+                float v[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) hand[e * kRows] = __uint_as_float(o[e]);
-                    }
-                    sync_threads<256>(1);
+                for (int e = 0; e < 32; ++e) {
+                    v[e] = __uint_as_float(o[e]);
+                    if (sum == 0.0f || absent) v[e] = 0.0f;  // nothing seen
+                    v[e] *= scale;
                 }
-                if (valid && writes) {
-                    float v[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        v[e] = __uint_as_float(o[e]);
-                        if (two) v[e] = v[e] * weight + hand[e * kRows] * other;
-                        if (sum == 0.0f || absent) v[e] = 0.0f;  // nothing seen
-                        v[e] *= scale;
-                    }
-                    if (some_odd) {
+                if (some_odd) {
 #pragma unroll 1
-                        for (int32_t t = 0; t <= i; ++t) {
-                            if (!(odd_nodes[t / 32] >> t % 32 & 1u) || !(line >> t & 1u)) continue;
-                            const T *value = static_cast<const T *>(a.v) + w.b * a.vs.batch + (w.cached + t) * a.vs.len + w.head_kv * a.vs.head + 32 * c;
+                    for (int32_t t = 0; t <= i; ++t) {
+                        if (!(odd_nodes[t / 32] >> t % 32 & 1u) || !(line >> t & 1u)) continue;
+                        const T *value = static_cast<const T *>(a.v) + w.b * a.vs.batch + (w.cached + t) * a.vs.len + w.head_kv * a.vs.head + col;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const float x = 32 * c + e < a.dim ? to_f32(value[e]) : 0.0f;
-                                if (!(fabsf(x) < INFINITY)) v[e] += x;
-                            }
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = col + e < a.dim ? to_f32(value[e]) : 0.0f;
+                            if (!(fabsf(x) < INFINITY)) v[e] += x;
                         }
                     }
-                    if (whole) {
+                }
+                if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            const float(&eight)[8] = *reinterpret_cast<const float(*)[8]>(&v[e]);
-                            if (32 * c + e < a.dim) store<T, 8>(o_row + 32 * c + e, eight);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2 *>(part + 32 * c + e) = make_float2(v[e], v[e + 1]);
+                    for (int e = 0; e < 32; e += 8) {
+                        const float(&eight)[8] = *reinterpret_cast<const float(*)[8]>(&v[e]);
+                        if (col + e < a.dim) store<T, 8>(o_row + col + e, eight);
                     }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2 *>(part + col + e) = make_float2(v[e], v[e + 1]);
                 }
             }
-            if (valid && writes) {
+            if (valid && half == 0) {
                 if (!whole)
                     part[kDim] = top * to_natural, part[kDim + 1] = absent ? -1.0f : sum;
                 else if (a.lse)
@@ -698,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const __gri
     }
     __syncthreads();
     tmem_fence_after();
-    if (warp == kMmaWarp) tmem_free<512>(tmem);
+    if (warp == S::kMmaWarp) tmem_free<512>(tmem);
 }
 
 // Puts the parts of the entries together that blocks have cut: a block to a
@@ -788,7 +782,7 @@ cudaError_t launch(const TreeParams &p, const TreePlan &f, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const size_t bytes = 1024 + S::kTable + (kBias ? S::kBuckets - S::kTable + 1040 : 0);
     static_assert(1024 + S::kBuckets + 1040 <= 222 * 1024, "beside the static arrays");
-    kernel<<<f.blocks, kThreads, bytes, s>>>(p);
+    kernel<<<f.blocks, S::kThreads, bytes, s>>>(p);
     note_launch();
     if (f.parts) {
         join_kernel<T, kDim, kTiles><<<dim3(f.blocks, (p.part_rows + 7) / 8), dim3(32, 8), 0, s>>>(p);
