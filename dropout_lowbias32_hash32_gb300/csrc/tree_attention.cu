@@ -43,7 +43,7 @@ struct TreeParams {
     // packs x pairs, rows of a part
     int32_t pack, nodes_per, packs, pairs, units, part_rows;
     Divider by_pack, by_pairs, by_group, by_blocks;
-    float *part;  // [blocks][2][part_rows][dim padded + 2]: O, max, sum
+    float *part;  // [blocks][2][dim padded + 2][part_rows]: O, max, sum, rows adjacent
     int4 *meta;   // [blocks][2]: batch entry, unit, first key tile, state
 };
 
@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = tmem_base;
-    Cursor cursor = shared_cursor;
-    cursor.end = cut_end;
+    const uint32_t tmem = uniform(tmem_base);
+    Cursor cursor{uniform(shared_cursor.at), uniform(cut_end), uniform(shared_cursor.base), uniform(shared_cursor.b),
+                  uniform(shared_cursor.cached), uniform(shared_cursor.tiles)};
     Piece w;
 
     if (warp >= S::kTmaWarp) {
@@ -330,12 +330,17 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                 if (fine && elect_one()) {
                     const uint64_t vd = ring_v + (u % S::kStages) * (S::kTileBytes / 16);
                     const uint32_t at = tmem + which * kKeys, o = tmem + (2 + unit) * kKeys;
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i) {
-                        if (i >= steps) break;
+                    auto step = [&](int i) {
                         const uint32_t from = at + (i / 2) * 32 + i % 2 * 8;
                         mma_step_tmem(o, from, vd + i * (2048 / 16), kOut, !first || i > 0);
                         if (kTwoTerms) mma_step_tmem(o, from + 16, vd + i * (2048 / 16), kOut, true);
+                    };
+                    if (steps >= kKeys / 16) {
+#pragma unroll
+                        for (int i = 0; i < kKeys / 16; ++i) step(i);
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < steps; ++i) step(i);
                     }
                     if (frees) mma_commit(empty + 8 * (u % S::kStages));
                     mma_commit(added + 8 * unit);
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
             }
             const float to_natural = kBias ? 1.0f : a.scale;
             const int32_t slot = parts == 0 ? 0 : 1;
-            float *part = p.part + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.part_rows + (kTiles == 2 ? unit * p.pack * p.nodes_per : 0) + r) * (kDim + 2);
+            float *part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.part_rows * (kDim + 2) + unit * kRows + r;
             const float scale = !whole ? 1.0f : sum == 0.0f || absent ? 0.0f : 1.0f / sum;
             T *o_row = static_cast<T *>(a.out) + w.b * a.os.batch + i * a.os.len + head * a.os.head;
 #pragma unroll 1
@@ -673,12 +678,12 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) *reinterpret_cast<float2 *>(part + col + e) = make_float2(v[e], v[e + 1]);
+                    for (int e = 0; e < 32; ++e) part[(col + e) * p.part_rows] = v[e];
                 }
             }
             if (valid && half == 0) {
                 if (!whole)
-                    part[kDim] = top * to_natural, part[kDim + 1] = absent ? -1.0f : sum;
+                    part[kDim * p.part_rows] = top * to_natural, part[(kDim + 1) * p.part_rows] = absent ? -1.0f : sum;
                 else if (a.lse)
                     a.lse[index] = sum == 0.0f || absent ? -INFINITY : top * to_natural + (logf(sum) - kLift * 0.6931471805599453f);
             }
@@ -696,50 +701,74 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
 }
 
 // Puts the parts of the entries together that blocks have cut: a block to a
-// block of the above and some rows, a warp to a row.  An entry's last part is the
-// first piece of its block; the others are found going back from there.
+// block of the above, 32 rows and 64 columns, a thread to a row and 8 columns.  An
+// entry's last part is the first piece of its block; the others lie in the blocks
+// before it, which a warp looks up 32 at a time.
 template <class T, int kDim, int kTiles>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeParams p)
 {
     const Attention &a = p.t.a;
-    int32_t block = blockIdx.x, slot = 0;
-    const int4 last = p.meta[block * 2];
+    const int4 last = p.meta[blockIdx.x * 2];
     if (!(last.w & kIsPart) || (last.w & kStarts) || !(last.w & kEnds)) return;
-    const uint32_t lane = threadIdx.x;
-    const int32_t row = blockIdx.y * 8 + threadIdx.y, pair = last.y % p.pairs;
-    const int32_t i = pair * kTiles * p.nodes_per + row / p.pack, head = last.y / p.pairs * p.pack + row % p.pack, b = last.x;
-    if (row >= p.part_rows || i >= a.len_q) return;
-    constexpr int kEach = kDim / 32;
     constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
-    float top = -INFINITY, sum = 0.0f, o[kEach] = {};
-    bool absent = false;
-    for (;;) {
-        const float2 *at = reinterpret_cast<const float2 *>(p.part + ((static_cast<int64_t>(block) * 2 + slot) * p.part_rows + row) * (kDim + 2));
-        const float2 stats = at[kDim / 2];
-        absent = absent || stats.y < 0.0f;
-        if (stats.y != 0.0f) {
-            const float next = fmaxf(top, stats.x), fade = exp2_approx((top - next) * kLog2e), weight = exp2_approx((stats.x - next) * kLog2e);
-            sum = (top == -INFINITY ? 0.0f : sum * fade) + stats.y * weight;
-#pragma unroll
-            for (int k = 0; k < kEach; k += 2) {
-                const float2 v = at[lane * (kEach / 2) + k / 2];
-                o[k] = (top == -INFINITY ? 0.0f : o[k] * fade) + v.x * weight, o[k + 1] = (top == -INFINITY ? 0.0f : o[k + 1] * fade) + v.y * weight;
-            }
-            top = next;
+    constexpr int kAtOnce = 4;
+    const int32_t lane = threadIdx.x, row = blockIdx.y * 32 + lane, col = blockIdx.z * 64 + threadIdx.y * 8;
+    int32_t pack, pair, local_node, head_at;
+    p.by_pairs.divide(last.y, pack, pair);
+    p.by_pack.divide(row % kRows, local_node, head_at);
+    const int32_t i = (pair * kTiles + row / kRows) * p.nodes_per + local_node, head = pack * p.pack + head_at, b = last.x;
+    const bool valid = local_node < p.nodes_per && i < a.len_q;
+    float top = -INFINITY, sum = 0.0f, o[8] = {};
+    bool absent = false, started = false;
+    for (int32_t block0 = blockIdx.x; !started && block0 >= 0; block0 -= 32) {
+        // a lane to a block: the slot of its part of this entry, -1 for none
+        const int32_t block = block0 - lane;
+        int32_t slot = -1;
+        bool starts = false;
+        if (block >= 0) {
+            const int4 first = p.meta[block * 2], second = p.meta[block * 2 + 1];
+            if (block == static_cast<int32_t>(blockIdx.x)) slot = 0;
+            else if (second.w & kIsPart) slot = 1, starts = true;
+            else if (first.w & kIsThere) slot = 0, starts = first.w & kStarts;
         }
-        if (p.meta[block * 2 + slot].w & kStarts) break;
-        do --block;
-        while (block > 0 && !(p.meta[block * 2].w & kIsThere));
-        if (block < 0) break;
-        slot = p.meta[block * 2 + 1].w & kIsPart ? 1 : 0;
-    }
-    if (absent) sum = 0.0f;
-    const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-    T *out = static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head;
+        const uint32_t stops = __ballot_sync(0xFFFFFFFFu, starts);
+        started = stops != 0;
+        uint32_t there = __ballot_sync(0xFFFFFFFFu, slot >= 0) & (stops ? (2u << (__ffs(stops) - 1)) - 1u : 0xFFFFFFFFu);
+        while (there) {
+            float stats[kAtOnce][2], v[kAtOnce][8];
 #pragma unroll
-    for (int k = 0; k < kEach; ++k)
-        if (lane * kEach + k < a.dim) out[lane * kEach + k] = from_f32<T>(sum == 0.0f ? 0.0f : o[k] * scale);
-    if (a.lse && lane == 0)
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int32_t which = there ? __ffs(there) - 1 : -1;
+                there &= there - 1u;
+                const int32_t at_slot = __shfl_sync(0xFFFFFFFFu, slot, which < 0 ? 0 : which);
+                const float *at = p.part + (static_cast<int64_t>(block0 - which) * 2 + at_slot) * p.part_rows * (kDim + 2) + row;
+                const bool reads = which >= 0 && valid;
+                stats[u][0] = reads ? at[kDim * p.part_rows] : -INFINITY, stats[u][1] = reads ? at[(kDim + 1) * p.part_rows] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[u][k] = reads ? at[(col + k) * p.part_rows] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                absent = absent || stats[u][1] < 0.0f;
+                if (stats[u][1] == 0.0f) continue;
+                const float next = fmaxf(top, stats[u][0]), fade = top == -INFINITY ? 0.0f : exp2_approx((top - next) * kLog2e);
+                const float weight = exp2_approx((stats[u][0] - next) * kLog2e);
+                sum = sum * fade + stats[u][1] * weight;
+                top = next;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = o[k] * fade + v[u][k] * weight;
+            }
+        }
+    }
+    if (!valid) return;
+    if (absent) sum = 0.0f;
+    if (col < a.dim) {
+        const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = sum == 0.0f ? 0.0f : o[k] * scale;
+        store<T, 8>(static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head + col, o);
+    }
+    if (a.lse && col == 0)
         a.lse[(static_cast<int64_t>(b) * a.heads + head) * a.len_q + i] = sum == 0.0f ? -INFINITY : top + (logf(sum) - kLift * 0.6931471805599453f);
 }
 
@@ -761,7 +790,7 @@ TreePlan tree_plan(const Attention &a)
     const int32_t tiles = (a.len_q + f.nodes_per - 1) / f.nodes_per;
     f.tiles = tiles == 1 ? 1 : 2;
     f.packs = a.heads / f.pack, f.pairs = (tiles + f.tiles - 1) / f.tiles;
-    f.part_rows = f.tiles * f.pack * f.nodes_per;
+    f.part_rows = f.tiles == 2 ? 2 * kRows : (f.pack * f.nodes_per + 31) / 32 * 32;
     const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
     f.parts = key_tiles >= 2 * kLeastPart;
     // the list of key tiles has less than 2^31 entries: more would be 2^38 rows of keys
@@ -785,7 +814,7 @@ cudaError_t launch(const TreeParams &p, const TreePlan &f, cudaStream_t s)
     kernel<<<f.blocks, S::kThreads, bytes, s>>>(p);
     note_launch();
     if (f.parts) {
-        join_kernel<T, kDim, kTiles><<<dim3(f.blocks, (p.part_rows + 7) / 8), dim3(32, 8), 0, s>>>(p);
+        join_kernel<T, kDim, kTiles><<<dim3(f.blocks, p.part_rows / 32, kDim / 64), dim3(32, 8), 0, s>>>(p);
         note_launch();
     }
     return cudaGetLastError();
