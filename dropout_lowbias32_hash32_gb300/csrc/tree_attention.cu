@@ -79,27 +79,30 @@ struct Piece {
     int32_t second;  // (kTiles = 2) whether the second tile has rows
 };
 
-// A block's pieces, one after the other.
+// A block's pieces, one after the other.  In the list that is cut, a unit's key
+// tiles come after kTiles entries that stand for what a unit costs beside them (its
+// first loads and last sums: about 1.2 tiles' time, 2 where tiles of rows share
+// them).
 struct Cursor {
-    uint32_t at, end, base;  // in the list of all key tiles; base: where the batch entry's begin
-    int32_t b, cached, tiles;  // its cached rows, and key tiles of one unit
+    uint32_t at, end, base;  // in the list; base: where the batch entry's units begin
+    int32_t b, cached, length;  // its cached rows, and entries of one unit
 
     template <int kTiles>
     __device__ __forceinline__ bool next(const TreeParams &p, Piece &w)
     {
         if (at >= end) return false;
         const Attention &a = p.t.a;
-        while (at >= base + static_cast<uint32_t>(tiles) * p.units) {
-            base += static_cast<uint32_t>(tiles) * p.units;
+        while (at >= base + static_cast<uint32_t>(length) * p.units) {
+            base += static_cast<uint32_t>(length) * p.units;
             cached = uniform(cached_of(a, ++b));
-            tiles = tiles_for(a, cached);
+            length = tiles_for(a, cached) + kTiles;
         }
         const uint32_t local = at - base;
-        w.b = b, w.all = tiles, w.cached = cached;
-        w.unit = static_cast<int32_t>(local / static_cast<uint32_t>(tiles));
-        w.tile0 = static_cast<int32_t>(local) - w.unit * tiles;
-        w.tiles = min(w.all - w.tile0, static_cast<int32_t>(end - at));
-        at += w.tiles;
+        w.unit = static_cast<int32_t>(local / static_cast<uint32_t>(length));
+        const int32_t from = static_cast<int32_t>(local) - w.unit * length, to = min(length, from + static_cast<int32_t>(end - at));
+        at += to - from;
+        w.b = b, w.cached = cached, w.all = length - kTiles;
+        w.tile0 = max(from - kTiles, 0), w.tiles = to - kTiles - w.tile0;
         int32_t pair;
         p.by_pairs.divide(w.unit, w.pack, pair);
         w.head0 = w.pack * p.pack, w.head_kv = p.by_group.quotient(w.head0);
@@ -110,10 +113,11 @@ struct Cursor {
 };
 
 // Where the list is cut at x: at a unit's own beginning or end rather than less than kLeastPart tiles from it.
-__device__ __forceinline__ uint32_t snapped(uint32_t x, uint32_t base, uint32_t tiles)
+template <int kTiles>
+__device__ __forceinline__ uint32_t snapped(uint32_t x, uint32_t base, uint32_t length)
 {
-    const uint32_t o = (x - base) % tiles;
-    return o < kLeastPart ? x - o : tiles - o < kLeastPart ? x - o + tiles : x;
+    const uint32_t o = (x - base) % length;
+    return o < kTiles + kLeastPart ? x - o : length - o < kLeastPart ? x - o + length : x;
 }
 
 // The lines of a tree's nodes (the node and those before it; none for an absent one) and the number of nodes before
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
         const int32_t mine = threadIdx.x;
         uint32_t sum = 0, before, so_far = 0;
         int32_t cached = 0;
-        for (int32_t b = mine; b < a.batch; b += kThreads) cached = cached_of(a, b), sum += tiles_for(a, cached);
+        for (int32_t b = mine; b < a.batch; b += kThreads) cached = cached_of(a, b), sum += tiles_for(a, cached) + kTiles;
         const uint32_t all = block_sum(sum, before) * p.units;
         const uint32_t share = p.by_blocks.quotient(all), left = all - share * p.by_blocks.by;
         const uint32_t from = blockIdx.x * share + min(blockIdx.x, left), to = from + share + (blockIdx.x < left ? 1 : 0);
@@ -230,15 +234,15 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
         for (int32_t b0 = 0; b0 < a.batch; b0 += kThreads) {
             const int32_t b = b0 + mine;
             if (a.batch > kThreads) {  // (else the first sum had one entry to a thread)
-                sum = b < a.batch ? cached = cached_of(a, b), tiles_for(a, cached) : 0;
+                sum = b < a.batch ? cached = cached_of(a, b), tiles_for(a, cached) + kTiles : 0;
                 const uint32_t part = block_sum(sum, before);
                 before += so_far, so_far += part;
             } else {
                 __syncthreads();
             }
             const uint32_t begin = before * p.units, past = begin + sum * p.units;
-            if (from >= begin && from < past) shared_cursor = Cursor{snapped(from, begin, sum), 0, begin, b, cached, static_cast<int32_t>(sum)};
-            if (to >= begin && to < past) cut_end = snapped(to, begin, sum);
+            if (from >= begin && from < past) shared_cursor = Cursor{snapped<kTiles>(from, begin, sum), 0, begin, b, cached, static_cast<int32_t>(sum)};
+            if (to >= begin && to < past) cut_end = snapped<kTiles>(to, begin, sum);
         }
     }
     tmem_fence_before();
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
     tmem_fence_after();
     const uint32_t tmem = uniform(tmem_base);
     Cursor cursor{uniform(shared_cursor.at), uniform(cut_end), uniform(shared_cursor.base), uniform(shared_cursor.b),
-                  uniform(shared_cursor.cached), uniform(shared_cursor.tiles)};
+                  uniform(shared_cursor.cached), uniform(shared_cursor.length)};
     Piece w;
 
     if (warp >= S::kTmaWarp) {
@@ -303,6 +307,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
             }
         } else if (warp == S::kMmaWarp) {
             // ---- MMA
+            constexpr int kUnrolled = kTiles == 1 ? 1 : 8;
             constexpr uint32_t kScores = mma_shape<T>(kKeys, false), kOut = mma_shape<T>(kDim, true);
             const uint64_t ring_v = column_major_tile(base + S::kRing, S::kBoxes > 1 ? kBox : 1024);
             const uint64_t ring_k = row_major_tile(base + S::kRing), qd = row_major_tile(base);
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
             auto score = [&](uint32_t which, uint32_t queries, uint32_t u, bool frees, bool frees_q, uint32_t buffer) {
                 if (fine && elect_one()) {
                     const uint64_t kd = ring_k + (u % S::kStages) * (S::kTileBytes / 16), q = qd + queries * (S::kTileBytes / 16);
-#pragma unroll
+#pragma unroll(kUnrolled)
                     for (int i = 0; i < kDim / 16; ++i) mma_step(tmem + which * kKeys, q + row_step(i, kBox), kd + row_step(i, kBox), kScores, i > 0);
                     mma_commit(scored + 8 * which);
                     if (frees) mma_commit(empty + 8 * (u % S::kStages));
@@ -330,17 +335,12 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                 if (fine && elect_one()) {
                     const uint64_t vd = ring_v + (u % S::kStages) * (S::kTileBytes / 16);
                     const uint32_t at = tmem + which * kKeys, o = tmem + (2 + unit) * kKeys;
-                    auto step = [&](int i) {
+#pragma unroll(kUnrolled)
+                    for (int i = 0; i < kKeys / 16; ++i) {
+                        if (i >= steps) break;
                         const uint32_t from = at + (i / 2) * 32 + i % 2 * 8;
                         mma_step_tmem(o, from, vd + i * (2048 / 16), kOut, !first || i > 0);
                         if (kTwoTerms) mma_step_tmem(o, from + 16, vd + i * (2048 / 16), kOut, true);
-                    };
-                    if (steps >= kKeys / 16) {
-#pragma unroll
-                        for (int i = 0; i < kKeys / 16; ++i) step(i);
-                    } else {
-#pragma unroll 1
-                        for (int i = 0; i < steps; ++i) step(i);
                     }
                     if (frees) mma_commit(empty + 8 * (u % S::kStages));
                     mma_commit(added + 8 * unit);
@@ -411,28 +411,40 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                     uint8_t *rows = smem + S::kRing + stage * S::kTileBytes;
                     // a finite number's bits without its sign, plus this, stay below 2^15
                     constexpr uint32_t kToSign = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
-#pragma unroll 4
-                    for (int32_t j = max(0, w.cached - j0) + static_cast<int32_t>(lane / 8); j < end; j += 4) {  // a row to 8 lanes
-                        const int32_t node = j0 + j - w.cached;
-                        const uint32_t word = node < 64 ? node < 32 ? there[0] : there[1] : node < 96 ? there[2] : there[3];
-                        const bool gone = node >= kMaxNodes || !(word >> node % 32 & 1u);
+                    constexpr int kAtOnce = 4;
+                    auto over = [&](uint32_t y) { return (y & 0x7FFF7FFFu) + kToSign; };
+                    auto finite = [&](uint32_t y) {
+                        const uint32_t o = over(y);
+                        return y & ~((o & 0x8000u ? 0xFFFFu : 0u) | (o & 0x80000000u ? 0xFFFF0000u : 0u));
+                    };
+                    uint8_t *at16 = rows + lane % 8 * 16;  // a row to 8 lanes
+#pragma unroll 1
+                    for (int32_t j4 = max(0, w.cached - j0) + static_cast<int32_t>(lane / 8); j4 < end; j4 += 4 * kAtOnce) {
+                        uint4 x[kAtOnce][S::kBoxes];
 #pragma unroll
-                        for (int c = 0; c < S::kBoxes; ++c) {
-                            uint4 *at16 = reinterpret_cast<uint4 *>(rows + c * kBox + j * 128 + lane % 8 * 16);
-                            if (gone) {
-                                *at16 = make_uint4(0, 0, 0, 0);
-                                continue;
+                        for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+                            for (int c = 0; c < S::kBoxes; ++c)
+                                x[u][c] = *reinterpret_cast<const uint4 *>(at16 + c * kBox + min(j4 + 4 * u, kKeys - 1) * 128);
+#pragma unroll
+                        for (int u = 0; u < kAtOnce; ++u) {
+                            const int32_t j = j4 + 4 * u, node = j0 + j - w.cached;
+                            const uint32_t word = node < 64 ? node < 32 ? there[0] : there[1] : node < 96 ? there[2] : there[3];
+                            const bool gone = node >= kMaxNodes || !(word >> node % 32 & 1u);
+                            bool infinite = false;
+#pragma unroll
+                            for (int c = 0; c < S::kBoxes; ++c) {
+                                const uint4 y = x[u][c];
+                                infinite = infinite || ((over(y.x) | over(y.y) | over(y.z) | over(y.w)) & 0x80008000u);
                             }
-                            uint4 x = *at16;
-                            auto over = [&](uint32_t y) { return (y & 0x7FFF7FFFu) + kToSign; };
-                            if ((over(x.x) | over(x.y) | over(x.z) | over(x.w)) & 0x80008000u) {
-                                auto finite = [&](uint32_t y) {
-                                    const uint32_t o = over(y);
-                                    return y & ~((o & 0x8000u ? 0xFFFFu : 0u) | (o & 0x80000000u ? 0xFFFF0000u : 0u));
-                                };
-                                *at16 = make_uint4(finite(x.x), finite(x.y), finite(x.z), finite(x.w));
-                                atomicOr(&odd_nodes[node / 32], 1u << node % 32);
+                            if (j >= end || !(gone || infinite)) continue;
+#pragma unroll
+                            for (int c = 0; c < S::kBoxes; ++c) {
+                                const uint4 y = x[u][c];
+                                *reinterpret_cast<uint4 *>(at16 + c * kBox + j * 128) =
+                                    gone ? make_uint4(0, 0, 0, 0) : make_uint4(finite(y.x), finite(y.y), finite(y.z), finite(y.w));
                             }
+                            if (!gone) atomicOr(&odd_nodes[node / 32], 1u << node % 32);
                         }
                     }
                     fence_async_shared();
@@ -521,44 +533,49 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                     uint64_t visible = ~uint64_t(0);
                     if (masked)
                         visible = static_cast<uint64_t>(absent ? Bits(0) : shift >= 0 ? ((Bits(1) << shift) - 1) | line << shift : shift > -kMaxNodes ? line >> -shift : Bits(0));
-                    float most[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t s[32];
-                        tmem_load(s, mine + 32 * c);
-                        tmem_wait_load(s);
-                        if (kBias) {
-                            const float2 scale = make_float2(a.scale, a.scale);
-                            if (!near) {
+                    uint32_t s[2][32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) tmem_load(s[c], mine + 32 * c);
+                    tmem_wait_load(s[0], s[1]);
+                    if (kBias) {
+                        const float2 scale = make_float2(a.scale, a.scale);
+                        if (!near) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    const float2 f = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale,
+                                    const float2 f = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale,
                                                           make_float2(far_bias, far_bias));
-                                    s[e] = __float_as_uint(f.x), s[e + 1] = __float_as_uint(f.y);
+                                    s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
                                 }
-                            } else {
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) {
                                     const int32_t node = 32 * c + e - shift;
                                     const int32_t d = my_depth - (node < 0 ? node : static_cast<int32_t>(depth[buffer][min(node, a.len_q - 1)]));
-                                    s[e] = __float_as_uint(fmaf(__uint_as_float(s[e]), a.scale, values[bucket[min(max(d, 0), far)] * p.pack]));
+                                    s[c][e] = __float_as_uint(fmaf(__uint_as_float(s[c][e]), a.scale, values[bucket[min(max(d, 0), far)] * p.pack]));
                                 }
-                            }
                         }
-                        if (masked) {
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
                             const uint32_t word = static_cast<uint32_t>(visible >> 32 * c);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (!(word >> e & 1u)) s[e] = __float_as_uint(-INFINITY);
-                        }
-                        if (kBias || masked) tmem_store(mine + 32 * c, s);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            most[0] = max3(most[0], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-                            most[1] = max3(most[1], __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+                                if (!(word >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);
                         }
                     }
-                    if (kBias || masked) tmem_wait_store();
+                    float most[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            most[0] = max3(most[0], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                            most[1] = max3(most[1], __uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3]));
+                        }
                     // the row's maximum, of both halves
                     float(&shared_tops)[2][kRows] = tops[n & 1][unit];
                     float tile_top = fmaxf(most[0], most[1]);
@@ -592,22 +609,22 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                     const float2 from2 = make_float2(from, from), shift2 = make_float2(shift_2, shift_2);
                     const float2 base2 = make_float2(to_base2, to_base2);
                     float2 total = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t s[32], q[16], rest[16];
-                        tmem_load(s, mine + 32 * c);
-                        tmem_wait_load(s);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float2 v = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+                    for (int c = 0; c < 4; ++c) {  // 16 columns at a time
+                        uint32_t q[8], rest[8];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const uint32_t(&two)[2] = *reinterpret_cast<const uint32_t(*)[2]>(&s[c / 2][c % 2 * 16 + e]);
+                            float2 v = make_float2(__uint_as_float(two[0]), __uint_as_float(two[1]));
                             if (kBias) v = add2(v, from2);
                             const float2 f = fma2(v, base2, shift2), x = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                             total = add2(total, x);
                             q[e / 2] = pack2<T>(x.x, x.y);
                             if (kTwoTerms) rest[e / 2] = rest2<T>(x, q[e / 2]);
                         }
-                        tmem_store(mine + 32 * c, q);
-                        if (kTwoTerms) tmem_store(mine + 32 * c + 16, rest);
+                        const uint32_t to = mine + 32 * (c / 2) + 8 * (c % 2);
+                        tmem_store(to, q);
+                        if (kTwoTerms) tmem_store(to + 16, rest);
                     }
                     sum += total.x + total.y;
                     tmem_wait_store();
@@ -794,8 +811,8 @@ TreePlan tree_plan(const Attention &a)
     const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
     f.parts = key_tiles >= 2 * kLeastPart;
     // the list of key tiles has less than 2^31 entries: more would be 2^38 rows of keys
-    const double most = static_cast<double>(a.batch) * f.packs * f.pairs * key_tiles;
-    f.blocks = most > 0x7FFFFFFF ? 0 : most < sm_count() ? static_cast<int32_t>(most) : static_cast<int32_t>(sm_count());
+    const double units = static_cast<double>(a.batch) * f.packs * f.pairs;
+    f.blocks = units * (key_tiles + f.tiles) > 0x7FFFFFFF ? 0 : units * key_tiles < sm_count() ? static_cast<int32_t>(units * key_tiles) : static_cast<int32_t>(sm_count());
     return f;
 }
 
