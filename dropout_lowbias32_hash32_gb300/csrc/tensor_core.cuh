@@ -105,6 +105,13 @@ struct WorkQueue {
     }
 };
 
+// ---- a launch that may begin under the one before it -----------------------------------
+// The next launch's blocks may start as soon as every block of this one has
+// said so and there is room; they wait for this one's end, and see its writes,
+// at grid_wait.
+__device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // A named barrier of kThreads threads; all_of also tells whether every one of
 // them agrees.
 template <int kThreads>

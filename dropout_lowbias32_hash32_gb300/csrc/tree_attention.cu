@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
     Cursor cursor{uniform(shared_cursor.at), uniform(cut_end), uniform(shared_cursor.base), uniform(shared_cursor.b),
                   uniform(shared_cursor.cached), uniform(shared_cursor.length)};
     Piece w;
+    grid_let_next();
 
     if (warp >= S::kTmaWarp) {
         give_registers<S::kOtherRegisters>();
@@ -718,24 +719,25 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
 }
 
 // Puts the parts of the entries together that blocks have cut: a block to a
-// block of the above, 32 rows and 64 columns, a thread to a row and 8 columns.  An
+// block of the above and 32 rows, a thread to a row and 16 columns.  An
 // entry's last part is the first piece of its block; the others lie in the blocks
 // before it, which a warp looks up 32 at a time.
 template <class T, int kDim, int kTiles>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeParams p)
+__global__ void __launch_bounds__(kDim * 2) join_kernel(const __grid_constant__ TreeParams p)
 {
     const Attention &a = p.t.a;
+    grid_wait();
     const int4 last = p.meta[blockIdx.x * 2];
     if (!(last.w & kIsPart) || (last.w & kStarts) || !(last.w & kEnds)) return;
     constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
-    constexpr int kAtOnce = 4;
-    const int32_t lane = threadIdx.x, row = blockIdx.y * 32 + lane, col = blockIdx.z * 64 + threadIdx.y * 8;
+    constexpr int kAtOnce = 4, kEach = 16;
+    const int32_t lane = threadIdx.x, row = blockIdx.y * 32 + lane, col = threadIdx.y * kEach;
     int32_t pack, pair, local_node, head_at;
     p.by_pairs.divide(last.y, pack, pair);
     p.by_pack.divide(row % kRows, local_node, head_at);
     const int32_t i = (pair * kTiles + row / kRows) * p.nodes_per + local_node, head = pack * p.pack + head_at, b = last.x;
     const bool valid = local_node < p.nodes_per && i < a.len_q;
-    float top = -INFINITY, sum = 0.0f, o[8] = {};
+    float top = -INFINITY, sum = 0.0f, o[kEach] = {};
     bool absent = false, started = false;
     for (int32_t block0 = blockIdx.x; !started && block0 >= 0; block0 -= 32) {
         // a lane to a block: the slot of its part of this entry, -1 for none
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeP
         started = stops != 0;
         uint32_t there = __ballot_sync(0xFFFFFFFFu, slot >= 0) & (stops ? (2u << (__ffs(stops) - 1)) - 1u : 0xFFFFFFFFu);
         while (there) {
-            float stats[kAtOnce][2], v[kAtOnce][8];
+            float stats[kAtOnce][2], v[kAtOnce][kEach];
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
                 const int32_t which = there ? __ffs(there) - 1 : -1;
@@ -762,7 +764,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeP
                 const bool reads = which >= 0 && valid;
                 stats[u][0] = reads ? at[kDim * p.part_rows] : -INFINITY, stats[u][1] = reads ? at[(kDim + 1) * p.part_rows] : 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[u][k] = reads ? at[(col + k) * p.part_rows] : 0.0f;
+                for (int k = 0; k < kEach; ++k) v[u][k] = reads ? at[(col + k) * p.part_rows] : 0.0f;
             }
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u) {
@@ -773,7 +775,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeP
                 sum = sum * fade + stats[u][1] * weight;
                 top = next;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = o[k] * fade + v[u][k] * weight;
+                for (int k = 0; k < kEach; ++k) o[k] = o[k] * fade + v[u][k] * weight;
             }
         }
     }
@@ -782,8 +784,11 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeP
     if (col < a.dim) {
         const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = sum == 0.0f ? 0.0f : o[k] * scale;
-        store<T, 8>(static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head + col, o);
+        for (int k = 0; k < kEach; ++k) o[k] = sum == 0.0f ? 0.0f : o[k] * scale;
+        T *out = static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head + col;
+#pragma unroll
+        for (int k = 0; k < kEach; k += 8)
+            if (col + k < a.dim) store<T, 8>(out + k, *reinterpret_cast<const float(*)[8]>(&o[k]));
     }
     if (a.lse && col == 0)
         a.lse[(static_cast<int64_t>(b) * a.heads + head) * a.len_q + i] = sum == 0.0f ? -INFINITY : top + (logf(sum) - kLift * 0.6931471805599453f);
@@ -831,7 +836,13 @@ cudaError_t launch(const TreeParams &p, const TreePlan &f, cudaStream_t s)
     kernel<<<f.blocks, S::kThreads, bytes, s>>>(p);
     note_launch();
     if (f.parts) {
-        join_kernel<T, kDim, kTiles><<<dim3(f.blocks, p.part_rows / 32, kDim / 64), dim3(32, 8), 0, s>>>(p);
+        cudaLaunchConfig_t config = {};
+        config.gridDim = dim3(f.blocks, p.part_rows / 32), config.blockDim = dim3(32, kDim / 16), config.stream = s;
+        cudaLaunchAttribute early;
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization, early.val.programmaticStreamSerializationAllowed = 1;
+        config.attrs = &early, config.numAttrs = 1;
+        const cudaError_t joined = cudaLaunchKernelEx(&config, join_kernel<T, kDim, kTiles>, p);
+        if (joined != cudaSuccess) return joined;
         note_launch();
     }
     return cudaGetLastError();
