@@ -718,20 +718,22 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
     if (warp == S::kMmaWarp) tmem_free<512>(tmem);
 }
 
-// Puts the parts of the entries together that blocks have cut: a block to a
-// block of the above and 32 rows, a thread to a row and 16 columns.  An
-// entry's last part is the first piece of its block; the others lie in the blocks
-// before it, which a warp looks up 32 at a time.
+// Puts the parts of the entries together that blocks have cut: blocks to a block
+// of the above and 32 rows, a thread to a row and 8 columns.  An entry's last part
+// is the first piece of its block; the others lie in the blocks before it, which a
+// warp looks up 32 at a time.  Few rows have many parts, which are read by many
+// small blocks, eight parts at once; many rows have few (8 x 64 nodes, 32 over 8
+// heads of 128: 28 MB of them).
 template <class T, int kDim, int kTiles>
-__global__ void __launch_bounds__(kDim * 2) join_kernel(const __grid_constant__ TreeParams p)
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeParams p)
 {
     const Attention &a = p.t.a;
     grid_wait();
     const int4 last = p.meta[blockIdx.x * 2];
     if (!(last.w & kIsPart) || (last.w & kStarts) || !(last.w & kEnds)) return;
     constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
-    constexpr int kAtOnce = 4, kEach = 16;
-    const int32_t lane = threadIdx.x, row = blockIdx.y * 32 + lane, col = threadIdx.y * kEach;
+    constexpr int kAtOnce = kTiles == 1 ? 8 : 4, kEach = 8;
+    const int32_t lane = threadIdx.x, row = blockIdx.y * 32 + lane, col = (blockIdx.z * blockDim.y + threadIdx.y) * kEach;
     int32_t pack, pair, local_node, head_at;
     p.by_pairs.divide(last.y, pack, pair);
     p.by_pack.divide(row % kRows, local_node, head_at);
@@ -785,10 +787,7 @@ __global__ void __launch_bounds__(kDim * 2) join_kernel(const __grid_constant__ 
         const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) o[k] = sum == 0.0f ? 0.0f : o[k] * scale;
-        T *out = static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head + col;
-#pragma unroll
-        for (int k = 0; k < kEach; k += 8)
-            if (col + k < a.dim) store<T, 8>(out + k, *reinterpret_cast<const float(*)[8]>(&o[k]));
+        store<T, 8>(static_cast<T *>(a.out) + b * a.os.batch + i * a.os.len + head * a.os.head + col, o);
     }
     if (a.lse && col == 0)
         a.lse[(static_cast<int64_t>(b) * a.heads + head) * a.len_q + i] = sum == 0.0f ? -INFINITY : top + (logf(sum) - kLift * 0.6931471805599453f);
@@ -837,7 +836,8 @@ cudaError_t launch(const TreeParams &p, const TreePlan &f, cudaStream_t s)
     note_launch();
     if (f.parts) {
         cudaLaunchConfig_t config = {};
-        config.gridDim = dim3(f.blocks, p.part_rows / 32), config.blockDim = dim3(32, kDim / 16), config.stream = s;
+        const int warps = p.part_rows <= 32 ? 2 : 8;
+        config.gridDim = dim3(f.blocks, p.part_rows / 32, kDim / 8 / warps), config.blockDim = dim3(32, warps), config.stream = s;
         cudaLaunchAttribute early;
         early.id = cudaLaunchAttributeProgrammaticStreamSerialization, early.val.programmaticStreamSerializationAllowed = 1;
         config.attrs = &early, config.numAttrs = 1;
