@@ -5,15 +5,16 @@
 // Verification.  A cluster of blocks has a batch entry, each block a slice of the
 // vocabulary, each warp a run of the slice.  What the walk needs of the drafts
 // (their probabilities at their parents) is fetched by one block for all at once,
-// so that walking down accepted drafts reads shared memory only; every block walks
-// for itself, from the same numbers.  A row is read when a draft has been rejected:
-// all blocks sum what is left, max(p - c q, 0), and share their sums.  The last
-// token's place is then looked for within the one warp's run where the sum passes
-// u[0] of the whole.
+// so that walking down accepted drafts reads shared memory only; in every block one
+// warp walks, from the same numbers.  A row is read when a draft has been rejected:
+// all warps sum what is left, max(p - c q, 0), and the blocks share their sums.  The
+// last token's place is then looked for within the one run where the sum passes u[0]
+// of the whole.
 //
 // The sums decide whole numbers, so they are kept in pairs of f32 (48 bits): f64
-// would be slower than HBM here (2 operations a cycle and SM), and f32 sums would
-// pick a neighbouring token about once in a thousand draws of a large vocabulary.
+// would be slower than HBM here (2 operations a cycle and SM; one warp of a block
+// may use it), and f32 sums would pick a neighbouring token about once in a thousand
+// draws of a large vocabulary.
 #include <cooperative_groups.h>
 
 #include "attention.h"
@@ -47,6 +48,11 @@ struct Pair {
         lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
         hi = s;
     }
+    __device__ __forceinline__ void add(const Pair &x)
+    {
+        add(x.hi);
+        lo = __fadd_rn(lo, x.lo);
+    }
     __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
 };
 
@@ -69,13 +75,47 @@ struct Nodes {
     float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // probabilities at the parent's row
 };
 
+// What a block's warps sum next: of a node's row, or nothing more.
+struct Command {
+    int32_t node;  // -1: nothing
+    float chi, clo;
+    bool removed;  // whether bits are set
+};
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ double up_to_lane(double w, int32_t lane)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const double y = __shfl_up_sync(0xFFFFFFFFu, w, d);
+        if (lane >= d) w += y;
+    }
+    return w;
+}
+
+// The first lane whose sum up to it, from `before` on, exceeds the bar; -1 for
+// none.  some: the last lane with any weight, -1 for none.  before: the sum before
+// that lane, or of all.
+__device__ __forceinline__ int32_t first_over(double w, double bar, int32_t lane, double &before, int32_t &some)
+{
+    const double up_to = up_to_lane(w, lane);
+    const uint32_t any = __ballot_sync(0xFFFFFFFFu, w > 0.0), over = __ballot_sync(0xFFFFFFFFu, w > 0.0 && before + up_to > bar);
+    some = any ? 31 - __clz(any) : -1;
+    const int32_t found = over ? __ffs(over) - 1 : -1;
+    const double at = __shfl_sync(0xFFFFFFFFu, up_to - w, found < 0 ? 0 : found), all = __shfl_sync(0xFFFFFFFFu, up_to, 31);
+    before += found < 0 ? all : at;
+    return found;
+}
+
 template <class T, bool kDraft>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams v)
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams v)
 {
     extern __shared__ uint32_t removed[];  // without draft probabilities: a bit to a token of the block's slice
     __shared__ Nodes n;
-    __shared__ double totals[2][kMaxCluster], sums[kWarps];
+    __shared__ double totals[2][kMaxCluster];
+    __shared__ Pair sums[kWarps];
     __shared__ int32_t path[kMaxNodes];
+    __shared__ Command command;
     const cg::cluster_group cluster = cg::this_cluster();
     const int32_t rank = static_cast<int32_t>(cluster.block_rank()), blocks = static_cast<int32_t>(cluster.num_blocks());
     const int32_t entry = static_cast<int32_t>(blockIdx.x) / blocks, x = threadIdx.x, warp = x / 32, lane = x % 32;
@@ -101,161 +141,176 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
             to.parent[x] = parent, to.token[x] = token, to.u[x] = u, to.p[x] = p, to.q[x] = q;
         }
     }
-    const int32_t slice = v.run * kWarps, begin = (rank * kWarps + warp) * v.run, end = min(begin + v.run, v.vocab);
-    auto forget = [&] {
-        if (!kDraft)
-            for (int32_t w = x; w < slice / 32; w += kThreads) removed[w] = 0;
-    };
-    forget();
+    const int32_t slice = v.run * kWarps, slice0 = rank * slice;
+    if (!kDraft)
+        for (int32_t w = x; w < slice / 32; w += kThreads) removed[w] = 0;
     cluster.sync();
 
-    // The sum over the whole vocabulary of what is left of a row; each warp's and block's parts stay in `sums` and `totals`.
-    uint32_t parity = 0;
-    auto left_at = [&](int32_t node, int32_t t, float chi, float clo) {
-        const float p = to_f32(target[node * v.target_node + t]);
-        if (kDraft) return left_of(p, to_f32(draft[node * v.draft_node + t]), chi, clo);
-        const uint32_t place = t - rank * slice;
-        return Pair{p > 0.0f && !(removed[place / 32] >> place % 32 & 1u) ? p : 0.0f, 0.0f};
+    // What is left of a token of a row.
+    auto left_at = [&](const Command &k, int32_t t, float p, float q) {
+        if (kDraft) return left_of(p, q, k.chi, k.clo);
+        const uint32_t place = t - slice0;
+        return Pair{p > 0.0f && !(k.removed && (removed[place / 32] >> place % 32 & 1u)) ? p : 0.0f, 0.0f};
     };
-    auto mass_of = [&](int32_t node, double c) {
-        const float chi = static_cast<float>(c), clo = static_cast<float>(c - chi);
-        Pair sum{0.0f, 0.0f};
-#pragma unroll 8
-        for (int32_t t = begin + lane; t < end; t += 32) {
-            const Pair w = left_at(node, t, chi, clo);
-            sum.add(w.hi);
-            if (kDraft) sum.lo = __fadd_rn(sum.lo, w.lo);
-        }
-        double s = sum.value();
-#pragma unroll
-        for (int d = 16; d; d /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        if (lane == 0) sums[warp] = s;
-        __syncthreads();
-        parity ^= 1u;
-        if (x < blocks) {
-            double block = 0.0;
-            for (int w = 0; w < kWarps; ++w) block += sums[w];
-            cluster.map_shared_rank(&totals[0][0], x)[parity * kMaxCluster + rank] = block;
-        }
-        cluster.sync();
-        double all = 0.0;
-        for (int32_t r = 0; r < blocks; ++r) all += totals[parity][r];
-        return all;
-    };
+    auto fetch = [&](const Command &k, int32_t t) { return left_at(k, t, to_f32(target[k.node * v.target_node + t]), kDraft ? to_f32(draft[k.node * v.draft_node + t]) : 0.0f); };
 
-    // ---- the walk
+    // ---- the walk's state, in the first warp of each block
+    constexpr int kWords = kMaxNodes / 32;
     int32_t at = 0, stood = 0;
     double c = 0.0, mass = 1.0;
-    if (x == 0) path[0] = 0;
-    for (bool further = true; further;) {
-        further = false;
-        bool known = true;  // whether mass is the present w's
-        for (int32_t i = at + 1; i < v.nodes; ++i) {
-            if (n.parent[i] != at) continue;
-            const int32_t t = n.token[i];
-            if (kDraft && !known) mass = mass_of(at, c), known = true;
-            double w = n.p[i], bar = n.u[i] * mass;
-            if (kDraft) {
-                w = fma(-c, static_cast<double>(n.q[i]), w);
-                bar *= static_cast<double>(n.q[i]);
-            } else if (__syncthreads_or(x > at && x < i && n.parent[x & (kMaxNodes - 1)] == at && n.token[x & (kMaxNodes - 1)] == t)) {
-                w = 0.0;  // rejected once already
-            }
-            if (!(w > 0.0)) w = 0.0;
-            if (bar < w) {
-                at = i, c = 0.0, mass = 1.0, further = true;
-                if (x == 0) path[++stood] = i;
-                else ++stood;
-                break;
-            }
-            if (kDraft) {
-                c += mass, known = false;
-            } else {
-                mass -= w;
-                const int32_t place = t - rank * slice;
-                if (x == 0 && place >= 0 && place < slice) removed[place / 32] |= 1u << place % 32;
-            }
-        }
-        if (!kDraft && further) {  // another row: nothing is removed there
-            __syncthreads();
-            forget();
-            __syncthreads();
-        }
-    }
-    __syncthreads();
-
-    // ---- the last token
-    double whole = mass_of(at, c);
-    if (!(whole > 0.0)) {
-        c = 0.0;
-        forget();
-        __syncthreads();
-        whole = mass_of(at, c);
-    }
-    int32_t *out = v.out + at0, *out_path = v.path + at0;
-    if (rank == 0) {
-        if (x == 0) v.accepted[entry] = stood;
-        for (int32_t k = x; k < v.nodes; k += kThreads) {
-            out_path[k] = k <= stood ? path[k] : -1;
-            if (k != stood) out[k] = k < stood ? n.token[path[k + 1]] : -1;
-        }
-    }
-    if (!(whole > 0.0)) {
-        if (rank == 0 && x == 0) out[stood] = -1;
-        return;
-    }
-    // The first of some parts for which the sum up to it exceeds the bar; the last that has any where rounding
-    // leaves none.  before: the sum up to it.
-    const double bar = n.u[0] * whole;
-    double before = 0.0;
-    auto pick = [&](const double *part, int32_t count) {
-        int32_t last = -1;
-        double up_to = before, at_last = before;
-        for (int32_t r = 0; r < count; ++r) {
-            if (part[r] > 0.0) last = r, at_last = up_to;
-            up_to += part[r];
-            if (part[r] > 0.0 && up_to > bar) break;
-        }
-        before = at_last;
-        return last;
-    };
-    if (pick(totals[parity], blocks) != rank) return;
-    if (pick(sums, kWarps) != warp) return;
-    // within a warp's run: the lane's part of it, then a token of that part
-    const float chi = static_cast<float>(c), clo = static_cast<float>(c - chi);
-    const int32_t each = v.run / 32, from = begin + lane * each, to = min(from + each, v.vocab);
-    Pair sum{0.0f, 0.0f};
-#pragma unroll 8
-    for (int32_t t = from; t < to; ++t) {
-        const Pair w = left_at(at, t, chi, clo);
-        sum.add(w.hi);
-        if (kDraft) sum.lo = __fadd_rn(sum.lo, w.lo);
-    }
-    auto up_to_lane = [&](double w) {
+    uint32_t kids[kWords];          // children of `at` that are still to be tried
+    bool known = true;              // whether mass is the present w's
+    bool some_removed = false, ending = false, from_p = false, finished = false;
+    uint32_t parity = 0;
+    Command now{0, 0.0f, 0.0f, false};
+    auto look_for_kids = [&] {
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const double y = __shfl_up_sync(0xFFFFFFFFu, w, d);
-            if (lane >= d) w += y;
-        }
-        return w;
+        for (int k = 0; k < kWords; ++k) kids[k] = __ballot_sync(0xFFFFFFFFu, n.parent[32 * k + lane] == at);
     };
-    const double part = sum.value(), up_to = up_to_lane(part);
-    const uint32_t some = __ballot_sync(0xFFFFFFFFu, part > 0.0), over = __ballot_sync(0xFFFFFFFFu, part > 0.0 && before + up_to > bar);
-    const int32_t which = over ? __ffs(over) - 1 : 31 - __clz(some);  // (the warp's sum is above 0: some lane's is)
-    before += __shfl_sync(0xFFFFFFFFu, up_to - part, which);
-    const int32_t first = begin + which * each, past = min(first + each, v.vocab);
-    int32_t token = -1;
-    for (int32_t t0 = first; t0 < past; t0 += 32) {
-        const double w = t0 + lane < past ? left_at(at, t0 + lane, chi, clo).value() : 0.0, so_far = before + up_to_lane(w);
-        const uint32_t any = __ballot_sync(0xFFFFFFFFu, w > 0.0), enough = __ballot_sync(0xFFFFFFFFu, w > 0.0 && so_far > bar);
-        if (enough) {
-            token = t0 + __ffs(enough) - 1;
-            break;
+    auto next_kid = [&] {
+        int32_t i = -1;
+#pragma unroll
+        for (int k = kWords - 1; k >= 0; --k)
+            if (kids[k]) i = 32 * k + __ffs(kids[k]) - 1;
+        return i;
+    };
+    // Bits of the children of `at` that were rejected, in the block's slice.
+    auto forget = [&] {
+        for (int32_t j = lane; j < v.nodes; j += 32) {
+            const uint32_t place = n.token[j] - slice0;
+            if (n.parent[j] == at && place < static_cast<uint32_t>(slice)) removed[place / 32] = 0;
         }
-        if (any) token = t0 + 31 - __clz(any);
-        before = __shfl_sync(0xFFFFFFFFu, so_far, 31);
+        __syncwarp();
+        some_removed = false;
+    };
+    if (warp == 0) {
+        if (lane == 0) path[0] = 0;
+        look_for_kids();
     }
-    if (lane == 0) out[stood] = token;
+
+    for (;;) {
+        if (warp == 0) {
+            while (!ending) {
+                const int32_t i = next_kid();
+                ending = i < 0;
+                if (ending || (kDraft && !known)) break;
+                const int32_t t = n.token[i];
+                const double q = kDraft ? n.q[i] : 1.0;
+                double w = kDraft ? fma(-c, q, static_cast<double>(n.p[i])) : n.p[i];
+                if (!kDraft) {  // a token that was rejected once has nothing left
+                    bool again = false;
+                    for (int32_t j = lane; j < i; j += 32) again = again || (n.parent[j] == at && n.token[j] == t);
+                    if (__any_sync(0xFFFFFFFFu, again)) w = 0.0;
+                }
+                if (!(w > 0.0)) w = 0.0;
+                if (n.u[i] * mass * q < w) {
+                    if (!kDraft && some_removed) forget();
+                    at = i, c = 0.0, mass = 1.0, known = true;
+                    ++stood;
+                    if (lane == 0) path[stood] = i;
+                    look_for_kids();
+                    continue;
+                }
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) kids[k] &= i / 32 == k ? ~(1u << i % 32) : 0xFFFFFFFFu;
+                if (kDraft) {
+                    c += mass, known = false;
+                } else {
+                    mass -= w;
+                    const uint32_t place = t - slice0;
+                    if (lane == 0 && place < static_cast<uint32_t>(slice)) removed[place / 32] |= 1u << place % 32;
+                    some_removed = true;
+                    __syncwarp();
+                }
+            }
+            const float chi = static_cast<float>(c);
+            now = Command{finished ? -1 : at, chi, static_cast<float>(c - chi), some_removed};
+            if (lane == 0) command = now;
+        }
+        __syncthreads();
+        now = command;
+        if (now.node < 0) break;
+        // ---- the sum of what is left of the row; a warp's part stays in `sums`, a block's in `totals`
+        {
+            const int32_t begin = slice0 + warp * v.run + lane, end = min(slice0 + (warp + 1) * v.run, v.vocab);
+            const T *p = target + now.node * v.target_node, *q = draft + now.node * v.draft_node;
+            constexpr int kAtOnce = 8;
+            Pair sum{0.0f, 0.0f};
+            int32_t t = begin;
+            for (; t + 32 * (kAtOnce - 1) < end; t += 32 * kAtOnce) {
+                float a[kAtOnce], b[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) a[k] = to_f32(p[t + 32 * k]), b[k] = kDraft ? to_f32(q[t + 32 * k]) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) sum.add(left_at(now, t + 32 * k, a[k], b[k]));
+            }
+            for (; t < end; t += 32) sum.add(fetch(now, t));
+#pragma unroll
+            for (int d = 16; d; d /= 2) sum.add(Pair{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, d), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, d)});
+            if (lane == 0) sums[warp] = sum;
+        }
+        __syncthreads();
+        parity ^= 1u;
+        if (warp == 0) {
+            double block = lane < kWarps ? sums[lane].value() : 0.0;
+#pragma unroll
+            for (int d = 16; d; d /= 2) block += __shfl_xor_sync(0xFFFFFFFFu, block, d);
+            if (lane < blocks) cluster.map_shared_rank(&totals[0][0], lane)[parity * kMaxCluster + rank] = block;
+        }
+        cluster.sync();
+        if (warp != 0) continue;
+        double part = lane < blocks ? totals[parity][lane] : 0.0;
+        mass = part;
+#pragma unroll
+        for (int d = 16; d; d /= 2) mass += __shfl_xor_sync(0xFFFFFFFFu, mass, d);
+        known = true;
+        if (!ending) continue;
+        if (!(mass > 0.0) && !from_p) {  // nothing is left: from p itself
+            from_p = true, c = 0.0;
+            if (!kDraft) forget();
+            continue;
+        }
+        // ---- the last token
+        int32_t *out = v.out + at0, *out_path = v.path + at0;
+        if (rank == 0) {
+            if (lane == 0) v.accepted[entry] = stood;
+            for (int32_t k = lane; k < v.nodes; k += 32) {
+                out_path[k] = k <= stood ? path[k] : -1;
+                if (k != stood) out[k] = k < stood ? n.token[path[k + 1]] : -1;
+            }
+        }
+        if (!(mass > 0.0)) {
+            if (rank == 0 && lane == 0) out[stood] = -1;
+        } else {
+            // the block, its warp, the lane's part of that warp's run, the token: each time the first whose sum exceeds the
+            // bar, or, where rounding leaves none, the last with any weight, and so on from there
+            double bar = n.u[0] * mass, before = 0.0;
+            auto pick = [&](double w) {
+                int32_t some;
+                const int32_t found = first_over(w, bar, lane, before, some);
+                if (found < 0) bar = INFINITY;
+                return found < 0 ? some : found;
+            };
+            if (pick(part) == rank) {
+                const int32_t begin = slice0 + pick(lane < kWarps ? sums[lane].value() : 0.0) * v.run, each = v.run / 32;
+                const int32_t from = begin + lane * each, to = min(from + each, v.vocab);
+                Pair sum{0.0f, 0.0f};
+#pragma unroll 8
+                for (int32_t t = from; t < to; ++t) sum.add(fetch(now, t));
+                const int32_t first = begin + pick(sum.value()) * each, past = min(first + each, v.vocab);
+                int32_t token = -1;
+                for (int32_t t0 = first; t0 < past; t0 += 32) {
+                    const double w = t0 + lane < past ? fetch(now, t0 + lane).value() : 0.0;
+                    int32_t some;
+                    const int32_t found = first_over(w, bar, lane, before, some);
+                    if (found >= 0 || some >= 0) token = t0 + (found < 0 ? some : found);
+                    if (found >= 0) break;
+                }
+                if (lane == 0) out[stood] = token;
+            }
+        }
+        finished = true;
+    }
 }
 
 // ---- the accepted rows' move
