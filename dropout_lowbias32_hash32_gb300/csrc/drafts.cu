@@ -69,6 +69,26 @@ __device__ __forceinline__ Pair left_of(float p, float q, float chi, float clo)
     return Pair{some ? hi : 0.0f, some ? __fsub_rn(lo, __fsub_rn(hi, s)) : 0.0f};
 }
 
+// The same for two sums at a time.
+struct Pairs {
+    float2 hi, lo;
+    __device__ __forceinline__ static float2 sub(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
+    __device__ __forceinline__ void add(float2 x)
+    {
+        const float2 s = add2(hi, x), b = sub(s, hi);
+        lo = add2(lo, add2(sub(hi, sub(s, b)), sub(x, b)));
+        hi = s;
+    }
+    // p - q, of p at or above 0 and q taken down to p: the difference's error as in a fast two-sum.
+    __device__ __forceinline__ void add_left(float2 p, float2 q)
+    {
+        p = make_float2(fmaxf(p.x, 0.0f), fmaxf(p.y, 0.0f)), q = make_float2(fminf(q.x, p.x), fminf(q.y, p.y));
+        const float2 s = sub(p, q);
+        add(s);
+        lo = add2(lo, sub(sub(p, s), q));
+    }
+};
+
 // What the walk needs, the same in every block of a cluster.
 struct Nodes {
     int32_t parent[kMaxNodes], token[kMaxNodes];
@@ -236,14 +256,24 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             const T *p = target + now.node * v.target_node, *q = draft + now.node * v.draft_node;
             constexpr int kAtOnce = 8;
             Pair sum{0.0f, 0.0f};
+            Pairs two{make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            // after one rejection c is 1, and without any 0: no product
+            const bool plain = kDraft ? now.clo == 0.0f && (now.chi == 0.0f || now.chi == 1.0f) : !now.removed;
+            const bool less = kDraft && now.chi != 0.0f;
             int32_t t = begin;
             for (; t + 32 * (kAtOnce - 1) < end; t += 32 * kAtOnce) {
                 float a[kAtOnce], b[kAtOnce];
 #pragma unroll
-                for (int k = 0; k < kAtOnce; ++k) a[k] = to_f32(p[t + 32 * k]), b[k] = kDraft ? to_f32(q[t + 32 * k]) : 0.0f;
+                for (int k = 0; k < kAtOnce; ++k) a[k] = to_f32(p[t + 32 * k]), b[k] = less ? to_f32(q[t + 32 * k]) : 0.0f;
+                if (plain) {
 #pragma unroll
-                for (int k = 0; k < kAtOnce; ++k) sum.add(left_at(now, t + 32 * k, a[k], b[k]));
+                    for (int k = 0; k < kAtOnce; k += 2) two.add_left(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) sum.add(left_at(now, t + 32 * k, a[k], b[k]));
+                }
             }
+            sum.add(Pair{two.hi.x, two.lo.x}), sum.add(Pair{two.hi.y, two.lo.y});
             for (; t < end; t += 32) sum.add(fetch(now, t));
 #pragma unroll
             for (int d = 16; d; d /= 2) sum.add(Pair{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, d), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, d)});
@@ -492,7 +522,7 @@ rng_status rng_verify_drafts(const rng_verify_drafts_args *args, void *stream)
                    a.draft_stride[1], a.tokens, a.parents, a.uniforms, seed_key(a.seed), a.first_counter, a.path, a.accepted,
                    a.out_tokens, 0};
     int cluster = 1;
-    while (cluster < kMaxCluster && a.vocab > cluster * 2048) cluster *= 2;
+    while (cluster < kMaxCluster && a.vocab > cluster * 2048 && int64_t(a.batch) * cluster * 2 <= 4 * int64_t(sm_count())) cluster *= 2;
     const int32_t warps = cluster * kWarps;
     v.run = ((a.vocab + warps - 1) / warps + 31) / 32 * 32;
     clear_error();
