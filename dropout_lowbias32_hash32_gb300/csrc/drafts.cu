@@ -7,14 +7,15 @@
 // (their probabilities at their parents) is fetched by one block for all at once,
 // so that walking down accepted drafts reads shared memory only; in every block one
 // warp walks, from the same numbers.  A row is read when a draft has been rejected:
-// all warps sum what is left, max(p - c q, 0), and the blocks share their sums.  The
-// last token's place is then looked for within the one run where the sum passes u[0]
-// of the whole.
+// all warps sum what is left, max(p - c q, 0), and the blocks share their sums.  c
+// only grows, so that what later rejections of the same row can leave is what the
+// first one left: while there are more children to try, those tokens' p and q are
+// kept in shared memory, and later sums read nothing else.  The last token is looked
+// for within the one run where the sum passes u[0] of the whole.
 //
 // The sums decide whole numbers, so they are kept in pairs of f32 (48 bits): f64
-// would be slower than HBM here (2 operations a cycle and SM; one warp of a block
-// may use it), and f32 sums would pick a neighbouring token about once in a thousand
-// draws of a large vocabulary.
+// would be slower than HBM here (2 operations a cycle and SM), and f32 sums would
+// pick a neighbouring token about once in a thousand draws of a large vocabulary.
 #include <cooperative_groups.h>
 
 #include "attention.h"
@@ -26,6 +27,7 @@ namespace {
 
 constexpr int kMaxNodes = RNG_MAX_TREE_NODES;
 constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr int kMostKept = 832;  // tokens that a warp keeps: 104 KB a block, two blocks an SM
 
 struct VerifyParams {
     int32_t batch, nodes, vocab;
@@ -35,11 +37,12 @@ struct VerifyParams {
     const float *uniforms;
     uint32_t key, first;
     int32_t *path, *accepted, *out;
-    int32_t run;  // tokens of a warp, a multiple of 32
+    int32_t run;   // tokens of a warp, a multiple of 32
+    int32_t room;  // of which so many have room in shared memory
 };
 
-// A sum of f32 values as a pair, error-free additions (Knuth's two-sum) with
-// intrinsics, which the compiler leaves as they are.
+// A number or a sum as a pair of f32, error-free additions (Knuth's two-sum) and
+// products with intrinsics, which the compiler leaves as they are.
 struct Pair {
     float hi, lo;
     __device__ __forceinline__ void add(float x)
@@ -53,23 +56,50 @@ struct Pair {
         add(x.hi);
         lo = __fadd_rn(lo, x.lo);
     }
-    __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+    // As large a first number as there is (it is the larger of the two already).
+    __device__ __forceinline__ Pair normal() const
+    {
+        const float s = __fadd_rn(hi, lo);
+        return Pair{s, __fsub_rn(lo, __fsub_rn(s, hi))};
+    }
 };
 
-// max(p - c q, 0) as a pair, c = chi + clo: the product's error by a fused
-// multiply-add, the difference's by two-sum.
-__device__ __forceinline__ Pair left_of(float p, float q, float chi, float clo)
+__device__ __forceinline__ Pair times(float a, float b)
 {
-    const float t = __fmul_rn(chi, q), te = __fmaf_rn(chi, q, -t);
+    const float t = __fmul_rn(a, b);
+    return Pair{t, __fmaf_rn(a, b, -t)};
+}
+__device__ __forceinline__ Pair times(const Pair &a, const Pair &b)
+{
+    Pair t = times(a.hi, b.hi);
+    t.lo = __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, t.lo));
+    return t.normal();
+}
+__device__ __forceinline__ Pair plus(Pair a, const Pair &b)
+{
+    a.add(b);
+    return a.normal();
+}
+__device__ __forceinline__ Pair minus(const Pair &a, const Pair &b) { return plus(a, Pair{-b.hi, -b.lo}); }
+__device__ __forceinline__ bool less(const Pair &a, const Pair &b)  // of normal pairs
+{
+    return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) < 0.0f;
+}
+
+// max(p - c q, 0): the product's error by a fused multiply-add, the difference's by
+// two-sum.
+__device__ __forceinline__ Pair left_of(float p, float q, const Pair &c)
+{
+    const float t = __fmul_rn(c.hi, q), te = __fmaf_rn(c.hi, q, -t);
     const float s = __fsub_rn(p, t), b = __fsub_rn(s, p);
     const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(s, b)), __fadd_rn(t, b));
-    const float lo = __fsub_rn(__fsub_rn(e, te), __fmul_rn(clo, q));
+    const float lo = __fsub_rn(__fsub_rn(e, te), __fmul_rn(c.lo, q));
     const float hi = __fadd_rn(s, lo);
     const bool some = hi > 0.0f;  // (not for NaN)
     return Pair{some ? hi : 0.0f, some ? __fsub_rn(lo, __fsub_rn(hi, s)) : 0.0f};
 }
 
-// The same for two sums at a time.
+// Two sums at a time.
 struct Pairs {
     float2 hi, lo;
     __device__ __forceinline__ static float2 sub(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
@@ -93,49 +123,73 @@ struct Pairs {
 struct Nodes {
     int32_t parent[kMaxNodes], token[kMaxNodes];
     float u[kMaxNodes], p[kMaxNodes], q[kMaxNodes];  // probabilities at the parent's row
+    int32_t stands[kMaxNodes];                       // as its parent's first child to be tried
 };
 
-// What a block's warps sum next: of a node's row, or nothing more.
+// What a block's warps do next.
 struct Command {
-    int32_t node;  // -1: nothing
-    float chi, clo;
-    bool removed;  // whether bits are set
+    enum Kind : int32_t { kEnd, kSum, kSumKept, kFind } kind;
+    int32_t node;
+    Pair c;
+    bool removed;        // whether bits are set
+    bool keeps;          // kSum: whether tokens that have something left are kept
+    int32_t begin, end, stood;  // kFind: the run, and where its token goes
 };
 
-// Sum over the lanes up to this one.
-__device__ __forceinline__ double up_to_lane(double w, int32_t lane)
+__device__ __forceinline__ Pair shuffled_up(const Pair &a, int d)
+{
+    return Pair{__shfl_up_sync(0xFFFFFFFFu, a.hi, d), __shfl_up_sync(0xFFFFFFFFu, a.lo, d)};
+}
+__device__ __forceinline__ Pair from_lane(const Pair &a, int l)
+{
+    return Pair{__shfl_sync(0xFFFFFFFFu, a.hi, l), __shfl_sync(0xFFFFFFFFu, a.lo, l)};
+}
+// The sum of the first kCount (a power of two) lanes' values, in all of those.
+template <int kCount>
+__device__ __forceinline__ Pair over_lanes(Pair sum)
 {
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const double y = __shfl_up_sync(0xFFFFFFFFu, w, d);
-        if (lane >= d) w += y;
-    }
-    return w;
+    for (int d = kCount / 2; d; d /= 2)
+        sum = plus(sum, Pair{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, d), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, d)});
+    return sum;
 }
 
-// The first lane whose sum up to it, from `before` on, exceeds the bar; -1 for
-// none.  some: the last lane with any weight, -1 for none.  before: the sum before
-// that lane, or of all.
-__device__ __forceinline__ int32_t first_over(double w, double bar, int32_t lane, double &before, int32_t &some)
-{
-    const double up_to = up_to_lane(w, lane);
-    const uint32_t any = __ballot_sync(0xFFFFFFFFu, w > 0.0), over = __ballot_sync(0xFFFFFFFFu, w > 0.0 && before + up_to > bar);
-    some = any ? 31 - __clz(any) : -1;
-    const int32_t found = over ? __ffs(over) - 1 : -1;
-    const double at = __shfl_sync(0xFFFFFFFFu, up_to - w, found < 0 ? 0 : found), all = __shfl_sync(0xFFFFFFFFu, up_to, 31);
-    before += found < 0 ? all : at;
-    return found;
-}
+// Looks for the first of some parts for which the sum up to it exceeds the bar, or,
+// where rounding leaves none, for the last with any weight.
+struct Search {
+    Pair bar, before;
+    // Among the first kCount lanes' parts; before becomes the sum before the one found.
+    template <int kCount>
+    __device__ __forceinline__ int32_t pick(const Pair &w, int32_t lane)
+    {
+        Pair up_to = w;
+#pragma unroll
+        for (int d = 1; d < kCount; d *= 2) {
+            const Pair y = shuffled_up(up_to, d);
+            if (lane >= d) up_to = plus(up_to, y);
+        }
+        const bool any_weight = w.hi > 0.0f && lane < kCount;
+        const uint32_t any = __ballot_sync(0xFFFFFFFFu, any_weight), over = __ballot_sync(0xFFFFFFFFu, any_weight && less(bar, plus(before, up_to)));
+        if (!over) bar = Pair{INFINITY, 0.0f};  // and so on from here
+        const int32_t found = over ? __ffs(over) - 1 : any ? 31 - __clz(any) : 0;
+        before = plus(before, from_lane(minus(up_to, w), found));
+        return found;
+    }
+};
 
 template <class T, bool kDraft>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams v)
 {
-    extern __shared__ uint32_t removed[];  // without draft probabilities: a bit to a token of the block's slice
+    // without draft probabilities, a bit to a token of the block's slice; with them, the kept tokens' p and q
+    extern __shared__ uint32_t dynamic[];
+    uint32_t *removed = dynamic;
+    float2 *kept = reinterpret_cast<float2 *>(dynamic) + threadIdx.x / 32 * v.room;
     __shared__ Nodes n;
-    __shared__ double totals[2][kMaxCluster];
+    __shared__ Pair totals[2][kMaxCluster];
     __shared__ Pair sums[kWarps];
-    __shared__ int32_t path[kMaxNodes];
+    __shared__ int32_t counts[kWarps], path[kMaxNodes];
     __shared__ Command command;
+    __shared__ Search search;
     const cg::cluster_group cluster = cg::this_cluster();
     const int32_t rank = static_cast<int32_t>(cluster.block_rank()), blocks = static_cast<int32_t>(cluster.num_blocks());
     const int32_t entry = static_cast<int32_t>(blockIdx.x) / blocks, x = threadIdx.x, warp = x / 32, lane = x % 32;
@@ -145,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 
     if (rank == 0 && x < kMaxNodes) {
         int32_t parent = -2, token = -1;
-        float u = 0.0f, p = 0.0f, q = 0.0f;
+        float u = 0.0f, p = 0.0f, q = 1.0f;
         if (x < v.nodes) {
             parent = x == 0 ? -1 : v.parents ? v.parents[at0 + x] : x - 1, token = v.tokens[at0 + x];
             u = v.uniforms ? v.uniforms[at0 + x] : lowbias32::uniform_of(draw32(v.key, v.first + static_cast<uint32_t>(at0) + x));
@@ -158,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         }
         for (int32_t r = 0; r < blocks; ++r) {
             Nodes &to = *cluster.map_shared_rank(&n, r);
+            to.stands[x] = parent >= 0 && p > 0.0f && less(times(u, q).normal(), Pair{p, 0.0f});
             to.parent[x] = parent, to.token[x] = token, to.u[x] = u, to.p[x] = p, to.q[x] = q;
         }
     }
@@ -166,33 +221,22 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         for (int32_t w = x; w < slice / 32; w += kThreads) removed[w] = 0;
     cluster.sync();
 
-    // What is left of a token of a row.
-    auto left_at = [&](const Command &k, int32_t t, float p, float q) {
-        if (kDraft) return left_of(p, q, k.chi, k.clo);
-        const uint32_t place = t - slice0;
-        return Pair{p > 0.0f && !(k.removed && (removed[place / 32] >> place % 32 & 1u)) ? p : 0.0f, 0.0f};
-    };
-    auto fetch = [&](const Command &k, int32_t t) { return left_at(k, t, to_f32(target[k.node * v.target_node + t]), kDraft ? to_f32(draft[k.node * v.draft_node + t]) : 0.0f); };
-
     // ---- the walk's state, in the first warp of each block
-    constexpr int kWords = kMaxNodes / 32;
+    const int32_t words = (v.nodes + 31) / 32;
     int32_t at = 0, stood = 0;
-    double c = 0.0, mass = 1.0;
-    uint32_t kids[kWords];          // children of `at` that are still to be tried
-    bool known = true;              // whether mass is the present w's
-    bool some_removed = false, ending = false, from_p = false, finished = false;
+    Pair c{0.0f, 0.0f}, mass{1.0f, 0.0f};
+    int32_t tried = 0;               // children of `at` up to this node were tried
+    bool known = true;               // whether mass is the present w's
+    bool has_kept = false;           // whether the present row's tokens are in shared memory
+    bool some_removed = false, ending = false, from_p = false;
     uint32_t parity = 0;
-    Command now{0, 0.0f, 0.0f, false};
-    auto look_for_kids = [&] {
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) kids[k] = __ballot_sync(0xFFFFFFFFu, n.parent[32 * k + lane] == at);
-    };
-    auto next_kid = [&] {
-        int32_t i = -1;
-#pragma unroll
-        for (int k = kWords - 1; k >= 0; --k)
-            if (kids[k]) i = 32 * k + __ffs(kids[k]) - 1;
-        return i;
+    auto next_child = [&] {
+        for (int32_t k = tried / 32; k < words; ++k) {
+            const int32_t j = 32 * k + lane;
+            const uint32_t kids = __ballot_sync(0xFFFFFFFFu, j > tried && j < v.nodes && n.parent[j] == at);
+            if (kids) return 32 * k + __ffs(kids) - 1;
+        }
+        return -1;
     };
     // Bits of the children of `at` that were rejected, in the block's slice.
     auto forget = [&] {
@@ -203,104 +247,152 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         __syncwarp();
         some_removed = false;
     };
-    if (warp == 0) {
-        if (lane == 0) path[0] = 0;
-        look_for_kids();
-    }
+    if (x == 0) path[0] = 0;
+    Command next{Command::kSum, 0, c, false, false, 0, 0, 0};
 
     for (;;) {
         if (warp == 0) {
-            while (!ending) {
-                const int32_t i = next_kid();
+            while (next.kind == Command::kSum && !ending) {
+                const int32_t i = next_child();
                 ending = i < 0;
+                next.keeps = kDraft && !ending && v.run <= 2 * v.room;
                 if (ending || (kDraft && !known)) break;
+                bool stands = n.stands[i] != 0;
                 const int32_t t = n.token[i];
-                const double q = kDraft ? n.q[i] : 1.0;
-                double w = kDraft ? fma(-c, q, static_cast<double>(n.p[i])) : n.p[i];
-                if (!kDraft) {  // a token that was rejected once has nothing left
+                Pair w = kDraft ? left_of(n.p[i], n.q[i], c) : Pair{fmaxf(n.p[i], 0.0f), 0.0f};
+                if (tried > at) {  // not the first
                     bool again = false;
-                    for (int32_t j = lane; j < i; j += 32) again = again || (n.parent[j] == at && n.token[j] == t);
-                    if (__any_sync(0xFFFFFFFFu, again)) w = 0.0;
+                    if (!kDraft)  // a token that was rejected once has nothing left
+                        for (int32_t j = lane; j < i; j += 32) again = again || (n.parent[j] == at && n.token[j] == t);
+                    if (__any_sync(0xFFFFFFFFu, again)) w.hi = 0.0f;
+                    stands = w.hi > 0.0f && less(times(times(n.u[i], n.q[i]).normal(), mass), w);
                 }
-                if (!(w > 0.0)) w = 0.0;
-                if (n.u[i] * mass * q < w) {
+                if (stands) {
                     if (!kDraft && some_removed) forget();
-                    at = i, c = 0.0, mass = 1.0, known = true;
+                    at = tried = i, c = Pair{0.0f, 0.0f}, mass = Pair{1.0f, 0.0f};
+                    known = true, has_kept = false;
                     ++stood;
                     if (lane == 0) path[stood] = i;
-                    look_for_kids();
                     continue;
                 }
-#pragma unroll
-                for (int k = 0; k < kWords; ++k) kids[k] &= i / 32 == k ? ~(1u << i % 32) : 0xFFFFFFFFu;
+                tried = i;
                 if (kDraft) {
-                    c += mass, known = false;
+                    c.add(mass), c = c.normal(), known = false;
                 } else {
-                    mass -= w;
+                    mass.add(-w.hi), mass = mass.normal();
                     const uint32_t place = t - slice0;
                     if (lane == 0 && place < static_cast<uint32_t>(slice)) removed[place / 32] |= 1u << place % 32;
                     some_removed = true;
                     __syncwarp();
                 }
             }
-            const float chi = static_cast<float>(c);
-            now = Command{finished ? -1 : at, chi, static_cast<float>(c - chi), some_removed};
-            if (lane == 0) command = now;
+            if (next.kind == Command::kSum && has_kept) next.kind = Command::kSumKept;
+            next.node = at, next.c = c, next.removed = some_removed;
+            if (lane == 0) command = next;
         }
         __syncthreads();
-        now = command;
-        if (now.node < 0) break;
+        const Command now = command;
+        if (now.kind == Command::kEnd) break;
+        const T *p = target + now.node * v.target_node, *q = draft + now.node * v.draft_node;
+        // What is left of a token.
+        auto left_at = [&](int32_t t, float a, float b) {
+            if (kDraft) return left_of(a, b, now.c);
+            const uint32_t place = t - slice0;
+            return Pair{a > 0.0f && !(now.removed && (removed[place / 32] >> place % 32 & 1u)) ? a : 0.0f, 0.0f};
+        };
+        auto fetch = [&](int32_t t) { return left_at(t, to_f32(p[t]), kDraft ? to_f32(q[t]) : 0.0f); };
+
+        if (now.kind == Command::kFind) {
+            // ---- the last token, in a run that all threads share: some adjacent tokens each
+            const int32_t each = (now.end - now.begin + kThreads - 1) / kThreads;
+            const int32_t from = min(now.begin + x * each, now.end), to = min(from + each, now.end);
+            Pair mine{0.0f, 0.0f};
+#pragma unroll 4
+            for (int32_t t = from; t < to; ++t) mine.add(fetch(t));
+            mine = mine.normal();
+            const Pair sum = over_lanes<32>(mine);
+            if (lane == 0) sums[warp] = sum;
+            __syncthreads();
+            Search s = search;
+            if (s.pick<kWarps>(sums[lane % kWarps], lane) != warp) break;
+            if (s.pick<32>(mine, lane) != lane) break;
+            int32_t token = -1;
+            for (int32_t t = from; t < to; ++t) {
+                const Pair w = fetch(t);
+                if (!(w.hi > 0.0f)) continue;
+                token = t, s.before = plus(s.before, w);
+                if (less(s.bar, s.before)) break;
+            }
+            v.out[at0 + now.stood] = token;
+            break;
+        }
+
         // ---- the sum of what is left of the row; a warp's part stays in `sums`, a block's in `totals`
-        {
+        Pair sum{0.0f, 0.0f};
+        int32_t count = 0;
+        if (now.kind == Command::kSumKept) {
+            const int32_t end = counts[warp];
+            for (int32_t j = lane; j < end; j += 32) sum.add(left_of(kept[j].x, kept[j].y, now.c));
+        } else {
             const int32_t begin = slice0 + warp * v.run + lane, end = min(slice0 + (warp + 1) * v.run, v.vocab);
-            const T *p = target + now.node * v.target_node, *q = draft + now.node * v.draft_node;
             constexpr int kAtOnce = 8;
-            Pair sum{0.0f, 0.0f};
             Pairs two{make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             // after one rejection c is 1, and without any 0: no product
-            const bool plain = kDraft ? now.clo == 0.0f && (now.chi == 0.0f || now.chi == 1.0f) : !now.removed;
-            const bool less = kDraft && now.chi != 0.0f;
+            const bool plain = kDraft ? now.c.lo == 0.0f && (now.c.hi == 0.0f || now.c.hi == 1.0f) : !now.removed;
+            const bool reads_q = kDraft && now.c.hi != 0.0f;
+            auto keep = [&](float a, float b) {
+                const bool more = a > b;
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, more);
+                const int32_t place = count + __popc(who & ((1u << lane) - 1u));
+                if (more && place < v.room) kept[place] = make_float2(a, b);
+                count += __popc(who);
+            };
             int32_t t = begin;
-            for (; t + 32 * (kAtOnce - 1) < end; t += 32 * kAtOnce) {
+            for (; t - lane + 32 * kAtOnce <= end; t += 32 * kAtOnce) {
                 float a[kAtOnce], b[kAtOnce];
 #pragma unroll
-                for (int k = 0; k < kAtOnce; ++k) a[k] = to_f32(p[t + 32 * k]), b[k] = less ? to_f32(q[t + 32 * k]) : 0.0f;
+                for (int k = 0; k < kAtOnce; ++k) a[k] = to_f32(p[t + 32 * k]), b[k] = reads_q ? to_f32(q[t + 32 * k]) : 0.0f;
                 if (plain) {
 #pragma unroll
                     for (int k = 0; k < kAtOnce; k += 2) two.add_left(make_float2(a[k], a[k + 1]), make_float2(b[k], b[k + 1]));
                 } else {
 #pragma unroll
-                    for (int k = 0; k < kAtOnce; ++k) sum.add(left_at(now, t + 32 * k, a[k], b[k]));
+                    for (int k = 0; k < kAtOnce; ++k) sum.add(left_at(t + 32 * k, a[k], b[k]));
+                }
+                if (kDraft && now.keeps) {
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) keep(a[k], b[k]);
                 }
             }
+            for (; t - lane < end; t += 32) {
+                const float a = t < end ? to_f32(p[t]) : 0.0f, b = kDraft && t < end ? to_f32(q[t]) : 0.0f;
+                if (t < end) sum.add(left_at(t, a, b));
+                if (kDraft && now.keeps) keep(a, b);
+            }
             sum.add(Pair{two.hi.x, two.lo.x}), sum.add(Pair{two.hi.y, two.lo.y});
-            for (; t < end; t += 32) sum.add(fetch(now, t));
-#pragma unroll
-            for (int d = 16; d; d /= 2) sum.add(Pair{__shfl_xor_sync(0xFFFFFFFFu, sum.hi, d), __shfl_xor_sync(0xFFFFFFFFu, sum.lo, d)});
-            if (lane == 0) sums[warp] = sum;
+            if (lane == 0) counts[warp] = count;
         }
-        __syncthreads();
+        sum = over_lanes<32>(sum.normal());
+        if (lane == 0) sums[warp] = sum;
+        const bool no_room = __syncthreads_or(count > v.room);
         parity ^= 1u;
         if (warp == 0) {
-            double block = lane < kWarps ? sums[lane].value() : 0.0;
-#pragma unroll
-            for (int d = 16; d; d /= 2) block += __shfl_xor_sync(0xFFFFFFFFu, block, d);
-            if (lane < blocks) cluster.map_shared_rank(&totals[0][0], lane)[parity * kMaxCluster + rank] = block;
+            const Pair block = over_lanes<kWarps>(sums[lane % kWarps]);
+            if (lane < blocks) *cluster.map_shared_rank(&totals[parity][rank], lane) = block;
         }
         cluster.sync();
         if (warp != 0) continue;
-        double part = lane < blocks ? totals[parity][lane] : 0.0;
-        mass = part;
-#pragma unroll
-        for (int d = 16; d; d /= 2) mass += __shfl_xor_sync(0xFFFFFFFFu, mass, d);
-        known = true;
+        const Pair part = lane < blocks ? totals[parity][lane] : Pair{0.0f, 0.0f};
+        mass = from_lane(over_lanes<kMaxCluster>(part), 0), known = true;
+        has_kept = now.kind == Command::kSumKept || (now.keeps && !no_room);
+        next.kind = Command::kSum;
         if (!ending) continue;
-        if (!(mass > 0.0) && !from_p) {  // nothing is left: from p itself
-            from_p = true, c = 0.0;
+        if (!(mass.hi > 0.0f) && !from_p) {  // nothing is left: from p itself
+            from_p = true, c = Pair{0.0f, 0.0f}, has_kept = false;
             if (!kDraft) forget();
             continue;
         }
-        // ---- the last token
+        // ---- the walk's end
         int32_t *out = v.out + at0, *out_path = v.path + at0;
         if (rank == 0) {
             if (lane == 0) v.accepted[entry] = stood;
@@ -309,37 +401,16 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 if (k != stood) out[k] = k < stood ? n.token[path[k + 1]] : -1;
             }
         }
-        if (!(mass > 0.0)) {
+        next.kind = Command::kEnd;
+        if (!(mass.hi > 0.0f)) {
             if (rank == 0 && lane == 0) out[stood] = -1;
-        } else {
-            // the block, its warp, the lane's part of that warp's run, the token: each time the first whose sum exceeds the
-            // bar, or, where rounding leaves none, the last with any weight, and so on from there
-            double bar = n.u[0] * mass, before = 0.0;
-            auto pick = [&](double w) {
-                int32_t some;
-                const int32_t found = first_over(w, bar, lane, before, some);
-                if (found < 0) bar = INFINITY;
-                return found < 0 ? some : found;
-            };
-            if (pick(part) == rank) {
-                const int32_t begin = slice0 + pick(lane < kWarps ? sums[lane].value() : 0.0) * v.run, each = v.run / 32;
-                const int32_t from = begin + lane * each, to = min(from + each, v.vocab);
-                Pair sum{0.0f, 0.0f};
-#pragma unroll 8
-                for (int32_t t = from; t < to; ++t) sum.add(fetch(now, t));
-                const int32_t first = begin + pick(sum.value()) * each, past = min(first + each, v.vocab);
-                int32_t token = -1;
-                for (int32_t t0 = first; t0 < past; t0 += 32) {
-                    const double w = t0 + lane < past ? fetch(now, t0 + lane).value() : 0.0;
-                    int32_t some;
-                    const int32_t found = first_over(w, bar, lane, before, some);
-                    if (found >= 0 || some >= 0) token = t0 + (found < 0 ? some : found);
-                    if (found >= 0) break;
-                }
-                if (lane == 0) out[stood] = token;
-            }
+            continue;
         }
-        finished = true;
+        Search s{times(Pair{n.u[0], 0.0f}, mass), Pair{0.0f, 0.0f}};
+        if (s.pick<kMaxCluster>(part, lane) != rank) continue;
+        const int32_t run = s.pick<kWarps>(sums[lane % kWarps], lane);
+        next.kind = Command::kFind, next.begin = slice0 + run * v.run, next.end = min(next.begin + v.run, v.vocab), next.stood = stood;
+        if (lane == 0) search = s;
     }
 }
 
@@ -467,7 +538,7 @@ cudaError_t launch_verify(const VerifyParams &v, int cluster, cudaStream_t s)
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(static_cast<unsigned>(v.batch) * cluster);
     config.blockDim = dim3(kThreads);
-    config.dynamicSmemBytes = kDraft ? 0 : v.run * kWarps / 8;
+    config.dynamicSmemBytes = kDraft ? v.room * kWarps * sizeof(float2) : v.run * kWarps / 8;
     config.stream = s;
     cudaLaunchAttribute shape;
     shape.id = cudaLaunchAttributeClusterDimension;
@@ -520,11 +591,12 @@ rng_status rng_verify_drafts(const rng_verify_drafts_args *args, void *stream)
     if (rng_status st = check_ranges(what, ranges)) return st;
     VerifyParams v{a.batch, a.nodes, a.vocab, a.target, a.draft, a.target_stride[0], a.target_stride[1], a.draft_stride[0],
                    a.draft_stride[1], a.tokens, a.parents, a.uniforms, seed_key(a.seed), a.first_counter, a.path, a.accepted,
-                   a.out_tokens, 0};
+                   a.out_tokens, 0, 0};
     int cluster = 1;
-    while (cluster < kMaxCluster && a.vocab > cluster * 2048 && int64_t(a.batch) * cluster * 2 <= 4 * int64_t(sm_count())) cluster *= 2;
+    while (cluster < kMaxCluster && a.vocab > cluster * 2048) cluster *= 2;
     const int32_t warps = cluster * kWarps;
     v.run = ((a.vocab + warps - 1) / warps + 31) / 32 * 32;
+    v.room = v.run < kMostKept ? v.run : kMostKept;
     clear_error();
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = a.dtype == RNG_F32   ? launch_verify<float>(v, cluster, s)

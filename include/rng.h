@@ -487,17 +487,19 @@ size_t rng_tree_attention_fwd_workspace(const rng_tree_attention_args *args);
  * token is drawn from what is left: the first v for which the sum of w up to v
  * exceeds u[0] times the whole sum; from p where w has no sum, and -1 where p
  * has none either.  draft == NULL: each draft was chosen, not drawn; child i
- * stands iff u[i] W < w(t), else W = W - w(t), w(t) = 0.  A child whose token is
- * outside 0 .. vocab - 1 does not stand and changes nothing.
+ * stands iff u[i] W < w(t), else W = W - w(t), w(t) = 0.  A token with w(t) = 0
+ * never stands (also where rounded probabilities have a sum above 1 and W ends
+ * below 0); a child whose token is outside 0 .. vocab - 1 does not stand and
+ * changes nothing.
  *
  * u[i] of entry b is uniforms[b * nodes + i], in [0, 1), or, where uniforms is
  * NULL, uniform(seed, first_counter + b * nodes + i).
  *
  * Written, each [batch, nodes] or [batch]: accepted[b], the number of drafts
  * that stand; path[b], node 0 and those drafts' nodes, then -1; out_tokens[b],
- * their tokens and the last one, then -1.  All comparisons are made to 2^-46 of
- * the sums or better (products and sums of f32 pairs or f64), the sums in an
- * order that depends on the sizes alone. */
+ * their tokens and the last one, then -1.  All comparisons are made to 2^-44 of
+ * the sums or better (pairs of f32, or f64), the sums in an order that depends on
+ * the sizes, and on which rows were read before, alone. */
 typedef struct rng_verify_drafts_args {
     rng_dtype dtype; /* of target and draft: RNG_F32, RNG_F16 or RNG_BF16 */
     int32_t batch, nodes, vocab;

@@ -62,7 +62,7 @@ def verify(target, draft, tokens, parents, u):
             bar = Fraction(u[i]) * mass
             if like is not None:
                 bar *= like[at][t]
-            if bar < w[t]:
+            if 0 < w[t] and bar < w[t]:
                 stands = i
                 break
             if like is None:

@@ -10,7 +10,7 @@ ut |o|, plus for f16 P's smallest step 2^-25 times sum|v|.  Where P enters as tw
 terms, its part is ut^2, not ut.
 
 Verification gives whole numbers, which have to be those of exact rational
-arithmetic: the kernel's sums hold 2^-46, and no comparison of these inputs is
+arithmetic: the kernel's sums hold 2^-44, and no comparison of these inputs is
 nearer to equality than that unless it is exactly equal.
 """
 import ctypes as C
