@@ -615,37 +615,59 @@ for _form, _args in (("@7i3P9qP3q3PfP3iPN", TreeAttentionArgs), ("@4i2P4q3P2I3P"
     assert struct.calcsize(_form) == C.sizeof(_args)
 
 
+def _small(t, name: str, n: int, like, like_name: str, dtype, index: int) -> int:
+    """_flat's pointer, 0 for None; index: like's device."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.get_device() != index or t.numel() != n or not t.is_contiguous():
+        return _flat(t, name, n, like, like_name, dtype) or 0
+    return t.data_ptr()
+
+
+def _like(t, name: str, shape, dtype, index: int, like) -> tuple:
+    """_heads, of a tensor whose shape, dtype and device are expected."""
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+        return _heads(t, name, shape, like)
+    b, l, h, d = t.stride()
+    if d != 1:
+        return _heads(t, name, shape, like)
+    return t.data_ptr(), b, l, h
+
+
 def _tree(q, k, v, o, lse, cache_lengths, parents, scale, bias_table, max_distance, bidirectional):
     """The fields of a TreeAttentionArgs before its workspace; without o, of sizes alone."""
     code = _first(q, "q")
-    if q.dim() != 4 or k is None or k.dim() != 4:
-        raise ValueError("q, k and v must be [batch, nodes or length, heads, head_dim]")
     shape = q.shape
+    if len(shape) != 4 or k is None or k.dim() != 4:
+        raise ValueError("q, k and v must be [batch, nodes or length, heads, head_dim]")
     batch, nodes, heads, dim = shape
-    key_shape = (batch, k.shape[1], k.shape[2], dim)
-    buckets = 0
+    _, length, heads_kv, _ = key_shape = k.shape
+    if key_shape[0] != batch or key_shape[3] != dim:
+        key_shape = (batch, length, heads_kv, dim)
+    index, dtype = q.get_device(), q.dtype
+    buckets = pt = 0
     if bias_table is not None:
         if bias_table.dim() != 2 or bias_table.shape[1] != heads:
             raise ValueError(f"bias_table has shape {tuple(bias_table.shape)}, not [num_buckets, heads]")
         buckets = bias_table.shape[0]
         if buckets == 0:  # whose null pointer would say that there is no table
             raise ValueError("bias_table has no buckets")
+        pt = _small(bias_table, "bias_table", buckets * heads, q, "q", dtype, index)
+    if scale is None:
+        scale = dim ** -0.5
+    far = max_distance if buckets else 0
     if o is None:
-        tensors = (0, 0, 0, *(0,) * 9, 0, 0, 0, 0, 0, 0, 0)
-    else:
-        pq, *sq = _heads(q, "q", shape, q)
-        pk, *sk = _heads(k, "k", key_shape, q)
-        pv, *sv = _heads(v, "v", key_shape, q)
-        po, *so = _heads(o, "o", shape, q)
-        if lse is not None and lse.shape != (batch, heads, nodes):
-            raise ValueError(f"lse has shape {tuple(lse.shape)}, not [batch, heads, nodes]")
-        plse = _flat(lse, "lse", batch * heads * nodes, q, "q", _torch.float32)
-        plen = _flat(cache_lengths, "cache_lengths", batch, q, "q", _torch.int32)
-        pp = _flat(parents, "parents", batch * nodes, q, "q", _torch.int32)
-        tensors = (pq, pk, pv, *sq, *sk, *sv, po, *so, plse or 0, plen or 0, pp or 0)
-    pt = _flat(bias_table, "bias_table", buckets * heads, q, "q", q.dtype)
-    return (code, batch, nodes, key_shape[1], heads, key_shape[2], dim, *tensors,
-            dim ** -0.5 if scale is None else scale, pt or 0, buckets, max_distance if buckets else 0,
+        return (code, batch, nodes, length, heads, heads_kv, dim, *(0,) * 19, scale, pt, buckets, far, bool(bidirectional))
+    pq, qb, ql, qh = _like(q, "q", shape, dtype, index, q)
+    pk, kb, kl, kh = _like(k, "k", key_shape, dtype, index, q)
+    pv, vb, vl, vh = _like(v, "v", key_shape, dtype, index, q)
+    po, ob, ol, oh = _like(o, "o", shape, dtype, index, q)
+    if lse is not None and lse.shape != (batch, heads, nodes):
+        raise ValueError(f"lse has shape {tuple(lse.shape)}, not [batch, heads, nodes]")
+    return (code, batch, nodes, length, heads, heads_kv, dim, pq, pk, pv, qb, ql, qh, kb, kl, kh, vb, vl, vh, po, ob, ol,
+            oh, _small(lse, "lse", batch * heads * nodes, q, "q", _torch.float32, index),
+            _small(cache_lengths, "cache_lengths", batch, q, "q", _torch.int32, index),
+            _small(parents, "parents", batch * nodes, q, "q", _torch.int32, index), scale, pt, buckets, far,
             bool(bidirectional))
 
 
@@ -680,16 +702,16 @@ def rng_tree_attention_fwd(q, k, v, o, *, lse=None, cache_lengths=None, parents=
     return o
 
 
-def _probabilities(t, name: str, like) -> tuple:
+def _probabilities(t, name: str, like, shape, dtype, index: int) -> tuple:
     """(pointer, batch stride, node stride) of a [batch, nodes, vocab] tensor; (0, 0, 0) for None."""
     if t is None:
         return 0, 0, 0
-    if t.dtype is not like.dtype or t.device != like.device:
-        _same(t, name, like, "target", like.dtype)
-    if t.shape != like.shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, target {tuple(like.shape)}")
+    if t.dtype is not dtype or t.get_device() != index:
+        _same(t, name, like, "target", dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, target {tuple(shape)}")
     b, n, v = t.stride()
-    if v != 1 and t.shape[2] != 1:
+    if v != 1 and shape[2] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return t.data_ptr(), b, n
 
@@ -702,20 +724,20 @@ def rng_verify_drafts(target, tokens, path, accepted, out_tokens, *, draft=None,
     first_counter); see rng.h.  Writes path [batch, nodes], accepted [batch] and out_tokens [batch, nodes], all int32;
     returns out_tokens."""
     code = _first(target, "target")
-    if target.dim() != 3:
+    shape = target.shape
+    if len(shape) != 3:
         raise ValueError("target must be [batch, nodes, vocab]")
-    batch, nodes, vocab = target.shape
-    i32, n = _torch.int32, batch * nodes
-    pt, tb, tn = _probabilities(target, "target", target)
-    pd, db, dn = _probabilities(draft, "draft", target)
-    ptok = _flat(tokens, "tokens", n, target, "target", i32)
-    ppar = _flat(parents, "parents", n, target, "target", i32)
-    pu = _flat(uniforms, "uniforms", n, target, "target", _torch.float32)
-    ppath, pacc = _flat(path, "path", n, target, "target", i32), _flat(accepted, "accepted", batch, target, "target", i32)
-    pout = _flat(out_tokens, "out_tokens", n, target, "target", i32)
-    args = _pack_verify(code, batch, nodes, vocab, pt, pd, tb, tn, db, dn, ptok or 0, ppar or 0, pu or 0,
-                        seed & 0xFFFFFFFF, first_counter & 0xFFFFFFFF, ppath or 0, pacc or 0, pout or 0)
-    index = target.get_device()
+    batch, nodes, vocab = shape
+    index, dtype, i32, n = target.get_device(), target.dtype, _torch.int32, batch * nodes
+    pt, tb, tn = _probabilities(target, "target", target, shape, dtype, index)
+    pd, db, dn = _probabilities(draft, "draft", target, shape, dtype, index)
+    args = _pack_verify(
+        code, batch, nodes, vocab, pt, pd, tb, tn, db, dn, _small(tokens, "tokens", n, target, "target", i32, index),
+        _small(parents, "parents", n, target, "target", i32, index),
+        _small(uniforms, "uniforms", n, target, "target", _torch.float32, index), seed & 0xFFFFFFFF,
+        first_counter & 0xFFFFFFFF, _small(path, "path", n, target, "target", i32, index),
+        _small(accepted, "accepted", batch, target, "target", i32, index),
+        _small(out_tokens, "out_tokens", n, target, "target", i32, index))
     with _Current(index):
         status = _lib.rng_verify_drafts(args, _handle(stream, index))
     if status:
@@ -724,25 +746,26 @@ def rng_verify_drafts(target, tokens, path, accepted, out_tokens, *, draft=None,
 
 
 def _caches(caches) -> tuple:
-    """(a cache, the pointers of all) of a list of caches, or of one tensor with the caches along its first dimension."""
-    if getattr(caches, "dim", None) is not None:
-        if caches.dim() != 5:
+    """(a cache, its shape and strides, the pointers of all) of a list of caches, or of one tensor with the caches along
+    its first dimension."""
+    if _torch is None:
+        _load_torch()
+    if isinstance(caches, _torch.Tensor):
+        shape, stride = caches.shape, caches.stride()
+        if len(shape) != 5 or shape[0] == 0:
             raise ValueError("caches must be a list of [batch, length, heads, head_dim] tensors, or a tensor of them")
-        _first(caches, "caches")
-        count, base = caches.shape[0], caches.data_ptr()
-        step = caches.stride(0) * caches.element_size()
-        if count == 0:
-            raise ValueError("caches must hold at least one cache")
-        return caches[0], [base + i * step for i in range(count)]
+        base, step = caches.data_ptr(), stride[0] * caches.element_size()
+        return caches, shape[1:], stride[1:], range(base, base + shape[0] * step, step) if step > 0 else [base] * shape[0]
     if len(caches) == 0:
         raise ValueError("caches must hold at least one cache")
     first = caches[0]
-    _first(first, "a cache")
-    shape, stride, device, dtype = first.shape, first.stride(), first.device, first.dtype
+    shape, stride, index, dtype = first.shape, first.stride(), first.get_device(), first.dtype
+    pointers = []
     for t in caches:
-        if t.shape != shape or t.stride() != stride or t.dtype is not dtype or t.device != device:
+        if t.dtype is not dtype or t.get_device() != index or t.shape != shape or t.stride() != stride:
             raise ValueError("all caches must have the same shape, strides, dtype and device")
-    return first, [t.data_ptr() for t in caches]
+        pointers.append(t.data_ptr())
+    return first, shape, stride, pointers
 
 
 def rng_cache_keep(caches, path, accepted, cache_lengths=None, new_lengths=None, *, stream=None):
@@ -750,21 +773,22 @@ def rng_cache_keep(caches, path, accepted, cache_lengths=None, new_lengths=None,
     the same shape and strides (or of one tensor with the caches along its first dimension), from path [batch, nodes]
     and accepted [batch] as rng_verify_drafts writes them; see rng.h.  Writes the caches and, where given, new_lengths
     [batch]; returns new_lengths."""
-    like, pointers = _caches(caches)
-    if like.dim() != 4 or like.element_size() != 2:
+    like, shape, stride, pointers = _caches(caches)
+    _first(like, "a cache")
+    if len(shape) != 4 or like.element_size() != 2:
         raise ValueError("a cache must be [batch, length, heads, head_dim] of a 2-byte type")
-    batch, length, heads, dim = like.shape
+    batch, length, heads, dim = shape
+    if stride[3] != 1:
+        raise ValueError("a cache's last dimension must be contiguous")
     if path.dim() != 2 or path.shape[0] != batch:
         raise ValueError(f"path has shape {tuple(path.shape)}, not [batch, nodes]")
-    nodes, i32 = path.shape[1], _torch.int32
-    _, sb, sl, sh = _heads(like, "a cache", like.shape, like)
-    small = [_flat(t, name, n, like, "a cache", i32) or 0
-             for t, name, n in ((cache_lengths, "cache_lengths", batch), (path, "path", batch * nodes),
-                                (accepted, "accepted", batch), (new_lengths, "new_lengths", batch))]
-    array = struct.pack(f"@{len(pointers)}P", *pointers)
-    hold = C.c_char_p(array)
-    args = _pack_keep(C.cast(hold, _p).value, len(pointers), batch, nodes, length, heads, dim, sb, sl, sh, *small)
-    index = like.get_device()
+    nodes, i32, index, count = path.shape[1], _torch.int32, like.get_device(), len(pointers)
+    array = (_p * count)(*pointers)
+    args = _pack_keep(C.addressof(array), count, batch, nodes, length, heads, dim, *stride[:3],
+                      _small(cache_lengths, "cache_lengths", batch, like, "a cache", i32, index),
+                      _small(path, "path", batch * nodes, like, "a cache", i32, index),
+                      _small(accepted, "accepted", batch, like, "a cache", i32, index),
+                      _small(new_lengths, "new_lengths", batch, like, "a cache", i32, index))
     with _Current(index):
         status = _lib.rng_cache_keep(args, _handle(stream, index))
     if status:

@@ -55,12 +55,18 @@ rng_status relative_buckets(const char *what, int32_t num_buckets, int32_t max_d
                     kMaxBuckets, bidirectional ? " or odd" : "");
     const int32_t count = bidirectional ? num_buckets / 2 : num_buckets;
     const int32_t exact = count / 2, m = count - exact;
+    static thread_local Buckets last{};  // a call asks for them twice, a model's layers for the same ones
+    if (last.total == num_buckets && last.count == count && last.max_distance == max_distance) {
+        *out = last;
+        return RNG_OK;
+    }
     if (max_distance <= exact || max_distance > kMaxDistance)
         return fail(RNG_EINVAL, "%s: max_distance = %d is outside %d .. %d", what, max_distance, exact + 1, kMaxDistance);
     out->total = num_buckets, out->count = count, out->past = bidirectional ? count : 0;
     out->max_distance = max_distance;
     for (int32_t i = 0; i < exact; ++i) out->starts[i] = i + 1;
     for (int32_t t = 1; t < m; ++t) out->starts[exact + t - 1] = boundary(exact, max_distance, m, t);
+    last = *out;
     return RNG_OK;
 }
 
@@ -193,6 +199,12 @@ bool meets(const Nest &x, int k, uintptr_t at, uintptr_t f0, uintptr_t f1)
     return to - first > 1 || meets(x, k + 1, at + first * step, f0, f1) || meets(x, k + 1, at + to * step, f0, f1);
 }
 
+bool meets_flat(const rng_attention_args &a, const Tensor &x, const Flat &f)
+{
+    const uintptr_t f0 = reinterpret_cast<uintptr_t>(f.p), f1 = f0 + f.bytes, x0 = reinterpret_cast<uintptr_t>(x.p);
+    return !empty(a, x) && f1 > x0 && x0 + extent(a, x) > f0 && meets(nest_of(a, x), 0, x0, f0, f1);
+}
+
 // Outputs share no byte with anything else (the tensors among themselves are
 // check_tensors's).
 template <size_t N, size_t M>
@@ -203,9 +215,7 @@ rng_status check_flat(const char *what, const rng_attention_args &a, const Flat 
         const uintptr_t f0 = reinterpret_cast<uintptr_t>(f[i].p), f1 = f0 + f[i].bytes;
         if (f1 < f0) return fail(RNG_EINVAL, "%s: %s runs past the end of the address space", what, f[i].name);
         for (const Tensor &x : t) {
-            const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p);
-            if (!(x.output || f[i].output) || empty(a, x) || f1 <= x0 || x0 + extent(a, x) <= f0) continue;
-            if (meets(nest_of(a, x), 0, x0, f0, f1))
+            if ((x.output || f[i].output) && meets_flat(a, x, f[i]))
                 return fail(RNG_EINVAL, "%s: %s and %s overlap", what, x.name, f[i].name);
         }
         for (size_t j = 0; j < i; ++j) {
@@ -484,9 +494,10 @@ rng_status rng_cache_keep(const rng_cache_keep_args *args, void *stream)
     if (rng_status st = check_flat(what, shape, flat, none)) return st;
     const void *sorted[kMaxCaches];
     for (int32_t i = 0; i < a.count; ++i) {
-        const Tensor t[] = {cache(a.caches[i])};
-        if (rng_status st = check_tensor(what, shape, t[0])) return st;
-        if (rng_status st = check_flat(what, shape, flat, t)) return st;
+        const Tensor t = cache(a.caches[i]);
+        if (rng_status st = check_tensor(what, shape, t)) return st;
+        for (const Flat &f : flat)
+            if (f.p && meets_flat(shape, t, f)) return fail(RNG_EINVAL, "%s: %s and %s overlap", what, t.name, f.name);
         sorted[i] = a.caches[i];
     }
     std::sort(sorted, sorted + a.count);

@@ -44,7 +44,7 @@ struct TreeParams {
     int32_t pack, nodes_per, packs, pairs, units, part_rows;
     Divider by_pack, by_pairs, by_group, by_blocks;
     float *part;  // [blocks][2][dim padded + 2][part_rows]: O, max, sum, rows adjacent
-    int4 *meta;   // [blocks][2]: batch entry, unit, first key tile, state
+    int4 *meta;   // [blocks][2]: batch entry, unit, first key tile, state; NULL where nothing is cut
 };
 
 // A part's state.
@@ -705,13 +705,13 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                 else if (a.lse)
                     a.lse[index] = sum == 0.0f || absent ? -INFINITY : top * to_natural + (logf(sum) - kLift * 0.6931471805599453f);
             }
-            if (threadIdx.x == 0 && (parts == 0 || !whole))
+            if (p.meta && threadIdx.x == 0 && (parts == 0 || !whole))
                 p.meta[blockIdx.x * 2 + slot] = make_int4(w.b, w.unit, w.tile0, kIsThere | (whole ? 0 : kIsPart) | (w.tile0 == 0 ? kStarts : 0) |
                                                                                        (w.tile0 + w.tiles == w.all ? kEnds : 0));
-            if (threadIdx.x == 0 && parts == 0) p.meta[blockIdx.x * 2 + 1] = make_int4(0, 0, 0, 0);
+            if (p.meta && threadIdx.x == 0 && parts == 0) p.meta[blockIdx.x * 2 + 1] = make_int4(0, 0, 0, 0);
             ++parts;
         }
-        if (threadIdx.x == 0 && parts == 0) p.meta[blockIdx.x * 2] = p.meta[blockIdx.x * 2 + 1] = make_int4(0, 0, 0, 0);
+        if (p.meta && threadIdx.x == 0 && parts == 0) p.meta[blockIdx.x * 2] = p.meta[blockIdx.x * 2 + 1] = make_int4(0, 0, 0, 0);
     }
     __syncthreads();
     tmem_fence_after();
@@ -868,7 +868,7 @@ size_t tree_attention_workspace(const TreeAttention &t)
     const Attention &a = t.a;
     if (a.batch == 0 || a.len_q == 0 || a.heads == 0) return 0;
     const TreePlan f = tree_plan(a);
-    return meta_bytes(f) + (f.parts ? sizeof(float) * 2 * f.blocks * f.part_rows * (f.dim + 2) : 0);
+    return f.parts ? meta_bytes(f) + sizeof(float) * 2 * f.blocks * f.part_rows * (f.dim + 2) : 0;
 }
 
 template <class T>
@@ -882,7 +882,7 @@ cudaError_t launch_tree_attention(const TreeAttention &t, cudaStream_t s)
     if (!f.blocks) return cudaErrorInvalidValue;
     p.units = f.packs * f.pairs;
     p.by_pack = Divider(f.pack), p.by_pairs = Divider(f.pairs), p.by_group = Divider(a.group), p.by_blocks = Divider(f.blocks);
-    p.meta = static_cast<int4 *>(a.workspace);
+    p.meta = f.parts ? static_cast<int4 *>(a.workspace) : nullptr;
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + meta_bytes(f));
     constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
     cudaError_t e = make_heads_map(&p.q, bf16, a.q, a.qs, a.batch, a.len_q, a.heads, a.dim, f.pack, f.nodes_per * f.pack);
