@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 import struct
+from array import array as _array
 
 from . import sharding  # noqa: F401  (counter ranges for multi-process fills)
 
@@ -755,7 +756,7 @@ def _caches(caches) -> tuple:
         if len(shape) != 5 or shape[0] == 0:
             raise ValueError("caches must be a list of [batch, length, heads, head_dim] tensors, or a tensor of them")
         base, step = caches.data_ptr(), stride[0] * caches.element_size()
-        return caches, shape[1:], stride[1:], range(base, base + shape[0] * step, step) if step > 0 else [base] * shape[0]
+        return caches, shape[1:], stride[1:], [base + i * step for i in range(shape[0])]
     if len(caches) == 0:
         raise ValueError("caches must hold at least one cache")
     first = caches[0]
@@ -783,8 +784,8 @@ def rng_cache_keep(caches, path, accepted, cache_lengths=None, new_lengths=None,
     if path.dim() != 2 or path.shape[0] != batch:
         raise ValueError(f"path has shape {tuple(path.shape)}, not [batch, nodes]")
     nodes, i32, index, count = path.shape[1], _torch.int32, like.get_device(), len(pointers)
-    array = (_p * count)(*pointers)
-    args = _pack_keep(C.addressof(array), count, batch, nodes, length, heads, dim, *stride[:3],
+    array = _array("Q", pointers)
+    args = _pack_keep(array.buffer_info()[0], count, batch, nodes, length, heads, dim, *stride[:3],
                       _small(cache_lengths, "cache_lengths", batch, like, "a cache", i32, index),
                       _small(path, "path", batch * nodes, like, "a cache", i32, index),
                       _small(accepted, "accepted", batch, like, "a cache", i32, index),

@@ -495,7 +495,10 @@ rng_status rng_cache_keep(const rng_cache_keep_args *args, void *stream)
     const void *sorted[kMaxCaches];
     for (int32_t i = 0; i < a.count; ++i) {
         const Tensor t = cache(a.caches[i]);
-        if (rng_status st = check_tensor(what, shape, t)) return st;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(t.p);
+        // (strides and sizes are the first one's)
+        if (i == 0 || at == 0 || at % 16 || extent(shape, t) > UINTPTR_MAX - at)
+            if (rng_status st = check_tensor(what, shape, t)) return st;
         for (const Flat &f : flat)
             if (f.p && meets_flat(shape, t, f)) return fail(RNG_EINVAL, "%s: %s and %s overlap", what, t.name, f.name);
         sorted[i] = a.caches[i];

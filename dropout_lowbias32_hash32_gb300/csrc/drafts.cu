@@ -10,7 +10,7 @@
 // all warps sum what is left, max(p - c q, 0), and the blocks share their sums.  c
 // only grows, so that what later rejections of the same row can leave is what the
 // first one left: while there are more children to try, those tokens' p and q are
-// kept in shared memory, and later sums read nothing else.  The last token is looked
+// kept in shared memory, as far as there is room, and later sums read little else.  The last token is looked
 // for within the one run where the sum passes u[0] of the whole.
 //
 // The sums decide whole numbers, so they are kept in pairs of f32 (48 bits): f64
@@ -26,8 +26,8 @@ namespace rngk {
 namespace {
 
 constexpr int kMaxNodes = RNG_MAX_TREE_NODES;
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
-constexpr int kMostKept = 832;  // tokens that a warp keeps: 104 KB a block, two blocks an SM
+constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr int kMostKept = 1120;  // tokens that a warp keeps: 70 KB a block, three blocks an SM
 
 struct VerifyParams {
     int32_t batch, nodes, vocab;
@@ -178,7 +178,7 @@ struct Search {
 };
 
 template <class T, bool kDraft>
-__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams v)
+__global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_constant__ VerifyParams v)
 {
     // without draft probabilities, a bit to a token of the block's slice; with them, the kept tokens' p and q
     extern __shared__ uint32_t dynamic[];
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     __shared__ Nodes n;
     __shared__ Pair totals[2][kMaxCluster];
     __shared__ Pair sums[kWarps];
-    __shared__ int32_t counts[kWarps], path[kMaxNodes];
+    __shared__ int32_t counts[kWarps], resumes[kWarps], path[kMaxNodes];  // a warp's kept tokens, and from where on none are
     __shared__ Command command;
     __shared__ Search search;
     const cg::cluster_group cluster = cg::this_cluster();
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             while (next.kind == Command::kSum && !ending) {
                 const int32_t i = next_child();
                 ending = i < 0;
-                next.keeps = kDraft && !ending && v.run <= 2 * v.room;
+                next.keeps = kDraft && !ending;
                 if (ending || (kDraft && !known)) break;
                 bool stands = n.stands[i] != 0;
                 const int32_t t = n.token[i];
@@ -329,25 +329,42 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 
         // ---- the sum of what is left of the row; a warp's part stays in `sums`, a block's in `totals`
         Pair sum{0.0f, 0.0f};
-        int32_t count = 0;
-        if (now.kind == Command::kSumKept) {
-            const int32_t end = counts[warp];
-            for (int32_t j = lane; j < end; j += 32) sum.add(left_of(kept[j].x, kept[j].y, now.c));
-        } else {
-            const int32_t begin = slice0 + warp * v.run + lane, end = min(slice0 + (warp + 1) * v.run, v.vocab);
-            constexpr int kAtOnce = 8;
+        const int32_t end = min(slice0 + (warp + 1) * v.run, v.vocab);
+        int32_t begin = slice0 + warp * v.run;
+        if (kDraft && now.kind == Command::kSumKept) {
+            const int32_t count = counts[warp];
+            constexpr int kAtOnce = 4;  // as many chains of additions
+            Pair four[kAtOnce] = {};
+            for (int32_t j = lane; j < count; j += 32 * kAtOnce) {
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const float2 pq = j + 32 * k < count ? kept[j + 32 * k] : make_float2(0.0f, 0.0f);
+                    four[k].add(left_of(pq.x, pq.y, now.c));
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) sum.add(four[k]);
+            begin = resumes[warp];
+        }
+        {
+            constexpr int kAtOnce = kDraft ? 8 : 16;
             Pairs two{make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             // after one rejection c is 1, and without any 0: no product
             const bool plain = kDraft ? now.c.lo == 0.0f && (now.c.hi == 0.0f || now.c.hi == 1.0f) : !now.removed;
             const bool reads_q = kDraft && now.c.hi != 0.0f;
+            int32_t count = 0, resume = end;
+            bool keeps = kDraft && now.keeps && now.kind == Command::kSum;
+            auto room_for = [&](int32_t t, int32_t tokens) {  // from t - lane on
+                if (count + tokens <= v.room) return;
+                keeps = false, resume = t - lane;
+            };
             auto keep = [&](float a, float b) {
                 const bool more = a > b;
                 const uint32_t who = __ballot_sync(0xFFFFFFFFu, more);
-                const int32_t place = count + __popc(who & ((1u << lane) - 1u));
-                if (more && place < v.room) kept[place] = make_float2(a, b);
+                if (more) kept[count + __popc(who & ((1u << lane) - 1u))] = make_float2(a, b);
                 count += __popc(who);
             };
-            int32_t t = begin;
+            int32_t t = begin + lane;
             for (; t - lane + 32 * kAtOnce <= end; t += 32 * kAtOnce) {
                 float a[kAtOnce], b[kAtOnce];
 #pragma unroll
@@ -359,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k) sum.add(left_at(t + 32 * k, a[k], b[k]));
                 }
-                if (kDraft && now.keeps) {
+                if (keeps) room_for(t, 32 * kAtOnce);
+                if (keeps) {
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k) keep(a[k], b[k]);
                 }
@@ -367,14 +385,15 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             for (; t - lane < end; t += 32) {
                 const float a = t < end ? to_f32(p[t]) : 0.0f, b = kDraft && t < end ? to_f32(q[t]) : 0.0f;
                 if (t < end) sum.add(left_at(t, a, b));
-                if (kDraft && now.keeps) keep(a, b);
+                if (keeps) room_for(t, 32);
+                if (keeps) keep(a, b);
             }
             sum.add(Pair{two.hi.x, two.lo.x}), sum.add(Pair{two.hi.y, two.lo.y});
-            if (lane == 0) counts[warp] = count;
+            if (kDraft && now.kind == Command::kSum && lane == 0) counts[warp] = count, resumes[warp] = resume;
         }
         sum = over_lanes<32>(sum.normal());
         if (lane == 0) sums[warp] = sum;
-        const bool no_room = __syncthreads_or(count > v.room);
+        __syncthreads();
         parity ^= 1u;
         if (warp == 0) {
             const Pair block = over_lanes<kWarps>(sums[lane % kWarps]);
@@ -384,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         if (warp != 0) continue;
         const Pair part = lane < blocks ? totals[parity][lane] : Pair{0.0f, 0.0f};
         mass = from_lane(over_lanes<kMaxCluster>(part), 0), known = true;
-        has_kept = now.kind == Command::kSumKept || (now.keeps && !no_room);
+        has_kept = now.kind == Command::kSumKept || now.keeps;
         next.kind = Command::kSum;
         if (!ending) continue;
         if (!(mass.hi > 0.0f) && !from_p) {  // nothing is left: from p itself
