@@ -29,7 +29,8 @@ constexpr int kRows = 128, kKeys = 128;  // a unit's tile
 constexpr uint32_t kBox = 16384;  // bytes of 128 rows of 64 elements
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxNodes = RNG_MAX_TREE_NODES;
-constexpr int kTableValues = 1024;  // bias values of a pack of heads in shared memory
+constexpr int kTableValues = 512;   // bias values of a pack of heads by bucket in shared memory
+constexpr int kNearValues = 4400;   // and by distance
 constexpr int kLeastPart = 2;       // key tiles of a part at least
 constexpr int kOddBuffers = 8;
 
@@ -62,7 +63,8 @@ struct Shape {
     static constexpr uint32_t kTileBytes = kBoxes * kBox;
     static constexpr uint32_t kRing = 2 * kTileBytes;                    // after two tiles of queries
     static constexpr uint32_t kTable = kRing + kStages * kTileBytes;     // bias values of two pieces
-    static constexpr uint32_t kBuckets = kTable + 2 * kTableValues * 4;  // bucket by distance
+    static constexpr uint32_t kNear = kTable + 2 * kTableValues * 4;     // by distance, of one
+    static constexpr uint32_t kBuckets = kNear + kNearValues * 4;        // bucket by distance
 };
 
 __device__ __forceinline__ int32_t cached_of(const Attention &a, int32_t b)
@@ -70,6 +72,10 @@ __device__ __forceinline__ int32_t cached_of(const Attention &a, int32_t b)
     const int32_t room = a.len_k - a.len_q;
     return a.key_lengths ? min(max(a.key_lengths[b], 0), room) : room;
 }
+// Distances that a table by distance has: half a tile that is not all past the last bucket's start has
+// 64 keys, and nodes up to 127 deep; odd, so that the heads' values of a distance lie in different banks.
+__host__ __device__ __forceinline__ int32_t near_reach(const Buckets &b) { return (b.max_distance + kKeys / 2 + kMaxNodes) | 1; }
+
 __device__ __forceinline__ int32_t tiles_for(const Attention &a, int32_t cached) { return (cached + a.len_q + kKeys - 1) / kKeys; }
 
 // A run of one unit's key tiles.
@@ -172,6 +178,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
     constexpr bool kTwoTerms = kTiles == 1;
     constexpr int kThreads = S::kThreads;
     constexpr int kLead = kTiles == 1 ? 2 : 1;  // tiles whose S there is room for
+    constexpr int kTogether = kBias ? 256 * kTiles : 256;  // threads that begin a piece together
     // f16 holds 2^15: P below 2^8 is lifted, so that long rows' small ones keep their bits
     constexpr float kLift = std::is_same<T, __half>::value ? 7.0f : 0.0f;
     constexpr uint32_t kBars = 3 * S::kStages + 11;  // that one arrival completes
@@ -497,7 +504,9 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
         const float to_base2 = kBias ? kLog2e : a.scale * kLog2e;
         const uint8_t *bucket = smem + S::kBuckets;
         const bool has_bias = kBias && a.table;
-        const int32_t far = has_bias ? a.buckets.max_distance : 0;
+        const int32_t far = has_bias ? a.buckets.max_distance : 0, reach = has_bias ? near_reach(a.buckets) : 0;
+        float *near_table = reinterpret_cast<float *>(smem + S::kNear);
+        int32_t near_of = -1;  // whose biases it holds
         uint32_t turns = 0, additions = 0, parts = 0;  // turns: bit s, the parity of S s's next tile
 #pragma unroll 1
         for (uint32_t piece = 0;; ++piece) {
@@ -505,19 +514,28 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
             tmem_fence_before();
             const uint32_t buffer = piece & 1u;
             const bool fine = barrier_wait(prepared + 8 * buffer, piece / 2 & 1u, &stalled);
-            if (!all_of<256>(1 + unit, fine && !stalled)) break;
+            if (!all_of<kTogether>(kBias ? 1 : 1 + unit, fine && !stalled)) break;
             w = pieces[buffer];
             if (w.tiles == 0) break;
+            const float *values = reinterpret_cast<const float *>(smem + S::kTable) + buffer * kTableValues;
+            if (has_bias && near_of != w.pack && w.cached - ((w.tile0 + w.tiles) * kKeys - 1) < far) {
+                near_of = w.pack;
+                for (int32_t d = threadIdx.x; d < reach; d += kTogether) {
+                    const float *by_head = values + bucket[min(d, far)] * p.pack;
+                    for (int32_t h = 0; h < p.pack; ++h) near_table[h * reach + d] = by_head[h];
+                }
+                sync_threads<kTogether>(1);
+            }
             const int32_t i = w.node0 + (kTiles == 2 ? unit * p.nodes_per : 0) + local_node, head = w.head0 + head_at;
             const bool valid = local_node < p.nodes_per && i < a.len_q;
             const bool any = __any_sync(0xFFFFFFFFu, valid);
             const bool tree = (w.tile0 + w.tiles) * kKeys > w.cached;  // whether the piece has rows of the tree
             const int64_t index = (static_cast<int64_t>(w.b) * a.heads + head) * a.len_q + i;
-            const float *values = reinterpret_cast<const float *>(smem + S::kTable) + buffer * kTableValues + (valid ? head_at : 0);
             const Bits line = (tree || has_bias) && valid ? seen[buffer][i] : 0;
             const bool absent = (tree || has_bias) && line == 0;
             const int32_t my_depth = has_bias && valid ? depth[buffer][i] : 0;
-            const float far_bias = has_bias ? values[bucket[far] * p.pack] : 0.0f;
+            const float far_bias = has_bias ? values[bucket[far] * p.pack + (valid ? head_at : 0)] : 0.0f;
+            const float *near_bias = near_table + (valid ? head_at : 0) * reach;
             float top = -INFINITY, sum = 0.0f;
             const int32_t count = unit == 0 || w.second ? w.tiles : 0;
 #pragma unroll 1
@@ -550,14 +568,24 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                                     s[c][e] = __float_as_uint(f.x), s[c][e + 1] = __float_as_uint(f.y);
                                 }
                         } else {
+                            const float *back = near_bias + my_depth + shift;  // of the first key; the next ones are nearer
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
+                            for (int c = 0; c < 2; ++c) {
+                                if (32 * c + 32 <= shift) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const int32_t node = 32 * c + e - shift;
-                                    const int32_t d = my_depth - (node < 0 ? node : static_cast<int32_t>(depth[buffer][min(node, a.len_q - 1)]));
-                                    s[c][e] = __float_as_uint(fmaf(__uint_as_float(s[c][e]), a.scale, values[bucket[min(max(d, 0), far)] * p.pack]));
+                                    for (int e = 0; e < 32; ++e)
+                                        s[c][e] = __float_as_uint(fmaf(__uint_as_float(s[c][e]), a.scale, back[-(32 * c + e)]));
+                                } else {  // some of the tree: a key's place among them from the lane that has looked it up
+                                    const int32_t key = 32 * c + static_cast<int32_t>(lane) - shift;
+                                    int32_t place = depth[buffer][min(max(key, 0), a.len_q - 1)];
+                                    place = key < 0 ? key : place;
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) {
+                                        const int32_t d = max(my_depth - __shfl_sync(0xFFFFFFFFu, place, e), 0);
+                                        s[c][e] = __float_as_uint(fmaf(__uint_as_float(s[c][e]), a.scale, near_bias[d]));
+                                    }
                                 }
+                            }
                         }
                     }
                     if (masked) {
@@ -805,7 +833,8 @@ TreePlan tree_plan(const Attention &a)
     f.dim = a.dim <= 64 ? 64 : 128;
     // heads side by side: the most of a key head's that divide them evenly, fit a tile, and whose biases fit their place
     f.pack = a.group < kRows ? a.group : kRows;
-    while (a.group % f.pack || (a.table && f.pack * a.buckets.total > kTableValues)) --f.pack;
+    while (a.group % f.pack || (a.table && f.pack > 1 && (f.pack * a.buckets.total > kTableValues || f.pack * near_reach(a.buckets) > kNearValues)))
+        --f.pack;
     f.nodes_per = kRows / f.pack;
     if (f.nodes_per > a.len_q) f.nodes_per = a.len_q;
     const int32_t tiles = (a.len_q + f.nodes_per - 1) / f.nodes_per;
@@ -831,7 +860,8 @@ cudaError_t launch(const TreeParams &p, const TreePlan &f, cudaStream_t s)
     const cudaError_t e = allow_shared(kernel, done);
     if (e != cudaSuccess) return e;
     const size_t bytes = 1024 + S::kTable + (kBias ? S::kBuckets - S::kTable + 1040 : 0);
-    static_assert(1024 + S::kBuckets + 1040 <= 222 * 1024, "beside the static arrays");
+    static_assert(1024 + S::kBuckets + 1040 + 11 * 1024 + 512 <= 227 * 1024 || kTiles == 1, "beside the static arrays");
+    static_assert(1024 + S::kBuckets + 1040 + 8 * 1024 + 512 <= 227 * 1024, "beside the static arrays");
     kernel<<<f.blocks, S::kThreads, bytes, s>>>(p);
     note_launch();
     if (f.parts) {
