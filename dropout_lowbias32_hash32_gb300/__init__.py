@@ -274,14 +274,16 @@ assert struct.calcsize("@7i3P9qP3q2P2if1P3if2I4P12q2PN") == C.sizeof(AttentionAr
 _torch = None  # torch, from the first call on (importing this package does not import it)
 _codes: dict = {}  # torch dtype -> rng_dtype
 _raw_stream = None  # device index -> the current stream's handle
+_device = None  # the current device's index
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _device
     import torch
     _codes.update({torch.float32: RNG_F32, torch.float16: RNG_F16, torch.bfloat16: RNG_BF16})
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
 
 
@@ -471,6 +473,17 @@ def _heads(t, name: str, shape, like) -> tuple:
     if d != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     return t.data_ptr(), b, l, h
+
+
+def _call(name: str, args, stream, index: int) -> None:
+    """A C call of packed arguments on the stream, with the device the current one."""
+    if _device() == index:
+        status = getattr(_lib, name)(args, _handle(stream, index))
+    else:
+        with _Current(index):
+            status = getattr(_lib, name)(args, _handle(stream, index))
+    if status:
+        _check(status, name)
 
 
 _NO_GRADIENT = (0, 0, 0, 0)  # pointer, strides
@@ -679,7 +692,13 @@ def rng_tree_attention_fwd_workspace(q, k=None, *, scale=None, bias_table=None, 
     if isinstance(q, TreeAttentionArgs):
         return _lib.rng_tree_attention_fwd_workspace(C.byref(q))
     args = _pack_tree(*_tree(q, k, None, None, None, None, None, scale, bias_table, max_distance, bidirectional), 0, 0)
-    with _Current(q.get_device()):
+    return _tree_workspace(args, q.get_device())
+
+
+def _tree_workspace(args, index: int) -> int:
+    if _device() == index:
+        return _lib.rng_tree_attention_fwd_workspace(args)
+    with _Current(index):
         return _lib.rng_tree_attention_fwd_workspace(args)
 
 
@@ -690,16 +709,12 @@ def rng_tree_attention_fwd(q, k, v, o, *, lse=None, cache_lengths=None, parents=
     strides, the last dimension contiguous), parents [batch, nodes] int32 (None: a chain); scale None:
     head_dim ** -0.5; see rng.h.  Writes o and, where given, lse [batch, heads, nodes]; returns o."""
     fields = _tree(q, k, v, o, lse, cache_lengths, parents, scale, bias_table, max_distance, bidirectional)
-    index = q.get_device()
-    with _Current(index):
-        args = _pack_tree(*fields, 0, 0)
-        ws, ws_bytes, hold = _scratch(workspace, _lib.rng_tree_attention_fwd_workspace(args), q, stream)
-        if ws_bytes:
-            args = _pack_tree(*fields, ws, ws_bytes)
-        status = _lib.rng_tree_attention_fwd(args, _handle(stream, index))
-    if status:
-        _check(status, "rng_tree_attention_fwd")
-    del hold
+    index, args = q.get_device(), _pack_tree(*fields, 0, 0)
+    need = _tree_workspace(args, index)
+    if need:
+        ws, ws_bytes, hold = _scratch(workspace, need, q, stream)
+        args = _pack_tree(*fields, ws, ws_bytes)
+    _call("rng_tree_attention_fwd", args, stream, index)
     return o
 
 
@@ -739,10 +754,7 @@ def rng_verify_drafts(target, tokens, path, accepted, out_tokens, *, draft=None,
         first_counter & 0xFFFFFFFF, _small(path, "path", n, target, "target", i32, index),
         _small(accepted, "accepted", batch, target, "target", i32, index),
         _small(out_tokens, "out_tokens", n, target, "target", i32, index))
-    with _Current(index):
-        status = _lib.rng_verify_drafts(args, _handle(stream, index))
-    if status:
-        _check(status, "rng_verify_drafts")
+    _call("rng_verify_drafts", args, stream, index)
     return out_tokens
 
 
@@ -790,10 +802,7 @@ def rng_cache_keep(caches, path, accepted, cache_lengths=None, new_lengths=None,
                       _small(path, "path", batch * nodes, like, "a cache", i32, index),
                       _small(accepted, "accepted", batch, like, "a cache", i32, index),
                       _small(new_lengths, "new_lengths", batch, like, "a cache", i32, index))
-    with _Current(index):
-        status = _lib.rng_cache_keep(args, _handle(stream, index))
-    if status:
-        _check(status, "rng_cache_keep")
+    _call("rng_cache_keep", args, stream, index)
     return new_lengths
 
 

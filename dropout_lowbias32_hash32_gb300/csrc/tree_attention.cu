@@ -127,27 +127,21 @@ __device__ __forceinline__ uint32_t snapped(uint32_t x, uint32_t base, uint32_t 
 }
 
 // The lines of a tree's nodes (the node and those before it; none for an absent one) and the number of nodes before
-// each, by a warp: each step doubles how far up a line reaches.
-__device__ __forceinline__ void find_lines(const TreeAttention &t, int32_t b, Bits (&seen)[kMaxNodes], int16_t (&depth)[kMaxNodes],
+// each, by a warp, from the lane's nodes' parents (node lane, lane + 32, ...): each step doubles how far up a line
+// reaches.
+constexpr int kLaneNodes = kMaxNodes / 32;
+__device__ __forceinline__ void find_lines(bool chain, int32_t (&up)[kLaneNodes], Bits (&seen)[kMaxNodes], int16_t (&depth)[kMaxNodes],
                                            int16_t (&jump)[kMaxNodes], uint32_t lane)
 {
-    constexpr int kEach = kMaxNodes / 32;
-    const int32_t nodes = t.a.len_q;
-    const int32_t *parents = t.parents ? t.parents + static_cast<int64_t>(b) * nodes : nullptr;
+    constexpr int kEach = kLaneNodes;
     Bits line[kEach];
-    int32_t up[kEach];
 #pragma unroll
     for (int c = 0; c < kEach; ++c) {
         const int32_t node = 32 * c + static_cast<int32_t>(lane);
-        if (parents) {
-            up[c] = node < nodes ? __ldg(parents + node) : -2;
-            if (up[c] < -1 || up[c] >= node) up[c] = -2;
-            line[c] = up[c] == -2 ? Bits(0) : Bits(1) << node;
-        } else {
-            up[c] = -1, line[c] = ~Bits(0) >> (kMaxNodes - 1 - node);
-        }
+        if (up[c] < -1 || up[c] >= node) up[c] = -2;
+        line[c] = chain ? ~Bits(0) >> (kMaxNodes - 1 - node) : up[c] == -2 ? Bits(0) : Bits(1) << node;
     }
-    bool further = parents != nullptr;
+    bool further = !chain;
 #pragma unroll 1
     while (further) {
         further = false;
@@ -169,6 +163,12 @@ __device__ __forceinline__ void find_lines(const TreeAttention &t, int32_t b, Bi
         seen[32 * c + lane] = line[c];
         depth[32 * c + lane] = static_cast<int16_t>(__popcll(static_cast<uint64_t>(line[c])) + __popcll(static_cast<uint64_t>(line[c] >> 64)) - 1);
     }
+}
+
+__device__ __forceinline__ void swap_two(int32_t (&v)[2])
+{
+    const int32_t t = v[0];
+    v[0] = v[1], v[1] = t;
 }
 
 template <class T, int kDim, int kTiles, bool kBias>
@@ -472,21 +472,41 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                 if (!more) w.tiles = 0;
                 if (lane == 0) pieces[buffer] = w;
                 const bool tree = (w.tile0 + w.tiles) * kKeys > w.cached;  // whether the piece has rows of the tree
-                if (more && (tree || has_bias) && (buffer ? lines_of[1] : lines_of[0]) != w.b) {
-                    if (buffer) lines_of[1] = w.b;
-                    else lines_of[0] = w.b;
-                    find_lines(p.t, w.b, seen[buffer], depth[buffer], jump, lane);
-                }
-                if (more && has_bias && (buffer ? values_of[1] : values_of[0]) != w.pack) {
-                    if (buffer) values_of[1] = w.pack;
-                    else values_of[0] = w.pack;
-                    float *values = reinterpret_cast<float *>(smem + S::kTable) + buffer * kTableValues;
-                    for (int32_t t = lane; t < a.buckets.total * p.pack; t += 32) {
-                        int32_t n, head;
-                        p.by_pack.divide(t, n, head);
-                        values[t] = to_f32(static_cast<const T *>(a.table)[n * a.heads + w.head0 + head]);
+                const bool lines = more && (tree || has_bias) && lines_of[0] != w.b, biases = more && has_bias && values_of[0] != w.pack;
+                // all loads first
+                int32_t up[kLaneNodes];
+                if (lines) {
+                    const int32_t *parents = p.t.parents ? p.t.parents + static_cast<int64_t>(w.b) * a.len_q : nullptr;
+#pragma unroll
+                    for (int k = 0; k < kLaneNodes; ++k) {
+                        const int32_t node = 32 * k + static_cast<int32_t>(lane);
+                        up[k] = parents && node < a.len_q ? __ldg(parents + node) : -2;
                     }
                 }
+                constexpr int kAtOnce = 4;
+                float *values = reinterpret_cast<float *>(smem + S::kTable) + buffer * kTableValues;
+                auto value_at = [&](int32_t t) {
+                    int32_t n, head;
+                    p.by_pack.divide(t, n, head);
+                    return static_cast<const T *>(a.table)[n * a.heads + w.head0 + head];
+                };
+                const int32_t count = biases ? a.buckets.total * p.pack : 0;
+                T first[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+                    if (static_cast<int32_t>(lane) + 32 * k < count) first[k] = value_at(lane + 32 * k);
+                if (lines) {
+                    lines_of[0] = w.b;
+                    find_lines(!p.t.parents, up, seen[buffer], depth[buffer], jump, lane);
+                }
+                if (biases) {
+                    values_of[0] = w.pack;
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k)
+                        if (static_cast<int32_t>(lane) + 32 * k < count) values[lane + 32 * k] = to_f32(first[k]);
+                    for (int32_t t = lane + 32 * kAtOnce; t < count; t += 32) values[t] = to_f32(value_at(t));
+                }
+                swap_two(lines_of), swap_two(values_of);  // [0]: of the buffer that comes next
                 __syncwarp();
                 if (lane == 0) barrier_arrive(prepared + 8 * buffer);
                 if (!more) break;
