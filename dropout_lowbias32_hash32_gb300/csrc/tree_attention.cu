@@ -32,6 +32,7 @@ constexpr int kMaxNodes = RNG_MAX_TREE_NODES;
 constexpr int kTableValues = 512;   // bias values of a pack of heads by bucket in shared memory
 constexpr int kNearValues = 4400;   // and by distance
 constexpr int kLeastPart = 2;       // key tiles of a part at least
+constexpr int kWhole = 6;           // key tiles that are not cut
 constexpr int kOddBuffers = 8;
 
 using Bits = unsigned __int128;
@@ -43,6 +44,7 @@ struct TreeParams {
     // heads side by side in a tile, nodes of a tile, packs of heads, pairs (kTiles = 1: single ones) of tiles of a pack,
     // packs x pairs, rows of a part
     int32_t pack, nodes_per, packs, pairs, units, part_rows;
+    int32_t least;  // key tiles of a part at least
     Divider by_pack, by_pairs, by_group, by_blocks;
     float *part;  // [blocks][2][dim padded + 2][part_rows]: O, max, sum, rows adjacent
     int4 *meta;   // [blocks][2]: batch entry, unit, first key tile, state; NULL where nothing is cut
@@ -118,12 +120,12 @@ struct Cursor {
     }
 };
 
-// Where the list is cut at x: at a unit's own beginning or end rather than less than kLeastPart tiles from it.
+// Where the list is cut at x: at a unit's own beginning or end rather than less than `least` tiles from it.
 template <int kTiles>
-__device__ __forceinline__ uint32_t snapped(uint32_t x, uint32_t base, uint32_t length)
+__device__ __forceinline__ uint32_t snapped(uint32_t x, uint32_t base, uint32_t length, uint32_t least)
 {
     const uint32_t o = (x - base) % length;
-    return o < kTiles + kLeastPart ? x - o : length - o < kLeastPart ? x - o + length : x;
+    return o < kTiles + least ? x - o : length - o < least ? x - o + length : x;
 }
 
 // The lines of a tree's nodes (the node and those before it; none for an absent one) and the number of nodes before
@@ -248,8 +250,8 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
                 __syncthreads();
             }
             const uint32_t begin = before * p.units, past = begin + sum * p.units;
-            if (from >= begin && from < past) shared_cursor = Cursor{snapped<kTiles>(from, begin, sum), 0, begin, b, cached, static_cast<int32_t>(sum)};
-            if (to >= begin && to < past) cut_end = snapped<kTiles>(to, begin, sum);
+            if (from >= begin && from < past) shared_cursor = Cursor{snapped<kTiles>(from, begin, sum, p.least), 0, begin, b, cached, static_cast<int32_t>(sum)};
+            if (to >= begin && to < past) cut_end = snapped<kTiles>(to, begin, sum, p.least);
         }
     }
     tmem_fence_before();
@@ -862,7 +864,8 @@ TreePlan tree_plan(const Attention &a)
     f.packs = a.heads / f.pack, f.pairs = (tiles + f.tiles - 1) / f.tiles;
     f.part_rows = f.tiles == 2 ? 2 * kRows : (f.pack * f.nodes_per + 31) / 32 * 32;
     const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
-    f.parts = key_tiles >= 2 * kLeastPart;
+    // (the parts' join, a second launch, takes as long as some four tiles, and twice that on the host)
+    f.parts = key_tiles > kWhole;
     // the list of key tiles has less than 2^31 entries: more would be 2^38 rows of keys
     const double units = static_cast<double>(a.batch) * f.packs * f.pairs;
     f.blocks = units * (key_tiles + f.tiles) > 0x7FFFFFFF ? 0 : units * key_tiles < sm_count() ? static_cast<int32_t>(units * key_tiles) : static_cast<int32_t>(sm_count());
@@ -931,6 +934,7 @@ cudaError_t launch_tree_attention(const TreeAttention &t, cudaStream_t s)
     p.pack = f.pack, p.nodes_per = f.nodes_per, p.packs = f.packs, p.pairs = f.pairs, p.part_rows = f.part_rows;
     if (!f.blocks) return cudaErrorInvalidValue;
     p.units = f.packs * f.pairs;
+    p.least = f.parts ? kLeastPart : kWhole;
     p.by_pack = Divider(f.pack), p.by_pairs = Divider(f.pairs), p.by_group = Divider(a.group), p.by_blocks = Divider(f.blocks);
     p.meta = f.parts ? static_cast<int4 *>(a.workspace) : nullptr;
     p.part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + meta_bytes(f));
