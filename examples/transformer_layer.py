@@ -1,5 +1,7 @@
 """A small decoder trained with the two transformer-layer operators, then run a
-token at a time from its cache.
+token at a time from its cache, then several at a time: a smaller decoder drafts
+a tree of tokens, the first one's attention takes them all at once, and of those
+that its probabilities let stand the rows stay in the caches.
 
     python examples/transformer_layer.py [steps]
 
@@ -103,6 +105,20 @@ class Layer(torch.nn.Module):
         return self.end("feed", self.down(F.gelu(self.up(x))), x, 0.0, 0)
 
 
+    @torch.no_grad()
+    def tree(self, x, cache, lengths, parents):
+        """A tree of new tokens an entry, x [batch, nodes, width], behind the lengths rows that the cache holds."""
+        q, k, v = self.heads_of(x)
+        rows = lengths.long()[:, None] + torch.arange(x.shape[1], device=x.device)
+        batch = torch.arange(len(lengths), device=x.device)[:, None]
+        cache[0][batch, rows], cache[1][batch, rows] = k, v
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        rng.rng_tree_attention_fwd(q, cache[0], cache[1], o, cache_lengths=lengths, parents=parents, bias_table=self.table,
+                                   max_distance=self.place["max_distance"], bidirectional=self.place["bidirectional"])
+        x = self.end("attention", self.out(o.flatten(2)), x, 0.0, 0)
+        return self.end("feed", self.down(F.gelu(self.up(x))), x, 0.0, 0)
+
+
 class Decoder(torch.nn.Module):
     def __init__(self, tokens=64, width=256, heads=4, heads_kv=2, layers=2, buckets=32, max_distance=128, p=0.1):
         super().__init__()
@@ -126,6 +142,71 @@ class Decoder(torch.nn.Module):
         for layer, cache in zip(self.layers, caches):
             x = layer.step(x, cache, lengths)
         return self.head(x)[:, 0]
+
+
+    @torch.no_grad()
+    def tree(self, tokens, caches, lengths, parents=None):
+        """The logits after every node of a tree of tokens [batch, nodes] (parents None: a chain)."""
+        x = self.embed(tokens)
+        for layer, cache in zip(self.layers, caches):
+            x = layer.tree(x, cache, lengths, parents)
+        return self.head(x)
+
+
+def probabilities(logits, greedy):
+    """Of the next token: softmax, or, greedily, all of it on the largest logit."""
+    logits = logits.float()
+    return F.one_hot(logits.argmax(-1), logits.shape[-1]).float() if greedy else logits.softmax(-1)
+
+
+def drawn(p, seed, first):
+    """A token from each row of p, by the library's uniforms from `first` on."""
+    u = torch.empty(p.shape[:-1], device=p.device)
+    rng.rng_fill_f32(seed, first, u)
+    up_to = p.double().cumsum(-1)
+    found = torch.searchsorted(up_to, u.double()[..., None] * up_to[..., -1:], right=True)[..., 0]
+    return found.clamp(max=p.shape[-1] - 1).int()
+
+
+@torch.no_grad()
+def speculate(model, drafter, prompt, rounds, width=3, depth=3, seed=1, greedy=False):
+    """The tokens that follow each prompt [batch, length], as lists, from `rounds` trees of `width` branches of `depth`
+    drafts each; and how many of the drafts stood."""
+    batch, length = prompt.shape
+    nodes = 1 + width * depth
+    # node 0, then level by level: each level's nodes follow the level before, the first level node 0
+    parents = torch.tensor([[-1] + [max(0, i - width) for i in range(1, nodes)]] * batch, dtype=torch.int32, device=prompt.device)
+    capacity = length + rounds * (depth + 1) + nodes
+    both = [(m, m.caches(batch, capacity, m.head.weight)) for m in (model, drafter)]
+    lengths = torch.zeros(batch, dtype=torch.int32, device=prompt.device)
+    if length > 1:
+        for m, caches in both:
+            m.tree(prompt[:, :-1], caches, lengths)
+    lengths += length - 1
+    root, new, stood = prompt[:, -1].int(), [[] for _ in range(batch)], 0
+    for r in range(rounds):
+        tokens = torch.zeros(batch, nodes, dtype=torch.int32, device=prompt.device)
+        tokens[:, 0] = root
+        q = torch.zeros(batch, nodes, model.head.out_features, device=prompt.device)
+        counter = 2 * r * batch * nodes  # the draws of this round: the drafts', then the verification's
+        for level in range(depth + 1):
+            known = 1 + level * width
+            q[:, :known] = probabilities(drafter.tree(tokens[:, :known], both[1][1], lengths, parents[:, :known].contiguous()), False)
+            if level < depth:
+                from_rows = q[:, [max(0, i - width) for i in range(known, known + width)]]
+                tokens[:, known:known + width] = drawn(from_rows, seed, counter + level * batch * width)
+        p = probabilities(model.tree(tokens, both[0][1], lengths, parents), greedy)
+        path, out = torch.empty_like(tokens), torch.empty_like(tokens)
+        accepted, after = torch.empty_like(lengths), torch.empty_like(lengths)
+        rng.rng_verify_drafts(p, tokens, path, accepted, out, draft=q, parents=parents, seed=seed, first_counter=counter + batch * nodes)
+        for _, caches in both:
+            rng.rng_cache_keep([t for pair in caches for t in pair], path, accepted, lengths, after)
+        lengths = after
+        root = out.gather(1, accepted.long()[:, None])[:, 0]
+        for b, (row, n) in enumerate(zip(out.tolist(), accepted.tolist())):
+            new[b] += row[:n + 1]
+            stood += n
+    return new, stood
 
 
 def sequences(batch, length, tokens, generator):
@@ -178,6 +259,12 @@ def main():
     print(f"loss {losses[0]:.3f} -> {sum(losses[-10:]) / len(losses[-10:]):.3f} in {steps} steps (uniform guess {math.log(64):.3f})")
     worst, most = cached_against_whole(model)
     print(f"a token at a time against whole sequences: logits differ by {worst:.3f} at most, of {most:.1f}")
+    drafter = Decoder(layers=1).cuda().bfloat16()
+    train(drafter, steps)
+    drafter.eval()
+    prompts = sequences(8, 20, 64, torch.Generator(device="cuda").manual_seed(3))
+    new, stood = speculate(model, drafter, prompts, 20)
+    print(f"{sum(map(len, new))} tokens for {len(new)} prompts in 20 rounds: {stood / 160:.2f} drafts a round stood")
 
 
 if __name__ == "__main__":
