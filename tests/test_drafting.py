@@ -50,7 +50,7 @@ def test_greedy_drafting_gives_what_the_model_alone_would(example, models):  # n
     new, stood = example.speculate(model, drafter, prompts, 6, greedy=True)
     assert stood > 0 and sum(map(len, new)) == stood + 4 * 6
     for prompt, tokens in zip(prompts.tolist(), new):
-        logits = model(torch.tensor([prompt + tokens], device="cuda")).float()[0, len(prompt) - 1:-1]
+        logits = model(torch.tensor([prompt + tokens], device="cuda")).detach().float()[0, len(prompt) - 1:-1]
         chosen = logits.gather(1, torch.tensor(tokens, device="cuda")[:, None])[:, 0]
         assert bool((chosen >= logits.amax(1) - 2 * bound(float(logits.abs().max()))).all())
 

@@ -160,6 +160,10 @@ MANY = {
     "long_and_short": case(b=24, n=16, lk=3000, h=8, hk=4, d=64, cached=[2984 if i % 7 == 3 else i for i in range(24)], parents="padded"),
     "wide": case(b=12, n=96, lk=700, h=16, hk=4, d=128, cached=[(211 * i) % 605 for i in range(12)]),
     "bias": case(b=20, n=12, lk=900, h=12, hk=3, d=96, buckets=32, cached=[(331 * i) % 889 for i in range(20)], dtype="float16"),
+    # more entries than a block has threads
+    "a_thousand": case(b=1000, n=2, lk=40, h=2, hk=1, d=16, cached=[(7 * i) % 39 for i in range(1000)], parents="padded"),
+    "hundreds_wide": case(b=660, n=17, lk=130, h=8, hk=1, d=8, cached=[(7 * i) % 114 for i in range(660)], dtype="float16"),
+    "hundreds_cut": case(b=500, n=3, lk=1500, h=4, hk=2, d=64, cached=[1497 if i % 61 == 7 else i % 50 for i in range(500)], buckets=8),
     "empty": case(b=40, n=6, lk=300, h=6, hk=2, parents="broken", cached=[(53 * i) % 295 for i in range(40)]),
 }
 
@@ -288,6 +292,40 @@ def test_tree_attention_twice_in_a_graph_and_on_another_stream(torch, rng, n, h,
             g.replay()
             torch.cuda.synchronize()
             assert torch.equal(og, o) and torch.equal(lg, lse)
+
+
+@pytest.mark.gpu
+def test_tree_attention_refuses_a_workspace(torch, rng):
+    """(How the work is cut, and so the size, goes by the device.)"""
+    r = Run(torch, rng, case(b=4, n=6, h=8, hk=2, d=128, lk=8000))
+    need = rng.rng_tree_attention_fwd_workspace(r.q, r.k)
+    assert 0 < need <= r.k.numel() * 2 and rng.rng_tree_attention_fwd_workspace(r.q[:, :2], r.k[:, :600]) == 0
+    for workspace in (torch.empty(need - 1, dtype=torch.uint8, device="cuda"), torch.empty(need + 16, dtype=torch.uint8, device="cuda")[1:]):
+        with pytest.raises(rng.RngError, match="workspace"):
+            r.forward(workspace=workspace)
+    with pytest.raises(rng.RngError, match="k and workspace overlap"):
+        r.forward(workspace=r.k.view(-1))
+    o, lse = r.forward(workspace=torch.full((need + 1000,), 255, dtype=torch.uint8, device="cuda"))
+    r.check(o, lse)
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once(torch, rng):
+    runs = [Run(torch, rng, case(b=3, n=n, h=8, hk=2, d=128, lk=3000, seed=n, buckets=b)) for n, b in ((6, 0), (40, 32))]
+    want = [r.forward() for r in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(10):
+        got.append([])
+        for r, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                got[-1].append(r.forward())
+    torch.cuda.synchronize()
+    for pair in got:
+        for (o, lse), (wo, wlse) in zip(pair, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wlse)
 
 
 @pytest.mark.gpu
