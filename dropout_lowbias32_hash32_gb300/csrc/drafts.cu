@@ -178,7 +178,7 @@ struct Search {
 };
 
 template <class T, bool kDraft>
-__global__ void __launch_bounds__(kThreads, 3) verify_kernel(const __grid_constant__ VerifyParams v)
+__global__ void __launch_bounds__(kThreads, kDraft ? 3 : 4) verify_kernel(const __grid_constant__ VerifyParams v)
 {
     // without draft probabilities, a bit to a token of the block's slice; with them, the kept tokens' p and q
     extern __shared__ uint32_t dynamic[];
