@@ -16,6 +16,13 @@
 // The sums decide whole numbers, so they are kept in pairs of f32 (48 bits): f64
 // would be slower than HBM here (2 operations a cycle and SM), and f32 sums would
 // pick a neighbouring token about once in a thousand draws of a large vocabulary.
+//
+// What bounds it, measured: latency. One request of 32768 tokens: 8.3 us in a graph (the
+// launch, 1.4 us for what the walk needs, 2 for the walk, 1 for the row's sums, 1 for the
+// blocks' exchange, 2 for the token); each further rejection of the same row 3 us.
+// 128 requests of 131072 tokens, 16 nodes (1.9 sums a request, 8 at most): 71 us for the
+// 117 MB that are read; issue slots 37 %, and the last requests alone for a quarter of
+// the time. Chosen drafts, 64 requests of 24 nodes: 22 us for 34 MB.
 #include <cooperative_groups.h>
 
 #include "attention.h"
@@ -449,7 +456,8 @@ __device__ __forceinline__ int32_t within(int32_t v, int32_t most) { return min(
 
 // A thread moves one vector of every row, kRowsAtOnce rows' loads at a time: row
 // path[k] > k is read before a later step may write it, since path ascends.  The
-// blocks after the caches' write the new lengths.
+// blocks after the caches' write the new lengths.  Bound by latency (the path, then
+// the rows): 64 caches of 32 entries, 8 heads of 128, 3.4 rows an entry: 24 MB in 7 us.
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constant__ KeepParams p)
 {
     const int32_t room = p.len_k - p.nodes;
