@@ -461,6 +461,44 @@ def test_verification_without_any_weight(torch, rng, vocab):
         assert out.tolist() == [[5, -1], [5, -1], [-1, -1], [-1, -1]]
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab", (7, 3001, 20000))
+@pytest.mark.parametrize("kind", ("drawn", "chosen"))
+def test_numbers_that_are_no_probabilities(torch, rng, vocab, kind):
+    """Infinities, NaN and less than 0 among the probabilities, any random numbers and tokens: each walk ends with a path of
+    its tree, the same each time, and other entries are what they are without them."""
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    b, n = 24, 9
+    target, draft = torch.rand(2, b, n, vocab, generator=g, device="cuda") * (2.0 / vocab)
+    tokens = torch.randint(vocab, (b, n), generator=g, device="cuda", dtype=torch.int32)
+    u = torch.rand(b, n, generator=g, device="cuda")
+    r = random.Random(vocab)
+    trees = [bushy(r, n) for _ in range(b)]
+    parents = torch.tensor(trees, dtype=torch.int32, device="cuda")
+    with_draft = lambda: draft if kind == "drawn" else None
+    plain = run_verify(torch, rng, target, with_draft(), tokens, parents, u)
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -1.0, 3e38, 1e-45], device="cuda")
+    for t in (target, draft):
+        for e in range(0, b, 2):
+            t[e, :, r.randrange(vocab)] = odd[e // 2 % 6]
+            t[e, 0, tokens[e, 1 + e % (n - 1)].item()] = odd[(e // 2 + 1) % 6]
+    for e in range(0, b, 2):
+        u[e, r.randrange(n)] = (math.nan, math.inf, -1.0, 1.0)[e // 2 % 4]
+        tokens[e, r.randrange(1, n)] = (-1, vocab, 2 ** 31 - 1, -2 ** 31)[e // 2 % 4]
+    got = run_verify(torch, rng, target, with_draft(), tokens, parents, u)
+    for x, y in zip(got, run_verify(torch, rng, target, with_draft(), tokens, parents, u)):
+        assert torch.equal(x, y)
+    for x, y in zip(got, plain):
+        assert torch.equal(x[1::2], y[1::2])
+    path, accepted, out = (x.tolist() for x in got)
+    for e in range(b):
+        k = accepted[e]
+        assert 0 <= k < n and path[e][0] == 0 and path[e][k + 1:] == [-1] * (n - 1 - k) and out[e][k + 1:] == [-1] * (n - 1 - k)
+        assert all(trees[e][y] == x for x, y in zip(path[e][:k], path[e][1:k + 1]))
+        assert out[e][:k] == [int(tokens[e, i]) for i in path[e][1:k + 1]] and all(0 <= t < vocab for t in out[e][:k])
+        assert -1 <= out[e][k] < vocab
+
+
 def how_often(p, q, drawn):
     total = 0.0
     for triple in itertools.product(range(len(p)), repeat=3):
