@@ -34,7 +34,9 @@ namespace {
 
 constexpr int kMaxNodes = RNG_MAX_TREE_NODES;
 constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxCluster = 8;
-constexpr int kMostKept = 1120;  // tokens that a warp keeps: 70 KB a block, three blocks an SM
+// Tokens that a warp keeps: 70 KB a block, three blocks an SM (four blocks with 800: 128 requests of 131072 tokens, mean
+// of eight seeds, 87 us for 74).  Without draft probabilities four (22 us for 32 with three; six, which spill, 29).
+constexpr int kMostKept = 1120;
 
 struct VerifyParams {
     int32_t batch, nodes, vocab;
@@ -619,6 +621,9 @@ rng_status rng_verify_drafts(const rng_verify_drafts_args *args, void *stream)
     VerifyParams v{a.batch, a.nodes, a.vocab, a.target, a.draft, a.target_stride[0], a.target_stride[1], a.draft_stride[0],
                    a.draft_stride[1], a.tokens, a.parents, a.uniforms, seed_key(a.seed), a.first_counter, a.path, a.accepted,
                    a.out_tokens, 0, 0};
+    // A block to 2048 tokens, so that its warps have more than a few vectors each.  128 drawn requests, clusters of 1, 2, 4,
+    // 8: 2048 tokens 19, 23, 25, 31 us; 8192 27, 22, 25, 40; 131072 177, 110, 73, 69; one request of 131072 83, 47, 27,
+    // 19.
     int cluster = 1;
     while (cluster < kMaxCluster && a.vocab > cluster * 2048) cluster *= 2;
     const int32_t warps = cluster * kWarps;

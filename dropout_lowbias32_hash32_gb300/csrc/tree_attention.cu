@@ -5,8 +5,8 @@
 // so that its keys are read once.  A unit is such a tile with an O in TMEM and two
 // warpgroups: two threads to a row, each with half of a tile's 128 keys; they
 // exchange the row's maximum of a tile through shared memory.
-//   kTiles = 1 (at most 128 rows): one unit with two S, so that a tile's products
-//     run under the next one's exponentials;
+//   kTiles = 1 (at most 128 rows of a key head, or little work): one unit with two S,
+//     so that a tile's products run under the next one's exponentials;
 //   kTiles = 2: two units that share the key tiles, with an S each.
 // A unit's step is S = Q K^T, P = exp(S - max) written back over S in 16 bits, O +=
 // P V.  One warp issues all products, one the TMA loads, one clears value rows that
@@ -876,15 +876,24 @@ TreePlan tree_plan(const Attention &a)
     f.nodes_per = kRows / f.pack;
     if (f.nodes_per > a.len_q) f.nodes_per = a.len_q;
     const int32_t tiles = (a.len_q + f.nodes_per - 1) / f.nodes_per;
-    f.tiles = tiles == 1 ? 1 : 2;
-    f.packs = a.heads / f.pack, f.pairs = (tiles + f.tiles - 1) / f.tiles;
-    f.part_rows = f.tiles == 2 ? 2 * kRows : (f.pack * f.nodes_per + 31) / 32 * 32;
-    const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys;
-    // (the parts' join, a second launch, takes as long as some four tiles, and twice that on the host)
+    const int32_t key_tiles = (a.len_k + kKeys - 1) / kKeys, sms = static_cast<int32_t>(sm_count());
+    // The parts' join, a second launch, costs the host as much as the first (call 11.5 us, 22 with it); on the device 6
+    // key tiles of 8 heads take 17.5 us uncut, 15.5 cut, with 8 entries 19.6 and 21.6; 12 tiles 23.7 and 19.6, 25.7 and
+    // 27.8.
     f.parts = key_tiles > kWhole;
+    // Two tiles of rows to a block where that fills the SMs: they share what is loaded, and one's products run beside
+    // the other's exponentials.  One where each tile can have an SM of its own, or where so few key tiles come to a
+    // block that its first and last steps count for more.  (32 heads over 8 of 128, 64 nodes: uncut, 8 x 700 rows 19.6 us
+    // with two and 15.4 with one, 16 x 700 20.1 and 25.7; cut, 4099 rows 23.5 and 19.5, 8 x 4099 46.4 and 56.5, and about
+    // the same at 3.5 key tiles a block.)
+    f.packs = a.heads / f.pack;
+    const double rows = static_cast<double>(a.batch) * f.packs;
+    const bool few = f.parts ? rows * ((tiles + 1) / 2) * key_tiles <= 3.0 * sms : rows * tiles <= sms;
+    f.tiles = tiles == 1 || few ? 1 : 2;
+    f.pairs = (tiles + f.tiles - 1) / f.tiles;
+    f.part_rows = f.tiles == 2 ? 2 * kRows : (f.pack * f.nodes_per + 31) / 32 * 32;
     // the list of key tiles has less than 2^31 entries: more would be 2^38 rows of keys
     const double units = static_cast<double>(a.batch) * f.packs * f.pairs;
-    const int32_t sms = static_cast<int32_t>(sm_count());
     f.most = units * (key_tiles + f.tiles) > 0x7FFFFFFF ? 0 : units * key_tiles < sms ? static_cast<int32_t>(units * key_tiles) : sms;
     f.blocks = f.most;
     // Entries of one length: the same number of blocks for each, where that leaves no more than a twentieth of the SMs

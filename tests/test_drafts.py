@@ -168,6 +168,42 @@ MANY = {
 }
 
 
+# More than 128 rows of a key head, and work enough that two tiles of rows share their keys: more tiles than SMs, or, past
+# six key tiles, more than three of those for each SM and pair.
+WIDE = {
+    "group_2": case(n=128, lk=260, h=80, hk=40), "group_3": case(n=100, lk=333, h=180, hk=60),
+    "group_8": case(n=64, lk=600, h=160, hk=20, d=128), "group_64": case(n=3, lk=300, h=2560, hk=40),
+    "group_200": case(b=1, n=2, lk=300, h=10000, hk=50, d=16), "dim_120": case(n=60, lk=300, d=120, h=160, hk=40, dtype="float16"),
+    "nothing_cached": case(n=90, lk=90, h=104, hk=26, parents="roots"), "apart": case(n=65, lk=200, h=104, hk=26, parents="apart"),
+    "padded": case(b=20, n=70, lk=300, h=16, hk=4, parents="padded", cached=[(37 * i) % 231 for i in range(20)]),
+    "broken": case(b=20, n=70, lk=300, h=16, hk=4, parents="broken", cached=[(37 * i) % 231 for i in range(20)], buckets=16),
+    "buckets": case(n=90, lk=400, h=104, hk=26, buckets=32, d=128), "buckets_group_20": case(n=30, lk=600, h=280, hk=14, buckets=32, far=128, two_way=False),
+    "sharp": case(n=64, lk=300, h=160, hk=40, spread=20.0, dtype="float16"),
+    "cut": case(b=2, n=64, lk=9000, h=32, hk=8, d=128), "cut_one": case(b=1, n=100, lk=9000, h=16, hk=4, dtype="float16"),
+    "cut_ragged": case(b=12, n=96, lk=1500, h=16, hk=4, d=128, cached=[(211 * i) % 1405 for i in range(12)]),
+    "cut_buckets": case(b=12, n=96, lk=1500, h=16, hk=4, buckets=32, cached=[(211 * i) % 1405 for i in range(12)], dtype="float16", parents="padded"),
+    "cut_chain": case(b=8, n=128, lk=1300, h=16, hk=8, buckets=16, far=40, parents="chain"),
+}
+# and nearly: the most tiles of rows that have an SM each, three key tiles for each SM and pair
+NEAR = {"uncut": case(b=1, n=64, lk=700, h=152, hk=38), "uncut_bias": case(b=3, n=100, lk=300, h=48, hk=12, buckets=32, dtype="float16", d=128),
+        "cut": case(b=2, n=64, lk=1700, h=64, hk=16, d=128), "cut_bias": case(b=3, n=40, lk=1800, h=28, hk=4, buckets=20, cached=[0, 1760, 900]),
+        "cut_long": case(b=1, n=64, lk=9000, h=16, hk=4, d=128, parents="chain")}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", WIDE)
+def test_tree_attention_of_many_rows(torch, rng, name):
+    Run(torch, rng, WIDE[name]).check()
+    assert rng.rng_debug_stalled_waits() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", NEAR)
+def test_tree_attention_of_many_rows_and_little_work(torch, rng, name):
+    Run(torch, rng, NEAR[name]).check()
+    assert rng.rng_debug_stalled_waits() == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", MANY)
 def test_tree_attention_of_many_requests(torch, rng, name):
@@ -198,7 +234,7 @@ def test_tree_attention_as_attention_sees_a_chain(torch, rng):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("buckets", (0, 16))
-@pytest.mark.parametrize("n,h,hk,d", ((20, 4, 2, 64), (100, 8, 2, 128)))
+@pytest.mark.parametrize("n,h,hk,d", ((20, 4, 2, 64), (100, 8, 2, 128), (100, 80, 20, 128)))
 def test_what_a_node_does_not_see_has_no_influence(torch, rng, buckets, n, h, hk, d):
     """Infinities and NaN in one node's query, key or value reach the nodes below it alone."""
     r = Run(torch, rng, case(b=2, n=n, lk=300, h=h, hk=hk, d=d, cached=[123, 40], buckets=buckets))
@@ -268,7 +304,8 @@ def test_tree_attention_layouts(torch, rng):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("n,h,hk,d,lk,b", ((6, 8, 2, 128, 3000, 3), (64, 8, 2, 128, 900, 2), (4, 2, 2, 64, 60, 2)))
+@pytest.mark.parametrize("n,h,hk,d,lk,b", ((6, 8, 2, 128, 3000, 3), (64, 8, 2, 128, 900, 2), (4, 2, 2, 64, 60, 2), (64, 64, 16, 128, 2000, 3),
+                                            (64, 96, 24, 64, 700, 4)))
 def test_tree_attention_twice_in_a_graph_and_on_another_stream(torch, rng, n, h, hk, d, lk, b):
     r = Run(torch, rng, case(b=b, n=n, h=h, hk=hk, d=d, lk=lk))
     o, lse = r.forward()
@@ -310,8 +347,9 @@ def test_tree_attention_refuses_a_workspace(torch, rng):
 
 
 @pytest.mark.gpu
-def test_calls_on_two_streams_at_once(torch, rng):
-    runs = [Run(torch, rng, case(b=3, n=n, h=8, hk=2, d=128, lk=3000, seed=n, buckets=b)) for n, b in ((6, 0), (40, 32))]
+@pytest.mark.parametrize("h,hk", ((8, 2), (64, 16)))
+def test_calls_on_two_streams_at_once(torch, rng, h, hk):
+    runs = [Run(torch, rng, case(b=3, n=n, h=h, hk=hk, d=128, lk=3000, seed=n, buckets=b)) for n, b in ((6, 0), (40, 32))]
     want = [r.forward() for r in runs]
     streams = [torch.cuda.Stream() for _ in runs]
     for s in streams:
@@ -329,9 +367,10 @@ def test_calls_on_two_streams_at_once(torch, rng):
 
 
 @pytest.mark.gpu
-def test_lengths_that_a_graph_sees_change(torch, rng):
+@pytest.mark.parametrize("n,h,hk", ((8, 8, 2), (64, 64, 16)))
+def test_lengths_that_a_graph_sees_change(torch, rng, n, h, hk):
     """The cut of the work goes by the lengths that a replay finds."""
-    r = Run(torch, rng, case(b=4, n=8, lk=2500, h=8, hk=2, d=128, cached=[2000, 0, 17, 900]))
+    r = Run(torch, rng, case(b=4, n=n, lk=2500, h=h, hk=hk, d=128, cached=[2000, 0, 17, 900]))
     graph = torch.cuda.CUDAGraph()
     r.forward()
     with torch.cuda.graph(graph):
@@ -341,7 +380,7 @@ def test_lengths_that_a_graph_sees_change(torch, rng):
         graph.replay()
         want, wlse = r.forward()
         assert torch.equal(o, want) and torch.equal(lse, wlse)
-        r.cached = lengths
+        r.cached = [min(x, 2500 - n) for x in lengths]
         r.k.nan_to_num_(nan=0.5), r.v.nan_to_num_(posinf=0.5)
         graph.replay()
         torch.cuda.synchronize()
