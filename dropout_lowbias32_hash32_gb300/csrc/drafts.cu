@@ -206,9 +206,12 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 3 : 4) verify_kernel(const 
     const T *draft = static_cast<const T *>(v.draft) + entry * v.draft_batch;
     const int64_t at0 = static_cast<int64_t>(entry) * v.nodes;
 
-    if (rank == 0 && x < kMaxNodes) {
-        int32_t parent = -2, token = -1;
-        float u = 0.0f, p = 0.0f, q = 1.0f;
+    // A block's shared memory is written by the cluster's first only when all of its blocks are known to run: they say so
+    // here, and the first waits for it when its loads have been issued.
+    cluster.barrier_arrive();
+    int32_t parent = -2, token = -1;
+    float u = 0.0f, p = 0.0f, q = 1.0f;
+    if (rank == 0) {
         if (x < v.nodes) {
             parent = x == 0 ? -1 : v.parents ? v.parents[at0 + x] : x - 1, token = v.tokens[at0 + x];
             u = v.uniforms ? v.uniforms[at0 + x] : lowbias32::uniform_of(draw32(v.key, v.first + static_cast<uint32_t>(at0) + x));
@@ -219,6 +222,9 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 3 : 4) verify_kernel(const 
                 if (kDraft) q = to_f32(draft[parent * v.draft_node + token]);
             }
         }
+    }
+    cluster.barrier_wait();
+    if (rank == 0 && x < kMaxNodes) {
         for (int32_t r = 0; r < blocks; ++r) {
             Nodes &to = *cluster.map_shared_rank(&n, r);
             to.stands[x] = parent >= 0 && p > 0.0f && less(times(u, q).normal(), Pair{p, 0.0f});

@@ -618,6 +618,36 @@ def test_verification_in_a_graph_on_a_stream_and_of_strided_rows(torch, rng):
         assert all(torch.equal(x, y) for x, y in zip(want, out))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab,nodes", ((2049, 1), (2100, 9), (8000, 3), (20011, 128)))
+def test_verifications_whose_blocks_wait_for_room(torch, rng, vocab, nodes):
+    """More requests than the SMs hold, beside another stream's products and each other: blocks of a cluster begin when
+    there is room for them, and none writes to another before both run."""
+    g = torch.Generator().manual_seed(vocab)
+    b = 400 if nodes < 100 else 30
+    target, draft = drafted(torch, g, b, nodes, vocab, "float32")
+    tokens, u = torch.randint(vocab, (b, nodes), generator=g).int().cuda(), torch.rand(b, nodes, generator=g).cuda()
+    parents = torch.tensor([bushy(random.Random(i), nodes) for i in range(b)], dtype=torch.int32, device="cuda")
+    want = [run_verify(torch, rng, target, d, tokens, parents, u) for d in (draft, None)]
+    if nodes < 100:
+        check_verify(torch, rng, target[:4], draft[:4], tokens[:4].cpu(), parents[:4].cpu(), u[:4].cpu(), tuple(x[:4] for x in want[0]))
+    busy = torch.randn(2048, 2048, device="cuda").bfloat16()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(6):
+        with torch.cuda.stream(streams[2]):
+            for _ in range(4):
+                busy @ busy
+        for s, d in zip(streams, (draft, None)):
+            with torch.cuda.stream(s):
+                got.append(run_verify(torch, rng, target, d, tokens, parents, u))
+    torch.cuda.synchronize()
+    for i, result in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(result, want[i % 2]))
+
+
 # ---- the accepted rows' move -------------------------------------------------------------
 
 
