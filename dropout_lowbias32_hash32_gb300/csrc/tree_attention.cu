@@ -172,6 +172,7 @@ __device__ __forceinline__ void find_lines(bool chain, int32_t (&up)[kLaneNodes]
             further = further || up[c] >= 0;
         }
         further = __any_sync(0xFFFFFFFFu, further);
+        __syncwarp();  // the next stores come after other lanes' loads (a vote orders no memory)
     }
 #pragma unroll
     for (int c = 0; c < kEach; ++c) {

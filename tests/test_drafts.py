@@ -212,6 +212,36 @@ def test_tree_attention_of_many_requests(torch, rng, name):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("buckets", (0, 8))
+def test_each_node_sees_its_line(torch, rng, buckets):
+    """Keys of 0 and a value of its own axis for each node: a node's output says whom it sees.  300 trees of 128 nodes, as
+    deep as there are and as steps that double reach, several a block."""
+    r, n, b = random.Random(8), 128, 300
+    kinds = (lambda i: i - 1, lambda i: i - 2, lambda i: i - 31, lambda i: i // 2, lambda i: i - 1 - r.randrange(3),
+             lambda i: r.randrange(i), lambda i: i - 33 if i > 40 else i - 1, lambda i: r.choice([i - 1, i - 1, i - 1, i - 5, i + 1]))
+    trees = [[-1] + [max(kinds[e % len(kinds)](i), -1 if e % 3 else 0) for i in range(1, n)] for e in range(b)]
+    import draft_reference as ref
+    lines = [ref.lines(t) for t in trees]
+    sees = torch.zeros(b, n, n, dtype=torch.bool)
+    for e in range(b):
+        for i, line in enumerate(lines[e]):
+            sees[e, i, line] = True
+    sees = sees.cuda()
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    q, k = torch.randn(b, n, 1, n, **bf), torch.zeros(b, n, 1, n, **bf)
+    v = torch.eye(n, **bf).expand(b, n, n).contiguous().view(b, n, 1, n)
+    table = torch.zeros(buckets, 1, **bf) if buckets else None
+    o, lse = torch.empty_like(q), torch.empty(b, 1, n, device="cuda")
+    for _ in range(3):
+        rng.rng_tree_attention_fwd(q, k, v, o, lse=lse, parents=torch.tensor(trees, dtype=torch.int32, device="cuda"),
+                                   bias_table=table, max_distance=16)
+        assert torch.equal(o[:, :, 0] != 0, sees)
+        count = sees.sum(2).double()
+        # log of the count of terms 1, each to 2^-22
+        assert bool(((lse[:, 0].double() - count.log()).abs() <= 2.0 ** -20 * (1 + count.log()))[count > 0].all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
 @pytest.mark.parametrize("d,h,hk,n", ((128, 8, 2, 16), (64, 4, 4, 128), (40, 3, 1, 9)))
 def test_few_rows_of_a_key_head_take_two_terms(torch, rng, dtype, d, h, hk, n):
