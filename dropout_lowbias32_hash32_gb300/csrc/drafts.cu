@@ -309,13 +309,15 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 3 : 4) verify_kernel(const 
         const Command now = command;
         if (now.kind == Command::kEnd) break;
         const T *p = target + now.node * v.target_node, *q = draft + now.node * v.draft_node;
+        // Without a rejection at this node c is 0, and the draft's row has no say, whatever it holds.
+        const bool reads_q = kDraft && now.c.hi != 0.0f;
         // What is left of a token.
         auto left_at = [&](int32_t t, float a, float b) {
-            if (kDraft) return left_of(a, b, now.c);
+            if (kDraft) return reads_q ? left_of(a, b, now.c) : Pair{fmaxf(a, 0.0f), 0.0f};
             const uint32_t place = t - slice0;
             return Pair{a > 0.0f && !(now.removed && (removed[place / 32] >> place % 32 & 1u)) ? a : 0.0f, 0.0f};
         };
-        auto fetch = [&](int32_t t) { return left_at(t, to_f32(p[t]), kDraft ? to_f32(q[t]) : 0.0f); };
+        auto fetch = [&](int32_t t) { return left_at(t, to_f32(p[t]), reads_q ? to_f32(q[t]) : 0.0f); };
 
         if (now.kind == Command::kFind) {
             // ---- the last token, in a run that all threads share: some adjacent tokens each
@@ -366,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 3 : 4) verify_kernel(const 
             Pairs two{make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
             // after one rejection c is 1, and without any 0: no product
             const bool plain = kDraft ? now.c.lo == 0.0f && (now.c.hi == 0.0f || now.c.hi == 1.0f) : !now.removed;
-            const bool reads_q = kDraft && now.c.hi != 0.0f;
             int32_t count = 0, resume = end;
             bool keeps = kDraft && now.keeps && now.kind == Command::kSum;
             auto room_for = [&](int32_t t, int32_t tokens) {  // from t - lane on
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, kDraft ? 3 : 4) verify_kernel(const 
                 }
             }
             for (; t - lane < end; t += 32) {
-                const float a = t < end ? to_f32(p[t]) : 0.0f, b = kDraft && t < end ? to_f32(q[t]) : 0.0f;
+                const float a = t < end ? to_f32(p[t]) : 0.0f, b = reads_q && t < end ? to_f32(q[t]) : 0.0f;
                 if (t < end) sum.add(left_at(t, a, b));
                 if (keeps) room_for(t, 32);
                 if (keeps) keep(a, b);

@@ -487,7 +487,9 @@ size_t rng_tree_attention_fwd_workspace(const rng_tree_attention_args *args);
  * The first that stands is the walk's next node.  Where none does, the last
  * token is drawn from what is left: the first v for which the sum of w up to v
  * exceeds u[0] times the whole sum; from p where w has no sum, and -1 where p
- * has none either.  draft == NULL: each draft was chosen, not drawn; child i
+ * has none either.  draft[b, i] has a say only at tokens of node i's children and,
+ * once one of those was rejected, as a whole: the row of a node without children
+ * may hold anything.  draft == NULL: each draft was chosen, not drawn; child i
  * stands iff u[i] W < w(t), else W = W - w(t), w(t) = 0.  A token with w(t) = 0
  * never stands (also where rounded probabilities have a sum above 1 and W ends
  * below 0); a child whose token is outside 0 .. vocab - 1 does not stand and

@@ -568,6 +568,60 @@ def test_numbers_that_are_no_probabilities(torch, rng, vocab, kind):
         assert -1 <= out[e][k] < vocab
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("float32", "bfloat16"))
+@pytest.mark.parametrize("vocab", (7, 33, 256, 700, 2049, 4096, 8200, 32768))
+@pytest.mark.parametrize("odd", (math.nan, math.inf, -math.inf, "all"))
+def test_draft_probabilities_that_nothing_was_drawn_from_have_no_say(torch, rng, vocab, dtype, odd):
+    """Where no child was rejected w is p, whatever the draft row holds: rows of leaves, of nodes whose children have no
+    valid token and of nodes that the walk passes by; and, where the first child stands, all of its row but its token's."""
+    import draft_reference as ref
+    g, r = torch.Generator().manual_seed(vocab), random.Random(vocab)
+    b, n = (12, 6) if vocab < 3000 else (5, 4)
+    # sums that are known but for the rounding of their type: the draft is the target for some entries, so that whole lines stand
+    target, draft = drafted(torch, g, b, n, vocab, dtype)
+    draft[::2] = target[::2]
+    trees = [list(range(-1, n - 1)) if e % 4 == 0 else bushy(r, n) for e in range(b)]
+    rows = torch.tensor(trees).clamp(min=0)
+    tokens = torch.multinomial(draft.float().cpu().gather(1, rows[:, :, None].expand(b, n, vocab)).reshape(b * n, vocab), 1,
+                               generator=g).view(b, n)
+    tokens[1::4, 1:] = torch.tensor([vocab, -1] * n)[:n - 1]  # none of them valid
+    u = torch.rand(b, n, generator=g)
+    given = draft.clone()
+    filling = torch.tensor([math.nan, math.inf, -math.inf, 3.0]) if odd == "all" else torch.tensor([odd])
+    wanted = []
+    for e in range(b):
+        path, out = ref.verify(target[e].double().tolist(), draft[e].double().tolist(), tokens[e].tolist(), trees[e], u[e].tolist())
+        wanted.append((path, out))
+        for i in range(n):
+            tried = [j for j in range(n) if trees[e][j] == i and 0 <= tokens[e, j] < vocab]
+            used = torch.zeros(vocab, dtype=torch.bool)
+            if i in path and tried:
+                if i != path[-1] and path[path.index(i) + 1] == tried[0]:
+                    used[tokens[e, tried[0]]] = True
+                else:
+                    used[:] = True
+            poison = filling[torch.randint(len(filling), (vocab,), generator=g)]
+            given[e, i] = torch.where(used.cuda(), given[e, i], poison.cuda().to(given.dtype))
+    assert not torch.equal(given.nan_to_num(9.0), draft)
+    path, accepted, out = run_verify(torch, rng, target, given, tokens, torch.tensor(trees), u)
+    for e, (want_path, want_out) in enumerate(wanted):
+        assert path[e].tolist() == want_path + [-1] * (n - len(want_path)), e
+        assert accepted[e] == len(want_path) - 1 and out[e].tolist() == want_out + [-1] * (n - len(want_out)), e
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab", (6, 700, 9000))
+def test_an_infinite_draft_leaves_the_target(torch, rng, vocab):
+    """A draft row of infinities rejects its child and leaves nothing: p itself then."""
+    p = torch.zeros(3, 3, vocab, device="cuda")
+    p[0, 0, 5], p[1, 0, vocab - 1], p[2, 0, 0], p[2, 0, 3] = 1.0, 1.0, 0.5, 0.5
+    q = torch.full_like(p, math.inf)
+    u = torch.full((3, 3), 0.75)
+    path, accepted, out = run_verify(torch, rng, p, q, torch.tensor([[0, 5, 5], [0, 1, 2], [0, 3, 3]]), torch.tensor([[-1, 0, 0]] * 3), u)
+    assert accepted.tolist() == [0] * 3 and out.tolist() == [[5, -1, -1], [vocab - 1, -1, -1], [3, -1, -1]]
+
+
 def how_often(p, q, drawn):
     total = 0.0
     for triple in itertools.product(range(len(p)), repeat=3):
