@@ -445,10 +445,9 @@ rng_status rng_relative_bucket(int64_t relative_position, int32_t num_buckets, i
  * whatever their bits; a node's key and value have none on nodes that do not see
  * it, infinities and NaN among them.  s, the statistics and all sums are f32; P is
  * rounded to dtype as the operand of the product with v, as two terms (the value
- * and what its rounding left) at least where a key head's rows, nodes * heads_q /
- * heads_kv, are at most 128.  The key axis is split by the lengths of the whole
- * batch, which changes the order of the f32 sums; the same call gives the same
- * bits every time. */
+ * and what its rounding left).  The key axis is split by the sizes and lengths of
+ * the whole batch, which changes the order of the f32 sums; the same call gives
+ * the same bits every time. */
 typedef struct rng_tree_attention_args {
     rng_dtype dtype;
     int32_t batch, nodes, len_k, heads_q, heads_kv, head_dim;

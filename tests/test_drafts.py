@@ -250,6 +250,24 @@ def test_few_rows_of_a_key_head_take_two_terms(torch, rng, dtype, d, h, hk, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name", ("group_3", "group_8", "dim_120", "padded", "buckets", "sharp", "cut", "cut_one", "cut_ragged", "cut_buckets"))
+def test_many_rows_of_a_key_head_take_two_terms(torch, rng, name):
+    Run(torch, rng, WIDE[name]).check(term=UT[WIDE[name]["dtype"]] ** 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
+@pytest.mark.parametrize("n,lk", ((64, 700), (64, 4163), (128, 400)))
+def test_neighbours_do_not_change_a_requests_rounding(torch, rng, dtype, n, lk):
+    """A request alone, among few and among many, and with a cache that has room for more: two terms throughout."""
+    for b, room in ((1, 0), (8, 0), (24, 0), (1, 3000)):
+        r = Run(torch, rng, case(b=b, n=n, lk=lk + room, h=32, hk=8, d=64, dtype=dtype, cached=[lk - n] * b))
+        o, lse = r.forward()
+        r.c["b"] = 1  # (the others are checked in one of the batches)
+        r.check(o[:1], lse[:1], term=UT[dtype] ** 2)
+
+
+@pytest.mark.gpu
 def test_tree_attention_as_attention_sees_a_chain(torch, rng):
     """A chain is what causal attention gives the last queries, to both operators' roundings."""
     for n, h, hk, d, buckets in ((5, 8, 2, 128, 0), (9, 4, 4, 64, 32)):
