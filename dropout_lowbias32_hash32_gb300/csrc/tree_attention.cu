@@ -5,7 +5,7 @@
 // so that its keys are read once.  A unit is such a tile with an O in TMEM and two
 // warpgroups: two threads to a row, each with half of a tile's 128 keys; they
 // exchange the row's maximum of a tile through shared memory.
-//   kTiles = 1 (at most 128 rows of a key head, or little work): one unit with two S,
+//   kTiles = 1 (at most 128 rows of a key head, or less work): one unit with two S,
 //     so that a tile's products run under the next one's exponentials;
 //   kTiles = 2: two units that share the key tiles, with an S each.
 // A unit's step is S = Q K^T, P = exp(S - max) written back over S in 16 bits, O +=
@@ -38,6 +38,8 @@
 //     heads of 40, a bias: 22 us for four pieces a block; one tree of 8 over 301 rows,
 //     10.4 us in a graph; of 19000 cycles, 2400 are set-up and 4300 the first piece's
 //     lines and biases.
+#include <cmath>
+
 #include "tensor_core.cuh"
 #include "tensor_map.h"
 
@@ -887,15 +889,18 @@ TreePlan tree_plan(const Attention &a)
     // key tiles of 8 heads take 17.5 us uncut, 15.5 cut, with 8 entries 19.6 and 21.6; 12 tiles 23.7 and 19.6, 25.7 and
     // 27.8.
     f.parts = key_tiles > kWhole;
-    // Two tiles of rows to a block where that fills the SMs: they share what is loaded, and one's products run beside
-    // the other's exponentials.  One where each tile can have an SM of its own, or where so few key tiles come to a
-    // block that its first and last steps count for more.  (32 heads over 8 of 128, 64 nodes: uncut, 8 x 700 rows 19.6 us
-    // with two and 15.4 with one, 16 x 700 20.1 and 25.7; cut, 4099 rows 23.5 and 19.5, 8 x 4099 46.4 and 56.5, and about
-    // the same at 3.5 key tiles a block.)
+    // Two tiles of rows to a block share what is loaded, and one's products run beside the other's exponentials, but the
+    // block's first and last steps take longer.  Uncut, a block with two takes 1.83 times one's time, and whole rounds of
+    // the SMs count: 32 heads over 8 of 128, 128 nodes, 700 rows, 16 entries 43.4 us with two and 52.9 with one (2 rounds
+    // and 4), 4 entries 24.0 and 16.6 (1 and 1); 64 nodes, 300 rows, 64 entries 56.8 and 50.8 (4 and 7).  Cut, two from
+    // ten key tiles a block on, where no half of a pair is idle: 64 nodes, 4 x 4099 rows (6.9) 38.0 and 33.6, 8 x 4099
+    // (13.9) 56.2 and 56.5, 32 x 2000 (26.9) 98.5 and 106; 16 heads over one, 40 nodes (five tiles of rows), 32 x 2000 48.4
+    // and 41.1.
     f.packs = a.heads / f.pack;
-    const double rows = static_cast<double>(a.batch) * f.packs;
-    const bool few = f.parts ? rows * ((tiles + 1) / 2) * key_tiles <= 3.0 * sms : rows * tiles <= sms;
-    f.tiles = tiles == 1 || few ? 1 : 2;
+    const double rows = static_cast<double>(a.batch) * f.packs, pairs = (tiles + 1) / 2;
+    const bool two = f.parts ? tiles % 2 == 0 && rows * pairs * key_tiles > 10.0 * sms
+                             : 1.83 * std::ceil(rows * pairs / sms) < std::ceil(rows * tiles / sms);
+    f.tiles = two ? 2 : 1;
     f.pairs = (tiles + f.tiles - 1) / f.tiles;
     f.part_rows = f.tiles == 2 ? 2 * kRows : (f.pack * f.nodes_per + 31) / 32 * 32;
     // the list of key tiles has less than 2^31 entries: more would be 2^38 rows of keys

@@ -204,6 +204,35 @@ def test_tree_attention_of_many_rows_and_little_work(torch, rng, name):
     assert rng.rng_debug_stalled_waits() == 0
 
 
+# Two tiles of rows to a block past six key tiles: an even number of them, and more than ten key tiles a block.
+CUT_PAIRS = {
+    "long": case(b=4, n=64, lk=9000, h=32, hk=8, d=128), "long_f16": case(b=2, n=100, lk=9100, h=64, hk=16, dtype="float16"),
+    "ragged": case(b=24, n=100, lk=1500, h=16, hk=4, d=128, cached=[(211 * i) % 1401 for i in range(24)]),
+    "ragged_padded": case(b=24, n=97, lk=1500, h=16, hk=4, cached=[(307 * i) % 1404 for i in range(24)], parents="padded", dtype="float16"),
+    "ragged_broken": case(b=24, n=128, lk=1500, h=16, hk=4, cached=[(101 * i) % 1373 for i in range(24)], parents="broken", buckets=16),
+    "buckets": case(b=12, n=64, lk=3000, h=32, hk=8, d=96, buckets=32, far=128, cached=[2936 - 200 * i for i in range(12)]),
+    "chain": case(b=24, n=128, lk=1300, h=16, hk=8, buckets=16, far=40, parents="chain"),
+    "sharp": case(b=20, n=64, lk=900, h=32, hk=8, spread=20.0), "short_and_long": case(b=24, n=64, lk=2000, h=32, hk=8, cached=[1936 if i % 5 == 2 else i for i in range(24)]),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", CUT_PAIRS)
+def test_tree_attention_of_many_rows_cut(torch, rng, name):
+    Run(torch, rng, CUT_PAIRS[name]).check(term=UT[CUT_PAIRS[name]["dtype"]] ** 2)
+    assert rng.rng_debug_stalled_waits() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lk", (200, 1280))
+@pytest.mark.parametrize("sms,more", ((0.5, 0), (0.5, 1), (1, 0), (1, 1), (1.5, 0), (1.5, 1), (2, 0)))
+def test_as_much_work_as_the_device_holds(torch, rng, lk, sms, more):
+    """Pairs of tiles of rows for a share of the SMs and one more: on each side of where one or two tiles go to a block."""
+    pairs = int(torch.cuda.get_device_properties(0).multi_processor_count * sms) + more
+    Run(torch, rng, case(b=1, n=64, lk=lk, h=4 * pairs, hk=pairs)).check(term=UT["bfloat16"] ** 2)
+    assert rng.rng_debug_stalled_waits() == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", MANY)
 def test_tree_attention_of_many_requests(torch, rng, name):
