@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
         for (int32_t b = mine; b < a.batch; b += kThreads) cached = cached_of(a, b), sum += tiles_for(a, cached) + kTiles;
         const uint32_t all = block_sum(sum, before) * p.units;
         const uint32_t share = p.by_blocks.quotient(all), left = all - share * p.by_blocks.by;
-        // at every all / blocks, rounded down: where each unit has as many blocks, at their boundaries
+        // at every all / blocks, rounded down
         auto cut = [&](uint32_t block) { return block * share + p.by_blocks.quotient(block * left); };
         const uint32_t from = cut(blockIdx.x), to = cut(blockIdx.x + 1);
         if (threadIdx.x == 0) shared_cursor = Cursor{all, all, all, a.batch - 1, 0, 1}, cut_end = all;
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeP
 
 // How a call is cut.
 struct TreePlan {
-    int32_t dim, tiles, pack, nodes_per, packs, pairs, part_rows, blocks, most;  // most: blocks, whatever the lengths
+    int32_t dim, tiles, pack, nodes_per, packs, pairs, part_rows, blocks;
     bool parts;  // whether an entry's keys may be cut
 };
 
@@ -905,19 +905,11 @@ TreePlan tree_plan(const Attention &a)
     f.part_rows = f.tiles == 2 ? 2 * kRows : (f.pack * f.nodes_per + 31) / 32 * 32;
     // the list of key tiles has less than 2^31 entries: more would be 2^38 rows of keys
     const double units = static_cast<double>(a.batch) * f.packs * f.pairs;
-    f.most = units * (key_tiles + f.tiles) > 0x7FFFFFFF ? 0 : units * key_tiles < sms ? static_cast<int32_t>(units * key_tiles) : sms;
-    f.blocks = f.most;
-    // Entries of one length: the same number of blocks for each, where that leaves no more than a twentieth of the SMs
-    // idle: no block has two parts then (a chain over 32768 rows, 8 units, 152 blocks: 35.4 us, 35.7 without; 8 x 64
-    // nodes, 64 units, 128 blocks: 50.5 us, 47.6 without).
-    if (!a.key_lengths && f.parts && units < f.most) {
-        const int32_t even = static_cast<int32_t>(units) * (f.most / static_cast<int32_t>(units));
-        if (even * 20 >= sms * 19) f.blocks = even;
-    }
+    f.blocks = units * (key_tiles + f.tiles) > 0x7FFFFFFF ? 0 : units * key_tiles < sms ? static_cast<int32_t>(units * key_tiles) : sms;
     return f;
 }
 
-size_t meta_bytes(const TreePlan &f) { return sizeof(int4) * 2 * f.most; }
+size_t meta_bytes(const TreePlan &f) { return sizeof(int4) * 2 * f.blocks; }
 
 template <class T, int kDim, int kTiles, bool kBias>
 cudaError_t launch(const TreeParams &p, const TreePlan &f, cudaStream_t s)
@@ -966,7 +958,7 @@ size_t tree_attention_workspace(const TreeAttention &t)
     const Attention &a = t.a;
     if (a.batch == 0 || a.len_q == 0 || a.heads == 0) return 0;
     const TreePlan f = tree_plan(a);
-    return f.parts ? meta_bytes(f) + sizeof(float) * 2 * f.most * f.part_rows * (f.dim + 2) : 0;
+    return f.parts ? meta_bytes(f) + sizeof(float) * 2 * f.blocks * f.part_rows * (f.dim + 2) : 0;
 }
 
 template <class T>
