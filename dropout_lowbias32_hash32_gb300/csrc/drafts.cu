@@ -628,11 +628,19 @@ rng_status rng_verify_drafts(const rng_verify_drafts_args *args, void *stream)
     VerifyParams v{a.batch, a.nodes, a.vocab, a.target, a.draft, a.target_stride[0], a.target_stride[1], a.draft_stride[0],
                    a.draft_stride[1], a.tokens, a.parents, a.uniforms, seed_key(a.seed), a.first_counter, a.path, a.accepted,
                    a.out_tokens, 0, 0};
-    // A block to 2048 tokens, so that its warps have more than a few vectors each.  128 drawn requests, clusters of 1, 2, 4,
-    // 8: 2048 tokens 19, 23, 25, 31 us; 8192 27, 22, 25, 40; 131072 177, 110, 73, 69; one request of 131072 83, 47, 27,
-    // 19.
+    // More blocks to a request while each keeps 2048 tokens and the SMs hold all of them (about three each); past that only
+    // where a block has so much to read that the next ones' wait is made up for, and more where already some wait.  Nine
+    // nodes, drawn (chosen), f32, clusters of 1, 2, 4, 8, us: 16 x 8192 13, 11, 10, 11 (10, 9, 10, 9); 16 x 131072 108, 58,
+    // 31, 20 (57, 32, 19, 14); 128 x 8192 16, 14, 17, 27 (10, 9, 11, 18); 128 x 32768 32, 24, 22, 28 (19, 14, 13, 19); 128 x
+    // 131072 140, 86, 57, 54 (65, 41, 27, 31); 256 x 8192 17, 19, 25, 47 (11, 11, 20, 31); 256 x 16384 24, 22, 28, 43 (14, 13,
+    // 19, 35); 256 x 65536 91, 57, 54, 69 (41, 28, 31, 41).
+    const int64_t room = 3 * static_cast<int64_t>(sm_count());
     int cluster = 1;
-    while (cluster < kMaxCluster && a.vocab > cluster * 2048) cluster *= 2;
+    for (; cluster < kMaxCluster; cluster *= 2) {
+        const int64_t now = static_cast<int64_t>(a.batch) * cluster;
+        const int32_t least = 2 * now <= room ? 2048 : now <= room ? 12288 : a.draft ? 24576 : 49152;
+        if (a.vocab <= cluster * least) break;
+    }
     const int32_t warps = cluster * kWarps;
     v.run = ((a.vocab + warps - 1) / warps + 31) / 32 * 32;
     v.room = v.run < kMostKept ? v.run : kMostKept;

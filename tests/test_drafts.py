@@ -669,6 +669,32 @@ def test_an_infinite_draft_leaves_the_target(torch, rng, vocab):
     assert accepted.tolist() == [0] * 3 and out.tolist() == [[5, -1, -1], [vocab - 1, -1, -1], [3, -1, -1]]
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ("drawn", "chosen"))
+@pytest.mark.parametrize("vocab", (2048, 2100, 8192, 20000, 33000))
+def test_the_size_of_a_batch_changes_no_token(torch, rng, vocab, kind):
+    """How many blocks share a request goes by the batch too: a request's tokens are what they are alone."""
+    g, n, most = torch.Generator(device="cuda").manual_seed(vocab), 5, 700
+    logits = torch.randn(3, n, vocab, generator=g, device="cuda") * 2
+    target, draft = torch.softmax(logits, 2), torch.softmax(logits + 0.5 * torch.randn(3, n, vocab, generator=g, device="cuda"), 2)
+    parents = torch.tensor([[-1, 0, 0, 1, 0], [-1, 0, 1, 2, 3], [-1, 0, 0, 0, 0]], dtype=torch.int32, device="cuda")
+    rows = draft.gather(1, parents.clamp(min=0).long()[:, :, None].expand_as(draft)).reshape(3 * n, vocab)
+    tokens = torch.multinomial(rows, most // 3 + 1, replacement=True, generator=g).view(3, n, -1).permute(2, 0, 1).reshape(-1, n)[:most].int()
+    u = torch.rand(most, n, generator=g, device="cuda")
+    entry = torch.arange(most, device="cuda") % 3
+    fewer = None
+    for b in (1, 2, 57, 114, 153, 228, 457, most):
+        like = entry[:b]
+        got = run_verify(torch, rng, target[like], draft[like] if kind == "drawn" else None, tokens[:b], parents[like], u[:b])
+        if fewer:
+            assert all(torch.equal(x[:len(y)], y) for x, y in zip(got, fewer)), b
+        fewer = got
+    if vocab < 9000:
+        like = entry[:6]
+        check_verify(torch, rng, target[like], draft[like] if kind == "drawn" else None, tokens[:6].cpu(), parents[like].cpu(), u[:6].cpu(),
+                     tuple(x[:6] for x in fewer))
+
+
 def how_often(p, q, drawn):
     total = 0.0
     for triple in itertools.product(range(len(p)), repeat=3):
