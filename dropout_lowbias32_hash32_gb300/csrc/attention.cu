@@ -121,6 +121,22 @@ rng_status check_tensor(const char *what, const rng_attention_args &a, const Ten
     return RNG_OK;
 }
 
+// The elements from the first to the last that a tensor uses of each period of one of its strides; 0 where its other
+// strides do not keep to the period.
+uint64_t used_of_period(const rng_attention_args &a, const Tensor &t, int i)
+{
+    const int32_t n[3] = {a.batch, t.len, t.heads};
+    const int64_t period = t.stride[i];
+    uint64_t used = a.head_dim;
+    if (period <= 0) return 0;
+    for (int j = 0; j < 3; ++j) {
+        if (j == i || n[j] == 1) continue;
+        if (t.stride[j] < period) used += static_cast<uint64_t>(n[j] - 1) * t.stride[j];
+        else if (t.stride[j] % period) return 0;
+    }
+    return used;
+}
+
 // Whether two tensors may share a byte.  Slices of one packed array (the same
 // strides, one beside the other in each step of some stride) do not.
 bool overlap(const rng_attention_args &a, const Tensor &x, const Tensor &y)
@@ -130,25 +146,43 @@ bool overlap(const rng_attention_args &a, const Tensor &x, const Tensor &y)
     if (x0 + extent(a, x) <= y0 || y0 + extent(a, y) <= x0) return false;
     if (std::memcmp(x.stride, y.stride, 3 * sizeof(int64_t)) != 0) return true;
     for (int i = 0; i < 3; ++i) {
-        const int64_t period = x.stride[i];
-        if (period <= 0) continue;
-        bool periodic = true;
-        uint64_t fx = a.head_dim, fy = a.head_dim;  // elements used of one period
-        for (int j = 0; j < 3; ++j) {
-            if (j == i) continue;
-            const int32_t nx = j == 0 ? a.batch : j == 1 ? x.len : x.heads, ny = j == 0 ? a.batch : j == 1 ? y.len : y.heads;
-            if (x.stride[j] >= period) {
-                periodic = periodic && x.stride[j] % period == 0;
-            } else {
-                fx += static_cast<uint64_t>(nx - 1) * x.stride[j];
-                fy += static_cast<uint64_t>(ny - 1) * y.stride[j];
-            }
-        }
+        const uint64_t fx = used_of_period(a, x, i), fy = used_of_period(a, y, i);
+        if (fx == 0 || fy == 0) continue;
+        const uint64_t period = x.stride[i];
         const bool x_low = x0 <= y0;
         const uint64_t d = (x_low ? y0 - x0 : x0 - y0) / 2 % period;
-        if (periodic && d >= (x_low ? fx : fy) && period - d >= (x_low ? fy : fx)) return false;
+        if (d >= (x_low ? fx : fy) && period - d >= (x_low ? fy : fx)) return false;
     }
     return true;
+}
+
+// Whether any two of `count` tensors at ascending addresses, all of one's sizes and strides, may share a byte.  Those whose
+// ranges touch are compared by their places in a period, all at once, and in pairs only where no stride keeps them apart.
+bool any_overlap(const rng_attention_args &a, Tensor one, const uintptr_t *at, int32_t count, uint64_t *places)
+{
+    if (empty(a, one)) return false;
+    const uint64_t reach = extent(a, one);
+    int32_t end;
+    for (int32_t begin = 0; begin < count; begin = end) {
+        for (end = begin + 1; end < count && at[end] - at[end - 1] < reach; ++end) {}
+        bool apart = end - begin == 1;
+        for (int i = 0; i < 3 && !apart; ++i) {
+            const uint64_t used = used_of_period(a, one, i), period = one.stride[i];
+            if (used == 0 || used > period) continue;
+            for (int32_t j = begin; j < end; ++j) places[j - begin] = (at[j] - at[begin]) / 2 % period;
+            std::sort(places, places + (end - begin));  // (the first is 0)
+            apart = period - places[end - begin - 1] >= used;
+            for (int32_t j = 1; j < end - begin; ++j) apart = apart && places[j] - places[j - 1] >= used;
+        }
+        if (apart) continue;
+        for (int32_t i = begin + 1; i < end; ++i)
+            for (int32_t j = i - 1; j >= begin && at[i] - at[j] < reach; --j) {
+                Tensor other = one;
+                one.p = reinterpret_cast<const void *>(at[i]), other.p = reinterpret_cast<const void *>(at[j]);
+                if (overlap(a, one, other)) return true;
+            }
+    }
+    return false;
 }
 
 // A contiguous array beside the tensors; output: written.
@@ -492,7 +526,8 @@ rng_status rng_cache_keep(const rng_cache_keep_args *args, void *stream)
     auto cache = [&](const void *p) { return Tensor{"a cache", p, a.stride, a.len_k, a.heads, true}; };
     const Tensor none[] = {{"", nullptr, a.stride, 0, 0, false}};
     if (rng_status st = check_flat(what, shape, flat, none)) return st;
-    const void *sorted[kMaxCaches];
+    uintptr_t sorted[kMaxCaches];
+    uint64_t places[kMaxCaches];
     for (int32_t i = 0; i < a.count; ++i) {
         const Tensor t = cache(a.caches[i]);
         const uintptr_t at = reinterpret_cast<uintptr_t>(t.p);
@@ -501,17 +536,10 @@ rng_status rng_cache_keep(const rng_cache_keep_args *args, void *stream)
             if (rng_status st = check_tensor(what, shape, t)) return st;
         for (const Flat &f : flat)
             if (f.p && meets_flat(shape, t, f)) return fail(RNG_EINVAL, "%s: %s and %s overlap", what, t.name, f.name);
-        sorted[i] = a.caches[i];
+        sorted[i] = at;
     }
     std::sort(sorted, sorted + a.count);
-    for (int32_t i = 1; a.heads && i < a.count; ++i) {
-        const uintptr_t at = reinterpret_cast<uintptr_t>(sorted[i]);
-        for (int32_t j = i - 1; j >= 0; --j) {
-            const Tensor x = cache(sorted[j]), y = cache(sorted[i]);
-            if (reinterpret_cast<uintptr_t>(sorted[j]) + extent(shape, x) <= at) break;
-            if (overlap(shape, x, y)) return fail(RNG_EINVAL, "%s: two caches overlap", what);
-        }
-    }
+    if (any_overlap(shape, cache(nullptr), sorted, a.count, places)) return fail(RNG_EINVAL, "%s: two caches overlap", what);
     const CacheKeep c{a.batch, a.nodes, a.len_k, a.heads, a.head_dim, Strides{a.stride[0], a.stride[1], a.stride[2]},
                       a.cache_lengths, a.path, a.accepted, a.new_lengths};
     clear_error();

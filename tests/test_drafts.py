@@ -975,6 +975,84 @@ def test_the_move_refuses_caches(rng, caches, says):
     assert says in rng.rng_last_error(), rng.rng_last_error()
 
 
+def without_a_device(torch):
+    """Calls that nothing refuses end at the launch: only where there is no GPU, whose memory they would follow."""
+    if torch.cuda.is_available():
+        pytest.skip("addresses that no GPU may follow")
+
+
+# of `count` caches in one array, [batch, len, heads] strides and what lies between two of them, in elements
+SLICES = {"entries": lambda n, ln, h, d: ((n * ln * h * d, h * d, d), ln * h * d), "rows": lambda n, ln, h, d: ((ln * n * h * d, n * h * d, d), h * d),
+          "heads": lambda n, ln, h, d: ((ln * h * n * d, h * n * d, n * d), d), "apart": lambda n, ln, h, d: ((ln * h * d, h * d, d), 5 * ln * h * d)}
+
+
+@pytest.mark.parametrize("layout", SLICES)
+@pytest.mark.parametrize("arrays", (1, 3))
+def test_many_caches_in_one_array_are_told_apart_quickly(torch, rng, layout, arrays):
+    """4095 slices of one array, or of three, in no order: their ranges all touch.  (Every pair compared: 0.1 s.)"""
+    import time
+    without_a_device(torch)
+    n, (stride, step) = 4095 // arrays, SLICES[layout](4095 // arrays, 20, 2, 64)
+    given = [(1 << 33) + k * ((1 << 40) + 96) + 2 * step * i for k in range(arrays) for i in range(n)]
+    random.Random(1).shuffle(given)
+    a, times = keep_args(rng, given, batch=3, len_k=20, stride=stride), []
+    for _ in range(5):
+        start = time.perf_counter()
+        assert rng.raw("rng_cache_keep")(C.byref(a), None) not in (rng.RNG_OK, rng.RNG_EINVAL), rng.rng_last_error()
+        times.append(time.perf_counter() - start)
+    assert min(times) < 0.02
+    a = keep_args(rng, given + [given[7] + 2 * (step // 2 // 8 * 8)], batch=3, len_k=20, stride=stride)
+    assert rng.raw("rng_cache_keep")(C.byref(a), None) == rng.RNG_EINVAL  # one more, in the middle of another
+    assert "two caches overlap" in rng.rng_last_error()
+
+
+def test_caches_that_share_an_element_are_refused(torch, rng):
+    """Any strides and addresses, against the sets of their elements; slices of one array are not refused."""
+    without_a_device(torch)
+    r, shared, apart = random.Random(3), 0, 0
+    for _ in range(3000):
+        b, ln, h = r.choice((1, 2, 3)), r.randint(4, 6), r.choice((1, 2, 3))
+        unit = r.choice((8, 8, 16))
+        stride = tuple(8 * r.choice((1, 2, 3, 4, 6, 8, 12, 24, 48, 96, 7, 50)) for _ in range(3))
+        given = [8 * A + 16 * r.randrange(0, 400) for _ in range(r.choice((2, 2, 3, 5)))]
+        elements = [{(p - 8 * A) // 2 + i * stride[0] + j * stride[1] + k * stride[2] + e for i in range(b) for j in range(ln) for k in range(h)
+                     for e in range(unit)} for p in given]
+        status = rng.raw("rng_cache_keep")(C.byref(keep_args(rng, given, batch=b, len_k=ln, heads=h, head_dim=unit, stride=stride)), None)
+        if any(x & y for x, y in itertools.combinations(elements, 2)):
+            assert status == rng.RNG_EINVAL
+            shared += 1
+        elif status != rng.RNG_EINVAL:
+            apart += 1
+    assert min(shared, apart) > 300  # (the draws reach both)
+    for layout, (n, b, ln, h) in itertools.product(SLICES, ((2, 1, 4, 1), (7, 3, 4, 2), (40, 1, 9, 3), (5, 4, 5, 1))):
+        stride, step = SLICES[layout](n, ln, h, 64)
+        given = [8 * A + 2 * step * i for i in range(n)]
+        for change, refused in ((0, False), (16, True)):
+            given[0] += change
+            status = rng.raw("rng_cache_keep")(C.byref(keep_args(rng, given, batch=b, len_k=ln, heads=h, stride=stride)), None)
+            assert (status == rng.RNG_EINVAL) == (refused and layout != "apart"), (layout, n, rng.rng_last_error())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dims", ((1, 0, 2, 3, 4), (1, 2, 0, 3, 4), (1, 2, 3, 0, 4), (0, 1, 2, 3, 4)))
+def test_rows_move_in_slices_of_one_array(torch, rng, dims):
+    """Caches between each other's entries, rows or heads, as a list and as one tensor."""
+    import draft_reference as ref
+    count, b, n, lk, h, d = 70, 3, 6, 40, 2, 64
+    plain = torch.randn(count, b, lk, h, d, device="cuda").bfloat16()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    path, accepted, lengths = torch.tensor([[0, 2, 5, -1, -1, -1], [0, 1, 3, 4, 5, -1], [0] + [-1] * 5], **i32), torch.tensor([2, 4, 0], **i32), torch.tensor([30, 0, 11], **i32)
+    want = plain.clone()
+    for c in range(count):
+        for i, kept in enumerate((2, 4, 0)):
+            want[c, i] = ref.keep(plain[c, i], path[i].tolist(), kept, int(lengths[i]))
+    back = [dims.index(i) for i in range(5)]
+    for form in (list, lambda t: t):
+        now = plain.clone().permute(dims).contiguous().permute(back)
+        rng.rng_cache_keep(form(now), path, accepted, lengths)
+        assert torch.equal(now, want)
+
+
 @pytest.mark.gpu
 def test_the_binding_checks_its_tensors(torch, rng):
     bf, i32 = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.int32, device="cuda")
