@@ -179,10 +179,10 @@ def speculate(model, drafter, prompt, rounds, width=3, depth=3, seed=1, greedy=F
     capacity = length + rounds * (depth + 1) + nodes
     both = [(m, m.caches(batch, capacity, m.head.weight)) for m in (model, drafter)]
     lengths = torch.zeros(batch, dtype=torch.int32, device=prompt.device)
-    if length > 1:
+    for part in prompt[:, :-1].split(rng.RNG_MAX_TREE_NODES, 1) if length > 1 else ():  # a chain has so many nodes at most
         for m, caches in both:
-            m.tree(prompt[:, :-1], caches, lengths)
-    lengths += length - 1
+            m.tree(part, caches, lengths)
+        lengths += part.shape[1]
     root, new, stood = prompt[:, -1].int(), [[] for _ in range(batch)], 0
     for r in range(rounds):
         tokens = torch.zeros(batch, nodes, dtype=torch.int32, device=prompt.device)

@@ -70,3 +70,17 @@ def test_the_same_seed_gives_the_same_tokens(example, models):  # noqa: F811
     prompts = example.sequences(4, 12, 64, torch.Generator(device="cuda").manual_seed(7))
     first, again, other = (example.speculate(*models, prompts, 5, seed=seed) for seed in (3, 3, 4))
     assert first == again and first != other
+
+
+@pytest.mark.parametrize("length", (1, 2, 128, 129, 130, 300))
+def test_prompts_of_any_length(example, models, length):  # noqa: F811
+    """One token, as many as a tree has nodes, and more: the tokens are the largest logits of the whole sequence's."""
+    import torch
+    model, drafter = models
+    prompts = example.sequences(2, length, 64, torch.Generator(device="cuda").manual_seed(length))
+    new, _ = example.speculate(model, drafter, prompts, 3, greedy=True)
+    for prompt, tokens in zip(prompts.tolist(), new):
+        assert len(tokens) >= 3
+        logits = model(torch.tensor([prompt + tokens], device="cuda")).detach().float()[0, len(prompt) - 1:-1]
+        chosen = logits.gather(1, torch.tensor(tokens, device="cuda")[:, None])[:, 0]
+        assert bool((chosen >= logits.amax(1) - 2 * bound(float(logits.abs().max()))).all())
