@@ -792,6 +792,8 @@ __global__ void __launch_bounds__(Shape<kDim, kTiles>::kThreads, 1) tree_attenti
     if (warp == S::kMmaWarp) tmem_free<512>(tmem);
 }
 
+__device__ __forceinline__ float scaled(float x, float by) { return by == 0.0f ? (fabsf(x) < INFINITY ? 0.0f : x) : x * by; }
+
 // Puts the parts of the entries together that blocks have cut: blocks to a block
 // of the above and 32 rows, a thread to a row and 8 columns.  An entry's last part
 // is the first piece of its block; the others lie in the blocks before it, which a
@@ -846,10 +848,16 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ TreeP
             for (int u = 0; u < kAtOnce; ++u) {
                 absent = absent || stats[u][1] < 0.0f;
                 if (stats[u][1] == 0.0f) continue;
-                const float next = fmaxf(top, stats[u][0]), fade = top == -INFINITY ? 0.0f : exp2_approx((top - next) * kLog2e);
+                const float next = fmaxf(top, stats[u][0]), fade = top == -INFINITY ? 1.0f : exp2_approx((top - next) * kLog2e);
                 const float weight = exp2_approx((stats[u][0] - next) * kLog2e);
                 sum = sum * fade + stats[u][1] * weight;
                 top = next;
+                // a factor that f32 no longer holds is more than 0 all the same: what is not finite stays
+                if (fade == 0.0f || weight == 0.0f) {
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) o[k] = scaled(o[k], fade) + scaled(v[u][k], weight);
+                    continue;
+                }
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) o[k] = o[k] * fade + v[u][k] * weight;
             }

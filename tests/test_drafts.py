@@ -339,6 +339,27 @@ def test_what_a_node_does_not_see_has_no_influence(torch, rng, buckets, n, h, hk
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lk", (300, 3000, 20000))
+@pytest.mark.parametrize("value", (math.inf, -math.inf, math.nan))
+def test_an_infinite_value_of_hardly_any_weight(torch, rng, lk, value):
+    """A node's value that is not finite reaches whoever sees it, also where a cached row's score is 400 above all others
+    and the keys are cut: P is more than 0 there, whatever of it f32 holds."""
+    n, h, d = 9, 8, 64
+    r = Run(torch, rng, case(b=2, n=n, lk=lk, h=h, hk=2, d=d))
+    r.q[:] = 1.0
+    r.k.mul_(0.01)
+    r.k[:, 5] = 50.0  # 64 x 50 / 8 = 400
+    clean, _ = r.forward()
+    import draft_reference as ref
+    bad = 3
+    sees = torch.tensor([bad in line for line in ref.lines(r.trees[0])], device="cuda")
+    r.v[0, lk - n + bad] = value
+    o, _ = r.forward()
+    assert torch.equal(o[0][~sees], clean[0][~sees]) and torch.equal(o[1], clean[1])
+    assert bool((o[0][sees] == value).all() if value == value else o[0][sees].isnan().all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ("bfloat16", "float16"))
 def test_tree_attention_with_a_bias_as_a_mask(torch, rng, dtype):
     """-inf hides distances; everywhere, it leaves rows that see nothing; the type's lowest value everywhere leaves
