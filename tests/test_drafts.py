@@ -716,6 +716,46 @@ def test_the_size_of_a_batch_changes_no_token(torch, rng, vocab, kind):
                      tuple(x[:6] for x in fewer))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ("float32", "float16"))
+@pytest.mark.parametrize("vocab", (75000, 131072))
+def test_rows_that_leave_more_than_a_block_keeps(torch, rng, vocab, dtype):
+    """Draft rows below the target's at most tokens, and children that are all tried: later sums read what is kept and,
+    from where there was no more room, the rows."""
+    g = torch.Generator().manual_seed(vocab)
+    n = 5
+    target = torch.softmax(torch.randn(3, n, vocab, generator=g), 2)
+    draft = target * (0.25 + 0.5 * torch.rand(3, n, vocab, generator=g))  # less than the target nearly everywhere,
+    tokens = torch.randint(vocab, (3, n), generator=g)
+    heavy = tokens[:, :, None].expand(3, n, n).transpose(1, 2)  # but not at the drafts
+    draft.scatter_(2, heavy, 0.08)
+    target, draft = (t.to("cuda", getattr(torch, dtype)) for t in (target, draft))
+    u = torch.rand(3, n, generator=g)
+    u[:, 1:] = 0.5 + u[:, 1:] / 2
+    parents = torch.tensor([[-1, 0, 0, 0, 0]] * 3)
+    check_verify(torch, rng, target, draft, tokens, parents, u)
+    assert run_verify(torch, rng, target, draft, tokens, parents, u)[1].tolist() == [0] * 3
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ("drawn", "chosen"))
+def test_the_largest_vocabulary(torch, rng, kind):
+    """2^23 tokens of which 300 have any weight, the first and the last among them: as the 300 alone say."""
+    import draft_reference as ref
+    g, n, vocab, some = torch.Generator().manual_seed(2), 5, 1 << 23, 300
+    at = torch.cat([torch.tensor([0, 1, vocab - 1]), torch.randperm(vocab - 10, generator=g)[:some - 3] + 5]).sort().values
+    target, draft = drafted(torch, g, 1, n, some, "float32", near=1.0)
+    wide = torch.zeros(2, 1, n, vocab, device="cuda")
+    wide[0, :, :, at], wide[1, :, :, at] = target, draft
+    for seed in range(12):
+        parents = bushy(random.Random(seed), n)
+        tokens, u = torch.randint(some, (n,), generator=g), torch.rand(n, generator=g)
+        path, out = ref.verify(target[0].double().tolist(), draft[0].double().tolist() if kind == "drawn" else None, tokens.tolist(), parents, u.tolist())
+        got = run_verify(torch, rng, wide[0], wide[1] if kind == "drawn" else None, at[tokens][None], torch.tensor([parents]), u[None])
+        assert got[0][0].tolist() == path + [-1] * (n - len(path)) and got[1].item() == len(path) - 1
+        assert got[2][0].tolist() == [int(at[t]) for t in out] + [-1] * (n - len(out))
+
+
 def how_often(p, q, drawn):
     total = 0.0
     for triple in itertools.product(range(len(p)), repeat=3):
