@@ -17,12 +17,12 @@
 // would be slower than HBM here (2 operations a cycle and SM), and f32 sums would
 // pick a neighbouring token about once in a thousand draws of a large vocabulary.
 //
-// What bounds it, measured: latency. One request of 32768 tokens: 8.3 us in a graph (the
+// What bounds it, measured: latency. One request of 32768 tokens: 8.5 us in a graph (the
 // launch, then 1.3 us for what the walk needs, 2.2 for the walk, 0.9 for the row's sums, 3
 // for the blocks' exchange and the token); each further rejection of the same row 3 us.
-// 128 requests of 131072 tokens, 16 nodes (1.9 sums a request, 8 at most): 71 us for the
+// 128 requests of 131072 tokens, 16 nodes (1.9 sums a request, 8 at most): 74 us for the
 // 117 MB that are read; issue slots 37 %, and the last requests alone for a quarter of
-// the time. Chosen drafts, 64 requests of 24 nodes: 22 us for 34 MB.
+// the time. Chosen drafts, 64 requests of 24 nodes: 23 us for 34 MB.
 #include <cooperative_groups.h>
 
 #include "attention.h"

@@ -500,8 +500,8 @@ size_t rng_tree_attention_fwd_workspace(const rng_tree_attention_args *args);
  * Written, each [batch, nodes] or [batch]: accepted[b], the number of drafts
  * that stand; path[b], node 0 and those drafts' nodes, then -1; out_tokens[b],
  * their tokens and the last one, then -1.  All comparisons are made to 2^-44 of
- * the sums or better (pairs of f32, or f64), the sums in an order that depends on
- * the sizes, and on which rows were read before, alone. */
+ * the sums or better (pairs of f32), the sums in an order that depends on the
+ * device, the sizes, and which rows were read before, alone. */
 typedef struct rng_verify_drafts_args {
     rng_dtype dtype; /* of target and draft: RNG_F32, RNG_F16 or RNG_BF16 */
     int32_t batch, nodes, vocab;

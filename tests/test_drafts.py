@@ -168,6 +168,8 @@ MANY = {
 }
 
 
+# (Since these were written, past six key tiles two tiles of rows share their keys from ten key tiles a block on: CUT_PAIRS
+# below has those; and test_as_much_work_as_the_device_holds the borders themselves.)
 # More than 128 rows of a key head, and work enough that two tiles of rows share their keys: more tiles than SMs, or, past
 # six key tiles, more than three of those for each SM and pair.
 WIDE = {
