@@ -33,7 +33,7 @@
 //     28 us and 8 us.
 //   more rows, the chain of product, exponentials, product in each unit: 8 trees of 64
 //     nodes over 4099 rows (256 rows of a key head): 47 us for 14 tiles of keys a block,
-//     whose products alone take 3072 cycles each; tensor core 52 %.
+//     six products of 512 cycles each; tensor core 52 %.
 //   short entries, what a piece costs once: 96 trees of 7 nodes over 115 rows and less, 6
 //     heads of 40, a bias: 22 us for four pieces a block; one tree of 8 over 301 rows,
 //     10.4 us in a graph; of 19000 cycles, 2400 are set-up and 4300 the first piece's
