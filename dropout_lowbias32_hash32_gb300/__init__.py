@@ -736,8 +736,9 @@ def rng_verify_drafts(target, tokens, path, accepted, out_tokens, *, draft=None,
                       first_counter=0, stream=None):
     """Verifies drafted tokens [batch, nodes] (node 0 the known one) against the target's probabilities
     [batch, nodes, vocab] after each node; draft: the probabilities that each node's children were drawn from (None:
-    they were chosen), parents int32 (None: a chain), uniforms [batch, nodes] f32 (None: drawn from seed and
-    first_counter); see rng.h.  Writes path [batch, nodes], accepted [batch] and out_tokens [batch, nodes], all int32;
+    they were chosen; the row of a node without children may hold anything), parents int32 (None: a chain), uniforms
+    [batch, nodes] f32 (None: drawn from seed and first_counter); see rng.h.  Writes path [batch, nodes], accepted
+    [batch] and out_tokens [batch, nodes], all int32;
     returns out_tokens."""
     code = _first(target, "target")
     shape = target.shape
